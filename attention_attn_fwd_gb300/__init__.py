@@ -24,6 +24,9 @@ __all__ = [
     "attn_tile_config", "attn_unit_plan", "attn_version", "attn_bwd",
     "attn_bwd_workspace_bytes",
     "fwd", "fwd_splitkv", "fwd_fp8", "bwd",
+    "attn_kv8_append", "attn_kv8_fwd", "attn_kv8_workspace_bytes",
+    "attn_kv8_evict",
+    "KV8Cache", "kv8_append", "kv8_fwd", "kv8_workspace", "kv8_evict",
     "library_path", "load_library",
 ]
 
@@ -58,6 +61,13 @@ class _Dispatch(ctypes.Structure):
         "block_m", "block_n", "q_tiles", "paired", "s_buffers", "stages",
         "order", "o_store", "hold_scores", "num_splits", "units",
         "smem_bytes", "merge")] + [("name", ctypes.c_char_p)]
+
+
+class _KV8(ctypes.Structure):
+    """attn_kv8_t of include/attn.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k", "v", "k_scale", "v_scale", "lens")] + [
+            (n, ctypes.c_int) for n in ("B", "Hkv", "capacity", "D", "block")]
 
 
 def library_path() -> str:
@@ -132,6 +142,16 @@ def load_library():
             vp, vp, vp, vp, vp, i, i, i, i, i, i, ctypes.c_float, i, i, i,
             ctypes.c_ulonglong, vp]
         lib.attn_selftest_wait_timeout.restype = i
+        cp = ctypes.POINTER(_KV8)
+        lib.attn_kv8_append.argtypes = [cp, vp, vp, i, vp, i, vp]
+        lib.attn_kv8_append.restype = i
+        lib.attn_kv8_fwd.argtypes = [cp, vp, vp, vp, vp, i, i, vp, f, i, i,
+                                     vp, sz, vp]
+        lib.attn_kv8_fwd.restype = i
+        lib.attn_kv8_workspace_bytes.argtypes = [i] * 7
+        lib.attn_kv8_workspace_bytes.restype = sz
+        lib.attn_kv8_evict.argtypes = [cp, cp, vp, vp, i, i, vp, vp]
+        lib.attn_kv8_evict.restype = i
         _lib = lib
         return lib
 
@@ -318,6 +338,35 @@ def attn_unit_plan(B, Hq, Hkv, Sq, Skv, D, causal, input_pos, grid,
         out["cta_units"] = [list(order[start[c]:start[c + 1]])
                             for c in range(g)]
     return out
+
+
+def attn_kv8_append(cache, K, V, Sq, new_lens, dtype, stream) -> int:
+    """Raw C-ABI call; ``cache`` is a ``KV8Cache``, pointers are integers."""
+    return int(load_library().attn_kv8_append(
+        cache.struct, K or None, V or None, Sq, new_lens or None, int(dtype),
+        stream or None))
+
+
+def attn_kv8_fwd(cache, Q, O, LSE, weights, Hq, Sq, new_lens, scale, causal,
+                 dtype, workspace, workspace_bytes, stream) -> int:
+    """Raw C-ABI call; ``cache`` is a ``KV8Cache``, pointers are integers."""
+    return int(load_library().attn_kv8_fwd(
+        cache.struct, Q or None, O or None, LSE or None, weights or None, Hq,
+        Sq, new_lens or None, float(scale), int(causal), int(dtype),
+        workspace or None, int(workspace_bytes), stream or None))
+
+
+def attn_kv8_workspace_bytes(B, Hq, Hkv, Sq, capacity, D, weights) -> int:
+    return int(load_library().attn_kv8_workspace_bytes(
+        B, Hq, Hkv, Sq, capacity, D, int(bool(weights))))
+
+
+def attn_kv8_evict(src, dst, weights, dst_weights, keep, recent, indices,
+                   stream) -> int:
+    """Raw C-ABI call; ``src`` and ``dst`` are ``KV8Cache``s."""
+    return int(load_library().attn_kv8_evict(
+        src.struct, dst.struct, weights or None, dst_weights or None, keep,
+        recent, indices or None, stream or None))
 
 
 def attn_version() -> int:
@@ -534,3 +583,219 @@ def bwd(q, k, v, o, lse, do, scale=None, causal=True, input_pos=0, window=0,
     if st != ATTN_OK:
         raise AttnError("attn_bwd: " + attn_status_string(st), st)
     return dq, dk, dv
+
+
+class KV8Cache:
+    """Handle of a KV cache held in 8 bits (``attn_kv8_t``): E4M3 codes with
+    one fp32 scale for each ``block`` tokens of a (batch, K/V head).
+
+    k, v [B, Hkv, capacity, D] (torch.float8_e4m3fn, or uint8 holding the
+    codes), k_scale, v_scale float32 [B, Hkv, ceil(capacity / block)], lens
+    int32 [B]: the tokens of each sequence, the current step's new ones
+    included.  All contiguous, on one CUDA device; the tensors stay the
+    caller's and are kept alive by the handle.  Advance ``lens`` first, then
+    ``kv8_append`` the new tokens, then ``kv8_fwd``; one ``lens`` tensor may
+    serve the caches of all layers.
+    """
+
+    def __init__(self, k, v, k_scale, v_scale, lens, block=64):
+        import torch
+        if k.dim() != 4:
+            raise AttnError("k must be 4-D [B, Hkv, capacity, D]",
+                            ATTN_ERR_INVALID_ARG)
+        B, Hkv, capacity, D = k.shape
+        if block not in (16, 32, 64, 128):
+            raise AttnError("block must be 16, 32, 64 or 128, got %r"
+                            % (block,), ATTN_ERR_UNSUPPORTED)
+        nblk = -(-capacity // block)
+        codes = (getattr(torch, "float8_e4m3fn", None), torch.uint8)
+        for name, t, shape, dtypes in (
+                ("k", k, (B, Hkv, capacity, D), codes),
+                ("v", v, (B, Hkv, capacity, D), codes),
+                ("k_scale", k_scale, (B, Hkv, nblk), (torch.float32,)),
+                ("v_scale", v_scale, (B, Hkv, nblk), (torch.float32,)),
+                ("lens", lens, (B,), (torch.int32,))):
+            if tuple(t.shape) != shape or t.dtype not in dtypes:
+                raise AttnError("%s must be %s of %s, got %s of %s" % (
+                    name, list(shape), dtypes[0], list(t.shape), t.dtype),
+                    ATTN_ERR_INVALID_ARG)
+            if not t.is_cuda or t.device != k.device or \
+                    not t.is_contiguous():
+                raise AttnError("%s must be a contiguous CUDA tensor on k's "
+                                "device" % name, ATTN_ERR_INVALID_ARG)
+        self.k, self.v = k, v
+        self.k_scale, self.v_scale, self.lens = k_scale, v_scale, lens
+        self.B, self.Hkv, self.capacity, self.D = B, Hkv, capacity, D
+        self.block, self.device = block, k.device
+        self.struct = ctypes.pointer(_KV8(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), lens.data_ptr(), B, Hkv, capacity, D, block))
+
+    @classmethod
+    def empty(cls, B, Hkv, capacity, D, block=64, lens=None, device="cuda"):
+        """A cache of new, uninitialised memory; ``lens`` (zeros unless
+        given) may be shared with other caches."""
+        import torch
+        k, v = (torch.empty((B, Hkv, capacity, D), dtype=torch.uint8,
+                            device=device).view(torch.float8_e4m3fn)
+                for _ in range(2))
+        ks, vs = (torch.empty((B, Hkv, -(-capacity // block)),
+                              dtype=torch.float32, device=device)
+                  for _ in range(2))
+        if lens is None:
+            lens = torch.zeros(B, dtype=torch.int32, device=device)
+        return cls(k, v, ks, vs, lens, block)
+
+
+def _check_tensor(name, t, shape, dtype, device):
+    """A contiguous tensor of this shape and type on this device."""
+    if tuple(t.shape) != shape or (dtype is not None and t.dtype != dtype):
+        raise AttnError("%s must be %s of %s, got %s of %s" % (
+            name, list(shape), dtype or "float16 or bfloat16",
+            list(t.shape), t.dtype), ATTN_ERR_INVALID_ARG)
+    if t.device != device or not t.is_contiguous():
+        raise AttnError("%s must be a contiguous tensor on the cache's device"
+                        % name, ATTN_ERR_INVALID_ARG)
+
+
+def kv8_append(cache, k, v, new_lens=None, stream=None):
+    """Quantise the K and V of new tokens into an 8-bit cache.
+
+    k, v [B, Hkv, Sq, D] (contiguous, float16 or bfloat16) hold the last
+    tokens of each sequence, positions lens - Sq .. lens - 1, or with
+    ``new_lens`` (int32 [B]) lens - new_lens .. lens - 1 in the first
+    new_lens rows.  ``cache.lens`` already counts them and is not changed.
+    """
+    import torch
+    dt = _dtype_code(k)
+    if k.dim() != 4:
+        raise AttnError("k must be 4-D [B, Hkv, Sq, D]", ATTN_ERR_INVALID_ARG)
+    Sq = k.shape[2]
+    shape = (cache.B, cache.Hkv, Sq, cache.D)
+    _check_tensor("k", k, shape, None, cache.device)
+    _check_tensor("v", v, shape, k.dtype, cache.device)
+    if new_lens is not None:
+        _check_tensor("new_lens", new_lens, (cache.B,), torch.int32,
+                      cache.device)
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    with torch.cuda.device(cache.device):
+        st = attn_kv8_append(
+            cache, k.data_ptr(), v.data_ptr(), Sq,
+            new_lens.data_ptr() if new_lens is not None else 0, dt,
+            stream.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError("attn_kv8_append: " + attn_status_string(st), st)
+
+
+def kv8_workspace(cache, Hq, Sq, weights=False):
+    """A workspace tensor for ``kv8_fwd`` calls of Hq heads and Sq rows
+    (``weights``: calls that accumulate attention weights)."""
+    import torch
+    with torch.cuda.device(cache.device):
+        n = attn_kv8_workspace_bytes(cache.B, Hq, cache.Hkv, Sq,
+                                     cache.capacity, cache.D, weights)
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=cache.device)
+
+
+def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
+            out=None, lse=None, need_lse=True, workspace=None, stream=None):
+    """Attention of q [B, Hq, Sq, D] (contiguous, float16 or bfloat16) over
+    an 8-bit cache.  Returns (O, LSE) like ``fwd``.
+
+    Row i of a sequence with n new rows (Sq, or ``new_lens[b]`` of them) sits
+    at position lens - n + i and sees the tokens up to it (``causal``), or
+    all lens tokens.  Rows that see nothing get O = 0 and LSE = -inf; rows at
+    or behind new_lens are left as they are in ``out`` and ``lse``.
+    ``weights`` (float32 [B, Hkv, capacity]): the attention weight each token
+    receives, summed over rows and the group's heads, is added to it.
+    ``workspace``: from ``kv8_workspace``, allocated when not given.
+    """
+    import torch
+    dt = _dtype_code(q)
+    if q.dim() != 4:
+        raise AttnError("q must be 4-D [B, Hq, Sq, D]", ATTN_ERR_INVALID_ARG)
+    B, Hq, Sq, D = q.shape
+    dev = cache.device
+    _check_tensor("q", q, (cache.B, Hq, Sq, cache.D), None, dev)
+    if new_lens is not None:
+        _check_tensor("new_lens", new_lens, (B,), torch.int32, dev)
+    if weights is not None:
+        _check_tensor("weights", weights, (B, cache.Hkv, cache.capacity),
+                      torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_tensor("out", out, (B, Hq, Sq, D), q.dtype, dev)
+    if not need_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
+    else:
+        _check_tensor("lse", lse, (B, Hq, Sq), torch.float32, dev)
+    if workspace is None:
+        workspace = kv8_workspace(cache, Hq, Sq, weights is not None)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        st = attn_kv8_fwd(
+            cache, q.data_ptr(), out.data_ptr(),
+            lse.data_ptr() if lse is not None else 0,
+            weights.data_ptr() if weights is not None else 0, Hq, Sq,
+            new_lens.data_ptr() if new_lens is not None else 0, scale, causal,
+            dt, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), stream.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError("attn_kv8_fwd: " + attn_status_string(st), st)
+    return out, lse
+
+
+def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
+              indices=None, stream=None):
+    """Keep ``keep`` tokens of every longer sequence and head: the
+    ``recent`` last ones and those of largest ``weights`` (float32 [B, Hkv,
+    capacity]), in their order, as the first tokens of ``out``.
+
+    ``out``: another ``KV8Cache`` of the same heads and block, of its own
+    memory, lens included; None: in place (the result shares ``cache``'s
+    buffers and has a lens tensor of its own; ``cache.lens`` keeps its
+    values).  ``out_weights`` (float32 [B, Hkv, out.capacity]) receives the
+    kept tokens' weights, then zeros; in place it defaults to ``weights``
+    itself.  Returns (out, out_weights, indices): indices int32 [B, Hkv,
+    keep] are the kept tokens' old places, -1 behind the last.
+    """
+    import torch
+    dev = cache.device
+    _check_tensor("weights", weights, (cache.B, cache.Hkv, cache.capacity),
+                  torch.float32, dev)
+    if out is None:
+        out = KV8Cache(cache.k, cache.v, cache.k_scale, cache.v_scale,
+                       torch.empty_like(cache.lens), cache.block)
+        if out_weights is None:
+            out_weights = weights
+    elif out.device != dev:
+        raise AttnError("out must be on the cache's device",
+                        ATTN_ERR_INVALID_ARG)
+    shape = (cache.B, cache.Hkv, out.capacity)
+    if out_weights is None:
+        out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _check_tensor("out_weights", out_weights, shape, torch.float32, dev)
+    shape = (cache.B, cache.Hkv, int(keep))
+    if keep < 1:
+        raise AttnError("keep must be at least 1", ATTN_ERR_INVALID_ARG)
+    if indices is None:
+        indices = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _check_tensor("indices", indices, shape, torch.int32, dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        st = attn_kv8_evict(cache, out, weights.data_ptr(),
+                            out_weights.data_ptr(), int(keep), int(recent),
+                            indices.data_ptr(), stream.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError("attn_kv8_evict: " + attn_status_string(st), st)
+    return out, out_weights, indices

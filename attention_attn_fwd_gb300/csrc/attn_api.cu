@@ -15,9 +15,11 @@
 
 #include "../../include/attn.h"
 #include "attn_bwd_kernel.cuh"
+#include "attn_host.h"
 #include "attn_launch.h"
 
-// Device status word: bit 0 = a pipeline wait ran out, bits 8-15 = role.
+// Device status word: bit 0 = a pipeline wait ran out, bits 8-15 = role;
+// bit 1 = a length outside its range (8-bit caches).
 __device__ unsigned int g_attn_status;
 
 namespace {
@@ -225,6 +227,15 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 }  // namespace
 
 namespace attn {
+unsigned int* device_status_word(int dev) { return status_ptr(dev); }
+int device_sms(int dev) { return num_sms(dev); }
+unsigned long long wait_timeout_ns() { return timeout_ns(); }
+bool on_device(const void* p, int dev) { return is_device_ptr(p, dev); }
+bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return na != 0 && nb != 0 && overlaps(a, na, b, nb);
+}
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encoder(); }
+
 bool current_context_id(unsigned long long* id) {
   std::call_once(g_ctx_once, [] {
     void* fn = nullptr;
@@ -643,6 +654,12 @@ attn_status_t fwd_impl(const Shape& s, const void* Q, const void* K,
                         withhold_first_load);
 }
 
+// Return code of a status word: waits that ran out come first.
+attn_status_t status_of(unsigned int v) {
+  if (v == 0) return ATTN_OK;
+  return v == attn::kStatusBadLength ? ATTN_ERR_INVALID_ARG : ATTN_ERR_TIMEOUT;
+}
+
 // Clears the status bits a status query has reported (bits set since, by
 // kernels on other streams, stay).
 __global__ void clear_status_bits(unsigned int* status, unsigned int bits) {
@@ -958,7 +975,7 @@ attn_status_t attn_device_status(unsigned int* code) {
       return ATTN_ERR_CUDA;
   }
   if (code != nullptr) *code = v;
-  return v != 0 ? ATTN_ERR_TIMEOUT : ATTN_OK;
+  return status_of(v);
 }
 
 attn_status_t attn_stream_status(attn_stream_t stream, unsigned int* code) {
@@ -979,7 +996,7 @@ attn_status_t attn_stream_status(attn_stream_t stream, unsigned int* code) {
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   }
   if (code != nullptr) *code = v;
-  return v != 0 ? ATTN_ERR_TIMEOUT : ATTN_OK;
+  return status_of(v);
 }
 
 attn_status_t attn_selftest_wait_timeout(const void* Q, const void* K,

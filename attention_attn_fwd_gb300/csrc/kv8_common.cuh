@@ -1,0 +1,148 @@
+// Parameters and arithmetic shared by the kernels of the 8-bit KV cache:
+// E4M3 codes [B, Hkv, capacity, D] with one fp32 scale per block of tokens
+// and head.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attn_host.h"
+#include "sm103_ptx.cuh"
+
+namespace attn {
+namespace kv8 {
+
+constexpr float kE4m3Max = 448.f;
+
+// A length read from device memory, brought into [0, most]; a value outside
+// sets the status word's length bit.
+__device__ __forceinline__ int clamp_len(int n, int most,
+                                         unsigned int* status) {
+  if (n < 0 || n > most) {
+    atomicOr(status, kStatusBadLength);
+    return n < 0 ? 0 : most;
+  }
+  return n;
+}
+
+// Exponent of the smallest power of two s with amax <= 448 s, 2^-126 at
+// least: 448 = 1.75 * 2^8, so it is amax's exponent - 8, one more when its
+// mantissa exceeds 1.75.  Exact for every finite amax >= 0.
+__device__ __forceinline__ int tight_exponent(float amax) {
+  const int bits = __float_as_int(amax);
+  const int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000);
+  return max(e, -126);
+}
+
+__device__ __forceinline__ float exp2_int(int e) {  // -126 <= e <= 127
+  return __int_as_float((e + 127) << 23);
+}
+
+// Magnitude that counts for a scale: finite values only.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.f;  // inf and NaN compare false
+}
+
+// Two 16-bit elements of a word as floats.
+template <bool kBF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (kBF16) {
+    return make_float2(__uint_as_float(w << 16),
+                       __uint_as_float(w & 0xffff0000u));
+  } else {
+    __half2 h;
+    *reinterpret_cast<uint32_t*>(&h) = w;
+    return __half22float2(h);
+  }
+}
+
+// Two E4M3 codes (low byte first) as a packed fp16 pair: exact, E4M3's
+// values (2^-9 steps up to 448, NaN) are all fp16 values.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+  return h;
+}
+
+// The four halves of a word of four codes.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t codes, uint32_t& lo,
+                                                uint32_t& hi) {
+  lo = e4m3x2_to_half2(static_cast<uint16_t>(codes & 0xffffu));
+  hi = e4m3x2_to_half2(static_cast<uint16_t>(codes >> 16));
+}
+
+__device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float* x) {
+  uint32_t lo, hi;
+  e4m3x4_to_half2(codes, lo, hi);
+  const float2 a = unpack2<false>(lo), b = unpack2<false>(hi);
+  x[0] = a.x;
+  x[1] = a.y;
+  x[2] = b.x;
+  x[3] = b.y;
+}
+
+struct AppendParams {
+  uint8_t* code[2];       // K, V
+  float* scale[2];
+  const void* x[2];       // new K, V [B, Hkv, Sq, D]
+  const int* lens;
+  const int* new_lens;    // or nullptr
+  int Hkv, Sq, capacity, nblk;
+  int units_per_seq;      // blocks of a head one call may touch
+  unsigned int* status;
+};
+
+struct FwdParams {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int* lens;
+  const int* new_lens;    // or nullptr
+  const void* q;
+  void* o;
+  float* lse;             // or nullptr
+  float* weights;         // or nullptr
+  int B, Hq, Hkv, Sq, capacity, nblk, block_shift;
+  int group;              // query heads per K/V head
+  int row_blocks;         // blocks of kRows query rows per (batch, K/V head)
+  int causal;
+  float scale_log2;       // scale * log2(e)
+  // Workspace: per (CTA, segment) partial rows, their (max, sum), per-row
+  // LSEs in log2 units, and (few rows) the scores of every key.
+  float* part_o;          // [slots, rows, D]
+  float2* part_ml;        // [slots, rows]
+  float* lse2;            // [B * Hkv, row_blocks * rows]
+  float* scores;          // [B * Hkv, capacity, rows]
+  int grid;               // CTAs of the forward launch
+  unsigned int* status;
+};
+
+struct EvictParams {
+  const uint8_t* src_code[2];
+  const float* src_scale[2];
+  uint8_t* dst_code[2];
+  float* dst_scale[2];
+  const int* src_lens;
+  int* dst_lens;
+  const float* weights;
+  float* dst_weights;
+  int* indices;           // [B, Hkv, keep]
+  int B, Hkv, src_capacity, dst_capacity, src_nblk, dst_nblk, block_shift;
+  int keep, recent;
+  int in_place;
+  unsigned int* status;
+};
+
+cudaError_t launch_append(int D, int block, bool bf16, const AppendParams& p,
+                          int B, cudaStream_t stream);
+cudaError_t launch_fwd(int D, bool bf16, int rows, const FwdParams& p,
+                       cudaStream_t stream);
+cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream);
+
+}  // namespace kv8
+}  // namespace attn

@@ -284,6 +284,141 @@ attn_status_t attn_bwd(const void* Q, const void* K, const void* V,
  * values per row, Sq padded to a multiple of 128 (0 on negative sizes). */
 size_t attn_bwd_workspace_bytes(int B, int Hq, int Sq);
 
+/*
+ * attn_kv8_t — a KV cache held in 8 bits: E4M3 codes with one fp32 scale for
+ * each block of `block` consecutive tokens of a (batch, K/V head), separate
+ * for K and V.  Token j of head (b, h) stands for the numbers
+ *   k[b,h,j,:] = k_scale[b,h, j / block] * K8[b,h,j,:]   (V likewise).
+ * "Flash Attention from Scratch", section "What's Next", names FP8 without a
+ * format; attn_fwd_fp8 above takes one factor per tensor, this cache one per
+ * block, so that late tokens do not have to share the range of early ones.
+ *
+ * k, v       device, [B, Hkv, capacity, D] one byte per element, 16-byte
+ *            aligned;
+ * k_scale, v_scale  device fp32 [B, Hkv, ceil(capacity / block)], 4-byte
+ *            aligned; finite and > 0 for every block that holds a token
+ *            (attn_kv8_append and attn_kv8_evict write powers of two);
+ * lens       device int32 [B]: tokens of sequence b in the cache, the new
+ *            tokens of the current step included, 0 <= lens[b] <= capacity.
+ *            One array may serve the caches of all layers; no function
+ *            changes the lens of a cache it reads or appends to.  A value
+ *            outside the range is taken as the nearer end of it and reported
+ *            by attn_device_status (bit 1 of the code).
+ * B >= 0, Hkv > 0, capacity >= 1, D in {64, 128}, block in {16, 32, 64, 128};
+ * B * Hkv < 2^24.  Codes and scales of tokens at lens[b] or later are never
+ * read: they need no initialisation.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int* lens;
+  int B, Hkv, capacity, D, block;
+} attn_kv8_t;
+
+/*
+ * attn_kv8_append — quantise the K and V of new tokens into the cache.
+ * The new tokens of sequence b are its last n_b tokens, positions
+ * lens[b] - n_b .. lens[b] - 1, with n_b = Sq, or new_lens[b].
+ *
+ * K, V      device, [B, Hkv, Sq, D] contiguous, dtype, 16-byte aligned (read);
+ *           rows i >= n_b are ignored;
+ * new_lens  device int32 [B] or NULL (n_b = Sq): 0 <= n_b <= Sq and
+ *           n_b <= lens[b]; values outside are taken as the nearer end and
+ *           reported like lens;
+ * dtype     ATTN_F16 or ATTN_BF16.
+ *
+ * Let a be the largest finite magnitude among the new tokens of one block of
+ * one head, and tight(a) the smallest power of two (2^-126 at least) with
+ * a <= 448 * tight(a).  A block that holds no earlier token gets the scale
+ * tight(a).  A block begun by earlier calls keeps its scale when
+ * a <= 448 * scale; else its scale becomes tight(a) and the codes it holds
+ * are requantised, round(code * old / new) -- with powers of two an exponent
+ * shift, exact unless the result is subnormal.  New codes are
+ * round(x / scale): to nearest, ties to even; infinities become +-448, NaN
+ * stays NaN.  Nothing else of the cache is written.  Deterministic.
+ */
+attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
+                              const void* V, int Sq, const int* new_lens,
+                              attn_dtype_t dtype, attn_stream_t stream);
+
+/*
+ * attn_kv8_fwd — attention of Sq query rows per sequence over an 8-bit
+ * cache, in the scores, softmax and sums of attn_fwd (fp32), on the numbers
+ * the cache stands for.
+ *
+ * Q         device, [B, Hq, Sq, D] contiguous, dtype (read);
+ * O         device, [B, Hq, Sq, D] contiguous, dtype (written);
+ * LSE       device fp32 [B, Hq, Sq] or NULL (written);
+ * weights   device fp32 [B, Hkv, capacity] or NULL: the attention weight each
+ *           cached token receives is added to it,
+ *             weights[b,h,j] += sum over the query heads of K/V head h and
+ *                               the rows i of softmax_ij;
+ *           entries of tokens nobody sees keep their bits;
+ * new_lens  device int32 [B] or NULL (n_b = Sq): rows i < n_b are computed,
+ *           0 <= n_b <= Sq; O and LSE of rows i >= n_b are left as they are
+ *           and their Q is ignored;
+ * causal    non-zero: row i of sequence b sits at position
+ *           lens[b] - n_b + i and sees the tokens up to it (the new tokens
+ *           are the cache's last n_b); 0: every row sees all lens[b] tokens
+ *           (cross attention to cached encoder states).
+ *           A row that sees no token gets O = 0 and LSE = -inf.
+ * Hq        a multiple of the cache's Hkv; scale finite, any sign;
+ * dtype     ATTN_F16 or ATTN_BF16;
+ * workspace device, 256-byte aligned, at least attn_kv8_workspace_bytes(...)
+ *           bytes; contents need no initialisation.  It must not be used by
+ *           another call until this one has run.
+ * Two kernels on `stream`, or three (weights of more than 16 query rows per
+ * K/V head).  O, LSE, weights and workspace must not overlap each other or
+ * any input.  B == 0 or Sq == 0 is a successful no-op.  Deterministic for a
+ * given device, shape and lengths.
+ */
+attn_status_t attn_kv8_fwd(const attn_kv8_t* cache, const void* Q, void* O,
+                           float* LSE, float* weights, int Hq, int Sq,
+                           const int* new_lens, float scale, int causal,
+                           attn_dtype_t dtype, void* workspace,
+                           size_t workspace_bytes, attn_stream_t stream);
+
+/* Workspace bytes attn_kv8_fwd needs (0 on bad sizes); `weights` non-zero
+ * when the call accumulates attention weights.  Host only; the value is for
+ * the current device's SM count (152 without a device). */
+size_t attn_kv8_workspace_bytes(int B, int Hq, int Hkv, int Sq, int capacity,
+                                int D, int weights);
+
+/*
+ * attn_kv8_evict — keep the tokens of a cache that received the most
+ * attention.  For every sequence with lens[b] > keep and every K/V head,
+ * the `recent` last tokens stay, and of the others the keep - recent with
+ * the largest weights (equal weights: the earlier token; NaN counts as less
+ * than every number).  Kept tokens keep their order and become tokens
+ * 0 .. keep - 1 of the same head of `dst`: per block of dst the scale is
+ * tight(largest magnitude of its kept numbers) and the codes are
+ * requantised as in attn_kv8_append.  Sequences with lens[b] <= keep are
+ * copied bit for bit.
+ *
+ * src          the cache (read);
+ * dst          the cache written: its k, v, scales, and lens (lens[b]
+ *              becomes min(lens[b], keep)).  Either all of k, v and both
+ *              scales are other memory than src's (any capacity >= keep), or
+ *              all four are src's own (in place, same capacity).
+ *              dst->lens is always other memory than src->lens.  B, Hkv, D
+ *              and block must agree.
+ * weights      device fp32 [B, Hkv, src capacity] (read);
+ * dst_weights  device fp32 [B, Hkv, dst capacity] (written): the kept
+ *              tokens' weights, then zeros to the capacity.  In place it may
+ *              be `weights` itself; else it must not overlap it;
+ * keep, recent 1 <= keep <= dst capacity, 0 <= recent <= keep;
+ * indices      device int32 [B, Hkv, keep] (written): the place in src of
+ *              each kept token, ascending; -1 behind the last one.
+ * Two kernels on `stream`.  Codes and scales of dst behind the kept tokens'
+ * last block are left as they are.  Deterministic.
+ */
+attn_status_t attn_kv8_evict(const attn_kv8_t* src, const attn_kv8_t* dst,
+                             const float* weights, float* dst_weights,
+                             int keep, int recent, int* indices,
+                             attn_stream_t stream);
+
 /* Short English description of a status code (static storage). */
 const char* attn_status_string(attn_status_t status);
 
@@ -291,8 +426,10 @@ const char* attn_status_string(attn_status_t status);
  * attn_device_status — synchronises the current device, then reads and
  * clears the library's device status word.  *code receives 0 when no kernel
  * wait has run out since the last call; otherwise a non-zero code
- * (bits 0-7: 1 = wait timed out; bits 8-15: the pipeline role that gave
- * up) and the function returns ATTN_ERR_TIMEOUT.  code may be NULL.
+ * (bit 0: a wait timed out, bits 8-15 then name the pipeline role that gave
+ * up; bit 1: an attn_kv8_* call met a length outside its range and clamped
+ * it) and the function returns ATTN_ERR_TIMEOUT, or ATTN_ERR_INVALID_ARG
+ * when bit 1 alone is set.  code may be NULL.
  * Every wait of every kernel in flight ORs into the one word, so the
  * device-wide form sees them all; attn_stream_status below waits for one
  * stream only.

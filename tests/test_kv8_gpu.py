@@ -1,0 +1,462 @@
+"""8-bit cache operators on the GPU against the float64 reference."""
+import math
+
+import pytest
+import torch
+
+import attention_attn_fwd_gb300 as attn
+from tests import kv8_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    attn.attn_device_status()
+    yield
+    torch.cuda.synchronize()
+    assert attn.attn_device_status() == (0, 0)
+
+
+def upload(c):
+    """KV8Cache with the reference cache's contents."""
+    return attn.KV8Cache(
+        c.code["k"].cuda(), c.code["v"].cuda(), c.scale["k"].float().cuda(),
+        c.scale["v"].float().cuda(),
+        torch.tensor(c.lens, dtype=torch.int32).cuda(), c.block)
+
+
+def counts(new):
+    return None if new is None else torch.tensor(
+        new, dtype=torch.int32).cuda()
+
+
+def same_cache(gpu, c, lens=True):
+    for n in "kv":
+        code = getattr(gpu, n).view(torch.uint8).cpu()
+        nan = ((code & 127) == 127) & ((c.code[n] & 127) == 127)
+        assert torch.equal(torch.where(nan, 127, code),
+                           torch.where(nan, 127, c.code[n])), n
+        assert torch.equal(getattr(gpu, n + "_scale").cpu().double(),
+                           c.scale[n]), n + "_scale"
+    if lens:
+        assert gpu.lens.cpu().tolist() == c.lens
+
+
+# ------------------------------------------------------------------ append
+
+APPENDS = [
+    # B, H, cap, D, block, before, new rows given, counts (None: all)
+    (1, 1, 1, 64, 16, [0], 1, None),
+    (2, 3, 70, 128, 64, [0, 63], 1, None),
+    (3, 2, 130, 64, 16, [15, 16, 17], 1, None),
+    (2, 2, 300, 128, 128, [127, 100], 2, None),
+    (4, 1, 257, 64, 32, [0, 5, 31, 64], 100, [100, 0, 1, 77]),
+    (2, 5, 513, 128, 32, [1, 33], 480, [480, 333]),
+    (1, 2, 1000, 128, 16, [0], 1000, None),
+    (3, 3, 200, 64, 128, [199, 128, 0], 5, [1, 5, 0]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", APPENDS)
+def test_append(case, dtype):
+    B, H, cap, D, block, before, Sq, new = case
+    c = ref.filled(B, H, cap, D, block, before, 1)
+    x = [(torch.randn(B, H, Sq, D, generator=ref.rng(s)) *
+          torch.exp(torch.randn(B, H, Sq, 1, generator=ref.rng(s + 9)))
+          ).to(DT[dtype]) for s in (2, 3)]
+    n = [Sq] * B if new is None else new
+    c.lens = [a + i for a, i in zip(before, n)]
+    gpu = upload(c)
+    attn.kv8_append(gpu, x[0].cuda(), x[1].cuda(), new_lens=counts(new))
+    c.append(x[0], x[1], new=n)
+    same_cache(gpu, c)
+
+
+def test_append_one_by_one_matches_the_reference_at_every_step():
+    B, H, cap, D, block = 2, 2, 80, 64, 32
+    c = ref.Cache(B, H, cap, D, block)
+    gpu = upload(c)
+    for t in range(70):
+        x = [(torch.randn(B, H, 1, D, generator=ref.rng(100 * s + t)) *
+              2.0 ** (t % 23 - 11)).bfloat16() for s in (1, 2)]
+        c.lens = [t + 1] * B
+        gpu.lens += 1
+        attn.kv8_append(gpu, x[0].cuda(), x[1].cuda())
+        c.append(x[0], x[1])
+        same_cache(gpu, c)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_append_extremes(dtype):
+    """Zeros, the type's largest and smallest numbers, infinities and NaN."""
+    B, H, cap, D, block = 1, 1, 96, 64, 16
+    info = torch.finfo(DT[dtype])
+    x = torch.zeros(1, 1, 96, 64, dtype=torch.float64)
+    x[0, 0, 16:32] = info.max * torch.linspace(-1, 1, 64).double()
+    x[0, 0, 32:48] = info.tiny * torch.linspace(-1, 1, 64).double()
+    x[0, 0, 48:64, 0] = math.inf
+    x[0, 0, 48:64, 1] = -math.inf
+    x[0, 0, 48:64, 2] = 3.0
+    x[0, 0, 64:80, 3] = math.nan
+    x[0, 0, 64:80, 4] = -5.0
+    x[0, 0, 80:96] = math.inf
+    x = x.to(DT[dtype])
+    c = ref.Cache(B, H, cap, D, block)
+    c.lens = [96]
+    gpu = upload(c)
+    attn.kv8_append(gpu, x.cuda(), x.cuda())
+    c.append(x, x)
+    same_cache(gpu, c)
+
+
+def test_append_keeps_a_scale_of_other_origin():
+    c = ref.filled(1, 1, 64, 64, 32, [5], 1)
+    for n in "kv":
+        c.scale[n][0, 0, 0] = float(torch.tensor(0.0123))
+    x = torch.randn(1, 1, 3, 64, generator=ref.rng(7)).half()
+    c.lens = [8]
+    gpu = upload(c)
+    attn.kv8_append(gpu, x.cuda(), x.cuda())
+    c.append(x, x)
+    # x / scale is rounded to fp32 before the rounding to E4M3, which moves a
+    # quotient across a tie at most: codes differ by one step, and seldom.
+    for n in "kv":
+        a = getattr(gpu, n).view(torch.uint8).cpu()[0, 0, :8].int()
+        b = c.code[n][0, 0, :8].int()
+        assert int((a - b).abs().max()) <= 1
+        assert float((a != b).float().mean()) < 0.01
+        assert torch.equal(getattr(gpu, n + "_scale").cpu().double(),
+                           c.scale[n])
+
+
+# --------------------------------------------------------------- attention
+
+def run_fwd(c, q, causal=True, new=None, scale=None, with_w=True, gpu=None,
+            **kw):
+    """GPU result on buffers of sentinels, checked to stay where they must."""
+    B, Hq, Sq, D = q.shape
+    gpu = gpu or upload(c)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    out = torch.full(q.shape, 7.5, dtype=q.dtype).cuda()
+    lse = torch.full((B, Hq, Sq), 3.25).cuda()
+    w0 = torch.rand(B, c.H, c.cap, generator=ref.rng(77))
+    w = w0.cuda() if with_w else None
+    ws = attn.kv8_workspace(gpu, Hq, Sq, with_w)
+    guard = torch.full((ws.numel() + 4096,), 0xA5, dtype=torch.uint8).cuda()
+    attn.kv8_fwd(gpu, q.cuda(), scale=scale, causal=causal,
+                 new_lens=counts(new), weights=w, out=out, lse=lse,
+                 workspace=guard[:ws.numel()], **kw)
+    torch.cuda.synchronize()
+    assert bool((guard[ws.numel():] == 0xA5).all()), "workspace overrun"
+    return (out.cpu(), lse.cpu(), w.cpu() if with_w else None, w0)
+
+
+def check_fwd(c, q, causal=True, new=None, scale=None, with_w=True, gpu=None):
+    B, Hq, Sq, D = q.shape
+    scale_ = 1.0 / math.sqrt(D) if scale is None else scale
+    out, lse, w, w0 = run_fwd(c, q, causal, new, scale, with_w, gpu)
+    o_r, l_r, w_r, t_o, t_l, t_w = ref.attention(c, q, scale_, causal, new)
+    for b in range(B):
+        n = Sq if new is None else new[b]
+        assert bool((out[b, :, n:] == 7.5).all())
+        assert bool((lse[b, :, n:] == 3.25).all())
+        e = (out[b, :, :n].double() - o_r[b, :, :n]).abs()
+        assert bool((e <= t_o[b, :, :n]).all()), (
+            "O", b, float((e - t_o[b, :, :n]).max()))
+        got, want = lse[b, :, :n].double(), l_r[b, :, :n]
+        empty = want == -math.inf
+        assert torch.equal(got == -math.inf, empty)
+        e = torch.where(empty, 0.0, got - torch.where(empty, 0.0, want)).abs()
+        assert bool((e <= t_l[b, :, :n]).all()), ("LSE", b, float(e.max()))
+        assert bool((out[b, :, :n][empty] == 0).all())
+        if with_w:
+            L = c.lens[b]
+            assert torch.equal(w[b, :, L:], w0[b, :, L:])
+            e = (w[b].double() - w0[b].double() - w_r[b]).abs()
+            # Adding to the accumulator rounds once more.
+            tol = t_w[b] + 2.0 ** -23 * (w0[b] + w_r[b])
+            assert bool((e <= tol).all()), ("w", b, float((e - tol).max()))
+
+
+FWDS = [
+    # B, Hq, Hkv, cap, D, block, lens, Sq, new
+    (1, 1, 1, 1, 64, 16, [1], 1, None),
+    (1, 8, 1, 40, 128, 16, [17], 1, None),
+    (2, 4, 4, 64, 64, 64, [64, 1], 1, None),
+    (3, 8, 2, 300, 128, 64, [0, 299, 300], 1, None),
+    (4, 14, 2, 1000, 64, 32, [1000, 15, 16, 129], 1, None),
+    (5, 6, 2, 515, 128, 128, [515, 0, 4, 200, 77], 5, [5, 5, 0, 3, 1]),
+    (2, 16, 1, 333, 64, 16, [333, 100], 1, None),
+    (2, 3, 3, 400, 64, 32, [3, 400], 9, [9, 7]),
+    (1, 7, 1, 700, 128, 64, [700], 3, None),
+    (2, 8, 2, 600, 64, 64, [600, 131], 40, [40, 17]),
+    (2, 4, 2, 257, 128, 32, [257, 64], 130, None),
+    (1, 6, 6, 150, 64, 16, [150], 150, None),
+    (40, 2, 1, 90, 64, 16, [(7 * i) % 91 for i in range(40)], 1, None),
+    (1, 4, 1, 9000, 128, 128, [8999], 1, None),
+    (1, 32, 4, 2500, 128, 64, [2500], 64, None),
+    (3, 4, 1, 520, 64, 64, [520, 0, 30], 64, [50, 64, 64]),
+]
+
+
+@pytest.mark.parametrize("with_w", [False, True])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", FWDS)
+def test_fwd(case, dtype, causal, with_w):
+    B, Hq, Hkv, cap, D, block, lens, Sq, new = case
+    c = ref.filled(B, Hkv, cap, D, block, lens, 11)
+    q = torch.randn(B, Hq, Sq, D, generator=ref.rng(12)).to(DT[dtype])
+    check_fwd(c, q, causal, new, with_w=with_w)
+
+
+@pytest.mark.parametrize("Sq", [1, 33])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.5])
+def test_fwd_scales(scale, Sq):
+    c = ref.filled(2, 2, 200, 64, 32, [200, 45], 21)
+    q = torch.randn(2, 8, Sq, 64, generator=ref.rng(22)).bfloat16()
+    check_fwd(c, q, scale=scale)
+
+
+@pytest.mark.parametrize("Sq", [1, 40])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_fwd_block_scales_of_unlike_size(dtype, Sq):
+    """Any positive scales, 2^-10 to 2^10 apart; rows of unlike size."""
+    c = ref.filled(2, 2, 500, 128, 16, [500, 123], 31)
+    g = ref.rng(32)
+    for n in "kv":
+        f = torch.exp2(20 * torch.rand(c.scale[n].shape, generator=g) - 10)
+        s = (c.scale[n] * f * (0.02 if n == "k" else 1)).float().double()
+        c.scale[n] = torch.where(c.scale[n].isfinite(), s, c.scale[n])
+    q = torch.randn(2, 4, Sq, 128, generator=g)
+    q = (q * torch.exp2(8 * torch.rand(2, 4, Sq, 1, generator=g) - 8)
+         ).to(DT[dtype])
+    check_fwd(c, q, scale=0.02)
+
+
+@pytest.mark.parametrize("Sq", [1, 30])
+def test_fwd_tiny_and_huge_queries(Sq):
+    c = ref.filled(1, 1, 100, 64, 16, [100], 41)
+    q = torch.randn(1, 2, Sq, 64, generator=ref.rng(42))
+    check_fwd(c, (q * 1e-30).bfloat16())
+    check_fwd(c, (q * 1e30).bfloat16(), scale=1e-30)
+    check_fwd(c, (q * 1e-5).half(), scale=100.0)
+
+
+@pytest.mark.parametrize("Sq", [1, 30])
+def test_fwd_nan_stays_in_its_row(Sq):
+    c = ref.filled(1, 1, 100, 64, 16, [100], 41)
+    q = torch.randn(1, 3, Sq, 64, generator=ref.rng(43)).half()
+    clean, lse, _, _ = run_fwd(c, q, with_w=False)
+    q[0, 1, Sq - 1, 5] = math.nan
+    out, lse2, _, _ = run_fwd(c, q, with_w=False)
+    assert bool(out[0, 1, Sq - 1].isnan().all())
+    assert bool(lse2[0, 1, Sq - 1].isnan())
+    keep = torch.ones(3, Sq, dtype=torch.bool)
+    keep[1, Sq - 1] = False
+    assert torch.equal(out[0][keep], clean[0][keep])
+    assert torch.equal(lse2[0][keep], lse[0][keep])
+
+
+@pytest.mark.parametrize("Sq", [1, 48])
+def test_fwd_is_deterministic_and_replays_in_a_graph(Sq):
+    c = ref.filled(3, 2, 700, 128, 64, [700, 3, 350], 51)
+    q = torch.randn(3, 8, Sq, 128, generator=ref.rng(52)).bfloat16()
+    first = run_fwd(c, q)
+    again = run_fwd(c, q)
+    for a, b in zip(first[:3], again[:3]):
+        assert torch.equal(a, b)
+    gpu, qd = upload(c), q.cuda()
+    out, lse = torch.zeros_like(qd), torch.zeros(3, 8, Sq).cuda()
+    w = first[3].cuda()
+    ws = attn.kv8_workspace(gpu, 8, Sq, True)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        attn.kv8_fwd(gpu, qd, weights=w, out=out, lse=lse, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), first[0])
+    assert torch.equal(lse.cpu(), first[1])
+    assert torch.equal(w.cpu(), first[2])
+    # Other lengths and queries, the same graph.
+    c.lens = [100, 0, 699]
+    q2 = torch.randn(3, 8, Sq, 128, generator=ref.rng(53)).bfloat16()
+    want = run_fwd(c, q2)
+    gpu.lens.copy_(torch.tensor(c.lens, dtype=torch.int32))
+    qd.copy_(q2)
+    w.copy_(first[3])
+    graph.replay()
+    torch.cuda.synchronize()
+    # The last sequence now reaches the NaN codes behind its tokens: bits.
+    assert torch.equal(out.cpu().view(torch.int16), want[0].view(torch.int16))
+    assert torch.equal(w.cpu().view(torch.int32), want[2].view(torch.int32))
+
+
+def test_fwd_two_streams_at_once():
+    c = ref.filled(2, 2, 900, 64, 32, [900, 450], 61)
+    q = [torch.randn(2, 4, 3, 64, generator=ref.rng(s)).half()
+         for s in (62, 63)]
+    want = [run_fwd(c, x)[:2] for x in q]
+    gpu, qd = upload(c), [x.cuda() for x in q]
+    ws = [attn.kv8_workspace(gpu, 4, 3) for _ in q]
+    got = [(torch.zeros_like(x), torch.zeros(2, 4, 3).cuda()) for x in qd]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, w, (o, l), s in zip(qd, ws, got, streams):
+            attn.kv8_fwd(gpu, x, out=o, lse=l, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for (o, l), (a, b) in zip(got, want):
+        assert torch.equal(o.cpu(), a) and torch.equal(l.cpu(), b)
+
+
+# ---------------------------------------------------------------- eviction
+
+EVICTS = [
+    # B, H, cap, D, block, lens, keep, recent
+    (1, 1, 20, 64, 16, [20], 1, 0),
+    (1, 1, 20, 64, 16, [20], 1, 1),
+    (2, 2, 100, 128, 16, [100, 40], 50, 10),
+    (3, 2, 300, 64, 64, [0, 300, 299], 299, 5),
+    (2, 3, 515, 128, 128, [515, 514], 129, 129),
+    (2, 1, 1000, 64, 32, [1000, 33], 700, 0),
+    (1, 2, 5000, 128, 64, [4999], 1234, 200),
+    (4, 1, 64, 64, 16, [64, 1, 63, 32], 64, 3),
+]
+
+
+def some_weights(B, H, cap, seed):
+    """Weights with many equal values, zeros of both signs and NaN."""
+    g = ref.rng(seed)
+    w = (torch.rand(B, H, cap, generator=g) * 8).floor() / 4
+    w = torch.where(w == 0.25, -0.0, w)
+    fine = torch.rand(B, H, cap, generator=g)
+    w = torch.where(fine > 0.6, fine, w)
+    return torch.where(fine < 0.02, math.nan, w)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", EVICTS)
+def test_evict(case, in_place):
+    B, H, cap, D, block, lens, keep, recent = case
+    c = ref.filled(B, H, cap, D, block, lens, 71)
+    g = ref.rng(72)
+    for n in "kv":  # blocks of unlike size, so that codes get requantised
+        f = torch.exp2((12 * torch.rand(c.scale[n].shape, generator=g)).floor())
+        c.scale[n] *= f
+    w = some_weights(B, H, cap, 73)
+    room = cap if in_place else keep + 7
+    want, ow, idx = c.evict(w, keep, recent, room)
+    gpu, wd = upload(c), w.cuda()
+    if in_place:
+        # What lies behind the kept tokens' last block stays.
+        for n in "kv":
+            for b in range(B):
+                m = want.lens[b]
+                nb = -(-m // block)
+                want.code[n][b, :, m:] = c.code[n][b, :, m:]
+                want.scale[n][b, :, nb:] = c.scale[n][b, :, nb:]
+        out, out_w, got = attn.kv8_evict(gpu, wd, keep, recent)
+        assert out_w is wd and out.k is gpu.k
+    else:
+        dst = upload(ref.Cache(B, H, room, D, block))
+        before = upload(c)
+        out, out_w, got = attn.kv8_evict(gpu, wd, keep, recent, out=dst)
+        for n in ("k", "v"):  # the source stays
+            assert torch.equal(getattr(gpu, n), getattr(before, n))
+        assert torch.equal(wd.cpu().nan_to_num(9), w.nan_to_num(9))
+    torch.cuda.synchronize()
+    assert torch.equal(got.cpu(), idx)
+    assert torch.equal(out_w.cpu().nan_to_num(9), ow.nan_to_num(9))
+    same_cache(out, want)
+    assert gpu.lens.cpu().tolist() == lens
+
+
+# ------------------------------------------------------------- all together
+
+def test_a_serving_run():
+    """Prompt, weights, eviction, then decoding steps over the smaller cache,
+    each against the reference on the same state."""
+    B, H, g, D, block, cap = 2, 2, 4, 64, 32, 400
+    c = ref.Cache(B, H, cap, D, block)
+    gpu = upload(c)
+    wd, w = torch.zeros(B, H, cap).cuda(), None
+    prompt = [300, 170]
+    x = [torch.randn(B, H, 300, D, generator=ref.rng(s)).bfloat16()
+         for s in (81, 82)]
+    q = torch.randn(B, H * g, 300, D, generator=ref.rng(83)).bfloat16()
+    c.lens = list(prompt)
+    gpu.lens.copy_(torch.tensor(prompt, dtype=torch.int32))
+    attn.kv8_append(gpu, x[0].cuda(), x[1].cuda(), new_lens=counts(prompt))
+    c.append(x[0], x[1], new=prompt)
+    same_cache(gpu, c)
+    check_fwd(c, q, new=prompt, gpu=gpu)
+    attn.kv8_fwd(gpu, q.cuda(), new_lens=counts(prompt), weights=wd)
+    w = wd.cpu()
+    small = attn.KV8Cache.empty(B, H, 128, D, block)
+    for t in ("k", "v"):
+        getattr(small, t).view(torch.uint8).fill_(0x7F)
+        getattr(small, t + "_scale").fill_(math.inf)
+    small, sw, idx = attn.kv8_evict(gpu, wd, 100, recent=20, out=small)
+    c, w_small, idx_r = c.evict(w, 100, 20, 128)
+    assert torch.equal(idx.cpu(), idx_r)
+    same_cache(small, c)
+    for step in range(12):
+        x = [torch.randn(B, H, 1, D, generator=ref.rng(90 + 2 * step + s))
+             .bfloat16() for s in (0, 1)]
+        q = torch.randn(B, H * g, 1, D, generator=ref.rng(200 + step)
+                        ).bfloat16()
+        small.lens += 1
+        c.lens = [n + 1 for n in c.lens]
+        attn.kv8_append(small, x[0].cuda(), x[1].cuda())
+        c.append(x[0], x[1])
+        same_cache(small, c)
+        check_fwd(c, q, gpu=small)
+        attn.kv8_fwd(small, q.cuda(), weights=sw)
+        if step == 6:  # in place, between two steps
+            ws = sw.cpu()
+            small, sw, idx = attn.kv8_evict(small, sw, 60, recent=8)
+            behind = c
+            c, _, idx_r = c.evict(ws, 60, 8, 128)
+            assert torch.equal(idx.cpu(), idx_r)
+            for n in "kv":  # the freed places keep what they held
+                for b in range(B):
+                    nb = -(-c.lens[b] // block)
+                    c.code[n][b, :, c.lens[b]:] = \
+                        behind.code[n][b, :, c.lens[b]:]
+                    c.scale[n][b, :, nb:] = behind.scale[n][b, :, nb:]
+            same_cache(small, c)
+
+
+# ---------------------------------------------------- lengths out of range
+
+def test_lengths_out_of_range_are_clamped_and_reported():
+    c = ref.filled(2, 1, 64, 64, 16, [64, 10], 91)
+    q = torch.randn(2, 2, 1, 64, generator=ref.rng(92)).half()
+    gpu = upload(c)
+    want = attn.kv8_fwd(gpu, q.cuda())[0]
+    gpu.lens.copy_(torch.tensor([70, 10], dtype=torch.int32))
+    got = attn.kv8_fwd(gpu, q.cuda())[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert attn.attn_device_status() == (attn.ATTN_ERR_INVALID_ARG, 2)
+    gpu.lens.copy_(torch.tensor([-3, 10], dtype=torch.int32))
+    got = attn.kv8_fwd(gpu, q.cuda())[0]
+    torch.cuda.synchronize()
+    assert bool((got[0] == 0).all()) and torch.equal(got[1], want[1])
+    assert attn.attn_device_status() == (attn.ATTN_ERR_INVALID_ARG, 2)
+    assert attn.attn_device_status() == (0, 0)
