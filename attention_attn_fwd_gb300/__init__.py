@@ -649,13 +649,34 @@ class KV8Cache:
 
 def _check_tensor(name, t, shape, dtype, device):
     """A contiguous tensor of this shape and type on this device."""
-    if tuple(t.shape) != shape or (dtype is not None and t.dtype != dtype):
+    if t.shape != shape or (dtype is not None and t.dtype != dtype):
         raise AttnError("%s must be %s of %s, got %s of %s" % (
             name, list(shape), dtype or "float16 or bfloat16",
             list(t.shape), t.dtype), ATTN_ERR_INVALID_ARG)
     if t.device != device or not t.is_contiguous():
         raise AttnError("%s must be a contiguous tensor on the cache's device"
                         % name, ATTN_ERR_INVALID_ARG)
+
+
+def _kv8_call(name, cache, stream, *args):
+    """Calls a C entry point with ``cache``'s device current, on ``stream``
+    or torch's current stream there.  (A decoding step of a small model waits
+    for the host: switching devices is skipped where none is needed, and the
+    stream's handle is taken without building a Stream object.)"""
+    import torch
+    index = cache.device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream.cuda_stream
+    f = getattr(_lib or load_library(), name)
+    if torch.cuda.current_device() == index:
+        st = f(cache.struct, *args, handle or None)
+    else:
+        with torch.cuda.device(index):
+            st = f(cache.struct, *args, handle or None)
+    if st != ATTN_OK:
+        raise AttnError("%s: %s" % (name, attn_status_string(st)), st)
 
 
 def kv8_append(cache, k, v, new_lens=None, stream=None):
@@ -677,15 +698,9 @@ def kv8_append(cache, k, v, new_lens=None, stream=None):
     if new_lens is not None:
         _check_tensor("new_lens", new_lens, (cache.B,), torch.int32,
                       cache.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device)
-    with torch.cuda.device(cache.device):
-        st = attn_kv8_append(
-            cache, k.data_ptr(), v.data_ptr(), Sq,
-            new_lens.data_ptr() if new_lens is not None else 0, dt,
-            stream.cuda_stream)
-    if st != ATTN_OK:
-        raise AttnError("attn_kv8_append: " + attn_status_string(st), st)
+    _kv8_call("attn_kv8_append", cache, stream, k.data_ptr() or None,
+              v.data_ptr() or None, Sq,
+              new_lens.data_ptr() if new_lens is not None else None, dt)
 
 
 def kv8_workspace(cache, Hq, Sq, weights=False):
@@ -715,7 +730,7 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     dt = _dtype_code(q)
     if q.dim() != 4:
         raise AttnError("q must be 4-D [B, Hq, Sq, D]", ATTN_ERR_INVALID_ARG)
-    B, Hq, Sq, D = q.shape
+    B, Hq, Sq, D = shape = q.shape
     dev = cache.device
     _check_tensor("q", q, (cache.B, Hq, Sq, cache.D), None, dev)
     if new_lens is not None:
@@ -726,7 +741,7 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_tensor("out", out, (B, Hq, Sq, D), q.dtype, dev)
+        _check_tensor("out", out, shape, q.dtype, dev)
     if not need_lse:
         lse = None
     elif lse is None:
@@ -737,18 +752,12 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
         workspace = kv8_workspace(cache, Hq, Sq, weights is not None)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        st = attn_kv8_fwd(
-            cache, q.data_ptr(), out.data_ptr(),
-            lse.data_ptr() if lse is not None else 0,
-            weights.data_ptr() if weights is not None else 0, Hq, Sq,
-            new_lens.data_ptr() if new_lens is not None else 0, scale, causal,
-            dt, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), stream.cuda_stream)
-    if st != ATTN_OK:
-        raise AttnError("attn_kv8_fwd: " + attn_status_string(st), st)
+    _kv8_call("attn_kv8_fwd", cache, stream, q.data_ptr() or None,
+              out.data_ptr() or None,
+              lse.data_ptr() if lse is not None else None,
+              weights.data_ptr() if weights is not None else None, Hq, Sq,
+              new_lens.data_ptr() if new_lens is not None else None, scale,
+              bool(causal), dt, workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
@@ -768,6 +777,9 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
     """
     import torch
     dev = cache.device
+    keep, recent = int(keep), int(recent)
+    if keep < 1:
+        raise AttnError("keep must be at least 1", ATTN_ERR_INVALID_ARG)
     _check_tensor("weights", weights, (cache.B, cache.Hkv, cache.capacity),
                   torch.float32, dev)
     if out is None:
@@ -783,19 +795,12 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
         out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         _check_tensor("out_weights", out_weights, shape, torch.float32, dev)
-    shape = (cache.B, cache.Hkv, int(keep))
-    if keep < 1:
-        raise AttnError("keep must be at least 1", ATTN_ERR_INVALID_ARG)
+    shape = (cache.B, cache.Hkv, keep)
     if indices is None:
         indices = torch.empty(shape, dtype=torch.int32, device=dev)
     else:
         _check_tensor("indices", indices, shape, torch.int32, dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        st = attn_kv8_evict(cache, out, weights.data_ptr(),
-                            out_weights.data_ptr(), int(keep), int(recent),
-                            indices.data_ptr(), stream.cuda_stream)
-    if st != ATTN_OK:
-        raise AttnError("attn_kv8_evict: " + attn_status_string(st), st)
+    _kv8_call("attn_kv8_evict", cache, stream, out.struct,
+              weights.data_ptr() or None, out_weights.data_ptr() or None,
+              keep, recent, indices.data_ptr() or None)
     return out, out_weights, indices

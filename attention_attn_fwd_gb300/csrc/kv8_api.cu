@@ -97,7 +97,7 @@ RowPlan plan_rows(int Hq, int Hkv, int Sq, int sms) {
   r.rows = static_cast<long long>(Hq / Hkv) * Sq;
   r.tile = r.rows <= 8 ? 8 : 16;
   r.blocks = (r.rows + r.tile - 1) / r.tile;
-  r.grid = sms * (r.tile == 8 ? 2 : 1);
+  r.grid = sms;
   return r;
 }
 
@@ -205,7 +205,7 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   const long long segs = static_cast<long long>(heads(*c)) * rp.blocks;
   const long long tiles = (c->capacity - 1LL) / 512 + 1;
   if (rp.rows > 0x7fffffffLL - 1024 || segs > 0x7fffffffLL ||
-      static_cast<long long>(heads(*c)) * tiles * 4 > 0x7fffffffLL)
+      segs * (rp.tile + tiles) > 0x7fffffffLL)
     return ATTN_ERR_INVALID_ARG;
   st = check_cache_memory(*c, dev);
   if (st != ATTN_OK) return st;

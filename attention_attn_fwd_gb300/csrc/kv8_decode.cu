@@ -2,32 +2,36 @@
 // merge of its partial results.
 //
 // Mathematics: flash-decoding.  The keys of all (batch, K/V head) segments
-// form one list of 16-key tiles, cut into equal consecutive shares, one per
-// CTA; a CTA's warps take its tiles in turn, each with its own running
-// maximum m, sum l and accumulator O, which meet in shared memory at the end
-// of a segment.  A partial result goes to workspace slot (CTA + segment):
-// both only grow along the list, so no two share one.  The merge kernel
-// joins a segment's partials by their maxima.  Lengths come from device
-// memory, so the cut follows them without the host's knowing: ragged batches
-// are balanced to a tile.
+// form one list of tiles (2 KB of K codes each), cut into equal consecutive
+// shares, one per CTA; a CTA's warps take its tiles in turn, each with its
+// own running maximum m, sum l and accumulator O, which meet in shared memory
+// at the end of a segment.  A partial result goes to workspace slot
+// (CTA + segment): both only grow along the list, so no two share one.  The
+// merge kernel joins a segment's partials by their maxima.  Lengths come from
+// device memory, so the cut follows them without the host's knowing: ragged
+// batches are balanced to a tile.
 //
 // Products: S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16 in fp16,
-// 16 keys (or 16 of D) by 8 query rows.  E4M3 codes are fp16 values, so
-// K and V convert exactly; Q is multiplied by a power of two per row that
-// brings its largest element to [2^13, 2^14), which makes bf16 -> fp16 exact
-// down to 2^-37 of the row's largest element (below fp32 accumulation's own
-// rounding).  Block scales multiply scores and weights in fp32.  P is rounded
-// to fp16 (2^-11 relative, the rounding of the 16-bit output itself or less)
-// with 2^7 of headroom used up so that weights down to 2^-29 of the row's
-// largest stay normal numbers.  The row sums take P unrounded.
+// 16 keys (or 16 of D) by 8 query rows: with 8 or 16 rows a 128-row
+// tcgen05 tile would be nearly empty, and the codes' bytes bound the kernel.
+// E4M3 codes are fp16 values, so K and V convert exactly; Q is multiplied by
+// a power of two per row that brings its largest element to [2^13, 2^14),
+// which makes bf16 -> fp16 exact down to 2^-37 of the row's largest element
+// (below fp32 accumulation's own rounding).  Block scales multiply scores and
+// weights in fp32.  P is rounded to fp16 (2^-11 relative, the rounding of an
+// fp16 output itself and an eighth of a bf16 one's), shifted by 2^7 so that
+// weights down to 2^-21 of the row's largest stay normal numbers.  The row
+// sums take P unrounded.
 //
-// Codes go from global memory straight to the registers of the lanes whose
-// MMA fragments need them, 16 bytes at a time: the d index of both products
-// may be permuted freely, so lane c of a quad owns bytes 16c.. of a 64-byte
-// half row of K (fragment columns) and lane group g8 owns bytes 16 g8.. of
-// four V rows.  No shared memory, no transposes but a byte permute and one
-// movmatrix per 8 x 8 weights.  Bound by the bytes of the codes: tiles are
-// prefetched one ahead per warp, about 64 KB in flight per SM.
+// Codes reach shared memory by 16-byte asynchronous copies, a ring of tiles
+// per warp that runs ahead across segments (190 KB in flight per SM; with the
+// codes loaded straight to registers one tile ahead, 64 KB, the kernel ran
+// at 2.8 TB/s on 8 x 4096 tokens and 4.4 TB/s on 131072).  Fragments are read
+// 16 bytes at a time: the d index of both products may be permuted freely, so
+// lane c of a quad owns bytes 16c.. of a 64-byte half row of K and lane group
+// g8 owns bytes (D/8) g8.. of four V rows; 16-byte chunks of a row are stored
+// XORed by its row so that those reads do not share banks.  No transposes but
+// a byte permute and one movmatrix per 8 x 8 weights.
 #include "kv8_common.cuh"
 
 namespace attn {
@@ -36,9 +40,14 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;          // keys per warp step
 constexpr float kTau = 8.f;        // lazy rescale threshold (log2 units)
 constexpr float kPScale = 128.f;   // 2^7: P <= 2^(8 + 7) < 65504
+
+// Keys of a list tile: 2 KB of K codes.
+template <int D>
+__host__ __device__ constexpr int tile_keys() {
+  return 2048 / D;
+}
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1,
                                         uint32_t a2, uint32_t a3, uint32_t b0,
@@ -58,24 +67,37 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
-// Codes are read once: keep them out of L1.
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p) {
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
                : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-// The list of tiles: sequence b contributes Hkv * row_blocks segments of
-// ceil(lens[b] / 16) tiles.
+// Exponent of the power of two that brings a query row's largest element to
+// [2^13, 2^14) (rows of zeros or of the smallest numbers: as far as it goes).
+__device__ __forceinline__ int row_shift(float amax) {
+  const int e = (__float_as_int(amax) >> 23) - 127;
+  return max(-114, min(13 - e, 126));
+}
+
+// 16-byte asynchronous copy past L1; `bytes` 0 writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src,
+                                           int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ int seq_len(const FwdParams& p, int b) {
   return clamp_len(p.lens[b], p.capacity, p.status);
 }
@@ -84,18 +106,31 @@ __device__ __forceinline__ int seq_new(const FwdParams& p, int b) {
                                : clamp_len(p.new_lens[b], p.Sq, p.status);
 }
 
-// Tiles of all sequences before `end` (every lane of the warp gets the sum).
-__device__ __forceinline__ long long tiles_before(const FwdParams& p, int end,
-                                                  int lane) {
-  long long t = 0;
-  for (int b = lane; b < end; b += 32)
-    t += (seq_len(p, b) + kTile - 1) / kTile;
+// The list of tiles: sequence b contributes Hkv * row_blocks segments of
+// ceil(lens[b] / kKeys) tiles.  Every lane of the calling warp gets the tiles
+// of all sequences (total) and of those before `seq`; up to 32 sequences take
+// one load per lane.
+template <int kKeys>
+__device__ __forceinline__ long long list_tiles(const FwdParams& p, int seq,
+                                                int lane, long long* before) {
+  long long t = 0, pre = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const int n = (seq_len(p, b) + kKeys - 1) / kKeys;
+    t += n;
+    if (b < seq) pre += n;
+  }
 #pragma unroll
-  for (int s = 16; s > 0; s /= 2) t += __shfl_xor_sync(0xffffffffu, t, s);
-  return t * p.Hkv * p.row_blocks;
+  for (int s = 16; s > 0; s /= 2) {
+    t += __shfl_xor_sync(0xffffffffu, t, s);
+    pre += __shfl_xor_sync(0xffffffffu, pre, s);
+  }
+  const int segs = p.Hkv * p.row_blocks;
+  *before = pre * segs;
+  return t * segs;
 }
 
 // Sequence that holds list position x (x < total), and the tiles before it.
+template <int kKeys>
 __device__ __forceinline__ int find_seq(const FwdParams& p, long long x,
                                         int lane, long long* before) {
   long long base = 0;
@@ -103,7 +138,7 @@ __device__ __forceinline__ int find_seq(const FwdParams& p, long long x,
     const int b = b0 + lane;
     long long t = 0;
     if (b < p.B)
-      t = static_cast<long long>((seq_len(p, b) + kTile - 1) / kTile) *
+      t = static_cast<long long>((seq_len(p, b) + kKeys - 1) / kKeys) *
           p.Hkv * p.row_blocks;
     long long incl = t;
 #pragma unroll
@@ -130,6 +165,28 @@ __device__ __forceinline__ long long shares(const FwdParams& p,
   return most < p.grid ? (most > 0 ? most : 1) : p.grid;
 }
 
+// A place in a CTA's share of the list.  pos counts tiles from the share's
+// start; the segment it lies in covers [seg_pos, seg_end).
+struct Cursor {
+  int pos, seg_pos, seg_end;  // seg_pos may be negative (share starts inside)
+  int b, seg;                 // sequence, segment of it
+  int len, tiles;
+};
+
+template <int kKeys>
+__device__ __forceinline__ void next_segment(const FwdParams& p, Cursor& c) {
+  c.seg_pos = c.seg_end;
+  if (++c.seg == p.Hkv * p.row_blocks) {
+    c.seg = 0;
+    do {  // some later sequence has tokens: the share is not at its end
+      ++c.b;
+      c.len = seq_len(p, c.b);
+    } while (c.len == 0);
+    c.tiles = (c.len + kKeys - 1) / kKeys;
+  }
+  c.seg_end = c.seg_pos + c.tiles;
+}
+
 // Visible tokens of row r (token-major: row r = token r / group, head
 // r % group) of a sequence.
 __device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
@@ -138,69 +195,68 @@ __device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
   return min(len, max(0, len - n_new + r / p.group + 1));
 }
 
-// One tile's codes in registers: K rows g8 and g8 + 8, V rows 2c, 2c + 1,
-// 2c + 8, 2c + 9 of the tile.
+// One tile of a warp's ring: 2 KB of K codes, then 2 KB of V codes.  Chunk j
+// (16 bytes) of row r lies at chunk j ^ swizzle(r): the rows read together by
+// the 8 lanes of a phase (K: rows 2q, 2q + 1; V: rows of one parity) then lie
+// in different banks (64-byte V rows: two lanes share one).
 template <int D>
-struct Codes {
-  static constexpr int kHalves = D / 64;   // 64-byte halves of a K row
-  static constexpr int kVWords = D / 32;   // words of a V row per lane
-  uint32_t k[2][kHalves][4];
-  uint32_t v[4][kVWords];
-};
-
+__device__ __forceinline__ int k_swizzle(int r) {
+  return D == 128 ? (r & 1) << 2 : 0;
+}
 template <int D>
-__device__ __forceinline__ void load_k(Codes<D>& t, const uint8_t* k, int key0,
-                                       int len, int g8, int c) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int key = key0 + g8 + 8 * i;
-#pragma unroll
-    for (int h = 0; h < Codes<D>::kHalves; ++h) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (key < len)
-        w = ld_codes16(k + static_cast<long long>(key) * D + 64 * h + 16 * c);
-      t.k[i][h][0] = w.x;
-      t.k[i][h][1] = w.y;
-      t.k[i][h][2] = w.z;
-      t.k[i][h][3] = w.w;
-    }
-  }
+__device__ __forceinline__ int v_swizzle(int r) {
+  return D == 128 ? ((r >> 1) & 3) << 1 : ((r >> 1) & 1) << 1;
 }
 
 template <int D>
-__device__ __forceinline__ void load_v(Codes<D>& t, const uint8_t* v, int key0,
-                                       int len, int g8, int c) {
+__device__ __forceinline__ void copy_tile(uint32_t dst, const FwdParams& p,
+                                          const Cursor& c, int lane) {
+  constexpr int kPerRow = D / 16;
+  constexpr int kKeys = tile_keys<D>();
+  const int h = c.seg / p.row_blocks;
+  const long long head =
+      (static_cast<long long>(c.b) * p.Hkv + h) * p.capacity * D;
+  const int key0 = (c.pos - c.seg_pos) * kKeys;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int key = key0 + 2 * c + (i & 1) + 8 * (i >> 1);
-    const uint8_t* at = v + static_cast<long long>(key) * D + (D / 8) * g8;
-    if constexpr (D == 128) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (key < len) w = ld_codes16(at);
-      t.v[i][0] = w.x;
-      t.v[i][1] = w.y;
-      t.v[i][2] = w.z;
-      t.v[i][3] = w.w;
-    } else {
-      uint2 w = make_uint2(0u, 0u);
-      if (key < len) w = ld_codes8(at);
-      t.v[i][0] = w.x;
-      t.v[i][1] = w.y;
-    }
+    const int ch = lane + 32 * i;
+    const int r = ch / kPerRow, j = ch % kPerRow;
+    const bool in = key0 + r < c.len;
+    const long long at =
+        head + static_cast<long long>(in ? key0 + r : 0) * D + 16 * j;
+    const int bytes = in ? 16 : 0;  // rows past the length become zeros
+    cp_async16(dst + r * D + ((j ^ k_swizzle<D>(r)) << 4), p.k + at, bytes);
+    cp_async16(dst + 2048 + r * D + ((j ^ v_swizzle<D>(r)) << 4), p.v + at,
+               bytes);
   }
 }
 
 // NT: 8-row groups of query rows a CTA holds (8 or 16 rows of a K/V head).
+template <int D, int NT>
+struct Ring {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kPitch = D + 4;  // floats: rows start 4 banks apart
+  static constexpr int kStages = NT == 1 ? 6 : 5;
+  static constexpr int kRingBytes = kWarps * kStages * 4096;
+  static constexpr int kMergeBytes = kWarps * kRows * (kPitch + 2) * 4;
+  static constexpr int kBytes = kRingBytes + kMergeBytes;
+  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+};
+
 template <int D, int NT, bool kBF16>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 1)
     kv8_decode_kernel(const FwdParams p) {
-  constexpr int kRows = 8 * NT;
+  using R = Ring<D, NT>;
+  constexpr int kRows = R::kRows;
+  constexpr int kPitch = R::kPitch;
+  constexpr int kStages = R::kStages;
+  constexpr int kKeys = tile_keys<D>();
+  constexpr int kSub = kKeys / 16;  // 16-key steps per tile
   constexpr int kKSteps = D / 16;
-  constexpr int kMT = D / 16;      // m-tiles of O^T
-  extern __shared__ float smem[];  // [kWarps][kRows][D + 4], then m, l
-  constexpr int kPitch = D + 4;    // floats: rows start 4 banks apart
-  float* sm_o = smem;
-  float* sm_m = smem + kWarps * kRows * kPitch;  // [kWarps][kRows]
+  constexpr int kMT = D / 16;       // m-tiles of O^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* sm_o = reinterpret_cast<float*>(smem + R::kRingBytes);
+  float* sm_m = sm_o + kWarps * kRows * kPitch;  // [kWarps][kRows]
   float* sm_l = sm_m + kWarps * kRows;           // [kWarps][kRows]
 
   // The merge kernel may be scheduled early: its CTAs wait for this grid.
@@ -208,40 +264,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g8 = lane / 4, c = lane % 4;
-  const long long total = tiles_before(p, p.B, lane);
+  long long unused;
+  const long long total = list_tiles<kKeys>(p, 0, lane, &unused);
   const long long n_cta = shares(p, total);
   const int cta = blockIdx.x;
   if (cta >= n_cta) return;
-  long long at = total * cta / n_cta;
-  const long long end = total * (cta + 1) / n_cta;
-  if (at >= end) return;
+  const long long first = total * cta / n_cta;
+  const int count = static_cast<int>(total * (cta + 1) / n_cta - first);
+  if (count == 0) return;
 
-  long long before;
-  int b = find_seq(p, at, lane, &before);
-  while (at < end) {
-    int len = seq_len(p, b);
-    long long tiles = (len + kTile - 1) / kTile;
-    while (at - before >= tiles * p.Hkv * p.row_blocks) {  // next sequence
-      before += tiles * p.Hkv * p.row_blocks;
-      ++b;
-      len = seq_len(p, b);
-      tiles = (len + kTile - 1) / kTile;
+  // The share's first segment.
+  Cursor seg;
+  {
+    long long before;
+    seg.b = find_seq<kKeys>(p, first, lane, &before);
+    seg.len = seq_len(p, seg.b);
+    seg.tiles = (seg.len + kKeys - 1) / kKeys;
+    seg.seg = static_cast<int>((first - before) / seg.tiles);
+    seg.seg_pos = -static_cast<int>((first - before) % seg.tiles);
+    seg.seg_end = seg.seg_pos + seg.tiles;
+    seg.pos = 0;
+  }
+  // This warp's loads run ahead of its products.
+  const uint32_t ring =
+      ptx::smem_u32(smem) + warp * kStages * 4096;
+  Cursor ld = seg;
+  ld.pos = warp;
+  auto load_next = [&](int stage) {
+    if (ld.pos < count) {
+      while (ld.pos >= ld.seg_end) next_segment<kKeys>(p, ld);
+      copy_tile<D>(ring + stage * 4096, p, ld, lane);
+      ld.pos += kWarps;
     }
-    const int seg_in_b = static_cast<int>((at - before) / tiles);
-    const int t_first = static_cast<int>((at - before) % tiles);
-    const int t_last = static_cast<int>(
-        min(tiles, static_cast<long long>(t_first) + (end - at)));
-    at += t_last - t_first;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) load_next(i);
 
-    const int h = seg_in_b / p.row_blocks;
-    const int rb = seg_in_b - h * p.row_blocks;
+  int stage = 0;
+  int pos = warp;  // this warp's next tile
+  while (true) {
+    const int seg_last = min(seg.seg_end, count);  // end of the CTA's part
+    const int b = seg.b, len = seg.len;
+    const int h = seg.seg / p.row_blocks;
+    const int rb = seg.seg - h * p.row_blocks;
     const int r0 = rb * kRows;
     const int bh = b * p.Hkv + h;
     const int n_new = seq_new(p, b);
-    const int n_rows = min(kRows, n_new * p.group - r0);  // valid rows
-    if (n_rows <= 0) continue;
-    const int min_end = row_end(p, len, n_new, r0);
-    const int max_end = row_end(p, len, n_new, r0 + n_rows - 1);
+    const int n_rows = max(0, min(kRows, n_new * p.group - r0));  // valid rows
+    const int min_end = n_rows > 0 ? row_end(p, len, n_new, r0) : 0;
+    const int max_end =
+        n_rows > 0 ? row_end(p, len, n_new, r0 + n_rows - 1) : 0;
 
     // This lane's two query rows per 8-row group (columns of S^T): how many
     // tokens they see, and the factor of their scores.
@@ -275,9 +348,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // Power of two that brings the row's largest element to [2^13, 2^14).
-      const int ex = (__float_as_int(amax) >> 23) - 127;
-      const int up = max(-114, min(13 - ex, 126));
+      const int up = row_shift(amax);
       const float f_up = exp2_int(up);
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf)
@@ -298,8 +369,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
     }
 
-    const uint8_t* kb = p.k + static_cast<long long>(bh) * p.capacity * D;
-    const uint8_t* vb = p.v + static_cast<long long>(bh) * p.capacity * D;
     const float* ksb = p.k_scale + static_cast<long long>(bh) * p.nblk;
     const float* vsb = p.v_scale + static_cast<long long>(bh) * p.nblk;
 
@@ -315,147 +384,189 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
 
-    // Tiles past every row's horizon hold nothing for this row block.
-    const int t_stop = min(t_last, (max_end + kTile - 1) / kTile);
-    Codes<D> cur;
-    int t = t_first + warp;
-    float ks = 0.f, vs = 0.f;
-    if (t < t_stop) {
-      load_k<D>(cur, kb, t * kTile, len, g8, c);
-      load_v<D>(cur, vb, t * kTile, len, g8, c);
-      ks = __ldg(ksb + ((t * kTile) >> p.block_shift));
-      vs = __ldg(vsb + ((t * kTile) >> p.block_shift));
-    }
-    for (; t < t_stop; t += kWarps) {
-      const int key0 = t * kTile;
-      const int t_next = t + kWarps;
-      const bool more = t_next < t_stop;
-      // S^T tile.
-      float s[NT][4];
+    // Block scales of a tile's 16-key steps, fetched one tile ahead.
+    float ks[kSub], vs[kSub];
+    auto load_scales = [&](int at) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-#pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_half2(cur.k[0][hf][w], a0, a2);
-          e4m3x4_to_half2(cur.k[1][hf][w], a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(s[nt], a0, a1, a2, a3, bq[nt][4 * hf + w][0],
-                    bq[nt][4 * hf + w][1]);
+      for (int u = 0; u < kSub; ++u) {
+        const int key = (at - seg.seg_pos) * kKeys + 16 * u;
+        ks[u] = vs[u] = 0.f;
+        if (at < seg_last && key < len) {
+          ks[u] = __ldg(ksb + (key >> p.block_shift));
+          vs[u] = __ldg(vsb + (key >> p.block_shift));
         }
-      const float ks_now = ks, vs_now = vs;
-      if (more) {
-        load_k<D>(cur, kb, t_next * kTile, len, g8, c);
-        ks = __ldg(ksb + ((t_next * kTile) >> p.block_shift));
-        vs = __ldg(vsb + ((t_next * kTile) >> p.block_shift));
       }
-      // Scores in log2 units; hidden ones are -inf.
-      bool grow = false;
+    };
+    load_scales(pos);
+    for (; pos < seg_last; pos += kWarps) {
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      float ks_now[kSub], vs_now[kSub];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < kSub; ++u) {
+        ks_now[u] = ks[u];
+        vs_now[u] = vs[u];
+      }
+      load_scales(pos + kWarps);
+      const uint32_t tile = ring + stage * 4096;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] *= mult[nt][e & 1] * ks_now;
-      if (key0 + kTile > min_end) {
+      for (int u = 0; u < kSub; ++u) {
+        const int key0 = (pos - seg.seg_pos) * kKeys + 16 * u;
+        if (key0 >= max_end) continue;  // past every row's horizon
+        // S^T of 16 keys, in two chains.
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf) {
+          uint4 kr[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 16 * u + g8 + 8 * i;
+            kr[i] = ptx::ld_shared_v4(
+                tile + r * D + (((4 * hf + c) ^ k_swizzle<D>(r)) << 4));
+          }
+          const uint32_t k0[4] = {kr[0].x, kr[0].y, kr[0].z, kr[0].w};
+          const uint32_t k1[4] = {kr[1].x, kr[1].y, kr[1].z, kr[1].w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_half2(k0[w], a0, a2);
+            e4m3x4_to_half2(k1[w], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16((w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3,
+                      bq[nt][4 * hf + w][0], bq[nt][4 * hf + w][1]);
+          }
+        }
+        // Scores in log2 units; hidden ones are -inf.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (key0 + g8 + 8 * (e >> 1) >= vis[nt][e & 1])
-              s[nt][e] = -INFINITY;
-      }
-      if (p.scores != nullptr) {
-        float* sc = p.scores +
-                    (static_cast<long long>(bh) * p.capacity + key0 + g8) *
-                        kRows + 2 * c;
+            s[nt][e] = (s[nt][e] + s2[nt][e]) * (mult[nt][e & 1] * ks_now[u]);
+        if (key0 + 16 > min_end) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (key0 + g8 < len)
-            *reinterpret_cast<float2*>(sc + 8 * nt) =
-                make_float2(s[nt][0], s[nt][1]);
-          if (key0 + g8 + 8 < len)
-            *reinterpret_cast<float2*>(sc + 8 * kRows + 8 * nt) =
-                make_float2(s[nt][2], s[nt][3]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + g8 + 8 * (e >> 1) >= vis[nt][e & 1])
+                s[nt][e] = -INFINITY;
         }
-      }
+        if (p.scores != nullptr) {
+          float* sc = p.scores +
+                      (static_cast<long long>(bh) * p.capacity + key0 + g8) *
+                          kRows + 2 * c;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          grow |= fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + kTau;
-      grow |= vs_now > unit;
-      // Lazy rescale: some row's maximum grew by more than 2^8, or a block's
-      // V scale exceeds the unit O is held in.
-      if (__any_sync(0xffffffffu, grow)) {
-        const float unit_new = fmaxf(unit, vs_now);
-        const float f_unit = unit_new > 0.f ? unit / unit_new : 1.f;
-        unit = unit_new;
+          for (int nt = 0; nt < NT; ++nt) {
+            if (key0 + g8 < len)
+              *reinterpret_cast<float2*>(sc + 8 * nt) =
+                  make_float2(s[nt][0], s[nt][1]);
+            if (key0 + g8 + 8 < len)
+              *reinterpret_cast<float2*>(sc + 8 * kRows + 8 * nt) =
+                  make_float2(s[nt][2], s[nt][3]);
+          }
+        }
+        bool grow = vs_now[u] > unit;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(s[nt][e], s[nt][e + 2]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m[nt][e], mx);
-            const float alpha =
-                m_new == -INFINITY ? 1.f : ptx::ex2(m[nt][e] - m_new);
-            m[nt][e] = m_new;
-            l[nt][e] *= alpha;
-            const float f = alpha * f_unit;
+          for (int e = 0; e < 2; ++e)
+            grow |= fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + kTau;
+        // Lazy rescale: some row's maximum grew by more than 2^8, or a
+        // block's V scale exceeds the unit O is held in.
+        if (__any_sync(0xffffffffu, grow)) {
+          const float unit_new = fmaxf(unit, vs_now[u]);
+          const float f_unit = unit_new > 0.f ? unit / unit_new : 1.f;
+          unit = unit_new;
 #pragma unroll
-            for (int i = 0; i < kMT; ++i) {
-              o[nt][i][e] *= f;
-              o[nt][i][e + 2] *= f;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(s[nt][e], s[nt][e + 2]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float m_new = fmaxf(m[nt][e], mx);
+              const float alpha =
+                  m_new == -INFINITY ? 1.f : ptx::ex2(m[nt][e] - m_new);
+              m[nt][e] = m_new;
+              l[nt][e] *= alpha;
+              const float f = alpha * f_unit;
+#pragma unroll
+              for (int i = 0; i < kMT; ++i) {
+                o[nt][i][e] *= f;
+                o[nt][i][e + 2] *= f;
+              }
             }
-          }
-      }
-      // P^T in fp16, times 2^7 and the block's V scale over the unit.
-      const float pf = unit > 0.f ? kPScale * vs_now / unit : 0.f;
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // A column nothing of which is visible yet has m = -inf (NaN
-          // scores stay NaN).
-          w[e] = s[nt][e] == -INFINITY ? 0.f
-                                       : ptx::ex2(s[nt][e] - m[nt][e & 1]);
-          l[nt][e & 1] += w[e];
         }
-        pb[nt][0] =
-            movmatrix_trans(ptx::pack2<false>(w[0] * pf, w[1] * pf));
-        pb[nt][1] =
-            movmatrix_trans(ptx::pack2<false>(w[2] * pf, w[3] * pf));
-      }
-      // O^T += V^T P^T.
-#pragma unroll
-      for (int w = 0; w < Codes<D>::kVWords; ++w) {
-        uint32_t a[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t lo = __byte_perm(cur.v[2 * i][w], cur.v[2 * i + 1][w],
-                                          0x5140);
-          const uint32_t hi = __byte_perm(cur.v[2 * i][w], cur.v[2 * i + 1][w],
-                                          0x7362);
-          e4m3x4_to_half2(lo, a[0][2 * i], a[0][2 * i + 1]);
-          e4m3x4_to_half2(hi, a[1][2 * i], a[1][2 * i + 1]);
-        }
+        // P^T in fp16, times 2^7 and the block's V scale over the unit.
+        const float pf = unit > 0.f ? kPScale * (vs_now[u] / unit) : 0.f;
+        uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(o[nt][2 * w], a[0][0], a[0][1], a[0][2], a[0][3], pb[nt][0],
-                  pb[nt][1]);
-          mma_f16(o[nt][2 * w + 1], a[1][0], a[1][1], a[1][2], a[1][3],
-                  pb[nt][0], pb[nt][1]);
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // A column nothing of which is visible yet has m = -inf (NaN
+            // scores stay NaN).
+            w[e] = s[nt][e] == -INFINITY
+                       ? 0.f
+                       : ptx::ex2(s[nt][e] - m[nt][e & 1]);
+            l[nt][e & 1] += w[e];
+          }
+          pb[nt][0] =
+              movmatrix_trans(ptx::pack2<false>(w[0] * pf, w[1] * pf));
+          pb[nt][1] =
+              movmatrix_trans(ptx::pack2<false>(w[2] * pf, w[3] * pf));
+        }
+        // O^T += V^T P^T: V rows 2c, 2c + 1, 2c + 8, 2c + 9 of the step.
+        constexpr int kVWords = D / 32;
+        uint32_t v[4][kVWords];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * u + 2 * c + (i & 1) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint4 x = ptx::ld_shared_v4(
+                tile + 2048 + r * D + ((g8 ^ v_swizzle<D>(r)) << 4));
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+            v[i][2] = x.z;
+            v[i][3] = x.w;
+          } else {
+            const uint2 x = ld_shared_v2(
+                tile + 2048 + r * D +
+                (((g8 >> 1) ^ v_swizzle<D>(r)) << 4) + 8 * (g8 & 1));
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kVWords; ++w) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t lo =
+                __byte_perm(v[2 * i][w], v[2 * i + 1][w], 0x5140);
+            const uint32_t hi =
+                __byte_perm(v[2 * i][w], v[2 * i + 1][w], 0x7362);
+            e4m3x4_to_half2(lo, a[0][2 * i], a[0][2 * i + 1]);
+            e4m3x4_to_half2(hi, a[1][2 * i], a[1][2 * i + 1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(o[nt][2 * w], a[0][0], a[0][1], a[0][2], a[0][3],
+                    pb[nt][0], pb[nt][1]);
+            mma_f16(o[nt][2 * w + 1], a[1][0], a[1][1], a[1][2], a[1][3],
+                    pb[nt][0], pb[nt][1]);
+          }
         }
       }
-      if (more) load_v<D>(cur, vb, t_next * kTile, len, g8, c);
+      __syncwarp();  // the tile has been read
+      load_next(stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
     // The warps' results meet: maxima, then O and l under the common one.
@@ -494,10 +605,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
     __syncthreads();
     const long long slot =
-        cta + (static_cast<long long>(b) * p.Hkv + h) * p.row_blocks + rb;
-    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+        cta + (static_cast<long long>(bh) * p.row_blocks + rb);
+    for (int i = threadIdx.x; i < n_rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d4 = i % (D / 4);
-      if (r >= n_rows) break;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -521,78 +631,113 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
       p.part_ml[slot * kRows + r] = make_float2(mx, sum);
     }
+    if (seg.seg_end >= count) break;
+    next_segment<kKeys>(p, seg);
   }
 }
 
 // ------------------------------------------------------------------ merge
-// One CTA per segment and part: part 0 merges the segment's partial rows
-// into O and LSE; with accumulated weights every part adds the weights of
-// its share of the keys, p = 2^(score - LSE), read back from the scores the
-// forward kernel left (4 bytes per key and row; recomputing them would read
-// the keys' codes again).
+// One CTA per query row of a segment joins the row's partials into O and LSE,
+// its threads over the columns and, in groups, over the partials (a
+// single long sequence has one per SM).  With accumulated weights further
+// CTAs, one per 512 keys of a segment, add p = 2^(score - LSE) over the rows,
+// read back from the scores the forward kernel left (4 bytes per key and row;
+// recomputing them would read the keys' codes again).
 constexpr int kMergeThreads = 256;
 constexpr int kKeysPerPart = 512;
+
+// Maximum and sum of row r over a segment's partials, by one warp (every lane
+// gets the result); the LSE in log2 units, -inf for a row that sees nothing.
+// (A NaN among the scores has made the sum NaN, also where no other score set
+// a maximum.)
+template <int kRows>
+__device__ __forceinline__ float2 row_total(const float2* ml, int r,
+                                            int n_slots, int lane) {
+  float mx = -INFINITY;
+  for (int s = lane; s < n_slots; s += 32) mx = fmaxf(mx, ml[s * kRows + r].x);
+#pragma unroll
+  for (int i = 16; i > 0; i /= 2)
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+  float sum = 0.f;
+  for (int s = lane; s < n_slots; s += 32) {
+    const float2 x = ml[s * kRows + r];
+    sum += x.y * (x.x == -INFINITY ? 0.f : ptx::ex2(x.x - mx));
+  }
+#pragma unroll
+  for (int i = 16; i > 0; i /= 2)
+    sum += __shfl_xor_sync(0xffffffffu, sum, i);
+  return make_float2(mx, sum);
+}
+__device__ __forceinline__ float total_lse2(float2 t) {
+  return t.y == 0.f ? -INFINITY : t.x + log2f(t.y);
+}
 
 template <int D, int NT, bool kBF16>
 __global__ void __launch_bounds__(kMergeThreads)
     kv8_merge_kernel(const FwdParams p, int parts) {
   constexpr int kRows = 8 * NT;
+  constexpr int kKeys = tile_keys<D>();
+  constexpr int kCols = D / 4;                      // float4 columns
+  constexpr int kGroups = kMergeThreads / kCols;    // partials at a time
   __shared__ float sm_lse[kRows];
-  ptx::griddep_wait();
-  const int lane = threadIdx.x % 32;
-  const long long seg = blockIdx.x / parts;
-  const int part = static_cast<int>(blockIdx.x - seg * parts);
+  __shared__ float4 sm_acc[kGroups][kCols];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per_seg = kRows + parts;  // CTAs of a segment
+  const long long seg = blockIdx.x / per_seg;
+  const int unit = static_cast<int>(blockIdx.x - seg * per_seg);
   const int rb = static_cast<int>(seg % p.row_blocks);
   const int bh = static_cast<int>(seg / p.row_blocks);
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int len = seq_len(p, b), n_new = seq_new(p, b);
   const int r0 = rb * kRows;
   const int n_rows = min(kRows, n_new * p.group - r0);
-  if (n_rows <= 0) return;
-  if (part > 0 && part * kKeysPerPart >= len) return;
+  const int key0 = (unit - kRows) * kKeysPerPart;
+  if (unit < kRows ? unit >= n_rows : (n_rows <= 0 || key0 >= len)) return;
 
-  const long long tiles = (len + kTile - 1) / kTile;
-  long long c0 = 0, n_slots = 0;
+  const int tiles = (len + kKeys - 1) / kKeys;
+  long long c0 = 0;
+  int n_slots = 0;
   if (tiles > 0) {
-    const long long total = tiles_before(p, p.B, lane);
+    long long first;
+    const long long total = list_tiles<kKeys>(p, b, lane, &first);
     const long long n_cta = shares(p, total);
-    const long long first =
-        tiles_before(p, b, lane) +
-        (static_cast<long long>(h) * p.row_blocks + rb) * tiles;
+    first += (static_cast<long long>(h) * p.row_blocks + rb) * tiles;
     // CTA c holds positions [total c / n, total (c + 1) / n).
     c0 = ((first + 1) * n_cta - 1) / total;
-    n_slots = ((first + tiles) * n_cta - 1) / total - c0 + 1;
+    n_slots = static_cast<int>(((first + tiles) * n_cta - 1) / total - c0 + 1);
   }
   const float2* ml = p.part_ml + (c0 + seg) * kRows;
-  const float4* po = reinterpret_cast<const float4*>(p.part_o) +
-                     (c0 + seg) * kRows * (D / 4);
-  for (int i = threadIdx.x; i < kRows * (D / 4); i += kMergeThreads) {
-    const int r = i / (D / 4), d4 = i % (D / 4);
-    if (r >= n_rows) break;
-    if (part > 0 && d4 != 0) continue;  // only the row's LSE is wanted
-    float mx = -INFINITY;
-    for (int s = 0; s < n_slots; ++s) mx = fmaxf(mx, ml[s * kRows + r].x);
-    float sum = 0.f;
+  ptx::griddep_wait();  // the forward kernel's partials
+
+  if (unit < kRows) {
+    const int r = unit;
+    const int g = threadIdx.x / kCols, d4 = threadIdx.x % kCols;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o) +
+                       ((c0 + seg) * kRows + r) * kCols + d4;
+    const float2 t = row_total<kRows>(ml, r, n_slots, lane);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < n_slots; ++s) {
-      const float2 x = ml[s * kRows + r];
-      const float f = x.x == -INFINITY ? 0.f : ptx::ex2(x.x - mx);
-      sum += x.y * f;
-      if (part == 0) {
-        const float4 y =
-            po[(static_cast<long long>(s) * kRows + r) * (D / 4) + d4];
-        acc.x += y.x * f;
-        acc.y += y.y * f;
-        acc.z += y.z * f;
-        acc.w += y.w * f;
-      }
+#pragma unroll 4
+    for (int s = g; s < n_slots; s += kGroups) {
+      const float mx = ml[s * kRows + r].x;
+      const float f = mx == -INFINITY ? 0.f : ptx::ex2(mx - t.x);
+      const float4 y = po[static_cast<long long>(s) * kRows * kCols];
+      acc.x += y.x * f;
+      acc.y += y.y * f;
+      acc.z += y.z * f;
+      acc.w += y.w * f;
     }
-    // A sum of 0: the row sees no token.  (A NaN among the scores has made
-    // the sum NaN, also where no other score set a maximum.)
-    const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
-    if (d4 == 0) sm_lse[r] = lse2;
-    if (part > 0) continue;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    sm_acc[g][d4] = acc;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+      const float4 y = sm_acc[i][d4];
+      acc.x += y.x;
+      acc.y += y.y;
+      acc.z += y.z;
+      acc.w += y.w;
+    }
+    const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
     const int tok = (r0 + r) / p.group, hd = (r0 + r) % p.group;
     const long long row =
         (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
@@ -601,25 +746,37 @@ __global__ void __launch_bounds__(kMergeThreads)
     out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[d4] = out;
     if (d4 == 0) {
+      const float lse2 = total_lse2(t);
       if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
       if (p.lse2 != nullptr)
         p.lse2[static_cast<long long>(bh) * p.row_blocks * kRows + r0 + r] =
             lse2;
     }
+    return;
   }
-  if (p.scores == nullptr) return;
+  for (int r = warp; r < n_rows; r += kMergeThreads / 32) {
+    const float lse2 = total_lse2(row_total<kRows>(ml, r, n_slots, lane));
+    if (lane == 0) sm_lse[r] = lse2;
+  }
   __syncthreads();
-  const int k_end = min(len, (part + 1) * kKeysPerPart);
-  for (int key = part * kKeysPerPart + threadIdx.x; key < k_end;
-       key += kMergeThreads) {
-    const float* s =
-        p.scores + (static_cast<long long>(bh) * p.capacity + key) * kRows;
-    float w = 0.f;
-    for (int r = 0; r < n_rows; ++r) {
-      const float x = s[r];
-      if (x != -INFINITY) w += ptx::ex2(x - sm_lse[r]);
+  const int k_end = min(len, key0 + kKeysPerPart);
+#pragma unroll 2
+  for (int key = key0 + threadIdx.x; key < k_end; key += kMergeThreads) {
+    const long long at = static_cast<long long>(bh) * p.capacity + key;
+    float x[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+      const float4 y = reinterpret_cast<const float4*>(p.scores + at * kRows)[i];
+      x[4 * i] = y.x;
+      x[4 * i + 1] = y.y;
+      x[4 * i + 2] = y.z;
+      x[4 * i + 3] = y.w;
     }
-    if (w != 0.f) p.weights[static_cast<long long>(bh) * p.capacity + key] += w;
+    float w = 0.f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (r < n_rows && x[r] != -INFINITY) w += ptx::ex2(x[r] - sm_lse[r]);
+    if (w != 0.f) p.weights[at] += w;
   }
 }
 
@@ -655,15 +812,20 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   uint32_t a[D / 16][4];
   {
-    Codes<D> t;
-    load_k<D>(t, p.k + static_cast<long long>(bh) * p.capacity * D, key0, len,
-              g8, c);
+    const uint8_t* k = p.k + static_cast<long long>(bh) * p.capacity * D;
 #pragma unroll
-    for (int hf = 0; hf < D / 64; ++hf)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        e4m3x4_to_half2(t.k[0][hf][w], a[4 * hf + w][0], a[4 * hf + w][2]);
-        e4m3x4_to_half2(t.k[1][hf][w], a[4 * hf + w][1], a[4 * hf + w][3]);
+      for (int hf = 0; hf < D / 64; ++hf) {
+        const int key = key0 + g8 + 8 * i;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (key < len)
+          x = __ldg(reinterpret_cast<const uint4*>(
+              k + static_cast<long long>(key) * D + 64 * hf + 16 * c));
+        e4m3x4_to_half2(x.x, a[4 * hf][i], a[4 * hf][2 + i]);
+        e4m3x4_to_half2(x.y, a[4 * hf + 1][i], a[4 * hf + 1][2 + i]);
+        e4m3x4_to_half2(x.z, a[4 * hf + 2][i], a[4 * hf + 2][2 + i]);
+        e4m3x4_to_half2(x.w, a[4 * hf + 3][i], a[4 * hf + 3][2 + i]);
       }
   }
   float ks = 0.f;
@@ -696,8 +858,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int s = kPer / 2; s > 0; s /= 2)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-      const int ex = (__float_as_int(amax) >> 23) - 127;
-      const int up = max(-114, min(13 - ex, 126));
+      const int up = row_shift(amax);
       const float f_up = exp2_int(up);
       uint32_t out[4];
 #pragma unroll
@@ -767,7 +928,7 @@ cudaError_t launch_pdl(Kernel kernel, long long grid, int threads,
 template <int D, int NT, bool kBF16>
 cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
   constexpr int kRows = 8 * NT;
-  constexpr int kSmem = kWarps * kRows * (D + 4 + 2) * 4;
+  constexpr int kSmem = Ring<D, NT>::kBytes;
   cudaError_t err = cudaFuncSetAttribute(
       kv8_decode_kernel<D, NT, kBF16>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -777,9 +938,9 @@ cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   const long long segs = static_cast<long long>(p.B) * p.Hkv * p.row_blocks;
   const int parts = p.scores == nullptr
-                        ? 1
+                        ? 0
                         : (p.capacity + kKeysPerPart - 1) / kKeysPerPart;
-  err = launch_pdl(kv8_merge_kernel<D, NT, kBF16>, segs * parts,
+  err = launch_pdl(kv8_merge_kernel<D, NT, kBF16>, segs * (kRows + parts),
                    kMergeThreads, stream, p, parts);
   if (err != cudaSuccess || p.weights == nullptr || p.scores != nullptr)
     return err;
