@@ -12,6 +12,7 @@
 namespace {
 
 constexpr size_t kWorkspaceAlign = 256;
+constexpr int kKeyTile = 128;  // keys of the many-row kernels' tiles
 
 size_t round_up(size_t x) {
   return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign;
@@ -84,41 +85,47 @@ attn_status_t check_counts(const int* p, int dev) {
   return attn::on_device(p, dev) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
-// Query rows a forward CTA holds, and the blocks of them per K/V head.
+// How the query rows of a K/V head are worked on: up to 16 by the decode
+// kernels (8 or 16 a CTA; bound by the codes' bytes), more by the tcgen05
+// kernel in units of 256 (a 128-row tile of 17 rows costs what one of 128
+// costs, yet 17 rows in two passes of the decode kernel read the codes
+// twice).
 struct RowPlan {
   long long rows;   // query rows per (batch, K/V head)
-  int tile;         // rows a CTA holds
-  long long blocks;
+  int tile;         // rows a CTA holds: 8, 16 or 256
+  long long blocks; // units of 256 rows (1 for few rows)
   int grid;         // CTAs of the forward launch
 };
+
+constexpr int kFewRows = 16;
 
 RowPlan plan_rows(int Hq, int Hkv, int Sq, int sms) {
   RowPlan r;
   r.rows = static_cast<long long>(Hq / Hkv) * Sq;
-  r.tile = r.rows <= 8 ? 8 : 16;
-  r.blocks = (r.rows + r.tile - 1) / r.tile;
+  r.tile = r.rows <= 8 ? 8 : r.rows <= kFewRows ? kFewRows : 256;
+  r.blocks = r.tile == 256 ? (r.rows + 255) / 256 : 1;
   r.grid = sms;
   return r;
 }
 
 struct Workspace {
-  size_t part_o, part_ml, lse2, scores, total;
+  size_t part_o, part_ml, scores, parts, lse2, total;
 };
 
 Workspace workspace_layout(int B, int Hkv, int capacity, int D,
                            const RowPlan& r, bool weights) {
   const size_t bh = static_cast<size_t>(B) * Hkv;
-  const size_t slots = r.grid + bh * r.blocks;
+  const bool few = r.tile <= kFewRows;
+  const size_t slots = few ? r.grid + bh : 2 * static_cast<size_t>(r.grid);
   Workspace w;
   w.part_o = 0;
   w.part_ml = w.part_o + round_up(slots * r.tile * D * 4);
-  w.lse2 = w.part_ml + round_up(slots * r.tile * 8);
-  w.scores = w.lse2 +
-             (weights && r.blocks > 1 ? round_up(bh * r.blocks * r.tile * 4)
-                                      : 0);
-  w.total = w.scores +
-            (weights && r.blocks == 1 ? round_up(bh * capacity * r.tile * 4)
-                                      : 0);
+  w.scores = w.part_ml + round_up(slots * r.tile * 8);
+  w.parts = w.scores +
+            (few && weights ? round_up(bh * capacity * r.tile * 4) : 0);
+  w.lse2 = w.parts + (few ? 0 : round_up(bh * r.blocks * 8));
+  w.total = w.lse2 +
+            (!few && weights ? round_up(bh * r.blocks * r.tile * 4) : 0);
   return w;
 }
 
@@ -202,10 +209,10 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   const int sms = attn::device_sms(dev);
   if (sms <= 0) return ATTN_ERR_CUDA;
   const RowPlan rp = plan_rows(Hq, c->Hkv, Sq, sms);
+  // Rows, CTAs of every launch, and steps (unit, key tile) fit 32 bits.
   const long long segs = static_cast<long long>(heads(*c)) * rp.blocks;
-  const long long tiles = (c->capacity - 1LL) / 512 + 1;
-  if (rp.rows > 0x7fffffffLL - 1024 || segs > 0x7fffffffLL ||
-      segs * (rp.tile + tiles) > 0x7fffffffLL)
+  const long long tiles = (c->capacity - 1LL) / kKeyTile + 1;
+  if (rp.rows > 0x7fffffffLL - 1024 || segs > 0x7fffffffLL / (16 + tiles))
     return ATTN_ERR_INVALID_ARG;
   st = check_cache_memory(*c, dev);
   if (st != ATTN_OK) return st;
@@ -261,16 +268,28 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
-  if (weights != nullptr && rp.blocks > 1)
-    p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
-  if (weights != nullptr && rp.blocks == 1)
+  const bool few = rp.tile <= kFewRows;
+  if (weights != nullptr && few)
     p.scores = reinterpret_cast<float*>(ws + w.scores);
+  if (weights != nullptr && !few)
+    p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+  p.parts = reinterpret_cast<int2*>(ws + w.parts);
   p.grid = rp.grid;
+  p.timeout_ns = attn::wait_timeout_ns();
   p.status = attn::device_status_word(dev);
   if (p.status == nullptr) return ATTN_ERR_CUDA;
-  const cudaError_t err =
-      attn::kv8::launch_fwd(c->D, dtype == ATTN_BF16, rp.tile, p,
-                            reinterpret_cast<cudaStream_t>(stream));
+  const bool bf16 = dtype == ATTN_BF16;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  if (few) {
+    err = attn::kv8::launch_decode(c->D, bf16, rp.tile, p, cs);
+  } else {
+    err = attn::kv8::launch_prefill(c->D, bf16, p, cs);
+    if (err == cudaSuccess && weights != nullptr)
+      err = attn::kv8::launch_weights(c->D, bf16,
+                                      static_cast<int>(rp.blocks * rp.tile),
+                                      p, cs);
+  }
   return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

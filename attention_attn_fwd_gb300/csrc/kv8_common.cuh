@@ -109,18 +109,63 @@ struct FwdParams {
   float* weights;         // or nullptr
   int B, Hq, Hkv, Sq, capacity, nblk, block_shift;
   int group;              // query heads per K/V head
-  int row_blocks;         // blocks of kRows query rows per (batch, K/V head)
+  int row_blocks;         // many rows: units of 256 per (batch, K/V head)
   int causal;
   float scale_log2;       // scale * log2(e)
-  // Workspace: per (CTA, segment) partial rows, their (max, sum), per-row
-  // LSEs in log2 units, and (few rows) the scores of every key.
+  // Workspace: partial rows and their (max, sum) of the parts of a split
+  // segment or unit; few rows: the scores of every key; many rows: where a
+  // unit's parts are, and the rows' LSEs in log2 units.
   float* part_o;          // [slots, rows, D]
   float2* part_ml;        // [slots, rows]
-  float* lse2;            // [B * Hkv, row_blocks * rows]
   float* scores;          // [B * Hkv, capacity, rows]
+  int2* parts;            // [B, row_blocks, Hkv]: first CTA, number of CTAs
+  float* lse2;            // [B * Hkv, row_blocks * 256]
   int grid;               // CTAs of the forward launch
+  int warps;              // few rows: warps of each
+  unsigned long long timeout_ns;  // limit of a pipeline wait
   unsigned int* status;
 };
+
+// ------------------------------------------------ shared by the forwards
+constexpr float kNone = -3.402823466e38f;  // running maximum of no score
+
+__device__ __forceinline__ int seq_len(const FwdParams& p, int b) {
+  return clamp_len(p.lens[b], p.capacity, p.status);
+}
+__device__ __forceinline__ int seq_new(const FwdParams& p, int b) {
+  return p.new_lens == nullptr ? p.Sq
+                               : clamp_len(p.new_lens[b], p.Sq, p.status);
+}
+// Visible tokens of row r (token-major: row r = token r / group, head
+// r % group) of a sequence.
+__device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
+                                       int r) {
+  if (!p.causal) return len;
+  return min(len, max(0, len - n_new + r / p.group + 1));
+}
+// Exponent of the power of two that brings a query row's largest element to
+// [2^13, 2^14) (rows of zeros or of the smallest numbers: as far as it goes).
+__device__ __forceinline__ int row_shift(float amax) {
+  const int e = (__float_as_int(amax) >> 23) - 127;
+  return max(-114, min(13 - e, 126));
+}
+
+// Launch that may be scheduled before the kernel ahead of it on the stream
+// has ended; the kernel waits for that itself (griddep_wait).
+template <class Kernel, class... Args>
+cudaError_t launch_pdl(Kernel kernel, long long grid, int threads,
+                       cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 struct EvictParams {
   const uint8_t* src_code[2];
@@ -140,8 +185,12 @@ struct EvictParams {
 
 cudaError_t launch_append(int D, int block, bool bf16, const AppendParams& p,
                           int B, cudaStream_t stream);
-cudaError_t launch_fwd(int D, bool bf16, int rows, const FwdParams& p,
-                       cudaStream_t stream);
+cudaError_t launch_decode(int D, bool bf16, int rows, const FwdParams& p,
+                          cudaStream_t stream);
+cudaError_t launch_prefill(int D, bool bf16, const FwdParams& p,
+                           cudaStream_t stream);
+cudaError_t launch_weights(int D, bool bf16, int lse2_rows,
+                           const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream);
 
 }  // namespace kv8

@@ -38,9 +38,8 @@ namespace attn {
 namespace kv8 {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr float kTau = 8.f;        // lazy rescale threshold (log2 units)
+constexpr float kMinUnit = 1.17549435e-38f;  // 2^-126, the smallest block scale
 constexpr float kPScale = 128.f;   // 2^7: P <= 2^(8 + 7) < 65504
 
 // Keys of a list tile: 2 KB of K codes.
@@ -76,18 +75,17 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   return v;
 }
 
-// Exponent of the power of two that brings a query row's largest element to
-// [2^13, 2^14) (rows of zeros or of the smallest numbers: as far as it goes).
-__device__ __forceinline__ int row_shift(float amax) {
-  const int e = (__float_as_int(amax) >> 23) - 127;
-  return max(-114, min(13 - e, 126));
+// 16-byte asynchronous copy past L1; the second form writes zeros and reads
+// nothing unless `in`.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+               "l"(src)
+               : "memory");
 }
-
-// 16-byte asynchronous copy past L1; `bytes` 0 writes zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src,
-                                           int bytes) {
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst,
+                                                   const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-               "l"(src), "r"(bytes)
+               "l"(src), "r"(in ? 16 : 0)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
@@ -98,22 +96,16 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ int seq_len(const FwdParams& p, int b) {
-  return clamp_len(p.lens[b], p.capacity, p.status);
-}
-__device__ __forceinline__ int seq_new(const FwdParams& p, int b) {
-  return p.new_lens == nullptr ? p.Sq
-                               : clamp_len(p.new_lens[b], p.Sq, p.status);
-}
-
-// The list of tiles: sequence b contributes Hkv * row_blocks segments of
-// ceil(lens[b] / kKeys) tiles.  Every lane of the calling warp gets the tiles
-// of all sequences (total) and of those before `seq`; up to 32 sequences take
-// one load per lane.
+// The list of tiles: sequence b contributes Hkv segments of
+// ceil(lens[b] / kKeys) tiles.  (Counts fit 32 bits: a tile of one segment
+// holds 4 KB of codes.)
+//
+// Tiles before sequence `seq` and of all sequences, for every lane of the
+// calling warp.
 template <int kKeys>
-__device__ __forceinline__ long long list_tiles(const FwdParams& p, int seq,
-                                                int lane, long long* before) {
-  long long t = 0, pre = 0;
+__device__ __forceinline__ int list_tiles(const FwdParams& p, int seq,
+                                          int lane, int* before) {
+  int t = 0, pre = 0;
   for (int b = lane; b < p.B; b += 32) {
     const int n = (seq_len(p, b) + kKeys - 1) / kKeys;
     t += n;
@@ -124,75 +116,96 @@ __device__ __forceinline__ long long list_tiles(const FwdParams& p, int seq,
     t += __shfl_xor_sync(0xffffffffu, t, s);
     pre += __shfl_xor_sync(0xffffffffu, pre, s);
   }
-  const int segs = p.Hkv * p.row_blocks;
-  *before = pre * segs;
-  return t * segs;
+  *before = pre * p.Hkv;
+  return t * p.Hkv;
 }
 
-// Sequence that holds list position x (x < total), and the tiles before it.
-template <int kKeys>
-__device__ __forceinline__ int find_seq(const FwdParams& p, long long x,
-                                        int lane, long long* before) {
-  long long base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    long long t = 0;
-    if (b < p.B)
-      t = static_cast<long long>((seq_len(p, b) + kKeys - 1) / kKeys) *
-          p.Hkv * p.row_blocks;
-    long long incl = t;
-#pragma unroll
-    for (int s = 1; s < 32; s *= 2) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, s);
-      if (lane >= s) incl += up;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
-    if (hit != 0u) {
-      const int l = __ffs(hit) - 1;
-      *before = base + __shfl_sync(0xffffffffu, incl - t, l);
-      return b0 + l;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+// The cut: CTA c of n takes q tiles, the first `rest` CTAs one more.
+struct Cut {
+  int n, q, rest;
+  __device__ __forceinline__ int first(int c) const {
+    return c * q + min(c, rest);
   }
-  *before = base;  // not reached for x < total
-  return p.B - 1;
+  __device__ __forceinline__ int owner(int x) const {
+    const int fat = rest * (q + 1);
+    return x < fat ? x / (q + 1) : rest + (x - fat) / q;
+  }
+};
+// At most one tile per warp is the finest cut.
+__device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
+  Cut c;
+  c.n = max(1, min(p.grid, (total + p.warps - 1) / p.warps));
+  c.q = total / c.n;
+  c.rest = total - c.q * c.n;
+  return c;
 }
 
-// CTAs that take a share: at most one tile per warp is the finest cut.
-__device__ __forceinline__ long long shares(const FwdParams& p,
-                                            long long total) {
-  const long long most = (total + kWarps - 1) / kWarps;
-  return most < p.grid ? (most > 0 ? most : 1) : p.grid;
-}
-
-// A place in a CTA's share of the list.  pos counts tiles from the share's
-// start; the segment it lies in covers [seg_pos, seg_end).
-struct Cursor {
-  int pos, seg_pos, seg_end;  // seg_pos may be negative (share starts inside)
-  int b, seg;                 // sequence, segment of it
+// A segment of the list as a CTA walks its share: it covers positions
+// [pos, end) counted from the share's start (pos < 0: it began earlier).
+struct Segment {
+  int pos, end;
+  int b, h;  // sequence, K/V head
   int len, tiles;
 };
 
+// CTA's share: its number of tiles (0: none) and first segment.
 template <int kKeys>
-__device__ __forceinline__ void next_segment(const FwdParams& p, Cursor& c) {
-  c.seg_pos = c.seg_end;
-  if (++c.seg == p.Hkv * p.row_blocks) {
-    c.seg = 0;
+__device__ __forceinline__ int take_share(const FwdParams& p, int cta,
+                                          int lane, Segment* s) {
+  int first = 0, count = 0, base = 0;
+  if (p.B > 32) {
+    const int total = list_tiles<kKeys>(p, 0, lane, &base);
+    const Cut cut = make_cut(p, total);
+    first = cut.first(cta);
+    count = cta < cut.n ? cut.first(cta + 1) - first : 0;
+    if (count == 0) return 0;
+  }
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int len = b < p.B ? seq_len(p, b) : 0;
+    const int t = (len + kKeys - 1) / kKeys * p.Hkv;
+    int incl = t;
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, i);
+      if (lane >= i) incl += up;
+    }
+    const int sum = __shfl_sync(0xffffffffu, incl, 31);
+    if (p.B <= 32) {  // one load per lane tells all
+      const Cut cut = make_cut(p, sum);
+      first = cut.first(cta);
+      count = cta < cut.n ? cut.first(cta + 1) - first : 0;
+      if (count == 0) return 0;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > first);
+    if (hit != 0u) {
+      const int l = __ffs(hit) - 1;
+      const int before = base + __shfl_sync(0xffffffffu, incl - t, l);
+      s->b = b0 + l;
+      s->len = __shfl_sync(0xffffffffu, len, l);
+      s->tiles = (s->len + kKeys - 1) / kKeys;
+      s->h = (first - before) / s->tiles;
+      s->pos = -((first - before) - s->h * s->tiles);
+      s->end = s->pos + s->tiles;
+      return count;
+    }
+    base += sum;
+  }
+  return 0;
+}
+
+template <int kKeys>
+__device__ __forceinline__ void next_segment(const FwdParams& p, Segment& c) {
+  c.pos = c.end;
+  if (++c.h == p.Hkv) {
+    c.h = 0;
     do {  // some later sequence has tokens: the share is not at its end
       ++c.b;
       c.len = seq_len(p, c.b);
     } while (c.len == 0);
     c.tiles = (c.len + kKeys - 1) / kKeys;
   }
-  c.seg_end = c.seg_pos + c.tiles;
-}
-
-// Visible tokens of row r (token-major: row r = token r / group, head
-// r % group) of a sequence.
-__device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
-                                       int r) {
-  if (!p.causal) return len;
-  return min(len, max(0, len - n_new + r / p.group + 1));
+  c.end = c.pos + c.tiles;
 }
 
 // One tile of a warp's ring: 2 KB of K codes, then 2 KB of V codes.  Chunk j
@@ -208,113 +221,134 @@ __device__ __forceinline__ int v_swizzle(int r) {
   return D == 128 ? ((r >> 1) & 3) << 1 : ((r >> 1) & 1) << 1;
 }
 
+// A warp's loads: they run ahead of its products, across segments.  Lane i
+// copies chunks i, i + 32, i + 64 and i + 96 of a tile.
 template <int D>
-__device__ __forceinline__ void copy_tile(uint32_t dst, const FwdParams& p,
-                                          const Cursor& c, int lane) {
-  constexpr int kPerRow = D / 16;
-  constexpr int kKeys = tile_keys<D>();
-  const int h = c.seg / p.row_blocks;
-  const long long head =
-      (static_cast<long long>(c.b) * p.Hkv + h) * p.capacity * D;
-  const int key0 = (c.pos - c.seg_pos) * kKeys;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ch = lane + 32 * i;
-    const int r = ch / kPerRow, j = ch % kPerRow;
-    const bool in = key0 + r < c.len;
+struct Loader {
+  static constexpr int kKeys = tile_keys<D>();
+  static constexpr int kPerRow = D / 16;
+  static constexpr int kRowStep = 32 / kPerRow;  // rows between the chunks
+  Segment seg;
+  int pos;                 // next tile, counted from the share's start
+  const uint8_t* k;        // this lane's first chunk of tile 0 of the segment
+  const uint8_t* v;
+  uint32_t dst_k, dst_v0, dst_v1;  // its places in a ring slot
+
+  __device__ __forceinline__ void set_segment(const FwdParams& p, int lane) {
     const long long at =
-        head + static_cast<long long>(in ? key0 + r : 0) * D + 16 * j;
-    const int bytes = in ? 16 : 0;  // rows past the length become zeros
-    cp_async16(dst + r * D + ((j ^ k_swizzle<D>(r)) << 4), p.k + at, bytes);
-    cp_async16(dst + 2048 + r * D + ((j ^ v_swizzle<D>(r)) << 4), p.v + at,
-               bytes);
+        (static_cast<long long>(seg.b) * p.Hkv + seg.h) * p.capacity * D +
+        16 * lane;
+    k = p.k + at;
+    v = p.v + at;
   }
-}
+  __device__ __forceinline__ void init(const FwdParams& p, const Segment& s,
+                                       int warp, int lane, uint32_t ring) {
+    seg = s;
+    pos = warp;
+    const int r = lane / kPerRow, j = lane % kPerRow;
+    dst_k = ring + r * D + ((j ^ k_swizzle<D>(r)) << 4);
+    dst_v0 = ring + 2048 + r * D + ((j ^ v_swizzle<D>(r)) << 4);
+    dst_v1 = ring + 2048 + r * D + ((j ^ v_swizzle<D>(r + kRowStep)) << 4);
+    set_segment(p, lane);
+  }
+  template <int kStep>
+  __device__ __forceinline__ void next(const FwdParams& p, int count,
+                                       int stage, int lane) {
+    if (pos < count) {
+      if (pos >= seg.end) {
+        do next_segment<kKeys>(p, seg);
+        while (pos >= seg.end);
+        set_segment(p, lane);
+      }
+      const int t = pos - seg.pos;
+      const long long off = static_cast<long long>(t) * 2048;
+      const uint32_t to = stage * 4096;
+      if ((t + 1) * kKeys <= seg.len) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cp_async16(dst_k + to + 512 * i, k + off + 512 * i);
+          cp_async16(((i & 1) ? dst_v1 : dst_v0) + to + 512 * i,
+                     v + off + 512 * i);
+        }
+      } else {  // rows past the length become zeros
+        const int left = seg.len - t * kKeys - lane / kPerRow;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = i * kRowStep < left;
+          const long long at = in ? off + 512 * i : 0;
+          cp_async16_or_zero(dst_k + to + 512 * i, k + at, in);
+          cp_async16_or_zero(((i & 1) ? dst_v1 : dst_v0) + to + 512 * i,
+                             v + at, in);
+        }
+      }
+      pos += kStep;
+    }
+    cp_async_commit();
+  }
+};
 
 // NT: 8-row groups of query rows a CTA holds (8 or 16 rows of a K/V head).
+// 8 rows leave registers for 16 warps an SM, 16 rows for 8.  At the end of a
+// segment the upper half of the warps hands its O to the lower half, which
+// sums in rows.
 template <int D, int NT>
-struct Ring {
+struct Config {
   static constexpr int kRows = 8 * NT;
+  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPitch = D + 4;  // floats: rows start 4 banks apart
-  static constexpr int kStages = NT == 1 ? 6 : 5;
+  static constexpr int kStages = NT == 1 ? 3 : 5;
   static constexpr int kRingBytes = kWarps * kStages * 4096;
-  static constexpr int kMergeBytes = kWarps * kRows * (kPitch + 2) * 4;
-  static constexpr int kBytes = kRingBytes + kMergeBytes;
+  static constexpr int kSums = kWarps / 2;  // warps that sum
+  static constexpr int kBytes =
+      kRingBytes + (kSums * kRows * kPitch + 2 * kWarps * kRows) * 4;
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
 template <int D, int NT, bool kBF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Config<D, NT>::kThreads, 1)
     kv8_decode_kernel(const FwdParams p) {
-  using R = Ring<D, NT>;
-  constexpr int kRows = R::kRows;
-  constexpr int kPitch = R::kPitch;
-  constexpr int kStages = R::kStages;
+  using C = Config<D, NT>;
+  constexpr int kWarps = C::kWarps;
+  constexpr int kThreads = C::kThreads;
+  constexpr int kRows = C::kRows;
+  constexpr int kPitch = C::kPitch;
+  constexpr int kStages = C::kStages;
   constexpr int kKeys = tile_keys<D>();
   constexpr int kSub = kKeys / 16;  // 16-key steps per tile
   constexpr int kKSteps = D / 16;
   constexpr int kMT = D / 16;       // m-tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
-  float* sm_o = reinterpret_cast<float*>(smem + R::kRingBytes);
-  float* sm_m = sm_o + kWarps * kRows * kPitch;  // [kWarps][kRows]
-  float* sm_l = sm_m + kWarps * kRows;           // [kWarps][kRows]
+  float* sm_o = reinterpret_cast<float*>(smem + C::kRingBytes);
+  float* sm_m = sm_o + C::kSums * kRows * kPitch;  // [kWarps][kRows]
+  float* sm_l = sm_m + kWarps * kRows;             // [kWarps][kRows]
 
   // The merge kernel may be scheduled early: its CTAs wait for this grid.
   ptx::griddep_launch_dependents();
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g8 = lane / 4, c = lane % 4;
-  long long unused;
-  const long long total = list_tiles<kKeys>(p, 0, lane, &unused);
-  const long long n_cta = shares(p, total);
   const int cta = blockIdx.x;
-  if (cta >= n_cta) return;
-  const long long first = total * cta / n_cta;
-  const int count = static_cast<int>(total * (cta + 1) / n_cta - first);
+  Segment seg;
+  const int count = take_share<kKeys>(p, cta, lane, &seg);
   if (count == 0) return;
-
-  // The share's first segment.
-  Cursor seg;
-  {
-    long long before;
-    seg.b = find_seq<kKeys>(p, first, lane, &before);
-    seg.len = seq_len(p, seg.b);
-    seg.tiles = (seg.len + kKeys - 1) / kKeys;
-    seg.seg = static_cast<int>((first - before) / seg.tiles);
-    seg.seg_pos = -static_cast<int>((first - before) % seg.tiles);
-    seg.seg_end = seg.seg_pos + seg.tiles;
-    seg.pos = 0;
-  }
-  // This warp's loads run ahead of its products.
-  const uint32_t ring =
-      ptx::smem_u32(smem) + warp * kStages * 4096;
-  Cursor ld = seg;
-  ld.pos = warp;
-  auto load_next = [&](int stage) {
-    if (ld.pos < count) {
-      while (ld.pos >= ld.seg_end) next_segment<kKeys>(p, ld);
-      copy_tile<D>(ring + stage * 4096, p, ld, lane);
-      ld.pos += kWarps;
-    }
-    cp_async_commit();
-  };
+  const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * 4096;
+  Loader<D> ld;
+  ld.init(p, seg, warp, lane, ring);
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) load_next(i);
+  for (int i = 0; i < kStages; ++i)
+    ld.template next<kWarps>(p, count, i, lane);
 
   int stage = 0;
   int pos = warp;  // this warp's next tile
   while (true) {
-    const int seg_last = min(seg.seg_end, count);  // end of the CTA's part
-    const int b = seg.b, len = seg.len;
-    const int h = seg.seg / p.row_blocks;
-    const int rb = seg.seg - h * p.row_blocks;
-    const int r0 = rb * kRows;
+    const int seg_last = min(seg.end, count);  // end of the CTA's part
+    const int b = seg.b, h = seg.h, len = seg.len;
     const int bh = b * p.Hkv + h;
     const int n_new = seq_new(p, b);
-    const int n_rows = max(0, min(kRows, n_new * p.group - r0));  // valid rows
-    const int min_end = n_rows > 0 ? row_end(p, len, n_new, r0) : 0;
-    const int max_end =
-        n_rows > 0 ? row_end(p, len, n_new, r0 + n_rows - 1) : 0;
+    const int n_rows = n_new * p.group;  // valid rows, kRows at most
+    const int min_end = n_rows > 0 ? row_end(p, len, n_new, 0) : 0;
+    const int max_end = n_rows > 0 ? len : 0;
 
     // This lane's two query rows per 8-row group (columns of S^T): how many
     // tokens they see, and the factor of their scores.
@@ -330,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int hf = 0; hf < D / 64; ++hf) {
         uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
         if (r < n_rows) {
-          const int tok = (r0 + r) / p.group, hd = (r0 + r) % p.group;
+          const int tok = r / p.group, hd = r % p.group;
           const uint16_t* q =
               static_cast<const uint16_t*>(p.q) +
               ((static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq +
@@ -365,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int up_col = __shfl_sync(0xffffffffu, up, 4 * col);
         mult[nt][e] = p.scale_log2 * exp2_int(-up_col);
         const int rr = 8 * nt + col;
-        vis[nt][e] = rr < n_rows ? row_end(p, len, n_new, r0 + rr) : max_end;
+        vis[nt][e] = rr < n_rows ? row_end(p, len, n_new, rr) : len;
       }
     }
 
@@ -373,10 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* vsb = p.v_scale + static_cast<long long>(bh) * p.nblk;
 
     float m[NT][2], l[NT][2], o[NT][kMT][4];
-    float unit = 0.f;  // O is held in units of this V scale (times 2^7)
+    // O is held in units of a V scale (times 2^7).
+    float unit = kMinUnit, inv_unit = 1.f / kMinUnit;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNone;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < kMT; ++i)
@@ -384,35 +419,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
 
-    // Block scales of a tile's 16-key steps, fetched one tile ahead.
-    float ks[kSub], vs[kSub];
-    auto load_scales = [&](int at) {
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        const int key = (at - seg.seg_pos) * kKeys + 16 * u;
-        ks[u] = vs[u] = 0.f;
-        if (at < seg_last && key < len) {
-          ks[u] = __ldg(ksb + (key >> p.block_shift));
-          vs[u] = __ldg(vsb + (key >> p.block_shift));
-        }
-      }
-    };
-    load_scales(pos);
+    // Block scales of this warp's next 32 / kSub tiles, one per lane (lane
+    // i: step i % kSub of tile i / kSub), fetched again when used up.
+    float ks_all = 0.f, vs_all = 0.f;
+    int held = 32 / kSub;  // tiles of the fetched ones that are used up
     for (; pos < seg_last; pos += kWarps) {
+      if (held == 32 / kSub) {
+        const int key =
+            (pos + (lane / kSub) * kWarps - seg.pos) * kKeys +
+            16 * (lane % kSub);
+        const bool in = key < len;
+        ks_all = in ? __ldg(ksb + (key >> p.block_shift)) : 0.f;
+        vs_all = in ? __ldg(vsb + (key >> p.block_shift)) : 0.f;
+        held = 0;
+      }
       cp_async_wait<kStages - 1>();
       __syncwarp();
-      float ks_now[kSub], vs_now[kSub];
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        ks_now[u] = ks[u];
-        vs_now[u] = vs[u];
-      }
-      load_scales(pos + kWarps);
       const uint32_t tile = ring + stage * 4096;
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        const int key0 = (pos - seg.seg_pos) * kKeys + 16 * u;
-        if (key0 >= max_end) continue;  // past every row's horizon
+        const int key0 = (pos - seg.pos) * kKeys + 16 * u;
+        const float ks =
+            __shfl_sync(0xffffffffu, ks_all, held * kSub + u);
+        const float vs =
+            __shfl_sync(0xffffffffu, vs_all, held * kSub + u);
+        if (key0 >= max_end) continue;  // no rows, or past the length
         // S^T of 16 keys, in two chains.
         float s[NT][4], s2[NT][4];
 #pragma unroll
@@ -446,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            s[nt][e] = (s[nt][e] + s2[nt][e]) * (mult[nt][e & 1] * ks_now[u]);
+            s[nt][e] = (s[nt][e] + s2[nt][e]) * (mult[nt][e & 1] * ks);
         if (key0 + 16 > min_end) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -469,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float2(s[nt][2], s[nt][3]);
           }
         }
-        bool grow = vs_now[u] > unit;
+        bool grow = vs > unit;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -478,9 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Lazy rescale: some row's maximum grew by more than 2^8, or a
         // block's V scale exceeds the unit O is held in.
         if (__any_sync(0xffffffffu, grow)) {
-          const float unit_new = fmaxf(unit, vs_now[u]);
-          const float f_unit = unit_new > 0.f ? unit / unit_new : 1.f;
+          const float unit_new = fmaxf(unit, vs);
+          const float f_unit = unit / unit_new;
           unit = unit_new;
+          inv_unit = 1.f / unit;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -490,8 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
               const float m_new = fmaxf(m[nt][e], mx);
-              const float alpha =
-                  m_new == -INFINITY ? 1.f : ptx::ex2(m[nt][e] - m_new);
+              const float alpha = ptx::ex2(m[nt][e] - m_new);
               m[nt][e] = m_new;
               l[nt][e] *= alpha;
               const float f = alpha * f_unit;
@@ -503,18 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // P^T in fp16, times 2^7 and the block's V scale over the unit.
-        const float pf = unit > 0.f ? kPScale * (vs_now[u] / unit) : 0.f;
+        const float pf = vs * inv_unit * kPScale;
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            // A column nothing of which is visible yet has m = -inf (NaN
-            // scores stay NaN).
-            w[e] = s[nt][e] == -INFINITY
-                       ? 0.f
-                       : ptx::ex2(s[nt][e] - m[nt][e & 1]);
+            // A hidden score is -inf, m never is: 0; NaN stays NaN.
+            w[e] = ptx::ex2(s[nt][e] - m[nt][e & 1]);
             l[nt][e & 1] += w[e];
           }
           pb[nt][0] =
@@ -565,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();  // the tile has been read
-      load_next(stage);
+      ld.template next<kWarps>(p, count, stage, lane);
+      ++held;
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
@@ -588,29 +617,66 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * nt + 2 * c + e;
-        float mx = -INFINITY;
+        float mx = kNone;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
           mx = fmaxf(mx, sm_m[w * kRows + r]);
-        const float f =
-            m[nt][e] == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - mx);
+        const float f = ptx::ex2(m[nt][e] - mx);
         const float fo = f * unit * (1.f / kPScale);
         if (g8 == 0) sm_l[warp * kRows + r] = l[nt][e] * f;
-        float* dst = sm_o + (warp * kRows + r) * kPitch + (D / 8) * g8;
 #pragma unroll
-        for (int i = 0; i < kMT; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(o[nt][i][e] * fo, o[nt][i][e + 2] * fo,
-                          o[nt][i + 1][e] * fo, o[nt][i + 1][e + 2] * fo);
+        for (int i = 0; i < kMT; ++i) {
+          o[nt][i][e] *= fo;
+          o[nt][i][e + 2] *= fo;
+        }
       }
+    // Fragment order between the halves: float4 i of lane j at 32 i + j.
+    float4* half = reinterpret_cast<float4*>(sm_o) +
+                   (warp % C::kSums) * (NT * kMT * 32) + lane;
+    static_assert(NT * kMT * 32 * 16 <= kRows * kPitch * 4, "hand-over fits");
+    if (warp >= C::kSums) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+          half[(nt * kMT + i) * 32] = make_float4(o[nt][i][0], o[nt][i][1],
+                                                  o[nt][i][2], o[nt][i][3]);
+    }
     __syncthreads();
-    const long long slot =
-        cta + (static_cast<long long>(bh) * p.row_blocks + rb);
+    if (warp < C::kSums) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+          const float4 x = half[(nt * kMT + i) * 32];
+          o[nt][i][0] += x.x;
+          o[nt][i][1] += x.y;
+          o[nt][i][2] += x.z;
+          o[nt][i][3] += x.w;
+        }
+    }
+    __syncthreads();
+    if (warp < C::kSums) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * nt + 2 * c + e;
+          float* dst = sm_o + (warp * kRows + r) * kPitch + (D / 8) * g8;
+#pragma unroll
+          for (int i = 0; i < kMT; i += 2)
+            *reinterpret_cast<float4*>(dst + 2 * i) =
+                make_float4(o[nt][i][e], o[nt][i][e + 2], o[nt][i + 1][e],
+                            o[nt][i + 1][e + 2]);
+        }
+    }
+    __syncthreads();
+    const long long slot = static_cast<long long>(cta) + bh;
     for (int i = threadIdx.x; i < n_rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d4 = i % (D / 4);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < C::kSums; ++w) {
         const float4 x = *reinterpret_cast<const float4*>(
             sm_o + (w * kRows + r) * kPitch + 4 * d4);
         acc.x += x.x;
@@ -623,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x < n_rows) {
       const int r = threadIdx.x;
-      float mx = -INFINITY, sum = 0.f;
+      float mx = kNone, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         mx = fmaxf(mx, sm_m[w * kRows + r]);
@@ -631,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       p.part_ml[slot * kRows + r] = make_float2(mx, sum);
     }
-    if (seg.seg_end >= count) break;
+    if (seg.end >= count) break;
     next_segment<kKeys>(p, seg);
   }
 }
@@ -653,7 +719,7 @@ constexpr int kKeysPerPart = 512;
 template <int kRows>
 __device__ __forceinline__ float2 row_total(const float2* ml, int r,
                                             int n_slots, int lane) {
-  float mx = -INFINITY;
+  float mx = kNone;
   for (int s = lane; s < n_slots; s += 32) mx = fmaxf(mx, ml[s * kRows + r].x);
 #pragma unroll
   for (int i = 16; i > 0; i /= 2)
@@ -661,7 +727,7 @@ __device__ __forceinline__ float2 row_total(const float2* ml, int r,
   float sum = 0.f;
   for (int s = lane; s < n_slots; s += 32) {
     const float2 x = ml[s * kRows + r];
-    sum += x.y * (x.x == -INFINITY ? 0.f : ptx::ex2(x.x - mx));
+    sum += x.y * ptx::ex2(x.x - mx);
   }
 #pragma unroll
   for (int i = 16; i > 0; i /= 2)
@@ -683,14 +749,11 @@ __global__ void __launch_bounds__(kMergeThreads)
   __shared__ float4 sm_acc[kGroups][kCols];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int per_seg = kRows + parts;  // CTAs of a segment
-  const long long seg = blockIdx.x / per_seg;
-  const int unit = static_cast<int>(blockIdx.x - seg * per_seg);
-  const int rb = static_cast<int>(seg % p.row_blocks);
-  const int bh = static_cast<int>(seg / p.row_blocks);
+  const int bh = blockIdx.x / per_seg;
+  const int unit = blockIdx.x - bh * per_seg;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int len = seq_len(p, b), n_new = seq_new(p, b);
-  const int r0 = rb * kRows;
-  const int n_rows = min(kRows, n_new * p.group - r0);
+  const int n_rows = n_new * p.group;
   const int key0 = (unit - kRows) * kKeysPerPart;
   if (unit < kRows ? unit >= n_rows : (n_rows <= 0 || key0 >= len)) return;
 
@@ -698,28 +761,26 @@ __global__ void __launch_bounds__(kMergeThreads)
   long long c0 = 0;
   int n_slots = 0;
   if (tiles > 0) {
-    long long first;
-    const long long total = list_tiles<kKeys>(p, b, lane, &first);
-    const long long n_cta = shares(p, total);
-    first += (static_cast<long long>(h) * p.row_blocks + rb) * tiles;
-    // CTA c holds positions [total c / n, total (c + 1) / n).
-    c0 = ((first + 1) * n_cta - 1) / total;
-    n_slots = static_cast<int>(((first + tiles) * n_cta - 1) / total - c0 + 1);
+    int first;
+    const int total = list_tiles<kKeys>(p, b, lane, &first);
+    const Cut cut = make_cut(p, total);
+    first += h * tiles;
+    c0 = cut.owner(first);
+    n_slots = cut.owner(first + tiles - 1) - static_cast<int>(c0) + 1;
   }
-  const float2* ml = p.part_ml + (c0 + seg) * kRows;
+  const float2* ml = p.part_ml + (c0 + bh) * kRows;
   ptx::griddep_wait();  // the forward kernel's partials
 
   if (unit < kRows) {
     const int r = unit;
     const int g = threadIdx.x / kCols, d4 = threadIdx.x % kCols;
     const float4* po = reinterpret_cast<const float4*>(p.part_o) +
-                       ((c0 + seg) * kRows + r) * kCols + d4;
+                       ((c0 + bh) * kRows + r) * kCols + d4;
     const float2 t = row_total<kRows>(ml, r, n_slots, lane);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = g; s < n_slots; s += kGroups) {
-      const float mx = ml[s * kRows + r].x;
-      const float f = mx == -INFINITY ? 0.f : ptx::ex2(mx - t.x);
+      const float f = ptx::ex2(ml[s * kRows + r].x - t.x);
       const float4 y = po[static_cast<long long>(s) * kRows * kCols];
       acc.x += y.x * f;
       acc.y += y.y * f;
@@ -738,20 +799,15 @@ __global__ void __launch_bounds__(kMergeThreads)
       acc.w += y.w;
     }
     const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
-    const int tok = (r0 + r) / p.group, hd = (r0 + r) % p.group;
+    const int tok = r / p.group, hd = r % p.group;
     const long long row =
         (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
     uint2 out;
     out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
     out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[d4] = out;
-    if (d4 == 0) {
-      const float lse2 = total_lse2(t);
-      if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
-      if (p.lse2 != nullptr)
-        p.lse2[static_cast<long long>(bh) * p.row_blocks * kRows + r0 + r] =
-            lse2;
-    }
+    if (d4 == 0 && p.lse != nullptr)
+      p.lse[row] = total_lse2(t) * 0.69314718055994531f;
     return;
   }
   for (int r = warp; r < n_rows; r += kMergeThreads / 32) {
@@ -787,6 +843,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 // p = 2^(score - LSE) summed over the rows.  Every key has one owner, so the
 // sums have one order.
 constexpr int kWRows = 64;
+constexpr int kThreads = 256;
 
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -910,44 +967,34 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <class Kernel, class... Args>
-cudaError_t launch_pdl(Kernel kernel, long long grid, int threads,
-                       cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D, int NT, bool kBF16>
-cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
+cudaError_t launch_rows(FwdParams p, cudaStream_t stream) {
   constexpr int kRows = 8 * NT;
-  constexpr int kSmem = Ring<D, NT>::kBytes;
+  using C = Config<D, NT>;
+  p.warps = C::kWarps;
   cudaError_t err = cudaFuncSetAttribute(
       kv8_decode_kernel<D, NT, kBF16>,
-      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
-  kv8_decode_kernel<D, NT, kBF16><<<p.grid, kThreads, kSmem, stream>>>(p);
+  kv8_decode_kernel<D, NT, kBF16>
+      <<<p.grid, C::kThreads, C::kBytes, stream>>>(p);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  const long long segs = static_cast<long long>(p.B) * p.Hkv * p.row_blocks;
+  const long long segs = static_cast<long long>(p.B) * p.Hkv;
   const int parts = p.scores == nullptr
                         ? 0
                         : (p.capacity + kKeysPerPart - 1) / kKeysPerPart;
-  err = launch_pdl(kv8_merge_kernel<D, NT, kBF16>, segs * (kRows + parts),
-                   kMergeThreads, stream, p, parts);
-  if (err != cudaSuccess || p.weights == nullptr || p.scores != nullptr)
-    return err;
+  return launch_pdl(kv8_merge_kernel<D, NT, kBF16>, segs * (kRows + parts),
+                    kMergeThreads, stream, p, parts);
+}
+
+template <int D, bool kBF16>
+cudaError_t launch_weights_dt(const FwdParams& p, int lse2_rows,
+                              cudaStream_t stream) {
   const long long tiles = (p.capacity + 127) / 128;
   return launch_pdl(kv8_weights_kernel<D, kBF16>,
                     static_cast<long long>(p.B) * p.Hkv * tiles, kThreads,
-                    stream, p, p.row_blocks * kRows);
+                    stream, p, lse2_rows);
 }
 
 template <int D, bool kBF16>
@@ -958,13 +1005,22 @@ cudaError_t launch_dt(int rows, const FwdParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_fwd(int D, bool bf16, int rows, const FwdParams& p,
-                       cudaStream_t stream) {
+cudaError_t launch_decode(int D, bool bf16, int rows, const FwdParams& p,
+                          cudaStream_t stream) {
   if (D == 64)
     return bf16 ? launch_dt<64, true>(rows, p, stream)
                 : launch_dt<64, false>(rows, p, stream);
   return bf16 ? launch_dt<128, true>(rows, p, stream)
               : launch_dt<128, false>(rows, p, stream);
+}
+
+cudaError_t launch_weights(int D, bool bf16, int lse2_rows,
+                           const FwdParams& p, cudaStream_t stream) {
+  if (D == 64)
+    return bf16 ? launch_weights_dt<64, true>(p, lse2_rows, stream)
+                : launch_weights_dt<64, false>(p, lse2_rows, stream);
+  return bf16 ? launch_weights_dt<128, true>(p, lse2_rows, stream)
+              : launch_weights_dt<128, false>(p, lse2_rows, stream);
 }
 
 }  // namespace kv8

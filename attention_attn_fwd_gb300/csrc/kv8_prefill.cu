@@ -1,0 +1,850 @@
+// Attention of many query rows per K/V head over the 8-bit cache.
+//
+// The query rows of a K/V head, token-major (row r = token r / group, head
+// r % group), are cut into units of two 128-row Q tiles that share one
+// stream of 128-key tiles.  S = Q K^T and O += P V run as tcgen05 MMAs with
+// fp16 operands and fp32 accumulators in TMEM, as in the 16-bit forward
+// kernel; what differs is that the operands do not exist in memory:
+//   - E4M3 codes are fp16 values, so a warpgroup converts each raw tile from
+//     one shared-memory ring into the 128-byte-swizzled fp16 tiles of
+//     another (exactly).  K's block scales multiply the scores in fp32, 16
+//     keys at a time; V's scale over the largest one of the unit's keys
+//     multiplies V's halves (exact for powers of two; else one fp16 rounding,
+//     2^-11, as P's own);
+//   - the same warpgroup brings Q rows to fp16 with a power of two per row
+//     (exact down to 2^-37 of the row's largest element) and the sign of the
+//     scale.
+// P is kept shifted by 2^7 (it is at most 2^15, and normal down to 2^-21 of
+// its row's largest), as are the row sums, which take P unrounded.
+//
+// Steps (unit, key tile) form one list, cut into equal consecutive shares, one
+// per CTA: lengths come from device memory and the cut follows them, whether
+// there are few units with many keys or many units.  A unit that one CTA
+// covers is finished by it; the parts of any other go to workspace slots (a
+// CTA has two at most: a unit begun before its share, one going on after it)
+// and are joined by the merge kernel.
+//
+// Roles (512 threads): warp 0 MMA issue, warp 1 bulk copies of the raw
+// tiles, warps 4-7 / 8-11 softmax and epilogue of Q tile 0 / 1, warps 12-15
+// conversion.  Every wait is bounded as in the forward kernel.
+#include "attn_sync.cuh"
+#include "kv8_common.cuh"
+
+namespace attn {
+namespace kv8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTM = 128;            // rows of a Q tile
+constexpr int kTN = 128;            // keys of a tile
+constexpr int kUnitRows = 2 * kTM;
+constexpr float kTau = 8.f;         // lazy rescale threshold (log2 units)
+constexpr float kShift = 7.f;       // log2 of P's scale
+// Registers: the launch gives every thread 128; the shares of the four
+// warpgroups add up to 4 * 128.
+constexpr int kRegsControl = 64;
+constexpr int kRegsSoftmax = 192;
+constexpr int kRegsConvert = 64;
+static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128,
+              "register split exceeds the launch allocation");
+
+template <int D>
+struct Smem {
+  static constexpr int kBox = kTN * 128;             // 128 rows x 128 bytes
+  static constexpr int kTile = kBox * (D / 64);      // one fp16 tile
+  static constexpr int kRaw = kTN * D;               // one raw tile
+  static constexpr int kSlots = 4;                   // fp16 tiles
+  static constexpr int kRawSlots = D == 128 ? 2 : 4; // raw tiles
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + 2 * kTile;
+  static constexpr int kRawRing = kRing + kSlots * kTile;
+  static constexpr int kShifts = kRawRing + kRawSlots * kRaw;  // [2][2][128]
+  static constexpr int kBars = kShifts + 2 * 2 * kTM;
+  // raw_full, raw_empty, kv_full, kv_empty, q_full[2], q_free[2], s[2],
+  // p[2], o[2], drain
+  static constexpr int kNumBars = 2 * kRawSlots + 2 * kSlots + 11;
+  static constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM base, abort
+  static constexpr int kUnit = kMisc + 8;             // V units, [4]
+  static constexpr int kBytes = kUnit + 16;
+  static_assert(kBytes + 1024 <= 227 * 1024, "shared memory per CTA");
+};
+
+// ------------------------------------------------------------- the list
+// Key tiles rows [r0, r1) of a sequence with `rows` rows see.
+__device__ __forceinline__ int tiles_seen(const FwdParams& p, int len,
+                                          int n_new, int r0, int r1) {
+  const int last = min(r1, n_new * p.group) - 1;
+  if (last < r0) return 0;
+  return (row_end(p, len, n_new, last) + kTN - 1) / kTN;
+}
+
+// A unit, or the part of one, that a CTA works on: key tiles [j0, j1) of its
+// `steps`.  Units are numbered (b, u, h), h fastest.
+struct Unit {
+  int b, u, h;
+  int len, n_new, steps;
+  int j0, j1;
+};
+
+__device__ __forceinline__ int pair_steps(const FwdParams& p, int i, int* len,
+                                          int* n_new) {
+  const int b = i / p.row_blocks, u = i - b * p.row_blocks;
+  *len = seq_len(p, b);
+  *n_new = seq_new(p, b);
+  return tiles_seen(p, *len, *n_new, u * kUnitRows, (u + 1) * kUnitRows);
+}
+
+// Walks a CTA's share.  take() and next() are warp-collective and return
+// whether there is a unit.
+struct Walk {
+  Unit w;
+  int left;      // steps of the share behind this unit's part
+  int cta;
+  int n, q, rest;  // the cut: CTA c of n takes q steps, the first rest one more
+
+  __device__ __forceinline__ int first(int c) const {
+    return c * q + min(c, rest);
+  }
+  __device__ __forceinline__ int owner(int x) const {
+    const int fat = rest * (q + 1);
+    return x < fat ? x / (q + 1) : rest + (x - fat) / q;
+  }
+  __device__ __forceinline__ void set_pair(const FwdParams& p, int i) {
+    w.b = i / p.row_blocks;
+    w.u = i - w.b * p.row_blocks;
+  }
+
+  __device__ __forceinline__ bool take(const FwdParams& p, int cta_, int lane) {
+    cta = cta_;
+    const int pairs = p.B * p.row_blocks;
+    int total = 0;
+    for (int i = lane; i < pairs; i += 32) {
+      int len, n_new;
+      total += pair_steps(p, i, &len, &n_new);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2)
+      total += __shfl_xor_sync(0xffffffffu, total, s);
+    total *= p.Hkv;
+    if (total == 0) return false;
+    n = min(p.grid, total);
+    q = total / n;
+    rest = total - q * n;
+    if (cta >= n) return false;
+    const int x = first(cta);
+    const int count = first(cta + 1) - x;
+    int base = 0;
+    for (int i0 = 0; i0 < pairs; i0 += 32) {
+      const int i = i0 + lane;
+      int len = 0, n_new = 0, steps = 0;
+      if (i < pairs) steps = pair_steps(p, i, &len, &n_new);
+      const int t = steps * p.Hkv;
+      int incl = t;
+#pragma unroll
+      for (int s = 1; s < 32; s *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += up;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
+      if (hit != 0u) {
+        const int l = __ffs(hit) - 1;
+        set_pair(p, i0 + l);
+        const int off = x - base - __shfl_sync(0xffffffffu, incl - t, l);
+        w.len = __shfl_sync(0xffffffffu, len, l);
+        w.n_new = __shfl_sync(0xffffffffu, n_new, l);
+        w.steps = __shfl_sync(0xffffffffu, steps, l);
+        w.h = off / w.steps;
+        w.j0 = off - w.h * w.steps;
+        w.j1 = min(w.steps, w.j0 + count);
+        left = count - (w.j1 - w.j0);
+        return true;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+  }
+
+  __device__ __forceinline__ bool next(const FwdParams& p) {
+    if (left == 0) return false;
+    if (++w.h == p.Hkv) {
+      w.h = 0;
+      int i = w.b * p.row_blocks + w.u;
+      do {  // some later unit has steps: the share is not at its end
+        ++i;
+        w.steps = pair_steps(p, i, &w.len, &w.n_new);
+      } while (w.steps == 0);
+      set_pair(p, i);
+    }
+    w.j0 = 0;
+    w.j1 = min(w.steps, left);
+    left -= w.j1;
+    return true;
+  }
+};
+
+// What a Q tile of the unit's part has to do.
+struct TileWork {
+  int r0;      // first row
+  int n_rows;  // valid rows
+  int n;       // key tiles of the part it sees, from j0
+  int full;    // key tiles below this one are seen whole by every valid row
+};
+__device__ __forceinline__ TileWork tile_work(const FwdParams& p,
+                                              const Unit& w, int t) {
+  TileWork k;
+  k.r0 = w.u * kUnitRows + t * kTM;
+  k.n_rows = max(0, min(kTM, w.n_new * p.group - k.r0));
+  const int hi = tiles_seen(p, w.len, w.n_new, k.r0, k.r0 + kTM);
+  k.n = max(0, min(hi, w.j1) - w.j0);
+  k.full = k.n_rows > 0 ? row_end(p, w.len, w.n_new, k.r0) / kTN : 0;
+  return k;
+}
+__device__ __forceinline__ long long q_row_index(const FwdParams& p,
+                                                 const Unit& w, int r) {
+  const int tok = r / p.group, hd = r - tok * p.group;
+  return (static_cast<long long>(w.b) * p.Hq + w.h * p.group + hd) * p.Sq +
+         tok;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
+                                          uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// ------------------------------------------------------------ the kernel
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_prefill_kernel(const FwdParams p) {
+  using L = Smem<D>;
+  constexpr int kOCol = 2 * kTN;  // TMEM: S0, S1, then O0, O1
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_base = ptx::smem_u32(smem);
+  const uint32_t bar_rfull = s_base + L::kBars;
+  const uint32_t bar_rempty = bar_rfull + 8 * L::kRawSlots;
+  const uint32_t bar_full = bar_rempty + 8 * L::kRawSlots;
+  const uint32_t bar_empty = bar_full + 8 * L::kSlots;
+  const uint32_t bar_q = bar_empty + 8 * L::kSlots;  // [2]
+  const uint32_t bar_qfree = bar_q + 16;             // [2]
+  const uint32_t bar_s = bar_qfree + 16;             // [2]
+  const uint32_t bar_p = bar_s + 16;                 // [2]
+  const uint32_t bar_o = bar_p + 16;                 // [2]
+  const uint32_t bar_drain = bar_o + 16;             // [1]
+  volatile signed char* q_shift =  // log2 of the factor each Q row got
+      reinterpret_cast<signed char*>(smem + L::kShifts);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
+  volatile float* v_unit = reinterpret_cast<float*>(smem + L::kUnit);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  ptx::griddep_launch_dependents();  // the merge kernel waits for this grid
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const uint32_t bar = s_base + L::kBars + 8 * i;
+      // Converted tiles, freed raw tiles and Q tiles: one arrival per
+      // converting warp; P: one per softmax thread of the tile.
+      uint32_t count = 1;
+      if ((bar >= bar_rempty && bar < bar_full) ||
+          (bar >= bar_full && bar < bar_empty) ||
+          (bar >= bar_q && bar < bar_qfree))
+        count = 4;
+      if (bar >= bar_p && bar < bar_o) count = kTM;
+      ptx::mbar_init(bar, count);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  Walk walk;
+  bool more = walk.take(p, static_cast<int>(blockIdx.x), lane);
+  bool ok = true;
+  auto wait = [&](uint32_t bar, int phase, int role) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1, abort_flag, p,
+                                                role)) != 0;
+  };
+
+  if (warp < 4) {
+    ptx::setmaxnreg_dec<kRegsControl>();
+    if (warp == 1) {
+      // ---------------------------------------------------- raw tile loads
+      int it = 0;
+      for (; more && ok; more = walk.next(p)) {
+        const Unit& w = walk.w;
+        const int n = w.j1 - w.j0;
+        const long long head =
+            (static_cast<long long>(w.b) * p.Hkv + w.h) * p.capacity * D;
+        for (int j = 0; j < n && ok; ++j) {
+          const int key0 = (w.j0 + j) * kTN;
+          const uint32_t bytes = min(kTN, w.len - key0) * D;
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = it % L::kRawSlots, use = it / L::kRawSlots;
+            if (use > 0) ok = wait(bar_rempty + 8 * slot, use - 1, 1);
+            if (!ok) break;
+            if (lane == 0) {
+              ptx::mbar_arrive_expect_tx(bar_rfull + 8 * slot, bytes);
+              bulk_load(s_base + L::kRawRing + slot * L::kRaw,
+                        (kv ? p.v : p.k) + head +
+                            static_cast<long long>(key0) * D,
+                        bytes, bar_rfull + 8 * slot);
+            }
+            ++it;
+          }
+        }
+      }
+      if (!ok) {  // let the copies in flight land
+        for (int i = max(0, it - L::kRawSlots); i < it; ++i)
+          drain_wait(bar_rfull + 8 * (i % L::kRawSlots),
+                     (i / L::kRawSlots) & 1, p);
+      }
+      __syncwarp();
+    } else if (warp == 0) {
+      // -------------------------------------------------------- MMA issue
+      const uint32_t idesc_qk = ptx::idesc_f16(false, kTM, kTN, false, false);
+      const uint32_t idesc_pv = ptx::idesc_f16(false, kTM, D, true, false);
+      constexpr uint32_t kHi = ptx::sdesc_hi_sw128(1024);
+      const uint32_t q_lo = ptx::sdesc_lo(s_base + L::kQ, 16);
+      const uint32_t k_lo = ptx::sdesc_lo(s_base + L::kRing, 16);
+      const uint32_t v_lo = ptx::sdesc_lo(s_base + L::kRing, L::kBox);
+      constexpr uint32_t kTile16 = L::kTile >> 4;
+      auto issue_qk = [&](int t, int slot) {
+        const uint32_t a0 = q_lo + t * kTile16, b0 = k_lo + slot * kTile16;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * L::kBox + (kk % 4) * 32) >> 4;
+          ptx::mma_ss_elect(tmem + t * kTN, a0 + off, b0 + off, kHi, idesc_qk,
+                            kk > 0 ? 1u : 0u);
+        }
+        ptx::tc_commit_elect(bar_s + 8 * t);
+      };
+      auto issue_pv = [&](int t, int slot, bool acc) {
+        const uint32_t b0 = v_lo + slot * kTile16;
+#pragma unroll
+        for (int kk = 0; kk < kTN / 16; ++kk)
+          ptx::mma_ts_elect(tmem + kOCol + t * D, tmem + t * kTN + kk * 8,
+                            b0 + ((kk * 16 * 128) >> 4), kHi, idesc_pv,
+                            (acc || kk > 0) ? 1u : 0u);
+      };
+      int it = 0;  // converted tiles consumed
+      int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+      bool issued = false;
+      for (; more && ok; more = walk.next(p)) {
+        const int n0 = tile_work(p, walk.w, 0).n;
+        const int n1 = tile_work(p, walk.w, 1).n;
+        const int n_kv = walk.w.j1 - walk.w.j0;  // = max(n0, n1)
+        ok = wait(bar_full + 8 * (it % L::kSlots), it / L::kSlots, 2);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int n = t ? n1 : n0;
+          if (!ok || n == 0) continue;
+          ok = wait(bar_q + 8 * t, q_uses[t], 2);
+          if (!ok) break;
+          ++q_uses[t];
+          ptx::tc_fence_after();
+          issue_qk(t, it % L::kSlots);
+          if (n == 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
+          issued = true;
+        }
+        if (!ok) break;
+        ptx::tc_commit_elect(bar_empty + 8 * (it % L::kSlots));
+        const int it0 = it;
+        for (int j = 0; j < n_kv && ok; ++j) {
+          const int it_v = it0 + 2 * j + 1, it_k = it0 + 2 * j + 2;
+          const int slot_v = it_v % L::kSlots, slot_k = it_k % L::kSlots;
+          ok = wait(bar_full + 8 * slot_v, it_v / L::kSlots, 2);
+          if (!ok) break;
+          bool k_ready = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int n = t ? n1 : n0;
+            if (!ok || j >= n) continue;
+            ok = wait(bar_p + 8 * t, p_uses[t], 2);
+            if (!ok) break;
+            ++p_uses[t];
+            ptx::tc_fence_after();
+            issue_pv(t, slot_v, j > 0);
+            if (j == n - 1) {
+              ptx::tc_commit_elect(bar_o + 8 * t);
+              continue;
+            }
+            if (!k_ready) {
+              ok = wait(bar_full + 8 * slot_k, it_k / L::kSlots, 2);
+              if (!ok) break;
+              k_ready = true;
+              ptx::tc_fence_after();
+            }
+            issue_qk(t, slot_k);
+            if (j + 1 == n - 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
+          }
+          if (!ok) break;
+          ptx::tc_commit_elect(bar_empty + 8 * slot_v);
+          if (j + 1 < n_kv) ptx::tc_commit_elect(bar_empty + 8 * slot_k);
+        }
+        it = it0 + 2 * n_kv;
+      }
+      if (!ok && issued) {  // the MMAs issued end before TMEM is released
+        ptx::tc_commit_elect(bar_drain);
+        drain_wait(bar_drain, 0, p);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------- conversion
+    ptx::setmaxnreg_dec<kRegsConvert>();
+    const int cw = warp - 12;
+    int it = 0;                 // tiles converted (K_0, V_0, K_1, ...)
+    int q_uses[2] = {0, 0};
+    int units = 0;
+    for (; more && ok; more = walk.next(p)) {
+      const Unit& w = walk.w;
+      const int bh = w.b * p.Hkv + w.h;
+      const TileWork tw[2] = {tile_work(p, w, 0), tile_work(p, w, 1)};
+      const int n_kv = w.j1 - w.j0;
+      // Unit of V: the largest scale of the part's keys.
+      const float* vs = p.v_scale + static_cast<long long>(bh) * p.nblk;
+      const int key_end = min(w.len, (w.j0 + n_kv) * kTN);
+      float unit = 1.17549435e-38f;
+      for (int i = ((w.j0 * kTN) >> p.block_shift) + lane;
+           i <= (key_end - 1) >> p.block_shift; i += 32)
+        unit = fmaxf(unit, __ldg(vs + i));
+#pragma unroll
+      for (int s = 16; s > 0; s /= 2)
+        unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, s));
+      if (cw == 0 && lane == 0) v_unit[units & 3] = unit;
+      const float inv_unit = 1.f / unit;
+      ++units;
+
+      for (int i = 0; i < 2 * n_kv && ok; ++i) {
+        const bool is_v = i & 1;
+        const int rslot = it % L::kRawSlots, slot = it % L::kSlots;
+        ok = wait(bar_rfull + 8 * rslot, it / L::kRawSlots, 8);
+        if (ok && it >= L::kSlots)
+          ok = wait(bar_empty + 8 * slot, it / L::kSlots - 1, 8);
+        if (!ok) break;
+        const uint32_t raw = s_base + L::kRawRing + rslot * L::kRaw;
+        const uint32_t out = s_base + L::kRing + slot * L::kTile;
+        const int key0 = (w.j0 + (i >> 1)) * kTN;
+        const int valid = w.len - key0;  // rows of the tile that hold tokens
+        // Eight lanes take four 16-byte raw chunks of each of two rows: the
+        // lower four of an even row and the upper four of the odd one (D =
+        // 128), so that neither the reads nor the swizzled writes share a
+        // bank.
+        constexpr int kPer = D / 16;  // raw chunks per row
+        constexpr int kItems = kTN * kPer / 128;
+#pragma unroll 2
+        for (int e = 0; e < kItems; ++e) {
+          const int q = cw * 32 + lane + 128 * e;
+          int row, ch;
+          if constexpr (D == 128) {
+            const int pair = q / 16, in = q % 16;
+            const int odd = (in >> 2) & 1;
+            row = 2 * pair + odd;
+            ch = ((in >> 3) ^ odd) * 4 + (in & 3);
+          } else {
+            row = q / 4;
+            ch = q % 4;
+          }
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < valid) x = ptx::ld_shared_v4(raw + row * D + ch * 16);
+          uint32_t h[8];
+          e4m3x4_to_half2(x.x, h[0], h[1]);
+          e4m3x4_to_half2(x.y, h[2], h[3]);
+          e4m3x4_to_half2(x.z, h[4], h[5]);
+          e4m3x4_to_half2(x.w, h[6], h[7]);
+          if (is_v && row < valid) {
+            const float f =
+                __ldg(vs + ((key0 + row) >> p.block_shift)) * inv_unit;
+            const uint32_t f2 = ptx::pack2<false>(f, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = hmul2(h[k], f2);
+          }
+          const uint32_t at = out + (ch / 4) * L::kBox + row * 128;
+          const uint32_t c0 = (ch % 4) * 2, sw = row % 8;
+          ptx::st_shared_v4(at + ((c0 ^ sw) << 4), h[0], h[1], h[2], h[3]);
+          ptx::st_shared_v4(at + (((c0 + 1) ^ sw) << 4), h[4], h[5], h[6],
+                            h[7]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar_full + 8 * slot);
+          ptx::mbar_arrive(bar_rempty + 8 * rslot);
+        }
+        ++it;
+        if (i > 0) continue;
+        // After the first K tile: the unit's Q tiles, one row per thread
+        // (their buffers are free once the previous unit's last S MMA on
+        // them is done).
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (tw[t].n == 0 || !ok) continue;
+          if (q_uses[t] > 0) ok = wait(bar_qfree + 8 * t, q_uses[t] - 1, 8);
+          if (!ok) break;
+          const int r = cw * 32 + lane;
+          const uint32_t dst =
+              s_base + L::kQ + t * L::kTile + r * 128;
+          const uint32_t sw = r % 8;
+          const bool in = r < tw[t].n_rows;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(p.q) +
+              (in ? q_row_index(p, w, tw[t].r0 + r) * D : 0));
+          float amax = 0.f;
+#pragma unroll 4
+          for (int k = 0; k < D / 8; ++k) {
+            const uint4 x = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              const float2 f = unpack2<kBF16>(xs[a]);
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          const int up = row_shift(amax);
+          float f_up = exp2_int(up);
+          if (p.scale_log2 < 0.f) f_up = -f_up;
+#pragma unroll 4
+          for (int k = 0; k < D / 8; ++k) {
+            const uint4 x = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              const float2 f = unpack2<kBF16>(xs[a]);
+              o[a] = ptx::pack2<false>(f.x * f_up, f.y * f_up);
+            }
+            ptx::st_shared_v4(dst + (k / 8) * L::kBox +
+                                  (((k % 8) ^ sw) << 4),
+                              o[0], o[1], o[2], o[3]);
+          }
+          q_shift[((q_uses[t] & 1) * 2 + t) * kTM + r] =
+              static_cast<signed char>(up);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_q + 8 * t);
+          ++q_uses[t];
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------ softmax, correction, epilogue
+    ptx::setmaxnreg_inc<kRegsSoftmax>();
+    const int t = warp / 4 - 1;
+    const int r = threadIdx.x % kTM;  // row within the tile
+    const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + t * kTN;
+    const uint32_t t_o = tmem + lane_off + kOCol + t * D;
+    int s_uses = 0, o_uses = 0, q_uses = 0, units = 0;
+    for (; more && ok; more = walk.next(p)) {
+      const Unit& w = walk.w;
+      const TileWork tw = tile_work(p, w, t);
+      const int bh = w.b * p.Hkv + w.h;
+      const bool row_ok = r < tw.n_rows;
+      const int vis = row_ok ? row_end(p, w.len, w.n_new, tw.r0 + r)
+                             : (w.j0 + tw.n) * kTN;
+      const float* ks_at = p.k_scale + static_cast<long long>(bh) * p.nblk;
+      float c = 0.f, unit = 1.f;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < tw.n; ++j) {
+        const int key0 = (w.j0 + j) * kTN;
+        // Lane g < 8 holds the K scale of keys 16 g.. of the tile.
+        const int kg = key0 + 16 * (lane & 7);
+        const float ks = kg < w.len ? __ldg(ks_at + (kg >> p.block_shift)) : 1.f;
+        ok = wait(bar_s + 8 * t, s_uses, 4);
+        if (!ok) break;
+        ++s_uses;
+        ptx::tc_fence_after();
+        if (j == 0) {
+          c = fabsf(p.scale_log2) *
+              exp2_int(-q_shift[((q_uses & 1) * 2 + t) * kTM + r]);
+          unit = v_unit[units & 3];
+          ++q_uses;
+        }
+        const bool masked = w.j0 + j >= tw.full || key0 + kTN > w.len;
+        const int lim = masked ? min(vis, w.len) - key0 : kTN;
+        uint32_t sr[kTN];
+#pragma unroll
+        for (int q = 0; q < kTN / 32; ++q) ptx::tmem_ld32(t_s + 32 * q, sr + 32 * q);
+        ptx::tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < kTN; ++q)
+            if (q >= lim) sr[q] = __float_as_uint(-INFINITY);
+        }
+        // Factor of each 16 keys; held off 0 so that -inf stays -inf (scores
+        // times 1e-37 vanish next to any maximum).
+        float f[8];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          f[g] = fmaxf(c * __shfl_sync(0xffffffffu, ks, g), 1e-37f);
+          const uint32_t* x = sr + 16 * g;
+          float a = ptx::fmax3(__uint_as_float(x[0]), __uint_as_float(x[1]),
+                               __uint_as_float(x[2]));
+          float b = ptx::fmax3(__uint_as_float(x[3]), __uint_as_float(x[4]),
+                               __uint_as_float(x[5]));
+          a = ptx::fmax3(a, __uint_as_float(x[6]), __uint_as_float(x[7]));
+          b = ptx::fmax3(b, __uint_as_float(x[8]), __uint_as_float(x[9]));
+          a = ptx::fmax3(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
+          b = ptx::fmax3(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
+          a = ptx::fmax3(a, __uint_as_float(x[14]), __uint_as_float(x[15]));
+          mx = fmaxf(mx, fmaxf(a, b) * f[g]);
+        }
+        float m_new = m_run;
+        if (__any_sync(0xffffffffu, mx > m_run + kTau)) m_new = fmaxf(m_run, mx);
+        const float alpha = (m_new == -INFINITY) ? 1.f : ptx::ex2(m_run - m_new);
+        const float neg_m = (m_new == -INFINITY) ? 0.f : kShift - m_new;
+        float sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < kTN / 32; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int k = 32 * q + 2 * e;
+            float x0, x1;
+            ptx::ffma2(x0, x1, __uint_as_float(sr[k]),
+                       __uint_as_float(sr[k + 1]), f[k / 16], neg_m);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+            if (e & 1)
+              ptx::fadd2(sm[2], sm[3], p0, p1);
+            else
+              ptx::fadd2(sm[0], sm[1], p0, p1);
+            pk[e] = ptx::pack2<false>(p0, p1);
+          }
+          ptx::tmem_st16(t_s + 16 * q, pk);
+        }
+        if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
+          // O *= alpha (the PV before was issued before this S, whose commit
+          // has been awaited).
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            ptx::tmem_ld32(t_o + 32 * q, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            ptx::tmem_st32(t_o + 32 * q, o);
+          }
+        }
+        l_run *= alpha;
+        ptx::tmem_wait_st();
+        l_run += (sm[0] + sm[1]) + (sm[2] + sm[3]);
+        m_run = m_new;
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar_p + 8 * t);
+      }
+      if (!ok) break;
+      if (tw.n > 0) {
+        ok = wait(bar_o + 8 * t, o_uses, 4);
+        if (!ok) break;
+        ++o_uses;
+        ptx::tc_fence_after();
+      }
+      ++units;
+      const bool whole = w.j0 == 0 && w.j1 == w.steps;
+      const int slot = 2 * walk.cta + (w.j0 == 0 ? 1 : 0);
+      if (whole) {
+        const float inv = l_run == 0.f ? 0.f : unit / l_run;
+        const long long row = row_ok ? q_row_index(p, w, tw.r0 + r) : 0;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
+                                              row * D);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (tw.n > 0) {
+            ptx::tmem_ld32(t_o + 32 * q, o);
+            ptx::tmem_wait_ld();
+          } else {  // no row of the tile sees a token
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (row_ok) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // A row that sees nothing: 0, whatever its accumulator holds.
+                const float a = __uint_as_float(o[8 * v + 2 * e]);
+                const float b = __uint_as_float(o[8 * v + 2 * e + 1]);
+                x[e] = l_run == 0.f ? 0u : ptx::pack2<kBF16>(a * inv, b * inv);
+              }
+              dst[4 * q + v] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+        if (row_ok) {
+          const float lse2 = l_run == 0.f
+                                 ? -INFINITY
+                                 : (m_run == -INFINITY ? kNone : m_run) +
+                                       log2f(l_run) - kShift;
+          if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
+          if (p.lse2 != nullptr)
+            p.lse2[(static_cast<long long>(bh) * p.row_blocks) * kUnitRows +
+                   tw.r0 + r] = lse2;
+        }
+      } else {
+        const long long at = static_cast<long long>(slot) * kUnitRows +
+                             t * kTM + r;
+        float4* dst = reinterpret_cast<float4*>(p.part_o) + at * (D / 4);
+        if (tw.n > 0) {
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            ptx::tmem_ld32(t_o + 32 * q, o);
+            ptx::tmem_wait_ld();
+            if (row_ok) {
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                dst[8 * q + v] =
+                    make_float4(__uint_as_float(o[4 * v]) * unit,
+                                __uint_as_float(o[4 * v + 1]) * unit,
+                                __uint_as_float(o[4 * v + 2]) * unit,
+                                __uint_as_float(o[4 * v + 3]) * unit);
+            }
+          }
+        }
+        if (row_ok)
+          p.part_ml[at] =
+              make_float2(m_run == -INFINITY ? kNone : m_run, l_run);
+        // The CTA of the last part says where the parts are.
+        if (w.j1 == w.steps && t == 0 && r == 0) {
+          const int here = walk.first(walk.cta + 1) - 1 - walk.left;
+          const int c0 = walk.owner(here - (w.steps - 1));
+          p.parts[(static_cast<long long>(w.b) * p.row_blocks + w.u) * p.Hkv +
+                  w.h] = make_int2(c0, walk.cta - c0 + 1);
+        }
+      }
+      if (whole && t == 0 && r == 0)
+        p.parts[(static_cast<long long>(w.b) * p.row_blocks + w.u) * p.Hkv +
+                w.h] = make_int2(walk.cta, 1);
+      ptx::tc_fence_before();
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// Joins the parts of the units that more than one CTA worked on, and writes
+// the rows of units that see nothing: a CTA takes 32 rows of a unit, a warp
+// one row at a time.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 32;
+
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kMergeThreads)
+    kv8_prefill_merge_kernel(const FwdParams p) {
+  constexpr int kPer = kUnitRows / kMergeRows;  // CTAs per unit
+  constexpr int kCols = D / 4;                  // float4 columns
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int unit = blockIdx.x / kPer;
+  const int part = blockIdx.x - unit * kPer;
+  const int pair = unit / p.Hkv, h = unit - pair * p.Hkv;
+  Unit w;
+  w.b = pair / p.row_blocks;
+  w.u = pair - w.b * p.row_blocks;
+  w.h = h;
+  w.steps = pair_steps(p, pair, &w.len, &w.n_new);
+  const int row0 = w.u * kUnitRows + part * kMergeRows;
+  const int n_rows = min(kMergeRows, w.n_new * p.group - row0);
+  if (n_rows <= 0) return;
+  ptx::griddep_wait();
+  int2 parts = make_int2(0, 0);
+  if (w.steps > 0) parts = p.parts[unit];
+  if (parts.y == 1) return;  // the CTA of the unit has finished it
+  const int col = lane % kCols;
+  for (int i = warp; i < n_rows; i += kMergeThreads / 32) {
+    float mx = kNone, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto slot_row = [&](int s) {
+      const int slot = s == 0 ? 2 * parts.x + 1 : 2 * (parts.x + s);
+      return static_cast<long long>(slot) * kUnitRows + part * kMergeRows + i;
+    };
+    for (int s = 0; s < parts.y; ++s)
+      mx = fmaxf(mx, p.part_ml[slot_row(s)].x);
+#pragma unroll 4
+    for (int s = 0; s < parts.y; ++s) {
+      const long long at = slot_row(s);
+      const float2 ml = p.part_ml[at];
+      if (ml.y == 0.f) continue;  // sees nothing of the part: not written
+      const float f = ptx::ex2(ml.x - mx);
+      const float4 y =
+          reinterpret_cast<const float4*>(p.part_o)[at * kCols + col];
+      sum += ml.y * f;
+      acc.x += y.x * f;
+      acc.y += y.y * f;
+      acc.z += y.z * f;
+      acc.w += y.w * f;
+    }
+    const long long row = q_row_index(p, w, row0 + i);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (lane < kCols) {
+      uint2 out;
+      out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
+      out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[col] =
+          out;
+    }
+    if (lane == 0) {
+      const float lse2 =
+          sum == 0.f ? -INFINITY : mx + log2f(sum) - kShift;
+      if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
+      if (p.lse2 != nullptr)
+        p.lse2[(static_cast<long long>(w.b) * p.Hkv + h) * p.row_blocks *
+                   kUnitRows + row0 + i] = lse2;
+    }
+  }
+}
+
+template <int D, bool kBF16>
+cudaError_t launch(const FwdParams& p, cudaStream_t stream) {
+  constexpr int kBytes = Smem<D>::kBytes + 1024;
+  cudaError_t err = cudaFuncSetAttribute(
+      kv8_prefill_kernel<D, kBF16>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (err != cudaSuccess) return err;
+  kv8_prefill_kernel<D, kBF16><<<p.grid, kThreads, kBytes, stream>>>(p);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kv8_prefill_merge_kernel<D, kBF16>,
+                    static_cast<long long>(p.B) * p.row_blocks * p.Hkv *
+                        (kUnitRows / kMergeRows),
+                    kMergeThreads, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(int D, bool bf16, const FwdParams& p,
+                           cudaStream_t stream) {
+  if (D == 64)
+    return bf16 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+  return bf16 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
+}
+
+}  // namespace kv8
+}  // namespace attn
