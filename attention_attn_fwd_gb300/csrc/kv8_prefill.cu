@@ -11,9 +11,9 @@
 //     keys at a time; V's scale over the largest one of the unit's keys
 //     multiplies V's halves (exact for powers of two; else one fp16 rounding,
 //     2^-11, as P's own);
-//   - the same warpgroup brings Q rows to fp16 with a power of two per row
+//   - each softmax thread brings its Q row to fp16 with a power of two
 //     (exact down to 2^-37 of the row's largest element) and the sign of the
-//     scale.
+//     scale, while the previous unit's last products run.
 // P is kept shifted by 2^7 (it is at most 2^15, and normal down to 2^-21 of
 // its row's largest), as are the row sums, which take P unrounded.
 //
@@ -25,8 +25,9 @@
 // and are joined by the merge kernel.
 //
 // Roles (512 threads): warp 0 MMA issue, warp 1 bulk copies of the raw
-// tiles, warps 4-7 / 8-11 softmax and epilogue of Q tile 0 / 1, warps 12-15
-// conversion.  Every wait is bounded as in the forward kernel.
+// tiles, warp 2 walks the share and publishes its units in shared memory,
+// warps 4-7 / 8-11 Q conversion, softmax and epilogue of Q tile 0 / 1, warps
+// 12-15 K and V conversion.  Every wait is bounded as in the forward kernel.
 #include "attn_sync.cuh"
 #include "kv8_common.cuh"
 
@@ -48,24 +49,42 @@ constexpr int kRegsConvert = 64;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128,
               "register split exceeds the launch allocation");
 
+constexpr int kUnits = 4;  // published units held at a time
+
+// A unit's part as the roles need it.
+struct Record {
+  int n_kv;       // key tiles of the part; 0: no more units
+  int j0;         // first of them
+  int b, h, len, n_new;
+  int row0;       // first row of tile 0
+  int slot;       // workspace slot of a part; -1: this CTA has all of the unit
+  int n[2];       // key tiles each Q tile sees
+  int full[2];    // tiles below this one are seen whole by each valid row
+  int unit;       // its index
+  int c0, parts;  // last part: first CTA of the unit, and how many; else 0
+  float v_unit;   // largest V scale of the part's keys (by the converters)
+};
+static_assert(sizeof(Record) == 64, "record size");
+
 template <int D>
 struct Smem {
   static constexpr int kBox = kTN * 128;             // 128 rows x 128 bytes
   static constexpr int kTile = kBox * (D / 64);      // one fp16 tile
   static constexpr int kRaw = kTN * D;               // one raw tile
-  static constexpr int kSlots = 4;                   // fp16 tiles
-  static constexpr int kRawSlots = D == 128 ? 2 : 4; // raw tiles
+  // fp16 tiles: V_j and K_j+1 in use, the next being written.  Raw tiles:
+  // as many bytes in flight as fit.
+  static constexpr int kSlots = D == 128 ? 3 : 5;
+  static constexpr int kRawSlots = D == 128 ? 4 : 8;
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
   static constexpr int kRawRing = kRing + kSlots * kTile;
-  static constexpr int kShifts = kRawRing + kRawSlots * kRaw;  // [2][2][128]
-  static constexpr int kBars = kShifts + 2 * 2 * kTM;
-  // raw_full, raw_empty, kv_full, kv_empty, q_full[2], q_free[2], s[2],
-  // p[2], o[2], drain
-  static constexpr int kNumBars = 2 * kRawSlots + 2 * kSlots + 11;
+  static constexpr int kBars = kRawRing + kRawSlots * kRaw;
+  // raw_full, raw_empty, kv_full, kv_empty, unit_full, unit_empty, q[2],
+  // s[2], p[2], o[2], drain
+  static constexpr int kNumBars = 2 * kRawSlots + 2 * kSlots + 2 * kUnits + 9;
   static constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM base, abort
-  static constexpr int kUnit = kMisc + 8;             // V units, [4]
-  static constexpr int kBytes = kUnit + 16;
+  static constexpr int kRecords = kMisc + 8;
+  static constexpr int kBytes = kRecords + kUnits * 64;
   static_assert(kBytes + 1024 <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -182,28 +201,39 @@ struct Walk {
   }
 };
 
-// What a Q tile of the unit's part has to do.
-struct TileWork {
-  int r0;      // first row
-  int n_rows;  // valid rows
-  int n;       // key tiles of the part it sees, from j0
-  int full;    // key tiles below this one are seen whole by every valid row
-};
-__device__ __forceinline__ TileWork tile_work(const FwdParams& p,
-                                              const Unit& w, int t) {
-  TileWork k;
-  k.r0 = w.u * kUnitRows + t * kTM;
-  k.n_rows = max(0, min(kTM, w.n_new * p.group - k.r0));
-  const int hi = tiles_seen(p, w.len, w.n_new, k.r0, k.r0 + kTM);
-  k.n = max(0, min(hi, w.j1) - w.j0);
-  k.full = k.n_rows > 0 ? row_end(p, w.len, w.n_new, k.r0) / kTN : 0;
-  return k;
-}
-__device__ __forceinline__ long long q_row_index(const FwdParams& p,
-                                                 const Unit& w, int r) {
+__device__ __forceinline__ long long q_row_index(const FwdParams& p, int b,
+                                                 int h, int r) {
   const int tok = r / p.group, hd = r - tok * p.group;
-  return (static_cast<long long>(w.b) * p.Hq + w.h * p.group + hd) * p.Sq +
-         tok;
+  return (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
+}
+
+__device__ __forceinline__ void fill_record(const FwdParams& p,
+                                            const Walk& walk,
+                                            volatile Record* rec) {
+  const Unit& w = walk.w;
+  rec->n_kv = w.j1 - w.j0;
+  rec->j0 = w.j0;
+  rec->b = w.b;
+  rec->h = w.h;
+  rec->len = w.len;
+  rec->n_new = w.n_new;
+  rec->row0 = w.u * kUnitRows;
+  const bool whole = w.j0 == 0 && w.j1 == w.steps;
+  rec->slot = whole ? -1 : 2 * walk.cta + (w.j0 == 0 ? 1 : 0);
+  for (int t = 0; t < 2; ++t) {
+    const int r0 = w.u * kUnitRows + t * kTM;
+    const int hi = tiles_seen(p, w.len, w.n_new, r0, r0 + kTM);
+    rec->n[t] = max(0, min(hi, w.j1) - w.j0);
+    rec->full[t] = row_end(p, w.len, w.n_new, r0) / kTN;
+  }
+  rec->unit = (w.b * p.row_blocks + w.u) * p.Hkv + w.h;
+  rec->c0 = rec->parts = 0;
+  if (w.j1 == w.steps) {  // position of the unit's last step, then its first
+    const int last = walk.first(walk.cta + 1) - 1 - walk.left;
+    const int c0 = walk.owner(last - (w.steps - 1));
+    rec->c0 = c0;
+    rec->parts = walk.cta - c0 + 1;
+  }
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
@@ -235,30 +265,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_rempty = bar_rfull + 8 * L::kRawSlots;
   const uint32_t bar_full = bar_rempty + 8 * L::kRawSlots;
   const uint32_t bar_empty = bar_full + 8 * L::kSlots;
-  const uint32_t bar_q = bar_empty + 8 * L::kSlots;  // [2]
-  const uint32_t bar_qfree = bar_q + 16;             // [2]
-  const uint32_t bar_s = bar_qfree + 16;             // [2]
-  const uint32_t bar_p = bar_s + 16;                 // [2]
-  const uint32_t bar_o = bar_p + 16;                 // [2]
-  const uint32_t bar_drain = bar_o + 16;             // [1]
-  volatile signed char* q_shift =  // log2 of the factor each Q row got
-      reinterpret_cast<signed char*>(smem + L::kShifts);
+  const uint32_t bar_unit = bar_empty + 8 * L::kSlots;  // [kUnits]
+  const uint32_t bar_ufree = bar_unit + 8 * kUnits;     // [kUnits]
+  const uint32_t bar_q = bar_ufree + 8 * kUnits;        // [2]
+  const uint32_t bar_s = bar_q + 16;                    // [2]
+  const uint32_t bar_p = bar_s + 16;                    // [2]
+  const uint32_t bar_o = bar_p + 16;                    // [2]
+  const uint32_t bar_drain = bar_o + 16;                // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
-  volatile float* v_unit = reinterpret_cast<float*>(smem + L::kUnit);
+  volatile Record* records = reinterpret_cast<Record*>(smem + L::kRecords);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   ptx::griddep_launch_dependents();  // the merge kernel waits for this grid
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       const uint32_t bar = s_base + L::kBars + 8 * i;
-      // Converted tiles, freed raw tiles and Q tiles: one arrival per
-      // converting warp; P: one per softmax thread of the tile.
+      // Converted tiles, freed raw tiles and Q tiles: one arrival per warp
+      // of the four; units read: one per warp of the other roles (14); P:
+      // one per softmax thread of the tile.
       uint32_t count = 1;
-      if ((bar >= bar_rempty && bar < bar_full) ||
-          (bar >= bar_full && bar < bar_empty) ||
-          (bar >= bar_q && bar < bar_qfree))
+      if ((bar >= bar_rempty && bar < bar_empty) ||
+          (bar >= bar_q && bar < bar_s))
         count = 4;
+      if (bar >= bar_ufree && bar < bar_q) count = 14;
       if (bar >= bar_p && bar < bar_o) count = kTM;
       ptx::mbar_init(bar, count);
     }
@@ -274,27 +304,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk walk;
-  bool more = walk.take(p, static_cast<int>(blockIdx.x), lane);
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase, int role) {
     return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1, abort_flag, p,
                                                 role)) != 0;
   };
+  // The k-th unit, nullptr at the end of the share (or on abort); and its
+  // release by this warp.
+  auto get_unit = [&](int k) -> volatile Record* {
+    ok = wait(bar_unit + 8 * (k % kUnits), k / kUnits, 1);
+    if (!ok) return nullptr;
+    volatile Record* rec = records + k % kUnits;
+    return rec->n_kv > 0 ? rec : nullptr;
+  };
+  auto release_unit = [&](int k) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar_ufree + 8 * (k % kUnits));
+  };
 
   if (warp < 4) {
     ptx::setmaxnreg_dec<kRegsControl>();
-    if (warp == 1) {
+    if (warp == 2) {
+      // ------------------------------------------------ units of the share
+      Walk walk;
+      bool more = walk.take(p, static_cast<int>(blockIdx.x), lane);
+      for (int k = 0; ok; ++k) {
+        if (k >= kUnits)
+          ok = wait(bar_ufree + 8 * (k % kUnits), k / kUnits - 1, 1);
+        if (!ok) break;
+        volatile Record* rec = records + k % kUnits;
+        if (lane == 0) {
+          if (more)
+            fill_record(p, walk, rec);
+          else
+            rec->n_kv = 0;
+          ptx::mbar_arrive(bar_unit + 8 * (k % kUnits));
+        }
+        __syncwarp();
+        if (!more) break;
+        more = walk.next(p);
+      }
+    } else if (warp == 1) {
       // ---------------------------------------------------- raw tile loads
       int it = 0;
-      for (; more && ok; more = walk.next(p)) {
-        const Unit& w = walk.w;
-        const int n = w.j1 - w.j0;
+      for (int k = 0; ok; ++k) {
+        volatile Record* rec = get_unit(k);
+        if (rec == nullptr) break;
+        const int n = rec->n_kv, j0 = rec->j0, len = rec->len;
         const long long head =
-            (static_cast<long long>(w.b) * p.Hkv + w.h) * p.capacity * D;
+            (static_cast<long long>(rec->b) * p.Hkv + rec->h) * p.capacity * D;
+        release_unit(k);
         for (int j = 0; j < n && ok; ++j) {
-          const int key0 = (w.j0 + j) * kTN;
-          const uint32_t bytes = min(kTN, w.len - key0) * D;
+          const int key0 = (j0 + j) * kTN;
+          const uint32_t bytes = min(kTN, len - key0) * D;
           for (int kv = 0; kv < 2; ++kv) {
             const int slot = it % L::kRawSlots, use = it / L::kRawSlots;
             if (use > 0) ok = wait(bar_rempty + 8 * slot, use - 1, 1);
@@ -346,10 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0;  // converted tiles consumed
       int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
       bool issued = false;
-      for (; more && ok; more = walk.next(p)) {
-        const int n0 = tile_work(p, walk.w, 0).n;
-        const int n1 = tile_work(p, walk.w, 1).n;
-        const int n_kv = walk.w.j1 - walk.w.j0;  // = max(n0, n1)
+      for (int k = 0; ok; ++k) {
+        volatile Record* rec = get_unit(k);
+        if (rec == nullptr) break;
+        const int n0 = rec->n[0], n1 = rec->n[1];
+        const int n_kv = rec->n_kv;  // = max(n0, n1)
+        release_unit(k);
         ok = wait(bar_full + 8 * (it % L::kSlots), it / L::kSlots, 2);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -360,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++q_uses[t];
           ptx::tc_fence_after();
           issue_qk(t, it % L::kSlots);
-          if (n == 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
           issued = true;
         }
         if (!ok) break;
@@ -392,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tc_fence_after();
             }
             issue_qk(t, slot_k);
-            if (j + 1 == n - 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
           }
           if (!ok) break;
           ptx::tc_commit_elect(bar_empty + 8 * slot_v);
@@ -410,137 +472,110 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------- conversion
     ptx::setmaxnreg_dec<kRegsConvert>();
     const int cw = warp - 12;
+    // Each thread converts one 16-byte raw chunk of every 16th (D = 64:
+    // 32nd) row.  Eight lanes take four chunks of each of two rows: D = 128
+    // the lower four of one row and the upper four of the next, so that
+    // neither the reads nor the swizzled writes share a bank.
+    constexpr int kItems = D / 16;
+    constexpr int kRowStep = kTN / kItems;
+    int row0, ch;
+    {
+      const int q = cw * 32 + lane;
+      if constexpr (D == 128) {
+        const int odd = (q >> 2) & 1;
+        row0 = 2 * (q / 16) + odd;
+        ch = (((q >> 3) & 1) ^ odd) * 4 + (q & 3);
+      } else {
+        row0 = q / 4;
+        ch = q % 4;
+      }
+    }
+    const uint32_t raw_off = row0 * D + ch * 16;
+    const uint32_t out_off = (ch / 4) * L::kBox + row0 * 128;
+    const uint32_t out0 = out_off + ((((ch % 4) * 2) ^ (row0 % 8)) << 4);
+    const uint32_t out1 = out_off + ((((ch % 4) * 2 + 1) ^ (row0 % 8)) << 4);
     int it = 0;                 // tiles converted (K_0, V_0, K_1, ...)
-    int q_uses[2] = {0, 0};
-    int units = 0;
-    for (; more && ok; more = walk.next(p)) {
-      const Unit& w = walk.w;
-      const int bh = w.b * p.Hkv + w.h;
-      const TileWork tw[2] = {tile_work(p, w, 0), tile_work(p, w, 1)};
-      const int n_kv = w.j1 - w.j0;
+    for (int k = 0; ok; ++k) {
+      volatile Record* rec = get_unit(k);
+      if (rec == nullptr) break;
+      const int bh = rec->b * p.Hkv + rec->h;
+      const int n_kv = rec->n_kv, j0 = rec->j0, len = rec->len;
       // Unit of V: the largest scale of the part's keys.
       const float* vs = p.v_scale + static_cast<long long>(bh) * p.nblk;
-      const int key_end = min(w.len, (w.j0 + n_kv) * kTN);
+      const int key_end = min(len, (j0 + n_kv) * kTN);
       float unit = 1.17549435e-38f;
-      for (int i = ((w.j0 * kTN) >> p.block_shift) + lane;
+      for (int i = ((j0 * kTN) >> p.block_shift) + lane;
            i <= (key_end - 1) >> p.block_shift; i += 32)
         unit = fmaxf(unit, __ldg(vs + i));
 #pragma unroll
       for (int s = 16; s > 0; s /= 2)
         unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, s));
-      if (cw == 0 && lane == 0) v_unit[units & 3] = unit;
+      if (cw == 0 && lane == 0) rec->v_unit = unit;
       const float inv_unit = 1.f / unit;
-      ++units;
+      release_unit(k);
 
       for (int i = 0; i < 2 * n_kv && ok; ++i) {
         const bool is_v = i & 1;
         const int rslot = it % L::kRawSlots, slot = it % L::kSlots;
-        ok = wait(bar_rfull + 8 * rslot, it / L::kRawSlots, 8);
-        if (ok && it >= L::kSlots)
-          ok = wait(bar_empty + 8 * slot, it / L::kSlots - 1, 8);
-        if (!ok) break;
-        const uint32_t raw = s_base + L::kRawRing + rslot * L::kRaw;
-        const uint32_t out = s_base + L::kRing + slot * L::kTile;
-        const int key0 = (w.j0 + (i >> 1)) * kTN;
-        const int valid = w.len - key0;  // rows of the tile that hold tokens
-        // Eight lanes take four 16-byte raw chunks of each of two rows: the
-        // lower four of an even row and the upper four of the odd one (D =
-        // 128), so that neither the reads nor the swizzled writes share a
-        // bank.
-        constexpr int kPer = D / 16;  // raw chunks per row
-        constexpr int kItems = kTN * kPer / 128;
-#pragma unroll 2
-        for (int e = 0; e < kItems; ++e) {
-          const int q = cw * 32 + lane + 128 * e;
-          int row, ch;
-          if constexpr (D == 128) {
-            const int pair = q / 16, in = q % 16;
-            const int odd = (in >> 2) & 1;
-            row = 2 * pair + odd;
-            ch = ((in >> 3) ^ odd) * 4 + (in & 3);
-          } else {
-            row = q / 4;
-            ch = q % 4;
-          }
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < valid) x = ptx::ld_shared_v4(raw + row * D + ch * 16);
-          uint32_t h[8];
-          e4m3x4_to_half2(x.x, h[0], h[1]);
-          e4m3x4_to_half2(x.y, h[2], h[3]);
-          e4m3x4_to_half2(x.z, h[4], h[5]);
-          e4m3x4_to_half2(x.w, h[6], h[7]);
-          if (is_v && row < valid) {
-            const float f =
-                __ldg(vs + ((key0 + row) >> p.block_shift)) * inv_unit;
-            const uint32_t f2 = ptx::pack2<false>(f, f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = hmul2(h[k], f2);
-          }
-          const uint32_t at = out + (ch / 4) * L::kBox + row * 128;
-          const uint32_t c0 = (ch % 4) * 2, sw = row % 8;
-          ptx::st_shared_v4(at + ((c0 ^ sw) << 4), h[0], h[1], h[2], h[3]);
-          ptx::st_shared_v4(at + (((c0 + 1) ^ sw) << 4), h[4], h[5], h[6],
-                            h[7]);
+        const int key0 = (j0 + (i >> 1)) * kTN;
+        const int valid = len - key0;  // rows of the tile that hold tokens
+        // V: lane g < 8 holds the factor of rows 16 g.. of the tile.
+        float f_all = 1.f;
+        if (is_v) {
+          const int key = key0 + 16 * (lane & 7);
+          if (key < len) f_all = __ldg(vs + (key >> p.block_shift)) * inv_unit;
         }
+        ok = wait(bar_rfull + 8 * rslot, it / L::kRawSlots, 8);
+        if (!ok) break;
+        const uint32_t raw = s_base + L::kRawRing + rslot * L::kRaw + raw_off;
+        const uint32_t out = s_base + L::kRing + slot * L::kTile;
+        constexpr int kBatch = 4;  // chunks in registers at a time
+#pragma unroll
+        for (int e0 = 0; e0 < kItems; e0 += kBatch) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e)
+            x[e] = ptx::ld_shared_v4(raw + (e0 + e) * kRowStep * D);
+          if (valid < kTN) {  // rows past the length: zeros
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              if (row0 + (e0 + e) * kRowStep >= valid)
+                x[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (e0 + kBatch >= kItems) {
+            // The raw tile has been read.
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_rempty + 8 * rslot);
+          }
+          if (e0 == 0 && it >= L::kSlots) {
+            ok = wait(bar_empty + 8 * slot, it / L::kSlots - 1, 8);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) {
+            uint32_t h[8];
+            e4m3x4_to_half2(x[e].x, h[0], h[1]);
+            e4m3x4_to_half2(x[e].y, h[2], h[3]);
+            e4m3x4_to_half2(x[e].z, h[4], h[5]);
+            e4m3x4_to_half2(x[e].w, h[6], h[7]);
+            if (is_v) {
+              // Rows of this step lie in one 16-key group.
+              const int g = D == 128 ? e0 + e : cw / 2 + 2 * (e0 + e);
+              const float f = __shfl_sync(0xffffffffu, f_all, g);
+              const uint32_t f2 = ptx::pack2<false>(f, f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) h[k] = hmul2(h[k], f2);
+            }
+            const uint32_t at = out + (e0 + e) * kRowStep * 128;
+            ptx::st_shared_v4(at + out0, h[0], h[1], h[2], h[3]);
+            ptx::st_shared_v4(at + out1, h[4], h[5], h[6], h[7]);
+          }
+        }
+        if (!ok) break;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar_full + 8 * slot);
-          ptx::mbar_arrive(bar_rempty + 8 * rslot);
-        }
+        if (lane == 0) ptx::mbar_arrive(bar_full + 8 * slot);
         ++it;
-        if (i > 0) continue;
-        // After the first K tile: the unit's Q tiles, one row per thread
-        // (their buffers are free once the previous unit's last S MMA on
-        // them is done).
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (tw[t].n == 0 || !ok) continue;
-          if (q_uses[t] > 0) ok = wait(bar_qfree + 8 * t, q_uses[t] - 1, 8);
-          if (!ok) break;
-          const int r = cw * 32 + lane;
-          const uint32_t dst =
-              s_base + L::kQ + t * L::kTile + r * 128;
-          const uint32_t sw = r % 8;
-          const bool in = r < tw[t].n_rows;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const uint16_t*>(p.q) +
-              (in ? q_row_index(p, w, tw[t].r0 + r) * D : 0));
-          float amax = 0.f;
-#pragma unroll 4
-          for (int k = 0; k < D / 8; ++k) {
-            const uint4 x = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-              const float2 f = unpack2<kBF16>(xs[a]);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          }
-          const int up = row_shift(amax);
-          float f_up = exp2_int(up);
-          if (p.scale_log2 < 0.f) f_up = -f_up;
-#pragma unroll 4
-          for (int k = 0; k < D / 8; ++k) {
-            const uint4 x = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-              const float2 f = unpack2<kBF16>(xs[a]);
-              o[a] = ptx::pack2<false>(f.x * f_up, f.y * f_up);
-            }
-            ptx::st_shared_v4(dst + (k / 8) * L::kBox +
-                                  (((k % 8) ^ sw) << 4),
-                              o[0], o[1], o[2], o[3]);
-          }
-          q_shift[((q_uses[t] & 1) * 2 + t) * kTM + r] =
-              static_cast<signed char>(up);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar_q + 8 * t);
-          ++q_uses[t];
-        }
       }
     }
     __syncwarp();
@@ -552,34 +587,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + t * kTN;
     const uint32_t t_o = tmem + lane_off + kOCol + t * D;
-    int s_uses = 0, o_uses = 0, q_uses = 0, units = 0;
-    for (; more && ok; more = walk.next(p)) {
-      const Unit& w = walk.w;
-      const TileWork tw = tile_work(p, w, t);
-      const int bh = w.b * p.Hkv + w.h;
-      const bool row_ok = r < tw.n_rows;
-      const int vis = row_ok ? row_end(p, w.len, w.n_new, tw.r0 + r)
-                             : (w.j0 + tw.n) * kTN;
-      const float* ks_at = p.k_scale + static_cast<long long>(bh) * p.nblk;
-      float c = 0.f, unit = 1.f;
+    int s_uses = 0, o_uses = 0;
+    // This thread's Q row of unit `rec` to fp16 in shared memory; returns the
+    // factor of its scores.  The buffer is free: every S of the tile has been
+    // read.
+    auto stage_q = [&](volatile Record* rec) -> float {
+      const int row = rec->row0 + t * kTM + r;
+      const bool in = row < rec->n_new * p.group;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(p.q) +
+          (in ? q_row_index(p, rec->b, rec->h, row) * D : 0));
+      uint32_t x[D / 2];
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        const uint4 y = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+        x[4 * k] = y.x;
+        x[4 * k + 1] = y.y;
+        x[4 * k + 2] = y.z;
+        x[4 * k + 3] = y.w;
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 2; ++k) {
+        const float2 f = unpack2<kBF16>(x[k]);
+        amax = ptx::fmax3(amax, fabsf(f.x), fabsf(f.y));
+      }
+      const int up = row_shift(amax);
+      float f_up = exp2_int(up);
+      if (p.scale_log2 < 0.f) f_up = -f_up;
+      const uint32_t dst = s_base + L::kQ + t * L::kTile + r * 128;
+      const uint32_t sw = r % 8;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        uint32_t o[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const float2 f = unpack2<kBF16>(x[4 * k + a]);
+          o[a] = ptx::pack2<false>(f.x * f_up, f.y * f_up);
+        }
+        ptx::st_shared_v4(dst + (k / 8) * L::kBox + (((k % 8) ^ sw) << 4),
+                          o[0], o[1], o[2], o[3]);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_q + 8 * t);
+      return fabsf(p.scale_log2) * exp2_int(-up);
+    };
+    volatile Record* rec = get_unit(0);
+    float c_next = 0.f;
+    if (rec != nullptr && rec->n[t] > 0) c_next = stage_q(rec);
+    for (int k = 0; rec != nullptr; ++k) {
+      const int n = rec->n[t], j0 = rec->j0, len = rec->len;
+      const int full = rec->full[t];
+      const float c = c_next;
+      const float* ks_at =
+          p.k_scale +
+          (static_cast<long long>(rec->b) * p.Hkv + rec->h) * p.nblk;
+      int vis;
+      {
+        const int row = rec->row0 + t * kTM + r, n_new = rec->n_new;
+        vis = row < n_new * p.group ? row_end(p, len, n_new, row) : len;
+      }
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < tw.n; ++j) {
-        const int key0 = (w.j0 + j) * kTN;
+      for (int j = 0; j < n; ++j) {
+        const int key0 = (j0 + j) * kTN;
         // Lane g < 8 holds the K scale of keys 16 g.. of the tile.
         const int kg = key0 + 16 * (lane & 7);
-        const float ks = kg < w.len ? __ldg(ks_at + (kg >> p.block_shift)) : 1.f;
+        const float ks = kg < len ? __ldg(ks_at + (kg >> p.block_shift)) : 1.f;
         ok = wait(bar_s + 8 * t, s_uses, 4);
         if (!ok) break;
         ++s_uses;
         ptx::tc_fence_after();
-        if (j == 0) {
-          c = fabsf(p.scale_log2) *
-              exp2_int(-q_shift[((q_uses & 1) * 2 + t) * kTM + r]);
-          unit = v_unit[units & 3];
-          ++q_uses;
-        }
-        const bool masked = w.j0 + j >= tw.full || key0 + kTN > w.len;
-        const int lim = masked ? min(vis, w.len) - key0 : kTN;
+        const bool masked = j0 + j >= full;
+        const int lim = masked ? vis - key0 : kTN;
         uint32_t sr[kTN];
 #pragma unroll
         for (int q = 0; q < kTN / 32; ++q) ptx::tmem_ld32(t_s + 32 * q, sr + 32 * q);
@@ -653,24 +733,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive(bar_p + 8 * t);
       }
       if (!ok) break;
-      if (tw.n > 0) {
+      // The next unit's Q while this one's last products run.
+      volatile Record* next = get_unit(k + 1);
+      if (!ok) break;
+      if (next != nullptr && next->n[t] > 0) c_next = stage_q(next);
+      if (n > 0) {
         ok = wait(bar_o + 8 * t, o_uses, 4);
         if (!ok) break;
         ++o_uses;
         ptx::tc_fence_after();
       }
-      ++units;
-      const bool whole = w.j0 == 0 && w.j1 == w.steps;
-      const int slot = 2 * walk.cta + (w.j0 == 0 ? 1 : 0);
-      if (whole) {
+      const float unit = rec->v_unit;
+      const int slot = rec->slot;
+      const int row_u = rec->row0 + t * kTM + r;  // row of the K/V head
+      const bool row_ok = row_u < rec->n_new * p.group;
+      if (slot < 0) {
         const float inv = l_run == 0.f ? 0.f : unit / l_run;
-        const long long row = row_ok ? q_row_index(p, w, tw.r0 + r) : 0;
+        const long long row =
+            row_ok ? q_row_index(p, rec->b, rec->h, row_u) : 0;
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
                                               row * D);
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
-          if (tw.n > 0) {
+          if (n > 0) {
             ptx::tmem_ld32(t_o + 32 * q, o);
             ptx::tmem_wait_ld();
           } else {  // no row of the tile sees a token
@@ -699,14 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        log2f(l_run) - kShift;
           if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
           if (p.lse2 != nullptr)
-            p.lse2[(static_cast<long long>(bh) * p.row_blocks) * kUnitRows +
-                   tw.r0 + r] = lse2;
+            p.lse2[(static_cast<long long>(rec->b) * p.Hkv + rec->h) *
+                       p.row_blocks * kUnitRows + row_u] = lse2;
         }
       } else {
-        const long long at = static_cast<long long>(slot) * kUnitRows +
-                             t * kTM + r;
+        const long long at =
+            static_cast<long long>(slot) * kUnitRows + t * kTM + r;
         float4* dst = reinterpret_cast<float4*>(p.part_o) + at * (D / 4);
-        if (tw.n > 0) {
+        if (n > 0) {
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
@@ -726,18 +812,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row_ok)
           p.part_ml[at] =
               make_float2(m_run == -INFINITY ? kNone : m_run, l_run);
-        // The CTA of the last part says where the parts are.
-        if (w.j1 == w.steps && t == 0 && r == 0) {
-          const int here = walk.first(walk.cta + 1) - 1 - walk.left;
-          const int c0 = walk.owner(here - (w.steps - 1));
-          p.parts[(static_cast<long long>(w.b) * p.row_blocks + w.u) * p.Hkv +
-                  w.h] = make_int2(c0, walk.cta - c0 + 1);
-        }
       }
-      if (whole && t == 0 && r == 0)
-        p.parts[(static_cast<long long>(w.b) * p.row_blocks + w.u) * p.Hkv +
-                w.h] = make_int2(walk.cta, 1);
+      // The CTA of a unit's last part says where its parts are.
+      if (t == 0 && r == 0 && rec->parts > 0)
+        p.parts[rec->unit] = make_int2(rec->c0, rec->parts);
       ptx::tc_fence_before();
+      release_unit(k);
+      rec = next;
     }
   }
 
@@ -801,7 +882,7 @@ __global__ void __launch_bounds__(kMergeThreads)
       acc.z += y.z * f;
       acc.w += y.w * f;
     }
-    const long long row = q_row_index(p, w, row0 + i);
+    const long long row = q_row_index(p, w.b, h, row0 + i);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (lane < kCols) {
       uint2 out;
