@@ -109,7 +109,7 @@ RowPlan plan_rows(int Hq, int Hkv, int Sq, int sms) {
 }
 
 struct Workspace {
-  size_t part_o, part_ml, scores, parts, lse2, total;
+  size_t part_o, part_ml, scores, split, lse2, total;
 };
 
 Workspace workspace_layout(int B, int Hkv, int capacity, int D,
@@ -121,9 +121,9 @@ Workspace workspace_layout(int B, int Hkv, int capacity, int D,
   w.part_o = 0;
   w.part_ml = w.part_o + round_up(slots * r.tile * D * 4);
   w.scores = w.part_ml + round_up(slots * r.tile * 8);
-  w.parts = w.scores +
+  w.split = w.scores +
             (few && weights ? round_up(bh * capacity * r.tile * 4) : 0);
-  w.lse2 = w.parts + (few ? 0 : round_up(bh * r.blocks * 8));
+  w.lse2 = w.split + (few ? 0 : round_up(static_cast<size_t>(r.grid) * 16));
   w.total = w.lse2 +
             (!few && weights ? round_up(bh * r.blocks * r.tile * 4) : 0);
   return w;
@@ -183,7 +183,7 @@ attn_status_t append_impl(const attn_kv8_t* c, const void* K, const void* V,
   // Sq tokens that start anywhere in a block touch so many blocks at most.
   const long long units = (static_cast<long long>(Sq) + c->block - 2) / c->block + 1;
   p.units_per_seq = static_cast<int>(units);
-  if (static_cast<long long>(heads(*c)) * units > 0x7fffffffLL)
+  if (static_cast<long long>(heads(*c)) * units > 0x7fffffffLL / 2)
     return ATTN_ERR_INVALID_ARG;
   p.status = attn::device_status_word(dev);
   if (p.status == nullptr) return ATTN_ERR_CUDA;
@@ -273,7 +273,7 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
     p.scores = reinterpret_cast<float*>(ws + w.scores);
   if (weights != nullptr && !few)
     p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
-  p.parts = reinterpret_cast<int2*>(ws + w.parts);
+  p.split = reinterpret_cast<int4*>(ws + w.split);
   p.grid = rp.grid;
   p.timeout_ns = attn::wait_timeout_ns();
   p.status = attn::device_status_word(dev);

@@ -33,10 +33,11 @@ __global__ void __launch_bounds__(unit_threads<D, kBlock>())
   static_assert(kChunks * kThreads == kBlock * kPerRow, "whole chunks");
   __shared__ float red[kWarps];
 
+  start_after_previous();
   // Unit = (batch, head), block of that head, K or V.
-  const int kv = blockIdx.y;
-  const int bh = blockIdx.x / p.units_per_seq;
-  const int u = blockIdx.x - bh * p.units_per_seq;
+  const int kv = blockIdx.x & 1;
+  const int bh = (blockIdx.x >> 1) / p.units_per_seq;
+  const int u = (blockIdx.x >> 1) - bh * p.units_per_seq;
   const int b = bh / p.Hkv;
   const int len = clamp_len(p.lens[b], p.capacity, p.status);
   const int n_new =
@@ -141,18 +142,17 @@ __global__ void __launch_bounds__(unit_threads<D, kBlock>())
 }
 
 template <int D, int kBlock>
-cudaError_t launch(bool bf16, const AppendParams& p, dim3 grid,
+cudaError_t launch(bool bf16, const AppendParams& p, long long grid,
                    cudaStream_t stream) {
   constexpr int kThreads = unit_threads<D, kBlock>();
-  if (bf16)
-    kv8_append_kernel<D, kBlock, true><<<grid, kThreads, 0, stream>>>(p);
-  else
-    kv8_append_kernel<D, kBlock, false><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return bf16 ? launch_pdl(kv8_append_kernel<D, kBlock, true>, grid, kThreads,
+                           0, stream, p)
+              : launch_pdl(kv8_append_kernel<D, kBlock, false>, grid, kThreads,
+                           0, stream, p);
 }
 
 template <int D>
-cudaError_t launch_d(int block, bool bf16, const AppendParams& p, dim3 grid,
+cudaError_t launch_d(int block, bool bf16, const AppendParams& p, long long grid,
                      cudaStream_t stream) {
   switch (block) {
     case 16: return launch<D, 16>(bf16, p, grid, stream);
@@ -166,7 +166,7 @@ cudaError_t launch_d(int block, bool bf16, const AppendParams& p, dim3 grid,
 
 cudaError_t launch_append(int D, int block, bool bf16, const AppendParams& p,
                           int B, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(B) * p.Hkv * p.units_per_seq, 2, 1);
+  const long long grid = 2LL * B * p.Hkv * p.units_per_seq;
   return D == 64 ? launch_d<64>(block, bf16, p, grid, stream)
                  : launch_d<128>(block, bf16, p, grid, stream);
 }

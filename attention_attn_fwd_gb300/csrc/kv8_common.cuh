@@ -85,6 +85,35 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float* x) {
   x[3] = b.y;
 }
 
+// Programmatic dependent launches: every kernel of the 8-bit cache may be
+// scheduled before the one ahead of it on the stream has ended, so that its
+// launch overlaps that one's tail.  Each begins with start_after_previous():
+// it waits for the kernel ahead (whatever that is) to end and be visible,
+// and only then lets the next one be scheduled -- so a kernel that reads
+// memory before its own wait can rely on everything but the kernel directly
+// ahead, and every thread block waits, also one without work (else a kernel
+// of idle blocks could end before the one ahead of it).
+__device__ __forceinline__ void start_after_previous() {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch_pdl(Kernel kernel, long long grid, int threads, int smem,
+                       cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct AppendParams {
   uint8_t* code[2];       // K, V
   float* scale[2];
@@ -113,12 +142,12 @@ struct FwdParams {
   int causal;
   float scale_log2;       // scale * log2(e)
   // Workspace: partial rows and their (max, sum) of the parts of a split
-  // segment or unit; few rows: the scores of every key; many rows: where a
-  // unit's parts are, and the rows' LSEs in log2 units.
+  // segment or unit; few rows: the scores of every key; many rows: the unit
+  // that goes on behind each CTA, and the rows' LSEs in log2 units.
   float* part_o;          // [slots, rows, D]
   float2* part_ml;        // [slots, rows]
   float* scores;          // [B * Hkv, capacity, rows]
-  int2* parts;            // [B, row_blocks, Hkv]: first CTA, number of CTAs
+  int4* split;            // [grid]: b, h, unit, number of CTAs (0: none)
   float* lse2;            // [B * Hkv, row_blocks * 256]
   int grid;               // CTAs of the forward launch
   int warps;              // few rows: warps of each
@@ -148,23 +177,6 @@ __device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
 __device__ __forceinline__ int row_shift(float amax) {
   const int e = (__float_as_int(amax) >> 23) - 127;
   return max(-114, min(13 - e, 126));
-}
-
-// Launch that may be scheduled before the kernel ahead of it on the stream
-// has ended; the kernel waits for that itself (griddep_wait).
-template <class Kernel, class... Args>
-cudaError_t launch_pdl(Kernel kernel, long long grid, int threads,
-                       cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 struct EvictParams {

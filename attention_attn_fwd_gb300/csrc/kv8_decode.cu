@@ -323,8 +323,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, 1)
   float* sm_m = sm_o + C::kSums * kRows * kPitch;  // [kWarps][kRows]
   float* sm_l = sm_m + kWarps * kRows;             // [kWarps][kRows]
 
-  // The merge kernel may be scheduled early: its CTAs wait for this grid.
-  ptx::griddep_launch_dependents();
+  start_after_previous();
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g8 = lane / 4, c = lane % 4;
@@ -752,15 +751,17 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int bh = blockIdx.x / per_seg;
   const int unit = blockIdx.x - bh * per_seg;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  // (Lengths are read ahead of the wait: the kernel ahead is the forward.)
   const int len = seq_len(p, b), n_new = seq_new(p, b);
   const int n_rows = n_new * p.group;
   const int key0 = (unit - kRows) * kKeysPerPart;
-  if (unit < kRows ? unit >= n_rows : (n_rows <= 0 || key0 >= len)) return;
+  const bool idle =
+      unit < kRows ? unit >= n_rows : (n_rows <= 0 || key0 >= len);
 
   const int tiles = (len + kKeys - 1) / kKeys;
   long long c0 = 0;
   int n_slots = 0;
-  if (tiles > 0) {
+  if (tiles > 0 && !idle) {
     int first;
     const int total = list_tiles<kKeys>(p, b, lane, &first);
     const Cut cut = make_cut(p, total);
@@ -769,7 +770,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     n_slots = cut.owner(first + tiles - 1) - static_cast<int>(c0) + 1;
   }
   const float2* ml = p.part_ml + (c0 + bh) * kRows;
-  ptx::griddep_wait();  // the forward kernel's partials
+  start_after_previous();
+  if (idle) return;
 
   if (unit < kRows) {
     const int r = unit;
@@ -852,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ __align__(16) uint16_t sq[kWRows * kPitch];
   __shared__ float s_mult[kWRows], s_lse[kWRows];
   __shared__ int s_vis[kWRows];
-  ptx::griddep_wait();
+  start_after_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g8 = lane / 4, c = lane % 4;
   const int tiles = (p.capacity + 127) / 128;
@@ -976,16 +978,15 @@ cudaError_t launch_rows(FwdParams p, cudaStream_t stream) {
       kv8_decode_kernel<D, NT, kBF16>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
-  kv8_decode_kernel<D, NT, kBF16>
-      <<<p.grid, C::kThreads, C::kBytes, stream>>>(p);
-  err = cudaGetLastError();
+  err = launch_pdl(kv8_decode_kernel<D, NT, kBF16>, p.grid, C::kThreads,
+                   C::kBytes, stream, p);
   if (err != cudaSuccess) return err;
   const long long segs = static_cast<long long>(p.B) * p.Hkv;
   const int parts = p.scores == nullptr
                         ? 0
                         : (p.capacity + kKeysPerPart - 1) / kKeysPerPart;
   return launch_pdl(kv8_merge_kernel<D, NT, kBF16>, segs * (kRows + parts),
-                    kMergeThreads, stream, p, parts);
+                    kMergeThreads, 0, stream, p, parts);
 }
 
 template <int D, bool kBF16>
@@ -993,7 +994,7 @@ cudaError_t launch_weights_dt(const FwdParams& p, int lse2_rows,
                               cudaStream_t stream) {
   const long long tiles = (p.capacity + 127) / 128;
   return launch_pdl(kv8_weights_kernel<D, kBF16>,
-                    static_cast<long long>(p.B) * p.Hkv * tiles, kThreads,
+                    static_cast<long long>(p.B) * p.Hkv * tiles, kThreads, 0,
                     stream, p, lse2_rows);
 }
 

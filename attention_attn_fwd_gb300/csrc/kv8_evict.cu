@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kSelThreads)
   __shared__ int2 sm_warp[32];
   __shared__ uint32_t s_digit;
   __shared__ int s_left;
+  start_after_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int bh = blockIdx.x;
   const int b = bh / p.Hkv;
@@ -297,6 +298,7 @@ __device__ __forceinline__ void move_weights(const EvictParams& p, int bh,
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads)
     kv8_move_kernel(const EvictParams p) {
+  start_after_previous();
   const int rank = blockIdx.x % kCluster;
   const int unit = blockIdx.x / kCluster;
   const int part = unit % 3;  // K, V, weights
@@ -320,22 +322,24 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * 3 * kCluster, 1, 1);
   cfg.blockDim = dim3(kMoveThreads, 1, 1);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kv8_move_kernel<D>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream) {
-  kv8_select_kernel<<<static_cast<unsigned>(p.B) * p.Hkv, kSelThreads, 0,
-                      stream>>>(p);
-  const cudaError_t err = cudaGetLastError();
+  const cudaError_t err =
+      launch_pdl(kv8_select_kernel, static_cast<long long>(p.B) * p.Hkv,
+                 kSelThreads, 0, stream, p);
   if (err != cudaSuccess) return err;
   return D == 64 ? launch_move<64>(p, stream) : launch_move<128>(p, stream);
 }

@@ -60,11 +60,8 @@ struct Record {
   int slot;       // workspace slot of a part; -1: this CTA has all of the unit
   int n[2];       // key tiles each Q tile sees
   int full[2];    // tiles below this one are seen whole by each valid row
-  int unit;       // its index
-  int c0, parts;  // last part: first CTA of the unit, and how many; else 0
   float v_unit;   // largest V scale of the part's keys (by the converters)
 };
-static_assert(sizeof(Record) == 64, "record size");
 
 template <int D>
 struct Smem {
@@ -84,7 +81,7 @@ struct Smem {
   static constexpr int kNumBars = 2 * kRawSlots + 2 * kSlots + 2 * kUnits + 9;
   static constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM base, abort
   static constexpr int kRecords = kMisc + 8;
-  static constexpr int kBytes = kRecords + kUnits * 64;
+  static constexpr int kBytes = kRecords + kUnits * sizeof(Record);
   static_assert(kBytes + 1024 <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -226,13 +223,29 @@ __device__ __forceinline__ void fill_record(const FwdParams& p,
     rec->n[t] = max(0, min(hi, w.j1) - w.j0);
     rec->full[t] = row_end(p, w.len, w.n_new, r0) / kTN;
   }
-  rec->unit = (w.b * p.row_blocks + w.u) * p.Hkv + w.h;
-  rec->c0 = rec->parts = 0;
-  if (w.j1 == w.steps) {  // position of the unit's last step, then its first
-    const int last = walk.first(walk.cta + 1) - 1 - walk.left;
-    const int c0 = walk.owner(last - (w.steps - 1));
-    rec->c0 = c0;
-    rec->parts = walk.cta - c0 + 1;
+}
+
+// Rows of units without steps (empty sequences, or rows before the first
+// token) see nothing: the warp writes their O and LSE, each CTA its share of
+// the units.
+template <int D>
+__device__ __forceinline__ void write_unseen(const FwdParams& p, int lane) {
+  for (int i = blockIdx.x; i < p.B * p.row_blocks; i += gridDim.x) {
+    int len, n_new;
+    if (pair_steps(p, i, &len, &n_new) > 0) continue;
+    const int b = i / p.row_blocks, r0 = (i - b * p.row_blocks) * kUnitRows;
+    const int n = min(kUnitRows, n_new * p.group - r0);
+    for (int j = lane; j < n * p.Hkv; j += 32) {
+      const int h = j / n, r = r0 + j - h * n;
+      const long long row = q_row_index(p, b, h, r);
+      uint4* dst =
+          reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D);
+      for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr) p.lse[row] = -INFINITY;
+      if (p.lse2 != nullptr)
+        p.lse2[(static_cast<long long>(b) * p.Hkv + h) * p.row_blocks *
+                   kUnitRows + r] = -INFINITY;
+    }
   }
 }
 
@@ -277,7 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile Record* records = reinterpret_cast<Record*>(smem + L::kRecords);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  ptx::griddep_launch_dependents();  // the merge kernel waits for this grid
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       const uint32_t bar = s_base + L::kBars + 8 * i;
@@ -303,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  start_after_previous();
 
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase, int role) {
@@ -328,6 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ units of the share
       Walk walk;
       bool more = walk.take(p, static_cast<int>(blockIdx.x), lane);
+      // The unit that begins here and goes on in later CTAs, for the merge.
+      int4 split = make_int4(0, 0, 0, 0);
       for (int k = 0; ok; ++k) {
         if (k >= kUnits)
           ok = wait(bar_ufree + 8 * (k % kUnits), k / kUnits - 1, 1);
@@ -342,8 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (!more) break;
+        const Unit& w = walk.w;
+        if (w.j0 == 0 && w.j1 < w.steps) {
+          const int last = walk.first(walk.cta + 1) - w.j1 + w.steps - 1;
+          split = make_int4(w.b, w.h, w.u, walk.owner(last) - walk.cta + 1);
+        }
         more = walk.next(p);
       }
+      if (lane == 0) p.split[blockIdx.x] = split;
+    } else if (warp == 3) {
+      write_unseen<D>(p, lane);
     } else if (warp == 1) {
       // ---------------------------------------------------- raw tile loads
       int it = 0;
@@ -813,9 +836,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_ml[at] =
               make_float2(m_run == -INFINITY ? kNone : m_run, l_run);
       }
-      // The CTA of a unit's last part says where its parts are.
-      if (t == 0 && r == 0 && rec->parts > 0)
-        p.parts[rec->unit] = make_int2(rec->c0, rec->parts);
       ptx::tc_fence_before();
       release_unit(k);
       rec = next;
@@ -831,74 +851,77 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the parts of the units that more than one CTA worked on, and writes
-// the rows of units that see nothing: a CTA takes 32 rows of a unit, a warp
-// one row at a time.
+// Joins the parts of the units that more than one CTA worked on: for each
+// CTA's unit that went on behind it, a warp per row.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 32;
+constexpr int kMergeRows = kMergeThreads / 32;
+constexpr int kMergeParts = kUnitRows / kMergeRows;  // CTAs per unit
 
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kMergeThreads)
     kv8_prefill_merge_kernel(const FwdParams p) {
-  constexpr int kPer = kUnitRows / kMergeRows;  // CTAs per unit
-  constexpr int kCols = D / 4;                  // float4 columns
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int unit = blockIdx.x / kPer;
-  const int part = blockIdx.x - unit * kPer;
-  const int pair = unit / p.Hkv, h = unit - pair * p.Hkv;
-  Unit w;
-  w.b = pair / p.row_blocks;
-  w.u = pair - w.b * p.row_blocks;
-  w.h = h;
-  w.steps = pair_steps(p, pair, &w.len, &w.n_new);
-  const int row0 = w.u * kUnitRows + part * kMergeRows;
-  const int n_rows = min(kMergeRows, w.n_new * p.group - row0);
-  if (n_rows <= 0) return;
-  ptx::griddep_wait();
-  int2 parts = make_int2(0, 0);
-  if (w.steps > 0) parts = p.parts[unit];
-  if (parts.y == 1) return;  // the CTA of the unit has finished it
+  constexpr int kCols = D / 4;  // float4 columns
+  const int lane = threadIdx.x % 32;
+  const int cta = blockIdx.x / kMergeParts;
+  const int i = (blockIdx.x - cta * kMergeParts) * kMergeRows +
+                threadIdx.x / 32;  // row of the unit
+  start_after_previous();
+  const int4 split = p.split[cta];
+  const int b = split.x, h = split.y, parts = split.w;
+  if (parts == 0) return;
+  const int r = split.z * kUnitRows + i;
+  if (r >= seq_new(p, b) * p.group) return;
+  // Part s lies in slot 2 cta + 1 (s = 0) or 2 (cta + s).
+  const long long at0 = (2LL * cta + 1) * kUnitRows + i;
+  const long long at = 2LL * cta * kUnitRows + i;
   const int col = lane % kCols;
-  for (int i = warp; i < n_rows; i += kMergeThreads / 32) {
-    float mx = kNone, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto slot_row = [&](int s) {
-      const int slot = s == 0 ? 2 * parts.x + 1 : 2 * (parts.x + s);
-      return static_cast<long long>(slot) * kUnitRows + part * kMergeRows + i;
-    };
-    for (int s = 0; s < parts.y; ++s)
-      mx = fmaxf(mx, p.part_ml[slot_row(s)].x);
+  float mx = kNone;
+  for (int s = lane; s < parts; s += 32)
+    mx = fmaxf(mx, p.part_ml[s == 0 ? at0 : at + 2LL * s * kUnitRows].x);
+#pragma unroll
+  for (int k = 16; k > 0; k /= 2)
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    // Lane s: factor and sum of part s0 + s.  (A part whose sum is 0 sees
+    // nothing and has no O.)
+    float2 ml = make_float2(kNone, 0.f);
+    if (s0 + lane < parts)
+      ml = p.part_ml[s0 + lane == 0
+                         ? at0
+                         : at + 2LL * (s0 + lane) * kUnitRows];
+    const float f_all = ptx::ex2(ml.x - mx);
+    const int n = min(32, parts - s0);
 #pragma unroll 4
-    for (int s = 0; s < parts.y; ++s) {
-      const long long at = slot_row(s);
-      const float2 ml = p.part_ml[at];
-      if (ml.y == 0.f) continue;  // sees nothing of the part: not written
-      const float f = ptx::ex2(ml.x - mx);
-      const float4 y =
-          reinterpret_cast<const float4*>(p.part_o)[at * kCols + col];
-      sum += ml.y * f;
+    for (int s = 0; s < n; ++s) {
+      const float l = __shfl_sync(0xffffffffu, ml.y, s);
+      const float f = __shfl_sync(0xffffffffu, f_all, s);
+      if (l == 0.f) continue;
+      const float4 y = reinterpret_cast<const float4*>(
+          p.part_o)[(s0 + s == 0 ? at0 : at + 2LL * (s0 + s) * kUnitRows) *
+                        kCols + col];
+      sum += l * f;
       acc.x += y.x * f;
       acc.y += y.y * f;
       acc.z += y.z * f;
       acc.w += y.w * f;
     }
-    const long long row = q_row_index(p, w.b, h, row0 + i);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (lane < kCols) {
-      uint2 out;
-      out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
-      out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
-      reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[col] =
-          out;
-    }
-    if (lane == 0) {
-      const float lse2 =
-          sum == 0.f ? -INFINITY : mx + log2f(sum) - kShift;
-      if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
-      if (p.lse2 != nullptr)
-        p.lse2[(static_cast<long long>(w.b) * p.Hkv + h) * p.row_blocks *
-                   kUnitRows + row0 + i] = lse2;
-    }
+  }
+  const long long row = q_row_index(p, b, h, r);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (lane < kCols) {
+    uint2 out;
+    out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
+    out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[col] = out;
+  }
+  if (lane == 0) {
+    const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum) - kShift;
+    if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
+    if (p.lse2 != nullptr)
+      p.lse2[(static_cast<long long>(b) * p.Hkv + h) * p.row_blocks *
+                 kUnitRows + r] = lse2;
   }
 }
 
@@ -909,13 +932,12 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream) {
       kv8_prefill_kernel<D, kBF16>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (err != cudaSuccess) return err;
-  kv8_prefill_kernel<D, kBF16><<<p.grid, kThreads, kBytes, stream>>>(p);
-  err = cudaGetLastError();
+  err = launch_pdl(kv8_prefill_kernel<D, kBF16>, p.grid, kThreads, kBytes,
+                   stream, p);
   if (err != cudaSuccess) return err;
   return launch_pdl(kv8_prefill_merge_kernel<D, kBF16>,
-                    static_cast<long long>(p.B) * p.row_blocks * p.Hkv *
-                        (kUnitRows / kMergeRows),
-                    kMergeThreads, stream, p);
+                    static_cast<long long>(p.grid) * kMergeParts,
+                    kMergeThreads, 0, stream, p);
 }
 
 }  // namespace
