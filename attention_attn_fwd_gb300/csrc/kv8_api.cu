@@ -99,18 +99,25 @@ struct RowPlan {
 
 constexpr int kFewRows = 16;
 
-RowPlan plan_rows(int Hq, int Hkv, int Sq, int sms) {
+RowPlan plan_rows(int Hq, int Hkv, int Sq, int D, int sms) {
   RowPlan r;
   r.rows = static_cast<long long>(Hq / Hkv) * Sq;
   r.tile = r.rows <= 8 ? 8 : r.rows <= kFewRows ? kFewRows : 256;
   r.blocks = r.tile == 256 ? (r.rows + 255) / 256 : 1;
-  r.grid = sms;
+  r.grid = sms * (r.tile <= kFewRows ? attn::kv8::decode_ctas(D, r.tile) : 1);
   return r;
 }
 
 struct Workspace {
   size_t part_o, part_ml, scores, split, lse2, total;
 };
+
+// log2 of the scores kept per key: the rows, padded to a power of two.
+int score_shift(const RowPlan& r) {
+  int s = 0;
+  while ((1 << s) < r.rows) ++s;
+  return s;
+}
 
 Workspace workspace_layout(int B, int Hkv, int capacity, int D,
                            const RowPlan& r, bool weights) {
@@ -122,7 +129,8 @@ Workspace workspace_layout(int B, int Hkv, int capacity, int D,
   w.part_ml = w.part_o + round_up(slots * r.tile * D * 4);
   w.scores = w.part_ml + round_up(slots * r.tile * 8);
   w.split = w.scores +
-            (few && weights ? round_up(bh * capacity * r.tile * 4) : 0);
+            (few && weights ? round_up(bh * capacity * 4 << score_shift(r))
+                              : 0);
   w.lse2 = w.split + (few ? 0 : round_up(static_cast<size_t>(r.grid) * 16));
   w.total = w.lse2 +
             (!few && weights ? round_up(bh * r.blocks * r.tile * 4) : 0);
@@ -208,7 +216,7 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
   const int sms = attn::device_sms(dev);
   if (sms <= 0) return ATTN_ERR_CUDA;
-  const RowPlan rp = plan_rows(Hq, c->Hkv, Sq, sms);
+  const RowPlan rp = plan_rows(Hq, c->Hkv, Sq, c->D, sms);
   // Rows, CTAs of every launch, and steps (unit, key tile) fit 32 bits.
   const long long segs = static_cast<long long>(heads(*c)) * rp.blocks;
   const long long tiles = (c->capacity - 1LL) / kKeyTile + 1;
@@ -269,8 +277,10 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   const bool few = rp.tile <= kFewRows;
-  if (weights != nullptr && few)
+  if (weights != nullptr && few) {
     p.scores = reinterpret_cast<float*>(ws + w.scores);
+    p.score_shift = score_shift(rp);
+  }
   if (weights != nullptr && !few)
     p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
   p.split = reinterpret_cast<int4*>(ws + w.split);
@@ -408,7 +418,7 @@ size_t attn_kv8_workspace_bytes(int B, int Hq, int Hkv, int Sq, int capacity,
       capacity <= 0 || (D != 64 && D != 128))
     return 0;
   if (B == 0 || Sq == 0) return 0;
-  const RowPlan rp = plan_rows(Hq, Hkv, Sq, current_sms());
+  const RowPlan rp = plan_rows(Hq, Hkv, Sq, D, current_sms());
   return workspace_layout(B, Hkv, capacity, D, rp, weights != 0).total;
 }
 

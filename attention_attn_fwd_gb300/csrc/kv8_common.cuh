@@ -114,6 +114,13 @@ cudaError_t launch_pdl(Kernel kernel, long long grid, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Few-row forward: warps of a CTA, and CTAs an SM holds at 8 and 16 query
+// rows each.
+constexpr int kDecodeWarps = 4;
+__host__ __device__ constexpr int decode_ctas(int D, int rows) {
+  return rows <= 8 ? (D == 128 ? 3 : 4) : 2;
+}
+
 struct AppendParams {
   uint8_t* code[2];       // K, V
   float* scale[2];
@@ -146,11 +153,11 @@ struct FwdParams {
   // that goes on behind each CTA, and the rows' LSEs in log2 units.
   float* part_o;          // [slots, rows, D]
   float2* part_ml;        // [slots, rows]
-  float* scores;          // [B * Hkv, capacity, rows]
+  float* scores;          // [B * Hkv, capacity, 1 << score_shift]
   int4* split;            // [grid]: b, h, unit, number of CTAs (0: none)
   float* lse2;            // [B * Hkv, row_blocks * 256]
   int grid;               // CTAs of the forward launch
-  int warps;              // few rows: warps of each
+  int score_shift;        // few rows: log2 of the scores' rows per key
   unsigned long long timeout_ns;  // limit of a pipeline wait
   unsigned int* status;
 };

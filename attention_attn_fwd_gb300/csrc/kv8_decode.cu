@@ -134,7 +134,7 @@ struct Cut {
 // At most one tile per warp is the finest cut.
 __device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
   Cut c;
-  c.n = max(1, min(p.grid, (total + p.warps - 1) / p.warps));
+  c.n = max(1, min(p.grid, (total + kDecodeWarps - 1) / kDecodeWarps));
   c.q = total / c.n;
   c.rest = total - c.q * c.n;
   return c;
@@ -288,29 +288,28 @@ struct Loader {
 };
 
 // NT: 8-row groups of query rows a CTA holds (8 or 16 rows of a K/V head).
-// 8 rows leave registers for 16 warps an SM, 16 rows for 8.  At the end of a
-// segment the upper half of the warps hands its O to the lower half, which
-// sums in rows.
+// CTAs of four warps, as many as registers and shared memory allow: one CTA's
+// start, end of a segment or tail runs under the others' loads (four CTAs an
+// SM against one of 16 warps: 29.0 -> 27 us on 8 x 4096 tokens, 57 -> 32 on
+// 256 segments of about 1000).
 template <int D, int NT>
 struct Config {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = NT == 1 ? 16 : 8;
-  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kThreads = 32 * kDecodeWarps;
+  static constexpr int kCtas = decode_ctas(D, kRows);
+  static constexpr int kStages = NT == 1 ? (D == 128 ? 3 : 2) : 4;
   static constexpr int kPitch = D + 4;  // floats: rows start 4 banks apart
-  static constexpr int kStages = NT == 1 ? 3 : 5;
-  static constexpr int kRingBytes = kWarps * kStages * 4096;
-  static constexpr int kSums = kWarps / 2;  // warps that sum
+  static constexpr int kRingBytes = kDecodeWarps * kStages * 4096;
   static constexpr int kBytes =
-      kRingBytes + (kSums * kRows * kPitch + 2 * kWarps * kRows) * 4;
-  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+      kRingBytes + kDecodeWarps * kRows * (kPitch + 2) * 4;
+  static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 template <int D, int NT, bool kBF16>
-__global__ void __launch_bounds__(Config<D, NT>::kThreads, 1)
+__global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
     kv8_decode_kernel(const FwdParams p) {
   using C = Config<D, NT>;
-  constexpr int kWarps = C::kWarps;
-  constexpr int kThreads = C::kThreads;
+  constexpr int kWarps = kDecodeWarps;
   constexpr int kRows = C::kRows;
   constexpr int kPitch = C::kPitch;
   constexpr int kStages = C::kStages;
@@ -320,8 +319,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, 1)
   constexpr int kMT = D / 16;       // m-tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   float* sm_o = reinterpret_cast<float*>(smem + C::kRingBytes);
-  float* sm_m = sm_o + C::kSums * kRows * kPitch;  // [kWarps][kRows]
-  float* sm_l = sm_m + kWarps * kRows;             // [kWarps][kRows]
+  float* sm_m = sm_o + kWarps * kRows * kPitch;  // [kWarps][kRows]
+  float* sm_l = sm_m + kWarps * kRows;
 
   start_after_previous();
 
@@ -486,18 +485,22 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, 1)
                 s[nt][e] = -INFINITY;
         }
         if (p.scores != nullptr) {
-          float* sc = p.scores +
-                      (static_cast<long long>(bh) * p.capacity + key0 + g8) *
-                          kRows + 2 * c;
+          // [key][row], rows padded to a power of two.
+          float* sc = p.scores + ((static_cast<long long>(bh) * p.capacity +
+                                   key0 + g8) << p.score_shift);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (key0 + g8 < len)
-              *reinterpret_cast<float2*>(sc + 8 * nt) =
-                  make_float2(s[nt][0], s[nt][1]);
-            if (key0 + g8 + 8 < len)
-              *reinterpret_cast<float2*>(sc + 8 * kRows + 8 * nt) =
-                  make_float2(s[nt][2], s[nt][3]);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 8 * nt + 2 * c;
+              if (key0 + g8 + 8 * i >= len || r >> p.score_shift) continue;
+              float* at = sc + (8 * i << p.score_shift) + r;
+              if (p.score_shift == 0)
+                *at = s[nt][2 * i];
+              else
+                *reinterpret_cast<float2*>(at) =
+                    make_float2(s[nt][2 * i], s[nt][2 * i + 1]);
+            }
         }
         bool grow = vs > unit;
 #pragma unroll
@@ -623,59 +626,21 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, 1)
         const float f = ptx::ex2(m[nt][e] - mx);
         const float fo = f * unit * (1.f / kPScale);
         if (g8 == 0) sm_l[warp * kRows + r] = l[nt][e] * f;
+        float* dst = sm_o + (warp * kRows + r) * kPitch + (D / 8) * g8;
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-          o[nt][i][e] *= fo;
-          o[nt][i][e + 2] *= fo;
-        }
+        for (int i = 0; i < kMT; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) =
+              make_float4(o[nt][i][e] * fo, o[nt][i][e + 2] * fo,
+                          o[nt][i + 1][e] * fo, o[nt][i + 1][e + 2] * fo);
       }
-    // Fragment order between the halves: float4 i of lane j at 32 i + j.
-    float4* half = reinterpret_cast<float4*>(sm_o) +
-                   (warp % C::kSums) * (NT * kMT * 32) + lane;
-    static_assert(NT * kMT * 32 * 16 <= kRows * kPitch * 4, "hand-over fits");
-    if (warp >= C::kSums) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
-          half[(nt * kMT + i) * 32] = make_float4(o[nt][i][0], o[nt][i][1],
-                                                  o[nt][i][2], o[nt][i][3]);
-    }
-    __syncthreads();
-    if (warp < C::kSums) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-          const float4 x = half[(nt * kMT + i) * 32];
-          o[nt][i][0] += x.x;
-          o[nt][i][1] += x.y;
-          o[nt][i][2] += x.z;
-          o[nt][i][3] += x.w;
-        }
-    }
-    __syncthreads();
-    if (warp < C::kSums) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * nt + 2 * c + e;
-          float* dst = sm_o + (warp * kRows + r) * kPitch + (D / 8) * g8;
-#pragma unroll
-          for (int i = 0; i < kMT; i += 2)
-            *reinterpret_cast<float4*>(dst + 2 * i) =
-                make_float4(o[nt][i][e], o[nt][i][e + 2], o[nt][i + 1][e],
-                            o[nt][i + 1][e + 2]);
-        }
-    }
     __syncthreads();
     const long long slot = static_cast<long long>(cta) + bh;
-    for (int i = threadIdx.x; i < n_rows * (D / 4); i += kThreads) {
+#pragma unroll 2
+    for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads) {
       const int r = i / (D / 4), d4 = i % (D / 4);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < C::kSums; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float4 x = *reinterpret_cast<const float4*>(
             sm_o + (w * kRows + r) * kPitch + 4 * d4);
         acc.x += x.x;
@@ -702,61 +667,91 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// One CTA per query row of a segment joins the row's partials into O and LSE,
-// its threads over the columns and, in groups, over the partials (a
-// single long sequence has one per SM).  With accumulated weights further
-// CTAs, one per 512 keys of a segment, add p = 2^(score - LSE) over the rows,
-// read back from the scores the forward kernel left (4 bytes per key and row;
-// recomputing them would read the keys' codes again).
+// CTAs 0 .. row_ctas - 1 of a segment join the rows' partials into O and LSE:
+// a warp per row where a segment has few partials, else all eight warps (a
+// single long sequence has 150 partials per head).  With accumulated weights
+// further CTAs, one per 512 keys of a segment, add p = 2^(score - LSE) over
+// the rows, read back from the scores the forward kernel left (4 bytes per
+// key and row; recomputing them would read the keys' codes again).
 constexpr int kMergeThreads = 256;
 constexpr int kKeysPerPart = 512;
 
+// Up to 256 partials' (max, sum) of a row, eight per lane and all loads in
+// flight at once: lane l holds partials l, l + 32, ...; f becomes their
+// factors 2^(max_s - mx).  mx and the lanes' shares of sum carry on from the
+// partials before; the return value is what those have to be multiplied by.
+// (A NaN among the scores has made a sum NaN, also where no other score set a
+// maximum.)
+constexpr int kHeld = 8;
+template <int kRows>
+__device__ __forceinline__ float take_partials(const float2* ml, int r, int s0,
+                                               int n_slots, int lane,
+                                               float* f, float& mx,
+                                               float& sum) {
+  float2 x[kHeld];
+  float m = mx;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int s = s0 + 32 * i + lane;
+    x[i] = make_float2(kNone, 0.f);
+    if (s < n_slots) x[i] = ml[s * kRows + r];
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) m = fmaxf(m, x[i].x);
+#pragma unroll
+  for (int i = 16; i > 0; i /= 2)
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+  const float before = ptx::ex2(mx - m);
+  sum *= before;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    f[i] = ptx::ex2(x[i].x - m);
+    sum += x[i].y * f[i];
+  }
+  mx = m;
+  return before;
+}
+
 // Maximum and sum of row r over a segment's partials, by one warp (every lane
-// gets the result); the LSE in log2 units, -inf for a row that sees nothing.
-// (A NaN among the scores has made the sum NaN, also where no other score set
-// a maximum.)
+// gets the result).
 template <int kRows>
 __device__ __forceinline__ float2 row_total(const float2* ml, int r,
                                             int n_slots, int lane) {
-  float mx = kNone;
-  for (int s = lane; s < n_slots; s += 32) mx = fmaxf(mx, ml[s * kRows + r].x);
+  float mx = kNone, sum = 0.f, f[kHeld];
+  for (int s0 = 0; s0 < n_slots; s0 += 32 * kHeld)
+    take_partials<kRows>(ml, r, s0, n_slots, lane, f, mx, sum);
 #pragma unroll
-  for (int i = 16; i > 0; i /= 2)
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-  float sum = 0.f;
-  for (int s = lane; s < n_slots; s += 32) {
-    const float2 x = ml[s * kRows + r];
-    sum += x.y * ptx::ex2(x.x - mx);
-  }
-#pragma unroll
-  for (int i = 16; i > 0; i /= 2)
-    sum += __shfl_xor_sync(0xffffffffu, sum, i);
+  for (int i = 16; i > 0; i /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, i);
   return make_float2(mx, sum);
 }
+// The LSE in log2 units, -inf for a row that sees nothing.
 __device__ __forceinline__ float total_lse2(float2 t) {
   return t.y == 0.f ? -INFINITY : t.x + log2f(t.y);
 }
 
 template <int D, int NT, bool kBF16>
-__global__ void __launch_bounds__(kMergeThreads)
-    kv8_merge_kernel(const FwdParams p, int parts) {
+__global__ void __launch_bounds__(kMergeThreads, 4)
+    kv8_merge_kernel(const FwdParams p, int row_ctas, int parts,
+                     int row_warps) {
   constexpr int kRows = 8 * NT;
   constexpr int kKeys = tile_keys<D>();
-  constexpr int kCols = D / 4;                      // float4 columns
-  constexpr int kGroups = kMergeThreads / kCols;    // partials at a time
+  constexpr int kCols = D / 4;               // float4 columns
+  constexpr int kGroups = 32 / kCols;        // partials a warp reads at a time
   __shared__ float sm_lse[kRows];
-  __shared__ float4 sm_acc[kGroups][kCols];
+  __shared__ float4 sm_acc[kMergeThreads / 32][kCols];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int per_seg = kRows + parts;  // CTAs of a segment
+  const int per_seg = row_ctas + parts;  // CTAs of a segment
   const int bh = blockIdx.x / per_seg;
   const int unit = blockIdx.x - bh * per_seg;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   // (Lengths are read ahead of the wait: the kernel ahead is the forward.)
   const int len = seq_len(p, b), n_new = seq_new(p, b);
   const int n_rows = n_new * p.group;
-  const int key0 = (unit - kRows) * kKeysPerPart;
-  const bool idle =
-      unit < kRows ? unit >= n_rows : (n_rows <= 0 || key0 >= len);
+  const int rows_per_cta = kMergeThreads / 32 / row_warps;
+  const int r = unit * rows_per_cta + warp / row_warps;
+  const int key0 = (unit - row_ctas) * kKeysPerPart;
+  const bool idle = unit < row_ctas ? unit * rows_per_cta >= n_rows
+                                    : (n_rows <= 0 || key0 >= len);
 
   const int tiles = (len + kKeys - 1) / kKeys;
   long long c0 = 0;
@@ -770,71 +765,135 @@ __global__ void __launch_bounds__(kMergeThreads)
     n_slots = cut.owner(first + tiles - 1) - static_cast<int>(c0) + 1;
   }
   const float2* ml = p.part_ml + (c0 + bh) * kRows;
+  // Accumulated weights of this CTA's keys (the forward does not touch them).
+  constexpr int kKeysPerThread = kKeysPerPart / kMergeThreads;
+  const long long key_at = static_cast<long long>(bh) * p.capacity;
+  float w[kKeysPerThread];
+#pragma unroll
+  for (int i = 0; i < kKeysPerThread; ++i) {
+    const int key = key0 + threadIdx.x + i * kMergeThreads;
+    w[i] = !idle && unit >= row_ctas && key < len ? p.weights[key_at + key]
+                                                  : 0.f;
+  }
   start_after_previous();
   if (idle) return;
 
-  if (unit < kRows) {
-    const int r = unit;
-    const int g = threadIdx.x / kCols, d4 = threadIdx.x % kCols;
-    const float4* po = reinterpret_cast<const float4*>(p.part_o) +
-                       ((c0 + bh) * kRows + r) * kCols + d4;
-    const float2 t = row_total<kRows>(ml, r, n_slots, lane);
+  if (unit < row_ctas) {
+    const bool live = r < n_rows;
+    const int d4 = lane % kCols;
+    // This lane's partials: sub, sub + step, ...
+    const int sub = (warp % row_warps) * kGroups + lane / kCols;
+    const int step = row_warps * kGroups;
+    float2 t = make_float2(kNone, 0.f);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = g; s < n_slots; s += kGroups) {
-      const float f = ptx::ex2(ml[s * kRows + r].x - t.x);
-      const float4 y = po[static_cast<long long>(s) * kRows * kCols];
-      acc.x += y.x * f;
-      acc.y += y.y * f;
-      acc.z += y.z * f;
-      acc.w += y.w * f;
-    }
-    sm_acc[g][d4] = acc;
-    __syncthreads();
-    if (g > 0) return;
+    if (live) {
+      const float4* po = reinterpret_cast<const float4*>(p.part_o) +
+                         ((c0 + bh) * kRows + r) * kCols + d4;
+      // The first partial's O is on its way while its factor is computed.
+      float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (sub < n_slots) y0 = po[static_cast<long long>(sub) * kRows * kCols];
+      for (int s0 = 0; s0 < n_slots; s0 += 32 * kHeld) {
+        float f[kHeld];
+        const float before = take_partials<kRows>(ml, r, s0, n_slots, lane, f,
+                                                  t.x, t.y);
+        acc.x *= before;
+        acc.y *= before;
+        acc.z *= before;
+        acc.w *= before;
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) {
-      const float4 y = sm_acc[i][d4];
-      acc.x += y.x;
-      acc.y += y.y;
-      acc.z += y.z;
-      acc.w += y.w;
+        for (int i = 0; i < kHeld; ++i) {
+          if (s0 + 32 * i >= n_slots) break;
+#pragma unroll 4
+          for (int k = sub; k < 32; k += step) {
+            const float fk = __shfl_sync(0xffffffffu, f[i], k);
+            const int s = s0 + 32 * i + k;
+            if (s < n_slots) {
+              const float4 y =
+                  s == sub ? y0 : po[static_cast<long long>(s) * kRows * kCols];
+              acc.x += y.x * fk;
+              acc.y += y.y * fk;
+              acc.z += y.z * fk;
+              acc.w += y.w * fk;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i /= 2)
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, i);
+      if constexpr (kGroups == 2) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+      }
     }
+    if (row_warps > 1) {
+      if (lane < kCols) sm_acc[warp][d4] = acc;
+      __syncthreads();
+      if (warp % row_warps != 0 || !live) return;
+      for (int i = 1; i < row_warps; ++i) {
+        const float4 y = sm_acc[warp + i][d4];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+    }
+    if (!live) return;
     const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
     const int tok = r / p.group, hd = r % p.group;
     const long long row =
         (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
-    uint2 out;
-    out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
-    out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[d4] = out;
-    if (d4 == 0 && p.lse != nullptr)
+    if (lane < kCols) {
+      uint2 out;
+      out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
+      out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[d4] =
+          out;
+    }
+    if (lane == 0 && p.lse != nullptr)
       p.lse[row] = total_lse2(t) * 0.69314718055994531f;
     return;
   }
-  for (int r = warp; r < n_rows; r += kMergeThreads / 32) {
-    const float lse2 = total_lse2(row_total<kRows>(ml, r, n_slots, lane));
-    if (lane == 0) sm_lse[r] = lse2;
+  // Scores and LSEs are fetched side by side.
+  float4 x[kKeysPerThread][kRows / 4];
+#pragma unroll
+  for (int i = 0; i < kKeysPerThread; ++i) {
+    const int key = key0 + threadIdx.x + i * kMergeThreads;
+    const float* at = p.scores + ((key_at + key) << p.score_shift);
+#pragma unroll
+    for (int k = 0; k < kRows / 4; ++k) {
+      x[i][k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (key >= len || 4 * k >= n_rows) continue;
+      if (p.score_shift >= 2) {
+        x[i][k] = *reinterpret_cast<const float4*>(at + 4 * k);
+      } else {
+        x[i][k].x = at[0];
+        if (n_rows > 1) x[i][k].y = at[1];
+      }
+    }
+  }
+  if (threadIdx.x < kRows) sm_lse[threadIdx.x] = 0.f;
+  __syncthreads();
+  for (int i = warp; i < n_rows; i += kMergeThreads / 32) {
+    const float lse2 = total_lse2(row_total<kRows>(ml, i, n_slots, lane));
+    if (lane == 0) sm_lse[i] = lse2;
   }
   __syncthreads();
-  const int k_end = min(len, key0 + kKeysPerPart);
-#pragma unroll 2
-  for (int key = key0 + threadIdx.x; key < k_end; key += kMergeThreads) {
-    const long long at = static_cast<long long>(bh) * p.capacity + key;
-    float x[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows / 4; ++i) {
-      const float4 y = reinterpret_cast<const float4*>(p.scores + at * kRows)[i];
-      x[4 * i] = y.x;
-      x[4 * i + 1] = y.y;
-      x[4 * i + 2] = y.z;
-      x[4 * i + 3] = y.w;
+  for (int i = 0; i < kKeysPerThread; ++i) {
+    const int key = key0 + threadIdx.x + i * kMergeThreads;
+    float add = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRows / 4; ++k) {
+      const float v[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)  // hidden scores and padding rows: -inf
+        if (4 * k + e < n_rows && v[e] != -INFINITY)
+          add += ptx::ex2(v[e] - sm_lse[4 * k + e]);
     }
-    float w = 0.f;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (r < n_rows && x[r] != -INFINITY) w += ptx::ex2(x[r] - sm_lse[r]);
-    if (w != 0.f) p.weights[at] += w;
+    if (add != 0.f) p.weights[key_at + key] = w[i] + add;
   }
 }
 
@@ -970,10 +1029,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int D, int NT, bool kBF16>
-cudaError_t launch_rows(FwdParams p, cudaStream_t stream) {
-  constexpr int kRows = 8 * NT;
+cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
   using C = Config<D, NT>;
-  p.warps = C::kWarps;
   cudaError_t err = cudaFuncSetAttribute(
       kv8_decode_kernel<D, NT, kBF16>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
@@ -985,8 +1042,12 @@ cudaError_t launch_rows(FwdParams p, cudaStream_t stream) {
   const int parts = p.scores == nullptr
                         ? 0
                         : (p.capacity + kKeysPerPart - 1) / kKeysPerPart;
-  return launch_pdl(kv8_merge_kernel<D, NT, kBF16>, segs * (kRows + parts),
-                    kMergeThreads, 0, stream, p, parts);
+  // Partials of a segment if all are equally long.
+  const int row_warps = segs * 16 <= p.grid ? kMergeThreads / 32 : 1;
+  const int rows_per_cta = kMergeThreads / 32 / row_warps;
+  const int row_ctas = (p.group * p.Sq + rows_per_cta - 1) / rows_per_cta;
+  return launch_pdl(kv8_merge_kernel<D, NT, kBF16>, segs * (row_ctas + parts),
+                    kMergeThreads, 0, stream, p, row_ctas, parts, row_warps);
 }
 
 template <int D, bool kBF16>
