@@ -21,7 +21,7 @@ SOURCES = ["attn_api.cu", "attn_fwd_d64.cu", "attn_fwd_d128.cu",
            "attn_fwd_d128_fp8.cu", "attn_fwd_d128_fp8_packed.cu",
            "attn_noalloc.cu", "attn_bwd.cu", "attn_merge.cu",
            "kv8_api.cu", "kv8_append.cu", "kv8_decode.cu",
-           "kv8_prefill.cu", "kv8_evict.cu"]
+           "kv8_prefill.cu", "kv8_weights.cu", "kv8_evict.cu"]
 HEADERS = ["attn_fwd_kernel.cuh", "attn_fwd_launch.cuh", "attn_sync.cuh",
            "fast_div.h",
            "attn_bwd_kernel.cuh", "attn_merge_kernel.cuh",

@@ -186,6 +186,17 @@ __device__ __forceinline__ int row_shift(float amax) {
   return max(-114, min(13 - e, 126));
 }
 
+// C (16 x 8, fp32) += A (16 x 16) B (16 x 8) in fp16.
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1,
+                                        uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 struct EvictParams {
   const uint8_t* src_code[2];
   const float* src_scale[2];

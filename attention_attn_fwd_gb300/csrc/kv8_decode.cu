@@ -48,16 +48,6 @@ __host__ __device__ constexpr int tile_keys() {
   return 2048 / D;
 }
 
-__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1,
-                                        uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;"
@@ -897,137 +887,6 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
   }
 }
 
-// ---------------------------------------------------------------- weights
-// Accumulated weights of many query rows: the scores of a 128-key tile are
-// computed again, S^T = K Q^T as above, with the keys' fragments kept in
-// registers and the query rows passing through shared memory 64 at a time;
-// p = 2^(score - LSE) summed over the rows.  Every key has one owner, so the
-// sums have one order.
-constexpr int kWRows = 64;
-constexpr int kThreads = 256;
-
-template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads, 2)
-    kv8_weights_kernel(const FwdParams p, int lse2_rows) {
-  constexpr int kPitch = D + 8;  // halves: rows 16 bytes apart in the banks
-  __shared__ __align__(16) uint16_t sq[kWRows * kPitch];
-  __shared__ float s_mult[kWRows], s_lse[kWRows];
-  __shared__ int s_vis[kWRows];
-  start_after_previous();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g8 = lane / 4, c = lane % 4;
-  const int tiles = (p.capacity + 127) / 128;
-  const int bh = blockIdx.x / tiles;
-  const int tile0 = (blockIdx.x - bh * tiles) * 128;
-  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-  const int len = seq_len(p, b), n_new = seq_new(p, b);
-  if (tile0 >= len) return;
-  const int rows = n_new * p.group;
-  // Rows before r_first see nothing of this tile.
-  int r_first = 0;
-  if (p.causal) r_first = max(0, tile0 - (len - n_new)) * p.group;
-  const int key0 = tile0 + warp * 16;
-
-  uint32_t a[D / 16][4];
-  {
-    const uint8_t* k = p.k + static_cast<long long>(bh) * p.capacity * D;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf) {
-        const int key = key0 + g8 + 8 * i;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (key < len)
-          x = __ldg(reinterpret_cast<const uint4*>(
-              k + static_cast<long long>(key) * D + 64 * hf + 16 * c));
-        e4m3x4_to_half2(x.x, a[4 * hf][i], a[4 * hf][2 + i]);
-        e4m3x4_to_half2(x.y, a[4 * hf + 1][i], a[4 * hf + 1][2 + i]);
-        e4m3x4_to_half2(x.z, a[4 * hf + 2][i], a[4 * hf + 2][2 + i]);
-        e4m3x4_to_half2(x.w, a[4 * hf + 3][i], a[4 * hf + 3][2 + i]);
-      }
-  }
-  float ks = 0.f;
-  if (key0 < len)
-    ks = __ldg(p.k_scale + static_cast<long long>(bh) * p.nblk +
-               (key0 >> p.block_shift));
-  float sum[2] = {0.f, 0.f};
-  for (int r0 = r_first; r0 < rows; r0 += kWRows) {
-    __syncthreads();
-    constexpr int kPer = D / 8;  // threads per row
-    for (int i = threadIdx.x; i < kWRows * kPer; i += kThreads) {
-      const int r = i / kPer, ch = i % kPer;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      const bool ok = r0 + r < rows;
-      if (ok) {
-        const int tok = (r0 + r) / p.group, hd = (r0 + r) % p.group;
-        w = __ldg(reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) +
-            ((static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq +
-             tok) * D + ch * 8));
-      }
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-      float2 f[4];
-      float amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[e] = unpack2<kBF16>(in[e]);
-        amax = fmaxf(amax, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
-      }
-#pragma unroll
-      for (int s = kPer / 2; s > 0; s /= 2)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-      const int up = row_shift(amax);
-      const float f_up = exp2_int(up);
-      uint32_t out[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        out[e] = ptx::pack2<false>(f[e].x * f_up, f[e].y * f_up);
-      *reinterpret_cast<uint4*>(sq + r * kPitch + ch * 8) =
-          make_uint4(out[0], out[1], out[2], out[3]);
-      if (ch == 0) {
-        s_mult[r] = p.scale_log2 * exp2_int(-up);
-        s_vis[r] = ok ? row_end(p, len, n_new, r0 + r) : 0;
-        s_lse[r] =
-            ok ? p.lse2[static_cast<long long>(bh) * lse2_rows + r0 + r]
-               : INFINITY;
-      }
-    }
-    __syncthreads();
-    if (key0 >= len) continue;
-#pragma unroll 2
-    for (int nt = 0; nt < kWRows / 8; ++nt) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf) {
-        const uint16_t* row = sq + (8 * nt + g8) * kPitch + 64 * hf + 16 * c;
-        const uint4 w0 = *reinterpret_cast<const uint4*>(row);
-        const uint4 w1 = *reinterpret_cast<const uint4*>(row + 8);
-        const uint32_t bw[8] = {w0.x, w0.y, w0.z, w0.w,
-                                w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          mma_f16(s, a[4 * hf + w][0], a[4 * hf + w][1], a[4 * hf + w][2],
-                  a[4 * hf + w][3], bw[2 * w], bw[2 * w + 1]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 8 * nt + 2 * c + (e & 1);
-        const int key = key0 + g8 + 8 * (e >> 1);
-        if (key < s_vis[r])
-          sum[e >> 1] += ptx::ex2(s[e] * (s_mult[r] * ks) - s_lse[r]);
-      }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-    const int key = key0 + g8 + 8 * e;
-    if (c == 0 && key < len && sum[e] != 0.f)
-      p.weights[static_cast<long long>(bh) * p.capacity + key] += sum[e];
-  }
-}
-
 template <int D, int NT, bool kBF16>
 cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
   using C = Config<D, NT>;
@@ -1051,15 +910,6 @@ cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
 }
 
 template <int D, bool kBF16>
-cudaError_t launch_weights_dt(const FwdParams& p, int lse2_rows,
-                              cudaStream_t stream) {
-  const long long tiles = (p.capacity + 127) / 128;
-  return launch_pdl(kv8_weights_kernel<D, kBF16>,
-                    static_cast<long long>(p.B) * p.Hkv * tiles, kThreads, 0,
-                    stream, p, lse2_rows);
-}
-
-template <int D, bool kBF16>
 cudaError_t launch_dt(int rows, const FwdParams& p, cudaStream_t stream) {
   return rows <= 8 ? launch_rows<D, 1, kBF16>(p, stream)
                    : launch_rows<D, 2, kBF16>(p, stream);
@@ -1074,15 +924,6 @@ cudaError_t launch_decode(int D, bool bf16, int rows, const FwdParams& p,
                 : launch_dt<64, false>(rows, p, stream);
   return bf16 ? launch_dt<128, true>(rows, p, stream)
               : launch_dt<128, false>(rows, p, stream);
-}
-
-cudaError_t launch_weights(int D, bool bf16, int lse2_rows,
-                           const FwdParams& p, cudaStream_t stream) {
-  if (D == 64)
-    return bf16 ? launch_weights_dt<64, true>(p, lse2_rows, stream)
-                : launch_weights_dt<64, false>(p, lse2_rows, stream);
-  return bf16 ? launch_weights_dt<128, true>(p, lse2_rows, stream)
-              : launch_weights_dt<128, false>(p, lse2_rows, stream);
 }
 
 }  // namespace kv8

@@ -432,10 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
       bool issued = false;
       for (int k = 0; ok; ++k) {
-        volatile Record* rec = get_unit(k);
-        if (rec == nullptr) break;
-        const int n0 = rec->n[0], n1 = rec->n[1];
-        const int n_kv = rec->n_kv;  // = max(n0, n1)
+        ok = wait(bar_unit + 8 * (k % kUnits), k / kUnits, 1);
+        if (!ok) break;
+        // Through a warp reduction the counts are warp-uniform to the
+        // compiler, and with them the ring position: descriptors then stay in
+        // uniform registers (else every MMA moves them there first).
+        volatile Record* rec = records + k % kUnits;
+        const int n0 = __reduce_max_sync(0xffffffffu, rec->n[0]);
+        const int n1 = __reduce_max_sync(0xffffffffu, rec->n[1]);
+        const int n_kv = __reduce_max_sync(0xffffffffu, rec->n_kv);
+        if (n_kv == 0) break;
         release_unit(k);
         ok = wait(bar_full + 8 * (it % L::kSlots), it / L::kSlots, 2);
 #pragma unroll
