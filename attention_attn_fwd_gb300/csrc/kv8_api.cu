@@ -316,6 +316,10 @@ attn_status_t evict_impl(const attn_kv8_t* src, const attn_kv8_t* dst,
   if (keep < 1 || keep > dst->capacity || recent < 0 || recent > keep)
     return ATTN_ERR_INVALID_ARG;
   if (src->B == 0) return ATTN_OK;
+  // CTAs of the move launch: K and V by blocks of a head, weights by 128.
+  if (2LL * src->B * src->Hkv *
+          ((keep - 1) / src->block + dst->capacity / 128 + 16) > 0x7fffffffLL)
+    return ATTN_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
   st = check_cache_memory(*src, dev);

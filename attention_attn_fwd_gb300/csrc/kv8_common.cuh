@@ -85,6 +85,12 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float* x) {
   x[3] = b.y;
 }
 
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Programmatic dependent launches: every kernel of the 8-bit cache may be
 // scheduled before the one ahead of it on the stream has ended, so that its
 // launch overlaps that one's tail.  Each begins with start_after_previous():
@@ -209,6 +215,7 @@ struct EvictParams {
   int* indices;           // [B, Hkv, keep]
   int B, Hkv, src_capacity, dst_capacity, src_nblk, dst_nblk, block_shift;
   int keep, recent;
+  int held_keys;          // select: keys a CTA holds in shared memory
   int in_place;
   unsigned int* status;
 };
@@ -221,7 +228,7 @@ cudaError_t launch_prefill(int D, bool bf16, const FwdParams& p,
                            cudaStream_t stream);
 cudaError_t launch_weights(int D, bool bf16, int lse2_rows,
                            const FwdParams& p, cudaStream_t stream);
-cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_evict(int D, EvictParams p, cudaStream_t stream);
 
 }  // namespace kv8
 }  // namespace attn

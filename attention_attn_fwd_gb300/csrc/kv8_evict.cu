@@ -1,18 +1,25 @@
 // Eviction from the 8-bit cache by accumulated attention weight.
 //
-// Kernel 1 (select), one CTA per (batch, K/V head): the candidates' weights
-// as order-preserving 32-bit keys; a radix select (four 8-bit digits from the
-// top, one histogram pass each) finds the key of the last token kept and how
-// many tokens of that very key stay (the earliest ones); a counting pass and
-// a writing pass then list the kept places in ascending order.
+// Kernel 1 (select), a cluster of 1 to 8 CTAs per (batch, K/V head), each with
+// a consecutive part of the tokens: the candidates' weights become
+// order-preserving 32-bit keys in shared memory (one pass over them in
+// memory); a radix select (four 8-bit digits from the top, the parts'
+// histograms summed over the cluster) finds the key of the last token kept
+// and how many tokens of that very key stay (the earliest ones); counts of
+// kept tokens, summed over the parts before, give each its place in the
+// ascending list.
 //
-// Kernel 2 (move), one cluster of CTAs per (batch, K/V head) and of K, V or
-// the weights: blocks of destination tokens in ascending rounds, each CTA of
-// the cluster one block a round: gather the codes to registers, reduce the
-// largest magnitude, settle the block's power-of-two scale, shift the codes
-// to it, store.  In place this is safe with one cluster barrier per round
-// between its reads and its writes: the n-th kept token comes from a place
-// >= n, so a round only overwrites places that no later round reads.
+// Kernel 2 (move), CTAs by (batch, K/V head) and K, V or the weights, one
+// block of destination tokens at a time: gather the codes to registers,
+// reduce the largest magnitude, settle the block's power-of-two scale, shift
+// the codes to it, store.  Into another cache every block is a CTA of its
+// own.  In place a cluster of eight takes the blocks in ascending rounds with
+// one cluster barrier per round between its reads and its writes: the n-th
+// kept token comes from a place >= n, so a round only overwrites places that
+// no later round reads.
+//
+// Bound by launch and barrier latency on short caches (select: four digits of
+// two barriers each) and by the gathered codes' traffic on long ones.
 #include "kv8_common.cuh"
 
 namespace attn {
@@ -29,109 +36,135 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kKeysPerCta = 8192;   // tokens from which on a cluster grows
+constexpr int kMaxHeld = 48 * 1024; // keys a CTA can hold in shared memory
 
-// Exclusive sum of two counters over the CTA's warps (lane 0's values
-// count); every thread of a warp gets its warp's offsets.
-__device__ __forceinline__ int2 warp_offsets(int2 v, int2* sm) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (lane == 0) sm[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    const int2 x = sm[lane];
-    int a = x.x, b = x.y;
-#pragma unroll
-    for (int s = 1; s < 32; s *= 2) {
-      const int ua = __shfl_up_sync(0xffffffffu, a, s);
-      const int ub = __shfl_up_sync(0xffffffffu, b, s);
-      if (lane >= s) {
-        a += ua;
-        b += ub;
-      }
-    }
-    sm[lane] = make_int2(a - x.x, b - x.y);
-  }
-  __syncthreads();
-  const int2 r = sm[warp];
-  __syncthreads();
-  return r;
+// Shared memory of a select CTA that peers read.
+struct Shared {
+  int hist[2][256];      // of the digit, double-buffered
+  int sum[256];          // the same, of the whole cluster
+  int2 count;            // kept for certain, equal to the threshold
+  int2 warp[kSelWarps];  // the same, per warp
+  unsigned digit;
+  int left;
+};
+
+__device__ __forceinline__ uint32_t ld_peer(const void* p, uint32_t rank) {
+  return static_cast<uint32_t>(ptx::ld_shared_cluster_s32(
+      ptx::mapa_shared(ptx::smem_u32(p), rank)));
+}
+__device__ __forceinline__ void cluster_barrier() {
+  ptx::cluster_arrive_release();
+  ptx::cluster_wait_acquire();
 }
 
-__global__ void __launch_bounds__(kSelThreads)
-    kv8_select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int2 sm_warp[32];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_left;
+__global__ void __launch_bounds__(kSelThreads, 1)
+    kv8_select_kernel(const EvictParams p, int ranks) {
+  extern __shared__ uint32_t keys[];  // of this CTA's candidates
+  __shared__ Shared sh;
   start_after_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int bh = blockIdx.x;
+  const int bh = blockIdx.x / ranks, rank = blockIdx.x - bh * ranks;
   const int b = bh / p.Hkv;
   const int len = clamp_len(p.src_lens[b], p.src_capacity, p.status);
   int* idx = p.indices + static_cast<long long>(bh) * p.keep;
-  if (len <= p.keep) {
-    for (int i = threadIdx.x; i < p.keep; i += kSelThreads)
+  if (len <= p.keep) {  // the whole cluster
+    for (int i = rank * kSelThreads + threadIdx.x; i < p.keep;
+         i += ranks * kSelThreads)
       idx[i] = i < len ? i : -1;
     return;
   }
   const float* w = p.weights + static_cast<long long>(bh) * p.src_capacity;
   const int cand = len - p.recent;        // candidates: places [0, cand)
   const int want = p.keep - p.recent;     // of which so many stay
+  // This CTA's places [a0, a1); its candidates' keys are held when they fit
+  // (else read from memory again in each pass).
+  const int per_cta = (len + ranks - 1) / ranks;
+  const int a0 = min(len, rank * per_cta), a1 = min(len, a0 + per_cta);
+  const int c1 = max(a0, min(cand, a1));  // candidates [a0, c1)
+  const bool held = c1 - a0 <= p.held_keys;
+  if (held) {
+#pragma unroll 4
+    for (int j = a0 + threadIdx.x; j < c1; j += kSelThreads)
+      keys[j - a0] = weight_key(__ldg(w + j));
+  }
+  auto key_at = [&](int j) { return held ? keys[j - a0] : weight_key(w[j]); };
+  for (int i = threadIdx.x; i < 512; i += kSelThreads) sh.hist[i / 256][i % 256] = 0;
+  __syncthreads();
+
   // Radix select of the want-th largest key.
   uint32_t prefix = 0u, mask = 0u;
   int left = want;  // tokens still wanted among keys matching the prefix
-  if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
+  for (int shift = 24, buf = 0; shift >= 0 && want > 0; shift -= 8, buf ^= 1) {
+    for (int j = a0 + threadIdx.x; j < c1; j += kSelThreads) {
+      const uint32_t key = key_at(j);
+      if ((key & mask) == prefix)
+        atomicAdd(&sh.hist[buf][(key >> shift) & 255u], 1);
+    }
+    if (ranks > 1)
+      cluster_barrier();
+    else
       __syncthreads();
-      for (int j = threadIdx.x; j < cand; j += kSelThreads) {
-        const uint32_t key = weight_key(w[j]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
+    if (threadIdx.x < 256) {
+      int n = 0;
+      if (ranks > 1) {
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < ranks)
+            n += static_cast<int>(ld_peer(&sh.hist[buf][threadIdx.x], r));
+      } else {
+        n = sh.hist[buf][threadIdx.x];
       }
-      __syncthreads();
-      if (warp == 0) {
-        // Digits from the top, eight per lane (lane 0 holds 255 .. 248).
-        int n[8], sum = 0;
+      sh.sum[threadIdx.x] = n;
+    } else if (threadIdx.x < 512 && shift < 24) {
+      // The other buffer was read ahead of this digit's barrier: clear it
+      // for the next one.
+      sh.hist[buf ^ 1][threadIdx.x - 256] = 0;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // Digits from the top, eight per lane (lane 0 holds 255 .. 248).
+      int n[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[e] = sh.sum[255 - (8 * lane + e)];
+        sum += n[e];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int s = 1; s < 32; s *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += up;
+      }
+      int before = incl - sum;
+      if (before < left && incl >= left) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          n[e] = hist[255 - (8 * lane + e)];
-          sum += n[e];
-        }
-        int incl = sum;
-#pragma unroll
-        for (int s = 1; s < 32; s *= 2) {
-          const int up = __shfl_up_sync(0xffffffffu, incl, s);
-          if (lane >= s) incl += up;
-        }
-        int before = incl - sum;
-        if (before < left && incl >= left) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (before < left && before + n[e] >= left) {
-              s_digit = 255u - (8 * lane + e);
-              s_left = left - before;
-            }
-            before += n[e];
+          if (before < left && before + n[e] >= left) {
+            sh.digit = 255u - (8 * lane + e);
+            sh.left = left - before;
           }
+          before += n[e];
         }
       }
-      __syncthreads();
-      prefix |= s_digit << shift;
-      mask |= 255u << shift;
-      left = s_left;
-      __syncthreads();
     }
+    __syncthreads();
+    prefix |= sh.digit << shift;
+    mask |= 255u << shift;
+    left = sh.left;
   }
   // Kept: keys above the threshold, the first `left` tokens of its very key,
   // and the recent ones.  Each warp takes a consecutive range of places.
-  const int per = (len + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
-  const int j0 = min(len, warp * per), j1 = min(len, j0 + per);
+  const int per = (a1 - a0 + kSelThreads - 1) / kSelThreads * 32;
+  const int j0 = min(a1, a0 + warp * per), j1 = min(a1, j0 + per);
   auto flags = [&](int j, unsigned* above, unsigned* equal) {
     bool a = false, q = false;
     if (j < j1) {
       if (j >= cand) {
         a = true;
       } else if (want > 0) {
-        const uint32_t key = weight_key(w[j]);
+        const uint32_t key = key_at(j);
         a = key > prefix;
         q = key == prefix;
       }
@@ -146,8 +179,35 @@ __global__ void __launch_bounds__(kSelThreads)
     n.x += __popc(a);
     n.y += __popc(q);
   }
-  const int2 off = warp_offsets(n, sm_warp);
-  int above = off.x, equal = off.y;
+  if (lane == 0) sh.warp[warp] = n;
+  __syncthreads();
+  if (warp == 0) {  // exclusive sums over the warps, and the CTA's total
+    const int2 x = sh.warp[lane];
+    int a = x.x, q = x.y;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const int ua = __shfl_up_sync(0xffffffffu, a, s);
+      const int uq = __shfl_up_sync(0xffffffffu, q, s);
+      if (lane >= s) {
+        a += ua;
+        q += uq;
+      }
+    }
+    sh.warp[lane] = make_int2(a - x.x, q - x.y);
+    if (lane == 31) sh.count = make_int2(a, q);
+  }
+  if (ranks > 1)
+    cluster_barrier();
+  else
+    __syncthreads();
+  int above = sh.warp[warp].x, equal = sh.warp[warp].y;
+  if (ranks > 1) {
+    for (int r = 0; r < rank; ++r) {
+      above += static_cast<int>(ld_peer(&sh.count.x, r));
+      equal += static_cast<int>(ld_peer(&sh.count.y, r));
+    }
+    ptx::cluster_arrive_release();  // awaited at the end: peers' reads
+  }
   for (int j = j0; j < j1; j += 32) {
     unsigned a, q;
     flags(j + lane, &a, &q);
@@ -162,19 +222,48 @@ __global__ void __launch_bounds__(kSelThreads)
     above += __popc(a);
     equal += __popc(q);
   }
+  if (ranks > 1) ptx::cluster_wait_acquire();
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kCluster = 8;
+constexpr int kMoveThreads = 512;  // most; two chunks of 16 codes a thread
+constexpr int kCluster = 8;  // CTAs per unit in place
 
-// One round of the codes: destination block `nb` of one head.
-template <int D>
+// Largest magnitude of 16 codes (NaN codes do not count).
+__device__ __forceinline__ float codes_amax(uint4 c) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t m = 0u;  // two halves
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t lo, hi;
+    e4m3x4_to_half2(w[e] & 0x7f7f7f7fu, lo, hi);
+    asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(lo));
+    asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(hi));
+  }
+  const float2 f = unpack2<false>(m);
+  return fmaxf(f.x, f.y);
+}
+
+// Four halves to four E4M3 codes, round to nearest even, saturating.
+__device__ __forceinline__ uint32_t half2x2_to_e4m3(uint32_t lo, uint32_t hi) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(d)
+      : "r"(lo), "r"(hi));
+  return d;
+}
+
+// The codes of K or V of one head: destination blocks rank, rank + ranks, ...
+template <int D, bool kInPlace>
 __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
-                                           int bh, int rank, int len,
-                                           int n_kept) {
+                                           int bh, int rank, int ranks,
+                                           int len, int n_kept) {
   constexpr int kPerRow = D / 16;                       // 16-byte chunks
-  constexpr int kMax = 128 * kPerRow / kMoveThreads;    // chunks per thread
+  constexpr int kMax = 2;
   __shared__ float red[kMoveThreads / 32];
+  const int threads = blockDim.x;  // of a block's chunks, half as many
   const int block = 1 << p.block_shift;
   const bool whole = len <= p.keep;  // nothing leaves: bit for bit
   const int* idx = p.indices + static_cast<long long>(bh) * p.keep;
@@ -186,160 +275,195 @@ __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
                  static_cast<long long>(bh) * p.dst_capacity * D;
   float* dst_scale = p.dst_scale[kv] + static_cast<long long>(bh) * p.dst_nblk;
   const int blocks = (n_kept + block - 1) >> p.block_shift;
-  const int rounds = (blocks + kCluster - 1) / kCluster;
-  const int chunks = block * kPerRow;
+  const int rounds = (blocks + ranks - 1) / ranks;
   for (int rd = 0; rd < rounds; ++rd) {
-    const int nb = rd * kCluster + rank;
+    const int nb = rd * ranks + rank;
+    if (!kInPlace && nb >= blocks) break;
     const int t0 = nb << p.block_shift;
     uint4 held[kMax];
     float factor[kMax];
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < kMax; ++i) {
-      const int ch = threadIdx.x + i * kMoveThreads;
+      const int ch = threadIdx.x + i * threads;
       const int tok = t0 + ch / kPerRow;
       held[i] = make_uint4(0u, 0u, 0u, 0u);
       factor[i] = 0.f;
-      if (ch < chunks && tok < n_kept) {
+      if (tok < n_kept) {
         const int from = whole ? tok : idx[tok];
         held[i] = *reinterpret_cast<const uint4*>(
             src + static_cast<long long>(from) * D + (ch % kPerRow) * 16);
         factor[i] = src_scale[from >> p.block_shift];
-        const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float f[4];
-          e4m3x4_to_float(w[e], f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            amax = fmaxf(amax, finite_abs(f[j] * factor[i]));
-        }
       }
     }
+#pragma unroll
+    for (int i = 0; i < kMax; ++i)
+      amax = fmaxf(amax, finite_abs(codes_amax(held[i]) * factor[i]));
 #pragma unroll
     for (int s = 16; s > 0; s /= 2)
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = amax;
-    float first = 0.f;
+    float first = 0.f;  // the block's scale, where nothing leaves
     if (whole && threadIdx.x == 0 && nb < blocks) first = src_scale[nb];
-    if (p.in_place) {
+    if constexpr (kInPlace) {
       // Every CTA of the cluster has read what this round overwrites.
-      ptx::cluster_arrive_release();
-      ptx::cluster_wait_acquire();
+      cluster_barrier();
     } else {
       __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < kMoveThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+    for (int i = 0; i < threads / 32; ++i) amax = fmaxf(amax, red[i]);
     const float now = exp2_int(tight_exponent(amax));
     const float inv = 1.f / now;
     if (threadIdx.x == 0 && nb < blocks) dst_scale[nb] = whole ? first : now;
 #pragma unroll
     for (int i = 0; i < kMax; ++i) {
-      const int ch = threadIdx.x + i * kMoveThreads;
+      const int ch = threadIdx.x + i * threads;
       const int tok = t0 + ch / kPerRow;
-      if (ch < chunks && tok < n_kept) {
-        uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-        if (!whole) {
+      if (tok >= n_kept) continue;
+      uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+      const float ratio = factor[i] * inv;
+      if (whole || ratio == 1.f) {
+        // As it is.
+      } else if ((__float_as_int(ratio) & 0x7fffff) == 0 && ratio > 1e-30f &&
+                 ratio <= 32768.f) {
+        // A shift of the exponent, in fp16: exact where a code above zero
+        // can result (its last bit is 2^-24 or more then).
+        const uint32_t r2 = ptx::pack2<false>(ratio, ratio);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float f[4];
-            e4m3x4_to_float(w[e], f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = f[j] * factor[i] * inv;
-            w[e] = ptx::pack4_e4m3(f[0], f[1], f[2], f[3]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          uint32_t lo, hi;
+          e4m3x4_to_half2(w[e], lo, hi);
+          w[e] = half2x2_to_e4m3(hmul2(lo, r2), hmul2(hi, r2));
         }
-        *reinterpret_cast<uint4*>(dst + static_cast<long long>(tok) * D +
-                                  (ch % kPerRow) * 16) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+      } else {  // a scale of other origin, or out of fp16's range
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float f[4];
+          e4m3x4_to_float(w[e], f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = f[j] * factor[i] * inv;
+          w[e] = ptx::pack4_e4m3(f[0], f[1], f[2], f[3]);
+        }
       }
+      *reinterpret_cast<uint4*>(dst + static_cast<long long>(tok) * D +
+                                (ch % kPerRow) * 16) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncthreads();  // red is free again
   }
 }
 
+template <bool kInPlace>
 __device__ __forceinline__ void move_weights(const EvictParams& p, int bh,
-                                             int rank, int n_kept) {
+                                             int rank, int ranks,
+                                             int n_kept) {
   const int* idx = p.indices + static_cast<long long>(bh) * p.keep;
   const float* src = p.weights + static_cast<long long>(bh) * p.src_capacity;
   float* dst = p.dst_weights + static_cast<long long>(bh) * p.dst_capacity;
-  constexpr int kPer = 4 * kMoveThreads;  // tokens a CTA moves per round
-  const int step = kPer * kCluster;
+  const int threads = blockDim.x;
+  const int per = 4 * threads;  // tokens a CTA moves per round
+  const int step = per * ranks;
   const int rounds = (n_kept + step - 1) / step;
   for (int rd = 0; rd < rounds; ++rd) {
-    const int t0 = rd * step + rank * kPer + threadIdx.x;
+    const int t0 = rd * step + rank * per + threadIdx.x;
     float w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int tok = t0 + i * kMoveThreads;
+      const int tok = t0 + i * threads;
       w[i] = tok < n_kept ? src[idx[tok]] : 0.f;
     }
-    if (p.in_place) {
-      ptx::cluster_arrive_release();
-      ptx::cluster_wait_acquire();
-    }
+    if constexpr (kInPlace) cluster_barrier();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int tok = t0 + i * kMoveThreads;
+      const int tok = t0 + i * threads;
       if (tok < n_kept) dst[tok] = w[i];
     }
   }
-  if (p.in_place && rounds == 0) {
-    ptx::cluster_arrive_release();
-    ptx::cluster_wait_acquire();
-  }
   // Every read of the sources is behind the last round's barrier.
-  for (int tok = n_kept + rank * kMoveThreads + threadIdx.x;
-       tok < p.dst_capacity; tok += kCluster * kMoveThreads)
+  for (int tok = n_kept + rank * threads + threadIdx.x;
+       tok < p.dst_capacity; tok += ranks * threads)
     dst[tok] = 0.f;
 }
 
-template <int D>
+template <int D, bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads)
-    kv8_move_kernel(const EvictParams p) {
+    kv8_move_kernel(const EvictParams p, int ranks, int weight_ranks) {
   start_after_previous();
-  const int rank = blockIdx.x % kCluster;
-  const int unit = blockIdx.x / kCluster;
-  const int part = unit % 3;  // K, V, weights
-  const int bh = unit / 3;
+  // K and V of every head, `ranks` CTAs each, then its weights.
+  const int heads = p.B * p.Hkv;
+  int x = blockIdx.x;
+  const bool codes = x < 2 * heads * ranks;
+  if (!codes) {
+    x -= 2 * heads * ranks;
+    ranks = weight_ranks;
+  }
+  const int unit = x / ranks, rank = x - unit * ranks;
+  const int bh = codes ? unit / 2 : unit;
   const int b = bh / p.Hkv;
   const int len = clamp_len(p.src_lens[b], p.src_capacity, p.status);
   const int n_kept = min(len, p.keep);
-  if (part < 2) {
-    if (p.in_place && len <= p.keep) return;  // stays as it is
-    move_codes<D>(p, part, bh, rank, len, n_kept);
+  if (codes) {
+    if (kInPlace && len <= p.keep) return;  // stays as it is
+    move_codes<D, kInPlace>(p, unit % 2, bh, rank, ranks, len, n_kept);
   } else {
-    move_weights(p, bh, rank, n_kept);
+    move_weights<kInPlace>(p, bh, rank, ranks, n_kept);
     if (bh % p.Hkv == 0 && rank == 0 && threadIdx.x == 0)
       p.dst_lens[b] = n_kept;
   }
 }
 
-template <int D>
-cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
+// Launch with clusters of `cluster` CTAs (1: none).
+template <class Kernel, class... Args>
+cudaError_t launch_cluster(Kernel kernel, long long grid, int threads,
+                           int smem, int cluster, cudaStream_t stream,
+                           Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * 3 * kCluster, 1, 1);
-  cfg.blockDim = dim3(kMoveThreads, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kv8_move_kernel<D>, p);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D>
+cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  const int threads = (D / 16 << p.block_shift) / 2;  // 32 to 512
+  if (p.in_place)
+    return launch_cluster(kv8_move_kernel<D, true>, heads * 3 * kCluster,
+                          threads, 0, kCluster, stream, p, kCluster, kCluster);
+  const int blocks = ((p.keep - 1) >> p.block_shift) + 1;
+  const int weight_ranks = (p.dst_capacity - 1) / (4 * threads) + 1;
+  return launch_cluster(kv8_move_kernel<D, false>,
+                        heads * (2 * blocks + weight_ranks), threads, 0, 1,
+                        stream, p, blocks, weight_ranks);
 }
 
 }  // namespace
 
-cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream) {
-  const cudaError_t err =
-      launch_pdl(kv8_select_kernel, static_cast<long long>(p.B) * p.Hkv,
-                 kSelThreads, 0, stream, p);
+cudaError_t launch_evict(int D, EvictParams p, cudaStream_t stream) {
+  // CTAs per head: parts of about 8192 tokens, a power of two of them.
+  int ranks = 1;
+  while (ranks < kMaxCluster && p.src_capacity > ranks * kKeysPerCta)
+    ranks *= 2;
+  const int part = (p.src_capacity - 1) / ranks + 1;
+  p.held_keys = part < kMaxHeld ? part : kMaxHeld;
+  const int smem = p.held_keys * 4;
+  cudaError_t err = cudaFuncSetAttribute(
+      kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  err = launch_cluster(kv8_select_kernel,
+                       static_cast<long long>(p.B) * p.Hkv * ranks,
+                       kSelThreads, smem, ranks, stream, p, ranks);
   if (err != cudaSuccess) return err;
   return D == 64 ? launch_move<64>(p, stream) : launch_move<128>(p, stream);
 }

@@ -336,6 +336,11 @@ EVICTS = [
     (2, 1, 1000, 64, 32, [1000, 33], 700, 0),
     (1, 2, 5000, 128, 64, [4999], 1234, 200),
     (4, 1, 64, 64, 16, [64, 1, 63, 32], 64, 3),
+    # Several CTAs select together: their parts uneven, all or none recent.
+    (1, 2, 9001, 64, 128, [9001], 4000, 700),
+    (2, 1, 20000, 64, 32, [19999, 12345], 777, 0),
+    (1, 1, 70000, 64, 64, [70000], 69999, 65000),
+    (2, 1, 40000, 64, 128, [40000, 90], 100, 100),
 ]
 
 
@@ -384,6 +389,33 @@ def test_evict(case, in_place):
     assert torch.equal(out_w.cpu().nan_to_num(9), ow.nan_to_num(9))
     same_cache(out, want)
     assert gpu.lens.cpu().tolist() == lens
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_of_blocks_that_lose_their_large_tokens(in_place):
+    """Kept codes shift up by as much as 2^17, or down to nothing."""
+    B, H, cap, D, block, keep = 1, 1, 128, 64, 32, 40
+    g = ref.rng(75)
+    x = torch.randn(1, 1, cap, D, generator=g).double()
+    size = torch.exp2((24 * torch.rand(cap, generator=g) - 24).floor())
+    size[::8] = 2.0 ** 12
+    x = (x * size[None, None, :, None]).float().bfloat16()
+    c = ref.Cache(B, H, cap, D, block)
+    c.lens = [cap]
+    c.append(x, x)
+    w = torch.rand(B, H, cap, generator=g)
+    w[0, 0, ::8] = 0.0       # the large ones leave,
+    w[0, 0, 64::8] = 1.0     # but for those of the last blocks
+    want, ow, idx = c.evict(w, keep, 0, cap)
+    gpu = upload(c)
+    out = None if in_place else upload(ref.Cache(B, H, cap, D, block))
+    out, out_w, got = attn.kv8_evict(gpu, w.cuda(), keep, 0, out=out)
+    assert torch.equal(got.cpu(), idx)
+    if in_place:
+        for n in "kv":
+            want.code[n][:, :, keep:] = c.code[n][:, :, keep:]
+            want.scale[n][:, :, 2:] = c.scale[n][:, :, 2:]
+    same_cache(out, want)
 
 
 # ------------------------------------------------------------- all together
