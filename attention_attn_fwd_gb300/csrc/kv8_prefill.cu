@@ -565,11 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (row0 + (e0 + e) * kRowStep >= valid)
                 x[e] = make_uint4(0u, 0u, 0u, 0u);
           }
-          if (e0 + kBatch >= kItems) {
-            // The raw tile has been read.
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar_rempty + 8 * rslot);
-          }
           if (e0 == 0 && it >= L::kSlots) {
             ok = wait(bar_empty + 8 * slot, it / L::kSlots - 1, 8);
             if (!ok) break;
@@ -597,7 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar_full + 8 * slot);
+        // The raw tile is released only now that its values have been used: a
+        // load that has been issued may still read shared memory after an
+        // arrival issued behind it, when the next copy is already landing.
+        if (lane == 0) {
+          ptx::mbar_arrive(bar_full + 8 * slot);
+          ptx::mbar_arrive(bar_rempty + 8 * rslot);
+        }
         ++it;
       }
     }

@@ -58,6 +58,13 @@ class Cache:
                                     dtype=torch.float64) for n in "kv"}
         self.lens = [0] * B
 
+    def to(self, device):
+        c = Cache(self.B, self.H, 1, self.D, self.block)
+        c.cap, c.lens = self.cap, list(self.lens)
+        c.code = {n: t.to(device) for n, t in self.code.items()}
+        c.scale = {n: t.to(device) for n, t in self.scale.items()}
+        return c
+
     def clone(self):
         c = Cache(self.B, self.H, self.cap, self.D, self.block)
         c.code = {n: t.clone() for n, t in self.code.items()}
@@ -142,9 +149,10 @@ def attention(cache, q, scale, causal, new=None):
     B, Hq, Sq, D = q.shape
     g = Hq // cache.H
     qd = q.double()
-    o = torch.zeros(B, Hq, Sq, D, dtype=torch.float64)
-    lse = torch.full((B, Hq, Sq), -math.inf, dtype=torch.float64)
-    w = torch.zeros(B, cache.H, cache.cap, dtype=torch.float64)
+    new_ = dict(dtype=torch.float64, device=q.device)
+    o = torch.zeros(B, Hq, Sq, D, **new_)
+    lse = torch.full((B, Hq, Sq), -math.inf, **new_)
+    w = torch.zeros(B, cache.H, cache.cap, **new_)
     tol_o, tol_lse = torch.zeros_like(o), torch.zeros_like(lse)
     tol_w = torch.zeros_like(w)
     eps = torch.finfo(q.dtype).eps / 2
@@ -156,10 +164,10 @@ def attention(cache, q, scale, causal, new=None):
         for h in range(Hq):
             k, v = (cache.values(n, b, h // g) for n in "kv")
             s = scale * (qd[b, h, :cnt] @ k.T)
-            end = torch.full((cnt,), L)
+            end = torch.full((cnt,), L, device=q.device)
             if causal:
-                end = torch.arange(L - cnt + 1, L + 1)
-            see = torch.arange(L)[None] < end[:, None]
+                end = torch.arange(L - cnt + 1, L + 1, device=q.device)
+            see = torch.arange(L, device=q.device)[None] < end[:, None]
             s = s.masked_fill(~see, -math.inf)
             lse[b, h, :cnt] = torch.logsumexp(s, 1)
             any_ = see.any(1)

@@ -163,11 +163,14 @@ def run_fwd(c, q, causal=True, new=None, scale=None, with_w=True, gpu=None,
     return (out.cpu(), lse.cpu(), w.cpu() if with_w else None, w0)
 
 
-def check_fwd(c, q, causal=True, new=None, scale=None, with_w=True, gpu=None):
+def check_fwd(c, q, causal=True, new=None, scale=None, with_w=True, gpu=None,
+              where="cpu"):
     B, Hq, Sq, D = q.shape
     scale_ = 1.0 / math.sqrt(D) if scale is None else scale
     out, lse, w, w0 = run_fwd(c, q, causal, new, scale, with_w, gpu)
-    o_r, l_r, w_r, t_o, t_l, t_w = ref.attention(c, q, scale_, causal, new)
+    o_r, l_r, w_r, t_o, t_l, t_w = (
+        t.cpu() for t in ref.attention(c.to(where), q.to(where), scale_,
+                                       causal, new))
     for b in range(B):
         n = Sq if new is None else new[b]
         assert bool((out[b, :, n:] == 7.5).all())
@@ -220,6 +223,46 @@ def test_fwd(case, dtype, causal, with_w):
     c = ref.filled(B, Hkv, cap, D, block, lens, 11)
     q = torch.randn(B, Hq, Sq, D, generator=ref.rng(12)).to(DT[dtype])
     check_fwd(c, q, causal, new, with_w=with_w)
+
+
+LONG = [
+    # Many key tiles and units for every CTA.
+    (4, 32, 8, 2100, 128, 64, [2100, 2077, 1500, 2099], 250, None),
+    (3, 24, 8, 3001, 64, 32, [3001, 2000, 2999], 333, [333, 1, 300]),
+    (8, 16, 16, 1030, 128, 16, [1030 - 7 * i for i in range(8)], 129, None),
+    (16, 16, 8, 1500, 128, 128, [1500 - 90 * i for i in range(16)], 1, None),
+    (16, 32, 4, 2049, 64, 64, [2049 - 120 * i for i in range(16)], 2, None),
+    (70, 8, 8, 300, 128, 32, [(37 * i) % 301 for i in range(70)], 2, None),
+    (2, 16, 4, 20000, 128, 128, [20000, 13001], 4, None),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", LONG)
+def test_fwd_long(case, dtype, causal):
+    """Against the float64 definition computed on the GPU, and again: the
+    same bits every time."""
+    B, Hq, Hkv, cap, D, block, lens, Sq, new = case
+    g = ref.rng(13)
+    c = ref.Cache(B, Hkv, cap, D, block)
+    c.lens = list(lens)
+    nblk = -(-cap // block)
+    for n in "kv":  # codes at random (no NaN), scales over four octaves
+        code = torch.randint(0, 256, (B, Hkv, cap, D), generator=g,
+                             dtype=torch.uint8)
+        c.code[n] = torch.where((code & 127) > 100, code & 0x9F, code)
+        c.scale[n] = torch.exp2(torch.randint(
+            -5, -1, (B, Hkv, nblk), generator=g).double())
+    q = torch.randn(B, Hq, Sq, D, generator=g).to(DT[dtype])
+    scale = 0.5 / math.sqrt(D)
+    check_fwd(c, q, causal, new, scale=scale, where="cuda")
+    gpu = upload(c)
+    first = run_fwd(c, q, causal, new, scale, gpu=gpu)
+    for _ in range(8):
+        again = run_fwd(c, q, causal, new, scale, gpu=gpu)
+        for a, b in zip(first[:3], again[:3]):
+            assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("Sq", [1, 33])
