@@ -215,7 +215,6 @@ struct EvictParams {
   int* indices;           // [B, Hkv, keep]
   int B, Hkv, src_capacity, dst_capacity, src_nblk, dst_nblk, block_shift;
   int keep, recent;
-  int held_keys;          // select: keys a CTA holds in shared memory
   int in_place;
   unsigned int* status;
 };
@@ -228,7 +227,7 @@ cudaError_t launch_prefill(int D, bool bf16, const FwdParams& p,
                            cudaStream_t stream);
 cudaError_t launch_weights(int D, bool bf16, int lse2_rows,
                            const FwdParams& p, cudaStream_t stream);
-cudaError_t launch_evict(int D, EvictParams p, cudaStream_t stream);
+cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream);
 
 }  // namespace kv8
 }  // namespace attn

@@ -2,8 +2,8 @@
 //
 // Kernel 1 (select), a cluster of 1 to 8 CTAs per (batch, K/V head), each with
 // a consecutive part of the tokens: the candidates' weights become
-// order-preserving 32-bit keys in shared memory (one pass over them in
-// memory); a radix select (four 8-bit digits from the top, the parts'
+// order-preserving 32-bit keys in registers (one pass over them in memory); a
+// radix select (four 8-bit digits from the top, the parts'
 // histograms summed over the cluster) finds the key of the last token kept
 // and how many tokens of that very key stay (the earliest ones); counts of
 // kept tokens, summed over the parts before, give each its place in the
@@ -37,15 +37,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kKeysPerCta = 8192;   // tokens from which on a cluster grows
-constexpr int kMaxHeld = 48 * 1024; // keys a CTA can hold in shared memory
+constexpr int kKeysAt = 16;         // most keys a thread holds
 
 // Shared memory of a select CTA that peers read.
 struct Shared {
   int hist[2][256];      // of the digit, double-buffered
   int sum[256];          // the same, of the whole cluster
   int2 count;            // kept for certain, equal to the threshold
-  int2 warp[kSelWarps];  // the same, per warp
+  int2 warp[kKeysAt * kSelWarps];  // the same, per 32 places in order
+  int2 group[kKeysAt];             // per 1024
   unsigned digit;
   int left;
 };
@@ -59,9 +59,12 @@ __device__ __forceinline__ void cluster_barrier() {
   ptx::cluster_wait_acquire();
 }
 
+// kPer: keys a thread holds; place i of thread t is a0 + 1024 i + t of the
+// CTA's part.  Parts of more than 1024 kPer tokens are walked in turns of that
+// many, their keys read again in each pass.
+template <int kPer>
 __global__ void __launch_bounds__(kSelThreads, 1)
     kv8_select_kernel(const EvictParams p, int ranks) {
-  extern __shared__ uint32_t keys[];  // of this CTA's candidates
   __shared__ Shared sh;
   start_after_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -78,29 +81,35 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   const float* w = p.weights + static_cast<long long>(bh) * p.src_capacity;
   const int cand = len - p.recent;        // candidates: places [0, cand)
   const int want = p.keep - p.recent;     // of which so many stay
-  // This CTA's places [a0, a1); its candidates' keys are held when they fit
-  // (else read from memory again in each pass).
-  const int per_cta = (len + ranks - 1) / ranks;
-  const int a0 = min(len, rank * per_cta), a1 = min(len, a0 + per_cta);
-  const int c1 = max(a0, min(cand, a1));  // candidates [a0, c1)
-  const bool held = c1 - a0 <= p.held_keys;
-  if (held) {
-#pragma unroll 4
-    for (int j = a0 + threadIdx.x; j < c1; j += kSelThreads)
-      keys[j - a0] = weight_key(__ldg(w + j));
-  }
-  auto key_at = [&](int j) { return held ? keys[j - a0] : weight_key(w[j]); };
-  for (int i = threadIdx.x; i < 512; i += kSelThreads) sh.hist[i / 256][i % 256] = 0;
+  constexpr int kTurn = kSelThreads * kPer;
+  const int part = (len + ranks - 1) / ranks;
+  const int a0 = min(len, rank * part), a1 = min(len, a0 + part);
+  const int turns = (part + kTurn - 1) / kTurn;
+  uint32_t key[kPer];
+  auto load = [&](int at) {  // the turn that begins at place `at`
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = at + i * kSelThreads + threadIdx.x;
+      key[i] = j < a1 && j < cand ? weight_key(__ldg(w + j)) : 0u;
+    }
+  };
+  load(a0);
+  if (threadIdx.x < 512) sh.hist[threadIdx.x / 256][threadIdx.x % 256] = 0;
   __syncthreads();
 
   // Radix select of the want-th largest key.
   uint32_t prefix = 0u, mask = 0u;
   int left = want;  // tokens still wanted among keys matching the prefix
   for (int shift = 24, buf = 0; shift >= 0 && want > 0; shift -= 8, buf ^= 1) {
-    for (int j = a0 + threadIdx.x; j < c1; j += kSelThreads) {
-      const uint32_t key = key_at(j);
-      if ((key & mask) == prefix)
-        atomicAdd(&sh.hist[buf][(key >> shift) & 255u], 1);
+    for (int t = 0; t < turns; ++t) {
+      const int at = a0 + t * kTurn;
+      if (turns > 1) load(at);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int j = at + i * kSelThreads + threadIdx.x;
+        if (j < a1 && j < cand && (key[i] & mask) == prefix)
+          atomicAdd(&sh.hist[buf][(key[i] >> shift) & 255u], 1);
+      }
     }
     if (ranks > 1)
       cluster_barrier();
@@ -155,72 +164,92 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     left = sh.left;
   }
   // Kept: keys above the threshold, the first `left` tokens of its very key,
-  // and the recent ones.  Each warp takes a consecutive range of places.
-  const int per = (a1 - a0 + kSelThreads - 1) / kSelThreads * 32;
-  const int j0 = min(a1, a0 + warp * per), j1 = min(a1, j0 + per);
-  auto flags = [&](int j, unsigned* above, unsigned* equal) {
-    bool a = false, q = false;
-    if (j < j1) {
-      if (j >= cand) {
-        a = true;
-      } else if (want > 0) {
-        const uint32_t key = key_at(j);
-        a = key > prefix;
-        q = key == prefix;
-      }
-    }
-    *above = __ballot_sync(0xffffffffu, a);
-    *equal = __ballot_sync(0xffffffffu, q);
+  // and the recent ones.
+  auto flags = [&](int at, int i, unsigned* above, unsigned* equal) {
+    const int j = at + i * kSelThreads + threadIdx.x;
+    const bool c = j < cand && j < a1 && want > 0;
+    *above = __ballot_sync(0xffffffffu, (j >= cand && j < a1) ||
+                                            (c && key[i] > prefix));
+    *equal = __ballot_sync(0xffffffffu, c && key[i] == prefix);
   };
-  int2 n = make_int2(0, 0);
-  for (int j = j0; j < j1; j += 32) {
-    unsigned a, q;
-    flags(j + lane, &a, &q);
-    n.x += __popc(a);
-    n.y += __popc(q);
-  }
-  if (lane == 0) sh.warp[warp] = n;
-  __syncthreads();
-  if (warp == 0) {  // exclusive sums over the warps, and the CTA's total
-    const int2 x = sh.warp[lane];
-    int a = x.x, q = x.y;
+  // Counts per 32 places in the order of places, and their sums before.
+  auto count = [&](int at) -> int2 {
 #pragma unroll
-    for (int s = 1; s < 32; s *= 2) {
-      const int ua = __shfl_up_sync(0xffffffffu, a, s);
-      const int uq = __shfl_up_sync(0xffffffffu, q, s);
-      if (lane >= s) {
-        a += ua;
-        q += uq;
-      }
+    for (int i = 0; i < kPer; ++i) {
+      unsigned a, q;
+      flags(at, i, &a, &q);
+      if (lane == 0)
+        sh.warp[i * kSelWarps + warp] = make_int2(__popc(a), __popc(q));
     }
-    sh.warp[lane] = make_int2(a - x.x, q - x.y);
-    if (lane == 31) sh.count = make_int2(a, q);
-  }
-  if (ranks > 1)
-    cluster_barrier();
-  else
     __syncthreads();
-  int above = sh.warp[warp].x, equal = sh.warp[warp].y;
+    int2 x = make_int2(0, 0), incl = x;
+    if (warp < kPer) {  // warp i: the 32 counts of place group i
+      x = incl = sh.warp[warp * kSelWarps + lane];
+#pragma unroll
+      for (int s = 1; s < 32; s *= 2) {
+        const int ua = __shfl_up_sync(0xffffffffu, incl.x, s);
+        const int uq = __shfl_up_sync(0xffffffffu, incl.y, s);
+        if (lane >= s) {
+          incl.x += ua;
+          incl.y += uq;
+        }
+      }
+      if (lane == 31) sh.group[warp] = incl;
+    }
+    __syncthreads();
+    int2 total = make_int2(0, 0), before = total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i == warp) before = total;
+      total.x += sh.group[i].x;
+      total.y += sh.group[i].y;
+    }
+    if (warp < kPer)
+      sh.warp[warp * kSelWarps + lane] = make_int2(
+          before.x + incl.x - x.x, before.y + incl.y - x.y);
+    __syncthreads();
+    return total;
+  };
+  int2 total = make_int2(0, 0);
+  for (int t = 0; t < turns; ++t) {
+    if (turns > 1) load(a0 + t * kTurn);
+    const int2 n = count(a0 + t * kTurn);
+    total.x += n.x;
+    total.y += n.y;
+  }
+  int above = 0, equal = 0;  // kept, equal ones before this turn's places
   if (ranks > 1) {
+    if (threadIdx.x == 0) sh.count = total;
+    cluster_barrier();
     for (int r = 0; r < rank; ++r) {
       above += static_cast<int>(ld_peer(&sh.count.x, r));
       equal += static_cast<int>(ld_peer(&sh.count.y, r));
     }
     ptx::cluster_arrive_release();  // awaited at the end: peers' reads
   }
-  for (int j = j0; j < j1; j += 32) {
-    unsigned a, q;
-    flags(j + lane, &a, &q);
-    const unsigned lower = (1u << lane) - 1u;
-    const int eq_rank = equal + __popc(q & lower);
-    const bool is_eq = (q >> lane) & 1u;
-    const bool kept = ((a >> lane) & 1u) || (is_eq && eq_rank < left);
-    if (kept) {
-      const int at = above + __popc(a & lower) + min(eq_rank, left);
-      idx[at] = j + lane;
+  for (int t = 0; t < turns; ++t) {
+    const int at = a0 + t * kTurn;
+    int2 n = total;
+    if (turns > 1) {
+      load(at);
+      n = count(at);
     }
-    above += __popc(a);
-    equal += __popc(q);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      unsigned a, q;
+      flags(at, i, &a, &q);
+      const unsigned lower = (1u << lane) - 1u;
+      const int2 pre = sh.warp[i * kSelWarps + warp];
+      const int eq_rank = equal + pre.y + __popc(q & lower);
+      const bool kept =
+          ((a >> lane) & 1u) || (((q >> lane) & 1u) && eq_rank < left);
+      if (kept)
+        idx[above + pre.x + __popc(a & lower) + min(eq_rank, left)] =
+            at + i * kSelThreads + threadIdx.x;
+    }
+    above += n.x;
+    equal += n.y;
+    if (turns > 1) __syncthreads();  // the counts have been read
   }
   if (ranks > 1) ptx::cluster_wait_acquire();
 }
@@ -450,20 +479,19 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_evict(int D, EvictParams p, cudaStream_t stream) {
-  // CTAs per head: parts of about 8192 tokens, a power of two of them.
+cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream) {
+  // CTAs per head: parts of up to 4096 tokens (four keys a thread), eight at
+  // most; then 16 keys a thread.
   int ranks = 1;
-  while (ranks < kMaxCluster && p.src_capacity > ranks * kKeysPerCta)
+  while (ranks < kMaxCluster && p.src_capacity > ranks * 4 * kSelThreads)
     ranks *= 2;
-  const int part = (p.src_capacity - 1) / ranks + 1;
-  p.held_keys = part < kMaxHeld ? part : kMaxHeld;
-  const int smem = p.held_keys * 4;
-  cudaError_t err = cudaFuncSetAttribute(
-      kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err != cudaSuccess) return err;
-  err = launch_cluster(kv8_select_kernel,
-                       static_cast<long long>(p.B) * p.Hkv * ranks,
-                       kSelThreads, smem, ranks, stream, p, ranks);
+  const long long grid = static_cast<long long>(p.B) * p.Hkv * ranks;
+  const cudaError_t err =
+      p.src_capacity <= ranks * 4 * kSelThreads
+          ? launch_cluster(kv8_select_kernel<4>, grid, kSelThreads, 0, ranks,
+                           stream, p, ranks)
+          : launch_cluster(kv8_select_kernel<kKeysAt>, grid, kSelThreads, 0,
+                           ranks, stream, p, ranks);
   if (err != cudaSuccess) return err;
   return D == 64 ? launch_move<64>(p, stream) : launch_move<128>(p, stream);
 }

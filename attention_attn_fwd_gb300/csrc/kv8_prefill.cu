@@ -258,6 +258,25 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
       : "memory");
 }
 
+// One 32-byte sector: a thread's row stores then fill sectors whole (16-byte
+// stores of rows 256 or 512 bytes apart leave half-written ones behind).
+__device__ __forceinline__ void store32(void* dst, const uint32_t* x) {
+  asm volatile(
+      "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+      "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+      "r"(x[6]), "r"(x[7])
+      : "memory");
+}
+__device__ __forceinline__ void store_row(uint4* dst, const uint32_t* x,
+                                          bool wide) {
+  if (wide) {
+    store32(dst, x);
+  } else {
+    dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 // ------------------------------------------------------------ the kernel
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -777,6 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             row_ok ? q_row_index(p, rec->b, rec->h, row_u) : 0;
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
                                               row * D);
+        // (O is 16-byte aligned, its rows whole 32-byte sectors from there.)
+        const bool wide = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -789,16 +810,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (row_ok) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t x[4];
+            for (int v = 0; v < 2; ++v) {
+              uint32_t x[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < 8; ++e) {
                 // A row that sees nothing: 0, whatever its accumulator holds.
-                const float a = __uint_as_float(o[8 * v + 2 * e]);
-                const float b = __uint_as_float(o[8 * v + 2 * e + 1]);
+                const float a = __uint_as_float(o[16 * v + 2 * e]);
+                const float b = __uint_as_float(o[16 * v + 2 * e + 1]);
                 x[e] = l_run == 0.f ? 0u : ptx::pack2<kBF16>(a * inv, b * inv);
               }
-              dst[4 * q + v] = make_uint4(x[0], x[1], x[2], x[3]);
+              store_row(dst + 4 * q + 2 * v, x, wide);
             }
           }
         }
@@ -824,12 +845,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_wait_ld();
             if (row_ok) {
 #pragma unroll
-              for (int v = 0; v < 8; ++v)
-                dst[8 * q + v] =
-                    make_float4(__uint_as_float(o[4 * v]) * unit,
-                                __uint_as_float(o[4 * v + 1]) * unit,
-                                __uint_as_float(o[4 * v + 2]) * unit,
-                                __uint_as_float(o[4 * v + 3]) * unit);
+              for (int v = 0; v < 4; ++v) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  o[8 * v + e] =
+                      __float_as_uint(__uint_as_float(o[8 * v + e]) * unit);
+                store32(dst + 8 * q + 2 * v, o + 8 * v);
+              }
             }
           }
         }

@@ -384,6 +384,9 @@ EVICTS = [
     (2, 1, 20000, 64, 32, [19999, 12345], 777, 0),
     (1, 1, 70000, 64, 64, [70000], 69999, 65000),
     (2, 1, 40000, 64, 128, [40000, 90], 100, 100),
+    (1, 1, 300000, 64, 128, [299999], 1000, 10),
+    (1, 1, 290000, 64, 64, [290000], 5000, 0),
+    (2, 2, 4097, 64, 16, [4097, 4096], 4095, 1),
 ]
 
 
