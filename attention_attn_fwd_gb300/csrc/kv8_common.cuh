@@ -185,6 +185,119 @@ __device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
   if (!p.causal) return len;
   return min(len, max(0, len - n_new + r / p.group + 1));
 }
+// The list of tiles: sequence b contributes Hkv segments of
+// ceil(lens[b] / kKeys) tiles.  (Counts fit 32 bits: a tile of one segment
+// holds 4 KB of codes.)
+//
+// Tiles before sequence `seq` and of all sequences, for every lane of the
+// calling warp.
+template <int kKeys>
+__device__ __forceinline__ int list_tiles(const FwdParams& p, int seq,
+                                          int lane, int* before) {
+  int t = 0, pre = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const int n = (seq_len(p, b) + kKeys - 1) / kKeys;
+    t += n;
+    if (b < seq) pre += n;
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s /= 2) {
+    t += __shfl_xor_sync(0xffffffffu, t, s);
+    pre += __shfl_xor_sync(0xffffffffu, pre, s);
+  }
+  *before = pre * p.Hkv;
+  return t * p.Hkv;
+}
+
+// The cut: CTA c of n takes q tiles, the first `rest` CTAs one more.
+struct Cut {
+  int n, q, rest;
+  __device__ __forceinline__ int first(int c) const {
+    return c * q + min(c, rest);
+  }
+  __device__ __forceinline__ int owner(int x) const {
+    const int fat = rest * (q + 1);
+    return x < fat ? x / (q + 1) : rest + (x - fat) / q;
+  }
+};
+// kLeast tiles a CTA, but for the last, are the finest cut.
+template <int kLeast>
+__device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
+  Cut c;
+  c.n = max(1, min(p.grid, (total + kLeast - 1) / kLeast));
+  c.q = total / c.n;
+  c.rest = total - c.q * c.n;
+  return c;
+}
+
+// A segment of the list as a CTA walks its share: it covers positions
+// [pos, end) counted from the share's start (pos < 0: it began earlier).
+struct Segment {
+  int pos, end;
+  int b, h;  // sequence, K/V head
+  int len, tiles;
+};
+
+// CTA's share: its number of tiles (0: none) and first segment.
+template <int kKeys, int kLeast>
+__device__ __forceinline__ int take_share(const FwdParams& p, int cta,
+                                          int lane, Segment* s) {
+  int first = 0, count = 0, base = 0;
+  if (p.B > 32) {
+    const int total = list_tiles<kKeys>(p, 0, lane, &base);
+    const Cut cut = make_cut<kLeast>(p, total);
+    first = cut.first(cta);
+    count = cta < cut.n ? cut.first(cta + 1) - first : 0;
+    if (count == 0) return 0;
+  }
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int len = b < p.B ? seq_len(p, b) : 0;
+    const int t = (len + kKeys - 1) / kKeys * p.Hkv;
+    int incl = t;
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, i);
+      if (lane >= i) incl += up;
+    }
+    const int sum = __shfl_sync(0xffffffffu, incl, 31);
+    if (p.B <= 32) {  // one load per lane tells all
+      const Cut cut = make_cut<kLeast>(p, sum);
+      first = cut.first(cta);
+      count = cta < cut.n ? cut.first(cta + 1) - first : 0;
+      if (count == 0) return 0;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > first);
+    if (hit != 0u) {
+      const int l = __ffs(hit) - 1;
+      const int before = base + __shfl_sync(0xffffffffu, incl - t, l);
+      s->b = b0 + l;
+      s->len = __shfl_sync(0xffffffffu, len, l);
+      s->tiles = (s->len + kKeys - 1) / kKeys;
+      s->h = (first - before) / s->tiles;
+      s->pos = -((first - before) - s->h * s->tiles);
+      s->end = s->pos + s->tiles;
+      return count;
+    }
+    base += sum;
+  }
+  return 0;
+}
+
+template <int kKeys>
+__device__ __forceinline__ void next_segment(const FwdParams& p, Segment& c) {
+  c.pos = c.end;
+  if (++c.h == p.Hkv) {
+    c.h = 0;
+    do {  // some later sequence has tokens: the share is not at its end
+      ++c.b;
+      c.len = seq_len(p, c.b);
+    } while (c.len == 0);
+    c.tiles = (c.len + kKeys - 1) / kKeys;
+  }
+  c.end = c.pos + c.tiles;
+}
+
 // Exponent of the power of two that brings a query row's largest element to
 // [2^13, 2^14) (rows of zeros or of the smallest numbers: as far as it goes).
 __device__ __forceinline__ int row_shift(float amax) {

@@ -86,118 +86,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The list of tiles: sequence b contributes Hkv segments of
-// ceil(lens[b] / kKeys) tiles.  (Counts fit 32 bits: a tile of one segment
-// holds 4 KB of codes.)
-//
-// Tiles before sequence `seq` and of all sequences, for every lane of the
-// calling warp.
-template <int kKeys>
-__device__ __forceinline__ int list_tiles(const FwdParams& p, int seq,
-                                          int lane, int* before) {
-  int t = 0, pre = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const int n = (seq_len(p, b) + kKeys - 1) / kKeys;
-    t += n;
-    if (b < seq) pre += n;
-  }
-#pragma unroll
-  for (int s = 16; s > 0; s /= 2) {
-    t += __shfl_xor_sync(0xffffffffu, t, s);
-    pre += __shfl_xor_sync(0xffffffffu, pre, s);
-  }
-  *before = pre * p.Hkv;
-  return t * p.Hkv;
-}
-
-// The cut: CTA c of n takes q tiles, the first `rest` CTAs one more.
-struct Cut {
-  int n, q, rest;
-  __device__ __forceinline__ int first(int c) const {
-    return c * q + min(c, rest);
-  }
-  __device__ __forceinline__ int owner(int x) const {
-    const int fat = rest * (q + 1);
-    return x < fat ? x / (q + 1) : rest + (x - fat) / q;
-  }
-};
-// At most one tile per warp is the finest cut.
-__device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
-  Cut c;
-  c.n = max(1, min(p.grid, (total + kDecodeWarps - 1) / kDecodeWarps));
-  c.q = total / c.n;
-  c.rest = total - c.q * c.n;
-  return c;
-}
-
-// A segment of the list as a CTA walks its share: it covers positions
-// [pos, end) counted from the share's start (pos < 0: it began earlier).
-struct Segment {
-  int pos, end;
-  int b, h;  // sequence, K/V head
-  int len, tiles;
-};
-
-// CTA's share: its number of tiles (0: none) and first segment.
-template <int kKeys>
-__device__ __forceinline__ int take_share(const FwdParams& p, int cta,
-                                          int lane, Segment* s) {
-  int first = 0, count = 0, base = 0;
-  if (p.B > 32) {
-    const int total = list_tiles<kKeys>(p, 0, lane, &base);
-    const Cut cut = make_cut(p, total);
-    first = cut.first(cta);
-    count = cta < cut.n ? cut.first(cta + 1) - first : 0;
-    if (count == 0) return 0;
-  }
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int len = b < p.B ? seq_len(p, b) : 0;
-    const int t = (len + kKeys - 1) / kKeys * p.Hkv;
-    int incl = t;
-#pragma unroll
-    for (int i = 1; i < 32; i *= 2) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, i);
-      if (lane >= i) incl += up;
-    }
-    const int sum = __shfl_sync(0xffffffffu, incl, 31);
-    if (p.B <= 32) {  // one load per lane tells all
-      const Cut cut = make_cut(p, sum);
-      first = cut.first(cta);
-      count = cta < cut.n ? cut.first(cta + 1) - first : 0;
-      if (count == 0) return 0;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > first);
-    if (hit != 0u) {
-      const int l = __ffs(hit) - 1;
-      const int before = base + __shfl_sync(0xffffffffu, incl - t, l);
-      s->b = b0 + l;
-      s->len = __shfl_sync(0xffffffffu, len, l);
-      s->tiles = (s->len + kKeys - 1) / kKeys;
-      s->h = (first - before) / s->tiles;
-      s->pos = -((first - before) - s->h * s->tiles);
-      s->end = s->pos + s->tiles;
-      return count;
-    }
-    base += sum;
-  }
-  return 0;
-}
-
-template <int kKeys>
-__device__ __forceinline__ void next_segment(const FwdParams& p, Segment& c) {
-  c.pos = c.end;
-  if (++c.h == p.Hkv) {
-    c.h = 0;
-    do {  // some later sequence has tokens: the share is not at its end
-      ++c.b;
-      c.len = seq_len(p, c.b);
-    } while (c.len == 0);
-    c.tiles = (c.len + kKeys - 1) / kKeys;
-  }
-  c.end = c.pos + c.tiles;
-}
-
 // One tile of a warp's ring: 2 KB of K codes, then 2 KB of V codes.  Chunk j
 // (16 bytes) of row r lies at chunk j ^ swizzle(r): the rows read together by
 // the 8 lanes of a phase (K: rows 2q, 2q + 1; V: rows of one parity) then lie
@@ -318,7 +206,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
   const int g8 = lane / 4, c = lane % 4;
   const int cta = blockIdx.x;
   Segment seg;
-  const int count = take_share<kKeys>(p, cta, lane, &seg);
+  const int count = take_share<kKeys, kDecodeWarps>(p, cta, lane, &seg);
   if (count == 0) return;
   const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * 4096;
   Loader<D> ld;
@@ -749,7 +637,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
   if (tiles > 0 && !idle) {
     int first;
     const int total = list_tiles<kKeys>(p, b, lane, &first);
-    const Cut cut = make_cut(p, total);
+    const Cut cut = make_cut<kDecodeWarps>(p, total);
     first += h * tiles;
     c0 = cut.owner(first);
     n_slots = cut.owner(first + tiles - 1) - static_cast<int>(c0) + 1;

@@ -1,14 +1,26 @@
 // Accumulated attention weights of many query rows over the 8-bit cache.
 //
 // w_j += sum over the rows i that see key j of 2^(s_ij - LSE_i), with the
-// rows' LSEs (log2 units) of the forward launch ahead of this one.  The scores
-// are computed again -- a stored score costs 8 bytes of traffic, a recomputed
-// one D / 8 MMAs of the 256 keys x 8 rows -- as S^T = K Q^T with mma.sync in
-// fp16 like the few-row kernel's (its header comment has the fragments and
-// the roundings): a warp keeps the fragments of its 32 keys in registers, the
-// rows pass through shared memory 64 at a time, the next 64 being loaded
-// meanwhile.  Each key has one owner that takes the rows in order: no atomics,
-// one order of sums.  Bound by issue (MMA, exp2 and their addressing).
+// rows' LSEs (log2 units) of the forward launches ahead of this one.  The
+// scores are computed again (a stored score would cost 8 bytes of traffic),
+// keys as rows: S^T = K Q^T for 128 keys and 256 query rows at a time, by
+// tcgen05 in fp16 with the operands of the many-row forward kernel (its header
+// comment has the roundings).  A thread of the epilogue owns one key: it adds
+// up its 256 columns, so no value crosses threads, and the rows' factors and
+// LSEs are broadcast from shared memory.
+//
+// The key tiles of all (batch, K/V head) segments are cut into equal
+// consecutive shares, one per CTA.  A pass is a segment's part of the share
+// under 256 query rows: their fp16 tile stays in shared memory while the key
+// tiles stream past it.  Tile j goes to accumulator and epilogue warpgroup
+// j % 2 in every pass, so a key has one owner, which adds the passes in order:
+// no atomics, one order of sums.
+//
+// Roles (512 threads): warp 0 MMA issue, warp 1 bulk copies of raw key tiles,
+// warps 4-7 conversion of query rows and key tiles, warps 8-11 / 12-15
+// epilogue of even / odd tiles.  Every wait is bounded as in the forward
+// kernel.  Bound by the conversion's latency (about 1.7k clocks a tile; the
+// MMAs take 1.0k, the epilogue's exp2 1.0k).
 #include "attn_sync.cuh"
 #include "kv8_common.cuh"
 
@@ -16,189 +28,427 @@ namespace attn {
 namespace kv8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kKeys = 32 * (kThreads / 32);  // keys of a CTA
-constexpr int kRowsAt = 64;                  // rows in shared memory at a time
+constexpr int kThreads = 512;
+constexpr int kTN = 128;    // keys of a tile
+constexpr int kRows = 256;  // query rows of a pass
+
+template <int D>
+struct Smem {
+  static constexpr int kBox = kTN * 128;            // 128 keys x 128 bytes
+  static constexpr int kTile = kBox * (D / 64);     // one fp16 key tile
+  static constexpr int kQBox = kRows * 128;
+  static constexpr int kRaw = kTN * D;              // one raw key tile
+  static constexpr int kSlots = 3, kRawSlots = 3;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + kQBox * (D / 64);
+  static constexpr int kRawRing = kRing + kSlots * kTile;
+  static constexpr int kConst = kRawRing + kRawSlots * kRaw;
+  // Per pair of rows: both factors, both negated LSEs.
+  static constexpr int kBars = kConst + kRows * 8;
+  // raw_full, raw_empty, full, empty, q, qfree, s[2], sfree[2], drain
+  static constexpr int kNumBars = 2 * kRawSlots + 2 * kSlots + 7;
+  static constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM base, abort
+  static constexpr int kBytes = kMisc + 8;
+  static_assert(kBytes + 1024 <= 227 * 1024, "shared memory per CTA");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
+                                          uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// (x0, x1) * (m0, m1) + (a0, a1).
+__device__ __forceinline__ void ffma2_pairs(float& y0, float& y1, float x0,
+                                            float x1, float m0, float m1,
+                                            float a0, float a1) {
+  asm("{\n\t.reg .b64 x, m, a, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\t"
+      "mov.b64 a, {%6, %7};\n\t"
+      "fma.rn.ftz.f32x2 y, x, m, a;\n\t"
+      "mov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y0), "=f"(y1)
+      : "f"(x0), "f"(x1), "f"(m0), "f"(m1), "f"(a0), "f"(a1));
+}
+
+// The passes of a CTA's share, walked alike by every role: tiles [t0, t1) of
+// a segment, query rows [256 u, 256 u + 256), of which tiles [t0, hi) see
+// some.
+struct Passes {
+  Segment seg;
+  int count;         // tiles of the share
+  int t0, t1, hi;
+  int u, n_new, rows;
+
+  __device__ __forceinline__ void enter(const FwdParams& p) {
+    n_new = seq_new(p, seg.b);
+    rows = n_new * p.group;
+    t0 = max(0, -seg.pos);
+    t1 = min(seg.end, count) - seg.pos;
+    u = 0;
+    set_hi(p);
+  }
+  __device__ __forceinline__ void set_hi(const FwdParams& p) {
+    const int last = min(rows, (u + 1) * kRows) - 1;
+    hi = last < u * kRows
+             ? t0
+             : min(t1, (row_end(p, seg.len, n_new, last) + kTN - 1) / kTN);
+  }
+  __device__ __forceinline__ bool first(const FwdParams& p, int lane) {
+    count = take_share<kTN, 1>(p, static_cast<int>(blockIdx.x), lane, &seg);
+    if (count == 0) return false;
+    enter(p);
+    return hi > t0 || next(p);
+  }
+  __device__ __forceinline__ bool next(const FwdParams& p) {
+    do {
+      if ((u + 1) * kRows < rows) {
+        ++u;
+        set_hi(p);
+      } else {
+        if (seg.end >= count) return false;
+        next_segment<kTN>(p, seg);
+        enter(p);
+      }
+    } while (hi <= t0);
+    return true;
+  }
+};
 
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads, 2)
-    kv8_weights_kernel(const FwdParams p, int tiles, int lse2_rows) {
-  constexpr int kPitch = D + 8;  // halves: rows 16 bytes apart in the banks
-  constexpr int kPer = D / 8;    // threads that load a row
-  constexpr int kLoads = kRowsAt * kPer / kThreads;
-  __shared__ __align__(16) uint16_t sq[2][kRowsAt * kPitch];
-  __shared__ float s_mult[2][kRowsAt], s_lse[2][kRowsAt];
-  start_after_previous();
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_weights_kernel(const FwdParams p, int lse2_rows) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_base = ptx::smem_u32(smem);
+  const uint32_t bar_rfull = s_base + L::kBars;
+  const uint32_t bar_rempty = bar_rfull + 8 * L::kRawSlots;
+  const uint32_t bar_full = bar_rempty + 8 * L::kRawSlots;
+  const uint32_t bar_empty = bar_full + 8 * L::kSlots;
+  const uint32_t bar_q = bar_empty + 8 * L::kSlots;
+  const uint32_t bar_qfree = bar_q + 8;
+  const uint32_t bar_s = bar_qfree + 8;      // [2]
+  const uint32_t bar_sfree = bar_s + 16;     // [2]
+  const uint32_t bar_drain = bar_sfree + 16;
+  float* consts = reinterpret_cast<float*>(smem + L::kConst);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
+
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g8 = lane / 4, c = lane % 4;
-  const int bh = blockIdx.x / tiles;
-  const int tile0 = (blockIdx.x - bh * tiles) * kKeys;
-  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-  const int len = seq_len(p, b), n_new = seq_new(p, b);
-  if (tile0 >= len) return;
-  const int rows = n_new * p.group;
-  // Rows before r_first see nothing of this tile.
-  const int r_first =
-      p.causal ? max(0, tile0 - (len - n_new)) * p.group : 0;
-  const int key0 = tile0 + warp * 32;
-
-  // Fragments of keys key0 + 16 u + g8 (+ 8).
-  uint32_t a[2][D / 16][4];
-  float ks[2];
-  const uint8_t* k = p.k + static_cast<long long>(bh) * p.capacity * D;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf) {
-        const int key = key0 + 16 * u + g8 + 8 * i;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (key < len)
-          x = __ldg(reinterpret_cast<const uint4*>(
-              k + static_cast<long long>(key) * D + 64 * hf + 16 * c));
-        e4m3x4_to_half2(x.x, a[u][4 * hf][i], a[u][4 * hf][2 + i]);
-        e4m3x4_to_half2(x.y, a[u][4 * hf + 1][i], a[u][4 * hf + 1][2 + i]);
-        e4m3x4_to_half2(x.z, a[u][4 * hf + 2][i], a[u][4 * hf + 2][2 + i]);
-        e4m3x4_to_half2(x.w, a[u][4 * hf + 3][i], a[u][4 * hf + 3][2 + i]);
-      }
-    ks[u] = 0.f;
-    if (key0 + 16 * u < len)
-      ks[u] = __ldg(p.k_scale + static_cast<long long>(bh) * p.nblk +
-                    ((key0 + 16 * u) >> p.block_shift));
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const uint32_t bar = s_base + L::kBars + 8 * i;
+      // One arrival per warp of the role that fills or frees; raw loads and
+      // MMAs arrive once.
+      uint32_t count = 1;
+      if ((bar >= bar_rempty && bar < bar_empty) || bar == bar_q ||
+          (bar >= bar_sfree && bar < bar_drain))
+        count = 4;
+      if (bar == bar_qfree) count = 8;
+      ptx::mbar_init(bar, count);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
   }
+  if (warp == 0) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  start_after_previous();
 
-  // Rows r0 .. r0 + 63: this thread's chunks, and its row's LSE.
-  uint4 x[kLoads];
-  float lse[kLoads];
-  auto load_rows = [&](int r0) {
-#pragma unroll
-    for (int e = 0; e < kLoads; ++e) {
-      const int i = threadIdx.x + e * kThreads;
-      const int r = r0 + i / kPer;
-      x[e] = make_uint4(0u, 0u, 0u, 0u);
-      lse[e] = INFINITY;  // a row of no weight
-      if (r < rows) {
-        const int tok = r / p.group, hd = r - tok * p.group;
-        x[e] = __ldg(reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) +
-            ((static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq +
-             tok) * D + i % kPer * 8));
-        lse[e] = p.lse2[static_cast<long long>(bh) * lse2_rows + r];
-        if (lse[e] == -INFINITY) lse[e] = INFINITY;  // sees nothing
-      }
-    }
+  bool ok = true;
+  auto wait = [&](uint32_t bar, int phase, int role) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1, abort_flag, p,
+                                                role)) != 0;
   };
-  auto store_rows = [&](int buf) {
-#pragma unroll
-    for (int e = 0; e < kLoads; ++e) {
-      const int i = threadIdx.x + e * kThreads;
-      const int r = i / kPer, ch = i % kPer;
-      const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-      float2 f[4];
-      float amax = 0.f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f[q] = unpack2<kBF16>(in[q]);
-        amax = fmaxf(amax, fmaxf(fabsf(f[q].x), fabsf(f[q].y)));
-      }
-#pragma unroll
-      for (int s = kPer / 2; s > 0; s /= 2)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-      const int up = row_shift(amax);
-      const float f_up = exp2_int(up);
-      uint32_t out[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        out[q] = ptx::pack2<false>(f[q].x * f_up, f[q].y * f_up);
-      *reinterpret_cast<uint4*>(&sq[buf][r * kPitch + ch * 8]) =
-          make_uint4(out[0], out[1], out[2], out[3]);
-      if (ch == 0) {
-        s_mult[buf][r] = p.scale_log2 * exp2_int(-up);
-        s_lse[buf][r] = lse[e];
-      }
-    }
-  };
+  Passes w;
+  bool more = (warp < 2 || warp >= 4) && w.first(p, lane);
 
-  float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-  auto add_rows = [&](int buf, int r0, auto masked_tag) {
-    constexpr bool kMasked = decltype(masked_tag)::value;
-#pragma unroll 1
-    for (int nt = 0; nt < kRowsAt / 8; ++nt) {
-      uint32_t bw[D / 64][8];
-#pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf) {
-        const uint16_t* row =
-            &sq[buf][(8 * nt + g8) * kPitch + 64 * hf + 16 * c];
-        const uint4 w0 = *reinterpret_cast<const uint4*>(row);
-        const uint4 w1 = *reinterpret_cast<const uint4*>(row + 8);
-        bw[hf][0] = w0.x; bw[hf][1] = w0.y; bw[hf][2] = w0.z; bw[hf][3] = w0.w;
-        bw[hf][4] = w1.x; bw[hf][5] = w1.y; bw[hf][6] = w1.z; bw[hf][7] = w1.w;
-      }
-      const float2 mult =
-          *reinterpret_cast<const float2*>(&s_mult[buf][8 * nt + 2 * c]);
-      const float2 l2 =
-          *reinterpret_cast<const float2*>(&s_lse[buf][8 * nt + 2 * c]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf)
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            mma_f16((w & 1) ? s2 : s, a[u][4 * hf + w][0], a[u][4 * hf + w][1],
-                    a[u][4 * hf + w][2], a[u][4 * hf + w][3], bw[hf][2 * w],
-                    bw[hf][2 * w + 1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = (e & 1) ? mult.y : mult.x;
-          const float l = (e & 1) ? l2.y : l2.x;
-          const float w = ptx::ex2(fmaf(s[e] + s2[e], m * ks[u], -l));
-          if constexpr (kMasked) {
-            const int key = key0 + 16 * u + g8 + 8 * (e >> 1);
-            const int r = r0 + 8 * nt + 2 * c + (e & 1);
-            if (r < rows && key < row_end(p, len, n_new, r))
-              sum[u][e >> 1] += w;
-          } else {
-            sum[u][e >> 1] += w;
-          }
+  if (warp == 1) {
+    // ------------------------------------------------------ raw key tiles
+    int it = 0;
+    for (; more && ok; more = w.next(p)) {
+      const uint8_t* k =
+          p.k + (static_cast<long long>(w.seg.b) * p.Hkv + w.seg.h) *
+                    p.capacity * D;
+      for (int j = w.t0; j < w.hi && ok; ++j, ++it) {
+        const int slot = it % L::kRawSlots, use = it / L::kRawSlots;
+        if (use > 0) ok = wait(bar_rempty + 8 * slot, use - 1, 1);
+        if (!ok) break;
+        const uint32_t bytes = min(kTN, w.seg.len - j * kTN) * D;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(bar_rfull + 8 * slot, bytes);
+          bulk_load(s_base + L::kRawRing + slot * L::kRaw,
+                    k + static_cast<long long>(j) * L::kRaw, bytes,
+                    bar_rfull + 8 * slot);
         }
       }
     }
-  };
-
-  load_rows(r_first);
-  int buf = 0;
-  for (int r0 = r_first; r0 < rows; r0 += kRowsAt, buf ^= 1) {
-    store_rows(buf);
-    __syncthreads();  // one buffer is written while the other may be read
-    if (r0 + kRowsAt < rows) load_rows(r0 + kRowsAt);
-    if (key0 >= len) continue;
-    // Rows see more and more tokens: the first one decides.
-    if (key0 + 32 > row_end(p, len, n_new, r0))
-      add_rows(buf, r0, BoolTag<true>{});
-    else
-      add_rows(buf, r0, BoolTag<false>{});
-  }
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float w = sum[u][e];
-      w += __shfl_xor_sync(0xffffffffu, w, 1);
-      w += __shfl_xor_sync(0xffffffffu, w, 2);
-      const int key = key0 + 16 * u + g8 + 8 * e;
-      if (c == 0 && key < len && w != 0.f)
-        p.weights[static_cast<long long>(bh) * p.capacity + key] += w;
+    if (!ok) {  // let the copies in flight land
+      for (int i = max(0, it - L::kRawSlots); i < it; ++i)
+        drain_wait(bar_rfull + 8 * (i % L::kRawSlots),
+                   (i / L::kRawSlots) & 1, p);
     }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ---------------------------------------------------------- MMA issue
+    const uint32_t idesc = ptx::idesc_f16(false, kTN, kRows, false, false);
+    constexpr uint32_t kHi = ptx::sdesc_hi_sw128(1024);
+    const uint32_t q_lo = ptx::sdesc_lo(s_base + L::kQ, 16);
+    const uint32_t k_lo = ptx::sdesc_lo(s_base + L::kRing, 16);
+    int it = 0, pass = 0, uses[2] = {0, 0};
+    bool issued = false;
+    for (; more && ok; more = w.next(p), ++pass) {
+      ok = wait(bar_q, pass, 2);
+      // (Warp-uniform to the compiler: descriptors in uniform registers.)
+      const int j0 = __reduce_max_sync(0xffffffffu, w.t0);
+      const int j1 = __reduce_max_sync(0xffffffffu, w.hi);
+      for (int j = j0; j < j1 && ok; ++j, ++it) {
+        const int slot = it % L::kSlots, buf = j & 1;
+        ok = wait(bar_full + 8 * slot, it / L::kSlots, 2);
+        const int used = buf ? uses[1] : uses[0];
+        if (ok && used > 0) ok = wait(bar_sfree + 8 * buf, used - 1, 2);
+        if (!ok) break;
+        if (buf) ++uses[1]; else ++uses[0];
+        ptx::tc_fence_after();
+        const uint32_t a0 = k_lo + slot * (L::kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ptx::mma_ss_elect(
+              tmem + buf * kRows,
+              a0 + (((kk / 4) * L::kBox + (kk % 4) * 32) >> 4),
+              q_lo + (((kk / 4) * L::kQBox + (kk % 4) * 32) >> 4), kHi, idesc,
+              kk > 0 ? 1u : 0u);
+        ptx::tc_commit_elect(bar_s + 8 * buf);
+        ptx::tc_commit_elect(bar_empty + 8 * slot);
+        issued = true;
+      }
+    }
+    if (!ok && issued) {  // the MMAs issued end before TMEM is released
+      ptx::tc_commit_elect(bar_drain);
+      drain_wait(bar_drain, 0, p);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {
+    // --------------------------------------------------------- conversion
+    const int cw = warp - 4;
+    const int tid = cw * 32 + lane;
+    constexpr int kItems = D / 16;          // 16-byte chunks of a tile
+    constexpr int kRowStep = kTN / kItems;  // rows between them
+    int row0, ch;  // as in the forward kernel: no bank shared
+    if constexpr (D == 128) {
+      const int odd = (tid >> 2) & 1;
+      row0 = 2 * (tid / 16) + odd;
+      ch = (((tid >> 3) & 1) ^ odd) * 4 + (tid & 3);
+    } else {
+      row0 = tid / 4;
+      ch = tid % 4;
+    }
+    const uint32_t raw_off = row0 * D + ch * 16;
+    const uint32_t out_off = (ch / 4) * L::kBox + row0 * 128;
+    const uint32_t out0 = out_off + ((((ch % 4) * 2) ^ (row0 % 8)) << 4);
+    const uint32_t out1 = out_off + ((((ch % 4) * 2 + 1) ^ (row0 % 8)) << 4);
+    int it = 0, pass = 0;
+    for (; more && ok; more = w.next(p), ++pass) {
+      if (pass > 0) ok = wait(bar_qfree, pass - 1, 8);
+      if (!ok) break;
+      const int bh = w.seg.b * p.Hkv + w.seg.h;
+      // Two query rows per thread.
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int r = half * 128 + tid, row = w.u * kRows + r;
+        const bool in = row < w.rows;
+        const int tok = row / p.group, hd = row - tok * p.group;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) +
+            (in ? ((static_cast<long long>(w.seg.b) * p.Hq +
+                    w.seg.h * p.group + hd) * p.Sq + tok) * D
+                : 0));
+        float lse = INFINITY;  // no weight: rows past the last, and rows
+        if (in) {              // that see nothing
+          lse = p.lse2[static_cast<long long>(bh) * lse2_rows + row];
+          if (lse == -INFINITY) lse = INFINITY;
+        }
+        uint32_t x[D / 2];
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 y = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+          x[4 * k] = y.x;
+          x[4 * k + 1] = y.y;
+          x[4 * k + 2] = y.z;
+          x[4 * k + 3] = y.w;
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) {
+          const float2 f = unpack2<kBF16>(x[k]);
+          amax = ptx::fmax3(amax, fabsf(f.x), fabsf(f.y));
+        }
+        const int up = row_shift(amax);
+        const float f_up = exp2_int(up);
+        const uint32_t dst = s_base + L::kQ + r * 128;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          uint32_t o[4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const float2 f = unpack2<kBF16>(x[4 * k + a]);
+            o[a] = ptx::pack2<false>(f.x * f_up, f.y * f_up);
+          }
+          ptx::st_shared_v4(dst + (k / 8) * L::kQBox +
+                                (((k % 8) ^ (r % 8)) << 4),
+                            o[0], o[1], o[2], o[3]);
+        }
+        consts[(r / 2) * 4 + r % 2] = p.scale_log2 * exp2_int(-up);
+        consts[(r / 2) * 4 + 2 + r % 2] = -lse;
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_q);
+      for (int j = w.t0; j < w.hi && ok; ++j, ++it) {
+        const int rslot = it % L::kRawSlots, slot = it % L::kSlots;
+        const int valid = w.seg.len - j * kTN;  // rows that hold tokens
+        ok = wait(bar_rfull + 8 * rslot, it / L::kRawSlots, 8);
+        if (ok && it >= L::kSlots)
+          ok = wait(bar_empty + 8 * slot, it / L::kSlots - 1, 8);
+        if (!ok) break;
+        const uint32_t raw = s_base + L::kRawRing + rslot * L::kRaw + raw_off;
+        const uint32_t out = s_base + L::kRing + slot * L::kTile;
+        uint4 x[kItems];
+#pragma unroll
+        for (int e = 0; e < kItems; ++e)
+          x[e] = ptx::ld_shared_v4(raw + e * kRowStep * D);
+        if (valid < kTN) {  // rows past the length: zeros
+#pragma unroll
+          for (int e = 0; e < kItems; ++e)
+            if (row0 + e * kRowStep >= valid) x[e] = make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int e = 0; e < kItems; ++e) {
+          uint32_t h[8];
+          e4m3x4_to_half2(x[e].x, h[0], h[1]);
+          e4m3x4_to_half2(x[e].y, h[2], h[3]);
+          e4m3x4_to_half2(x[e].z, h[4], h[5]);
+          e4m3x4_to_half2(x[e].w, h[6], h[7]);
+          const uint32_t at = out + e * kRowStep * 128;
+          ptx::st_shared_v4(at + out0, h[0], h[1], h[2], h[3]);
+          ptx::st_shared_v4(at + out1, h[4], h[5], h[6], h[7]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {  // (the raw values have been used: see the forward)
+          ptx::mbar_arrive(bar_full + 8 * slot);
+          ptx::mbar_arrive(bar_rempty + 8 * rslot);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ----------------------------------------------------------- epilogue
+    const int buf = (warp - 8) / 4;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) +
+                         buf * kRows;
+    const int r = threadIdx.x % kTN;  // key of the tile
+    int pass = 0, uses = 0;
+    for (; more && ok; more = w.next(p), ++pass) {
+      ok = wait(bar_q, pass, 4);  // the rows' factors and LSEs
+      const int bh = w.seg.b * p.Hkv + w.seg.h;
+      const int first_row = w.u * kRows;
+      const int n_rows = min(kRows, w.rows - first_row);
+      const int seen = row_end(p, w.seg.len, w.n_new, first_row);
+      for (int j = w.t0; j < w.hi && ok; ++j) {
+        if ((j & 1) != buf) continue;
+        const int key = j * kTN + r;
+        const bool in = key < w.seg.len;
+        float ks = 0.f, before = 0.f;
+        float* at = p.weights + static_cast<long long>(bh) * p.capacity + key;
+        if (in) {
+          ks = __ldg(p.k_scale + static_cast<long long>(bh) * p.nblk +
+                     (key >> p.block_shift));
+          before = *at;
+        }
+        // Rows below `low` do not see the key (rows see more and more).
+        int low = 0;
+        if ((j + 1) * kTN > seen && p.causal)
+          low = max(0, (key - (w.seg.len - w.n_new))) * p.group - first_row;
+        const bool masked =
+            __any_sync(0xffffffffu, low > 0 || n_rows < kRows) != 0;
+        ok = wait(bar_s + 8 * buf, uses, 4);
+        if (!ok) break;
+        ++uses;
+        ptx::tc_fence_after();
+        float sm[4] = {0.f, 0.f, 0.f, 0.f};
+        auto add = [&](auto masked_tag) {
+          constexpr bool kMasked = decltype(masked_tag)::value;
+#pragma unroll 2
+          for (int q = 0; q < kRows / 32; ++q) {
+            uint32_t s[32];
+            ptx::tmem_ld32(t_s + 32 * q, s);
+            ptx::tmem_wait_ld();
+            const float4* c4 =
+                reinterpret_cast<const float4*>(consts) + 16 * q;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float4 k = c4[e];
+              float x0, x1;
+              ffma2_pairs(x0, x1, __uint_as_float(s[2 * e]) * ks,
+                          __uint_as_float(s[2 * e + 1]) * ks, k.x, k.y, k.z,
+                          k.w);
+              float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              if constexpr (kMasked) {
+                const int c0 = 32 * q + 2 * e;
+                if (c0 < low || c0 >= n_rows) p0 = 0.f;
+                if (c0 + 1 < low || c0 + 1 >= n_rows) p1 = 0.f;
+              }
+              if (e & 1)
+                ptx::fadd2(sm[2], sm[3], p0, p1);
+              else
+                ptx::fadd2(sm[0], sm[1], p0, p1);
+            }
+          }
+        };
+        if (masked)
+          add(BoolTag<true>{});
+        else
+          add(BoolTag<false>{});
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_sfree + 8 * buf);
+        const float sum = (sm[0] + sm[1]) + (sm[2] + sm[3]);
+        if (in && sum != 0.f) *at = before + sum;
+      }
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(bar_qfree);
+    }
+    __syncwarp();
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
 }
 
 template <int D, bool kBF16>
 cudaError_t launch(const FwdParams& p, int lse2_rows, cudaStream_t stream) {
-  const int tiles = (p.capacity - 1) / kKeys + 1;
-  return launch_pdl(kv8_weights_kernel<D, kBF16>,
-                    static_cast<long long>(p.B) * p.Hkv * tiles, kThreads, 0,
-                    stream, p, tiles, lse2_rows);
+  constexpr int kBytes = Smem<D>::kBytes + 1024;
+  const cudaError_t err = cudaFuncSetAttribute(
+      kv8_weights_kernel<D, kBF16>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kv8_weights_kernel<D, kBF16>, p.grid, kThreads, kBytes,
+                    stream, p, lse2_rows);
 }
 
 }  // namespace
