@@ -186,17 +186,22 @@ __device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
   return min(len, max(0, len - n_new + r / p.group + 1));
 }
 // The list of tiles: sequence b contributes Hkv segments of
-// ceil(lens[b] / kKeys) tiles.  (Counts fit 32 bits: a tile of one segment
-// holds 4 KB of codes.)
+// ceil(lens[b] / kKeys) tiles, and kOver empty places before each, which stand
+// for the time that a segment takes besides its tiles.  (Counts fit 32 bits:
+// a tile of one segment holds 4 KB of codes.)
+template <int kKeys, int kOver>
+__device__ __forceinline__ int places(int len) {
+  return len > 0 ? (len + kKeys - 1) / kKeys + kOver : 0;
+}
 //
-// Tiles before sequence `seq` and of all sequences, for every lane of the
+// Places before sequence `seq` and of all sequences, for every lane of the
 // calling warp.
-template <int kKeys>
+template <int kKeys, int kOver>
 __device__ __forceinline__ int list_tiles(const FwdParams& p, int seq,
                                           int lane, int* before) {
   int t = 0, pre = 0;
   for (int b = lane; b < p.B; b += 32) {
-    const int n = (seq_len(p, b) + kKeys - 1) / kKeys;
+    const int n = places<kKeys, kOver>(seq_len(p, b));
     t += n;
     if (b < seq) pre += n;
   }
@@ -209,7 +214,7 @@ __device__ __forceinline__ int list_tiles(const FwdParams& p, int seq,
   return t * p.Hkv;
 }
 
-// The cut: CTA c of n takes q tiles, the first `rest` CTAs one more.
+// The cut: CTA c of n takes q places, the first `rest` CTAs one more.
 struct Cut {
   int n, q, rest;
   __device__ __forceinline__ int first(int c) const {
@@ -220,7 +225,7 @@ struct Cut {
     return x < fat ? x / (q + 1) : rest + (x - fat) / q;
   }
 };
-// kLeast tiles a CTA, but for the last, are the finest cut.
+// kLeast places a CTA are the finest cut.
 template <int kLeast>
 __device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
   Cut c;
@@ -230,21 +235,21 @@ __device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
   return c;
 }
 
-// A segment of the list as a CTA walks its share: it covers positions
-// [pos, end) counted from the share's start (pos < 0: it began earlier).
+// A segment of the list as a CTA walks its share: its tiles lie at [pos, end)
+// counted from the share's start (pos < 0: it began earlier).
 struct Segment {
   int pos, end;
   int b, h;  // sequence, K/V head
   int len, tiles;
 };
 
-// CTA's share: its number of tiles (0: none) and first segment.
-template <int kKeys, int kLeast>
+// CTA's share: its number of places (0: none) and first segment.
+template <int kKeys, int kOver, int kLeast>
 __device__ __forceinline__ int take_share(const FwdParams& p, int cta,
                                           int lane, Segment* s) {
   int first = 0, count = 0, base = 0;
   if (p.B > 32) {
-    const int total = list_tiles<kKeys>(p, 0, lane, &base);
+    const int total = list_tiles<kKeys, kOver>(p, 0, lane, &base);
     const Cut cut = make_cut<kLeast>(p, total);
     first = cut.first(cta);
     count = cta < cut.n ? cut.first(cta + 1) - first : 0;
@@ -253,7 +258,7 @@ __device__ __forceinline__ int take_share(const FwdParams& p, int cta,
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
     const int len = b < p.B ? seq_len(p, b) : 0;
-    const int t = (len + kKeys - 1) / kKeys * p.Hkv;
+    const int t = places<kKeys, kOver>(len) * p.Hkv;
     int incl = t;
 #pragma unroll
     for (int i = 1; i < 32; i *= 2) {
@@ -274,8 +279,8 @@ __device__ __forceinline__ int take_share(const FwdParams& p, int cta,
       s->b = b0 + l;
       s->len = __shfl_sync(0xffffffffu, len, l);
       s->tiles = (s->len + kKeys - 1) / kKeys;
-      s->h = (first - before) / s->tiles;
-      s->pos = -((first - before) - s->h * s->tiles);
+      s->h = (first - before) / (s->tiles + kOver);
+      s->pos = kOver - ((first - before) - s->h * (s->tiles + kOver));
       s->end = s->pos + s->tiles;
       return count;
     }
@@ -284,9 +289,9 @@ __device__ __forceinline__ int take_share(const FwdParams& p, int cta,
   return 0;
 }
 
-template <int kKeys>
+template <int kKeys, int kOver>
 __device__ __forceinline__ void next_segment(const FwdParams& p, Segment& c) {
-  c.pos = c.end;
+  c.pos = c.end + kOver;
   if (++c.h == p.Hkv) {
     c.h = 0;
     do {  // some later sequence has tokens: the share is not at its end

@@ -38,6 +38,12 @@ namespace attn {
 namespace kv8 {
 namespace {
 
+// A segment takes a CTA time besides its tiles (2 us: query rows and scales
+// fetched, partials joined and stored).  Without empty places for it in the
+// cut, heads of short sequences that share a CTA held the whole launch up: 16
+// sequences of 0 .. 2048 tokens, 16 heads, 20-44 us by the draw; with 4 places
+// 20-22, with 12 19-20 (8 x 4096 tokens 25.0 -> 23.5, 16 or 24 about the same).
+constexpr int kOver = 12;
 constexpr float kTau = 8.f;        // lazy rescale threshold (log2 units)
 constexpr float kMinUnit = 1.17549435e-38f;  // 2^-126, the smallest block scale
 constexpr float kPScale = 128.f;   // 2^7: P <= 2^(8 + 7) < 65504
@@ -132,12 +138,19 @@ struct Loader {
   template <int kStep>
   __device__ __forceinline__ void next(const FwdParams& p, int count,
                                        int stage, int lane) {
-    if (pos < count) {
+    bool moved = false;
+    while (pos < count) {
       if (pos >= seg.end) {
-        do next_segment<kKeys>(p, seg);
-        while (pos >= seg.end);
-        set_segment(p, lane);
+        next_segment<kKeys, kOver>(p, seg);
+        moved = true;
+      } else if (pos < seg.pos) {
+        pos += kStep;
+      } else {
+        break;
       }
+    }
+    if (pos < count) {
+      if (moved) set_segment(p, lane);
       const int t = pos - seg.pos;
       const long long off = static_cast<long long>(t) * 2048;
       const uint32_t to = stage * 4096;
@@ -206,8 +219,9 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
   const int g8 = lane / 4, c = lane % 4;
   const int cta = blockIdx.x;
   Segment seg;
-  const int count = take_share<kKeys, kDecodeWarps>(p, cta, lane, &seg);
-  if (count == 0) return;
+  seg.pos = 0;
+  const int count = take_share<kKeys, kOver, kDecodeWarps>(p, cta, lane, &seg);
+  if (seg.pos >= count) return;  // (also: no share)
   const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * 4096;
   Loader<D> ld;
   ld.init(p, seg, warp, lane, ring);
@@ -299,6 +313,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
     // i: step i % kSub of tile i / kSub), fetched again when used up.
     float ks_all = 0.f, vs_all = 0.f;
     int held = 32 / kSub;  // tiles of the fetched ones that are used up
+    while (pos < seg.pos) pos += kWarps;
     for (; pos < seg_last; pos += kWarps) {
       if (held == 32 / kSub) {
         const int key =
@@ -540,7 +555,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
       p.part_ml[slot * kRows + r] = make_float2(mx, sum);
     }
     if (seg.end >= count) break;
-    next_segment<kKeys>(p, seg);
+    next_segment<kKeys, kOver>(p, seg);
+    if (seg.pos >= count) break;
   }
 }
 
@@ -636,9 +652,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
   int n_slots = 0;
   if (tiles > 0 && !idle) {
     int first;
-    const int total = list_tiles<kKeys>(p, b, lane, &first);
+    const int total = list_tiles<kKeys, kOver>(p, b, lane, &first);
     const Cut cut = make_cut<kDecodeWarps>(p, total);
-    first += h * tiles;
+    first += h * (tiles + kOver) + kOver;
     c0 = cut.owner(first);
     n_slots = cut.owner(first + tiles - 1) - static_cast<int>(c0) + 1;
   }

@@ -98,7 +98,7 @@ struct Passes {
              : min(t1, (row_end(p, seg.len, n_new, last) + kTN - 1) / kTN);
   }
   __device__ __forceinline__ bool first(const FwdParams& p, int lane) {
-    count = take_share<kTN, 1>(p, static_cast<int>(blockIdx.x), lane, &seg);
+    count = take_share<kTN, 0, 1>(p, static_cast<int>(blockIdx.x), lane, &seg);
     if (count == 0) return false;
     enter(p);
     return hi > t0 || next(p);
@@ -110,7 +110,7 @@ struct Passes {
         set_hi(p);
       } else {
         if (seg.end >= count) return false;
-        next_segment<kTN>(p, seg);
+        next_segment<kTN, 0>(p, seg);
         enter(p);
       }
     } while (hi <= t0);
