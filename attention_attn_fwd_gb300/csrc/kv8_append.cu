@@ -6,7 +6,8 @@
 // codes: each input element is read once and each code written once.  A block
 // begun by an earlier call whose scale has to grow also has its held codes
 // read, shifted to the new scale and written back.  Powers of two make both
-// the division by the scale and the requantisation of normal codes exact, so
+// the product with the scale's reciprocal and the requantisation of
+// normal codes exact, so
 // the only rounding is the one to E4M3.
 //
 // Bound by memory traffic (2 bytes in, 1 out per element) on prompts and by
@@ -24,11 +25,12 @@ __host__ __device__ constexpr int unit_threads() {
 }
 
 template <int D, int kBlock, bool kBF16>
-__global__ void __launch_bounds__(unit_threads<D, kBlock>())
+__global__ void __launch_bounds__(unit_threads<D, kBlock>(),
+                                  896 / unit_threads<D, kBlock>())
     kv8_append_kernel(const AppendParams p) {
   constexpr int kThreads = unit_threads<D, kBlock>();
   constexpr int kWarps = kThreads / 32;
-  constexpr int kPerRow = D / 8;                        // 16-byte chunks
+  constexpr int kPerRow = D / 16;                       // 16-element chunks
   constexpr int kChunks = kBlock * kPerRow / kThreads;  // per thread
   static_assert(kChunks * kThreads == kBlock * kPerRow, "whole chunks");
   __shared__ float red[kWarps];
@@ -56,26 +58,31 @@ __global__ void __launch_bounds__(unit_threads<D, kBlock>())
   uint8_t* code = p.code[kv] + static_cast<long long>(bh) * p.capacity * D;
   float* scale = p.scale[kv] + static_cast<long long>(bh) * p.nblk + blk;
 
-  uint4 in[kChunks];
+  uint4 in[kChunks][2];
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
     const int c = threadIdx.x + i * kThreads;
     const int tok = base + c / kPerRow;
-    in[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tok >= t0 && tok < t1)
-      in[i] = __ldg(reinterpret_cast<const uint4*>(
-          x + static_cast<long long>(tok) * D + (c % kPerRow) * 8));
-  }
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack2<kBF16>(w[e]);
-      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+    in[i][0] = in[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (tok >= t0 && tok < t1) {
+      const uint4* at = reinterpret_cast<const uint4*>(
+          x + static_cast<long long>(tok) * D + (c % kPerRow) * 16);
+      in[i][0] = __ldg(at);
+      in[i][1] = __ldg(at + 1);
     }
   }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t w[4] = {in[i][q].x, in[i][q].y, in[i][q].z, in[i][q].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack2<kBF16>(w[e]);
+        amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+      }
+    }
 #pragma unroll
   for (int s = 16; s > 0; s /= 2)
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
@@ -95,38 +102,37 @@ __global__ void __launch_bounds__(unit_threads<D, kBlock>())
   const float now = keep ? old : exp2_int(e);
   if (threadIdx.x == 0 && !keep) *scale = now;
 
-  // 1 / now is exact for the powers of two this library writes; a kept
-  // scale of other origin divides.
-  const bool pow2 = (__float_as_int(now) & 0x7fffff) == 0;
-  const float inv = 1.f / now;
+  // Exact for the powers of two this library writes; with a kept scale of
+  // other origin the quotient is off by an fp32 rounding or two.
+  const float inv = reciprocal(now);
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
     const int c = threadIdx.x + i * kThreads;
     const int tok = base + c / kPerRow;
     if (tok < t0 || tok >= t1) continue;
-    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-    float f[8];
+    uint32_t out[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 v = unpack2<kBF16>(w[j]);
-      f[2 * j] = v.x;
-      f[2 * j + 1] = v.y;
-    }
-    if (pow2) {
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t w[4] = {in[i][q].x, in[i][q].y, in[i][q].z, in[i][q].w};
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = unpack2<kBF16>(w[j]);
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= inv;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] / now;
+      out[2 * q] = ptx::pack4_e4m3(f[0], f[1], f[2], f[3]);
+      out[2 * q + 1] = ptx::pack4_e4m3(f[4], f[5], f[6], f[7]);
     }
-    const uint2 out = make_uint2(ptx::pack4_e4m3(f[0], f[1], f[2], f[3]),
-                                 ptx::pack4_e4m3(f[4], f[5], f[6], f[7]));
-    *reinterpret_cast<uint2*>(code + static_cast<long long>(tok) * D +
-                              (c % kPerRow) * 8) = out;
+    *reinterpret_cast<uint4*>(code + static_cast<long long>(tok) * D +
+                              (c % kPerRow) * 16) =
+        make_uint4(out[0], out[1], out[2], out[3]);
   }
   if (begun && !keep) {
     // The block's scale grew: the codes it holds move to the new one.
-    for (int c = threadIdx.x; c < (start - base) * kPerRow; c += kThreads) {
+    for (int c = threadIdx.x; c < (start - base) * (D / 8); c += kThreads) {
       uint2* at = reinterpret_cast<uint2*>(
           code + static_cast<long long>(base) * D + c * 8);
       const uint2 held = *at;

@@ -342,7 +342,7 @@ __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
     }
     for (int i = 0; i < threads / 32; ++i) amax = fmaxf(amax, red[i]);
     const float now = exp2_int(tight_exponent(amax));
-    const float inv = 1.f / now;
+    const float inv = reciprocal(now);
     if (threadIdx.x == 0 && nb < blocks) dst_scale[nb] = whole ? first : now;
 #pragma unroll
     for (int i = 0; i < kMax; ++i) {

@@ -296,8 +296,9 @@ size_t attn_bwd_workspace_bytes(int B, int Hq, int Sq);
  * k, v       device, [B, Hkv, capacity, D] one byte per element, 16-byte
  *            aligned;
  * k_scale, v_scale  device fp32 [B, Hkv, ceil(capacity / block)], 4-byte
- *            aligned; finite and > 0 for every block that holds a token
- *            (attn_kv8_append and attn_kv8_evict write powers of two);
+ *            aligned; positive normal numbers for every block that holds a
+ *            token (attn_kv8_append and attn_kv8_evict write powers of two,
+ *            2^-126 to 2^120);
  * lens       device int32 [B]: tokens of sequence b in the cache, the new
  *            tokens of the current step included, 0 <= lens[b] <= capacity.
  *            One array may serve the caches of all layers; no function
@@ -336,8 +337,10 @@ typedef struct {
  * a <= 448 * scale; else its scale becomes tight(a) and the codes it holds
  * are requantised, round(code * old / new) -- with powers of two an exponent
  * shift, exact unless the result is subnormal.  New codes are
- * round(x / scale): to nearest, ties to even; infinities become +-448, NaN
- * stays NaN.  Nothing else of the cache is written.  Deterministic.
+ * round(x / scale): to nearest, ties to even (a scale of other origin: after
+ * the fp32 rounding of x times its reciprocal); infinities become +-448, NaN
+ * stays NaN.  Nothing else of the cache is written.  Sq <= capacity.
+ * Deterministic.
  */
 attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
                               const void* V, int Sq, const int* new_lens,
