@@ -37,15 +37,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kKeysAt = 16;         // most keys a thread holds
+constexpr int kQuadsAt = 4;         // most quads of keys a thread holds
 
 // Shared memory of a select CTA that peers read.
 struct Shared {
   int hist[2][256];      // of the digit, double-buffered
   int sum[256];          // the same, of the whole cluster
   int2 count;            // kept for certain, equal to the threshold
-  int2 warp[kKeysAt * kSelWarps];  // the same, per 32 places in order
-  int2 group[kKeysAt];             // per 1024
+  int2 warp[kQuadsAt * kSelWarps];  // the same, before each 128 places
+  int2 group[kQuadsAt];             // per 4096
   unsigned digit;
   int left;
 };
@@ -59,10 +59,10 @@ __device__ __forceinline__ void cluster_barrier() {
   ptx::cluster_wait_acquire();
 }
 
-// kPer: keys a thread holds; place i of thread t is a0 + 1024 i + t of the
-// CTA's part.  Parts of more than 1024 kPer tokens are walked in turns of that
-// many, their keys read again in each pass.
-template <int kPer>
+// kQuads: quads of keys a thread holds; element e of quad i of thread t is
+// place 4 (1024 i + t) + e of the CTA's part.  Longer parts are walked in
+// turns of 4096 kQuads places, their keys read again in each pass.
+template <int kQuads>
 __global__ void __launch_bounds__(kSelThreads, 1)
     kv8_select_kernel(const EvictParams p, int ranks) {
   __shared__ Shared sh;
@@ -81,16 +81,34 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   const float* w = p.weights + static_cast<long long>(bh) * p.src_capacity;
   const int cand = len - p.recent;        // candidates: places [0, cand)
   const int want = p.keep - p.recent;     // of which so many stay
-  constexpr int kTurn = kSelThreads * kPer;
-  const int part = (len + ranks - 1) / ranks;
+  constexpr int kTurn = 4 * kSelThreads * kQuads;
+  const int part = ((len + ranks - 1) / ranks + 3) / 4 * 4;
   const int a0 = min(len, rank * part), a1 = min(len, a0 + part);
+  const int c1 = min(a1, cand);  // candidates of this CTA: [a0, c1)
   const int turns = (part + kTurn - 1) / kTurn;
-  uint32_t key[kPer];
+  const bool aligned = (reinterpret_cast<uintptr_t>(w + a0) & 15) == 0;
+  uint32_t key[kQuads][4];
   auto load = [&](int at) {  // the turn that begins at place `at`
+    float4 x[kQuads];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int j = at + i * kSelThreads + threadIdx.x;
-      key[i] = j < a1 && j < cand ? weight_key(__ldg(w + j)) : 0u;
+    for (int i = 0; i < kQuads; ++i) {
+      const int j = at + 4 * (i * kSelThreads + threadIdx.x);
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (aligned && j + 4 <= c1) {
+        x[i] = __ldg(reinterpret_cast<const float4*>(w + j));
+      } else {
+        if (j < c1) x[i].x = __ldg(w + j);
+        if (j + 1 < c1) x[i].y = __ldg(w + j + 1);
+        if (j + 2 < c1) x[i].z = __ldg(w + j + 2);
+        if (j + 3 < c1) x[i].w = __ldg(w + j + 3);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      key[i][0] = weight_key(x[i].x);
+      key[i][1] = weight_key(x[i].y);
+      key[i][2] = weight_key(x[i].z);
+      key[i][3] = weight_key(x[i].w);
     }
   };
   load(a0);
@@ -105,11 +123,13 @@ __global__ void __launch_bounds__(kSelThreads, 1)
       const int at = a0 + t * kTurn;
       if (turns > 1) load(at);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int j = at + i * kSelThreads + threadIdx.x;
-        if (j < a1 && j < cand && (key[i] & mask) == prefix)
-          atomicAdd(&sh.hist[buf][(key[i] >> shift) & 255u], 1);
-      }
+      for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = at + 4 * (i * kSelThreads + threadIdx.x) + e;
+          if (j < c1 && (key[i][e] & mask) == prefix)
+            atomicAdd(&sh.hist[buf][(key[i][e] >> shift) & 255u], 1);
+        }
     }
     if (ranks > 1)
       cluster_barrier();
@@ -165,25 +185,42 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   }
   // Kept: keys above the threshold, the first `left` tokens of its very key,
   // and the recent ones.
-  auto flags = [&](int at, int i, unsigned* above, unsigned* equal) {
-    const int j = at + i * kSelThreads + threadIdx.x;
-    const bool c = j < cand && j < a1 && want > 0;
-    *above = __ballot_sync(0xffffffffu, (j >= cand && j < a1) ||
-                                            (c && key[i] > prefix));
-    *equal = __ballot_sync(0xffffffffu, c && key[i] == prefix);
+  // Bits e: element e of quad i is above the threshold (or recent); bits
+  // 4 + e: equal to it.
+  auto flags = [&](int at, int i) {
+    unsigned f = 0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = at + 4 * (i * kSelThreads + threadIdx.x) + e;
+      const bool c = j < c1 && want > 0;
+      if ((j >= cand && j < a1) || (c && key[i][e] > prefix)) f |= 1u << e;
+      if (c && key[i][e] == prefix) f |= 16u << e;
+    }
+    return f;
   };
-  // Counts per 32 places in the order of places, and their sums before.
+  // Kept for certain (low half) and equal (high half) before this thread's
+  // quads among its warp's 128 places; sh.warp: before those in the turn.
+  unsigned lower[kQuads];
   auto count = [&](int at) -> int2 {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      unsigned a, q;
-      flags(at, i, &a, &q);
-      if (lane == 0)
-        sh.warp[i * kSelWarps + warp] = make_int2(__popc(a), __popc(q));
+    for (int i = 0; i < kQuads; ++i) {
+      const unsigned f = flags(at, i);
+      const unsigned x = __popc(f & 15u) | (__popc(f >> 4) << 16);
+      unsigned incl = x;
+#pragma unroll
+      for (int s = 1; s < 32; s *= 2) {
+        const unsigned up = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += up;
+      }
+      lower[i] = incl - x;
+      if (lane == 31)
+        sh.warp[i * kSelWarps + warp] =
+            make_int2(static_cast<int>(incl & 0xffffu),
+                      static_cast<int>(incl >> 16));
     }
     __syncthreads();
     int2 x = make_int2(0, 0), incl = x;
-    if (warp < kPer) {  // warp i: the 32 counts of place group i
+    if (warp < kQuads) {  // warp i: the 32 counts of quad i
       x = incl = sh.warp[warp * kSelWarps + lane];
 #pragma unroll
       for (int s = 1; s < 32; s *= 2) {
@@ -199,12 +236,12 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     __syncthreads();
     int2 total = make_int2(0, 0), before = total;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < kQuads; ++i) {
       if (i == warp) before = total;
       total.x += sh.group[i].x;
       total.y += sh.group[i].y;
     }
-    if (warp < kPer)
+    if (warp < kQuads)
       sh.warp[warp * kSelWarps + lane] = make_int2(
           before.x + incl.x - x.x, before.y + incl.y - x.y);
     __syncthreads();
@@ -235,17 +272,20 @@ __global__ void __launch_bounds__(kSelThreads, 1)
       n = count(at);
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      unsigned a, q;
-      flags(at, i, &a, &q);
-      const unsigned lower = (1u << lane) - 1u;
+    for (int i = 0; i < kQuads; ++i) {
+      const unsigned f = flags(at, i);
       const int2 pre = sh.warp[i * kSelWarps + warp];
-      const int eq_rank = equal + pre.y + __popc(q & lower);
-      const bool kept =
-          ((a >> lane) & 1u) || (((q >> lane) & 1u) && eq_rank < left);
-      if (kept)
-        idx[above + pre.x + __popc(a & lower) + min(eq_rank, left)] =
-            at + i * kSelThreads + threadIdx.x;
+      int a = above + pre.x + static_cast<int>(lower[i] & 0xffffu);
+      int q = equal + pre.y + static_cast<int>(lower[i] >> 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool is_eq = (f >> (4 + e)) & 1u;
+        if (((f >> e) & 1u) || (is_eq && q < left))
+          idx[a + min(q, left)] =
+              at + 4 * (i * kSelThreads + threadIdx.x) + e;
+        a += (f >> e) & 1u;
+        q += is_eq;
+      }
     }
     above += n.x;
     equal += n.y;
@@ -488,9 +528,9 @@ cudaError_t launch_evict(int D, const EvictParams& p, cudaStream_t stream) {
   const long long grid = static_cast<long long>(p.B) * p.Hkv * ranks;
   const cudaError_t err =
       p.src_capacity <= ranks * 4 * kSelThreads
-          ? launch_cluster(kv8_select_kernel<4>, grid, kSelThreads, 0, ranks,
+          ? launch_cluster(kv8_select_kernel<1>, grid, kSelThreads, 0, ranks,
                            stream, p, ranks)
-          : launch_cluster(kv8_select_kernel<kKeysAt>, grid, kSelThreads, 0,
+          : launch_cluster(kv8_select_kernel<kQuadsAt>, grid, kSelThreads, 0,
                            ranks, stream, p, ranks);
   if (err != cudaSuccess) return err;
   return D == 64 ? launch_move<64>(p, stream) : launch_move<128>(p, stream);
