@@ -627,6 +627,13 @@ class KV8Cache:
         self.k_scale, self.v_scale, self.lens = k_scale, v_scale, lens
         self.B, self.Hkv, self.capacity, self.D = B, Hkv, capacity, D
         self.block, self.device = block, k.device
+        # What every call needs, looked up once: a decoding step of a small
+        # model waits for the host.
+        self.dtypes = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16}
+        self.int32, self.float32 = torch.int32, torch.float32
+        self.lib, self.index = load_library(), k.device.index
+        self.current_device = torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.struct = ctypes.pointer(_KV8(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), lens.data_ptr(), B, Hkv, capacity, D, block))
@@ -649,32 +656,42 @@ class KV8Cache:
 
 def _check_tensor(name, t, shape, dtype, device):
     """A contiguous tensor of this shape and type on this device."""
-    if t.shape != shape or (dtype is not None and t.dtype != dtype):
+    if t.shape == shape and t.dtype == dtype and t.device == device and \
+            t.is_contiguous():
+        return
+    if t.shape != shape or t.dtype != dtype:
         raise AttnError("%s must be %s of %s, got %s of %s" % (
-            name, list(shape), dtype or "float16 or bfloat16",
-            list(t.shape), t.dtype), ATTN_ERR_INVALID_ARG)
-    if t.device != device or not t.is_contiguous():
-        raise AttnError("%s must be a contiguous tensor on the cache's device"
-                        % name, ATTN_ERR_INVALID_ARG)
+            name, list(shape), dtype, list(t.shape), t.dtype),
+            ATTN_ERR_INVALID_ARG)
+    raise AttnError("%s must be a contiguous tensor on the cache's device"
+                    % name, ATTN_ERR_INVALID_ARG)
 
 
-def _kv8_call(name, cache, stream, *args):
+def _kv8_dtype(cache, name, t):
+    """Code of a 4-D float16 or bfloat16 tensor's element type."""
+    dt = cache.dtypes.get(t.dtype)
+    if dt is None:
+        raise AttnError("%s must be float16 or bfloat16, got %s"
+                        % (name, t.dtype), ATTN_ERR_INVALID_ARG)
+    if t.dim() != 4:
+        raise AttnError("%s must be 4-D [B, H, Sq, D]" % name,
+                        ATTN_ERR_INVALID_ARG)
+    return dt
+
+
+def _kv8_call(name, f, cache, stream, *args):
     """Calls a C entry point with ``cache``'s device current, on ``stream``
-    or torch's current stream there.  (A decoding step of a small model waits
-    for the host: switching devices is skipped where none is needed, and the
-    stream's handle is taken without building a Stream object.)"""
-    import torch
-    index = cache.device.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
+    or torch's current stream there.  (Switching devices is skipped where
+    none is needed, and the stream's handle is taken without building a
+    Stream object.)"""
+    handle = (cache.raw_stream(cache.index) if stream is None
+              else stream.cuda_stream) or None
+    if cache.current_device() == cache.index:
+        st = f(cache.struct, *args, handle)
     else:
-        handle = stream.cuda_stream
-    f = getattr(_lib or load_library(), name)
-    if torch.cuda.current_device() == index:
-        st = f(cache.struct, *args, handle or None)
-    else:
-        with torch.cuda.device(index):
-            st = f(cache.struct, *args, handle or None)
+        import torch
+        with torch.cuda.device(cache.index):
+            st = f(cache.struct, *args, handle)
     if st != ATTN_OK:
         raise AttnError("%s: %s" % (name, attn_status_string(st)), st)
 
@@ -687,20 +704,16 @@ def kv8_append(cache, k, v, new_lens=None, stream=None):
     ``new_lens`` (int32 [B]) lens - new_lens .. lens - 1 in the first
     new_lens rows.  ``cache.lens`` already counts them and is not changed.
     """
-    import torch
-    dt = _dtype_code(k)
-    if k.dim() != 4:
-        raise AttnError("k must be 4-D [B, Hkv, Sq, D]", ATTN_ERR_INVALID_ARG)
-    Sq = k.shape[2]
+    dt = _kv8_dtype(cache, "k", k)
+    dev, dtype, Sq = cache.device, k.dtype, k.shape[2]
     shape = (cache.B, cache.Hkv, Sq, cache.D)
-    _check_tensor("k", k, shape, None, cache.device)
-    _check_tensor("v", v, shape, k.dtype, cache.device)
+    _check_tensor("k", k, shape, dtype, dev)
+    _check_tensor("v", v, shape, dtype, dev)
     if new_lens is not None:
-        _check_tensor("new_lens", new_lens, (cache.B,), torch.int32,
-                      cache.device)
-    _kv8_call("attn_kv8_append", cache, stream, k.data_ptr() or None,
-              v.data_ptr() or None, Sq,
-              new_lens.data_ptr() if new_lens is not None else None, dt)
+        _check_tensor("new_lens", new_lens, (cache.B,), cache.int32, dev)
+        new_lens = new_lens.data_ptr()
+    _kv8_call("attn_kv8_append", cache.lib.attn_kv8_append, cache, stream,
+              k.data_ptr() or None, v.data_ptr() or None, Sq, new_lens, dt)
 
 
 def kv8_workspace(cache, Hq, Sq, weights=False):
@@ -726,38 +739,41 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     receives, summed over rows and the group's heads, is added to it.
     ``workspace``: from ``kv8_workspace``, allocated when not given.
     """
-    import torch
-    dt = _dtype_code(q)
-    if q.dim() != 4:
-        raise AttnError("q must be 4-D [B, Hq, Sq, D]", ATTN_ERR_INVALID_ARG)
-    B, Hq, Sq, D = shape = q.shape
-    dev = cache.device
-    _check_tensor("q", q, (cache.B, Hq, Sq, cache.D), None, dev)
-    if new_lens is not None:
-        _check_tensor("new_lens", new_lens, (B,), torch.int32, dev)
-    if weights is not None:
-        _check_tensor("weights", weights, (B, cache.Hkv, cache.capacity),
-                      torch.float32, dev)
+    dt = _kv8_dtype(cache, "q", q)
+    dev, dtype, B = cache.device, q.dtype, cache.B
+    _, Hq, Sq, _ = q.shape
+    shape = (B, Hq, Sq, cache.D)
+    _check_tensor("q", q, shape, dtype, dev)
     if out is None:
+        import torch
         out = torch.empty_like(q)
     else:
-        _check_tensor("out", out, shape, q.dtype, dev)
+        _check_tensor("out", out, shape, dtype, dev)
     if not need_lse:
         lse = None
     elif lse is None:
+        import torch
         lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
     else:
-        _check_tensor("lse", lse, (B, Hq, Sq), torch.float32, dev)
+        _check_tensor("lse", lse, (B, Hq, Sq), cache.float32, dev)
     if workspace is None:
         workspace = kv8_workspace(cache, Hq, Sq, weights is not None)
+    elif not workspace.is_contiguous():
+        raise AttnError("workspace must be contiguous", ATTN_ERR_INVALID_ARG)
+    if new_lens is not None:
+        _check_tensor("new_lens", new_lens, (B,), cache.int32, dev)
+        new_lens = new_lens.data_ptr()
+    if weights is not None:
+        _check_tensor("weights", weights, (B, cache.Hkv, cache.capacity),
+                      cache.float32, dev)
+        weights = weights.data_ptr()
     if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    _kv8_call("attn_kv8_fwd", cache, stream, q.data_ptr() or None,
-              out.data_ptr() or None,
-              lse.data_ptr() if lse is not None else None,
-              weights.data_ptr() if weights is not None else None, Hq, Sq,
-              new_lens.data_ptr() if new_lens is not None else None, scale,
-              bool(causal), dt, workspace.data_ptr(), workspace.nbytes)
+        scale = cache.D ** -0.5
+    _kv8_call("attn_kv8_fwd", cache.lib.attn_kv8_fwd, cache, stream,
+              q.data_ptr() or None, out.data_ptr() or None,
+              lse.data_ptr() if lse is not None else None, weights, Hq, Sq,
+              new_lens, scale, bool(causal), dt, workspace.data_ptr(),
+              workspace.nbytes)
     return out, lse
 
 
@@ -800,7 +816,8 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
         indices = torch.empty(shape, dtype=torch.int32, device=dev)
     else:
         _check_tensor("indices", indices, shape, torch.int32, dev)
-    _kv8_call("attn_kv8_evict", cache, stream, out.struct,
+    _kv8_call("attn_kv8_evict", cache.lib.attn_kv8_evict, cache, stream,
+              out.struct,
               weights.data_ptr() or None, out_weights.data_ptr() or None,
               keep, recent, indices.data_ptr() or None)
     return out, out_weights, indices

@@ -50,7 +50,7 @@ size_t scale_bytes(const attn_kv8_t& c) {
   return heads(c) * blocks(c) * 4;
 }
 
-// Sizes of a cache (its pointers are checked by check_cache_memory).
+// Sizes of a cache.
 attn_status_t check_cache_sizes(const attn_kv8_t* c) {
   if (c == nullptr) return ATTN_ERR_INVALID_ARG;
   if (c->B < 0 || c->Hkv <= 0 || c->capacity <= 0 || c->D <= 0 ||
@@ -66,23 +66,26 @@ attn_status_t check_cache_sizes(const attn_kv8_t* c) {
   return ATTN_OK;
 }
 
-attn_status_t check_cache_memory(const attn_kv8_t& c, int dev) {
+// NULL and misaligned pointers (found without a device).
+attn_status_t check_cache_pointers(const attn_kv8_t& c) {
   const void* p[] = {c.k, c.v, c.k_scale, c.v_scale, c.lens};
   for (const void* x : p)
     if (x == nullptr) return ATTN_ERR_INVALID_ARG;
   if (misaligned(c.k, 16) || misaligned(c.v, 16) || misaligned(c.k_scale, 4) ||
       misaligned(c.v_scale, 4) || misaligned(c.lens, 4))
     return ATTN_ERR_ALIGNMENT;
-  for (const void* x : p)
-    if (!attn::on_device(x, dev)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
-// Optional int32 array of B counts.
-attn_status_t check_counts(const int* p, int dev) {
-  if (p == nullptr) return ATTN_OK;
-  if (misaligned(p, 4)) return ATTN_ERR_ALIGNMENT;
-  return attn::on_device(p, dev) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+// Every non-NULL pointer is memory of the current device.
+bool all_on_device(const attn_kv8_t& c, const void* const* more, int count,
+                   int dev) {
+  const void* p[] = {c.k, c.v, c.k_scale, c.v_scale, c.lens};
+  for (const void* x : p)
+    if (!attn::on_device(x, dev)) return false;
+  for (int i = 0; i < count; ++i)
+    if (more[i] != nullptr && !attn::on_device(more[i], dev)) return false;
+  return true;
 }
 
 // How the query rows of a K/V head are worked on: up to 16 by the decode
@@ -153,16 +156,11 @@ attn_status_t append_impl(const attn_kv8_t* c, const void* K, const void* V,
     return ATTN_ERR_INVALID_ARG;
   if (c->B == 0 || Sq == 0) return ATTN_OK;
   if (Sq > c->capacity) return ATTN_ERR_INVALID_ARG;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
-  st = check_cache_memory(*c, dev);
+  st = check_cache_pointers(*c);
   if (st != ATTN_OK) return st;
   if (K == nullptr || V == nullptr) return ATTN_ERR_INVALID_ARG;
-  if (misaligned(K, 16) || misaligned(V, 16)) return ATTN_ERR_ALIGNMENT;
-  if (!attn::on_device(K, dev) || !attn::on_device(V, dev))
-    return ATTN_ERR_INVALID_ARG;
-  st = check_counts(new_lens, dev);
-  if (st != ATTN_OK) return st;
+  if (misaligned(K, 16) || misaligned(V, 16) || misaligned(new_lens, 4))
+    return ATTN_ERR_ALIGNMENT;
   const size_t x_bytes = heads(*c) * Sq * c->D * 2;
   const Range in[] = {{K, x_bytes},
                       {V, x_bytes},
@@ -175,6 +173,10 @@ attn_status_t append_impl(const attn_kv8_t* c, const void* K, const void* V,
   for (int i = 0; i < 4; ++i)
     if (any_overlap(out[i], in, 4) || any_overlap(out[i], out + i + 1, 3 - i))
       return ATTN_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  const void* mem[] = {K, V, new_lens};
+  if (!all_on_device(*c, mem, 3, dev)) return ATTN_ERR_INVALID_ARG;
   attn::kv8::AppendParams p{};
   p.code[0] = static_cast<uint8_t*>(c->k);
   p.code[1] = static_cast<uint8_t*>(c->v);
@@ -212,6 +214,14 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
       (dtype != ATTN_F16 && dtype != ATTN_BF16))
     return ATTN_ERR_INVALID_ARG;
   if (c->B == 0 || Sq == 0) return ATTN_OK;
+  st = check_cache_pointers(*c);
+  if (st != ATTN_OK) return st;
+  if (Q == nullptr || O == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(LSE, 4) ||
+      misaligned(weights, 4) || misaligned(new_lens, 4))
+    return ATTN_ERR_ALIGNMENT;
+  if (workspace == nullptr || misaligned(workspace, kWorkspaceAlign))
+    return ATTN_ERR_ALIGNMENT;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
   const int sms = attn::device_sms(dev);
@@ -222,19 +232,6 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   const long long tiles = (c->capacity - 1LL) / kKeyTile + 1;
   if (rp.rows > 0x7fffffffLL - 1024 || segs > 0x7fffffffLL / (16 + tiles))
     return ATTN_ERR_INVALID_ARG;
-  st = check_cache_memory(*c, dev);
-  if (st != ATTN_OK) return st;
-  if (Q == nullptr || O == nullptr) return ATTN_ERR_INVALID_ARG;
-  if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(LSE, 4) ||
-      misaligned(weights, 4))
-    return ATTN_ERR_ALIGNMENT;
-  if (workspace == nullptr || misaligned(workspace, kWorkspaceAlign))
-    return ATTN_ERR_ALIGNMENT;
-  const void* mem[] = {Q, O, LSE, weights, workspace};
-  for (const void* x : mem)
-    if (x != nullptr && !attn::on_device(x, dev)) return ATTN_ERR_INVALID_ARG;
-  st = check_counts(new_lens, dev);
-  if (st != ATTN_OK) return st;
   const Workspace w = workspace_layout(c->B, c->Hkv, c->capacity, c->D, rp,
                                        weights != nullptr);
   if (workspace_bytes < w.total) return ATTN_ERR_INVALID_ARG;
@@ -251,6 +248,8 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   for (int i = 0; i < 4; ++i)
     if (any_overlap(out[i], in, 7) || any_overlap(out[i], out + i + 1, 3 - i))
       return ATTN_ERR_INVALID_ARG;
+  const void* mem[] = {Q, O, LSE, weights, workspace, new_lens};
+  if (!all_on_device(*c, mem, 6, dev)) return ATTN_ERR_INVALID_ARG;
   attn::kv8::FwdParams p{};
   p.k = static_cast<const uint8_t*>(c->k);
   p.v = static_cast<const uint8_t*>(c->v);
@@ -320,20 +319,15 @@ attn_status_t evict_impl(const attn_kv8_t* src, const attn_kv8_t* dst,
   if (2LL * src->B * src->Hkv *
           ((keep - 1) / src->block + dst->capacity / 128 + 16) > 0x7fffffffLL)
     return ATTN_ERR_INVALID_ARG;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
-  st = check_cache_memory(*src, dev);
+  st = check_cache_pointers(*src);
   if (st != ATTN_OK) return st;
-  st = check_cache_memory(*dst, dev);
+  st = check_cache_pointers(*dst);
   if (st != ATTN_OK) return st;
   if (weights == nullptr || dst_weights == nullptr || indices == nullptr)
     return ATTN_ERR_INVALID_ARG;
   if (misaligned(weights, 4) || misaligned(dst_weights, 4) ||
       misaligned(indices, 4))
     return ATTN_ERR_ALIGNMENT;
-  if (!attn::on_device(weights, dev) || !attn::on_device(dst_weights, dev) ||
-      !attn::on_device(indices, dev))
-    return ATTN_ERR_INVALID_ARG;
   const bool in_place = src->k == dst->k && src->v == dst->v &&
                         src->k_scale == dst->k_scale &&
                         src->v_scale == dst->v_scale;
@@ -366,6 +360,11 @@ attn_status_t evict_impl(const attn_kv8_t* src, const attn_kv8_t* dst,
   // Distinct sources, too: K must not be V.
   for (int j = 0; j < 6; ++j)
     if (any_overlap(in[j], in + j + 1, 5 - j)) return ATTN_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  const void* mem[] = {dst->k,       dst->v, dst->k_scale, dst->v_scale,
+                       dst->lens, weights, dst_weights,  indices};
+  if (!all_on_device(*src, mem, 8, dev)) return ATTN_ERR_INVALID_ARG;
   attn::kv8::EvictParams p{};
   p.src_code[0] = static_cast<const uint8_t*>(src->k);
   p.src_code[1] = static_cast<const uint8_t*>(src->v);

@@ -320,6 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
+  // Tensor memory is taken behind the wait for the kernel ahead (which may
+  // still have to take its own) and before the one behind may start.
+  ptx::griddep_wait();
   if (warp == 0) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  start_after_previous();
+  ptx::griddep_launch_dependents();
 
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase, int role) {
@@ -916,14 +919,15 @@ __global__ void __launch_bounds__(kMergeThreads)
                          : at + 2LL * (s0 + lane) * kUnitRows];
     const float f_all = ptx::ex2(ml.x - mx);
     const int n = min(32, parts - s0);
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < n; ++s) {
       const float l = __shfl_sync(0xffffffffu, ml.y, s);
       const float f = __shfl_sync(0xffffffffu, f_all, s);
-      if (l == 0.f) continue;
-      const float4 y = reinterpret_cast<const float4*>(
+      // (Read in any case, so that the loads need not wait for l.)
+      float4 y = reinterpret_cast<const float4*>(
           p.part_o)[(s0 + s == 0 ? at0 : at + 2LL * (s0 + s) * kUnitRows) *
                         kCols + col];
+      if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
       sum += l * f;
       acc.x += y.x * f;
       acc.y += y.y * f;

@@ -155,6 +155,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
+  // Tensor memory is taken behind the wait for the kernel ahead (which may
+  // still have to take its own) and before the one behind may start.
+  ptx::griddep_wait();
   if (warp == 0) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  start_after_previous();
+  ptx::griddep_launch_dependents();
 
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase, int role) {

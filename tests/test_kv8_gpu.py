@@ -538,3 +538,180 @@ def test_lengths_out_of_range_are_clamped_and_reported():
     assert bool((got[0] == 0).all()) and torch.equal(got[1], want[1])
     assert attn.attn_device_status() == (attn.ATTN_ERR_INVALID_ARG, 2)
     assert attn.attn_device_status() == (0, 0)
+
+
+def test_new_counts_out_of_range_are_clamped_and_reported():
+    c = ref.filled(2, 1, 64, 64, 16, [64, 10], 93)
+    q = torch.randn(2, 2, 3, 64, generator=ref.rng(94)).half()
+    want = run_fwd(c, q, new=[3, 0], with_w=False)
+    got = run_fwd(c, q, new=[9, -1], with_w=False)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert attn.attn_device_status() == (attn.ATTN_ERR_INVALID_ARG, 2)
+    # Appending more tokens than the length counts: the length decides.
+    x = torch.randn(2, 1, 3, 64, generator=ref.rng(95)).half()
+    a, b = upload(c), upload(c)
+    a.lens.copy_(torch.tensor([64, 2], dtype=torch.int32))
+    b.lens.copy_(torch.tensor([64, 2], dtype=torch.int32))
+    attn.kv8_append(a, x.cuda(), x.cuda(), new_lens=counts([3, 3]))
+    torch.cuda.synchronize()
+    assert attn.attn_stream_status() == (attn.ATTN_ERR_INVALID_ARG, 2)
+    attn.kv8_append(b, x.cuda(), x.cuda(), new_lens=counts([3, 2]))
+    for n in ("k", "v"):
+        assert torch.equal(getattr(a, n).view(torch.uint8),
+                           getattr(b, n).view(torch.uint8))
+
+
+# ------------------------------------------------- graphs, streams, refusals
+
+def test_a_decoding_step_in_a_graph():
+    """lens += 1, append, attention with weights: captured once, replayed."""
+    B, H, g, D, block, cap = 2, 2, 4, 128, 32, 96
+    c = ref.filled(B, H, cap, D, block, [40, 7], 101)
+    gpu = upload(c)
+    k, v = (torch.empty(B, H, 1, D, dtype=torch.float16).cuda()
+            for _ in range(2))
+    q = torch.empty(B, H * g, 1, D, dtype=torch.float16).cuda()
+    w = torch.zeros(B, H, cap).cuda()
+    out, lse = torch.empty_like(q), torch.empty(B, H * g, 1).cuda()
+    ws = attn.kv8_workspace(gpu, H * g, 1, True)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        gpu.lens += 1
+        attn.kv8_append(gpu, k, v)
+        attn.kv8_fwd(gpu, q, weights=w, out=out, lse=lse, workspace=ws)
+    total = torch.zeros(B, H, cap, dtype=torch.float64)
+    tol = torch.zeros_like(total)
+    for step in range(40):
+        x = [torch.randn(B, H, 1, D, generator=ref.rng(300 + 2 * step + s))
+             .half() for s in (0, 1)]
+        y = torch.randn(B, H * g, 1, D, generator=ref.rng(500 + step)).half()
+        k.copy_(x[0])
+        v.copy_(x[1])
+        q.copy_(y)
+        graph.replay()
+        c.lens = [n + 1 for n in c.lens]
+        c.append(x[0], x[1])
+        o_r, l_r, w_r, t_o, t_l, t_w = ref.attention(c, y, D ** -0.5, True)
+        assert bool(((out.cpu().double() - o_r).abs() <= t_o).all())
+        assert bool(((lse.cpu().double() - l_r).abs() <= t_l).all())
+        total += w_r
+        tol += t_w + 2.0 ** -23 * total
+    same_cache(gpu, c)
+    assert bool(((w.cpu().double() - total).abs() <= tol).all())
+
+
+def test_calls_take_the_given_stream_and_the_tensors_device():
+    c = ref.filled(1, 2, 64, 64, 16, [50], 103)
+    q = torch.randn(1, 4, 2, 64, generator=ref.rng(104)).half()
+    want = run_fwd(c, q)
+    side = torch.cuda.Stream()
+    got = run_fwd(c, q, stream=side)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes of K codes: append, attention of few
+    and many rows, weights and eviction at its end."""
+    B, H, cap, D, block = 2, 2, 20_000_000, 64, 128
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    gpu = attn.KV8Cache.empty(B, H, cap, D, block)
+    assert gpu.k.numel() > 1 << 32
+    for n in ("k", "v"):
+        getattr(gpu, n).view(torch.uint8).zero_()
+        getattr(gpu, n + "_scale").fill_(2.0 ** -126)  # blocks of zeros
+    gpu.lens.copy_(torch.tensor([3, cap], dtype=torch.int32))
+    x = torch.zeros(B, H, 2, D)
+    x[:, :, 1] = torch.eye(D)[:H][None] * 16
+    val = torch.randn(B, H, 2, D, generator=ref.rng(105))
+    attn.kv8_append(gpu, x.half().cuda(), val.half().cuda())
+    c = ref.Cache(1, H, 4, D, 16)  # the last four tokens of sequence 1
+    c.lens = [4]
+    pad = torch.zeros(1, H, 2, D)
+    c.append(torch.cat([pad, x[1:].half().float()], 2),
+             torch.cat([pad, val[1:].half().float()], 2))
+    for n in "kv":
+        got = ref.decode(getattr(gpu, n)[1, :, -4:].view(torch.uint8).cpu())
+        scale = getattr(gpu, n + "_scale")[1, :, -1].cpu().double()
+        for h in range(H):
+            assert torch.equal(got[h] * scale[h], c.values(n, 0, h))
+    for Sq in (2, 40):
+        q = torch.zeros(B, H, Sq, D)
+        q[:, :, :] = torch.eye(D)[:H][None, :, None] * 16
+        new = torch.tensor([0, Sq], dtype=torch.int32)
+        w = torch.zeros(B, H, cap).cuda()
+        out, lse = attn.kv8_fwd(gpu, q.half().cuda(), scale=1.0,
+                                new_lens=new.cuda(), weights=w)
+        # Score 256 against zeros: the last token takes all of the last row.
+        v = torch.stack([c.values("v", 0, h)[-1] for h in range(H)])
+        assert torch.equal(out[1, :, -1].cpu(), v.half())
+        assert torch.allclose(lse[1, :, -1].cpu(), torch.tensor(256.0))
+        # The rows before see zeros only: every weight 1 / tokens seen.
+        seen = cap - 1 - torch.arange(Sq - 1).flip(0)
+        assert torch.allclose(lse[1, :, :-1].cpu().double(),
+                              torch.log(seen.double()).expand(H, -1),
+                              atol=1e-4, rtol=0)
+        assert torch.allclose(w[1, :, -1].cpu(), torch.tensor(1.0))
+        total = w[1].double().sum(1).cpu()
+        assert torch.allclose(total, torch.full((H,), float(Sq)).double(),
+                              rtol=1e-4)
+        assert float(w[0].abs().sum()) == 0.0
+        del w
+    w = torch.zeros(B, H, cap).cuda()
+    w[1, :, 5] = 2.0
+    w[1, :, cap - 9] = 1.0
+    small, sw, idx = attn.kv8_evict(
+        gpu, w, 4, recent=2, out=attn.KV8Cache.empty(B, H, 4, D, block))
+    assert idx[1].cpu().tolist() == [[5, cap - 9, cap - 2, cap - 1]] * H
+    assert small.lens.cpu().tolist() == [3, 4]
+    got = ref.decode(small.v[1, :, 2:].view(torch.uint8).cpu())
+    for h in range(H):
+        assert torch.equal(got[h] * float(small.v_scale[1, h, 0]),
+                           c.values("v", 0, h)[-2:])
+
+
+def test_refusals_on_the_device():
+    c = ref.filled(1, 2, 64, 64, 16, [50], 106)
+    gpu = upload(c)
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.float16).cuda()
+    k = torch.zeros(1, 2, 2, 64, dtype=torch.float16).cuda()
+    ws = attn.kv8_workspace(gpu, 4, 2)
+    bad = [
+        lambda: attn.kv8_append(gpu, k.float(), k),
+        lambda: attn.kv8_append(gpu, k, k.bfloat16()),
+        lambda: attn.kv8_append(gpu, k[:, :1], k),
+        lambda: attn.kv8_append(gpu, k.transpose(1, 2), k),
+        lambda: attn.kv8_append(gpu, k.cpu(), k),
+        lambda: attn.kv8_append(gpu, k, k, new_lens=gpu.lens.long()),
+        lambda: attn.kv8_append(gpu, k, k, new_lens=gpu.lens.cpu()),
+        lambda: attn.kv8_fwd(gpu, q[0]),
+        lambda: attn.kv8_fwd(gpu, q[:, :3]),
+        lambda: attn.kv8_fwd(gpu, q.transpose(2, 3).contiguous()),
+        lambda: attn.kv8_fwd(gpu, q.transpose(1, 2).contiguous()
+                             .transpose(1, 2)),
+        lambda: attn.kv8_fwd(gpu, q, out=q),
+        lambda: attn.kv8_fwd(gpu, q, scale=float("nan")),
+        lambda: attn.kv8_fwd(gpu, q, workspace=ws[:-256]),
+        lambda: attn.kv8_fwd(gpu, q, workspace=ws.cpu()),
+        lambda: attn.kv8_fwd(gpu, q, workspace=ws[128:]),
+        lambda: attn.kv8_fwd(gpu, q, workspace=ws[:1].expand(ws.numel())),
+        lambda: attn.kv8_fwd(gpu, q, weights=torch.zeros(1, 2, 63).cuda()),
+        lambda: attn.kv8_fwd(gpu, q, weights=torch.zeros(1, 2, 64)),
+        lambda: attn.kv8_fwd(gpu, q, lse=torch.zeros(1, 4, 2)),
+        lambda: attn.kv8_evict(gpu, torch.zeros(1, 2, 64).cuda(), 0),
+        lambda: attn.kv8_evict(gpu, torch.zeros(1, 2, 64).cuda(), 65),
+        lambda: attn.kv8_evict(gpu, torch.zeros(1, 2, 64).cuda(), 9, 10),
+        lambda: attn.kv8_evict(gpu, torch.zeros(1, 2, 64).cuda(), 9, out=gpu),
+        lambda: attn.kv8_evict(gpu, torch.zeros(1, 2, 64), 9),
+        lambda: attn.kv8_evict(
+            gpu, torch.zeros(1, 2, 64).cuda(), 9,
+            out=attn.KV8Cache.empty(1, 2, 64, 64, block=32)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(attn.AttnError):
+            f()
+            pytest.fail("call %d was taken" % i)
+    torch.cuda.synchronize()
+    same_cache(gpu, c)
