@@ -305,8 +305,8 @@ size_t attn_bwd_workspace_bytes(int B, int Hq, int Sq);
  *            changes the lens of a cache it reads or appends to.  A value
  *            outside the range is taken as the nearer end of it and reported
  *            by attn_device_status (bit 1 of the code).
- * B >= 0, Hkv > 0, capacity >= 1, D in {64, 128}, block in {16, 32, 64, 128};
- * B * Hkv < 2^24.  Codes and scales of tokens at lens[b] or later are never
+ * B >= 0, Hkv > 0, 1 <= capacity < 2^31 - 2^16 - 1, D in {64, 128}, block in
+ * {16, 32, 64, 128}; B * Hkv < 2^24.  Codes and scales of tokens at lens[b] or later are never
  * read: they need no initialisation.
  */
 typedef struct {

@@ -76,6 +76,15 @@ def test_bad_caches_are_refused(lib, change, code):
     assert evict(lib, cache(), other(**change)) == code
 
 
+def test_capacities_near_int32_are_refused(lib):
+    """Kernels count up to 16384 places past a length in 32 bits."""
+    for over in (0, 1, 16384, 1 << 16):
+        c = cache(B=1, Hkv=1, capacity=0x7fffffff - over)
+        assert append(lib, c) == INVALID
+        assert fwd(lib, c) == INVALID
+        assert evict(lib, c, other(B=1, Hkv=1)) == INVALID
+
+
 def test_null_cache(lib):
     assert lib.attn_kv8_append(None, 64 * MB, 65 * MB, 1, None, BF16,
                                None) == INVALID
