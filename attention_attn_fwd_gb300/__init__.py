@@ -9,6 +9,7 @@ library is missing.
 Layouts follow the host launcher of "Flash Attention in CUDA Tile (cuTile)":
 Q, O are [B, Hq, Sq, D] and K, V are [B, Hkv, Skv, D], contiguous.
 """
+import contextlib
 import ctypes
 import math
 import os
@@ -696,6 +697,16 @@ def _kv8_call(name, f, cache, stream, *args):
         raise AttnError("%s: %s" % (name, attn_status_string(st)), st)
 
 
+def _kv8_memory(cache, stream):
+    """Context in which a call on ``stream`` allocates: memory of that
+    stream's own, so that it is neither still in use by work of the current
+    stream nor handed out again there before the call has run."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream)
+
+
 def kv8_append(cache, k, v, new_lens=None, stream=None):
     """Quantise the K and V of new tokens into an 8-bit cache.
 
@@ -737,7 +748,8 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     or behind new_lens are left as they are in ``out`` and ``lse``.
     ``weights`` (float32 [B, Hkv, capacity]): the attention weight each token
     receives, summed over rows and the group's heads, is added to it.
-    ``workspace``: from ``kv8_workspace``, allocated when not given.
+    ``workspace``: from ``kv8_workspace``, allocated when not given.  What a
+    call on ``stream`` allocates is that stream's memory.
     """
     dt = _kv8_dtype(cache, "q", q)
     dev, dtype, B = cache.device, q.dtype, cache.B
@@ -746,18 +758,21 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     _check_tensor("q", q, shape, dtype, dev)
     if out is None:
         import torch
-        out = torch.empty_like(q)
+        with _kv8_memory(cache, stream):
+            out = torch.empty_like(q)
     else:
         _check_tensor("out", out, shape, dtype, dev)
     if not need_lse:
         lse = None
     elif lse is None:
         import torch
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
+        with _kv8_memory(cache, stream):
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
     else:
         _check_tensor("lse", lse, (B, Hq, Sq), cache.float32, dev)
     if workspace is None:
-        workspace = kv8_workspace(cache, Hq, Sq, weights is not None)
+        with _kv8_memory(cache, stream):
+            workspace = kv8_workspace(cache, Hq, Sq, weights is not None)
     elif not workspace.is_contiguous():
         raise AttnError("workspace must be contiguous", ATTN_ERR_INVALID_ARG)
     if new_lens is not None:
@@ -789,7 +804,8 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
     values).  ``out_weights`` (float32 [B, Hkv, out.capacity]) receives the
     kept tokens' weights, then zeros; in place it defaults to ``weights``
     itself.  Returns (out, out_weights, indices): indices int32 [B, Hkv,
-    keep] are the kept tokens' old places, -1 behind the last.
+    keep] are the kept tokens' old places, -1 behind the last.  What a call
+    on ``stream`` allocates is that stream's memory.
     """
     import torch
     dev = cache.device
@@ -799,8 +815,10 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
     _check_tensor("weights", weights, (cache.B, cache.Hkv, cache.capacity),
                   torch.float32, dev)
     if out is None:
-        out = KV8Cache(cache.k, cache.v, cache.k_scale, cache.v_scale,
-                       torch.empty_like(cache.lens), cache.block)
+        with _kv8_memory(cache, stream):
+            lens = torch.empty_like(cache.lens)
+        out = KV8Cache(cache.k, cache.v, cache.k_scale, cache.v_scale, lens,
+                       cache.block)
         if out_weights is None:
             out_weights = weights
     elif out.device != dev:
@@ -808,12 +826,14 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
                         ATTN_ERR_INVALID_ARG)
     shape = (cache.B, cache.Hkv, out.capacity)
     if out_weights is None:
-        out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        with _kv8_memory(cache, stream):
+            out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         _check_tensor("out_weights", out_weights, shape, torch.float32, dev)
     shape = (cache.B, cache.Hkv, keep)
     if indices is None:
-        indices = torch.empty(shape, dtype=torch.int32, device=dev)
+        with _kv8_memory(cache, stream):
+            indices = torch.empty(shape, dtype=torch.int32, device=dev)
     else:
         _check_tensor("indices", indices, shape, torch.int32, dev)
     _kv8_call("attn_kv8_evict", cache.lib.attn_kv8_evict, cache, stream,

@@ -611,6 +611,87 @@ def test_calls_take_the_given_stream_and_the_tensors_device():
         assert torch.equal(a, b)
 
 
+def test_a_call_on_another_stream_allocates_there():
+    """Memory that the current stream still reads (its tensor is gone) must
+    not be handed to a call that runs on another stream meanwhile."""
+    c = ref.filled(1, 2, 64, 64, 16, [50], 107)
+    q = torch.randn(1, 64, 64, 64, generator=ref.rng(108)).half().cuda()
+    gpu = upload(c)
+    want = run_fwd(c, q.cpu(), with_w=False)
+    side = torch.cuda.Stream()
+    w = torch.rand(1, 2, 64, generator=ref.rng(109)).cuda()
+    small = attn.KV8Cache.empty(1, 2, 32, 64, 16)
+    # Freed blocks of every size that the calls ask for, read late.
+    old = [torch.full((n,), 3, dtype=torch.uint8).cuda()
+           for n in (q.nbytes, 4 * 64 * 64,
+                     attn.kv8_workspace(gpu, 64, 64).nbytes,
+                     4 * 2 * 32, 4 * 2 * 20)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    late = [t.clone() for t in old]
+    del old
+    out, lse = attn.kv8_fwd(gpu, q, stream=side)
+    attn.kv8_evict(gpu, w, 20, out=small, stream=side)
+    torch.cuda.synchronize()
+    assert all(bool((t == 3).all()) for t in late)
+    assert torch.equal(out.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("Sq", [1, 24])
+def test_work_of_other_streams_is_awaited(Sq, captured):
+    """The queries come late from a second stream, joined by an event between
+    append and attention; then the next step's keys, read from the output."""
+    B, H, g, D, block = 1, 2, 4, 64, 16
+    c = ref.filled(B, H, 300, D, block, [250], 110)
+    x = torch.randn(B, H, Sq, D, generator=ref.rng(111)).half()
+    y = torch.randn(B, H * g, Sq, D, generator=ref.rng(112)).half()
+    c.lens = [250 + Sq]
+    gpu = upload(c)
+    c.append(x, x)
+    want = run_fwd(c, y, with_w=False)
+    xd, yd = x.cuda(), y.cuda()
+    ws = attn.kv8_workspace(gpu, H * g, Sq)
+    q = torch.zeros_like(yd)
+    out, lse = torch.zeros_like(yd), torch.zeros(B, H * g, Sq).cuda()
+    copy = torch.zeros_like(out)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(4_000_000)  # about 2 ms
+            q.copy_(yd)
+        attn.kv8_append(gpu, xd, xd)
+        main.wait_stream(side)
+        attn.kv8_fwd(gpu, q, out=out, lse=lse, workspace=ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            copy.copy_(out)
+        main.wait_stream(side)
+        attn.kv8_append(gpu, xd, xd)  # (the same tokens again)
+
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        run = graph.replay
+    else:
+        run = step
+    for _ in range(3):
+        q.zero_()
+        out.zero_()
+        copy.zero_()
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want[0])
+        assert torch.equal(lse.cpu(), want[1])
+        assert torch.equal(copy, out)
+    same_cache(gpu, c)
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 bytes of K codes: append, attention of few
     and many rows, weights and eviction at its end."""
