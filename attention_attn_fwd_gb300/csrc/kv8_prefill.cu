@@ -17,8 +17,8 @@
 // P is kept shifted by 2^7 (it is at most 2^15, and normal down to 2^-21 of
 // its row's largest), as are the row sums, which take P unrounded.
 //
-// Steps (unit, key tile) form one list, cut into equal consecutive shares, one
-// per CTA: lengths come from device memory and the cut follows them, whether
+// Steps (unit, key tile) form one list, with some empty places before each
+// unit's, cut into equal consecutive shares, one per CTA: lengths come from device memory and the cut follows them, whether
 // there are few units with many keys or many units.  A unit that one CTA
 // covers is finished by it; the parts of any other go to workspace slots (a
 // CTA has two at most: a unit begun before its share, one going on after it)
@@ -50,6 +50,14 @@ static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsConvert <= 4 * 128,
               "register split exceeds the launch allocation");
 
 constexpr int kUnits = 4;  // published units held at a time
+// Empty places of the list before each unit's steps: they stand for what a
+// part of a unit takes besides them (query rows, the first tile's fill, the
+// output: about 13000 clocks against 3400 a step), so that CTAs with more
+// parts get fewer steps.  8 x 512 rows over 4096 tokens, 32 heads: CTAs took
+// 398k to 438k clocks without, 238 us; with 2 / 4 / 6 places 234.5 / 232 / 232
+// (2 x 64 rows over 8192: 77 -> 73 / 70 / 68; 4 x 200 rows over 1500, 16 heads:
+// 23.0 -> 21.9 / 22.6 / 23.9).
+constexpr int kOver = 4;
 
 // A unit's part as the roles need it.
 struct Record {
@@ -94,6 +102,10 @@ __device__ __forceinline__ int tiles_seen(const FwdParams& p, int len,
   return (row_end(p, len, n_new, last) + kTN - 1) / kTN;
 }
 
+__device__ __forceinline__ int places(int steps) {
+  return steps > 0 ? steps + kOver : 0;
+}
+
 // A unit, or the part of one, that a CTA works on: key tiles [j0, j1) of its
 // `steps`.  Units are numbered (b, u, h), h fastest.
 struct Unit {
@@ -136,7 +148,7 @@ struct Walk {
     int total = 0;
     for (int i = lane; i < pairs; i += 32) {
       int len, n_new;
-      total += pair_steps(p, i, &len, &n_new);
+      total += places(pair_steps(p, i, &len, &n_new));
     }
 #pragma unroll
     for (int s = 16; s > 0; s /= 2)
@@ -154,7 +166,7 @@ struct Walk {
       const int i = i0 + lane;
       int len = 0, n_new = 0, steps = 0;
       if (i < pairs) steps = pair_steps(p, i, &len, &n_new);
-      const int t = steps * p.Hkv;
+      const int t = places(steps) * p.Hkv;
       int incl = t;
 #pragma unroll
       for (int s = 1; s < 32; s *= 2) {
@@ -169,11 +181,13 @@ struct Walk {
         w.len = __shfl_sync(0xffffffffu, len, l);
         w.n_new = __shfl_sync(0xffffffffu, n_new, l);
         w.steps = __shfl_sync(0xffffffffu, steps, l);
-        w.h = off / w.steps;
-        w.j0 = off - w.h * w.steps;
-        w.j1 = min(w.steps, w.j0 + count);
-        left = count - (w.j1 - w.j0);
-        return true;
+        w.h = off / places(w.steps);
+        // Steps of the unit before the share (negative: empty places).
+        const int at = off - w.h * places(w.steps) - kOver;
+        w.j0 = max(0, at);
+        w.j1 = min(w.steps, at + count);
+        left = count - (w.j1 - at);
+        return w.j1 > w.j0;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -181,7 +195,7 @@ struct Walk {
   }
 
   __device__ __forceinline__ bool next(const FwdParams& p) {
-    if (left == 0) return false;
+    if (left <= kOver) return false;
     if (++w.h == p.Hkv) {
       w.h = 0;
       int i = w.b * p.row_blocks + w.u;
@@ -192,8 +206,8 @@ struct Walk {
       set_pair(p, i);
     }
     w.j0 = 0;
-    w.j1 = min(w.steps, left);
-    left -= w.j1;
+    w.j1 = min(w.steps, left - kOver);
+    left -= w.j1 + kOver;
     return true;
   }
 };
@@ -303,21 +317,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile Record* records = reinterpret_cast<Record*>(smem + L::kRecords);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) {
-      const uint32_t bar = s_base + L::kBars + 8 * i;
-      // Converted tiles, freed raw tiles and Q tiles: one arrival per warp
-      // of the four; units read: one per warp of the other roles (14); P:
-      // one per softmax thread of the tile.
-      uint32_t count = 1;
-      if ((bar >= bar_rempty && bar < bar_empty) ||
-          (bar >= bar_q && bar < bar_s))
-        count = 4;
-      if (bar >= bar_ufree && bar < bar_q) count = 14;
-      if (bar >= bar_p && bar < bar_o) count = kTM;
-      ptx::mbar_init(bar, count);
-    }
-    *abort_flag = 0;
+  if (threadIdx.x < L::kNumBars) {
+    const uint32_t bar = s_base + L::kBars + 8 * threadIdx.x;
+    // Converted tiles, freed raw tiles and Q tiles: one arrival per warp of
+    // the four; units read: one per warp of the other roles (14); P: one per
+    // softmax thread of the tile.
+    uint32_t count = 1;
+    if ((bar >= bar_rempty && bar < bar_empty) ||
+        (bar >= bar_q && bar < bar_s))
+      count = 4;
+    if (bar >= bar_ufree && bar < bar_q) count = 14;
+    if (bar >= bar_p && bar < bar_o) count = kTM;
+    ptx::mbar_init(bar, count);
+    if (threadIdx.x == 0) *abort_flag = 0;
     ptx::fence_mbar_init();
   }
   // Tensor memory is taken behind the wait for the kernel ahead (which may
