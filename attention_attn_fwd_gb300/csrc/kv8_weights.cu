@@ -31,6 +31,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kTN = 128;    // keys of a tile
 constexpr int kRows = 256;  // query rows of a pass
+// Empty places of the cut per segment, for its query rows (2 x 64 rows over
+// 8192 tokens, 32 heads, forward included: 69.0 us without, with 2 / 4 / 8
+// places 65.4 / 63.8 / 65.1).
+constexpr int kOver = 4;
 
 template <int D>
 struct Smem {
@@ -74,6 +78,67 @@ __device__ __forceinline__ void ffma2_pairs(float& y0, float& y1, float x0,
       : "f"(x0), "f"(x1), "f"(m0), "f"(m1), "f"(a0), "f"(a1));
 }
 
+// 32 query rows to fp16 operand rows in shared memory (128-byte swizzled boxes
+// of `box` bytes, the first row at `dst`, a multiple of 8 rows from its box's
+// start), each times its row_shift's power of two, negated if `negate`.
+// `off`: this lane's row, in elements from q, or -1 (zeros).  Returns the
+// shift of this lane's row.  The rows come by coalesced asynchronous copies
+// and are converted where they land, a row per lane, in small loops: a row of
+// loads per lane, unrolled, touched 32 lines with each load and fetched its
+// instructions anew at every call (weights kernel 31 -> 26 us at 2 x 64 rows
+// over 8192 tokens; the forward kernel, whose softmax warps hold their rows in
+// registers, gained nothing from it).
+template <int D, bool kBF16>
+__device__ __forceinline__ int stage_rows(const void* q, long long off,
+                                          uint32_t dst, uint32_t box,
+                                          bool negate, int lane) {
+  constexpr int kChunks = D / 8;         // lanes of a row
+  constexpr int kAtOnce = 32 / kChunks;  // rows of an instruction
+  {
+    const int c = lane % kChunks, sub = lane / kChunks;
+    const uint32_t to = dst + (c / 8) * box;
+#pragma unroll 2
+    for (int row = sub; row < 32; row += kAtOnce) {
+      const long long at = __shfl_sync(0xffffffffu, off, row);
+      const uint32_t d = to + row * 128 + (((c % 8) ^ (row % 8)) << 4);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
+                   "l"(static_cast<const uint16_t*>(q) +
+                       (at < 0 ? 0 : at + 8 * c)),
+                   "r"(at < 0 ? 0 : 16)
+                   : "memory");
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const uint32_t mine = dst + lane * 128;
+  float amax = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < kChunks; ++k) {
+    const uint4 x = ptx::ld_shared_v4(mine + (k / 8) * box +
+                                      (((k % 8) ^ (lane % 8)) << 4));
+    const float2 a = unpack2<kBF16>(x.x), b = unpack2<kBF16>(x.y);
+    const float2 c = unpack2<kBF16>(x.z), d = unpack2<kBF16>(x.w);
+    amax = ptx::fmax3(amax, fabsf(a.x), fabsf(a.y));
+    amax = ptx::fmax3(amax, fabsf(b.x), fabsf(b.y));
+    amax = ptx::fmax3(amax, fabsf(c.x), fabsf(c.y));
+    amax = ptx::fmax3(amax, fabsf(d.x), fabsf(d.y));
+  }
+  const int up = row_shift(amax);
+  const float f = negate ? -exp2_int(up) : exp2_int(up);
+#pragma unroll 2
+  for (int k = 0; k < kChunks; ++k) {
+    const uint32_t at = mine + (k / 8) * box + (((k % 8) ^ (lane % 8)) << 4);
+    const uint4 x = ptx::ld_shared_v4(at);
+    const float2 a = unpack2<kBF16>(x.x), b = unpack2<kBF16>(x.y);
+    const float2 c = unpack2<kBF16>(x.z), d = unpack2<kBF16>(x.w);
+    ptx::st_shared_v4(at, ptx::pack2<false>(a.x * f, a.y * f),
+                      ptx::pack2<false>(b.x * f, b.y * f),
+                      ptx::pack2<false>(c.x * f, c.y * f),
+                      ptx::pack2<false>(d.x * f, d.y * f));
+  }
+  return up;
+}
+
 // The passes of a CTA's share, walked alike by every role: tiles [t0, t1) of
 // a segment, query rows [256 u, 256 u + 256), of which tiles [t0, hi) see
 // some.
@@ -98,8 +163,9 @@ struct Passes {
              : min(t1, (row_end(p, seg.len, n_new, last) + kTN - 1) / kTN);
   }
   __device__ __forceinline__ bool first(const FwdParams& p, int lane) {
-    count = take_share<kTN, 0, 1>(p, static_cast<int>(blockIdx.x), lane, &seg);
-    if (count == 0) return false;
+    count =
+        take_share<kTN, kOver, 1>(p, static_cast<int>(blockIdx.x), lane, &seg);
+    if (count == 0 || seg.pos >= count) return false;
     enter(p);
     return hi > t0 || next(p);
   }
@@ -110,7 +176,8 @@ struct Passes {
         set_hi(p);
       } else {
         if (seg.end >= count) return false;
-        next_segment<kTN, 0>(p, seg);
+        next_segment<kTN, kOver>(p, seg);
+        if (seg.pos >= count) return false;
         enter(p);
       }
     } while (hi <= t0);
@@ -140,19 +207,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) {
-      const uint32_t bar = s_base + L::kBars + 8 * i;
-      // One arrival per warp of the role that fills or frees; raw loads and
-      // MMAs arrive once.
-      uint32_t count = 1;
-      if ((bar >= bar_rempty && bar < bar_empty) || bar == bar_q ||
-          (bar >= bar_sfree && bar < bar_drain))
-        count = 4;
-      if (bar == bar_qfree) count = 8;
-      ptx::mbar_init(bar, count);
-    }
-    *abort_flag = 0;
+  if (threadIdx.x < L::kNumBars) {
+    const uint32_t bar = s_base + L::kBars + 8 * threadIdx.x;
+    // One arrival per warp of the role that fills or frees; raw loads and
+    // MMAs arrive once.
+    uint32_t count = 1;
+    if ((bar >= bar_rempty && bar < bar_empty) || bar == bar_q ||
+        (bar >= bar_sfree && bar < bar_drain))
+      count = 4;
+    if (bar == bar_qfree) count = 8;
+    ptx::mbar_init(bar, count);
+    if (threadIdx.x == 0) *abort_flag = 0;
     ptx::fence_mbar_init();
   }
   // Tensor memory is taken behind the wait for the kernel ahead (which may
@@ -162,6 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
   }
+  Passes w;
+  const bool first = (warp < 2 || warp >= 4) && w.first(p, lane);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -173,8 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1, abort_flag, p,
                                                 role)) != 0;
   };
-  Passes w;
-  bool more = (warp < 2 || warp >= 4) && w.first(p, lane);
+  bool more = first;
 
   if (warp == 1) {
     // ------------------------------------------------------ raw key tiles
@@ -271,46 +337,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = half * 128 + tid, row = w.u * kRows + r;
         const bool in = row < w.rows;
         const int tok = row / p.group, hd = row - tok * p.group;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) +
-            (in ? ((static_cast<long long>(w.seg.b) * p.Hq +
-                    w.seg.h * p.group + hd) * p.Sq + tok) * D
-                : 0));
         float lse = INFINITY;  // no weight: rows past the last, and rows
         if (in) {              // that see nothing
           lse = p.lse2[static_cast<long long>(bh) * lse2_rows + row];
           if (lse == -INFINITY) lse = INFINITY;
         }
-        uint32_t x[D / 2];
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const uint4 y = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-          x[4 * k] = y.x;
-          x[4 * k + 1] = y.y;
-          x[4 * k + 2] = y.z;
-          x[4 * k + 3] = y.w;
-        }
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 2; ++k) {
-          const float2 f = unpack2<kBF16>(x[k]);
-          amax = ptx::fmax3(amax, fabsf(f.x), fabsf(f.y));
-        }
-        const int up = row_shift(amax);
-        const float f_up = exp2_int(up);
-        const uint32_t dst = s_base + L::kQ + r * 128;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          uint32_t o[4];
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const float2 f = unpack2<kBF16>(x[4 * k + a]);
-            o[a] = ptx::pack2<false>(f.x * f_up, f.y * f_up);
-          }
-          ptx::st_shared_v4(dst + (k / 8) * L::kQBox +
-                                (((k % 8) ^ (r % 8)) << 4),
-                            o[0], o[1], o[2], o[3]);
-        }
+        const int up = stage_rows<D, kBF16>(
+            p.q,
+            in ? ((static_cast<long long>(w.seg.b) * p.Hq +
+                   w.seg.h * p.group + hd) * p.Sq + tok) * D
+               : -1,
+            s_base + L::kQ + (half * 128 + cw * 32) * 128, L::kQBox, false,
+            lane);
         consts[(r / 2) * 4 + r % 2] = p.scale_log2 * exp2_int(-up);
         consts[(r / 2) * 4 + 2 + r % 2] = -lse;
       }
