@@ -91,9 +91,11 @@ bool all_on_device(const attn_kv8_t& c, const void* const* more, int count,
 
 // How the query rows of a K/V head are worked on: up to 16 by the decode
 // kernels (8 or 16 a CTA; bound by the codes' bytes), more by the tcgen05
-// kernel in units of 256 (a 128-row tile of 17 rows costs what one of 128
-// costs, yet 17 rows in two passes of the decode kernel read the codes
-// twice).
+// kernel in units of 256.  At 16 rows decode against tcgen05: 26 / 37 us on
+// 8 x 4096 tokens of 8 heads, 54 / 99 on 131072 of 8, 10 / 14 on 2000 of 2
+// (D = 128), 20 / 36 on 16 x 1024 of 16 (D = 64).  At 20 to 32 rows, where
+// decode would take two passes of that, tcgen05 takes the same 37 to 38, 99,
+// 14 and 36.
 struct RowPlan {
   long long rows;   // query rows per (batch, K/V head)
   int tile;         // rows a CTA holds: 8, 16 or 256

@@ -24,14 +24,22 @@
 // sums take P unrounded.
 //
 // Codes reach shared memory by 16-byte asynchronous copies, a ring of tiles
-// per warp that runs ahead across segments (190 KB in flight per SM; with the
-// codes loaded straight to registers one tile ahead, 64 KB, the kernel ran
-// at 2.8 TB/s on 8 x 4096 tokens and 4.4 TB/s on 131072).  Fragments are read
+// per warp that runs ahead across segments (128 to 144 KB in flight per SM;
+// with the codes loaded straight to registers one tile ahead, 64 KB, the
+// kernel ran at 2.8 TB/s on 8 x 4096 tokens and 4.4 TB/s on 131072, without
+// its merge).  Fragments are read
 // 16 bytes at a time: the d index of both products may be permuted freely, so
 // lane c of a quad owns bytes 16c.. of a 64-byte half row of K and lane group
 // g8 owns bytes (D/8) g8.. of four V rows; 16-byte chunks of a row are stored
 // XORed by its row so that those reads do not share banks.  No transposes but
 // a byte permute and one movmatrix per 8 x 8 weights.
+//
+// Measured, merge included: 8 x 4096 tokens, 8 heads of 4 rows, D = 128, with
+// accumulated weights 23.3 us (69 MB); 131072 tokens, 4 heads of 8 rows 32.3
+// us (134 MB, 4.2 TB/s).  With the products taken out the first two thirds of
+// that stay (15.8 and 25.0 us, the loads), the products add about 4 us and the
+// merge's launch behind the last CTA 4 to 7: on short caches latency bounds
+// the pair, on long ones the codes' bytes.
 #include "kv8_common.cuh"
 
 namespace attn {

@@ -9,8 +9,9 @@
 //     one shared-memory ring into the 128-byte-swizzled fp16 tiles of
 //     another (exactly).  K's block scales multiply the scores in fp32, 16
 //     keys at a time; V's scale over the largest one of the unit's keys
-//     multiplies V's halves (exact for powers of two; else one fp16 rounding,
-//     2^-11, as P's own);
+//     multiplies V's halves: exact for powers of two within 2^15 of the
+//     largest (below that, off by 2^-25 of the largest at most), else one
+//     fp16 rounding, 2^-11, as P's own;
 //   - each softmax thread brings its Q row to fp16 with a power of two
 //     (exact down to 2^-37 of the row's largest element) and the sign of the
 //     scale, while the previous unit's last products run.
@@ -28,6 +29,15 @@
 // tiles, warp 2 walks the share and publishes its units in shared memory,
 // warps 4-7 / 8-11 Q conversion, softmax and epilogue of Q tile 0 / 1, warps
 // 12-15 K and V conversion.  Every wait is bounded as in the forward kernel.
+//
+// Measured: 8 x 512 rows of 32 heads over 4096 tokens of 8 heads, D = 128,
+// causal (258 GFLOP): 233 us, 1.11 PFLOP/s, against 187 for the 16-bit forward
+// kernel on the same numbers.  A step (256 rows, 128 keys) takes about 3400
+// clocks against 2048 of MMAs.  Nothing alone bounds it: with the conversion
+// left out the call (then 238 us) took 223, with exp2 left out 235, with both
+// 212; shared memory carries both operands of Q K^T, the raw tiles and the
+// converted ones.  A fifth warpgroup for V's conversion took 268 (spills), raw
+// tiles read past shared memory 255, four converted and two raw slots 262.
 #include "attn_sync.cuh"
 #include "kv8_common.cuh"
 

@@ -369,6 +369,13 @@ attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
  *           A row that sees no token gets O = 0 and LSE = -inf.
  * Hq        a multiple of the cache's Hkv; scale finite, any sign;
  * dtype     ATTN_F16 or ATTN_BF16;
+ *           NaN: a row of Q with NaN gets NaN and leaves the others alone; a
+ *           NaN code of K reaches the rows that see its token; a NaN code of V
+ *           may reach every row of its sequence and head in the call, also
+ *           rows before its token (0 * NaN, as in attn_fwd).  A V scale
+ *           more than 2^15 below the largest one among the lens[b] tokens of
+ *           its sequence and head costs precision: its numbers are then off
+ *           by up to 2^-23 of the largest scale.
  * workspace device, 256-byte aligned, at least attn_kv8_workspace_bytes(...)
  *           bytes; contents need no initialisation.  It must not be used by
  *           another call until this one has run.
