@@ -655,17 +655,15 @@ class KV8Cache:
         return cls(k, v, ks, vs, lens, block)
 
 
-def _check_tensor(name, t, shape, dtype, device):
-    """A contiguous tensor of this shape and type on this device."""
-    if t.shape == shape and t.dtype == dtype and t.device == device and \
-            t.is_contiguous():
-        return
+def _check_tensor(name, t, shape, dtype):
+    """A contiguous tensor of this shape and type.  (Whether it is memory of
+    the cache's device is checked behind the C ABI, pointer by pointer.)"""
     if t.shape != shape or t.dtype != dtype:
         raise AttnError("%s must be %s of %s, got %s of %s" % (
             name, list(shape), dtype, list(t.shape), t.dtype),
             ATTN_ERR_INVALID_ARG)
-    raise AttnError("%s must be a contiguous tensor on the cache's device"
-                    % name, ATTN_ERR_INVALID_ARG)
+    if not t.is_contiguous():
+        raise AttnError("%s must be contiguous" % name, ATTN_ERR_INVALID_ARG)
 
 
 def _kv8_dtype(cache, name, t):
@@ -716,12 +714,12 @@ def kv8_append(cache, k, v, new_lens=None, stream=None):
     new_lens rows.  ``cache.lens`` already counts them and is not changed.
     """
     dt = _kv8_dtype(cache, "k", k)
-    dev, dtype, Sq = cache.device, k.dtype, k.shape[2]
+    dtype, Sq = k.dtype, k.shape[2]
     shape = (cache.B, cache.Hkv, Sq, cache.D)
-    _check_tensor("k", k, shape, dtype, dev)
-    _check_tensor("v", v, shape, dtype, dev)
+    _check_tensor("k", k, shape, dtype)
+    _check_tensor("v", v, shape, dtype)
     if new_lens is not None:
-        _check_tensor("new_lens", new_lens, (cache.B,), cache.int32, dev)
+        _check_tensor("new_lens", new_lens, (cache.B,), cache.int32)
         new_lens = new_lens.data_ptr()
     _kv8_call("attn_kv8_append", cache.lib.attn_kv8_append, cache, stream,
               k.data_ptr() or None, v.data_ptr() or None, Sq, new_lens, dt)
@@ -752,35 +750,36 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     call on ``stream`` allocates is that stream's memory.
     """
     dt = _kv8_dtype(cache, "q", q)
-    dev, dtype, B = cache.device, q.dtype, cache.B
+    dtype, B = q.dtype, cache.B
     _, Hq, Sq, _ = q.shape
     shape = (B, Hq, Sq, cache.D)
-    _check_tensor("q", q, shape, dtype, dev)
+    _check_tensor("q", q, shape, dtype)
     if out is None:
         import torch
         with _kv8_memory(cache, stream):
             out = torch.empty_like(q)
     else:
-        _check_tensor("out", out, shape, dtype, dev)
+        _check_tensor("out", out, shape, dtype)
     if not need_lse:
         lse = None
     elif lse is None:
         import torch
         with _kv8_memory(cache, stream):
-            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32,
+                              device=cache.device)
     else:
-        _check_tensor("lse", lse, (B, Hq, Sq), cache.float32, dev)
+        _check_tensor("lse", lse, (B, Hq, Sq), cache.float32)
     if workspace is None:
         with _kv8_memory(cache, stream):
             workspace = kv8_workspace(cache, Hq, Sq, weights is not None)
     elif not workspace.is_contiguous():
         raise AttnError("workspace must be contiguous", ATTN_ERR_INVALID_ARG)
     if new_lens is not None:
-        _check_tensor("new_lens", new_lens, (B,), cache.int32, dev)
+        _check_tensor("new_lens", new_lens, (B,), cache.int32)
         new_lens = new_lens.data_ptr()
     if weights is not None:
         _check_tensor("weights", weights, (B, cache.Hkv, cache.capacity),
-                      cache.float32, dev)
+                      cache.float32)
         weights = weights.data_ptr()
     if scale is None:
         scale = cache.D ** -0.5
@@ -813,7 +812,7 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
     if keep < 1:
         raise AttnError("keep must be at least 1", ATTN_ERR_INVALID_ARG)
     _check_tensor("weights", weights, (cache.B, cache.Hkv, cache.capacity),
-                  torch.float32, dev)
+                  torch.float32)
     if out is None:
         with _kv8_memory(cache, stream):
             lens = torch.empty_like(cache.lens)
@@ -829,13 +828,13 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
         with _kv8_memory(cache, stream):
             out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
-        _check_tensor("out_weights", out_weights, shape, torch.float32, dev)
+        _check_tensor("out_weights", out_weights, shape, torch.float32)
     shape = (cache.B, cache.Hkv, keep)
     if indices is None:
         with _kv8_memory(cache, stream):
             indices = torch.empty(shape, dtype=torch.int32, device=dev)
     else:
-        _check_tensor("indices", indices, shape, torch.int32, dev)
+        _check_tensor("indices", indices, shape, torch.int32)
     _kv8_call("attn_kv8_evict", cache.lib.attn_kv8_evict, cache, stream,
               out.struct,
               weights.data_ptr() or None, out_weights.data_ptr() or None,
