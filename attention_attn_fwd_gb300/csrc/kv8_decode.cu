@@ -9,7 +9,8 @@
 // (CTA + segment): both only grow along the list, so no two share one.  The
 // merge kernel joins a segment's partials by their maxima.  Lengths come from
 // device memory, so the cut follows them without the host's knowing: ragged
-// batches are balanced to a tile.
+// batches are balanced to a tile.  Short caches take a CTA per segment instead,
+// which writes the results itself (whole_bytes below).
 //
 // Products: S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16 in fp16,
 // 16 keys (or 16 of D) by 8 query rows: with 8 or 16 rows a 128-row
@@ -200,11 +201,55 @@ struct Config {
   static constexpr int kPitch = D + 4;  // floats: rows start 4 banks apart
   static constexpr int kRingBytes = kDecodeWarps * kStages * 4096;
   static constexpr int kBytes =
-      kRingBytes + kDecodeWarps * kRows * (kPitch + 2) * 4;
+      kRingBytes + kDecodeWarps * kRows * (kPitch + 2) * 4 + kRows * 4;
   static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
-template <int D, int NT, bool kBF16>
+__device__ __forceinline__ long long out_row(const FwdParams& p, int b, int h,
+                                             int r) {
+  const int tok = r / p.group, hd = r - tok * p.group;
+  return (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
+}
+// The LSE in log2 units of a row's (max, sum), -inf for one that sees nothing.
+__device__ __forceinline__ float total_lse2(float2 t) {
+  return t.y == 0.f ? -INFINITY : t.x + log2f(t.y);
+}
+
+// The scores of one key that the forward left, rows beyond n_rows as hidden
+// ones; and the weight they make under the rows' LSEs.
+template <int kRows>
+__device__ __forceinline__ void load_scores(const FwdParams& p, long long key,
+                                            int n_rows, float4* x) {
+  const float* at = p.scores + (key << p.score_shift);
+#pragma unroll
+  for (int k = 0; k < kRows / 4; ++k) {
+    x[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (4 * k >= n_rows) continue;
+    if (p.score_shift >= 2) {
+      x[k] = *reinterpret_cast<const float4*>(at + 4 * k);
+    } else {
+      x[k].x = at[0];
+      if (n_rows > 1) x[k].y = at[1];
+    }
+  }
+}
+template <int kRows>
+__device__ __forceinline__ float weight_of(const float4* x, const float* lse2,
+                                           int n_rows) {
+  float add = 0.f;
+#pragma unroll
+  for (int k = 0; k < kRows / 4; ++k) {
+    const float v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // hidden scores and padding rows: -inf
+      if (4 * k + e < n_rows && v[e] != -INFINITY)
+        add += ptx::ex2(v[e] - lse2[4 * k + e]);
+  }
+  return add;
+}
+
+// kWhole: a CTA per segment, which writes the results itself.
+template <int D, int NT, bool kBF16, bool kWhole>
 __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
     kv8_decode_kernel(const FwdParams p) {
   using C = Config<D, NT>;
@@ -220,6 +265,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
   float* sm_o = reinterpret_cast<float*>(smem + C::kRingBytes);
   float* sm_m = sm_o + kWarps * kRows * kPitch;  // [kWarps][kRows]
   float* sm_l = sm_m + kWarps * kRows;
+  float* sm_lse = sm_l + kWarps * kRows;  // kWhole: [kRows]
 
   start_after_previous();
 
@@ -228,8 +274,16 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
   const int cta = blockIdx.x;
   Segment seg;
   seg.pos = 0;
-  const int count = take_share<kKeys, kOver, kDecodeWarps>(p, cta, lane, &seg);
-  if (seg.pos >= count) return;  // (also: no share)
+  int count;
+  if constexpr (kWhole) {
+    seg.b = cta / p.Hkv;
+    seg.h = cta - seg.b * p.Hkv;
+    seg.len = seq_len(p, seg.b);
+    seg.tiles = seg.end = count = (seg.len + kKeys - 1) / kKeys;
+  } else {
+    count = take_share<kKeys, kOver, kDecodeWarps>(p, cta, lane, &seg);
+    if (seg.pos >= count) return;  // (also: no share)
+  }
   const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * 4096;
   Loader<D> ld;
   ld.init(p, seg, warp, lane, ring);
@@ -535,6 +589,55 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
                           o[nt][i + 1][e] * fo, o[nt][i + 1][e + 2] * fo);
       }
     __syncthreads();
+    if constexpr (kWhole) {
+      for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads) {
+        const int r = i / (D / 4), d4 = i % (D / 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(
+              sm_o + (w * kRows + r) * kPitch + 4 * d4);
+          acc.x += x.x;
+          acc.y += x.y;
+          acc.z += x.z;
+          acc.w += x.w;
+          sum += sm_l[w * kRows + r];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint2 out;
+        out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
+        out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) +
+                                 out_row(p, b, h, r) * D)[d4] = out;
+      }
+      if (threadIdx.x < n_rows) {
+        const int r = threadIdx.x;
+        float2 t = make_float2(kNone, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          t.x = fmaxf(t.x, sm_m[w * kRows + r]);
+          t.y += sm_l[w * kRows + r];
+        }
+        const float lse2 = total_lse2(t);
+        sm_lse[r] = lse2;
+        if (p.lse != nullptr)
+          p.lse[out_row(p, b, h, r)] = lse2 * 0.69314718055994531f;
+      }
+      if (p.scores != nullptr && n_rows > 0) {
+        __syncthreads();  // the segment's scores and LSEs have been written
+        const long long key_at = static_cast<long long>(bh) * p.capacity;
+#pragma unroll 2
+        for (int key = threadIdx.x; key < len; key += C::kThreads) {
+          const float before = p.weights[key_at + key];
+          float4 x[kRows / 4];
+          load_scores<kRows>(p, key_at + key, n_rows, x);
+          const float add = weight_of<kRows>(x, sm_lse, n_rows);
+          if (add != 0.f) p.weights[key_at + key] = before + add;
+        }
+      }
+      return;
+    }
     const long long slot = static_cast<long long>(cta) + bh;
 #pragma unroll 2
     for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads) {
@@ -625,10 +728,6 @@ __device__ __forceinline__ float2 row_total(const float2* ml, int r,
 #pragma unroll
   for (int i = 16; i > 0; i /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, i);
   return make_float2(mx, sum);
-}
-// The LSE in log2 units, -inf for a row that sees nothing.
-__device__ __forceinline__ float total_lse2(float2 t) {
-  return t.y == 0.f ? -INFINITY : t.x + log2f(t.y);
 }
 
 template <int D, int NT, bool kBF16>
@@ -744,9 +843,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
     }
     if (!live) return;
     const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
-    const int tok = r / p.group, hd = r % p.group;
-    const long long row =
-        (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
+    const long long row = out_row(p, b, h, r);
     if (lane < kCols) {
       uint2 out;
       out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
@@ -763,18 +860,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
 #pragma unroll
   for (int i = 0; i < kKeysPerThread; ++i) {
     const int key = key0 + threadIdx.x + i * kMergeThreads;
-    const float* at = p.scores + ((key_at + key) << p.score_shift);
-#pragma unroll
-    for (int k = 0; k < kRows / 4; ++k) {
-      x[i][k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (key >= len || 4 * k >= n_rows) continue;
-      if (p.score_shift >= 2) {
-        x[i][k] = *reinterpret_cast<const float4*>(at + 4 * k);
-      } else {
-        x[i][k].x = at[0];
-        if (n_rows > 1) x[i][k].y = at[1];
-      }
-    }
+    load_scores<kRows>(p, key_at + key, key < len ? n_rows : 0, x[i]);
   }
   if (threadIdx.x < kRows) sm_lse[threadIdx.x] = 0.f;
   __syncthreads();
@@ -786,30 +872,47 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
 #pragma unroll
   for (int i = 0; i < kKeysPerThread; ++i) {
     const int key = key0 + threadIdx.x + i * kMergeThreads;
-    float add = 0.f;
-#pragma unroll
-    for (int k = 0; k < kRows / 4; ++k) {
-      const float v[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)  // hidden scores and padding rows: -inf
-        if (4 * k + e < n_rows && v[e] != -INFINITY)
-          add += ptx::ex2(v[e] - sm_lse[4 * k + e]);
-    }
+    const float add = weight_of<kRows>(x[i], sm_lse, n_rows);
     if (add != 0.f) p.weights[key_at + key] = w[i] + add;
   }
 }
 
-template <int D, int NT, bool kBF16>
-cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
+// Segments of up to this many bytes of K codes (by the capacity: lengths are
+// not known here) are left to one CTA each, which needs no partials and no
+// second launch.  Cut and merged against whole, us in a graph / call by call,
+// D = 128 with 4 rows: 256 tokens of 2 segments 6.0 / 10.1 against 5.1 / 8.0,
+// of 96 9.3 / 9.9 against 5.5 / 7.9; 512 tokens of 2 segments 6.1 against 7.0,
+// of 40 9.7 against 7.3, of 256 15.1 against 10.4.  Adding weights costs a whole
+// segment 1.5 to 2 us more than the merge: 512 tokens of 40 segments 9.9
+// against 9.4, 1024 of D = 64 8.7 against 12.5, of 256 segments 18.0 against
+// 16.8.  Longer segments are whole at the price of the longest one (16
+// sequences of 0 to 2048 tokens, 16 heads: 19 us cut, 28 whole).
+constexpr long long whole_bytes(long long segs, int sms, bool weights) {
+  return (weights ? segs : 4 * segs) >= sms ? 64 * 1024 : 32 * 1024;
+}
+
+template <int D, int NT, bool kBF16, bool kWhole>
+cudaError_t launch_tiles(const FwdParams& p, long long grid,
+                         cudaStream_t stream) {
   using C = Config<D, NT>;
-  cudaError_t err = cudaFuncSetAttribute(
-      kv8_decode_kernel<D, NT, kBF16>,
+  const cudaError_t err = cudaFuncSetAttribute(
+      kv8_decode_kernel<D, NT, kBF16, kWhole>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(kv8_decode_kernel<D, NT, kBF16>, p.grid, C::kThreads,
-                   C::kBytes, stream, p);
-  if (err != cudaSuccess) return err;
+  return launch_pdl(kv8_decode_kernel<D, NT, kBF16, kWhole>, grid, C::kThreads,
+                    C::kBytes, stream, p);
+}
+
+template <int D, int NT, bool kBF16>
+cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
   const long long segs = static_cast<long long>(p.B) * p.Hkv;
+  const int sms = p.grid / Config<D, NT>::kCtas;
+  if (static_cast<long long>(p.capacity) * D <=
+      whole_bytes(segs, sms, p.scores != nullptr))
+    return launch_tiles<D, NT, kBF16, true>(p, segs, stream);
+  const cudaError_t err =
+      launch_tiles<D, NT, kBF16, false>(p, p.grid, stream);
+  if (err != cudaSuccess) return err;
   const int parts = p.scores == nullptr
                         ? 0
                         : (p.capacity + kKeysPerPart - 1) / kKeysPerPart;

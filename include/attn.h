@@ -379,7 +379,8 @@ attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
  * workspace device, 256-byte aligned, at least attn_kv8_workspace_bytes(...)
  *           bytes; contents need no initialisation.  It must not be used by
  *           another call until this one has run.
- * Two kernels on `stream`, or three (weights of more than 16 query rows per
+ * One to three kernels on `stream` (one: few rows over short caches; three:
+ * weights of more than 16 query rows per
  * K/V head).  O, LSE, weights and workspace must not overlap each other or
  * any input.  B == 0 or Sq == 0 is a successful no-op.  Deterministic for a
  * given device, shape and lengths.

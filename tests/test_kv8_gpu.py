@@ -225,6 +225,35 @@ def test_fwd(case, dtype, causal, with_w):
     check_fwd(c, q, causal, new, with_w=with_w)
 
 
+SHORT = [
+    # Caches around the sizes up to which a CTA takes a whole segment (by
+    # capacity, segments and whether weights are accumulated).
+    (4, 8, 2, 256, 128, 64, [0, 256, 1, 100], 3, [3, 0, 2, 3]),
+    (4, 8, 2, 257, 128, 64, [0, 257, 1, 100], 3, [3, 0, 2, 3]),
+    (3, 6, 2, 512, 64, 32, [0, 511, 77], 5, [5, 5, 0]),
+    (3, 6, 2, 513, 64, 32, [0, 511, 77], 5, [5, 5, 0]),
+    (3, 4, 4, 200, 64, 16, [2, 200, 5], 13, [13, 13, 9]),
+    (3, 32, 16, 512, 128, 128, [512, 0, 300], 1, None),
+    (3, 32, 16, 513, 128, 128, [512, 0, 300], 1, None),
+    (40, 16, 8, 1024, 64, 64, [(89 * i) % 1025 for i in range(40)], 2, None),
+    (40, 4, 2, 1100, 64, 32, [(97 * i) % 1101 for i in range(40)], 1, None),
+    (50, 4, 1, 600, 128, 16, [(41 * i) % 601 for i in range(50)], 3,
+     [i % 4 for i in range(50)]),
+    (2, 16, 16, 1, 128, 16, [1, 0], 1, None),
+]
+
+
+@pytest.mark.parametrize("with_w", [False, True])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", SHORT)
+def test_fwd_short(case, dtype, causal, with_w):
+    B, Hq, Hkv, cap, D, block, lens, Sq, new = case
+    c = ref.filled(B, Hkv, cap, D, block, lens, 15)
+    q = torch.randn(B, Hq, Sq, D, generator=ref.rng(16)).to(DT[dtype])
+    check_fwd(c, q, causal, new, with_w=with_w)
+
+
 LONG = [
     # Many key tiles and units for every CTA.
     (4, 32, 8, 2100, 128, 64, [2100, 2077, 1500, 2099], 250, None),
