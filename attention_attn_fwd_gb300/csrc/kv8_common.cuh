@@ -160,6 +160,7 @@ struct FwdParams {
   int group;              // query heads per K/V head
   int row_blocks;         // many rows: units of 256 per (batch, K/V head)
   int causal;
+  int whole;              // many rows: units are not split
   float scale_log2;       // scale * log2(e)
   // Workspace: partial rows and their (max, sum) of the parts of a split
   // segment or unit; few rows: the scores of every key; many rows: the unit

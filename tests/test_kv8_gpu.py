@@ -263,6 +263,14 @@ LONG = [
     (16, 32, 4, 2049, 64, 64, [2049 - 120 * i for i in range(16)], 2, None),
     (70, 8, 8, 300, 128, 32, [(37 * i) % 301 for i in range(70)], 2, None),
     (2, 16, 4, 20000, 128, 128, [20000, 13001], 4, None),
+    # Many rows, units cut.
+    (2, 32, 8, 4100, 128, 64, [4100, 3001], 250, None),
+    (4, 16, 16, 1500, 128, 16, [1500, 0, 1499, 700], 129, [129, 3, 0, 129]),
+    (33, 1, 1, 4000, 64, 128, [121 * i for i in range(33)], 20, None),
+    # Many rows, whole units, several to a CTA.
+    (20, 16, 16, 300, 128, 32, [300 - 15 * i for i in range(20)], 129, None),
+    (40, 4, 4, 300, 64, 16, [(37 * i) % 301 for i in range(40)], 70,
+     [(11 * i) % 71 for i in range(40)]),
 ]
 
 
