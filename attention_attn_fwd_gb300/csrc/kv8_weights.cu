@@ -17,13 +17,15 @@
 // no atomics, one order of sums.
 //
 // Roles (512 threads): warp 0 MMA issue, warp 1 bulk copies of raw key tiles,
-// warps 4-7 conversion of query rows and key tiles, warps 8-11 / 12-15
-// epilogue of even / odd tiles.  Every wait is bounded as in the forward
+// warps 4-7 conversion of key tiles, warps 8-15 query rows, then the epilogue
+// of even (8-11) and odd tiles.  Every wait is bounded as in the forward
 // kernel.  Measured: 2 x 64 rows of 32 heads over 8192 tokens, 7 key tiles a
-// CTA, 26 us of the call's 64 (16.1 GFLOP of products run again: 9 us at
-// cuBLAS's rate).  The start and a segment's query rows take half of it, the
-// hand-over from conversion to MMA to epilogue the rest.  The first form, on
-// mma.sync, took 77 us.
+// CTA, 24 us of the call's 62 (8 GFLOP of products run again: 4 us at cuBLAS's
+// rate).  The start and the query rows take about 13000 clocks, a tile 3400,
+// the epilogue's time (its exp2 alone would take 1000); a loop of 32 columns
+// is kept rolled, for its code is fetched anew in every launch (unrolled twice
+// 63.2 us, whole 66; 64 columns a turn 66; columns loaded a turn ahead 66).
+// The first form, on mma.sync, took 77 us.
 #include "attn_sync.cuh"
 #include "kv8_common.cuh"
 
@@ -83,7 +85,7 @@ __device__ __forceinline__ void ffma2_pairs(float& y0, float& y1, float x0,
 
 // 32 query rows to fp16 operand rows in shared memory (128-byte swizzled boxes
 // of `box` bytes, the first row at `dst`, a multiple of 8 rows from its box's
-// start), each times its row_shift's power of two, negated if `negate`.
+// start), each times its row_shift's power of two.
 // `off`: this lane's row, in elements from q, or -1 (zeros).  Returns the
 // shift of this lane's row.  The rows come by coalesced asynchronous copies
 // and are converted where they land, a row per lane, in small loops: a row of
@@ -94,7 +96,7 @@ __device__ __forceinline__ void ffma2_pairs(float& y0, float& y1, float x0,
 template <int D, bool kBF16>
 __device__ __forceinline__ int stage_rows(const void* q, long long off,
                                           uint32_t dst, uint32_t box,
-                                          bool negate, int lane) {
+                                          int lane) {
   constexpr int kChunks = D / 8;         // lanes of a row
   constexpr int kAtOnce = 32 / kChunks;  // rows of an instruction
   {
@@ -127,7 +129,7 @@ __device__ __forceinline__ int stage_rows(const void* q, long long off,
     amax = ptx::fmax3(amax, fabsf(d.x), fabsf(d.y));
   }
   const int up = row_shift(amax);
-  const float f = negate ? -exp2_int(up) : exp2_int(up);
+  const float f = exp2_int(up);
 #pragma unroll 2
   for (int k = 0; k < kChunks; ++k) {
     const uint32_t at = mine + (k / 8) * box + (((k % 8) ^ (lane % 8)) << 4);
@@ -215,10 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One arrival per warp of the role that fills or frees; raw loads and
     // MMAs arrive once.
     uint32_t count = 1;
-    if ((bar >= bar_rempty && bar < bar_empty) || bar == bar_q ||
+    if ((bar >= bar_rempty && bar < bar_empty) ||
         (bar >= bar_sfree && bar < bar_drain))
       count = 4;
-    if (bar == bar_qfree) count = 8;
+    if (bar == bar_q || bar == bar_qfree) count = 8;
     ptx::mbar_init(bar, count);
     if (threadIdx.x == 0) *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -329,35 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t out_off = (ch / 4) * L::kBox + row0 * 128;
     const uint32_t out0 = out_off + ((((ch % 4) * 2) ^ (row0 % 8)) << 4);
     const uint32_t out1 = out_off + ((((ch % 4) * 2 + 1) ^ (row0 % 8)) << 4);
-    int it = 0, pass = 0;
-    for (; more && ok; more = w.next(p), ++pass) {
-      if (pass > 0) ok = wait(bar_qfree, pass - 1, 8);
-      if (!ok) break;
-      const int bh = w.seg.b * p.Hkv + w.seg.h;
-      // Two query rows per thread.
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int r = half * 128 + tid, row = w.u * kRows + r;
-        const bool in = row < w.rows;
-        const int tok = row / p.group, hd = row - tok * p.group;
-        float lse = INFINITY;  // no weight: rows past the last, and rows
-        if (in) {              // that see nothing
-          lse = p.lse2[static_cast<long long>(bh) * lse2_rows + row];
-          if (lse == -INFINITY) lse = INFINITY;
-        }
-        const int up = stage_rows<D, kBF16>(
-            p.q,
-            in ? ((static_cast<long long>(w.seg.b) * p.Hq +
-                   w.seg.h * p.group + hd) * p.Sq + tok) * D
-               : -1,
-            s_base + L::kQ + (half * 128 + cw * 32) * 128, L::kQBox, false,
-            lane);
-        consts[(r / 2) * 4 + r % 2] = p.scale_log2 * exp2_int(-up);
-        consts[(r / 2) * 4 + 2 + r % 2] = -lse;
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar_q);
+    int it = 0;
+    for (; more && ok; more = w.next(p)) {
       for (int j = w.t0; j < w.hi && ok; ++j, ++it) {
         const int rslot = it % L::kRawSlots, slot = it % L::kSlots;
         const int valid = w.seg.len - j * kTN;  // rows that hold tokens
@@ -402,9 +377,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) +
                          buf * kRows;
     const int r = threadIdx.x % kTN;  // key of the tile
+    const int q_row = (warp - 8) * 32 + lane;  // query row this lane brings
     int pass = 0, uses = 0;
     for (; more && ok; more = w.next(p), ++pass) {
-      ok = wait(bar_q, pass, 4);  // the rows' factors and LSEs
+      // The rows of the pass, once every tile of the one before has been
+      // added up.
+      if (pass > 0) ok = wait(bar_qfree, pass - 1, 4);
+      if (!ok) break;
+      {
+        const int row = w.u * kRows + q_row;
+        const bool in = row < w.rows;
+        const int tok = row / p.group, hd = row - tok * p.group;
+        float lse = INFINITY;  // no weight: rows past the last, and rows
+        if (in) {              // that see nothing
+          lse = p.lse2[(static_cast<long long>(w.seg.b) * p.Hkv + w.seg.h) *
+                           lse2_rows + row];
+          if (lse == -INFINITY) lse = INFINITY;
+        }
+        const int up = stage_rows<D, kBF16>(
+            p.q,
+            in ? ((static_cast<long long>(w.seg.b) * p.Hq +
+                   w.seg.h * p.group + hd) * p.Sq + tok) * D
+               : -1,
+            s_base + L::kQ + (warp - 8) * 32 * 128, L::kQBox, lane);
+        consts[(q_row / 2) * 4 + q_row % 2] = p.scale_log2 * exp2_int(-up);
+        consts[(q_row / 2) * 4 + 2 + q_row % 2] = -lse;
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_q);
+      ok = wait(bar_q, pass, 4);
       const int bh = w.seg.b * p.Hkv + w.seg.h;
       const int first_row = w.u * kRows;
       const int n_rows = min(kRows, w.rows - first_row);
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sm[4] = {0.f, 0.f, 0.f, 0.f};
         auto add = [&](auto masked_tag) {
           constexpr bool kMasked = decltype(masked_tag)::value;
-#pragma unroll 2
+#pragma unroll 1
           for (int q = 0; q < kRows / 32; ++q) {
             uint32_t s[32];
             ptx::tmem_ld32(t_s + 32 * q, s);
