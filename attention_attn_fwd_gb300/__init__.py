@@ -633,7 +633,8 @@ class KV8Cache:
         self.dtypes = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16}
         self.int32, self.float32 = torch.int32, torch.float32
         self.lib, self.index = load_library(), k.device.index
-        self.current_device = torch.cuda.current_device
+        # (torch.cuda.current_device without its check for a first use.)
+        self.current_device = torch._C._cuda_getDevice
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.struct = ctypes.pointer(_KV8(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
@@ -658,12 +659,13 @@ class KV8Cache:
 def _check_tensor(name, t, shape, dtype):
     """A contiguous tensor of this shape and type.  (Whether it is memory of
     the cache's device is checked behind the C ABI, pointer by pointer.)"""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
     if t.shape != shape or t.dtype != dtype:
         raise AttnError("%s must be %s of %s, got %s of %s" % (
             name, list(shape), dtype, list(t.shape), t.dtype),
             ATTN_ERR_INVALID_ARG)
-    if not t.is_contiguous():
-        raise AttnError("%s must be contiguous" % name, ATTN_ERR_INVALID_ARG)
+    raise AttnError("%s must be contiguous" % name, ATTN_ERR_INVALID_ARG)
 
 
 def _kv8_dtype(cache, name, t):
@@ -684,7 +686,7 @@ def _kv8_call(name, f, cache, stream, *args):
     none is needed, and the stream's handle is taken without building a
     Stream object.)"""
     handle = (cache.raw_stream(cache.index) if stream is None
-              else stream.cuda_stream) or None
+              else stream.cuda_stream)
     if cache.current_device() == cache.index:
         st = f(cache.struct, *args, handle)
     else:
@@ -722,7 +724,7 @@ def kv8_append(cache, k, v, new_lens=None, stream=None):
         _check_tensor("new_lens", new_lens, (cache.B,), cache.int32)
         new_lens = new_lens.data_ptr()
     _kv8_call("attn_kv8_append", cache.lib.attn_kv8_append, cache, stream,
-              k.data_ptr() or None, v.data_ptr() or None, Sq, new_lens, dt)
+              k.data_ptr(), v.data_ptr(), Sq, new_lens, dt)
 
 
 def kv8_workspace(cache, Hq, Sq, weights=False):
@@ -750,10 +752,10 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     call on ``stream`` allocates is that stream's memory.
     """
     dt = _kv8_dtype(cache, "q", q)
-    dtype, B = q.dtype, cache.B
-    _, Hq, Sq, _ = q.shape
-    shape = (B, Hq, Sq, cache.D)
-    _check_tensor("q", q, shape, dtype)
+    dtype, B, shape = q.dtype, cache.B, q.shape
+    _, Hq, Sq, D = shape
+    if shape[0] != B or D != cache.D or not q.is_contiguous():
+        _check_tensor("q", q, (B, Hq, Sq, cache.D), dtype)
     if out is None:
         import torch
         with _kv8_memory(cache, stream):
@@ -784,7 +786,7 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     if scale is None:
         scale = cache.D ** -0.5
     _kv8_call("attn_kv8_fwd", cache.lib.attn_kv8_fwd, cache, stream,
-              q.data_ptr() or None, out.data_ptr() or None,
+              q.data_ptr(), out.data_ptr(),
               lse.data_ptr() if lse is not None else None, weights, Hq, Sq,
               new_lens, scale, bool(causal), dt, workspace.data_ptr(),
               workspace.nbytes)
@@ -837,6 +839,6 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
         _check_tensor("indices", indices, shape, torch.int32)
     _kv8_call("attn_kv8_evict", cache.lib.attn_kv8_evict, cache, stream,
               out.struct,
-              weights.data_ptr() or None, out_weights.data_ptr() or None,
-              keep, recent, indices.data_ptr() or None)
+              weights.data_ptr(), out_weights.data_ptr(), keep, recent,
+              indices.data_ptr())
     return out, out_weights, indices
