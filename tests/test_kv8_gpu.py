@@ -404,6 +404,120 @@ def test_fwd_two_streams_at_once():
         assert torch.equal(o.cpu(), a) and torch.equal(l.cpu(), b)
 
 
+@pytest.mark.parametrize("Sq", [1, 40])
+def test_fwd_buffers_of_the_least_alignment(Sq):
+    """Q and O 16 bytes, LSE, weights and scales 4 bytes aligned."""
+    c = ref.filled(2, 2, 600, 64, 32, [600, 77], 121)
+    q = torch.randn(2, 8, Sq, 64, generator=ref.rng(122)).bfloat16()
+    want = run_fwd(c, q)
+    gpu = upload(c)
+
+    def shifted(t, by):
+        """A contiguous copy `by` elements behind an aligned address."""
+        flat = torch.empty(t.numel() + by, dtype=t.dtype).cuda()[by:]
+        return flat.view(t.shape).copy_(t)
+
+    odd = attn.KV8Cache(
+        shifted(gpu.k.view(torch.uint8), 16),
+        shifted(gpu.v.view(torch.uint8), 48), shifted(gpu.k_scale, 1),
+        shifted(gpu.v_scale, 3), shifted(gpu.lens, 1), 32)
+    out = shifted(torch.full(q.shape, 7.5, dtype=q.dtype), 8)
+    assert out.data_ptr() % 32 == 16
+    lse = shifted(torch.full((2, 8, Sq), 3.25), 1)
+    w = shifted(want[3], 1)
+    attn.kv8_fwd(odd, shifted(q, 24), weights=w, out=out, lse=lse)
+    assert torch.equal(out.cpu(), want[0])
+    assert torch.equal(lse.cpu(), want[1])
+    assert torch.equal(w.cpu(), want[2])
+    x = torch.randn(2, 2, 5, 64, generator=ref.rng(123)).half()
+    gpu.lens.copy_(torch.tensor([600, 82]))
+    odd.lens.copy_(gpu.lens)
+    attn.kv8_append(gpu, x.cuda(), x.cuda())
+    attn.kv8_append(odd, shifted(x, 8), shifted(x, 24))
+    for a, b in ((gpu.k, odd.k), (gpu.v, odd.v)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(gpu.k_scale, odd.k_scale)
+    w1, w2 = w.clone(), shifted(w, 3)
+    a = attn.kv8_evict(gpu, w1, 100, 10)
+    b = attn.kv8_evict(odd, w2, 100, 10)
+    assert torch.equal(a[2], b[2]) and torch.equal(w1, w2)
+    for n in ("k", "v"):
+        assert torch.equal(getattr(gpu, n)[:, :, :100].view(torch.uint8),
+                           getattr(odd, n)[:, :, :100].view(torch.uint8))
+
+
+def test_many_rows_weights_and_eviction_on_two_streams_and_in_graphs():
+    """Two runs of append, attention with weights and eviction at once, eager
+    and as graphs that replay side by side, to the bits of one alone."""
+    def start(seed):
+        c = ref.filled(2, 2, 700, 128, 64, [650, 300], seed)
+        x = torch.randn(2, 2, 50, 128, generator=ref.rng(seed + 1)).bfloat16()
+        q = torch.randn(2, 8, 50, 128, generator=ref.rng(seed + 2)).bfloat16()
+        gpu = upload(c)
+        return dict(
+            cache=gpu, k=gpu.k.view(torch.uint8).clone(),
+            v=gpu.v.view(torch.uint8).clone(), ks=gpu.k_scale.clone(),
+            vs=gpu.v_scale.clone(), lens=gpu.lens + 50, x=x.cuda(),
+            q=q.cuda(), w=torch.zeros(2, 2, 700).cuda(),
+            out=torch.zeros(2, 8, 50, 128, dtype=torch.bfloat16).cuda(),
+            lse=torch.zeros(2, 8, 50).cuda(),
+            ws=attn.kv8_workspace(gpu, 8, 50, True),
+            dst=attn.KV8Cache.empty(2, 2, 256, 128, 64),
+            dw=torch.zeros(2, 2, 256).cuda(),
+            idx=torch.zeros(2, 2, 200, dtype=torch.int32).cuda())
+
+    def run(s):
+        g = s["cache"]
+        g.k.view(torch.uint8).copy_(s["k"])
+        g.v.view(torch.uint8).copy_(s["v"])
+        g.k_scale.copy_(s["ks"])
+        g.v_scale.copy_(s["vs"])
+        g.lens.copy_(s["lens"])
+        s["w"].zero_()
+        attn.kv8_append(g, s["x"], s["x"])
+        attn.kv8_fwd(g, s["q"], weights=s["w"], out=s["out"], lse=s["lse"],
+                     workspace=s["ws"])
+        attn.kv8_evict(g, s["w"], 200, 30, out=s["dst"], out_weights=s["dw"],
+                       indices=s["idx"])
+
+    def result(s):
+        n = int(s["dst"].lens.max())
+        return [t.clone() for t in (
+            s["out"], s["lse"], s["w"], s["dw"], s["idx"], s["dst"].lens,
+            s["dst"].k.view(torch.uint8)[:, :, :n],
+            s["dst"].v_scale[:, :, :-(-n // 64)])]
+
+    states = [start(131), start(141)]
+    want = []
+    for s in states:
+        run(s)
+        torch.cuda.synchronize()
+        want.append(result(s))
+
+    def same():
+        torch.cuda.synchronize()
+        for s, w in zip(states, want):
+            for a, b in zip(result(s), w):
+                assert torch.equal(a.cpu(), b.cpu())
+
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(10):
+        for s, st in zip(states, streams):
+            with torch.cuda.stream(st):
+                run(s)
+    same()
+    graphs = []
+    for s in states:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run(s)
+    for _ in range(10):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    same()
+
+
 # ---------------------------------------------------------------- eviction
 
 EVICTS = [
