@@ -111,20 +111,37 @@ __device__ __forceinline__ void start_after_previous() {
   ptx::griddep_launch_dependents();
 }
 
+// Launch with clusters of `cluster` CTAs (1: none).
 template <class Kernel, class... Args>
-cudaError_t launch_pdl(Kernel kernel, long long grid, int threads, int smem,
-                       cudaStream_t stream, Args... args) {
+cudaError_t launch_cluster(Kernel kernel, long long grid, int threads,
+                           int smem, int cluster, cudaStream_t stream,
+                           Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch_pdl(Kernel kernel, long long grid, int threads, int smem,
+                       cudaStream_t stream, Args... args) {
+  return launch_cluster(kernel, grid, threads, smem, 1, stream, args...);
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  ptx::cluster_arrive_release();
+  ptx::cluster_wait_acquire();
 }
 
 // Few-row forward: warps of a CTA, and CTAs an SM holds at 8 and 16 query
@@ -161,6 +178,7 @@ struct FwdParams {
   int row_blocks;         // many rows: units of 256 per (batch, K/V head)
   int causal;
   int whole;              // many rows: units are not split
+  int ranks;              // few rows: CTAs of a cluster that takes a segment
   float scale_log2;       // scale * log2(e)
   // Workspace: partial rows and their (max, sum) of the parts of a split
   // segment or unit; few rows: the scores of every key; many rows: the unit

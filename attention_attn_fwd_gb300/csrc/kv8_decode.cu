@@ -9,8 +9,9 @@
 // (CTA + segment): both only grow along the list, so no two share one.  The
 // merge kernel joins a segment's partials by their maxima.  Lengths come from
 // device memory, so the cut follows them without the host's knowing: ragged
-// batches are balanced to a tile.  Short caches take a CTA per segment instead,
-// which writes the results itself (whole_bytes below).
+// batches are balanced to a tile.  Over short caches a cluster of 1 to 8 CTAs
+// takes each segment instead and writes the results itself (cluster_ranks
+// below): its CTAs' sums meet in distributed shared memory.
 //
 // Products: S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16 in fp16,
 // 16 keys (or 16 of D) by 8 query rows: with 8 or 16 rows a 128-row
@@ -35,7 +36,7 @@
 // XORed by its row so that those reads do not share banks.  No transposes but
 // a byte permute and one movmatrix per 8 x 8 weights.
 //
-// Measured, merge included: 8 x 4096 tokens, 8 heads of 4 rows, D = 128, with
+// Measured, cut and merged: 8 x 4096 tokens, 8 heads of 4 rows, D = 128, with
 // accumulated weights 23.3 us (69 MB); 131072 tokens, 4 heads of 8 rows 32.3
 // us (134 MB, 4.2 TB/s).  With the products taken out the first two thirds of
 // that stay (15.8 and 25.0 us, the loads), the products add about 4 us and the
@@ -248,7 +249,10 @@ __device__ __forceinline__ float weight_of(const float4* x, const float* lse2,
   return add;
 }
 
-// kWhole: a CTA per segment, which writes the results itself.
+constexpr int kMaxRanks = 8;
+
+// kWhole: a CTA per segment, or a cluster of a few that divide its tiles
+// evenly, which write the results themselves.
 template <int D, int NT, bool kBF16, bool kWhole>
 __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
     kv8_decode_kernel(const FwdParams p) {
@@ -275,11 +279,17 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
   Segment seg;
   seg.pos = 0;
   int count;
+  int rank = 0;
   if constexpr (kWhole) {
-    seg.b = cta / p.Hkv;
-    seg.h = cta - seg.b * p.Hkv;
+    const int bh = cta / p.ranks;
+    rank = cta - bh * p.ranks;
+    seg.b = bh / p.Hkv;
+    seg.h = bh - seg.b * p.Hkv;
     seg.len = seq_len(p, seg.b);
-    seg.tiles = seg.end = count = (seg.len + kKeys - 1) / kKeys;
+    seg.tiles = (seg.len + kKeys - 1) / kKeys;
+    seg.pos = -(seg.tiles * rank / p.ranks);
+    seg.end = seg.tiles + seg.pos;
+    count = seg.tiles * (rank + 1) / p.ranks + seg.pos;
   } else {
     count = take_share<kKeys, kOver, kDecodeWarps>(p, cta, lane, &seg);
     if (seg.pos >= count) return;  // (also: no share)
@@ -590,10 +600,12 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
       }
     __syncthreads();
     if constexpr (kWhole) {
+      // This CTA's sums, then those of the cluster's.
+      float4* own_o = reinterpret_cast<float4*>(smem);  // (the ring is free)
+      float2* own_ml = reinterpret_cast<float2*>(smem + kRows * D * 4);
       for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads) {
         const int r = i / (D / 4), d4 = i % (D / 4);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float4 x = *reinterpret_cast<const float4*>(
@@ -602,14 +614,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
           acc.y += x.y;
           acc.z += x.z;
           acc.w += x.w;
-          sum += sm_l[w * kRows + r];
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint2 out;
-        out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
-        out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) +
-                                 out_row(p, b, h, r) * D)[d4] = out;
+        own_o[i] = acc;
       }
       if (threadIdx.x < n_rows) {
         const int r = threadIdx.x;
@@ -619,16 +625,81 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
           t.x = fmaxf(t.x, sm_m[w * kRows + r]);
           t.y += sm_l[w * kRows + r];
         }
-        const float lse2 = total_lse2(t);
-        sm_lse[r] = lse2;
-        if (p.lse != nullptr)
-          p.lse[out_row(p, b, h, r)] = lse2 * 0.69314718055994531f;
+        own_ml[r] = t;
       }
+      if (p.ranks > 1)
+        cluster_barrier();
+      else
+        __syncthreads();
+      const uint32_t at_o = ptx::smem_u32(own_o), at_ml = ptx::smem_u32(own_ml);
+      // Row r's (max, sum) and the CTAs' factors.
+      auto total = [&](int r, float* f) -> float2 {
+        if (p.ranks == 1) {
+          f[0] = 1.f;
+          return own_ml[r];
+        }
+        float2 x[kMaxRanks];
+        float2 t = make_float2(kNone, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) {
+          x[k] = make_float2(kNone, 0.f);
+          if (k < p.ranks) {
+            const uint32_t at = ptx::mapa_shared(at_ml + 8 * r, k);
+            x[k].x = ptx::ld_shared_cluster_f32(at);
+            x[k].y = ptx::ld_shared_cluster_f32(at + 4);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) t.x = fmaxf(t.x, x[k].x);
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) {
+          f[k] = ptx::ex2(x[k].x - t.x);
+          t.y += x[k].y * f[k];
+        }
+        return t;
+      };
+      for (int i = rank * C::kThreads + threadIdx.x; i < n_rows * (D / 4);
+           i += p.ranks * C::kThreads) {
+        const int r = i / (D / 4), d4 = i % (D / 4);
+        float f[kMaxRanks];
+        const float2 t = total(r, f);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.ranks == 1) {
+          acc = own_o[i];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kMaxRanks; ++k) {
+            if (k >= p.ranks) break;
+            const float4 x = ptx::ld_shared_cluster_v4(
+                ptx::mapa_shared(at_o + 16 * i, k));
+            acc.x += x.x * f[k];
+            acc.y += x.y * f[k];
+            acc.z += x.z * f[k];
+            acc.w += x.w * f[k];
+          }
+        }
+        const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
+        const long long row = out_row(p, b, h, r);
+        uint2 out;
+        out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
+        out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[d4] =
+            out;
+        if (d4 == 0 && p.lse != nullptr)
+          p.lse[row] = total_lse2(t) * 0.69314718055994531f;
+      }
+      if (p.scores != nullptr && threadIdx.x < n_rows) {
+        float f[kMaxRanks];
+        sm_lse[threadIdx.x] = total_lse2(total(threadIdx.x, f));
+      }
+      if (p.ranks > 1) ptx::cluster_arrive_release();  // peers' sums are read
       if (p.scores != nullptr && n_rows > 0) {
-        __syncthreads();  // the segment's scores and LSEs have been written
+        __syncthreads();  // the part's scores and the LSEs have been written
         const long long key_at = static_cast<long long>(bh) * p.capacity;
+        const int key_end = min(len, (count - seg.pos) * kKeys);
 #pragma unroll 2
-        for (int key = threadIdx.x; key < len; key += C::kThreads) {
+        for (int key = threadIdx.x - seg.pos * kKeys; key < key_end;
+             key += C::kThreads) {
           const float before = p.weights[key_at + key];
           float4 x[kRows / 4];
           load_scores<kRows>(p, key_at + key, n_rows, x);
@@ -636,6 +707,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
           if (add != 0.f) p.weights[key_at + key] = before + add;
         }
       }
+      if (p.ranks > 1) ptx::cluster_wait_acquire();
       return;
     }
     const long long slot = static_cast<long long>(cta) + bh;
@@ -877,18 +949,30 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
   }
 }
 
-// Segments of up to this many bytes of K codes (by the capacity: lengths are
-// not known here) are left to one CTA each, which needs no partials and no
-// second launch.  Cut and merged against whole, us in a graph / call by call,
-// D = 128 with 4 rows: 256 tokens of 2 segments 6.0 / 10.1 against 5.1 / 8.0,
-// of 96 9.3 / 9.9 against 5.5 / 7.9; 512 tokens of 2 segments 6.1 against 7.0,
-// of 40 9.7 against 7.3, of 256 15.1 against 10.4.  Adding weights costs a whole
-// segment 1.5 to 2 us more than the merge: 512 tokens of 40 segments 9.9
-// against 9.4, 1024 of D = 64 8.7 against 12.5, of 256 segments 18.0 against
-// 16.8.  Longer segments are whole at the price of the longest one (16
-// sequences of 0 to 2048 tokens, 16 heads: 19 us cut, 28 whole).
-constexpr long long whole_bytes(long long segs, int sms, bool weights) {
-  return (weights ? segs : 4 * segs) >= sms ? 64 * 1024 : 32 * 1024;
+// CTAs of the cluster that takes a segment, which saves the partials and the
+// second launch; 0: the list is cut and merged.  Decided by the capacity
+// (lengths are not known here), and alike with and without weights, so that
+// these change no bit of O: 256 tokens a CTA, fewer and larger parts where
+// clusters of that size were not all on the machine at once, up to 512 tokens
+// and only with segments enough to fill it.
+//
+// Cut against clusters, us a call (in a graph), D = 128, 4 rows: 512 tokens of
+// 2 segments 9.4 (6.2) against 8.0 (6.5), of 32 10.1 (9.7) against 7.9 (6.9),
+// of 256 15.4 (15.3) against 11.1 (10.9); 2048 tokens of 2 segments 9.5 (7.0)
+// against 7.9 (7.3), of 32 12.9 (12.3) against 9.5 (8.9), of 96 18.6 against
+// 14.5; 16 rows with weights, 512 tokens of 256 segments 28.7 against 19.5.
+// In a graph a few segments with weights lose up to a fifth (1024 tokens of 2
+// segments 6.6 against 8.2; call by call 10.0 against 8.6).  Larger parts pay
+// for the longest sequence (16 of 0 to 2048 tokens, 16 heads of D = 64, with
+// weights: 19 cut, 28 with a CTA each).
+int cluster_ranks(const FwdParams& p, int ctas) {
+  const long long segs = static_cast<long long>(p.B) * p.Hkv;
+  constexpr int kPart = 256;
+  int ranks = 1;
+  while (ranks < kMaxRanks && p.capacity > ranks * kPart) ranks *= 2;
+  while (ranks > 1 && segs * ranks > p.grid) ranks /= 2;
+  const bool many = 8 * segs >= p.grid / ctas;
+  return p.capacity <= ranks * (many ? 2 * kPart : kPart) ? ranks : 0;
 }
 
 template <int D, int NT, bool kBF16, bool kWhole>
@@ -899,17 +983,17 @@ cudaError_t launch_tiles(const FwdParams& p, long long grid,
       kv8_decode_kernel<D, NT, kBF16, kWhole>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
-  return launch_pdl(kv8_decode_kernel<D, NT, kBF16, kWhole>, grid, C::kThreads,
-                    C::kBytes, stream, p);
+  return launch_cluster(kv8_decode_kernel<D, NT, kBF16, kWhole>, grid,
+                        C::kThreads, C::kBytes, kWhole ? p.ranks : 1, stream,
+                        p);
 }
 
 template <int D, int NT, bool kBF16>
-cudaError_t launch_rows(const FwdParams& p, cudaStream_t stream) {
+cudaError_t launch_rows(FwdParams p, cudaStream_t stream) {
   const long long segs = static_cast<long long>(p.B) * p.Hkv;
-  const int sms = p.grid / Config<D, NT>::kCtas;
-  if (static_cast<long long>(p.capacity) * D <=
-      whole_bytes(segs, sms, p.scores != nullptr))
-    return launch_tiles<D, NT, kBF16, true>(p, segs, stream);
+  p.ranks = cluster_ranks(p, Config<D, NT>::kCtas);
+  if (p.ranks > 0)
+    return launch_tiles<D, NT, kBF16, true>(p, segs * p.ranks, stream);
   const cudaError_t err =
       launch_tiles<D, NT, kBF16, false>(p, p.grid, stream);
   if (err != cudaSuccess) return err;

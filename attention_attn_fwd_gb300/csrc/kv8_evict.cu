@@ -59,11 +59,6 @@ __device__ __forceinline__ uint32_t ld_peer(const void* p, uint32_t rank) {
   return static_cast<uint32_t>(ptx::ld_shared_cluster_s32(
       ptx::mapa_shared(ptx::smem_u32(p), rank)));
 }
-__device__ __forceinline__ void cluster_barrier() {
-  ptx::cluster_arrive_release();
-  ptx::cluster_wait_acquire();
-}
-
 // kQuads: quads of keys a thread holds; element e of quad i of thread t is
 // place 4 (1024 i + t) + e of the CTA's part.  Longer parts are walked in
 // turns of 4096 kQuads places, their keys read again in each pass.
@@ -484,28 +479,6 @@ __global__ void __launch_bounds__(kMoveThreads)
     if (bh % p.Hkv == 0 && rank == 0 && threadIdx.x == 0)
       p.dst_lens[b] = n_kept;
   }
-}
-
-// Launch with clusters of `cluster` CTAs (1: none).
-template <class Kernel, class... Args>
-cudaError_t launch_cluster(Kernel kernel, long long grid, int threads,
-                           int smem, int cluster, cudaStream_t stream,
-                           Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D>

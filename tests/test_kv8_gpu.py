@@ -240,6 +240,12 @@ SHORT = [
     (50, 4, 1, 600, 128, 16, [(41 * i) % 601 for i in range(50)], 3,
      [i % 4 for i in range(50)]),
     (2, 16, 16, 1, 128, 16, [1, 0], 1, None),
+    # Clusters of up to 8, with fewer tiles than CTAs, and none.
+    (3, 8, 2, 2000, 128, 64, [2000, 3, 0], 1, None),
+    (3, 8, 2, 2000, 128, 64, [1999, 17, 700], 3, [3, 1, 0]),
+    (2, 16, 2, 1500, 64, 32, [1500, 40], 2, None),
+    (2, 16, 2, 4000, 64, 128, [4000, 2049], 2, [2, 1]),
+    (5, 32, 8, 4000, 128, 128, [4000, 0, 1, 2222, 333], 1, None),
 ]
 
 
@@ -263,6 +269,7 @@ LONG = [
     (16, 32, 4, 2049, 64, 64, [2049 - 120 * i for i in range(16)], 2, None),
     (70, 8, 8, 300, 128, 32, [(37 * i) % 301 for i in range(70)], 2, None),
     (2, 16, 4, 20000, 128, 128, [20000, 13001], 4, None),
+    (40, 8, 8, 1100, 128, 64, [(97 * i) % 1101 for i in range(40)], 2, None),
     # Many rows, units cut.
     (2, 32, 8, 4100, 128, 64, [4100, 3001], 250, None),
     (4, 16, 16, 1500, 128, 16, [1500, 0, 1499, 700], 129, [129, 3, 0, 129]),
