@@ -139,9 +139,18 @@ cudaError_t launch_pdl(Kernel kernel, long long grid, int threads, int smem,
   return launch_cluster(kernel, grid, threads, smem, 1, stream, args...);
 }
 
-__device__ __forceinline__ void cluster_barrier() {
+// (The cluster's barrier wants whole warps, as loops may have left them apart.)
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   ptx::cluster_arrive_release();
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   ptx::cluster_wait_acquire();
+}
+__device__ __forceinline__ void cluster_barrier() {
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Few-row forward: warps of a CTA, and CTAs an SM holds at 8 and 16 query

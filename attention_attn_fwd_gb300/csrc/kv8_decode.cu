@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
         float f[kMaxRanks];
         sm_lse[threadIdx.x] = total_lse2(total(threadIdx.x, f));
       }
-      if (p.ranks > 1) ptx::cluster_arrive_release();  // peers' sums are read
+      if (p.ranks > 1) cluster_arrive();  // peers' sums are read
       if (p.scores != nullptr && n_rows > 0) {
         __syncthreads();  // the part's scores and the LSEs have been written
         const long long key_at = static_cast<long long>(bh) * p.capacity;
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
           if (add != 0.f) p.weights[key_at + key] = before + add;
         }
       }
-      if (p.ranks > 1) ptx::cluster_wait_acquire();
+      if (p.ranks > 1) cluster_wait();
       return;
     }
     const long long slot = static_cast<long long>(cta) + bh;

@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
       above += static_cast<int>(ld_peer(&sh.count.x, r));
       equal += static_cast<int>(ld_peer(&sh.count.y, r));
     }
-    ptx::cluster_arrive_release();  // awaited at the end: peers' reads
+    cluster_arrive();  // awaited at the end: peers' reads
   }
   for (int t = 0; t < turns; ++t) {
     const int at = a0 + t * kTurn;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     equal += n.y;
     if (turns > 1) __syncthreads();  // the counts have been read
   }
-  if (ranks > 1) ptx::cluster_wait_acquire();
+  if (ranks > 1) cluster_wait();
 }
 
 constexpr int kMoveThreads = 512;  // most; two chunks of 16 codes a thread

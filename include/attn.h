@@ -379,11 +379,11 @@ attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
  * workspace device, 256-byte aligned, at least attn_kv8_workspace_bytes(...)
  *           bytes; contents need no initialisation.  It must not be used by
  *           another call until this one has run.
- * One to three kernels on `stream` (one: few rows over short caches; three:
- * weights of more than 16 query rows per
- * K/V head).  O, LSE, weights and workspace must not overlap each other or
- * any input.  B == 0 or Sq == 0 is a successful no-op.  Deterministic for a
- * given device, shape and lengths.
+ * One to three kernels on `stream` (one over short caches, three with weights
+ * of more than 16 query rows per K/V head).  O, LSE, weights and workspace must
+ * not overlap each other or any input.  B == 0 or Sq == 0 is a successful
+ * no-op.  Deterministic for a given device, shape and lengths; O and LSE are
+ * the same with and without weights.
  */
 attn_status_t attn_kv8_fwd(const attn_kv8_t* cache, const void* Q, void* O,
                            float* LSE, float* weights, int Hq, int Sq,

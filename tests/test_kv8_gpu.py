@@ -393,6 +393,16 @@ def test_fwd_is_deterministic_and_replays_in_a_graph(Sq):
     assert torch.equal(w.cpu().view(torch.int32), want[2].view(torch.int32))
 
 
+@pytest.mark.parametrize("cap", [200, 700, 1500, 5000])
+@pytest.mark.parametrize("Sq", [1, 4, 30])
+def test_fwd_results_do_not_depend_on_weights(Sq, cap):
+    c = ref.filled(3, 4, cap, 64, 64, [cap, 3, cap // 2], 151)
+    q = torch.randn(3, 16, Sq, 64, generator=ref.rng(152)).half()
+    a = run_fwd(c, q, with_w=True)
+    b = run_fwd(c, q, with_w=False)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_fwd_two_streams_at_once():
     c = ref.filled(2, 2, 900, 64, 32, [900, 450], 61)
     q = [torch.randn(2, 4, 3, 64, generator=ref.rng(s)).half()
