@@ -32,7 +32,7 @@
 // 12-15 K and V conversion.  Every wait is bounded as in the forward kernel.
 //
 // Measured: 8 x 512 rows of 32 heads over 4096 tokens of 8 heads, D = 128,
-// causal (258 GFLOP): 233 us, 1.11 PFLOP/s, against 187 for the 16-bit forward
+// causal (258 GFLOP): 234 us, 1.10 PFLOP/s, against 187 for the 16-bit forward
 // kernel on the same numbers.  A step (256 rows, 128 keys) takes about 3400
 // clocks against 2048 of MMAs.  Nothing alone bounds it: with the conversion
 // left out the call (then 238 us) took 223, with exp2 left out 235, with both
