@@ -25,7 +25,8 @@ SOURCES = ["attn_api.cu", "attn_fwd_d64.cu", "attn_fwd_d128.cu",
 HEADERS = ["attn_fwd_kernel.cuh", "attn_fwd_launch.cuh", "attn_sync.cuh",
            "fast_div.h",
            "attn_bwd_kernel.cuh", "attn_merge_kernel.cuh",
-           "sm103_ptx.cuh", "attn_launch.h", "attn_host.h", "kv8_common.cuh"]
+           "sm103_ptx.cuh", "attn_launch.h", "attn_host.h", "kv8_common.cuh",
+           "kv8_index.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -58,8 +58,10 @@ attn_status_t check_cache_sizes(const attn_kv8_t* c) {
     return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(c->B) * c->Hkv >= (1 << 24))
     return ATTN_ERR_INVALID_ARG;
-  // Places past the end that the kernels count to (a select turn of 16384
-  // tokens at most) must stay within int32.
+  // Places that the kernels count to behind a length (a turn of the select
+  // kernel or an in-place round of moved weights, 16384 tokens each, at most)
+  // must stay within int32.  Sums of two token counts are not among them: they
+  // are taken by kv8_index.h.
   if (c->capacity >= 0x7fffffff - (1 << 16)) return ATTN_ERR_INVALID_ARG;
   if (c->D != 64 && c->D != 128) return ATTN_ERR_UNSUPPORTED;
   if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)

@@ -15,6 +15,7 @@
 // rate); 8-byte stores and a division per element took 39.6.  One new token
 // per sequence: 6.7 us, the call itself.
 #include "kv8_common.cuh"
+#include "kv8_index.h"
 
 namespace attn {
 namespace kv8 {
@@ -49,9 +50,10 @@ __global__ void __launch_bounds__(unit_threads<D, kBlock>(),
           ? clamp_len(p.Sq, len, p.status)
           : clamp_len(p.new_lens[b], min(p.Sq, len), p.status);
   const int start = len - n_new;  // position of the first new token
-  const int blk = start / kBlock + u;
+  if (n_new == 0) return;
+  const int blk = append_block(start, len, kBlock, u);
+  if (blk < 0) return;
   const int base = blk * kBlock;  // first token of the block
-  if (base >= len || n_new == 0) return;
 
   // Tokens [base, start) of the block are held already, [t0, t1) are new.
   const int t0 = max(start, base), t1 = min(len, base + kBlock);
