@@ -26,6 +26,7 @@
 // rows has come).  Keys one per lane instead of in quads: 31.8 us on the long
 // one; one CTA per head for the select 191 us.
 #include "kv8_common.cuh"
+#include "kv8_index.h"
 
 namespace attn {
 namespace kv8 {
@@ -432,7 +433,7 @@ __device__ __forceinline__ void move_weights(const EvictParams& p, int bh,
   const int threads = blockDim.x;
   const int per = 4 * threads;  // tokens a CTA moves per round
   const int step = per * ranks;
-  const int rounds = (n_kept + step - 1) / step;
+  const int rounds = round_count(n_kept, step);
   for (int rd = 0; rd < rounds; ++rd) {
     const int t0 = rd * step + rank * per + threadIdx.x;
     float w[4];
@@ -449,7 +450,7 @@ __device__ __forceinline__ void move_weights(const EvictParams& p, int bh,
     }
   }
   // Every read of the sources is behind the last round's barrier.
-  for (int tok = n_kept + rank * threads + threadIdx.x;
+  for (long long tok = cleared_place(n_kept, rank, threads, threadIdx.x);
        tok < p.dst_capacity; tok += ranks * threads)
     dst[tok] = 0.f;
 }

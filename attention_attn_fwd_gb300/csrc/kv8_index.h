@@ -22,5 +22,20 @@ ATTN_KV8_INDEX int append_block(int start, int len, int block, int u) {
   return blk <= (len - 1) / block ? blk : -1;
 }
 
+// Rounds of `step` places that cover n >= 0 of them.  (Into another cache a
+// round has as many places as that cache: n + step passes 2^31 from half of
+// the largest capacity on.)
+ATTN_KV8_INDEX int round_count(int n, int step) {
+  return n / step + (n % step != 0 ? 1 : 0);
+}
+
+// The first place behind n kept ones that a thread clears, with `rank`
+// thread blocks before its own: n and a quarter of the capacity at most.
+ATTN_KV8_INDEX long long cleared_place(int n, int rank, int threads,
+                                       int thread) {
+  return static_cast<long long>(n) + static_cast<long long>(rank) * threads +
+         thread;
+}
+
 }  // namespace kv8
 }  // namespace attn

@@ -91,3 +91,40 @@ int main() {
     }
   }
 """)
+
+
+def test_moved_weights_reach_every_place(tmp_path):
+    """Rounds and cleared places of an eviction into a cache of up to the
+    largest capacity, and in place."""
+    run(tmp_path, r"""
+int main() {
+  auto check = [&](ll cap, ll kept, ll threads, bool in_place) {
+    const ll ranks = in_place ? 8 : (cap - 1) / (4 * threads) + 1;
+    const ll step = 4 * threads * ranks;
+    const ll want = (kept + step - 1) / step;
+    const ll got = round_count(static_cast<int>(kept), static_cast<int>(step));
+    ll wrong = got != want;
+    for (ll rank : {0ll, 1ll, ranks / 2, ranks - 1})
+      for (ll t : {0ll, threads - 1}) {
+        if (rank < 0 || rank >= ranks) continue;
+        const ll place = cleared_place(
+            static_cast<int>(kept), static_cast<int>(rank),
+            static_cast<int>(threads), static_cast<int>(t));
+        wrong += place != kept + rank * threads + t;
+      }
+    ++n;
+    if (wrong != 0 && bad++ < 5)
+      std::printf("cap %lld kept %lld threads %lld: %lld rounds of %lld\n",
+                  cap, kept, threads, got, want);
+  };
+  for (ll threads : {32, 64, 128, 256, 512})
+    for (bool in_place : {false, true}) {
+      for (ll cap : {kMost, kMost - 1, (1ll << 30) - 1, 1ll << 30, 5000ll, 1ll})
+        for (ll kept : {cap, cap - 1, cap / 2, 1ll, 0ll})
+          check(cap, kept, threads, in_place);
+      for (int i = 0; i < 50000; ++i) {
+        const ll cap = rnd(1, kMost);
+        check(cap, rnd(0, cap), threads, in_place);
+      }
+    }
+""")
