@@ -41,11 +41,13 @@ __device__ __forceinline__ float exp2_int(int e) {  // -126 <= e <= 127
   return __int_as_float((e + 127) << 23);
 }
 
-// 1 / s of a positive normal number: exact for powers of two up to 2^126.
+__device__ __forceinline__ bool is_power_of_two(float s) {  // s normal
+  return (__float_as_int(s) & 0x7fffff) == 0;
+}
+
+// 1 / s of a normal power of two, exact (2^127's is the subnormal 2^-127).
 __device__ __forceinline__ float reciprocal(float s) {
-  const int bits = __float_as_int(s);
-  return (bits & 0x7fffff) == 0 ? __int_as_float((254 << 23) - bits)
-                                : ptx::rcp(s);
+  return __int_as_float(max((254 << 23) - __float_as_int(s), 1 << 22));
 }
 
 // Magnitude that counts for a scale: finite values only.

@@ -338,7 +338,7 @@ typedef struct {
  * are requantised, round(code * old / new) -- with powers of two an exponent
  * shift, exact unless the result is subnormal.  New codes are
  * round(x / scale): to nearest, ties to even (a scale of other origin: after
- * the fp32 rounding of x times its reciprocal); infinities become +-448, NaN
+ * the fp32 rounding of the quotient); infinities become +-448, NaN
  * stays NaN.  Nothing else of the cache is written.  Sq <= capacity.
  * Deterministic.
  */

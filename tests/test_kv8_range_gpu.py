@@ -1,0 +1,47 @@
+"""8-bit cache operators at the ends of their range, on the GPU against the
+float64 reference."""
+import math
+
+import pytest
+import torch
+
+import attention_attn_fwd_gb300 as attn
+from tests import kv8_reference as ref
+from tests.test_kv8_gpu import (  # noqa: F401
+    built, clean_status, same_cache, upload)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ large scales
+
+@pytest.mark.parametrize("D,block", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("scale", [
+    2.0 ** 125, 2.0 ** 126, 2.0 ** 127, 1.5 * 2.0 ** 126, 1.75 * 2.0 ** 127,
+    1.25 * 2.0 ** -126])
+def test_append_into_a_block_that_keeps_a_scale_at_the_end_of_the_range(
+        scale, D, block):
+    c = ref.filled(1, 2, 40, D, block, [5], 1)
+    for n in "kv":
+        c.scale[n][:, :, 0] = scale
+    g = ref.rng(7)
+    x = (torch.rand(1, 2, 9, D, generator=g) * 2 - 1).double()
+    x = x * torch.exp2((-8 * torch.rand(1, 2, 9, 1, generator=g)).double())
+    # Up to 2^127.99 or 440 scales, whichever is less.
+    x = (x * min(2.0 ** 127.99, 440 * scale)).bfloat16()
+    c.lens = [14]
+    gpu = upload(c)
+    attn.kv8_append(gpu, x.cuda(), x.cuda())
+    c.append(x, x)
+    if math.frexp(scale)[0] == 0.5:  # a power of two: exact
+        same_cache(gpu, c)
+        return
+    # The quotient's fp32 rounding moves it across a tie at most: codes differ
+    # by one step, and seldom.
+    for n in "kv":
+        a = getattr(gpu, n).view(torch.uint8).cpu()[:, :, :14].int()
+        b = c.code[n][:, :, :14].int()
+        assert int((a - b).abs().max()) <= 1
+        assert float((a != b).float().mean()) < 0.01
+        assert torch.equal(getattr(gpu, n + "_scale").cpu().double(),
+                           c.scale[n])
