@@ -325,6 +325,25 @@ __device__ __forceinline__ uint32_t half2x2_to_e4m3(uint32_t lo, uint32_t hi) {
   return d;
 }
 
+// Key of a magnitude for the comparison of magnitudes and for a scale: its
+// bits as an fp32 number, and past fp32's range (a code of 448 under a scale of
+// 2^127 is 2^136) what they would be with another exponent bit.
+__device__ __forceinline__ uint32_t magnitude_key(float code, float factor) {
+  const uint32_t key = __float_as_uint(code * factor);
+  return key < 0x7f800000u
+             ? key
+             : __float_as_uint(code * (factor * 0x1p-16f)) + (16u << 23);
+}
+
+// Its tight scale's exponent (cf. tight_exponent), fp32's largest at most: a
+// scale between 2^127 and 2^128 may have made numbers past 448 * 2^127, which
+// become 448.
+__device__ __forceinline__ int tight_exponent_of_key(uint32_t key) {
+  const int e = static_cast<int>(key >> 23) - 127 - 8 +
+                ((key & 0x7fffff) > 0x600000);
+  return min(max(e, -126), 127);
+}
+
 // The codes of K or V of one head: destination blocks rank, rank + ranks, ...
 template <int D, bool kInPlace>
 __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
@@ -332,7 +351,7 @@ __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
                                            int len, int n_kept) {
   constexpr int kPerRow = D / 16;                       // 16-byte chunks
   constexpr int kMax = 2;
-  __shared__ float red[kMoveThreads / 32];
+  __shared__ uint32_t red[kMoveThreads / 32];
   const int threads = blockDim.x;  // of a block's chunks, half as many
   const int block = 1 << p.block_shift;
   const bool whole = len <= p.keep;  // nothing leaves: bit for bit
@@ -352,7 +371,7 @@ __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
     const int t0 = nb << p.block_shift;
     uint4 held[kMax];
     float factor[kMax];
-    float amax = 0.f;
+    uint32_t largest = 0u;
 #pragma unroll
     for (int i = 0; i < kMax; ++i) {
       const int ch = threadIdx.x + i * threads;
@@ -368,11 +387,9 @@ __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
     }
 #pragma unroll
     for (int i = 0; i < kMax; ++i)
-      amax = fmaxf(amax, finite_abs(codes_amax(held[i]) * factor[i]));
-#pragma unroll
-    for (int s = 16; s > 0; s /= 2)
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = amax;
+      largest = max(largest, magnitude_key(codes_amax(held[i]), factor[i]));
+    largest = __reduce_max_sync(0xffffffffu, largest);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = largest;
     float first = 0.f;  // the block's scale, where nothing leaves
     if (whole && threadIdx.x == 0 && nb < blocks) first = src_scale[nb];
     if constexpr (kInPlace) {
@@ -381,8 +398,8 @@ __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
     } else {
       __syncthreads();
     }
-    for (int i = 0; i < threads / 32; ++i) amax = fmaxf(amax, red[i]);
-    const float now = exp2_int(tight_exponent(amax));
+    for (int i = 0; i < threads / 32; ++i) largest = max(largest, red[i]);
+    const float now = exp2_int(tight_exponent_of_key(largest));
     const float inv = reciprocal(now);
     if (threadIdx.x == 0 && nb < blocks) dst_scale[nb] = whole ? first : now;
 #pragma unroll
@@ -406,12 +423,14 @@ __device__ __forceinline__ void move_codes(const EvictParams& p, int kv,
           w[e] = half2x2_to_e4m3(hmul2(lo, r2), hmul2(hi, r2));
         }
       } else {  // a scale of other origin, or out of fp16's range
+        // (Past 2^18 only for zeros, which stay zeros.)
+        const float r = fminf(ratio, 0x1p100f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float f[4];
           e4m3x4_to_float(w[e], f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = f[j] * factor[i] * inv;
+          for (int j = 0; j < 4; ++j) f[j] *= r;
           w[e] = ptx::pack4_e4m3(f[0], f[1], f[2], f[3]);
         }
       }

@@ -331,8 +331,8 @@ typedef struct {
  * dtype     ATTN_F16 or ATTN_BF16.
  *
  * Let a be the largest finite magnitude among the new tokens of one block of
- * one head, and tight(a) the smallest power of two (2^-126 at least) with
- * a <= 448 * tight(a).  A block that holds no earlier token gets the scale
+ * one head, and tight(a) the smallest power of two (2^-126 at least, 2^127 at
+ * most) with a <= 448 * tight(a).  A block that holds no earlier token gets the scale
  * tight(a).  A block begun by earlier calls keeps its scale when
  * a <= 448 * scale; else its scale becomes tight(a) and the codes it holds
  * are requantised, round(code * old / new) -- with powers of two an exponent

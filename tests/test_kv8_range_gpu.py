@@ -45,3 +45,34 @@ def test_append_into_a_block_that_keeps_a_scale_at_the_end_of_the_range(
         assert float((a != b).float().mean()) < 0.01
         assert torch.equal(getattr(gpu, n + "_scale").cpu().double(),
                            c.scale[n])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("top", [120, 127])
+def test_evict_of_numbers_past_the_largest_fp32(top, in_place):
+    """A code times its scale may exceed 2^128 (bf16's largest numbers round
+    up to it): the kept block's scale is still that of its largest number."""
+    B, H, cap, D, block, keep = 1, 2, 256, 64, 16, 90
+    c = ref.filled(B, H, cap, D, block, [cap], 75)
+    g = ref.rng(76)
+    for n in "kv":
+        e = torch.randint(0, 9, c.scale[n].shape, generator=g)
+        c.scale[n] = torch.exp2((top - e).double())
+        # Blocks of zeros under every scale, and of the smallest ones.
+        c.code[n][:, :, 32:48] = 0
+        c.code[n][:, :, 0:16, 0] = 0x7E
+        c.scale[n][:, :, 5] = 2.0 ** -126
+        c.scale[n][:, :, 6] = 2.0 ** -120
+    w = torch.rand(B, H, cap, generator=g)
+    want, ow, idx = c.evict(w, keep, 10, cap)
+    gpu = upload(c)
+    out = None if in_place else upload(ref.Cache(B, H, cap, D, block))
+    out, out_w, got = attn.kv8_evict(gpu, w.cuda(), keep, 10, out=out)
+    assert torch.equal(got.cpu(), idx)
+    assert torch.equal(out_w.cpu(), ow)
+    if in_place:
+        nb = -(-keep // block)
+        for n in "kv":
+            want.code[n][:, :, keep:] = c.code[n][:, :, keep:]
+            want.scale[n][:, :, nb:] = c.scale[n][:, :, nb:]
+    same_cache(out, want)
