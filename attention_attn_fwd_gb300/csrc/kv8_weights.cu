@@ -446,9 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) {
               const float4 k = c4[e];
               float x0, x1;
-              ffma2_pairs(x0, x1, __uint_as_float(s[2 * e]) * ks,
-                          __uint_as_float(s[2 * e + 1]) * ks, k.x, k.y, k.z,
-                          k.w);
+              // (The factors first: a score reaches 2^30 times K's scale
+              // before its row's factor, past fp32 under large scales.)
+              ffma2_pairs(x0, x1, __uint_as_float(s[2 * e]),
+                          __uint_as_float(s[2 * e + 1]), ks * k.x, ks * k.y,
+                          k.z, k.w);
               float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
               if constexpr (kMasked) {
                 const int c0 = 32 * q + 2 * e;

@@ -8,7 +8,7 @@ import torch
 import attention_attn_fwd_gb300 as attn
 from tests import kv8_reference as ref
 from tests.test_kv8_gpu import (  # noqa: F401
-    built, clean_status, same_cache, upload)
+    built, check_fwd, clean_status, same_cache, upload)
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,13 @@ def test_evict_of_numbers_past_the_largest_fp32(top, in_place):
             want.code[n][:, :, keep:] = c.code[n][:, :, keep:]
             want.scale[n][:, :, nb:] = c.scale[n][:, :, nb:]
     same_cache(out, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq", [2, 64, 150])
+def test_fwd_weights_of_keys_near_the_largest_fp32(Sq, D):
+    """Keys of 2^115 under queries of 2^-112: scores of ordinary size."""
+    c = ref.filled(2, 2, 300, D, 32, [300, 170], 161)
+    c.scale["k"] *= 2.0 ** 115
+    q = torch.randn(2, 4, Sq, D, generator=ref.rng(162)) * 2.0 ** -112
+    check_fwd(c, q.bfloat16(), scale=0.125 / math.sqrt(D))
