@@ -22,8 +22,10 @@
 // (below fp32 accumulation's own rounding).  Block scales multiply scores and
 // weights in fp32.  P is rounded to fp16 (2^-11 relative, the rounding of an
 // fp16 output itself and an eighth of a bf16 one's), shifted by 2^7 so that
-// weights down to 2^-21 of the row's largest stay normal numbers.  The row
-// sums take P unrounded.
+// weights down to 2^-21 of the row's largest stay normal numbers.  V's scales
+// are kept out of it, for each factor of two between two blocks would cost P a
+// bit of its range: O is held in units of the scale of the keys at hand and
+// multiplied, in fp32, when that changes.  The row sums take P unrounded.
 //
 // Codes reach shared memory by 16-byte asynchronous copies, a ring of tiles
 // per warp that runs ahead across segments (128 to 144 KB in flight per SM;
@@ -57,6 +59,9 @@ constexpr int kOver = 12;
 constexpr float kTau = 8.f;        // lazy rescale threshold (log2 units)
 constexpr float kMinUnit = 1.17549435e-38f;  // 2^-126, the smallest block scale
 constexpr float kPScale = 128.f;   // 2^7: P <= 2^(8 + 7) < 65504
+// Least unit of O against the largest V scale met: O stays below 2^128 (2^64
+// times 448, 2^15 of P and up to 2^31 keys).
+constexpr float kLeastUnit = 0x1p-64f;
 
 // Keys of a list tile: 2 KB of K codes.
 template <int D>
@@ -369,8 +374,10 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
     const float* vsb = p.v_scale + static_cast<long long>(bh) * p.nblk;
 
     float m[NT][2], l[NT][2], o[NT][kMT][4];
-    // O is held in units of a V scale (times 2^7).
-    float unit = kMinUnit, inv_unit = 1.f / kMinUnit;
+    // O is held in units of a V scale (times 2^7): that of the keys before,
+    // `vs_last`, or one 2^64 below the largest, `vs_most`, if that is more.
+    float unit = kMinUnit, vs_last = kMinUnit, vs_most = kMinUnit;
+    float p_factor = kPScale;  // 2^7 vs_last / unit
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = kNone;
@@ -467,19 +474,28 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
                     make_float2(s[nt][2 * i], s[nt][2 * i + 1]);
             }
         }
-        bool grow = vs > unit;
+        if (vs != vs_last) {  // O to the unit of these keys
+          vs_last = vs;
+          vs_most = fmaxf(vs_most, vs);
+          const float now = fmaxf(vs, vs_most * kLeastUnit);
+          const float f = unit / now;
+          unit = now;
+          p_factor = vs / now * kPScale;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][i][e] *= f;
+        }
+        bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             grow |= fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + kTau;
-        // Lazy rescale: some row's maximum grew by more than 2^8, or a
-        // block's V scale exceeds the unit O is held in.
+        // Lazy rescale: some row's maximum grew by more than 2^8.
         if (__any_sync(0xffffffffu, grow)) {
-          const float unit_new = fmaxf(unit, vs);
-          const float f_unit = unit / unit_new;
-          unit = unit_new;
-          inv_unit = 1.f / unit;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -492,16 +508,14 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
               const float alpha = ptx::ex2(m[nt][e] - m_new);
               m[nt][e] = m_new;
               l[nt][e] *= alpha;
-              const float f = alpha * f_unit;
 #pragma unroll
               for (int i = 0; i < kMT; ++i) {
-                o[nt][i][e] *= f;
-                o[nt][i][e + 2] *= f;
+                o[nt][i][e] *= alpha;
+                o[nt][i][e + 2] *= alpha;
               }
             }
         }
-        // P^T in fp16, times 2^7 and the block's V scale over the unit.
-        const float pf = vs * inv_unit * kPScale;
+        // P^T in fp16, times 2^7.
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -513,9 +527,9 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
             l[nt][e & 1] += w[e];
           }
           pb[nt][0] =
-              movmatrix_trans(ptx::pack2<false>(w[0] * pf, w[1] * pf));
+              movmatrix_trans(ptx::pack2<false>(w[0] * p_factor, w[1] * p_factor));
           pb[nt][1] =
-              movmatrix_trans(ptx::pack2<false>(w[2] * pf, w[3] * pf));
+              movmatrix_trans(ptx::pack2<false>(w[2] * p_factor, w[3] * p_factor));
         }
         // O^T += V^T P^T: V rows 2c, 2c + 1, 2c + 8, 2c + 9 of the step.
         constexpr int kVWords = D / 32;

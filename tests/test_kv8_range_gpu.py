@@ -8,7 +8,7 @@ import torch
 import attention_attn_fwd_gb300 as attn
 from tests import kv8_reference as ref
 from tests.test_kv8_gpu import (  # noqa: F401
-    built, check_fwd, clean_status, same_cache, upload)
+    built, check_fwd, clean_status, run_fwd, same_cache, upload)
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,75 @@ def test_fwd_weights_of_keys_near_the_largest_fp32(Sq, D):
     c.scale["k"] *= 2.0 ** 115
     q = torch.randn(2, 4, Sq, D, generator=ref.rng(162)) * 2.0 ** -112
     check_fwd(c, q.bfloat16(), scale=0.125 / math.sqrt(D))
+
+
+# --------------------------------------------------- V scales far apart
+
+def uneven(B, H, cap, D, block, gap, big):
+    """A cache whose first `big` tokens have V scales `gap` times the others'
+    and next to no weight under q = (1, 0, ..), followed by `big` tokens of
+    weight 1 whose values are 0 in the first half of D; the rest share weights
+    of 2^-11 to 2^-19 and values of one sign."""
+    g = ref.rng(171)
+    some = min(2, H)  # heads that differ
+    k = torch.randn(1, some, cap, D, generator=g) * 0.5
+    k[..., 0] = -7.5 - 5.5 * torch.rand(1, some, cap, generator=g)
+    k[:, :, :big, 0] = -44.0
+    k[:, :, big:2 * big, 0] = 0.0
+    v = 0.5 + 0.5 * torch.rand(1, some, cap, D, generator=g)
+    v[:, :, big:2 * big, :D // 2] = 0.0
+    c = ref.Cache(1, some, cap, D, block)
+    c.lens = [cap]
+    c.append(k.half(), v.half())
+    c.scale["v"][:, :, :big // block] *= gap
+    for n in "kv":
+        c.code[n] = c.code[n].repeat(B, H // some, 1, 1)
+        c.scale[n] = c.scale[n].repeat(B, H // some, 1)
+    c.B, c.H, c.lens = B, H, [cap] * B
+    return c
+
+
+UNEVEN = [
+    # B, H, cap: segments by clusters, cut, one to a CTA or a few.
+    (2, 2, 700), (1, 2, 3000), (1, 4, 6000),
+    # As many segments as CTAs: each is walked by one.
+    (10, 64, 1100),
+]
+
+
+@pytest.mark.parametrize("D,block", [(64, 32), (128, 16), (64, 128)])
+@pytest.mark.parametrize("rows", [1, 3, 12, 40])
+@pytest.mark.parametrize("gap", [12, 14, 15])
+@pytest.mark.parametrize("case", UNEVEN)
+def test_fwd_small_values_beside_a_block_of_a_large_scale(case, gap, rows, D,
+                                                          block):
+    """Up to 2^15 apart, block scales cost no precision: the output comes from
+    blocks far below the largest scale and from weights far below 1."""
+    B, H, cap = case
+    c = uneven(B, H, cap, D, block, 2.0 ** gap, 128)
+    q = torch.zeros(B, H, rows, D)
+    q[..., 0] = 1.0
+    check_fwd(c, q.half(), causal=False, scale=1.0, with_w=False,
+              where="cuda")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", [2, 64])  # units cut, whole
+@pytest.mark.parametrize("rows", [1])
+@pytest.mark.parametrize("gap", [16, 24, 25, 26, 40])
+def test_fwd_block_scales_further_apart(gap, rows, H, D):
+    """Beyond 2^15 a number of many-row calls is off by half of fp16's least
+    step, 2^-25, of the largest scale at most (and 2^-35 for the factor's own
+    rounding); few rows hold it exactly."""
+    B, cap, block = 1, 700, 32
+    c = uneven(B, H, cap, D, block, 2.0 ** gap, 128)
+    q = torch.zeros(B, H, rows, D)
+    q[..., 0] = 1.0
+    q = q.bfloat16()
+    out, lse, _, _ = run_fwd(c, q, False, scale=1.0, with_w=False)
+    o_r, l_r, _, t_o, t_l, _ = ref.attention(c, q, 1.0, False)
+    largest = float(c.scale["v"].max())
+    extra = (2.0 ** -25 + 2.0 ** -35) * largest if rows > 16 else 0.0
+    e = (out.double() - o_r).abs()
+    assert bool((e <= t_o + extra).all()), float((e - t_o).max() / largest)
+    assert bool(((lse.double() - l_r).abs() <= t_l).all())
