@@ -8,10 +8,13 @@
 //   - E4M3 codes are fp16 values, so a warpgroup converts each raw tile from
 //     one shared-memory ring into the 128-byte-swizzled fp16 tiles of
 //     another (exactly).  K's block scales multiply the scores in fp32, 16
-//     keys at a time; V's scale over the largest one of the unit's keys
-//     multiplies V's halves: exact for powers of two within 2^15 of the
-//     largest (below that, off by 2^-25 of the largest at most), else one
-//     fp16 rounding, 2^-11, as P's own;
+//     keys at a time; V's scale over 2^-7 of the largest one of the part's
+//     keys (codes times 2^7 are fp16 numbers still) multiplies V's halves:
+//     exact for powers of two within 2^22 of the largest, else two fp16
+//     roundings, 2^-11 each as P's own.  Further below, numbers are off by
+//     2^-23 of the largest scale at most: the factor's half loses bits below
+//     2^-14 and is 0 below 2^-25, a distance of 2^32 (448 * 2^-32 < 2^-23), and
+//     the product is rounded to multiples of 2^-24;
 //   - each softmax thread brings its Q row to fp16 with a power of two
 //     (exact down to 2^-37 of the row's largest element) and the sign of the
 //     scale, while the previous unit's last products run.
@@ -79,7 +82,7 @@ struct Record {
   int slot;       // workspace slot of a part; -1: this CTA has all of the unit
   int n[2];       // key tiles each Q tile sees
   int full[2];    // tiles below this one are seen whole by each valid row
-  float v_unit;   // largest V scale of the part's keys (by the converters)
+  float v_unit;   // V's unit of the part (by the converters)
 };
 
 template <int D>
@@ -574,16 +577,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rec == nullptr) break;
       const int bh = rec->b * p.Hkv + rec->h;
       const int n_kv = rec->n_kv, j0 = rec->j0, len = rec->len;
-      // Unit of V: the largest scale of the part's keys.
+      // Unit of V: 2^-7 of the largest scale of the part's keys.
       const float* vs = p.v_scale + static_cast<long long>(bh) * p.nblk;
       const int key_end = min(len, (j0 + n_kv) * kTN);
-      float unit = 1.17549435e-38f;
+      float unit = 0x1p-119f;
       for (int i = ((j0 * kTN) >> p.block_shift) + lane;
            i <= (key_end - 1) >> p.block_shift; i += 32)
         unit = fmaxf(unit, __ldg(vs + i));
 #pragma unroll
       for (int s = 16; s > 0; s /= 2)
         unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, s));
+      unit *= 0x1p-7f;
       if (cw == 0 && lane == 0) rec->v_unit = unit;
       const float inv_unit = 1.f / unit;
       release_unit(k);

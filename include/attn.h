@@ -349,7 +349,9 @@ attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
 /*
  * attn_kv8_fwd — attention of Sq query rows per sequence over an 8-bit
  * cache, in the scores, softmax and sums of attn_fwd (fp32), on the numbers
- * the cache stands for.
+ * the cache stands for.  As there, the softmax's weights are rounded to 16
+ * bits for their product with V: to fp16, 2^-11 relative down to 2^-21 of the
+ * row's largest.
  *
  * Q         device, [B, Hq, Sq, D] contiguous, dtype (read);
  * O         device, [B, Hq, Sq, D] contiguous, dtype (written);
@@ -373,9 +375,10 @@ attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
  *           NaN code of K reaches the rows that see its token; a NaN code of V
  *           may reach every row of its sequence and head in the call, also
  *           rows before its token (0 * NaN, as in attn_fwd).  A V scale
- *           more than 2^15 below the largest one among the lens[b] tokens of
- *           its sequence and head costs precision: its numbers are then off
- *           by up to 2^-23 of the largest scale.
+ *           more than 2^22 (2^64 where Hq / Hkv * Sq <= 16) below the
+ *           largest one among the lens[b] tokens of its sequence and head
+ *           costs precision: its numbers are then off by up to 2^-23 of the
+ *           largest scale;
  * workspace device, 256-byte aligned, at least attn_kv8_workspace_bytes(...)
  *           bytes; contents need no initialisation.  It must not be used by
  *           another call until this one has run.
