@@ -135,7 +135,7 @@ Workspace workspace_layout(int B, int Hkv, int capacity, int D,
   Workspace w;
   w.part_o = 0;
   w.part_ml = w.part_o + round_up(slots * r.tile * D * 4);
-  w.scores = w.part_ml + round_up(slots * r.tile * 8);
+  w.scores = w.part_ml + round_up(slots * r.tile * (few ? 4 : 8));
   w.split = w.scores +
             (few && weights ? round_up(bh * capacity * 4 << score_shift(r))
                               : 0);
@@ -279,8 +279,11 @@ attn_status_t fwd_impl(const attn_kv8_t* c, const void* Q, void* O, float* LSE,
   p.scale_log2 = scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
-  p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   const bool few = rp.tile <= kFewRows;
+  if (few)
+    p.part_lse2 = reinterpret_cast<float*>(ws + w.part_ml);
+  else
+    p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   if (weights != nullptr && few) {
     p.scores = reinterpret_cast<float*>(ws + w.scores);
     p.score_shift = score_shift(rp);

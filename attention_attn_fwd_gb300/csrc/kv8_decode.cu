@@ -24,8 +24,9 @@
 // fp16 output itself and an eighth of a bf16 one's), shifted by 2^7 so that
 // weights down to 2^-21 of the row's largest stay normal numbers.  V's scales
 // are kept out of it, for each factor of two between two blocks would cost P a
-// bit of its range: O is held in units of the scale of the keys at hand and
-// multiplied, in fp32, when that changes.  The row sums take P unrounded.
+// bit of its range: O is held in units of a power of two, that of the keys at
+// hand, and moved to another, in fp32, when that changes.  The row sums take P
+// unrounded.
 //
 // Codes reach shared memory by 16-byte asynchronous copies, a ring of tiles
 // per warp that runs ahead across segments (128 to 144 KB in flight per SM;
@@ -57,11 +58,12 @@ namespace {
 // 20-22, with 12 19-20 (8 x 4096 tokens 25.0 -> 23.5, 16 or 24 about the same).
 constexpr int kOver = 12;
 constexpr float kTau = 8.f;        // lazy rescale threshold (log2 units)
-constexpr float kMinUnit = 1.17549435e-38f;  // 2^-126, the smallest block scale
 constexpr float kPScale = 128.f;   // 2^7: P <= 2^(8 + 7) < 65504
-// Least unit of O against the largest V scale met: O stays below 2^128 (2^64
-// times 448, 2^15 of P and up to 2^31 keys).
-constexpr float kLeastUnit = 0x1p-64f;
+// Exponents of O's unit: the least one, and how far below that of the largest V
+// scale met it may lie (O stays below 2^128: 2^64 times 448, 2^15 of P and up to
+// 2^31 keys).
+constexpr int kMinUnit = -125;
+constexpr int kUnitDepth = 64;
 
 // Keys of a list tile: 2 KB of K codes.
 template <int D>
@@ -207,7 +209,8 @@ struct Config {
   static constexpr int kPitch = D + 4;  // floats: rows start 4 banks apart
   static constexpr int kRingBytes = kDecodeWarps * kStages * 4096;
   static constexpr int kBytes =
-      kRingBytes + kDecodeWarps * kRows * (kPitch + 2) * 4 + kRows * 4;
+      kRingBytes + kDecodeWarps * kRows * (kPitch + 2) * 4 +
+      (kRows + kDecodeWarps) * 4;
   static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -216,9 +219,10 @@ __device__ __forceinline__ long long out_row(const FwdParams& p, int b, int h,
   const int tok = r / p.group, hd = r - tok * p.group;
   return (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
 }
-// The LSE in log2 units of a row's (max, sum), -inf for one that sees nothing.
-__device__ __forceinline__ float total_lse2(float2 t) {
-  return t.y == 0.f ? -INFINITY : t.x + log2f(t.y);
+// The LSE in log2 units of a row's maximum and sum, -inf for one that sees
+// nothing.
+__device__ __forceinline__ float lse2_of(float mx, float sum) {
+  return sum == 0.f ? -INFINITY : mx + log2f(sum);
 }
 
 // The scores of one key that the forward left, rows beyond n_rows as hidden
@@ -275,6 +279,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
   float* sm_m = sm_o + kWarps * kRows * kPitch;  // [kWarps][kRows]
   float* sm_l = sm_m + kWarps * kRows;
   float* sm_lse = sm_l + kWarps * kRows;  // kWhole: [kRows]
+  int* sm_unit = reinterpret_cast<int*>(sm_lse + kRows);  // [kWarps]
 
   start_after_previous();
 
@@ -374,10 +379,12 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
     const float* vsb = p.v_scale + static_cast<long long>(bh) * p.nblk;
 
     float m[NT][2], l[NT][2], o[NT][kMT][4];
-    // O is held in units of a V scale (times 2^7): that of the keys before,
-    // `vs_last`, or one 2^64 below the largest, `vs_most`, if that is more.
-    float unit = kMinUnit, vs_last = kMinUnit, vs_most = kMinUnit;
-    float p_factor = kPScale;  // 2^7 vs_last / unit
+    // O is held in units of 2^unit (times 2^7): the least power of two that is
+    // no less than the V scale of the keys before, vs_last, if kUnitDepth
+    // allows; unit_most: of the largest one.
+    int unit = kMinUnit, unit_most = kMinUnit;
+    float vs_last = 0.f;
+    float p_factor = 0.f;  // 2^7 vs_last / 2^unit, 2^7 at most
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = kNone;
@@ -474,19 +481,25 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
                     make_float2(s[nt][2 * i], s[nt][2 * i + 1]);
             }
         }
-        if (vs != vs_last) {  // O to the unit of these keys
+        if (vs != vs_last) {
           vs_last = vs;
-          vs_most = fmaxf(vs_most, vs);
-          const float now = fmaxf(vs, vs_most * kLeastUnit);
-          const float f = unit / now;
-          unit = now;
-          p_factor = vs / now * kPScale;
+          const int bits = __float_as_int(vs), frac = bits & 0x7fffff;
+          const int e = (bits >> 23) - 127;
+          const int up = e + (frac != 0 ? 1 : 0);
+          unit_most = max(unit_most, up);
+          const int now = max(max(up, kMinUnit), unit_most - kUnitDepth);
+          p_factor =
+              __int_as_float(frac | (max(127 + 7 + e - now, 1) << 23));
+          if (now != unit) {  // O to the unit of these keys
+            const float f = exp2_int(max(unit - now, -126));
+            unit = now;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < kMT; ++i)
+              for (int i = 0; i < kMT; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][i][e] *= f;
+                for (int k = 0; k < 4; ++k) o[nt][i][k] *= f;
+          }
         }
         bool grow = false;
 #pragma unroll
@@ -579,7 +592,9 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
-    // The warps' results meet: maxima, then O and l under the common one.
+    // The warps' results meet: maxima and units, then O and l under the common
+    // ones.  O leaves as the average that it is: a sum of many V could pass
+    // fp32's largest.
     __syncthreads();  // the previous segment's sums have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -592,7 +607,14 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
         l[nt][e] = x;
         if (g8 == 0) sm_m[warp * kRows + 8 * nt + 2 * c + e] = m[nt][e];
       }
+    if (lane == 0) sm_unit[warp] = unit;
     __syncthreads();
+    int unit_cta = sm_unit[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) unit_cta = max(unit_cta, sm_unit[w]);
+    const float f_unit = exp2_int(max(unit - unit_cta, -126));
+    // (A unit of 2^128 has scales between that and 2^127.)
+    const float v_unit = exp2_int(unit_cta - 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -603,7 +625,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
         for (int w = 0; w < kWarps; ++w)
           mx = fmaxf(mx, sm_m[w * kRows + r]);
         const float f = ptx::ex2(m[nt][e] - mx);
-        const float fo = f * unit * (1.f / kPScale);
+        const float fo = f * f_unit;
         if (g8 == 0) sm_l[warp * kRows + r] = l[nt][e] * f;
         float* dst = sm_o + (warp * kRows + r) * kPitch + (D / 8) * g8;
 #pragma unroll
@@ -613,70 +635,77 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
                           o[nt][i + 1][e] * fo, o[nt][i + 1][e + 2] * fo);
       }
     __syncthreads();
+    // Row r's sum over the warps, and what they have of its O.
+    auto cta_sum = [&](int r) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += sm_l[w * kRows + r];
+      return sum;
+    };
+    auto cta_lse2 = [&](int r) {
+      float mx = kNone;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w * kRows + r]);
+      return lse2_of(mx, cta_sum(r));
+    };
+    auto cta_o = [&](int r, int d4) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(
+            sm_o + (w * kRows + r) * kPitch + 4 * d4);
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      const float sum = cta_sum(r);
+      const float inv = sum == 0.f ? 0.f : ptx::rcp(sum) * (2.f / kPScale);
+      return make_float4(acc.x * inv * v_unit, acc.y * inv * v_unit,
+                         acc.z * inv * v_unit, acc.w * inv * v_unit);
+    };
     if constexpr (kWhole) {
-      // This CTA's sums, then those of the cluster's.
+      // This CTA's rows, then those of the cluster's.
       float4* own_o = reinterpret_cast<float4*>(smem);  // (the ring is free)
-      float2* own_ml = reinterpret_cast<float2*>(smem + kRows * D * 4);
-      for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads) {
-        const int r = i / (D / 4), d4 = i % (D / 4);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(
-              sm_o + (w * kRows + r) * kPitch + 4 * d4);
-          acc.x += x.x;
-          acc.y += x.y;
-          acc.z += x.z;
-          acc.w += x.w;
-        }
-        own_o[i] = acc;
-      }
-      if (threadIdx.x < n_rows) {
-        const int r = threadIdx.x;
-        float2 t = make_float2(kNone, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          t.x = fmaxf(t.x, sm_m[w * kRows + r]);
-          t.y += sm_l[w * kRows + r];
-        }
-        own_ml[r] = t;
-      }
+      float* own_lse2 = reinterpret_cast<float*>(smem + kRows * D * 4);
+      for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads)
+        own_o[i] = cta_o(i / (D / 4), i % (D / 4));
+      if (threadIdx.x < n_rows) own_lse2[threadIdx.x] = cta_lse2(threadIdx.x);
       if (p.ranks > 1)
         cluster_barrier();
       else
         __syncthreads();
-      const uint32_t at_o = ptx::smem_u32(own_o), at_ml = ptx::smem_u32(own_ml);
-      // Row r's (max, sum) and the CTAs' factors.
-      auto total = [&](int r, float* f) -> float2 {
-        if (p.ranks == 1) {
-          f[0] = 1.f;
-          return own_ml[r];
-        }
-        float2 x[kMaxRanks];
-        float2 t = make_float2(kNone, 0.f);
+      const uint32_t at_o = ptx::smem_u32(own_o);
+      const uint32_t at_lse2 = ptx::smem_u32(own_lse2);
+      // Row r's LSE, and the CTAs' shares of its sum.
+      auto total = [&](int r, float* f) -> float {
+        if (p.ranks == 1) return own_lse2[r];
+        float x[kMaxRanks];
+        float mx = kNone, sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kMaxRanks; ++k) {
-          x[k] = make_float2(kNone, 0.f);
-          if (k < p.ranks) {
-            const uint32_t at = ptx::mapa_shared(at_ml + 8 * r, k);
-            x[k].x = ptx::ld_shared_cluster_f32(at);
-            x[k].y = ptx::ld_shared_cluster_f32(at + 4);
-          }
+          x[k] = -INFINITY;
+          if (k < p.ranks)
+            x[k] = ptx::ld_shared_cluster_f32(
+                ptx::mapa_shared(at_lse2 + 4 * r, k));
         }
 #pragma unroll
-        for (int k = 0; k < kMaxRanks; ++k) t.x = fmaxf(t.x, x[k].x);
+        for (int k = 0; k < kMaxRanks; ++k) mx = fmaxf(mx, x[k]);
 #pragma unroll
         for (int k = 0; k < kMaxRanks; ++k) {
-          f[k] = ptx::ex2(x[k].x - t.x);
-          t.y += x[k].y * f[k];
+          f[k] = ptx::ex2(x[k] - mx);
+          sum += f[k];
         }
-        return t;
+        const float inv = sum == 0.f ? 0.f : ptx::rcp(sum);
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) f[k] *= inv;
+        return lse2_of(mx, sum);
       };
       for (int i = rank * C::kThreads + threadIdx.x; i < n_rows * (D / 4);
            i += p.ranks * C::kThreads) {
         const int r = i / (D / 4), d4 = i % (D / 4);
         float f[kMaxRanks];
-        const float2 t = total(r, f);
+        const float lse2 = total(r, f);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.ranks == 1) {
           acc = own_o[i];
@@ -692,19 +721,18 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
             acc.w += x.w * f[k];
           }
         }
-        const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
         const long long row = out_row(p, b, h, r);
         uint2 out;
-        out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
-        out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
+        out.x = ptx::pack2<kBF16>(acc.x, acc.y);
+        out.y = ptx::pack2<kBF16>(acc.z, acc.w);
         reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[d4] =
             out;
         if (d4 == 0 && p.lse != nullptr)
-          p.lse[row] = total_lse2(t) * 0.69314718055994531f;
+          p.lse[row] = lse2 * 0.69314718055994531f;
       }
       if (p.scores != nullptr && threadIdx.x < n_rows) {
         float f[kMaxRanks];
-        sm_lse[threadIdx.x] = total_lse2(total(threadIdx.x, f));
+        sm_lse[threadIdx.x] = total(threadIdx.x, f);
       }
       if (p.ranks > 1) cluster_arrive();  // peers' sums are read
       if (p.scores != nullptr && n_rows > 0) {
@@ -728,29 +756,11 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
 #pragma unroll 2
     for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads) {
       const int r = i / (D / 4), d4 = i % (D / 4);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(
-            sm_o + (w * kRows + r) * kPitch + 4 * d4);
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-      }
       reinterpret_cast<float4*>(p.part_o)[(slot * kRows + r) * (D / 4) + d4] =
-          acc;
+          cta_o(r, d4);
     }
-    if (threadIdx.x < n_rows) {
-      const int r = threadIdx.x;
-      float mx = kNone, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        mx = fmaxf(mx, sm_m[w * kRows + r]);
-        sum += sm_l[w * kRows + r];
-      }
-      p.part_ml[slot * kRows + r] = make_float2(mx, sum);
-    }
+    if (threadIdx.x < n_rows)
+      p.part_lse2[slot * kRows + threadIdx.x] = cta_lse2(threadIdx.x);
     if (seg.end >= count) break;
     next_segment<kKeys, kOver>(p, seg);
     if (seg.pos >= count) break;
@@ -767,28 +777,29 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
 constexpr int kMergeThreads = 256;
 constexpr int kKeysPerPart = 512;
 
-// Up to 256 partials' (max, sum) of a row, eight per lane and all loads in
-// flight at once: lane l holds partials l, l + 32, ...; f becomes their
-// factors 2^(max_s - mx).  mx and the lanes' shares of sum carry on from the
+// Up to 256 partials' LSEs of a row, eight per lane and all loads in flight at
+// once: lane l holds partials l, l + 32, ...; f becomes their factors
+// 2^(LSE_s - mx - kSlack).  mx and the lanes' shares of sum carry on from the
 // partials before; the return value is what those have to be multiplied by.
-// (A NaN among the scores has made a sum NaN, also where no other score set a
-// maximum.)
+// (A NaN among the scores has made an LSE NaN, which sets no maximum.)
 constexpr int kHeld = 8;
+// log2 of the most partials (152 SMs of four CTAs): their sum times V stays
+// within fp32.
+constexpr float kSlack = 10.f;
 template <int kRows>
-__device__ __forceinline__ float take_partials(const float2* ml, int r, int s0,
+__device__ __forceinline__ float take_partials(const float* lse2, int r, int s0,
                                                int n_slots, int lane,
                                                float* f, float& mx,
                                                float& sum) {
-  float2 x[kHeld];
+  float x[kHeld];
   float m = mx;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int s = s0 + 32 * i + lane;
-    x[i] = make_float2(kNone, 0.f);
-    if (s < n_slots) x[i] = ml[s * kRows + r];
+    x[i] = s < n_slots ? lse2[s * kRows + r] : -INFINITY;
   }
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) m = fmaxf(m, x[i].x);
+  for (int i = 0; i < kHeld; ++i) m = fmaxf(m, x[i]);
 #pragma unroll
   for (int i = 16; i > 0; i /= 2)
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
@@ -796,24 +807,23 @@ __device__ __forceinline__ float take_partials(const float2* ml, int r, int s0,
   sum *= before;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
-    f[i] = ptx::ex2(x[i].x - m);
-    sum += x[i].y * f[i];
+    f[i] = ptx::ex2((x[i] - m) - kSlack);
+    sum += f[i];
   }
   mx = m;
   return before;
 }
 
-// Maximum and sum of row r over a segment's partials, by one warp (every lane
-// gets the result).
+// LSE of row r over a segment's partials, by one warp (every lane gets it).
 template <int kRows>
-__device__ __forceinline__ float2 row_total(const float2* ml, int r,
-                                            int n_slots, int lane) {
+__device__ __forceinline__ float row_lse2(const float* lse2, int r,
+                                          int n_slots, int lane) {
   float mx = kNone, sum = 0.f, f[kHeld];
   for (int s0 = 0; s0 < n_slots; s0 += 32 * kHeld)
-    take_partials<kRows>(ml, r, s0, n_slots, lane, f, mx, sum);
+    take_partials<kRows>(lse2, r, s0, n_slots, lane, f, mx, sum);
 #pragma unroll
   for (int i = 16; i > 0; i /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-  return make_float2(mx, sum);
+  return lse2_of(mx, sum) + kSlack;
 }
 
 template <int D, int NT, bool kBF16>
@@ -851,7 +861,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
     c0 = cut.owner(first);
     n_slots = cut.owner(first + tiles - 1) - static_cast<int>(c0) + 1;
   }
-  const float2* ml = p.part_ml + (c0 + bh) * kRows;
+  const float* part_lse2 = p.part_lse2 + (c0 + bh) * kRows;
   // Accumulated weights of this CTA's keys (the forward does not touch them).
   constexpr int kKeysPerThread = kKeysPerPart / kMergeThreads;
   const long long key_at = static_cast<long long>(bh) * p.capacity;
@@ -881,8 +891,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
       if (sub < n_slots) y0 = po[static_cast<long long>(sub) * kRows * kCols];
       for (int s0 = 0; s0 < n_slots; s0 += 32 * kHeld) {
         float f[kHeld];
-        const float before = take_partials<kRows>(ml, r, s0, n_slots, lane, f,
-                                                  t.x, t.y);
+        const float before = take_partials<kRows>(part_lse2, r, s0, n_slots,
+                                                  lane, f, t.x, t.y);
         acc.x *= before;
         acc.y *= before;
         acc.z *= before;
@@ -938,7 +948,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
           out;
     }
     if (lane == 0 && p.lse != nullptr)
-      p.lse[row] = total_lse2(t) * 0.69314718055994531f;
+      p.lse[row] = (lse2_of(t.x, t.y) + kSlack) * 0.69314718055994531f;
     return;
   }
   // Scores and LSEs are fetched side by side.
@@ -951,7 +961,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
   if (threadIdx.x < kRows) sm_lse[threadIdx.x] = 0.f;
   __syncthreads();
   for (int i = warp; i < n_rows; i += kMergeThreads / 32) {
-    const float lse2 = total_lse2(row_total<kRows>(ml, i, n_slots, lane));
+    const float lse2 = row_lse2<kRows>(part_lse2, i, n_slots, lane);
     if (lane == 0) sm_lse[i] = lse2;
   }
   __syncthreads();

@@ -55,6 +55,9 @@ constexpr int kTN = 128;            // keys of a tile
 constexpr int kUnitRows = 2 * kTM;
 constexpr float kTau = 8.f;         // lazy rescale threshold (log2 units)
 constexpr float kShift = 7.f;       // log2 of P's scale
+// Below this, a unit of V times 1 over a row's sum (2^46 at most, P's scale in
+// it) may be no normal number.
+constexpr float kSmallUnit = 0x1p-80f;
 // Registers: the launch gives every thread 128; the shares of the four
 // warpgroups add up to 4 * 128.
 constexpr int kRegsControl = 64;
@@ -826,8 +829,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = rec->slot;
       const int row_u = rec->row0 + t * kTM + r;  // row of the K/V head
       const bool row_ok = row_u < rec->n_new * p.group;
+      // O leaves as the average that it is: a sum of many large V could pass
+      // fp32's largest.
+      float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      if (unit >= kSmallUnit || n == 0) {
+        inv *= unit;
+      } else {
+        // The factor would be a subnormal number: the average first.
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          ptx::tmem_ld32(t_o + 32 * q, o);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+          ptx::tmem_st32(t_o + 32 * q, o);
+        }
+        ptx::tmem_wait_st();
+        inv = unit;
+      }
       if (slot < 0) {
-        const float inv = l_run == 0.f ? 0.f : unit / l_run;
         const long long row =
             row_ok ? q_row_index(p, rec->b, rec->h, row_u) : 0;
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
@@ -885,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                   o[8 * v + e] =
-                      __float_as_uint(__uint_as_float(o[8 * v + e]) * unit);
+                      __float_as_uint(__uint_as_float(o[8 * v + e]) * inv);
                 store32(dst + 8 * q + 2 * v, o + 8 * v);
               }
             }
@@ -915,6 +937,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = kMergeThreads / 32;
 constexpr int kMergeParts = kUnitRows / kMergeRows;  // CTAs per unit
+// log2 of the most parts, one per SM: their sum times V stays within fp32.
+constexpr float kSlack = 8.f;
 
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kMergeThreads)
@@ -934,34 +958,33 @@ __global__ void __launch_bounds__(kMergeThreads)
   const long long at0 = (2LL * cta + 1) * kUnitRows + i;
   const long long at = 2LL * cta * kUnitRows + i;
   const int col = lane % kCols;
+  // A part's weight: its LSE in log2 units (-inf: sees nothing).
+  auto weight = [&](int s) {
+    const float2 ml = p.part_ml[s == 0 ? at0 : at + 2LL * s * kUnitRows];
+    return ml.x + __log2f(ml.y);
+  };
   float mx = kNone;
-  for (int s = lane; s < parts; s += 32)
-    mx = fmaxf(mx, p.part_ml[s == 0 ? at0 : at + 2LL * s * kUnitRows].x);
+  for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, weight(s));
 #pragma unroll
   for (int k = 16; k > 0; k /= 2)
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < parts; s0 += 32) {
-    // Lane s: factor and sum of part s0 + s.  (A part whose sum is 0 sees
-    // nothing and has no O.)
-    float2 ml = make_float2(kNone, 0.f);
-    if (s0 + lane < parts)
-      ml = p.part_ml[s0 + lane == 0
-                         ? at0
-                         : at + 2LL * (s0 + lane) * kUnitRows];
-    const float f_all = ptx::ex2(ml.x - mx);
+    // Lane s: factor of part s0 + s.  (A part that sees nothing has the factor
+    // 0 and no O.)
+    const float f_all =
+        s0 + lane < parts ? ptx::ex2((weight(s0 + lane) - mx) - kSlack) : 0.f;
     const int n = min(32, parts - s0);
 #pragma unroll 8
     for (int s = 0; s < n; ++s) {
-      const float l = __shfl_sync(0xffffffffu, ml.y, s);
       const float f = __shfl_sync(0xffffffffu, f_all, s);
-      // (Read in any case, so that the loads need not wait for l.)
+      // (Read in any case, so that the loads need not wait for f.)
       float4 y = reinterpret_cast<const float4*>(
           p.part_o)[(s0 + s == 0 ? at0 : at + 2LL * (s0 + s) * kUnitRows) *
                         kCols + col];
-      if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
-      sum += l * f;
+      if (f == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum += f;
       acc.x += y.x * f;
       acc.y += y.y * f;
       acc.z += y.z * f;
@@ -977,7 +1000,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[col] = out;
   }
   if (lane == 0) {
-    const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum) - kShift;
+    const float lse2 =
+        sum == 0.f ? -INFINITY : mx + log2f(sum) + (kSlack - kShift);
     if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
     if (p.lse2 != nullptr)
       p.lse2[(static_cast<long long>(b) * p.Hkv + h) * p.row_blocks *

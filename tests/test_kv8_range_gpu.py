@@ -161,3 +161,36 @@ def test_fwd_block_scales_further_apart(gap, rows, H, D):
     e = (out.double() - o_r).abs()
     assert bool((e <= t_o + extra).all()), float((e - t_o).max() / largest)
     assert bool(((lse.double() - l_r).abs() <= t_l).all())
+
+
+# ------------------------------------------ values at the ends of the range
+
+ENDS = [
+    # Hq, Hkv, cap, len, Sq: clusters, cut, a long cut one, whole units, split
+    # ones.
+    (4, 2, 300, 300, 1), (4, 2, 2000, 1999, 2), (8, 1, 9000, 9000, 1),
+    (2, 2, 200, 200, 40), (4, 2, 5000, 5000, 64), (2, 1, 3000, 2222, 300),
+]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("exponent", [-126, -120, 110, 119])
+@pytest.mark.parametrize("case", ENDS)
+def test_fwd_values_at_the_ends_of_the_range(case, exponent, D):
+    """V of one sign under flat weights: every output is an average of them,
+    of their size, also where their sum leaves fp32."""
+    Hq, Hkv, cap, n, Sq = case
+    g = ref.rng(181)
+    c = ref.filled(1, Hkv, cap, D, 64, [n], 182)
+    # Codes 0x30 to 0x7E: 0.5 to 448.
+    c.code["v"][:, :, :n] = torch.randint(
+        0x30, 0x7F, (1, Hkv, n, D), generator=g, dtype=torch.uint8)
+    c.scale["v"][c.scale["v"].isfinite()] = 2.0 ** exponent
+    q = (torch.randn(1, Hq, Sq, D, generator=g) * 0.1).bfloat16()
+    out, lse, _, _ = run_fwd(c, q, with_w=False)
+    o_r, l_r, _, t_o, t_l, _ = ref.attention(c, q, D ** -0.5, True)
+    # The bound without its absolute term; half of bf16's least step instead.
+    t_o = t_o - 1e-30 + 2.0 ** -134
+    e = (out.double() - o_r).abs()
+    assert bool((e <= t_o).all()), float((e / o_r.abs()).max())
+    assert bool(((lse.double() - l_r).abs() <= t_l).all())
