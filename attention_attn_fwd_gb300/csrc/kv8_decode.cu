@@ -660,7 +660,10 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
         acc.w += x.w;
       }
       const float sum = cta_sum(r);
-      const float inv = sum == 0.f ? 0.f : ptx::rcp(sum) * (2.f / kPScale);
+      // A row that sees nothing: 0, whatever its accumulators hold (NaN codes
+      // of V reach them).
+      if (sum == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
+      const float inv = ptx::rcp(sum) * (2.f / kPScale);
       return make_float4(acc.x * inv * v_unit, acc.y * inv * v_unit,
                          acc.z * inv * v_unit, acc.w * inv * v_unit);
     };

@@ -194,3 +194,23 @@ def test_fwd_values_at_the_ends_of_the_range(case, exponent, D):
     e = (out.double() - o_r).abs()
     assert bool((e <= t_o).all()), float((e / o_r.abs()).max())
     assert bool(((lse.double() - l_r).abs() <= t_l).all())
+
+
+# ------------------------------------------------- rows that see nothing
+
+@pytest.mark.parametrize("cap", [100, 5000])
+@pytest.mark.parametrize("Sq", [3, 40, 200])
+def test_fwd_rows_that_see_nothing_beside_a_nan_value(Sq, cap):
+    """Two tokens and Sq rows at positions 2 - Sq .. 1: all but the last two
+    see none and get 0, though V's codes are NaN."""
+    c = ref.filled(1, 2, cap, 64, 16, [2], 191)
+    c.code["v"][:, :, :2] = 0x7F
+    q = torch.randn(1, 4, Sq, 64, generator=ref.rng(192)).half()
+    w = [None, torch.zeros(1, 2, cap).cuda()]
+    for weights in w:
+        out, lse = attn.kv8_fwd(upload(c), q.cuda(), weights=weights)
+        out, lse = out.cpu(), lse.cpu()
+        assert bool((out[:, :, :-2] == 0).all())
+        assert bool((lse[:, :, :-2] == -math.inf).all())
+        assert bool(out[:, :, -2:].isnan().all())
+        assert bool(lse[:, :, -2:].isfinite().all())
