@@ -234,7 +234,6 @@ bool on_device(const void* p, int dev) { return is_device_ptr(p, dev); }
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
   return na != 0 && nb != 0 && overlaps(a, na, b, nb);
 }
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encoder(); }
 
 bool current_context_id(unsigned long long* id) {
   std::call_once(g_ctx_once, [] {

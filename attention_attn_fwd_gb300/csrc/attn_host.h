@@ -3,9 +3,6 @@
 
 #include <cstddef>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 namespace attn {
 
 // Status-word bit 1: a kernel met a length outside its range and clamped it.
@@ -21,7 +18,5 @@ unsigned long long wait_timeout_ns();
 bool on_device(const void* p, int dev);
 // Whether two byte ranges share a byte.
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb);
-// cuTensorMapEncodeTiled, or nullptr when the driver has none.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 }  // namespace attn

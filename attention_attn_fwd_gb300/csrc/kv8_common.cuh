@@ -232,7 +232,7 @@ template <int kKeys, int kOver>
 __device__ __forceinline__ int places(int len) {
   return len > 0 ? (len + kKeys - 1) / kKeys + kOver : 0;
 }
-//
+
 // Places before sequence `seq` and of all sequences, for every lane of the
 // calling warp.
 template <int kKeys, int kOver>
