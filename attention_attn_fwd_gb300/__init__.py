@@ -729,7 +729,9 @@ def kv8_append(cache, k, v, new_lens=None, stream=None):
 
 def kv8_workspace(cache, Hq, Sq, weights=False):
     """A workspace tensor for ``kv8_fwd`` calls of Hq heads and Sq rows
-    (``weights``: calls that accumulate attention weights)."""
+    (``weights``: calls that accumulate attention weights; with 16 or fewer
+    query rows per K/V head it then holds 4 bytes per row and token of the
+    capacity)."""
     import torch
     with torch.cuda.device(cache.device):
         n = attn_kv8_workspace_bytes(cache.B, Hq, cache.Hkv, Sq,
@@ -749,7 +751,8 @@ def kv8_fwd(cache, q, scale=None, causal=True, new_lens=None, weights=None,
     ``weights`` (float32 [B, Hkv, capacity]): the attention weight each token
     receives, summed over rows and the group's heads, is added to it.
     ``workspace``: from ``kv8_workspace``, allocated when not given.  What a
-    call on ``stream`` allocates is that stream's memory.
+    call on ``stream`` allocates is that stream's memory.  As in ``fwd``,
+    ``need_lse=False`` writes no LSE, also where ``lse`` is given.
     """
     dt = _kv8_dtype(cache, "q", q)
     dtype, B, shape = q.dtype, cache.B, q.shape

@@ -40,7 +40,7 @@
 // a byte permute and one movmatrix per 8 x 8 weights.
 //
 // Measured, cut and merged: 8 x 4096 tokens, 8 heads of 4 rows, D = 128, with
-// accumulated weights 23.4 us (69 MB); 131072 tokens, 4 heads of 8 rows 32.5
+// accumulated weights 23.8 us (69 MB); 131072 tokens, 4 heads of 8 rows 32.5
 // us (134 MB, 4.1 TB/s).  With the products taken out the first two thirds of
 // that stay (15.8 and 25.0 us, the loads), the products add about 4 us and the
 // merge's launch behind the last CTA 4 to 7: on short caches latency bounds

@@ -35,12 +35,13 @@
 // 12-15 K and V conversion.  Every wait is bounded as in the forward kernel.
 //
 // Measured: 8 x 512 rows of 32 heads over 4096 tokens of 8 heads, D = 128,
-// causal (258 GFLOP): 234 us, 1.10 PFLOP/s, against 187 for the 16-bit forward
+// causal (258 GFLOP): 236 us, 1.09 PFLOP/s, against 187 for the 16-bit forward
 // kernel on the same numbers.  A step (256 rows, 128 keys) takes about 3400
-// clocks against 2048 of MMAs.  Nothing alone bounds it: with the conversion
-// left out the call (then 238 us) took 223, with exp2 left out 235, with both
-// 212; shared memory carries both operands of Q K^T, the raw tiles and the
-// converted ones.  A fifth warpgroup for V's conversion took 268 (spills), raw
+// clocks against 2048 of MMAs.  Conversion and exp2 are not most of that gap:
+// with the conversion left out the call (then 238 us) took 223, with exp2 left
+// out 235, with both 212.  The rest has not been traced; three converted slots
+// that K and V share, and shared memory that carries both operands of Q K^T, the
+// raw tiles and the converted ones, are what differs from the 16-bit kernel.  A fifth warpgroup for V's conversion took 268 (spills), raw
 // tiles read past shared memory 255, four converted and two raw slots 262.
 #include "attn_sync.cuh"
 #include "kv8_common.cuh"

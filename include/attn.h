@@ -381,7 +381,11 @@ attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
  *           largest scale;
  * workspace device, 256-byte aligned, at least attn_kv8_workspace_bytes(...)
  *           bytes; contents need no initialisation.  It must not be used by
- *           another call until this one has run.
+ *           another call until this one has run.  Where weights are
+ *           accumulated under 16 or fewer query rows per K/V head it holds
+ *           their scores: 4 bytes for every row (of Hq / Hkv * Sq, rounded up
+ *           to a power of two) and every one of the capacity's tokens of a
+ *           head, up to 64 bytes a token against 2 D of codes.
  * One to three kernels on `stream` (one over short caches, three with weights
  * of more than 16 query rows per K/V head).  O, LSE, weights and workspace must
  * not overlap each other or any input.  B == 0 or Sq == 0 is a successful
