@@ -193,8 +193,9 @@ struct FwdParams {
   float scale_log2;       // scale * log2(e)
   // Workspace: rows of the parts of a split segment or unit, each the average
   // that it is, and their LSEs in log2 units (-inf: sees nothing; few rows) or
-  // (max, sum) (many: the logarithm is cheaper in the merge there); few rows: the scores of every key; many rows: the unit
-  // that goes on behind each CTA, and the rows' LSEs in log2 units.
+  // (max, sum) (many: the logarithm is cheaper in the merge there); few rows:
+  // the scores of every key; many rows: the unit that goes on behind each CTA,
+  // and the rows' LSEs in log2 units.
   float* part_o;          // [slots, rows, D]
   float* part_lse2;       // [slots, rows]
   float2* part_ml;        // [slots, rows]

@@ -59,9 +59,9 @@ namespace {
 constexpr int kOver = 12;
 constexpr float kTau = 8.f;        // lazy rescale threshold (log2 units)
 constexpr float kPScale = 128.f;   // 2^7: P <= 2^(8 + 7) < 65504
-// Exponents of O's unit: the least one, and how far below that of the largest V
-// scale met it may lie (O stays below 2^128: 2^64 times 448, 2^15 of P and up to
-// 2^31 keys).
+// Exponents of O's unit: the least one, and how far below that of the largest
+// V scale met it may lie (O stays below 2^128: 2^64 times 448, 2^15 of P and up
+// to 2^31 keys).
 constexpr int kMinUnit = -125;
 constexpr int kUnitDepth = 64;
 
@@ -539,10 +539,10 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
             w[e] = ptx::ex2(s[nt][e] - m[nt][e & 1]);
             l[nt][e & 1] += w[e];
           }
-          pb[nt][0] =
-              movmatrix_trans(ptx::pack2<false>(w[0] * p_factor, w[1] * p_factor));
-          pb[nt][1] =
-              movmatrix_trans(ptx::pack2<false>(w[2] * p_factor, w[3] * p_factor));
+          pb[nt][0] = movmatrix_trans(
+              ptx::pack2<false>(w[0] * p_factor, w[1] * p_factor));
+          pb[nt][1] = movmatrix_trans(
+              ptx::pack2<false>(w[2] * p_factor, w[3] * p_factor));
         }
         // O^T += V^T P^T: V rows 2c, 2c + 1, 2c + 8, 2c + 9 of the step.
         constexpr int kVWords = D / 32;

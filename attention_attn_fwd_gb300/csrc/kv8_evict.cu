@@ -19,13 +19,13 @@
 // no later round reads.
 //
 // Measured: 8 x 8 heads of 4096 tokens to 2048, D = 128, 24.0 us; 4 heads of
-// 131072 tokens to 16384, 27.5 us; one call by itself, 29 and 33 us, in place 41
-// and 64 (its rounds wait for one another).  Select is bound by latency (four digits
-// of a cluster barrier and two block barriers each: 9 and 20 us of the two
-// when launched alone), move by the gather (17 and 11 us, 69 and 36 MB: a
-// block's largest magnitude is known only after the last of its scattered
-// rows has come).  Keys one per lane instead of in quads: 31.8 us on the long
-// one; one CTA per head for the select 191 us.
+// 131072 tokens to 16384, 27.5 us; one call by itself, 29 and 33 us, in place
+// 41 and 64 (its rounds wait for one another).  Select is bound by latency
+// (four digits of a cluster barrier and two block barriers each: 9 and 20 us
+// of the two when launched alone), move by the gather (17 and 11 us, 69 and 36
+// MB: a block's largest magnitude is known only after the last of its
+// scattered rows has come).  Keys one per lane instead of in quads: 31.8 us on
+// the long one; one CTA per head for the select 191 us.
 #include "kv8_common.cuh"
 #include "kv8_index.h"
 

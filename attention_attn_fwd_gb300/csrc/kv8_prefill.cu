@@ -40,9 +40,10 @@
 // clocks against 2048 of MMAs.  Conversion and exp2 are not most of that gap:
 // with the conversion left out the call (then 238 us) took 223, with exp2 left
 // out 235, with both 212.  The rest has not been traced; three converted slots
-// that K and V share, and shared memory that carries both operands of Q K^T, the
-// raw tiles and the converted ones, are what differs from the 16-bit kernel.  A fifth warpgroup for V's conversion took 268 (spills), raw
-// tiles read past shared memory 255, four converted and two raw slots 262.
+// that K and V share, and shared memory that carries both operands of Q K^T,
+// the raw tiles and the converted ones, are what differs from the 16-bit
+// kernel.  A fifth warpgroup for V's conversion took 268 (spills), raw tiles
+// read past shared memory 255, four converted and two raw slots 262.
 #include "attn_sync.cuh"
 #include "kv8_common.cuh"
 

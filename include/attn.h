@@ -332,8 +332,8 @@ typedef struct {
  *
  * Let a be the largest finite magnitude among the new tokens of one block of
  * one head, and tight(a) the smallest power of two (2^-126 at least, 2^127 at
- * most) with a <= 448 * tight(a).  A block that holds no earlier token gets the scale
- * tight(a).  A block begun by earlier calls keeps its scale when
+ * most) with a <= 448 * tight(a).  A block that holds no earlier token gets the
+ * scale tight(a).  A block begun by earlier calls keeps its scale when
  * a <= 448 * scale; else its scale becomes tight(a) and the codes it holds
  * are requantised, round(code * old / new) -- with powers of two an exponent
  * shift, exact unless the result is subnormal.  New codes are
@@ -378,7 +378,8 @@ attn_status_t attn_kv8_append(const attn_kv8_t* cache, const void* K,
  *           more than 2^22 (2^64 where Hq / Hkv * Sq <= 16) below the
  *           largest one among the lens[b] tokens of its sequence and head
  *           costs precision: its numbers are then off by up to 2^-23 of the
- *           largest scale;
+ *           largest scale.  V scales that are no powers of two add two
+ *           roundings of 2^-11 where Hq / Hkv * Sq > 16;
  * workspace device, 256-byte aligned, at least attn_kv8_workspace_bytes(...)
  *           bytes; contents need no initialisation.  It must not be used by
  *           another call until this one has run.  Where weights are
