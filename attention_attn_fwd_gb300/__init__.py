@@ -28,6 +28,9 @@ __all__ = [
     "attn_kv8_append", "attn_kv8_fwd", "attn_kv8_workspace_bytes",
     "attn_kv8_evict",
     "KV8Cache", "kv8_append", "kv8_fwd", "kv8_workspace", "kv8_evict",
+    "attn_rope_phase", "attn_qk_rope", "attn_qk_rope_bwd",
+    "attn_qk_rope_bwd_workspace_bytes",
+    "Rope", "qk_rope", "qk_rope_bwd", "qk_rope_bwd_workspace",
     "library_path", "load_library",
 ]
 
@@ -69,6 +72,18 @@ class _KV8(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "k", "v", "k_scale", "v_scale", "lens")] + [
             (n, ctypes.c_int) for n in ("B", "Hkv", "capacity", "D", "block")]
+
+
+class _RopeStruct(ctypes.Structure):
+    """attn_rope_t of include/attn.h."""
+    _fields_ = [("phase", ctypes.c_void_p), ("axis", ctypes.c_void_p)] + [
+        (n, ctypes.c_int) for n in ("D", "rot", "axes", "interleaved")]
+
+
+class _Heads(ctypes.Structure):
+    """attn_heads_t of include/attn.h."""
+    _fields_ = [("p", ctypes.c_void_p)] + [
+        (n, ctypes.c_longlong) for n in ("stride_b", "stride_s", "stride_h")]
 
 
 def library_path() -> str:
@@ -153,6 +168,19 @@ def load_library():
         lib.attn_kv8_workspace_bytes.restype = sz
         lib.attn_kv8_evict.argtypes = [cp, cp, vp, vp, i, i, vp, vp]
         lib.attn_kv8_evict.restype = i
+        rp, hp = ctypes.POINTER(_RopeStruct), ctypes.POINTER(_Heads)
+        lib.attn_rope_phase.argtypes = [ctypes.POINTER(ctypes.c_double), i,
+                                        ctypes.POINTER(ctypes.c_ulonglong)]
+        lib.attn_rope_phase.restype = i
+        lib.attn_qk_rope.argtypes = [rp, hp, hp, hp, vp, vp, i, f, vp, vp, vp,
+                                     vp, vp, vp, vp, i, i, i, i, i, i, vp]
+        lib.attn_qk_rope.restype = i
+        lib.attn_qk_rope_bwd.argtypes = [rp, vp, vp, vp, hp, hp, vp, vp, i, f,
+                                         vp, vp, hp, hp, hp, vp, vp, i, i, i,
+                                         i, i, vp, sz, vp]
+        lib.attn_qk_rope_bwd.restype = i
+        lib.attn_qk_rope_bwd_workspace_bytes.argtypes = [i]
+        lib.attn_qk_rope_bwd_workspace_bytes.restype = sz
         _lib = lib
         return lib
 
@@ -368,6 +396,49 @@ def attn_kv8_evict(src, dst, weights, dst_weights, keep, recent, indices,
     return int(load_library().attn_kv8_evict(
         src.struct, dst.struct, weights or None, dst_weights or None, keep,
         recent, indices or None, stream or None))
+
+
+def attn_rope_phase(freq):
+    """Phases (a list of integers, units of 2^-64 of a turn per position) of
+    frequencies in radians per position (host only)."""
+    n = len(freq)
+    out = (ctypes.c_ulonglong * max(n, 1))()
+    st = int(load_library().attn_rope_phase(
+        (ctypes.c_double * max(n, 1))(*[float(x) for x in freq]), n, out))
+    if st != ATTN_OK:
+        raise AttnError("attn_rope_phase: " + attn_status_string(st), st)
+    return list(out[:n])
+
+
+def attn_qk_rope(rope, q, k, v, q_weight, k_weight, weight_f32, eps,
+                 positions, lens, new_lens, offset, q_out, k_out, v_out, B, S,
+                 Hq, Hkv, capacity, dtype, stream) -> int:
+    """Raw C-ABI call; ``rope`` is a ``Rope``, q, k, v are (pointer, stride_b,
+    stride_s, stride_h) or None, other pointers integers."""
+    return int(load_library().attn_qk_rope(
+        rope.struct, *[_Heads(*x) if x else None for x in (q, k, v)],
+        q_weight or None, k_weight or None, int(weight_f32), float(eps),
+        positions or None, lens or None, new_lens or None, offset or None,
+        q_out or None, k_out or None, v_out or None, B, S, Hq, Hkv, capacity,
+        int(dtype), stream or None))
+
+
+def attn_qk_rope_bwd(rope, dq_out, dk_out, dv_out, q, k, q_weight, k_weight,
+                     weight_f32, eps, positions, offset, dq, dk, dv,
+                     dq_weight, dk_weight, B, S, Hq, Hkv, dtype, workspace,
+                     workspace_bytes, stream) -> int:
+    """Raw C-ABI call; arguments like those of ``attn_qk_rope``."""
+    view = [_Heads(*x) if x else None for x in (q, k, dq, dk, dv)]
+    return int(load_library().attn_qk_rope_bwd(
+        rope.struct, dq_out or None, dk_out or None, dv_out or None,
+        view[0], view[1], q_weight or None, k_weight or None, int(weight_f32),
+        float(eps), positions or None, offset or None, *view[2:],
+        dq_weight or None, dk_weight or None, B, S, Hq, Hkv, int(dtype),
+        workspace or None, int(workspace_bytes), stream or None))
+
+
+def attn_qk_rope_bwd_workspace_bytes(D) -> int:
+    return int(load_library().attn_qk_rope_bwd_workspace_bytes(D))
 
 
 def attn_version() -> int:
@@ -845,3 +916,255 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
               weights.data_ptr(), out_weights.data_ptr(), keep, recent,
               indices.data_ptr())
     return out, out_weights, indices
+
+
+class Rope:
+    """Handle of a rotation of heads by position (``attn_rope_t``).
+
+    ``freq``: the rot / 2 pairs' frequencies in radians per position (any
+    sequence or tensor of numbers; float64 keeps far positions exact); pair i
+    is elements (i, i + rot / 2) of a head's D, or (2i, 2i + 1) with
+    ``interleaved``.  ``axes``: the axis of each pair, 0 up (all 0 unless
+    given), for positions on several axes (time, height, width).
+    """
+
+    def __init__(self, freq, D, axes=None, interleaved=False, device="cuda"):
+        import torch
+        freq = [float(x) for x in freq]
+        axes = [0] * len(freq) if axes is None else [int(a) for a in axes]
+        if D not in (64, 128) or (2 * len(freq)) % 8:
+            raise AttnError("D must be 64 or 128 and the rotated elements a "
+                            "multiple of 8, got %r and %d"
+                            % (D, 2 * len(freq)), ATTN_ERR_UNSUPPORTED)
+        if 2 * len(freq) > D or len(axes) != len(freq) or \
+                not all(0 <= a < 255 for a in axes):
+            raise AttnError("at most D / 2 frequencies, and as many axes "
+                            "below 255", ATTN_ERR_INVALID_ARG)
+        phase = attn_rope_phase(freq)
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise AttnError("device must be a CUDA device",
+                            ATTN_ERR_INVALID_ARG)
+        signed = [x - (1 << 64) if x >> 63 else x for x in phase]
+        self.phase = torch.tensor(signed, dtype=torch.int64, device=dev)
+        self.axis = torch.tensor(axes, dtype=torch.uint8, device=dev)
+        self.D, self.rot = D, 2 * len(freq)
+        self.axes = max(axes, default=0) + 1
+        self.interleaved = bool(interleaved)
+        self.device = self.phase.device
+        # What every call needs, looked up once.
+        self.dtypes = {torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16}
+        self.int32, self.float32 = torch.int32, torch.float32
+        self.lib, self.index = load_library(), self.device.index
+        self.current_device = torch._C._cuda_getDevice
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.struct = ctypes.pointer(_RopeStruct(
+            self.phase.data_ptr() or None, self.axis.data_ptr() or None, D,
+            self.rot, self.axes, self.interleaved))
+
+    @classmethod
+    def make(cls, D, base=10000.0, rot=None, sections=None, interleaved=False,
+             device="cuda"):
+        """Frequencies base^(-2i / rot) of rot (D unless given) elements;
+        ``sections``: pairs of each axis in turn, rot / 2 in all."""
+        rot = D if rot is None else rot
+        axes = None
+        if sections is not None:
+            axes = [a for a, n in enumerate(sections) for _ in range(n)]
+        return cls([base ** (-2.0 * i / rot) for i in range(rot // 2)], D,
+                   axes, interleaved, device)
+
+
+def _heads_view(name, t, B, S, H, D, dtype):
+    """attn_heads_t of a [B, S, H, D] tensor of any strides but the last."""
+    if t.shape != (B, S, H, D) or t.dtype is not dtype:
+        raise AttnError("%s must be %s of %s, got %s of %s" % (
+            name, [B, S, H, D], dtype, list(t.shape), t.dtype),
+            ATTN_ERR_INVALID_ARG)
+    b, s, h, d = t.stride()
+    if d != 1:
+        raise AttnError("%s's last dimension must be contiguous" % name,
+                        ATTN_ERR_INVALID_ARG)
+    return _Heads(t.data_ptr(), b, s, h)
+
+
+def _rope_weights(rope, q_weight, k_weight, dtype):
+    """(pointer, pointer, whether float32) of the norms' weights."""
+    out, f32 = [None, None], None
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is None:
+            continue
+        if w.shape != (rope.D,) or not w.is_contiguous() or \
+                w.dtype not in (dtype, rope.float32):
+            raise AttnError("weights must be contiguous [%d] of %s or float32"
+                            % (rope.D, dtype), ATTN_ERR_INVALID_ARG)
+        if f32 not in (None, w.dtype is rope.float32):
+            raise AttnError("both weights must be of one type",
+                            ATTN_ERR_INVALID_ARG)
+        f32 = w.dtype is rope.float32
+        out[i] = w.data_ptr()
+    return out[0], out[1], bool(f32)
+
+
+def _rope_positions(rope, positions, B, S):
+    if positions is None:
+        return None
+    if rope.axes > 1 or positions.dim() == 3:
+        _check_tensor("positions", positions, (rope.axes, B, S), rope.int32)
+    else:
+        _check_tensor("positions", positions, (B, S), rope.int32)
+    return positions.data_ptr()
+
+
+def _rope_dtype(rope, name, t):
+    dt = rope.dtypes.get(t.dtype)
+    if dt is None or t.dim() != 4:
+        raise AttnError("%s must be 4-D, float16 or bfloat16, got %s of %s"
+                        % (name, list(t.shape), t.dtype),
+                        ATTN_ERR_INVALID_ARG)
+    return dt
+
+
+def qk_rope(rope, q, k, v=None, q_weight=None, k_weight=None, eps=1e-6,
+            positions=None, lens=None, new_lens=None, offset=None, q_out=None,
+            k_out=None, v_out=None, stream=None):
+    """Norm of queries and keys per head, their rotation by position, and the
+    layout that attention reads, in one pass.
+
+    q [B, S, Hq, D], k and v [B, S, Hkv, D] (float16 or bfloat16, any strides
+    that are multiples of 8 with a contiguous last dimension: projections'
+    outputs, or parts of a packed one).  Returns (q, k, v) as [B, H, S, D];
+    v is copied, or None.  ``q_weight``, ``k_weight`` ([D], float32 or q's
+    type): weights of the norm x / sqrt(mean(x^2) + eps) * weight; None: not
+    normed.  ``positions`` int32 [axes, B, S] (or [B, S]); None: counted, from
+    ``offset`` (int32 [1]) up.  ``new_lens`` (int32 [B]): rows of each
+    sequence; the outputs behind them are left as they are.
+
+    ``lens`` (int32 [B]): k_out and v_out [B, Hkv, capacity, D] are a cache,
+    whose last new_lens (or S) of lens tokens the rows are; without
+    ``positions`` they count from there.
+    """
+    dt = _rope_dtype(rope, "q", q)
+    dtype, D = q.dtype, rope.D
+    B, S, Hq, _ = q.shape
+    Hkv = k.shape[2] if k.dim() == 4 else 0
+    heads = [_heads_view("q", q, B, S, Hq, D, dtype),
+             _heads_view("k", k, B, S, Hkv, D, dtype),
+             None if v is None else _heads_view("v", v, B, S, Hkv, D, dtype)]
+    wq, wk, f32 = _rope_weights(rope, q_weight, k_weight, dtype)
+    pos = _rope_positions(rope, positions, B, S)
+    for name, t, n in (("lens", lens, B), ("new_lens", new_lens, B),
+                       ("offset", offset, 1)):
+        if t is not None:
+            _check_tensor(name, t, (n,), rope.int32)
+    if q_out is None or k_out is None or (v_out is None and v is not None):
+        if lens is not None and (k_out is None or
+                                 (v_out is None and v is not None)):
+            raise AttnError("k_out and v_out must be given with lens",
+                            ATTN_ERR_INVALID_ARG)
+        import torch
+        with _kv8_memory(rope, stream):
+            if q_out is None:
+                q_out = torch.empty((B, Hq, S, D), dtype=dtype,
+                                    device=rope.device)
+            if k_out is None:
+                k_out = torch.empty((B, Hkv, S, D), dtype=dtype,
+                                    device=rope.device)
+            if v_out is None and v is not None:
+                v_out = torch.empty_like(k_out)
+    cap = k_out.shape[2] if k_out.dim() == 4 else 0
+    _check_tensor("q_out", q_out, (B, Hq, S, D), dtype)
+    _check_tensor("k_out", k_out, (B, Hkv, cap, D), dtype)
+    if v is not None:
+        _check_tensor("v_out", v_out, (B, Hkv, cap, D), dtype)
+    _kv8_call("attn_qk_rope", rope.lib.attn_qk_rope, rope, stream, *heads, wq,
+              wk, f32, eps, pos,
+              None if lens is None else lens.data_ptr(),
+              None if new_lens is None else new_lens.data_ptr(),
+              None if offset is None else offset.data_ptr(),
+              q_out.data_ptr(), k_out.data_ptr(),
+              None if v is None else v_out.data_ptr(), B, S, Hq, Hkv, cap, dt)
+    return q_out, k_out, v_out
+
+
+def qk_rope_bwd_workspace(rope):
+    """A workspace tensor for ``qk_rope_bwd`` calls of any size."""
+    import torch
+    with torch.cuda.device(rope.device):
+        return torch.empty(attn_qk_rope_bwd_workspace_bytes(rope.D),
+                           dtype=torch.uint8, device=rope.device)
+
+
+def qk_rope_bwd(rope, dq, dk, q=None, k=None, dv=None, q_weight=None,
+                k_weight=None, eps=1e-6, positions=None, offset=None,
+                dq_out=None, dk_out=None, dv_out=None, dq_weight=None,
+                dk_weight=None, workspace=None, stream=None):
+    """Backward pass of ``qk_rope`` (without ``lens`` and ``new_lens``).
+
+    dq, dk, dv [B, H, S, D] (contiguous): the gradients of its outputs, as
+    ``bwd`` returns them; q, k: its inputs (needed where they were normed).
+    Returns (dq, dk, dv, dq_weight, dk_weight): the inputs' gradients [B, S,
+    H, D] (``dq_out`` ... may be given, of any strides that qk_rope takes,
+    parts of one packed tensor among them) and the weights', float32 [D] or
+    None.  ``workspace``: from ``qk_rope_bwd_workspace``, allocated when not
+    given.
+    """
+    import torch
+    dt = _rope_dtype(rope, "dq", dq)
+    dtype, D = dq.dtype, rope.D
+    B, Hq, S, _ = dq.shape
+    Hkv = dk.shape[1] if dk.dim() == 4 else 0
+    _check_tensor("dq", dq, (B, Hq, S, D), dtype)
+    _check_tensor("dk", dk, (B, Hkv, S, D), dtype)
+    if dv is not None:
+        _check_tensor("dv", dv, (B, Hkv, S, D), dtype)
+    wq, wk, f32 = _rope_weights(rope, q_weight, k_weight, dtype)
+    pos = _rope_positions(rope, positions, B, S)
+    if offset is not None:
+        _check_tensor("offset", offset, (1,), rope.int32)
+    x = [None, None]
+    for i, (name, t, w, H) in enumerate((("q", q, wq, Hq), ("k", k, wk, Hkv))):
+        if w is None:
+            continue
+        if t is None:
+            raise AttnError("%s was normed and must be given" % name,
+                            ATTN_ERR_INVALID_ARG)
+        x[i] = _heads_view(name, t, B, S, H, D, dtype)
+    with _kv8_memory(rope, stream):
+        if dq_out is None:
+            dq_out = torch.empty((B, S, Hq, D), dtype=dtype,
+                                 device=rope.device)
+        if dk_out is None:
+            dk_out = torch.empty((B, S, Hkv, D), dtype=dtype,
+                                 device=rope.device)
+        if dv is None:
+            dv_out = None
+        elif dv_out is None:
+            dv_out = torch.empty((B, S, Hkv, D), dtype=dtype,
+                                 device=rope.device)
+        dw = [dq_weight, dk_weight]
+        for i, w in enumerate((wq, wk)):
+            if w is None:
+                dw[i] = None
+            elif dw[i] is None:
+                dw[i] = torch.empty(D, dtype=torch.float32,
+                                    device=rope.device)
+            else:
+                _check_tensor("weights' gradients", dw[i], (D,), rope.float32)
+        if workspace is None and (wq or wk):
+            workspace = qk_rope_bwd_workspace(rope)
+    if workspace is not None and not workspace.is_contiguous():
+        raise AttnError("workspace must be contiguous", ATTN_ERR_INVALID_ARG)
+    out = [_heads_view("dq_out", dq_out, B, S, Hq, D, dtype),
+           _heads_view("dk_out", dk_out, B, S, Hkv, D, dtype),
+           None if dv is None else
+           _heads_view("dv_out", dv_out, B, S, Hkv, D, dtype)]
+    _kv8_call("attn_qk_rope_bwd", rope.lib.attn_qk_rope_bwd, rope, stream,
+              dq.data_ptr(), dk.data_ptr(),
+              None if dv is None else dv.data_ptr(), *x, wq, wk, f32, eps, pos,
+              None if offset is None else offset.data_ptr(), *out,
+              None if dw[0] is None else dw[0].data_ptr(),
+              None if dw[1] is None else dw[1].data_ptr(), B, S, Hq, Hkv, dt,
+              None if workspace is None else workspace.data_ptr(),
+              0 if workspace is None else workspace.nbytes)
+    return dq_out, dk_out, dv_out, dw[0], dw[1]

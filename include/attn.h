@@ -438,6 +438,124 @@ attn_status_t attn_kv8_evict(const attn_kv8_t* src, const attn_kv8_t* dst,
                              int keep, int recent, int* indices,
                              attn_stream_t stream);
 
+/*
+ * attn_rope_t — a rotation of heads by position, on one or several axes.
+ * The pages' listings take Q and K as they come; this is what a decoder does
+ * to them before.  The first `rot` of a head's D elements form rot / 2 pairs:
+ * (i, i + rot / 2), or with `interleaved` (2i, 2i + 1).  At position t_a on
+ * axis a, pair i with axis[i] = a turns by the angle t_a * freq[i]:
+ *   (x, y) -> (x cos - y sin, x sin + y cos).
+ *
+ * phase  device, [rot / 2]: freq[i] in units of 2^-64 of a turn, from
+ *        attn_rope_phase.  Positions are multiplied with it modulo 2^64, so
+ *        that the fraction of a turn is exact at any distance; the angle is
+ *        then off by 2^-22 or less;
+ * axis   device, [rot / 2] values below `axes`; not read when axes is 1.
+ * D in {64, 128}, rot a multiple of 8 from 0 (norm only) to D, 1 <= axes <=
+ * 255.
+ */
+typedef struct {
+  const unsigned long long* phase;
+  const unsigned char* axis;
+  int D, rot, axes, interleaved;
+} attn_rope_t;
+
+/* A strided view [B, S, H, D] of 16-bit elements on the device, as a
+ * projection gives them: p 16-byte aligned, strides in elements, multiples of
+ * 8 and not negative (those of dimensions of one element are not read). */
+typedef struct {
+  void* p;
+  long long stride_b, stride_s, stride_h;
+} attn_heads_t;
+
+/* Frequencies (radians per position, host, |freq| <= 2^32) to the phases of
+ * attn_rope_t (host).  Host only. */
+attn_status_t attn_rope_phase(const double* freq, int n,
+                              unsigned long long* phase);
+
+/*
+ * attn_qk_rope — norm of queries and keys per head, their rotation, and the
+ * layout that attention reads, in one pass: for every row x of D elements of
+ * q and k
+ *   n = x / sqrt(mean(x^2) + eps) * weight      (n = x without a weight)
+ * and then the rotation above; v is copied.
+ *
+ * q          view with Hq heads; k, v  views with Hkv heads (read);
+ * v          NULL (with v_out NULL): no values;
+ * q_weight, k_weight  device [D] or NULL (no norm); float32 if weight_f32,
+ *            else dtype;
+ * eps        positive and finite (not looked at without a norm);
+ * q_out      device, [B, Hq, S, D] contiguous (written);
+ * k_out, v_out  device, [B, Hkv, capacity, D] contiguous (written), capacity
+ *            >= S: row i of a sequence goes to place i, or with lens to place
+ *            lens[b] - n_b + i, the last n_b of a cache whose length already
+ *            counts them (attn_prefix_cache_t's k and v are such);
+ * lens, new_lens  device int32 [B] or NULL: n_b = S, or new_lens[b] rows,
+ *            0 <= n_b <= S, n_b <= lens[b] <= capacity.  Values outside are
+ *            taken as the nearer end and reported by attn_device_status (bit 1
+ *            of the code).  Rows i >= n_b are ignored and nothing is written
+ *            for them;
+ * positions  device int32 [axes, B, S] or NULL: then a row's position on every
+ *            axis is its place (i, or lens[b] - n_b + i), plus *offset;
+ * offset     device int32 [1] or NULL (0), only without positions.  (The
+ *            length of a shared prefix ahead of the cache.)
+ * dtype      ATTN_F16 or ATTN_BF16: of all views and outputs.
+ *
+ * Computed in fp32 and rounded once.  Rows whose squares pass fp32's largest
+ * number are scaled by a power of two first.  Outputs must not overlap each
+ * other nor the range of memory that a view spans.  B == 0 or S == 0 is a
+ * successful no-op.  Deterministic.
+ */
+attn_status_t attn_qk_rope(const attn_rope_t* rope, const attn_heads_t* q,
+                           const attn_heads_t* k, const attn_heads_t* v,
+                           const void* q_weight, const void* k_weight,
+                           int weight_f32, float eps, const int* positions,
+                           const int* lens, const int* new_lens,
+                           const int* offset, void* q_out, void* k_out,
+                           void* v_out, int B, int S, int Hq, int Hkv,
+                           int capacity, attn_dtype_t dtype,
+                           attn_stream_t stream);
+
+/*
+ * attn_qk_rope_bwd — backward pass of attn_qk_rope without lens (every
+ * sequence has S rows): from the gradients of its outputs, as attn_bwd leaves
+ * them, those of its inputs and weights.  With dn the rotation of the upstream
+ * gradient by the opposite angles, r = 1 / sqrt(mean(x^2) + eps) and g = dn *
+ * weight:
+ *   dx = r * (g - x r^2 mean(g x)),  dweight = sum over rows of dn * x r;
+ * without a weight dx = dn.
+ *
+ * dq_out, dk_out, dv_out  device, [B, Hq or Hkv, S, D] contiguous (read);
+ *            dv_out may be NULL (with dv NULL);
+ * q, k       the forward's views (read where they were normed; else NULL
+ *            will do);
+ * dq, dk, dv views (written): the gradients of q, k and v.  No two of their
+ *            places may share an element; they may lie side by side within
+ *            each token of one buffer, as the forward's inputs may;
+ * dq_weight, dk_weight  device float32 [D] (written), given exactly where the
+ *            weight is; summed in fp32 in a fixed order;
+ * workspace  device, 256-byte aligned, at least
+ *            attn_qk_rope_bwd_workspace_bytes(D) bytes; contents need no
+ *            initialisation; not looked at without weights.  It must not be
+ *            used by another call until this one has run.
+ * Other arguments as attn_qk_rope.  One kernel on `stream`, two with weights.
+ * Outputs and workspace must not overlap each other or any input.  B == 0 or
+ * S == 0 writes zeros to the weights' gradients.  Deterministic.
+ */
+attn_status_t attn_qk_rope_bwd(
+    const attn_rope_t* rope, const void* dq_out, const void* dk_out,
+    const void* dv_out, const attn_heads_t* q, const attn_heads_t* k,
+    const void* q_weight, const void* k_weight, int weight_f32, float eps,
+    const int* positions, const int* offset, const attn_heads_t* dq,
+    const attn_heads_t* dk, const attn_heads_t* dv, float* dq_weight,
+    float* dk_weight, int B, int S, int Hq, int Hkv, attn_dtype_t dtype,
+    void* workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* Workspace bytes attn_qk_rope_bwd needs (0 for another D than 64 and 128).
+ * Host only; the value is for the current device's SM count (152 without a
+ * device). */
+size_t attn_qk_rope_bwd_workspace_bytes(int D);
+
 /* Short English description of a status code (static storage). */
 const char* attn_status_string(attn_status_t status);
 
