@@ -31,6 +31,8 @@ __all__ = [
     "attn_rope_phase", "attn_qk_rope", "attn_qk_rope_bwd",
     "attn_qk_rope_bwd_workspace_bytes",
     "Rope", "qk_rope", "qk_rope_bwd", "qk_rope_bwd_workspace",
+    "attn_prefix_fwd", "attn_prefix_workspace_bytes",
+    "PrefixCache", "prefix_fwd", "prefix_workspace",
     "library_path", "load_library",
 ]
 
@@ -84,6 +86,14 @@ class _Heads(ctypes.Structure):
     """attn_heads_t of include/attn.h."""
     _fields_ = [("p", ctypes.c_void_p)] + [
         (n, ctypes.c_longlong) for n in ("stride_b", "stride_s", "stride_h")]
+
+
+class _Prefix(ctypes.Structure):
+    """attn_prefix_cache_t of include/attn.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "prefix_k", "prefix_v", "prefix_len", "k", "v", "lens")] + [
+            (n, ctypes.c_int) for n in ("B", "Hkv", "prefix_capacity",
+                                        "capacity", "D")]
 
 
 def library_path() -> str:
@@ -181,6 +191,11 @@ def load_library():
         lib.attn_qk_rope_bwd.restype = i
         lib.attn_qk_rope_bwd_workspace_bytes.argtypes = [i]
         lib.attn_qk_rope_bwd_workspace_bytes.restype = sz
+        lib.attn_prefix_fwd.argtypes = [ctypes.POINTER(_Prefix), vp, vp, vp, i,
+                                        i, vp, f, i, i, vp, sz, vp]
+        lib.attn_prefix_fwd.restype = i
+        lib.attn_prefix_workspace_bytes.argtypes = [i] * 7
+        lib.attn_prefix_workspace_bytes.restype = sz
         _lib = lib
         return lib
 
@@ -439,6 +454,22 @@ def attn_qk_rope_bwd(rope, dq_out, dk_out, dv_out, q, k, q_weight, k_weight,
 
 def attn_qk_rope_bwd_workspace_bytes(D) -> int:
     return int(load_library().attn_qk_rope_bwd_workspace_bytes(D))
+
+
+def attn_prefix_fwd(cache, Q, O, LSE, Hq, Sq, new_lens, scale, causal, dtype,
+                    workspace, workspace_bytes, stream) -> int:
+    """Raw C-ABI call; ``cache`` is a ``PrefixCache``, pointers are
+    integers."""
+    return int(load_library().attn_prefix_fwd(
+        cache.struct, Q or None, O or None, LSE or None, Hq, Sq,
+        new_lens or None, float(scale), int(causal), int(dtype),
+        workspace or None, int(workspace_bytes), stream or None))
+
+
+def attn_prefix_workspace_bytes(B, Hq, Hkv, Sq, prefix_capacity, capacity,
+                                D) -> int:
+    return int(load_library().attn_prefix_workspace_bytes(
+        B, Hq, Hkv, Sq, prefix_capacity, capacity, D))
 
 
 def attn_version() -> int:
@@ -1168,3 +1199,136 @@ def qk_rope_bwd(rope, dq, dk, q=None, k=None, dv=None, q_weight=None,
               None if workspace is None else workspace.data_ptr(),
               0 if workspace is None else workspace.nbytes)
     return dq_out, dk_out, dv_out, dw[0], dw[1]
+
+
+class PrefixCache:
+    """Handle of the keys and values of a batch whose sequences share a prefix
+    (``attn_prefix_cache_t``).
+
+    prefix_k, prefix_v [1, Hkv, prefix_capacity, D]: the prefix's, of which
+    prefix_len (int32 [1]) tokens are used; k, v [B, Hkv, capacity, D]: each
+    sequence's own behind it, of which lens (int32 [B]) are used, the current
+    step's new ones included.  All contiguous, float16 or bfloat16, on one CUDA
+    device; the tensors stay the caller's and are kept alive by the handle.
+    Advance ``lens`` first, then write the new tokens (``qk_rope`` with
+    lens=cache.lens, offset=cache.prefix_len, k_out=cache.k, v_out=cache.v),
+    then ``prefix_fwd``.
+    """
+
+    def __init__(self, prefix_k, prefix_v, prefix_len, k, v, lens):
+        import torch
+        if k.dim() != 4 or prefix_k.dim() != 4:
+            raise AttnError("k must be 4-D [B, Hkv, capacity, D] and prefix_k "
+                            "[1, Hkv, prefix_capacity, D]",
+                            ATTN_ERR_INVALID_ARG)
+        B, Hkv, capacity, D = k.shape
+        P = prefix_k.shape[2]
+        types = (torch.float16, torch.bfloat16)
+        if k.dtype not in types:
+            raise AttnError("k must be float16 or bfloat16, got %s" % k.dtype,
+                            ATTN_ERR_INVALID_ARG)
+        for name, t, shape, dtype in (
+                ("prefix_k", prefix_k, (1, Hkv, P, D), k.dtype),
+                ("prefix_v", prefix_v, (1, Hkv, P, D), k.dtype),
+                ("prefix_len", prefix_len, (1,), torch.int32),
+                ("k", k, (B, Hkv, capacity, D), k.dtype),
+                ("v", v, (B, Hkv, capacity, D), k.dtype),
+                ("lens", lens, (B,), torch.int32)):
+            _check_tensor(name, t, shape, dtype)
+            if not t.is_cuda or t.device != k.device:
+                raise AttnError("%s must be a CUDA tensor on k's device"
+                                % name, ATTN_ERR_INVALID_ARG)
+        self.prefix_k, self.prefix_v = prefix_k, prefix_v
+        self.prefix_len, self.k, self.v, self.lens = prefix_len, k, v, lens
+        self.B, self.Hkv, self.capacity, self.D = B, Hkv, capacity, D
+        self.prefix_capacity = P
+        self.device, self.dtype = k.device, k.dtype
+        # What every call needs, looked up once.
+        self.dtypes = {k.dtype: ATTN_F16 if k.dtype == torch.float16
+                       else ATTN_BF16}
+        self.int32, self.float32 = torch.int32, torch.float32
+        self.lib, self.index = load_library(), k.device.index
+        self.current_device = torch._C._cuda_getDevice
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.struct = ctypes.pointer(_Prefix(
+            prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_len.data_ptr(),
+            k.data_ptr(), v.data_ptr(), lens.data_ptr(), B, Hkv, P, capacity,
+            D))
+
+    @classmethod
+    def empty(cls, prefix_k, prefix_v, B, capacity, prefix_len=None,
+              lens=None):
+        """Caches of new, uninitialised memory for B sequences behind a prefix
+        (all of prefix_k's tokens unless ``prefix_len`` is given); ``lens``:
+        zeros unless given."""
+        import torch
+        _, Hkv, P, D = prefix_k.shape
+        dev = prefix_k.device
+        k, v = (torch.empty((B, Hkv, capacity, D), dtype=prefix_k.dtype,
+                            device=dev) for _ in range(2))
+        if prefix_len is None:
+            prefix_len = torch.tensor([P], dtype=torch.int32, device=dev)
+        if lens is None:
+            lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        return cls(prefix_k, prefix_v, prefix_len, k, v, lens)
+
+
+def prefix_workspace(cache, Hq, Sq):
+    """A workspace tensor for ``prefix_fwd`` calls of Hq heads and Sq rows."""
+    import torch
+    with torch.cuda.device(cache.device):
+        n = attn_prefix_workspace_bytes(cache.B, Hq, cache.Hkv, Sq,
+                                        cache.prefix_capacity, cache.capacity,
+                                        cache.D)
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=cache.device)
+
+
+def prefix_fwd(cache, q, scale=None, causal=True, new_lens=None, out=None,
+               lse=None, need_lse=True, workspace=None, stream=None):
+    """Attention of q [B, Hq, Sq, D] (contiguous, the cache's type) over a
+    shared prefix and each sequence's own tokens behind it.  Returns (O, LSE)
+    like ``fwd``.
+
+    Row i of a sequence with n new rows (Sq, or ``new_lens[b]`` of them) is its
+    own token lens - n + i: it sees the prefix and its own tokens up to it
+    (``causal``), or all of them.  Rows that see nothing get O = 0 and LSE =
+    -inf; rows at or behind new_lens are left as they are in ``out`` and
+    ``lse``.  ``workspace``: from ``prefix_workspace``, allocated when not
+    given.  What a call on ``stream`` allocates is that stream's memory.
+    """
+    dt = _kv8_dtype(cache, "q", q)
+    dtype, B, shape = q.dtype, cache.B, q.shape
+    _, Hq, Sq, D = shape
+    if shape[0] != B or D != cache.D or not q.is_contiguous():
+        _check_tensor("q", q, (B, Hq, Sq, cache.D), dtype)
+    if out is None:
+        import torch
+        with _kv8_memory(cache, stream):
+            out = torch.empty_like(q)
+    else:
+        _check_tensor("out", out, shape, dtype)
+    if not need_lse:
+        lse = None
+    elif lse is None:
+        import torch
+        with _kv8_memory(cache, stream):
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32,
+                              device=cache.device)
+    else:
+        _check_tensor("lse", lse, (B, Hq, Sq), cache.float32)
+    if workspace is None:
+        with _kv8_memory(cache, stream):
+            workspace = prefix_workspace(cache, Hq, Sq)
+    elif not workspace.is_contiguous():
+        raise AttnError("workspace must be contiguous", ATTN_ERR_INVALID_ARG)
+    if new_lens is not None:
+        _check_tensor("new_lens", new_lens, (B,), cache.int32)
+        new_lens = new_lens.data_ptr()
+    if scale is None:
+        scale = cache.D ** -0.5
+    _kv8_call("attn_prefix_fwd", cache.lib.attn_prefix_fwd, cache, stream,
+              q.data_ptr(), out.data_ptr(),
+              lse.data_ptr() if lse is not None else None, Hq, Sq, new_lens,
+              scale, bool(causal), dt, workspace.data_ptr(),
+              workspace.nbytes)
+    return out, lse

@@ -234,6 +234,11 @@ bool on_device(const void* p, int dev) { return is_device_ptr(p, dev); }
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
   return na != 0 && nb != 0 && overlaps(a, na, b, nb);
 }
+bool make_tile_map(CUtensorMap* m, const void* base, bool bf16, int D,
+                   int rows, long long planes, int box_rows) {
+  return make_map(m, base, bf16 ? ATTN_BF16 : ATTN_F16, D, rows, planes,
+                  box_rows);
+}
 
 bool current_context_id(unsigned long long* id) {
   std::call_once(g_ctx_once, [] {

@@ -3,6 +3,8 @@
 
 #include <cstddef>
 
+#include <cuda.h>
+
 namespace attn {
 
 // Status-word bit 1: a kernel met a length outside its range and clamped it.
@@ -18,5 +20,11 @@ unsigned long long wait_timeout_ns();
 bool on_device(const void* p, int dev);
 // Whether two byte ranges share a byte.
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb);
+
+// Map of a [planes, rows, D] tensor of 16-bit elements for copies of box_rows
+// rows by one 128-byte segment, 128-byte swizzled (false: it could not be
+// made).
+bool make_tile_map(CUtensorMap* m, const void* base, bool bf16, int D,
+                   int rows, long long planes, int box_rows);
 
 }  // namespace attn

@@ -209,18 +209,22 @@ struct FwdParams {
 };
 
 // ------------------------------------------------ shared by the forwards
+// (Params: this header's or another cache's with the fields used here.)
 constexpr float kNone = -3.402823466e38f;  // running maximum of no score
 
-__device__ __forceinline__ int seq_len(const FwdParams& p, int b) {
+template <class Params>
+__device__ __forceinline__ int seq_len(const Params& p, int b) {
   return clamp_len(p.lens[b], p.capacity, p.status);
 }
-__device__ __forceinline__ int seq_new(const FwdParams& p, int b) {
+template <class Params>
+__device__ __forceinline__ int seq_new(const Params& p, int b) {
   return p.new_lens == nullptr ? p.Sq
                                : clamp_len(p.new_lens[b], p.Sq, p.status);
 }
 // Visible tokens of row r (token-major: row r = token r / group, head
 // r % group) of a sequence.
-__device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
+template <class Params>
+__device__ __forceinline__ int row_end(const Params& p, int len, int n_new,
                                        int r) {
   if (!p.causal) return len;
   return min(len, max(0, len - n_new + r / p.group + 1));
@@ -236,8 +240,8 @@ __device__ __forceinline__ int places(int len) {
 
 // Places before sequence `seq` and of all sequences, for every lane of the
 // calling warp.
-template <int kKeys, int kOver>
-__device__ __forceinline__ int list_tiles(const FwdParams& p, int seq,
+template <int kKeys, int kOver, class Params>
+__device__ __forceinline__ int list_tiles(const Params& p, int seq,
                                           int lane, int* before) {
   int t = 0, pre = 0;
   for (int b = lane; b < p.B; b += 32) {
@@ -266,8 +270,8 @@ struct Cut {
   }
 };
 // kLeast places a CTA are the finest cut.
-template <int kLeast>
-__device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
+template <int kLeast, class Params>
+__device__ __forceinline__ Cut make_cut(const Params& p, int total) {
   Cut c;
   c.n = max(1, min(p.grid, (total + kLeast - 1) / kLeast));
   c.q = total / c.n;
@@ -284,8 +288,8 @@ struct Segment {
 };
 
 // CTA's share: its number of places (0: none) and first segment.
-template <int kKeys, int kOver, int kLeast>
-__device__ __forceinline__ int take_share(const FwdParams& p, int cta,
+template <int kKeys, int kOver, int kLeast, class Params>
+__device__ __forceinline__ int take_share(const Params& p, int cta,
                                           int lane, Segment* s) {
   int first = 0, count = 0, base = 0;
   if (p.B > 32) {
@@ -329,8 +333,8 @@ __device__ __forceinline__ int take_share(const FwdParams& p, int cta,
   return 0;
 }
 
-template <int kKeys, int kOver>
-__device__ __forceinline__ void next_segment(const FwdParams& p, Segment& c) {
+template <int kKeys, int kOver, class Params>
+__device__ __forceinline__ void next_segment(const Params& p, Segment& c) {
   c.pos = c.end + kOver;
   if (++c.h == p.Hkv) {
     c.h = 0;

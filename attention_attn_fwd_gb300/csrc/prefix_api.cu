@@ -1,0 +1,281 @@
+// C ABI of the attention behind a shared prefix: argument checks, the choice
+// of kernels and launches.  No device memory is allocated here.
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/attn.h"
+#include "attn_host.h"
+#include "prefix_common.cuh"
+
+namespace {
+
+using attn::prefix::PrefixParams;
+
+constexpr size_t kWorkspaceAlign = 256;
+
+size_t round_up(size_t x) {
+  return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign;
+}
+
+bool misaligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) != 0;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+bool any_overlap(const Range& a, const Range* others, int count) {
+  for (int i = 0; i < count; ++i)
+    if (attn::ranges_overlap(a.p, a.n, others[i].p, others[i].n)) return true;
+  return false;
+}
+
+struct Sizes {
+  int B, Hq, Hkv, Sq, prefix_capacity, capacity, D;
+};
+
+attn_status_t check_sizes(const Sizes& z) {
+  if (z.B < 0 || z.Hkv <= 0 || z.Hq <= 0 || z.Hq % z.Hkv != 0 || z.Sq < 0 ||
+      z.prefix_capacity < 1 || z.capacity < 1 || z.D <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (z.D != 64 && z.D != 128) return ATTN_ERR_UNSUPPORTED;
+  // Counts of tokens, tiles and rows stay within int32 with a tile behind.
+  constexpr long long kMost = 0x7fffffffLL - (1 << 16);
+  if (z.prefix_capacity >= kMost || z.capacity >= kMost ||
+      static_cast<long long>(z.B) * z.Hkv >= (1 << 24))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+// How the rows of a K/V head meet the keys; see Mode.
+struct Plan {
+  int mode;
+  long long rows;        // R
+  long long pack_blocks, row_blocks;
+  int many_grid, few_grid;
+};
+
+// Rows of a sequence that fill 256-row units well are not packed with others:
+// packed, their results over the prefix and over their own keys have to meet
+// in memory.
+bool fills_units(long long rows) {
+  const long long blocks = (rows + attn::prefix::kUnitRows - 1) /
+                           attn::prefix::kUnitRows;
+  return 4 * rows >= 3 * blocks * attn::prefix::kUnitRows;
+}
+
+Plan make_plan(const Sizes& z, int sms) {
+  Plan p;
+  p.rows = static_cast<long long>(z.Hq / z.Hkv) * z.Sq;
+  p.mode = p.rows <= 16 ? attn::prefix::kFew
+           : fills_units(p.rows) || z.B == 1 ? attn::prefix::kJoint
+                                             : attn::prefix::kPacked;
+  const long long unit = attn::prefix::kUnitRows;
+  p.pack_blocks =
+      p.mode == attn::prefix::kJoint ? 0 : (z.B * p.rows + unit - 1) / unit;
+  p.row_blocks =
+      p.mode == attn::prefix::kFew ? 0 : (p.rows + unit - 1) / unit;
+  p.many_grid = sms;
+  p.few_grid =
+      p.mode == attn::prefix::kFew
+          ? sms * attn::prefix::few_ctas(
+                      z.D, attn::prefix::few_rows(static_cast<int>(p.rows)))
+          : 0;
+  return p;
+}
+
+// Whether the kernels' counts of rows and list places fit 32 bits.
+bool counts_fit(const Sizes& z, const Plan& p) {
+  const long long kMost = 0x7fffffffLL - 4096;
+  if (p.rows > kMost || z.B * p.rows > kMost) return false;
+  const double tiles = z.prefix_capacity / 128.0 + z.capacity / 128.0 + 16;
+  const double units =
+      static_cast<double>(z.Hkv) * (p.pack_blocks + z.B * p.row_blocks);
+  if (units * tiles > kMost) return false;
+  const double few = static_cast<double>(z.B) * z.Hkv *
+                     (z.capacity / (2048.0 / z.D) + 16);
+  return p.mode != attn::prefix::kFew || few <= kMost;
+}
+
+struct Workspace {
+  size_t base_o, base_lse2, slot_o, slot_lse2, info, split, few_o, few_lse2;
+  size_t total;
+};
+
+Workspace workspace_layout(const Sizes& z, const Plan& p) {
+  const bool joint = p.mode == attn::prefix::kJoint;
+  const size_t row = static_cast<size_t>(z.D) * 4;
+  const size_t all = static_cast<size_t>(z.B) * z.Hkv * p.rows;
+  const size_t base = joint ? 0 : p.mode == attn::prefix::kFew ? all : 2 * all;
+  const size_t slots = static_cast<size_t>(p.many_grid) * (joint ? 2 : 1) *
+                       attn::prefix::kUnitRows;
+  const size_t units =
+      joint ? 0 : static_cast<size_t>(p.pack_blocks + z.B * p.row_blocks) * z.Hkv;
+  const size_t few =
+      p.mode == attn::prefix::kFew
+          ? (p.few_grid + static_cast<size_t>(z.B) * z.Hkv) *
+                attn::prefix::few_rows(static_cast<int>(p.rows))
+          : 0;
+  Workspace w;
+  w.base_o = 0;
+  w.base_lse2 = w.base_o + round_up(base * row);
+  w.slot_o = w.base_lse2 + round_up(base * 4);
+  w.slot_lse2 = w.slot_o + round_up(slots * row);
+  w.info = w.slot_lse2 + round_up(slots * 4);
+  w.split = w.info + round_up(units * 8);
+  w.few_o = w.split + (joint ? round_up(p.many_grid * size_t(16)) : 0);
+  w.few_lse2 = w.few_o + round_up(few * row);
+  w.total = w.few_lse2 + round_up(few * 4);
+  return w;
+}
+
+int current_sms() {
+  int dev = -1, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) sms = attn::device_sms(dev);
+  cudaGetLastError();  // no device: not an error of the caller's
+  return sms > 0 ? sms : 152;  // a GB300's without a device
+}
+
+attn_status_t fwd_impl(const attn_prefix_cache_t* c, const void* Q, void* O,
+                       float* LSE, int Hq, int Sq, const int* new_lens,
+                       float scale, int causal, attn_dtype_t dtype,
+                       void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  if (c == nullptr) return ATTN_ERR_INVALID_ARG;
+  const Sizes z{c->B, Hq, c->Hkv, Sq, c->prefix_capacity, c->capacity, c->D};
+  attn_status_t st = check_sizes(z);
+  if (st != ATTN_OK) return st;
+  if (!std::isfinite(scale) || (dtype != ATTN_F16 && dtype != ATTN_BF16))
+    return ATTN_ERR_INVALID_ARG;
+  if (z.B == 0 || Sq == 0) return ATTN_OK;
+  const void* need[] = {c->prefix_k, c->prefix_v, c->prefix_len, c->k,
+                        c->v,        c->lens,     Q,             O};
+  for (const void* x : need)
+    if (x == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (misaligned(c->prefix_k, 16) || misaligned(c->prefix_v, 16) ||
+      misaligned(c->k, 16) || misaligned(c->v, 16) || misaligned(Q, 16) ||
+      misaligned(O, 16) || misaligned(c->prefix_len, 4) ||
+      misaligned(c->lens, 4) || misaligned(LSE, 4) || misaligned(new_lens, 4))
+    return ATTN_ERR_ALIGNMENT;
+  if (workspace == nullptr || misaligned(workspace, kWorkspaceAlign))
+    return ATTN_ERR_ALIGNMENT;
+  const Plan plan = make_plan(z, current_sms());
+  if (!counts_fit(z, plan)) return ATTN_ERR_INVALID_ARG;
+  const Workspace w = workspace_layout(z, plan);
+  if (workspace_bytes < w.total) return ATTN_ERR_INVALID_ARG;
+  const size_t rows = static_cast<size_t>(z.B) * Hq * Sq;
+  const size_t head = static_cast<size_t>(z.D) * 2;
+  const size_t pre = static_cast<size_t>(z.Hkv) * z.prefix_capacity * head;
+  const size_t own = static_cast<size_t>(z.B) * z.Hkv * z.capacity * head;
+  const size_t len_bytes = static_cast<size_t>(z.B) * 4;
+  const Range in[] = {{c->prefix_k, pre}, {c->prefix_v, pre},
+                      {c->prefix_len, 4}, {c->k, own},
+                      {c->v, own},        {c->lens, len_bytes},
+                      {Q, rows * head},
+                      {new_lens, new_lens ? len_bytes : 0}};
+  const Range out[] = {{O, rows * head},
+                       {LSE, LSE ? rows * 4 : 0},
+                       {workspace, w.total}};
+  for (int i = 0; i < 3; ++i)
+    if (any_overlap(out[i], in, 8) || any_overlap(out[i], out + i + 1, 2 - i))
+      return ATTN_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  const void* more[] = {LSE, new_lens, workspace};
+  for (const void* x : need)
+    if (!attn::on_device(x, dev)) return ATTN_ERR_INVALID_ARG;
+  for (const void* x : more)
+    if (x != nullptr && !attn::on_device(x, dev)) return ATTN_ERR_INVALID_ARG;
+  PrefixParams p{};
+  p.k = static_cast<const uint16_t*>(c->k);
+  p.v = static_cast<const uint16_t*>(c->v);
+  p.plen = c->prefix_len;
+  p.lens = c->lens;
+  p.new_lens = new_lens;
+  p.q = static_cast<const uint16_t*>(Q);
+  p.o = static_cast<uint16_t*>(O);
+  p.lse = LSE;
+  p.B = z.B;
+  p.Hq = Hq;
+  p.Hkv = z.Hkv;
+  p.Sq = Sq;
+  p.prefix_capacity = z.prefix_capacity;
+  p.capacity = z.capacity;
+  p.group = Hq / z.Hkv;
+  p.rows = static_cast<int>(plan.rows);
+  p.mode = plan.mode;
+  p.causal = causal != 0;
+  p.pack_blocks = static_cast<int>(plan.pack_blocks);
+  p.row_blocks = static_cast<int>(plan.row_blocks);
+  p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
+  p.negate = scale < 0.f;
+  char* ws = static_cast<char*>(workspace);
+  p.base_o = reinterpret_cast<float*>(ws + w.base_o);
+  p.base_lse2 = reinterpret_cast<float*>(ws + w.base_lse2);
+  p.slot_o = reinterpret_cast<float*>(ws + w.slot_o);
+  p.slot_lse2 = reinterpret_cast<float*>(ws + w.slot_lse2);
+  p.info = reinterpret_cast<int2*>(ws + w.info);
+  p.split = reinterpret_cast<int4*>(ws + w.split);
+  p.few_o = reinterpret_cast<float*>(ws + w.few_o);
+  p.few_lse2 = reinterpret_cast<float*>(ws + w.few_lse2);
+  p.many_grid = plan.many_grid;
+  p.few_grid = plan.few_grid;
+  p.timeout_ns = attn::wait_timeout_ns();
+  p.status = attn::device_status_word(dev);
+  if (p.status == nullptr) return ATTN_ERR_CUDA;
+  const bool bf16 = dtype == ATTN_BF16;
+  // (The many-row kernel reads a sequence's own keys only where it works on
+  // them.)
+  CUtensorMap maps[8];
+  const void* bases[] = {c->prefix_k, c->prefix_v, c->k, c->v};
+  for (int i = 0; i < 4; ++i) {
+    const bool is_own = i >= 2;
+    for (int tail = 0; tail < 2; ++tail) {
+      CUtensorMap* m = &maps[(is_own ? 4 : 0) + 2 * tail + i % 2];
+      if (is_own && plan.mode == attn::prefix::kFew)
+        *m = maps[2 * tail + i % 2];
+      else if (!attn::make_tile_map(
+                   m, bases[i], bf16, z.D,
+                   is_own ? z.capacity : z.prefix_capacity,
+                   is_own ? static_cast<long long>(z.B) * z.Hkv : z.Hkv,
+                   tail ? attn::prefix::kTailRows : attn::prefix::kTN))
+        return ATTN_ERR_CUDA;
+    }
+  }
+  cudaError_t err = attn::prefix::launch_many(z.D, bf16, p, maps, stream);
+  if (err == cudaSuccess && plan.mode == attn::prefix::kFew)
+    err = attn::prefix::launch_few(z.D, bf16, p, stream);
+  if (err == cudaSuccess)
+    err = attn::prefix::launch_merge(z.D, bf16, p, stream);
+  return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_prefix_fwd(const attn_prefix_cache_t* cache, const void* Q,
+                              void* O, float* LSE, int Hq, int Sq,
+                              const int* new_lens, float scale, int causal,
+                              attn_dtype_t dtype, void* workspace,
+                              size_t workspace_bytes, attn_stream_t stream) {
+  return fwd_impl(cache, Q, O, LSE, Hq, Sq, new_lens, scale, causal, dtype,
+                  workspace, workspace_bytes,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t attn_prefix_workspace_bytes(int B, int Hq, int Hkv, int Sq,
+                                   int prefix_capacity, int capacity, int D) {
+  const Sizes z{B, Hq, Hkv, Sq, prefix_capacity, capacity, D};
+  if (check_sizes(z) != ATTN_OK || B == 0 || Sq == 0) return 0;
+  const Plan plan = make_plan(z, current_sms());
+  if (!counts_fit(z, plan)) return 0;
+  return workspace_layout(z, plan).total;
+}
+
+}  // extern "C"

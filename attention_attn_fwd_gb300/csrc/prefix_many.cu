@@ -1,0 +1,878 @@
+// Attention of many query rows over a shared prefix, and over the sequences'
+// own keys where a K/V head has more than 16 query rows.
+//
+// The prefix's keys are the same for every sequence, so its query rows are
+// packed across the batch: row x of a K/V head is row x % R of sequence x / R.
+// 256 of them (two 128-row Q tiles) make a unit, which streams the prefix's
+// 128-key tiles once: with B sequences the prefix is read once instead of B
+// times, and a decoding step's few rows fill the tensor cores' tiles.  Units
+// of one sequence's rows take its own keys; where those rows fill a unit
+// themselves (kJoint) its list of tiles is the prefix's and then its own, and
+// one pass makes the result.
+//
+// S = Q K^T and O += P V run as tcgen05 MMAs with fp32 accumulators in TMEM, K
+// and V by tensor-map copies into a ring of 128-byte-swizzled tiles.  A tile
+// that lengths end in is copied in boxes of 16 rows, its P V has as many
+// 16-key steps, and a warp clears V's rows between the length and the last
+// step's end (what lies there was never written and may be NaN; P is 0 there).
+// P is rounded to the inputs' type (2^-12 relative in fp16, 2^-9 in bf16: half
+// a step, that of O itself) and held times 2^kShift: in fp16, whose numbers end at
+// 65504, so that weights stay normal down to 2^-21 of the row's largest; in
+// bf16, whose V may come near fp32's largest number, so that sums of P V do not
+// pass it.  The row sums take P unrounded.
+//
+// Steps (unit, key tile) form one list, with some empty places before each
+// unit's, cut into equal consecutive shares, one per CTA: lengths come from
+// device memory and the cut follows them.  A unit's parts are joined by the
+// merge kernels (prefix_merge.cu).
+//
+// Roles (384 threads): warp 0 MMA issue, warp 1 tile copies, warp 2 walks the
+// share and publishes its units in shared memory, warp 3 clears the ends of V,
+// warps 4-7 / 8-11 query rows, softmax and output of Q tile 0 / 1.  Every wait
+// is bounded as in the forward kernel.
+#include "attn_sync.cuh"
+#include "prefix_common.cuh"
+
+namespace attn {
+namespace prefix {
+namespace {
+
+using kv8::kNone;
+
+constexpr int kThreads = 384;
+constexpr float kTau = 8.f;  // lazy rescale threshold (log2 units)
+// Registers: the launch gives every thread 168; the shares of the three
+// warpgroups add up to 3 * 168.
+constexpr int kRegsControl = 88;
+constexpr int kRegsSoftmax = 208;
+static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * 168,
+              "register split exceeds the launch allocation");
+
+constexpr int kUnits = 4;  // published units held at a time
+// Empty places of the list before each unit's steps, for what a part of a unit
+// takes besides them.
+constexpr int kOver = 4;
+
+// Tile maps: keys and values of the prefix and the sequences, whole tiles and
+// boxes of their last ones.
+struct Maps {
+  CUtensorMap m[8];  // 4 * own + 2 * tail + (V)
+};
+
+// Where a unit's part goes, other than a slot (>= 0).
+constexpr int kFinal = -2, kBase = -1;
+
+// A unit's part as the roles need it.
+struct Record {
+  int n_kv;       // key tiles of the part; 0: no more units
+  int j0;         // first of them
+  int np, plen;   // tiles and keys of the prefix in the unit's list
+  int b, h, len, n_new;  // b < 0: rows of all sequences
+  int row0;       // first row of tile 0
+  int dest;
+  int n[2];       // key tiles each Q tile sees
+  int full[2];    // own tiles below this one are seen whole by each valid row
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kBox = kTN * 128;             // 128 rows x 128 bytes
+  static constexpr int kTile = kBox * (D / 64);
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + 2 * kTile;
+  static constexpr int kBars = kRing + kSlots * kTile;
+  // kv_full, kv_empty [slots], unit_full, unit_empty, q[2], s[2], p[2], o[2],
+  // end, cleared, drain
+  static constexpr int kNumBars = 2 * kSlots + 2 * kUnits + 11;
+  static constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM base, abort
+  static constexpr int kRecords = kMisc + 8;
+  static constexpr int kBytes = kRecords + kUnits * sizeof(Record);
+  static_assert(kBytes + 1024 <= 227 * 1024, "shared memory per CTA");
+};
+
+// Valid keys of tile j of a unit's list, and whether it is the sequence's own.
+__device__ __forceinline__ int tile_keys(int j, int np, int plen, int len,
+                                         bool* own) {
+  *own = j >= np;
+  return *own ? min(kTN, len - (j - np) * kTN) : min(kTN, plen - j * kTN);
+}
+
+// ------------------------------------------------------------- the list
+__device__ __forceinline__ int places(int steps) {
+  return steps == 0 ? 0 : steps + kOver;
+}
+
+// A unit, or the part of one, that a CTA works on: key tiles [j0, j1) of its
+// `steps`.  Units are numbered (i, h), h fastest: i < pack_blocks rows of all
+// sequences, then (b, block).
+struct Unit {
+  int i, b, u, h;
+  int len, n_new, steps;
+  int j0, j1;
+};
+
+__device__ __forceinline__ int all_pairs(const PrefixParams& p) {
+  return p.pack_blocks + p.B * p.row_blocks;
+}
+
+__device__ __forceinline__ int pair_steps(const PrefixParams& p, int np, int i,
+                                          int* len, int* n_new) {
+  if (i < p.pack_blocks) {
+    *len = *n_new = 0;
+    return np;
+  }
+  const int b = (i - p.pack_blocks) / p.row_blocks;
+  const int u = i - p.pack_blocks - b * p.row_blocks;
+  *len = kv8::seq_len(p, b);
+  *n_new = kv8::seq_new(p, b);
+  if (u * kUnitRows >= *n_new * p.group) return 0;
+  return tiles_seen(p, *len, *n_new, u * kUnitRows, (u + 1) * kUnitRows) +
+         (p.mode == kJoint ? np : 0);
+}
+
+// Walks a CTA's share.  take() and next() are warp-collective and return
+// whether there is a unit.
+struct Walk {
+  Unit w;
+  int np;
+  int left;      // places of the share behind this unit's part
+  int cta;
+  kv8::Cut cut;
+
+  __device__ __forceinline__ void set_pair(const PrefixParams& p, int i) {
+    w.i = i;
+    if (i < p.pack_blocks) {
+      w.b = -1;
+      w.u = i;
+    } else {
+      w.b = (i - p.pack_blocks) / p.row_blocks;
+      w.u = i - p.pack_blocks - w.b * p.row_blocks;
+    }
+  }
+
+  __device__ __forceinline__ bool take(const PrefixParams& p, int cta_,
+                                       int lane) {
+    cta = cta_;
+    np = prefix_tiles(p);
+    const int pairs = all_pairs(p);
+    int total = 0;
+    for (int i = lane; i < pairs; i += 32) {
+      int len, n_new;
+      total += places(pair_steps(p, np, i, &len, &n_new));
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2)
+      total += __shfl_xor_sync(0xffffffffu, total, s);
+    total *= p.Hkv;
+    if (total == 0) return false;
+    cut = kv8::make_cut<1>(p, total);
+    if (cta >= cut.n) return false;
+    const int x = cut.first(cta);
+    const int count = cut.first(cta + 1) - x;
+    int base = 0;
+    for (int i0 = 0; i0 < pairs; i0 += 32) {
+      const int i = i0 + lane;
+      int len = 0, n_new = 0, steps = 0;
+      if (i < pairs) steps = pair_steps(p, np, i, &len, &n_new);
+      const int t = places(steps) * p.Hkv;
+      int incl = t;
+#pragma unroll
+      for (int s = 1; s < 32; s *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += up;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
+      if (hit != 0u) {
+        const int l = __ffs(hit) - 1;
+        set_pair(p, i0 + l);
+        const int off = x - base - __shfl_sync(0xffffffffu, incl - t, l);
+        w.len = __shfl_sync(0xffffffffu, len, l);
+        w.n_new = __shfl_sync(0xffffffffu, n_new, l);
+        w.steps = __shfl_sync(0xffffffffu, steps, l);
+        w.h = off / places(w.steps);
+        // Steps of the unit before the share (negative: empty places).
+        const int at = off - w.h * places(w.steps) - kOver;
+        w.j0 = max(0, at);
+        w.j1 = min(w.steps, at + count);
+        left = count - (w.j1 - at);
+        return w.j1 > w.j0;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+  }
+
+  __device__ __forceinline__ bool next(const PrefixParams& p) {
+    if (left <= kOver) return false;
+    if (++w.h == p.Hkv) {
+      w.h = 0;
+      int i = w.i;
+      do {  // some later unit has steps: the share is not at its end
+        ++i;
+        w.steps = pair_steps(p, np, i, &w.len, &w.n_new);
+      } while (w.steps == 0);
+      set_pair(p, i);
+    }
+    w.j0 = 0;
+    w.j1 = min(w.steps, left - kOver);
+    left -= places(w.j1);
+    return true;
+  }
+
+  // The CTA that has the unit's last step.
+  __device__ __forceinline__ int last_cta() const {
+    return cut.owner(cut.first(cta + 1) - 1 - left - w.j1 + w.steps);
+  }
+};
+
+__device__ __forceinline__ void fill_record(const PrefixParams& p,
+                                            const Walk& walk, int plen,
+                                            volatile Record* rec) {
+  const Unit& w = walk.w;
+  rec->n_kv = w.j1 - w.j0;
+  rec->j0 = w.j0;
+  const int np = w.b < 0 || p.mode == kJoint ? walk.np : 0;
+  rec->np = np;
+  rec->plen = plen;
+  rec->b = w.b;
+  rec->h = w.h;
+  rec->len = w.len;
+  rec->n_new = w.n_new;
+  rec->row0 = w.u * kUnitRows;
+  const bool whole = w.j0 == 0 && w.j1 == w.steps;
+  if (p.mode == kJoint)
+    rec->dest = whole ? kFinal : walk.cta + (w.j0 == 0 ? p.many_grid : 0);
+  else
+    rec->dest = w.j0 == 0 ? kBase : walk.cta;
+  for (int t = 0; t < 2; ++t) {
+    const int r0 = w.u * kUnitRows + t * kTM;
+    int hi = 0;
+    rec->full[t] = 0;
+    if (w.b < 0) {
+      if (r0 < static_cast<long long>(p.B) * p.rows) hi = np;
+    } else if (r0 < w.n_new * p.group) {
+      hi = np + tiles_seen(p, w.len, w.n_new, r0, r0 + kTM);
+      rec->full[t] = kv8::row_end(p, w.len, w.n_new, r0) / kTN;
+    }
+    rec->n[t] = max(0, min(hi, w.j1) - w.j0);
+  }
+}
+
+// kJoint: rows of units without steps see nothing: the warp writes their O and
+// LSE, each CTA its share of the units.  (Elsewhere the merge does.)
+template <int D>
+__device__ __forceinline__ void write_unseen(const PrefixParams& p, int lane) {
+  if (p.mode != kJoint) return;
+  const int np = prefix_tiles(p);
+  for (int i = blockIdx.x; i < p.B * p.row_blocks; i += gridDim.x) {
+    int len, n_new;
+    if (pair_steps(p, np, i, &len, &n_new) > 0) continue;
+    const int b = i / p.row_blocks, r0 = (i - b * p.row_blocks) * kUnitRows;
+    const int n = min(kUnitRows, n_new * p.group - r0);
+    for (int j = lane; j < n * p.Hkv; j += 32) {
+      const int h = j / n, r = r0 + j - h * n;
+      const long long row = q_row_index(p, b, h, r);
+      uint4* dst = reinterpret_cast<uint4*>(p.o + row * D);
+      for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr) p.lse[row] = -INFINITY;
+    }
+  }
+}
+
+// One 32-byte sector: a thread's row stores then fill sectors whole.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* x) {
+  asm volatile(
+      "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+      "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+      "r"(x[6]), "r"(x[7])
+      : "memory");
+}
+__device__ __forceinline__ void store_row(uint4* dst, const uint32_t* x,
+                                          bool wide) {
+  if (wide) {
+    store32(dst, x);
+  } else {
+    dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// ------------------------------------------------------------ the kernel
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_many_kernel(const __grid_constant__ Maps maps,
+                       const __grid_constant__ PrefixParams p) {
+  using L = Smem<D>;
+  constexpr int kOCol = 2 * kTN;  // TMEM: S0, S1, then O0, O1
+  constexpr float kShift = kBF16 ? -24.f : 7.f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_base = ptx::smem_u32(smem);
+  const uint32_t bar_full = s_base + L::kBars;           // [kSlots]
+  const uint32_t bar_empty = bar_full + 8 * L::kSlots;   // [kSlots]
+  const uint32_t bar_unit = bar_empty + 8 * L::kSlots;   // [kUnits]
+  const uint32_t bar_ufree = bar_unit + 8 * kUnits;      // [kUnits]
+  const uint32_t bar_q = bar_ufree + 8 * kUnits;         // [2]
+  const uint32_t bar_s = bar_q + 16;                     // [2]
+  const uint32_t bar_p = bar_s + 16;                     // [2]
+  const uint32_t bar_o = bar_p + 16;                     // [2]
+  const uint32_t bar_end = bar_o + 16;                   // [1]
+  const uint32_t bar_cleared = bar_end + 8;              // [1]
+  const uint32_t bar_drain = bar_end + 16;               // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
+  volatile Record* records = reinterpret_cast<Record*>(smem + L::kRecords);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x < L::kNumBars) {
+    const uint32_t bar = s_base + L::kBars + 8 * threadIdx.x;
+    // Q tiles: one arrival per warp of the four; units read: one per warp of
+    // the other roles (11); P: one per softmax thread of the tile.
+    uint32_t count = 1;
+    if (bar >= bar_ufree && bar < bar_q) count = 11;
+    if (bar >= bar_q && bar < bar_s) count = 4;
+    if (bar >= bar_p && bar < bar_o) count = kTM;
+    ptx::mbar_init(bar, count);
+    if (threadIdx.x == 0) *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (threadIdx.x >= 32 && threadIdx.x < 40)
+    ptx::prefetch_tensormap(&maps.m[threadIdx.x - 32]);
+  // Tensor memory is taken behind the wait for the kernel ahead (which may
+  // still have to take its own) and before the one behind may start.
+  ptx::griddep_wait();
+  if (warp == 0) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ptx::griddep_launch_dependents();
+
+  bool ok = true;
+  auto wait = [&](uint32_t bar, int phase, int role) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1, abort_flag, p,
+                                                role)) != 0;
+  };
+  // The k-th unit, nullptr at the end of the share (or on abort); and its
+  // release by this warp.
+  auto get_unit = [&](int k) -> volatile Record* {
+    ok = wait(bar_unit + 8 * (k % kUnits), k / kUnits, 1);
+    if (!ok) return nullptr;
+    volatile Record* rec = records + k % kUnits;
+    return rec->n_kv > 0 ? rec : nullptr;
+  };
+  auto release_unit = [&](int k) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar_ufree + 8 * (k % kUnits));
+  };
+
+  if (warp < 4) {
+    ptx::setmaxnreg_dec<kRegsControl>();
+    if (warp == 2) {
+      // ------------------------------------------------ units of the share
+      Walk walk;
+      bool more = walk.take(p, static_cast<int>(blockIdx.x), lane);
+      const int plen = prefix_len(p);
+      int4 split = make_int4(0, 0, 0, 0);
+      for (int k = 0; ok; ++k) {
+        if (k >= kUnits)
+          ok = wait(bar_ufree + 8 * (k % kUnits), k / kUnits - 1, 1);
+        if (!ok) break;
+        volatile Record* rec = records + k % kUnits;
+        if (lane == 0) {
+          if (more)
+            fill_record(p, walk, plen, rec);
+          else
+            rec->n_kv = 0;
+          ptx::mbar_arrive(bar_unit + 8 * (k % kUnits));
+        }
+        __syncwarp();
+        if (!more) break;
+        const Unit& w = walk.w;
+        if (w.j0 == 0) {
+          const int parts =
+              w.j1 < w.steps ? walk.last_cta() - walk.cta + 1 : 1;
+          if (p.mode == kJoint) {
+            if (parts > 1) split = make_int4(w.b, w.h, w.u, parts);
+          } else if (lane == 0) {
+            p.info[static_cast<long long>(w.i) * p.Hkv + w.h] =
+                make_int2(walk.cta, parts);
+          }
+        }
+        more = walk.next(p);
+      }
+      if (lane == 0 && p.mode == kJoint) p.split[blockIdx.x] = split;
+    } else if (warp == 3) {
+      // --------------------------------------- ends of V's last tiles
+      // In step with the MMA issuer, which asks for each when it has arrived
+      // (a warp that looked at some phases only of the ring's barriers could
+      // take one for another).
+      int it = 1;  // V tiles of the stream are odd
+      int uses = 0;
+      for (int k = 0; ok; ++k) {
+        volatile Record* rec = get_unit(k);
+        if (rec == nullptr) break;
+        const int n = rec->n_kv, j0 = rec->j0, np = rec->np;
+        const int plen = rec->plen, len = rec->len;
+        release_unit(k);
+        for (int j = 0; j < n; ++j, it += 2) {
+          bool own;
+          const int valid = tile_keys(j0 + j, np, plen, len, &own);
+          if (valid % 16 == 0) continue;
+          const int slot = it % L::kSlots;
+          ok = wait(bar_end, uses++, 5);
+          if (!ok) break;
+          const uint32_t at = s_base + L::kRing + slot * L::kTile;
+          const int rows = 16 - valid % 16;
+          for (int i = lane; i < rows * (D / 8); i += 32) {
+            const int c = i % 8, x = i / 8;
+            const int box = x / rows, r = valid + x - box * rows;
+            ptx::st_shared_v4(at + box * L::kBox + r * 128 + c * 16, 0u, 0u,
+                              0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_cleared);
+        }
+      }
+      write_unseen<D>(p, lane);
+    } else if (warp == 1) {
+      // -------------------------------------------------------- tile copies
+      int it = 0;
+      for (int k = 0; ok; ++k) {
+        volatile Record* rec = get_unit(k);
+        if (rec == nullptr) break;
+        const int n = rec->n_kv, j0 = rec->j0, np = rec->np;
+        const int plen = rec->plen, len = rec->len, h = rec->h;
+        const int own_plane = rec->b * p.Hkv + h;
+        release_unit(k);
+        for (int j = 0; j < n && ok; ++j) {
+          bool own;
+          const int valid = tile_keys(j0 + j, np, plen, len, &own);
+          const int row = (own ? j0 + j - np : j0 + j) * kTN;
+          const int plane = own ? own_plane : h;
+          const bool tail = valid <= kTN - kTailRows;
+          const int rows =
+              tail ? (valid + kTailRows - 1) / kTailRows * kTailRows : kTN;
+          const int step = tail ? kTailRows : kTN;
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = it % L::kSlots, use = it / L::kSlots;
+            if (use > 0) ok = wait(bar_empty + 8 * slot, use - 1, 1);
+            if (!ok) break;
+            if (lane == 0) {
+              const uint32_t bar = bar_full + 8 * slot;
+              const uint32_t dst = s_base + L::kRing + slot * L::kTile;
+              const CUtensorMap* m =
+                  &maps.m[(own ? 4 : 0) + (tail ? 2 : 0) + kv];
+              ptx::mbar_arrive_expect_tx(bar, rows * D * 2);
+              for (int r = 0; r < rows; r += step)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  ptx::tma_load_3d(dst + c * L::kBox + r * 128, m, bar, c * 64,
+                                   row + r, plane);
+            }
+            ++it;
+          }
+        }
+      }
+      if (!ok) {  // let the copies in flight land
+        for (int i = max(0, it - L::kSlots); i < it; ++i)
+          drain_wait(bar_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1, p);
+      }
+      __syncwarp();
+    } else if (warp == 0) {
+      // -------------------------------------------------------- MMA issue
+      const uint32_t idesc_qk = ptx::idesc_f16(kBF16, kTM, kTN, false, false);
+      const uint32_t idesc_pv = ptx::idesc_f16(kBF16, kTM, D, true, false);
+      constexpr uint32_t kHi = ptx::sdesc_hi_sw128(1024);
+      const uint32_t q_lo = ptx::sdesc_lo(s_base + L::kQ, 16);
+      const uint32_t k_lo = ptx::sdesc_lo(s_base + L::kRing, 16);
+      const uint32_t v_lo = ptx::sdesc_lo(s_base + L::kRing, L::kBox);
+      constexpr uint32_t kTile16 = L::kTile >> 4;
+      auto issue_qk = [&](int t, int slot) {
+        const uint32_t a0 = q_lo + t * kTile16, b0 = k_lo + slot * kTile16;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * L::kBox + (kk % 4) * 32) >> 4;
+          ptx::mma_ss_elect(tmem + t * kTN, a0 + off, b0 + off, kHi, idesc_qk,
+                            kk > 0 ? 1u : 0u);
+        }
+        ptx::tc_commit_elect(bar_s + 8 * t);
+      };
+      // `steps` of 16 keys.
+      auto issue_pv = [&](int t, int slot, bool acc, int steps) {
+        const uint32_t b0 = v_lo + slot * kTile16;
+#pragma unroll
+        for (int kk = 0; kk < kTN / 16; ++kk)
+          if (kk < steps)
+            ptx::mma_ts_elect(tmem + kOCol + t * D, tmem + t * kTN + kk * 8,
+                              b0 + ((kk * 16 * 128) >> 4), kHi, idesc_pv,
+                              (acc || kk > 0) ? 1u : 0u);
+      };
+      int it = 0;  // tiles consumed
+      int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+      int ends = 0;  // tiles cleared behind their last key
+      bool issued = false;
+      for (int k = 0; ok; ++k) {
+        ok = wait(bar_unit + 8 * (k % kUnits), k / kUnits, 1);
+        if (!ok) break;
+        // Through a warp reduction the counts are warp-uniform to the
+        // compiler, and with them the ring position: descriptors then stay in
+        // uniform registers (else every MMA moves them there first).
+        volatile Record* rec = records + k % kUnits;
+        const int n0 = __reduce_max_sync(0xffffffffu, rec->n[0]);
+        const int n1 = __reduce_max_sync(0xffffffffu, rec->n[1]);
+        const int n_kv = __reduce_max_sync(0xffffffffu, rec->n_kv);
+        const int j0 = __reduce_max_sync(0xffffffffu, rec->j0);
+        const int np = __reduce_max_sync(0xffffffffu, rec->np);
+        const int plen = __reduce_max_sync(0xffffffffu, rec->plen);
+        const int len = __reduce_max_sync(0xffffffffu, rec->len);
+        if (n_kv == 0) break;
+        release_unit(k);
+        ok = wait(bar_full + 8 * (it % L::kSlots), it / L::kSlots, 2);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int n = t ? n1 : n0;
+          if (!ok || n == 0) continue;
+          ok = wait(bar_q + 8 * t, q_uses[t], 2);
+          if (!ok) break;
+          ++q_uses[t];
+          ptx::tc_fence_after();
+          issue_qk(t, it % L::kSlots);
+          issued = true;
+        }
+        if (!ok) break;
+        ptx::tc_commit_elect(bar_empty + 8 * (it % L::kSlots));
+        const int it0 = it;
+        for (int j = 0; j < n_kv && ok; ++j) {
+          const int it_v = it0 + 2 * j + 1, it_k = it0 + 2 * j + 2;
+          const int slot_v = it_v % L::kSlots, slot_k = it_k % L::kSlots;
+          bool own;
+          const int valid = tile_keys(j0 + j, np, plen, len, &own);
+          const int steps = (valid + 15) / 16;
+          ok = wait(bar_full + 8 * slot_v, it_v / L::kSlots, 2);
+          if (!ok) break;
+          bool clear = valid % 16 != 0;
+          if (clear && lane == 0) ptx::mbar_arrive(bar_end);
+          bool k_ready = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int n = t ? n1 : n0;
+            if (!ok || j >= n) continue;
+            ok = wait(bar_p + 8 * t, p_uses[t], 2);
+            if (!ok) break;
+            ++p_uses[t];
+            if (clear) {
+              ok = wait(bar_cleared, ends++, 2);
+              if (!ok) break;
+              clear = false;
+            }
+            ptx::tc_fence_after();
+            issue_pv(t, slot_v, j > 0, steps);
+            if (j == n - 1) {
+              ptx::tc_commit_elect(bar_o + 8 * t);
+              continue;
+            }
+            if (!k_ready) {
+              ok = wait(bar_full + 8 * slot_k, it_k / L::kSlots, 2);
+              if (!ok) break;
+              k_ready = true;
+              ptx::tc_fence_after();
+            }
+            issue_qk(t, slot_k);
+          }
+          if (!ok) break;
+          ptx::tc_commit_elect(bar_empty + 8 * slot_v);
+          if (j + 1 < n_kv) {
+            // (Where no Q tile sees the next keys, nobody waited for them.)
+            if (!k_ready) ok = wait(bar_full + 8 * slot_k, it_k / L::kSlots, 2);
+            if (!ok) break;
+            ptx::tc_commit_elect(bar_empty + 8 * slot_k);
+          }
+        }
+        it = it0 + 2 * n_kv;
+      }
+      if (!ok && issued) {  // the MMAs issued end before TMEM is released
+        ptx::tc_commit_elect(bar_drain);
+        drain_wait(bar_drain, 0, p);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------ softmax, correction, epilogue
+    ptx::setmaxnreg_inc<kRegsSoftmax>();
+    const int t = warp / 4 - 1;
+    const int r = threadIdx.x % kTM;  // row within the tile
+    const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + t * kTN;
+    const uint32_t t_o = tmem + lane_off + kOCol + t * D;
+    // Factor of the scores, held off 0 so that -inf stays -inf (scores times
+    // 1e-37 vanish next to any maximum).
+    const float c = fmaxf(p.scale_log2, 1e-37f);
+    int s_uses = 0, o_uses = 0;
+    // This thread's row of unit `rec`: the sequence (-1: none) and its row of
+    // the K/V head there.
+    auto row_of = [&](volatile Record* rec, int* row) -> int {
+      int x = rec->row0 + t * kTM + r;
+      int b = rec->b;
+      if (b >= 0) {
+        *row = x;
+        return x < rec->n_new * p.group ? b : -1;
+      }
+      b = x / p.rows;
+      x -= b * p.rows;
+      *row = x;
+      if (b >= p.B) return -1;
+      return x < kv8::seq_new(p, b) * p.group ? b : -1;
+    };
+    // This thread's Q row of unit `rec` to shared memory, with the sign of the
+    // scale.  The buffer is free: every S of the tile has been read.
+    auto stage_q = [&](volatile Record* rec) {
+      int row;
+      const int b = row_of(rec, &row);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (b >= 0 ? q_row_index(p, b, rec->h, row) * D : 0));
+      const uint32_t sign = p.negate ? 0x80008000u : 0u;
+      const uint32_t dst = s_base + L::kQ + t * L::kTile + r * 128;
+      const uint32_t sw = r % 8;
+      uint4 y[D / 8];
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k)
+        y[k] = b >= 0 ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k)
+        ptx::st_shared_v4(dst + (k / 8) * L::kBox + (((k % 8) ^ sw) << 4),
+                          y[k].x ^ sign, y[k].y ^ sign, y[k].z ^ sign,
+                          y[k].w ^ sign);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_q + 8 * t);
+    };
+    volatile Record* rec = get_unit(0);
+    if (rec != nullptr && rec->n[t] > 0) stage_q(rec);
+    for (int k = 0; rec != nullptr; ++k) {
+      const int n = rec->n[t], j0 = rec->j0, np = rec->np;
+      const int plen = rec->plen, len = rec->len;
+      const int full = rec->full[t];
+      int vis = len;  // own keys that this row sees
+      if (rec->b >= 0) {
+        const int row = rec->row0 + t * kTM + r, n_new = rec->n_new;
+        if (row < n_new * p.group) vis = kv8::row_end(p, len, n_new, row);
+      }
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n; ++j) {
+        bool own;
+        int lim = tile_keys(j0 + j, np, plen, len, &own);
+        if (own && j0 + j - np >= full)
+          lim = min(lim, vis - (j0 + j - np) * kTN);
+        const bool masked = __any_sync(0xffffffffu, lim < kTN);
+        ok = wait(bar_s + 8 * t, s_uses, 4);
+        if (!ok) break;
+        ++s_uses;
+        ptx::tc_fence_after();
+        uint32_t sr[kTN];
+#pragma unroll
+        for (int q = 0; q < kTN / 32; ++q)
+          ptx::tmem_ld32(t_s + 32 * q, sr + 32 * q);
+        ptx::tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < kTN; ++q)
+            if (q >= lim) sr[q] = __float_as_uint(-INFINITY);
+        }
+        float mx4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mx4[q] = ptx::fmax3(__uint_as_float(sr[q]),
+                              __uint_as_float(sr[q + 4]),
+                              __uint_as_float(sr[q + 8]));
+#pragma unroll
+        for (int q = 12; q < kTN; q += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx4[e] = q + 4 + e < kTN
+                         ? ptx::fmax3(mx4[e], __uint_as_float(sr[q + e]),
+                                      __uint_as_float(sr[q + 4 + e]))
+                         : fmaxf(mx4[e], __uint_as_float(sr[q + e]));
+        }
+        const float mx =
+            fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+        float m_new = m_run;
+        if (__any_sync(0xffffffffu, mx > m_run + kTau))
+          m_new = fmaxf(m_run, mx);
+        const float alpha =
+            (m_new == -INFINITY) ? 1.f : ptx::ex2(m_run - m_new);
+        const float neg_m = (m_new == -INFINITY) ? 0.f : kShift - m_new;
+        float sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < kTN / 32; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int i = 32 * q + 2 * e;
+            float x0, x1;
+            ptx::ffma2(x0, x1, __uint_as_float(sr[i]),
+                       __uint_as_float(sr[i + 1]), c, neg_m);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+            if (e & 1)
+              ptx::fadd2(sm[2], sm[3], p0, p1);
+            else
+              ptx::fadd2(sm[0], sm[1], p0, p1);
+            pk[e] = ptx::pack2<kBF16>(p0, p1);
+          }
+          ptx::tmem_st16(t_s + 16 * q, pk);
+        }
+        if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
+          // O *= alpha (the PV before was issued before this S, whose commit
+          // has been awaited).
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            ptx::tmem_ld32(t_o + 32 * q, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            ptx::tmem_st32(t_o + 32 * q, o);
+          }
+        }
+        l_run *= alpha;
+        ptx::tmem_wait_st();
+        l_run += (sm[0] + sm[1]) + (sm[2] + sm[3]);
+        m_run = m_new;
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar_p + 8 * t);
+      }
+      if (!ok) break;
+      // The next unit's Q while this one's last products run.
+      volatile Record* next = get_unit(k + 1);
+      if (!ok) break;
+      if (next != nullptr && next->n[t] > 0) stage_q(next);
+      if (n > 0) {
+        ok = wait(bar_o + 8 * t, o_uses, 4);
+        if (!ok) break;
+        ++o_uses;
+        ptx::tc_fence_after();
+      }
+      const int dest = rec->dest, h = rec->h;
+      int row;
+      const int b = row_of(rec, &row);
+      const bool row_ok = b >= 0;
+      // O leaves as the average that it is.  A row that sees nothing: 0,
+      // whatever its accumulator holds.
+      const bool seen = l_run != 0.f;
+      const float inv = seen ? 1.f / l_run : 0.f;
+      const float lse2 =
+          seen ? (m_run == -INFINITY ? kNone : m_run) + log2f(l_run) - kShift
+               : -INFINITY;
+      if (dest == kFinal) {
+        const long long at = row_ok ? q_row_index(p, b, h, row) : 0;
+        uint4* dst = reinterpret_cast<uint4*>(p.o + at * D);
+        // (O is 16-byte aligned, its rows whole 32-byte sectors from there.)
+        const bool wide = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (n > 0) {
+            ptx::tmem_ld32(t_o + 32 * q, o);
+            ptx::tmem_wait_ld();
+          }
+          if (row_ok) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              uint32_t x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                x[e] = !seen ? 0u
+                             : ptx::pack2<kBF16>(
+                                   __uint_as_float(o[16 * v + 2 * e]) * inv,
+                                   __uint_as_float(o[16 * v + 2 * e + 1]) *
+                                       inv);
+              store_row(dst + 4 * q + 2 * v, x, wide);
+            }
+          }
+        }
+        if (row_ok && p.lse != nullptr) p.lse[at] = lse2 * 0.69314718055994531f;
+      } else {
+        // Rows of a unit over the prefix lie packed, a sequence's own behind.
+        long long at;
+        float *dst_o = p.slot_o, *dst_lse2 = p.slot_lse2;
+        if (dest == kBase) {
+          dst_o = p.base_o;
+          dst_lse2 = p.base_lse2;
+          const long long all = static_cast<long long>(p.B) * p.rows;
+          at = rec->b < 0 ? h * all + rec->row0 + t * kTM + r
+                          : p.Hkv * all +
+                                (static_cast<long long>(b) * p.Hkv + h) *
+                                    p.rows + row;
+        } else {
+          at = static_cast<long long>(dest) * kUnitRows + t * kTM + r;
+        }
+        if (n > 0) {
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            ptx::tmem_ld32(t_o + 32 * q, o);
+            ptx::tmem_wait_ld();
+            if (row_ok && seen) {
+              float4* dst = reinterpret_cast<float4*>(dst_o) + at * (D / 4);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  o[8 * v + e] =
+                      __float_as_uint(__uint_as_float(o[8 * v + e]) * inv);
+                store32(dst + 8 * q + 2 * v, o + 8 * v);
+              }
+            }
+          }
+        }
+        if (row_ok) dst_lse2[at] = lse2;
+      }
+      ptx::tc_fence_before();
+      release_unit(k);
+      rec = next;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool kBF16>
+cudaError_t launch(PrefixParams p, const CUtensorMap* maps,
+                   cudaStream_t stream) {
+  p.grid = p.many_grid;
+  constexpr int kBytes = Smem<D>::kBytes + 1024;
+  const cudaError_t err = cudaFuncSetAttribute(
+      prefix_many_kernel<D, kBF16>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (err != cudaSuccess) return err;
+  Maps m;
+  for (int i = 0; i < 8; ++i) m.m[i] = maps[i];
+  return kv8::launch_pdl(prefix_many_kernel<D, kBF16>, p.many_grid, kThreads,
+                         kBytes, stream, m, p);
+}
+
+}  // namespace
+
+cudaError_t launch_many(int D, bool bf16, const PrefixParams& p,
+                        const CUtensorMap* maps, cudaStream_t stream) {
+  if (D == 64)
+    return bf16 ? launch<64, true>(p, maps, stream)
+                : launch<64, false>(p, maps, stream);
+  return bf16 ? launch<128, true>(p, maps, stream)
+              : launch<128, false>(p, maps, stream);
+}
+
+}  // namespace prefix
+}  // namespace attn

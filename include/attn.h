@@ -556,6 +556,77 @@ attn_status_t attn_qk_rope_bwd(
  * device). */
 size_t attn_qk_rope_bwd_workspace_bytes(int D);
 
+/*
+ * attn_prefix_cache_t — 16-bit keys and values of a batch whose sequences
+ * share a prefix (a system prompt, a document, one prompt of many samples):
+ * the prefix's are held once, each sequence's own behind it in a cache of its
+ * own.  The pages' listings read one K and V per batch entry; here the B
+ * sequences' query rows meet the prefix's keys together, so that these are
+ * read once.
+ *
+ * prefix_k, prefix_v  device, [Hkv, prefix_capacity, D], 16-byte aligned;
+ * prefix_len  device int32 [1]: tokens of the prefix, 0 <= *prefix_len <=
+ *             prefix_capacity;
+ * k, v        device, [B, Hkv, capacity, D], 16-byte aligned;
+ * lens        device int32 [B]: a sequence's own tokens in k and v, the new
+ *             ones of the current step included, 0 <= lens[b] <= capacity.
+ * Lengths outside their range are taken as the nearer end of it and reported
+ * by attn_device_status (bit 1 of the code).  What lies behind a length is not
+ * used: it needs no initialisation.
+ * B >= 0, Hkv > 0, B * Hkv < 2^24, capacities from 1 to below 2^31 - 2^16 - 1,
+ * D in {64, 128}.
+ */
+typedef struct {
+  const void* prefix_k;
+  const void* prefix_v;
+  const int* prefix_len;
+  const void* k;
+  const void* v;
+  const int* lens;
+  int B, Hkv, prefix_capacity, capacity, D;
+} attn_prefix_cache_t;
+
+/*
+ * attn_prefix_fwd — attention of Sq query rows per sequence over the prefix
+ * and the sequence's own tokens behind it, one softmax over both, in the
+ * scores, softmax and sums of attn_fwd (fp32; the weights are rounded to the
+ * inputs' type for their product with V).
+ *
+ * Q         device, [B, Hq, Sq, D] contiguous, dtype (read);
+ * O         device, [B, Hq, Sq, D] contiguous, dtype (written);
+ * LSE       device fp32 [B, Hq, Sq] or NULL (written);
+ * new_lens  device int32 [B] or NULL (n_b = Sq): rows i < n_b are computed,
+ *           0 <= n_b <= Sq; O and LSE of rows i >= n_b are left as they are
+ *           and their Q is ignored;
+ * causal    non-zero: row i of sequence b is its own token lens[b] - n_b + i
+ *           and sees the prefix and its own tokens up to it (the new tokens
+ *           are its last n_b); 0: every row sees all lens[b] of them.
+ *           A row that sees no token gets O = 0 and LSE = -inf.
+ * Hq        a multiple of the cache's Hkv; scale finite, any sign;
+ * dtype     ATTN_F16 or ATTN_BF16, of Q, O and the cache;
+ *           NaN: a row of Q with NaN gets NaN and leaves the others alone; a
+ *           NaN of K reaches the rows that see its token; a NaN or infinity of
+ *           V may reach every row of the sequences that hold its token, also
+ *           rows before it (0 * NaN, as in attn_fwd).
+ * workspace device, 256-byte aligned, at least
+ *           attn_prefix_workspace_bytes(...) bytes; contents need no
+ *           initialisation.  It must not be used by another call until this
+ *           one has run.
+ * Two or three kernels on `stream`.  O, LSE and workspace must not overlap each
+ * other or any input.  B == 0 or Sq == 0 is a successful no-op.  Deterministic
+ * for a given device, shape and lengths.
+ */
+attn_status_t attn_prefix_fwd(const attn_prefix_cache_t* cache, const void* Q,
+                              void* O, float* LSE, int Hq, int Sq,
+                              const int* new_lens, float scale, int causal,
+                              attn_dtype_t dtype, void* workspace,
+                              size_t workspace_bytes, attn_stream_t stream);
+
+/* Workspace bytes attn_prefix_fwd needs (0 on bad sizes).  Host only; the
+ * value is for the current device's SM count (152 without a device). */
+size_t attn_prefix_workspace_bytes(int B, int Hq, int Hkv, int Sq,
+                                   int prefix_capacity, int capacity, int D);
+
 /* Short English description of a status code (static storage). */
 const char* attn_status_string(attn_status_t status);
 
