@@ -23,13 +23,13 @@ SOURCES = ["attn_api.cu", "attn_fwd_d64.cu", "attn_fwd_d128.cu",
            "kv8_api.cu", "kv8_append.cu", "kv8_decode.cu",
            "kv8_prefill.cu", "kv8_weights.cu", "kv8_evict.cu",
            "rope_api.cu", "rope.cu",
-           "prefix_api.cu", "prefix_many.cu", "prefix_few.cu",
-           "prefix_merge.cu"]
+           "prefix_api.cu", "prefix_many.cu", "prefix_merge.cu"]
 HEADERS = ["attn_fwd_kernel.cuh", "attn_fwd_launch.cuh", "attn_sync.cuh",
            "fast_div.h",
            "attn_bwd_kernel.cuh", "attn_merge_kernel.cuh",
            "sm103_ptx.cuh", "attn_launch.h", "attn_host.h", "kv8_common.cuh",
-           "kv8_index.h", "rope_common.cuh", "prefix_common.cuh"]
+           "kv8_index.h", "rope_common.cuh", "prefix_common.cuh",
+           "prefix_few.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

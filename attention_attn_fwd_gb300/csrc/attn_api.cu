@@ -240,6 +240,29 @@ bool make_tile_map(CUtensorMap* m, const void* base, bool bf16, int D,
                   box_rows);
 }
 
+bool make_rows_map(CUtensorMap* m, const void* base, bool bf16, int D, int S,
+                   int H, int B, int box_h, int box_s, int box_b) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t dims[4] = {
+      static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+      static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {S * row, row, H * (S * row)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_h),
+                             static_cast<cuuint32_t>(box_s),
+                             static_cast<cuuint32_t>(box_b)};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  const CUresult r =
+      enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+          4, const_cast<void*>(base), dims, strides, box, estride,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool current_context_id(unsigned long long* id) {
   std::call_once(g_ctx_once, [] {
     void* fn = nullptr;

@@ -27,4 +27,10 @@ bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb);
 bool make_tile_map(CUtensorMap* m, const void* base, bool bf16, int D,
                    int rows, long long planes, int box_rows);
 
+// Map of a [B, H, S, D] tensor of 16-bit elements for copies whose rows lie in
+// the order (sequence, token, head): of box_b, box_s and box_h of these, by one
+// 128-byte segment, 128-byte swizzled.
+bool make_rows_map(CUtensorMap* m, const void* base, bool bf16, int D, int S,
+                   int H, int B, int box_h, int box_s, int box_b);
+
 }  // namespace attn

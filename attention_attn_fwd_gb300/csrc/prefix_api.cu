@@ -44,6 +44,7 @@ attn_status_t check_sizes(const Sizes& z) {
       z.prefix_capacity < 1 || z.capacity < 1 || z.D <= 0)
     return ATTN_ERR_INVALID_ARG;
   if (z.D != 64 && z.D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (z.Hq / z.Hkv > attn::prefix::kTM) return ATTN_ERR_UNSUPPORTED;
   // Counts of tokens, tiles and rows stay within int32 with a tile behind.
   constexpr long long kMost = 0x7fffffffLL - (1 << 16);
   if (z.prefix_capacity >= kMost || z.capacity >= kMost ||
@@ -52,40 +53,38 @@ attn_status_t check_sizes(const Sizes& z) {
   return ATTN_OK;
 }
 
-// How the rows of a K/V head meet the keys; see Mode.
+// How the rows of a K/V head meet the keys; see Mode.  Rows of a sequence that
+// fill a tile are not packed with others': packed, their results over the
+// prefix and over their own keys have to meet in memory.
 struct Plan {
   int mode;
   long long rows;        // R
+  int tile_seqs, tile_rows;
   long long pack_blocks, row_blocks;
-  int many_grid, few_grid;
+  int grid;
 };
 
-// Rows of a sequence that fill 256-row units well are not packed with others:
-// packed, their results over the prefix and over their own keys have to meet
-// in memory.
-bool fills_units(long long rows) {
-  const long long blocks = (rows + attn::prefix::kUnitRows - 1) /
-                           attn::prefix::kUnitRows;
-  return 4 * rows >= 3 * blocks * attn::prefix::kUnitRows;
-}
+long long units_of(long long tiles) { return (tiles + 1) / 2; }
 
 Plan make_plan(const Sizes& z, int sms) {
+  constexpr int kTM = attn::prefix::kTM;
   Plan p;
-  p.rows = static_cast<long long>(z.Hq / z.Hkv) * z.Sq;
-  p.mode = p.rows <= 16 ? attn::prefix::kFew
-           : fills_units(p.rows) || z.B == 1 ? attn::prefix::kJoint
-                                             : attn::prefix::kPacked;
-  const long long unit = attn::prefix::kUnitRows;
-  p.pack_blocks =
-      p.mode == attn::prefix::kJoint ? 0 : (z.B * p.rows + unit - 1) / unit;
-  p.row_blocks =
-      p.mode == attn::prefix::kFew ? 0 : (p.rows + unit - 1) / unit;
-  p.many_grid = sms;
-  p.few_grid =
-      p.mode == attn::prefix::kFew
-          ? sms * attn::prefix::few_ctas(
-                      z.D, attn::prefix::few_rows(static_cast<int>(p.rows)))
-          : 0;
+  const int group = z.Hq / z.Hkv;
+  p.rows = static_cast<long long>(group) * z.Sq;
+  p.mode = p.rows <= 16                ? attn::prefix::kFew
+           : p.rows > kTM || z.B == 1 ? attn::prefix::kJoint
+                                      : attn::prefix::kPacked;
+  p.tile_seqs =
+      p.mode == attn::prefix::kJoint ? 1 : static_cast<int>(kTM / p.rows);
+  p.tile_rows = kTM / group * group;
+  if (p.tile_rows > p.rows) p.tile_rows = static_cast<int>(p.rows);
+  p.pack_blocks = p.mode == attn::prefix::kJoint
+                      ? 0
+                      : units_of((z.B + p.tile_seqs - 1) / p.tile_seqs);
+  p.row_blocks = p.mode == attn::prefix::kFew
+                     ? 0
+                     : units_of((p.rows + p.tile_rows - 1) / p.tile_rows);
+  p.grid = sms > 2 ? sms : 2;  // (one for the prefix, one for own keys)
   return p;
 }
 
@@ -103,7 +102,7 @@ bool counts_fit(const Sizes& z, const Plan& p) {
 }
 
 struct Workspace {
-  size_t base_o, base_lse2, slot_o, slot_lse2, info, split, few_o, few_lse2;
+  size_t base_o, base_lse2, slot_o, slot_lse2, info, split, few_o, few_lse2, own_info;
   size_t total;
 };
 
@@ -112,13 +111,14 @@ Workspace workspace_layout(const Sizes& z, const Plan& p) {
   const size_t row = static_cast<size_t>(z.D) * 4;
   const size_t all = static_cast<size_t>(z.B) * z.Hkv * p.rows;
   const size_t base = joint ? 0 : p.mode == attn::prefix::kFew ? all : 2 * all;
-  const size_t slots = static_cast<size_t>(p.many_grid) * (joint ? 2 : 1) *
+  const size_t slots = static_cast<size_t>(p.grid) * (joint ? 2 : 1) *
                        attn::prefix::kUnitRows;
   const size_t units =
       joint ? 0 : static_cast<size_t>(p.pack_blocks + z.B * p.row_blocks) * z.Hkv;
   const size_t few =
       p.mode == attn::prefix::kFew
-          ? (p.few_grid + static_cast<size_t>(z.B) * z.Hkv) *
+          ? (static_cast<size_t>(p.grid) * attn::prefix::kFewWarps +
+             static_cast<size_t>(z.B) * z.Hkv) *
                 attn::prefix::few_rows(static_cast<int>(p.rows))
           : 0;
   Workspace w;
@@ -128,9 +128,11 @@ Workspace workspace_layout(const Sizes& z, const Plan& p) {
   w.slot_lse2 = w.slot_o + round_up(slots * row);
   w.info = w.slot_lse2 + round_up(slots * 4);
   w.split = w.info + round_up(units * 8);
-  w.few_o = w.split + (joint ? round_up(p.many_grid * size_t(16)) : 0);
+  w.few_o = w.split + (joint ? round_up(p.grid * size_t(16)) : 0);
   w.few_lse2 = w.few_o + round_up(few * row);
-  w.total = w.few_lse2 + round_up(few * 4);
+  w.own_info = w.few_lse2 + round_up(few * 4);
+  w.total = w.own_info +
+            (few ? round_up(static_cast<size_t>(z.B) * z.Hkv * 8) : 0);
   return w;
 }
 
@@ -212,6 +214,8 @@ attn_status_t fwd_impl(const attn_prefix_cache_t* c, const void* Q, void* O,
   p.causal = causal != 0;
   p.pack_blocks = static_cast<int>(plan.pack_blocks);
   p.row_blocks = static_cast<int>(plan.row_blocks);
+  p.tile_seqs = plan.tile_seqs;
+  p.tile_rows = plan.tile_rows;
   p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
   p.negate = scale < 0.f;
   char* ws = static_cast<char*>(workspace);
@@ -223,15 +227,24 @@ attn_status_t fwd_impl(const attn_prefix_cache_t* c, const void* Q, void* O,
   p.split = reinterpret_cast<int4*>(ws + w.split);
   p.few_o = reinterpret_cast<float*>(ws + w.few_o);
   p.few_lse2 = reinterpret_cast<float*>(ws + w.few_lse2);
-  p.many_grid = plan.many_grid;
-  p.few_grid = plan.few_grid;
+  p.own_info = reinterpret_cast<int2*>(ws + w.own_info);
+  p.grid = plan.grid;
+  p.fd_group = attn::make_fast_div(p.group);
+  p.fd_rows = attn::make_fast_div(p.rows);
+  p.fd_blocks = attn::make_fast_div(p.row_blocks > 0 ? p.row_blocks : 1);
+  p.fd_tile_seqs = attn::make_fast_div(p.tile_seqs);
+  p.fd_tile_rows = attn::make_fast_div(p.tile_rows);
   p.timeout_ns = attn::wait_timeout_ns();
   p.status = attn::device_status_word(dev);
   if (p.status == nullptr) return ATTN_ERR_CUDA;
   const bool bf16 = dtype == ATTN_BF16;
   // (The many-row kernel reads a sequence's own keys only where it works on
   // them.)
-  CUtensorMap maps[8];
+  CUtensorMap maps[9];
+  const bool joint = plan.mode == attn::prefix::kJoint;
+  if (!attn::make_rows_map(&maps[8], Q, bf16, z.D, Sq, Hq, z.B, p.group,
+                           joint ? p.tile_rows / p.group : Sq, p.tile_seqs))
+    return ATTN_ERR_CUDA;
   const void* bases[] = {c->prefix_k, c->prefix_v, c->k, c->v};
   for (int i = 0; i < 4; ++i) {
     const bool is_own = i >= 2;
@@ -248,8 +261,6 @@ attn_status_t fwd_impl(const attn_prefix_cache_t* c, const void* Q, void* O,
     }
   }
   cudaError_t err = attn::prefix::launch_many(z.D, bf16, p, maps, stream);
-  if (err == cudaSuccess && plan.mode == attn::prefix::kFew)
-    err = attn::prefix::launch_few(z.D, bf16, p, stream);
   if (err == cudaSuccess)
     err = attn::prefix::launch_merge(z.D, bf16, p, stream);
   return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

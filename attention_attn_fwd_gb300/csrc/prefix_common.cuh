@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include "fast_div.h"
 #include "kv8_common.cuh"
 
 namespace attn {
@@ -13,16 +14,17 @@ namespace prefix {
 
 constexpr int kTM = 128;             // rows of a Q tile
 constexpr int kTN = 128;             // keys of a tile
-constexpr int kUnitRows = 2 * kTM;   // rows of a unit
+constexpr int kUnitRows = 2 * kTM;   // rows of a unit's two tiles
 constexpr int kTailRows = 16;        // rows of a copy of a last tile
-constexpr int kFewWarps = 4;
+constexpr int kFewWarps = 8;         // of a block that works on few rows
 
 // How the query rows meet the keys (R rows of a K/V head per sequence, row r =
 // token r / group, head r % group):
-//   kFew    R <= 16: units of 256 rows of all sequences over the prefix, the
-//           sequences' own keys by the few-row kernel;
-//   kPacked such units over the prefix, and units of each sequence over its
-//           own keys;
+//   kFew    R <= 16: units of two Q tiles, each the rows of as many sequences as
+//           it holds, over the prefix; the sequences' own keys by thread blocks
+//           set aside for them (prefix_few.cuh);
+//   kPacked R <= 128: such units over the prefix, and units of each sequence
+//           over its own keys;
 //   kJoint  units of each sequence over the prefix and its own keys in turn.
 enum Mode { kFew = 0, kPacked = 1, kJoint = 2 };
 
@@ -40,6 +42,8 @@ struct PrefixParams {
   int mode, causal;
   int pack_blocks;        // units of a head over the prefix (0: kJoint)
   int row_blocks;         // units of a (sequence, head) (0: kFew)
+  int tile_seqs;          // sequences of a Q tile over the prefix
+  int tile_rows;          // rows of a sequence's Q tile: whole tokens
   float scale_log2;       // |scale| * log2(e)
   int negate;             // scale < 0
   // Parts of a row, each the average that it is, and their LSEs in log2 units
@@ -52,11 +56,12 @@ struct PrefixParams {
   float* slot_lse2;
   int2* info;             // [units]: first CTA and number of parts
   int4* split;            // kJoint [grid]: b, h, block, parts (0: none)
-  // Own keys of few rows: slot CTA + segment.
+  // Own keys of few rows: slot warp + segment.
   float* few_o;           // [slots, 8 or 16, D]
   float* few_lse2;
-  int grid;               // CTAs that the list at hand is cut for
-  int many_grid, few_grid;
+  int2* own_info;         // [B, Hkv]: first warp and number of parts
+  int grid;               // CTAs of the launch
+  FastDiv fd_group, fd_rows, fd_blocks, fd_tile_seqs, fd_tile_rows;
   unsigned long long timeout_ns;
   unsigned int* status;
 };
@@ -70,36 +75,38 @@ __device__ __forceinline__ int prefix_tiles(const PrefixParams& p) {
 // Query row r of K/V head h of sequence b, in Q, O and LSE.
 __device__ __forceinline__ long long q_row_index(const PrefixParams& p, int b,
                                                  int h, int r) {
-  const int tok = r / p.group, hd = r - tok * p.group;
+  const int tok = fast_div(r, p.fd_group), hd = r - tok * p.group;
   return (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
 }
 
-// The few-row kernel's tiles: 4 KB of keys; and empty places before a segment.
+// The few-row work's tiles: 4 KB of keys; and empty places before a segment.
 template <int D>
 __host__ __device__ constexpr int few_keys() {
   return 2048 / D;
 }
-constexpr int kFewOver = 6;
+constexpr int kFewOver = 2;
+
+// Own tokens that row r of a sequence sees.
+__device__ __forceinline__ int row_end(const PrefixParams& p, int len,
+                                       int n_new, int r) {
+  if (!p.causal) return len;
+  return min(len, max(0, len - n_new + fast_div(r, p.fd_group) + 1));
+}
 
 // Own key tiles that rows [r0, r1) of a sequence with n_new tokens see.
 __device__ __forceinline__ int tiles_seen(const PrefixParams& p, int len,
                                           int n_new, int r0, int r1) {
   const int last = min(r1, n_new * p.group) - 1;
   if (last < r0) return 0;
-  return (kv8::row_end(p, len, n_new, last) + kTN - 1) / kTN;
+  return (row_end(p, len, n_new, last) + kTN - 1) / kTN;
 }
 
 cudaError_t launch_many(int D, bool bf16, const PrefixParams& p,
                         const CUtensorMap* maps, cudaStream_t stream);
-cudaError_t launch_few(int D, bool bf16, const PrefixParams& p,
-                       cudaStream_t stream);
 cudaError_t launch_merge(int D, bool bf16, const PrefixParams& p,
                          cudaStream_t stream);
 
-// CTAs of the few-row kernel that an SM holds, and rows it works on.
-__host__ __device__ constexpr int few_ctas(int D, int rows) {
-  return 2;
-}
+// Rows that the few-row work is compiled for.
 __host__ __device__ constexpr int few_rows(int rows) {
   return rows <= 8 ? 8 : 16;
 }

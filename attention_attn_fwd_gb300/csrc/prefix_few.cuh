@@ -1,37 +1,29 @@
 // Attention of up to 16 query rows per K/V head over each sequence's own keys,
-// behind a shared prefix.
+// behind a shared prefix: the work of the thread blocks that the many-row
+// kernel sets aside for it.
 //
-// Mathematics: flash-decoding, as the few-row kernel of the 8-bit cache does
-// it.  The keys of all (sequence, K/V head) segments form one list of tiles (4
-// KB of keys), cut into equal consecutive shares, one per CTA; a CTA's warps
-// take its tiles in turn, each with its own running maximum, sum and
-// accumulator, which meet in shared memory at the end of a segment.  A result
-// goes to workspace slot (CTA + segment) and is joined with the others and the
-// prefix's by the merge kernel.
+// Mathematics: flash-decoding.  The keys of all (sequence, K/V head) segments
+// form one list of tiles (4 KB of keys), cut into equal consecutive shares, one
+// per warp.  A warp has its own running maximum, sum and accumulator; a part of
+// a segment goes to workspace slot (warp + segment) -- both only grow along the
+// list, so no two share one -- and is joined with the others and the prefix's
+// by the merge kernel.
 //
 // Products: S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16, 16 keys (or
 // 16 of D) by 8 query rows: a 128-row tcgen05 tile would be nearly empty, and
-// the bytes of K and V bound the kernel.  P is rounded to the inputs' type and
+// the bytes of K and V bound this work.  P is rounded to the inputs' type and
 // held times 2^kShift as in the many-row kernel.
 //
 // Tiles reach shared memory by 16-byte asynchronous copies, a ring per warp
 // that runs ahead across segments; rows past a length are filled with zeros
 // and read nothing.  Chunk j of row r lies at chunk j ^ r % 8, so that
 // ldmatrix reads share no banks.
-//
-// The kernel reads what was there before the prefix's kernel ahead of it, not
-// that one's results: it starts while that one drains, and waits for it only
-// at its end (so that the merge behind has waited for both).
+#pragma once
+
 #include "prefix_common.cuh"
 
 namespace attn {
 namespace prefix {
-namespace {
-
-using kv8::kNone;
-using kv8::Segment;
-
-constexpr float kTau = 8.f;  // lazy rescale threshold (log2 units)
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
@@ -91,19 +83,89 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0,
   }
 }
 
-template <int D, int NT>
-struct Config {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kThreads = 32 * kFewWarps;
-  static constexpr int kCtas = few_ctas(D, kRows);
-  static constexpr int kStages = NT == 1 ? 3 : 2;
-  static constexpr int kTile = 4096;     // bytes of K, and of V
-  static constexpr int kPitch = D + 4;   // floats: rows start 4 banks apart
-  static constexpr int kRingBytes = kFewWarps * kStages * 2 * kTile;
-  static constexpr int kBytes =
-      kRingBytes + kFewWarps * kRows * (kPitch + 2) * 4;
-  static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory");
+constexpr int kFewStages = 3;
+constexpr int kFewTile = 4096;  // bytes of keys in a tile, and of values
+constexpr int kFewRing = kFewStages * 2 * kFewTile;  // bytes of a warp's ring
+
+// Places of a segment in the list.
+template <int D>
+__device__ __forceinline__ int few_places(int tiles) {
+  return tiles > 0 ? tiles + kFewOver : 0;
+}
+// Tiles of a sequence (of each of its heads): none where no row wants them.
+template <int D>
+__device__ __forceinline__ int few_tiles(const PrefixParams& p, int b) {
+  const int len = kv8::seq_len(p, b);
+  return kv8::seq_new(p, b) > 0 ? (len + few_keys<D>() - 1) / few_keys<D>()
+                                : 0;
+}
+
+// Places of all segments, for every lane of the calling warp.
+template <int D>
+__device__ __forceinline__ int few_total(const PrefixParams& p, int lane) {
+  int t = 0;
+  for (int b = lane; b < p.B; b += 32) t += few_places<D>(few_tiles<D>(p, b));
+#pragma unroll
+  for (int s = 16; s > 0; s /= 2) t += __shfl_xor_sync(0xffffffffu, t, s);
+  return t * p.Hkv;
+}
+
+// A segment as a warp walks its share: its tiles lie at [pos, end) counted from
+// the share's start (pos < 0: it began earlier).
+struct FewSegment {
+  int pos, end;
+  int b, h, len, tiles;
 };
+
+template <int D>
+__device__ __forceinline__ void few_enter(const PrefixParams& p, int b,
+                                          FewSegment& s) {
+  s.b = b;
+  s.len = kv8::seq_len(p, b);
+  s.tiles = few_tiles<D>(p, b);
+}
+
+// The segment that holds place `first` of the list (there is one).
+template <int D>
+__device__ __forceinline__ void few_find(const PrefixParams& p, int first,
+                                         int lane, FewSegment& s) {
+  int base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int t =
+        b < p.B ? few_places<D>(few_tiles<D>(p, b)) * p.Hkv : 0;
+    int incl = t;
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, i);
+      if (lane >= i) incl += up;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > first);
+    if (hit != 0u) {
+      const int l = __ffs(hit) - 1;
+      const int off = first - base - __shfl_sync(0xffffffffu, incl - t, l);
+      few_enter<D>(p, b0 + l, s);
+      s.h = off / few_places<D>(s.tiles);
+      s.pos = kFewOver - (off - s.h * few_places<D>(s.tiles));
+      s.end = s.pos + s.tiles;
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void few_next(const PrefixParams& p,
+                                         FewSegment& s) {
+  s.pos = s.end + kFewOver;
+  if (++s.h == p.Hkv) {
+    s.h = 0;
+    do {  // some later sequence has tiles: the share is not at its end
+      few_enter<D>(p, s.b + 1, s);
+    } while (s.tiles == 0);
+  }
+  s.end = s.pos + s.tiles;
+}
 
 // Byte offset of 16-byte chunk j of row r in a tile.
 template <int D>
@@ -112,18 +174,16 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int j) {
 }
 
 // A warp's loads: they run ahead of its products, across segments.
-template <int D, int NT>
-struct Loader {
-  using C = Config<D, NT>;
+template <int D>
+struct FewLoader {
   static constexpr int kKeys = few_keys<D>();
   static constexpr int kPerRow = D / 8;          // chunks
   static constexpr int kRowStep = 32 / kPerRow;  // rows between a lane's chunks
-  static constexpr int kChunks = C::kTile / 16 / 32;
-  Segment seg;
+  static constexpr int kChunks = kFewTile / 16 / 32;
+  FewSegment seg;
   int pos;                 // next tile, counted from the share's start
   const uint16_t* k;       // this lane's first chunk of the segment
   const uint16_t* v;
-  uint32_t ring;
 
   __device__ __forceinline__ void set_segment(const PrefixParams& p,
                                               int lane) {
@@ -133,84 +193,74 @@ struct Loader {
     k = p.k + at;
     v = p.v + at;
   }
-  __device__ __forceinline__ void init(const PrefixParams& p,
-                                       const Segment& s, int warp, int lane,
-                                       uint32_t ring_) {
-    seg = s;
-    pos = warp;
-    ring = ring_;
-    set_segment(p, lane);
-  }
   __device__ __forceinline__ void next(const PrefixParams& p, int count,
-                                       int stage, int lane) {
+                                       uint32_t to, int lane) {
     bool moved = false;
-    while (pos < count) {
-      if (pos >= seg.end) {
-        kv8::next_segment<kKeys, kFewOver>(p, seg);
-        moved = true;
-      } else if (pos < seg.pos) {
-        pos += kFewWarps;
-      } else {
-        break;
-      }
+    while (pos < count && pos >= seg.end) {
+      few_next<D>(p, seg);
+      pos = seg.pos;
+      moved = true;
     }
     if (pos < count) {
       if (moved) set_segment(p, lane);
       const int t = pos - seg.pos;
       const long long off = static_cast<long long>(t) * kKeys * D;
-      const uint32_t to = ring + stage * 2 * C::kTile;
       const int r0 = lane / kPerRow, j = lane % kPerRow;
-      const int left = seg.len - t * kKeys - r0;
+      const int left = seg.len - t * kKeys;
+      if (left >= kKeys) {
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int r = r0 + i * kRowStep;
-        const uint32_t dst = to + chunk_at<D>(r, j);
-        const bool in = i * kRowStep < left;
-        const long long at = in ? off + i * kRowStep * D : 0;
-        if (left >= kKeys) {
+        for (int i = 0; i < kChunks; ++i) {
+          const uint32_t dst = to + chunk_at<D>(r0 + i * kRowStep, j);
           cp_async16(dst, k + off + i * kRowStep * D);
-          cp_async16(dst + C::kTile, v + off + i * kRowStep * D);
-        } else {
+          cp_async16(dst + kFewTile, v + off + i * kRowStep * D);
+        }
+      } else {
+#pragma unroll 2
+        for (int i = 0; i < kChunks; ++i) {
+          const uint32_t dst = to + chunk_at<D>(r0 + i * kRowStep, j);
+          const bool in = r0 + i * kRowStep < left;
+          const long long at = in ? off + i * kRowStep * D : 0;
           cp_async16_or_zero(dst, k + at, in);
-          cp_async16_or_zero(dst + C::kTile, v + at, in);
+          cp_async16_or_zero(dst + kFewTile, v + at, in);
         }
       }
-      pos += kFewWarps;
+      ++pos;
     }
     cp_async_commit();
   }
 };
 
+// The share of warp `gw` of `warps` of a list of `total` places.  NT: 8-row
+// groups of query rows.
 template <int D, int NT, bool kBF16>
-__device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
-  using C = Config<D, NT>;
-  constexpr int kWarps = kFewWarps;
-  constexpr int kRows = C::kRows;
-  constexpr int kPitch = C::kPitch;
-  constexpr int kStages = C::kStages;
+__device__ __forceinline__ void few_share(const PrefixParams& p, int gw,
+                                          int warps, int total, int lane,
+                                          uint32_t ring) {
+  constexpr int kRows = 8 * NT;
   constexpr int kKeys = few_keys<D>();
   constexpr int kSub = kKeys / 16;  // 16-key steps per tile
   constexpr int kKSteps = D / 16;
   constexpr float kShift = kBF16 ? -24.f : 7.f;
-  extern __shared__ __align__(128) uint8_t smem[];
-  float* sm_o = reinterpret_cast<float*>(smem + C::kRingBytes);
-  float* sm_m = sm_o + kWarps * kRows * kPitch;  // [kWarps][kRows]
-  float* sm_l = sm_m + kWarps * kRows;
+  constexpr float kTau = 8.f;  // lazy rescale threshold (log2 units)
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (total == 0) return;
+  kv8::Cut cut;
+  cut.n = min(warps, total);
+  cut.q = total / cut.n;
+  cut.rest = total - cut.q * cut.n;
+  if (gw >= cut.n) return;
+  const int first = cut.first(gw), count = cut.first(gw + 1) - first;
+  FewSegment seg;
+  few_find<D>(p, first, lane, seg);
+  if (seg.pos >= count) return;  // empty places alone
   const int g8 = lane / 4, c = lane % 4;
-  const int cta = blockIdx.x;
-  Segment seg;
-  seg.pos = 0;
-  const int count =
-      kv8::take_share<kKeys, kFewOver, kWarps>(p, cta, lane, &seg);
-  if (seg.pos >= count) return;  // (also: no share)
-  const uint32_t ring =
-      ptx::smem_u32(smem) + warp * kStages * 2 * C::kTile;
-  Loader<D, NT> ld;
-  ld.init(p, seg, warp, lane, ring);
+  FewLoader<D> ld;
+  ld.seg = seg;
+  ld.pos = max(seg.pos, 0);
+  ld.set_segment(p, lane);
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) ld.next(p, count, i, lane);
+  for (int i = 0; i < kFewStages; ++i)
+    ld.next(p, count, ring + i * 2 * kFewTile, lane);
   // This lane's rows of ldmatrix's four 8 x 8 matrices: of K (keys 0-7 and
   // 8-15, then the next 8 of D) and of V (the next 8 of D, then keys 8-15).
   const int k_row = lane % 8 + 8 * ((lane / 8) & 1), k_col = lane / 16;
@@ -218,14 +268,15 @@ __device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
   const float mult = p.negate ? -p.scale_log2 : p.scale_log2;
 
   int stage = 0;
-  int pos = warp;  // this warp's next tile
   while (true) {
-    const int seg_last = min(seg.end, count);  // end of the CTA's part
     const int b = seg.b, h = seg.h, len = seg.len;
+    const int bh = b * p.Hkv + h;
     const int n_new = kv8::seq_new(p, b);
     const int n_rows = n_new * p.group;  // valid rows, kRows at most
-    const int min_end = n_rows > 0 ? kv8::row_end(p, len, n_new, 0) : 0;
-    const int max_end = n_rows > 0 ? len : 0;
+    const int min_end = row_end(p, len, n_new, 0);
+    if (seg.pos >= 0 && lane == 0)  // it begins here
+      p.own_info[bh] =
+          make_int2(gw, cut.owner(first + seg.end - 1) - gw + 1);
 
     // This lane's two query rows per 8-row group (columns of S^T): how many
     // tokens they see.
@@ -244,14 +295,14 @@ __device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rr = 8 * nt + 2 * c + e;
-        vis[nt][e] = rr < n_rows ? kv8::row_end(p, len, n_new, rr) : len;
+        vis[nt][e] = rr < n_rows ? row_end(p, len, n_new, rr) : len;
       }
     }
 
     float m[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = kNone;
+      m[nt][0] = m[nt][1] = kv8::kNone;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -259,15 +310,15 @@ __device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
 
-    while (pos < seg.pos) pos += kWarps;
-    for (; pos < seg_last; pos += kWarps) {
-      cp_async_wait<kStages - 1>();
+    const int last = min(seg.end, count);  // end of the warp's part
+    for (int pos = max(seg.pos, 0); pos < last; ++pos) {
+      cp_async_wait<kFewStages - 1>();
       __syncwarp();
-      const uint32_t tile = ring + stage * 2 * C::kTile;
+      const uint32_t tile = ring + stage * 2 * kFewTile;
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
         const int key0 = (pos - seg.pos) * kKeys + 16 * u;
-        if (key0 >= max_end) continue;  // no rows, or past the length
+        if (key0 >= len) continue;
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -282,7 +333,6 @@ __device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
             mma<kBF16>(s[nt], a, bq[nt][ks][0], bq[nt][ks][1]);
         }
         // Scores in log2 units; hidden ones are -inf.
-        bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -295,6 +345,7 @@ __device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
               if (key0 + g8 + 8 * (e >> 1) >= vis[nt][e & 1])
                 s[nt][e] = -INFINITY;
         }
+        bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -338,7 +389,7 @@ __device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t a[4];
-          ldmatrix4_trans(a, tile + C::kTile +
+          ldmatrix4_trans(a, tile + kFewTile +
                                  chunk_at<D>(16 * u + v_row, 2 * i + v_col));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -346,110 +397,40 @@ __device__ __forceinline__ void few_rows_share(const PrefixParams& p) {
         }
       }
       __syncwarp();  // the tile has been read
-      ld.next(p, count, stage, lane);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      ld.next(p, count, tile, lane);
+      stage = stage + 1 == kFewStages ? 0 : stage + 1;
     }
 
-    // The warps' results meet: maxima, then O and l under the common ones.
-    __syncthreads();  // the previous segment's sums have been read
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = l[nt][e];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        l[nt][e] = x;
-        if (g8 == 0) sm_m[warp * kRows + 8 * nt + 2 * c + e] = m[nt][e];
-      }
-    __syncthreads();
+    // The part's averages and LSEs to its slot.
+    const long long slot = static_cast<long long>(gw) + bh;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * nt + 2 * c + e;
-        float mx = kNone;
+        float sum = l[nt][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (r >= n_rows) continue;
+        const bool seen = sum != 0.f;
+        const float inv = seen ? 1.f / sum : 0.f;
+        float* dst = p.few_o + (slot * kRows + r) * D + g8;
+        if (seen) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w * kRows + r]);
-        const float f = ptx::ex2(m[nt][e] - mx);
-        if (g8 == 0) sm_l[warp * kRows + r] = l[nt][e] * f;
-        float* dst = sm_o + (warp * kRows + r) * kPitch + g8;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          dst[16 * i] = o[nt][i][e] * f;
-          dst[16 * i + 8] = o[nt][i][e + 2] * f;
+          for (int i = 0; i < D / 16; ++i) {
+            dst[16 * i] = o[nt][i][e] * inv;
+            dst[16 * i + 8] = o[nt][i][e + 2] * inv;
+          }
         }
+        if (g8 == 0)
+          p.few_lse2[slot * kRows + r] =
+              seen ? m[nt][e] + log2f(sum) - kShift : -INFINITY;
       }
-    __syncthreads();
-    const long long slot =
-        static_cast<long long>(cta) + static_cast<long long>(b) * p.Hkv + h;
-    for (int i = threadIdx.x; i < n_rows * (D / 4); i += C::kThreads) {
-      const int r = i / (D / 4), d4 = i % (D / 4);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f, mx = kNone;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(
-            sm_o + (w * kRows + r) * kPitch + 4 * d4);
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-        sum += sm_l[w * kRows + r];
-        mx = fmaxf(mx, sm_m[w * kRows + r]);
-      }
-      const bool seen = sum != 0.f;
-      const float inv = seen ? 1.f / sum : 0.f;
-      if (seen)
-        reinterpret_cast<float4*>(p.few_o)[(slot * kRows + r) * (D / 4) + d4] =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      if (d4 == 0)
-        p.few_lse2[slot * kRows + r] =
-            seen ? mx + log2f(sum) - kShift : -INFINITY;
-    }
     if (seg.end >= count) break;
-    kv8::next_segment<kKeys, kFewOver>(p, seg);
+    few_next<D>(p, seg);
     if (seg.pos >= count) break;
   }
-}
-
-template <int D, int NT, bool kBF16>
-__global__ void __launch_bounds__(Config<D, NT>::kThreads,
-                                  Config<D, NT>::kCtas)
-    prefix_few_kernel(const __grid_constant__ PrefixParams p) {
-  ptx::griddep_launch_dependents();
-  few_rows_share<D, NT, kBF16>(p);
-  ptx::griddep_wait();
-}
-
-template <int D, int NT, bool kBF16>
-cudaError_t launch(PrefixParams p, cudaStream_t stream) {
-  using C = Config<D, NT>;
-  p.grid = p.few_grid;
-  const cudaError_t err = cudaFuncSetAttribute(
-      prefix_few_kernel<D, NT, kBF16>,
-      cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-  if (err != cudaSuccess) return err;
-  return kv8::launch_pdl(prefix_few_kernel<D, NT, kBF16>, p.few_grid,
-                         C::kThreads, C::kBytes, stream, p);
-}
-
-template <int D, bool kBF16>
-cudaError_t launch_dt(const PrefixParams& p, cudaStream_t stream) {
-  return p.rows <= 8 ? launch<D, 1, kBF16>(p, stream)
-                     : launch<D, 2, kBF16>(p, stream);
-}
-
-}  // namespace
-
-cudaError_t launch_few(int D, bool bf16, const PrefixParams& p,
-                       cudaStream_t stream) {
-  if (D == 64)
-    return bf16 ? launch_dt<64, true>(p, stream)
-                : launch_dt<64, false>(p, stream);
-  return bf16 ? launch_dt<128, true>(p, stream)
-              : launch_dt<128, false>(p, stream);
 }
 
 }  // namespace prefix

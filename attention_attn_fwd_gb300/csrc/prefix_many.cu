@@ -2,13 +2,13 @@
 // own keys where a K/V head has more than 16 query rows.
 //
 // The prefix's keys are the same for every sequence, so its query rows are
-// packed across the batch: row x of a K/V head is row x % R of sequence x / R.
-// 256 of them (two 128-row Q tiles) make a unit, which streams the prefix's
-// 128-key tiles once: with B sequences the prefix is read once instead of B
+// packed across the batch: a 128-row Q tile holds the rows of as many
+// sequences as fit, and two of them make a unit, which streams the prefix's
+// 128-key tiles once.  With B sequences the prefix is read once instead of B
 // times, and a decoding step's few rows fill the tensor cores' tiles.  Units
-// of one sequence's rows take its own keys; where those rows fill a unit
-// themselves (kJoint) its list of tiles is the prefix's and then its own, and
-// one pass makes the result.
+// of one sequence's rows take its own keys; where those rows fill a tile
+// themselves (kJoint) its list of key tiles is the prefix's and then its own,
+// and one pass makes the result.
 //
 // S = Q K^T and O += P V run as tcgen05 MMAs with fp32 accumulators in TMEM, K
 // and V by tensor-map copies into a ring of 128-byte-swizzled tiles.  A tile
@@ -27,11 +27,17 @@
 // merge kernels (prefix_merge.cu).
 //
 // Roles (384 threads): warp 0 MMA issue, warp 1 tile copies, warp 2 walks the
-// share and publishes its units in shared memory, warp 3 clears the ends of V,
-// warps 4-7 / 8-11 query rows, softmax and output of Q tile 0 / 1.  Every wait
-// is bounded as in the forward kernel.
+// share and publishes its units in shared memory, warp 3 copies the units'
+// query rows and clears the ends of V, warps 4-7 / 8-11 softmax and output of Q
+// tile 0 / 1.  Every wait is bounded as in the forward kernel.
+//
+// A Q tile is one copy by a tensor map whose box is (heads of the group, tokens,
+// sequences), asked for as soon as the last S of the unit before is done.
+// (Gathered by the softmax threads, a row each, it took them 3 to 5 us between
+// two units; by one warp's 16-byte copies 2.5 to 4.)
 #include "attn_sync.cuh"
 #include "prefix_common.cuh"
+#include "prefix_few.cuh"
 
 namespace attn {
 namespace prefix {
@@ -54,9 +60,10 @@ constexpr int kUnits = 4;  // published units held at a time
 constexpr int kOver = 4;
 
 // Tile maps: keys and values of the prefix and the sequences, whole tiles and
-// boxes of their last ones.
+// boxes of their last ones; and the query rows.
 struct Maps {
   CUtensorMap m[8];  // 4 * own + 2 * tail + (V)
+  CUtensorMap q;
 };
 
 // Where a unit's part goes, other than a slot (>= 0).
@@ -68,7 +75,7 @@ struct Record {
   int j0;         // first of them
   int np, plen;   // tiles and keys of the prefix in the unit's list
   int b, h, len, n_new;  // b < 0: rows of all sequences
-  int row0;       // first row of tile 0
+  int tile0;      // first Q tile
   int dest;
   int n[2];       // key tiles each Q tile sees
   int full[2];    // own tiles below this one are seen whole by each valid row
@@ -82,13 +89,14 @@ struct Smem {
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
   static constexpr int kBars = kRing + kSlots * kTile;
-  // kv_full, kv_empty [slots], unit_full, unit_empty, q[2], s[2], p[2], o[2],
-  // end, cleared, drain
-  static constexpr int kNumBars = 2 * kSlots + 2 * kUnits + 11;
+  // kv_full, kv_empty [slots], unit_full, unit_empty, q[2], q_free[2], s[2],
+  // p[2], o[2], end, cleared, drain
+  static constexpr int kNumBars = 2 * kSlots + 2 * kUnits + 13;
   static constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM base, abort
   static constexpr int kRecords = kMisc + 8;
   static constexpr int kBytes = kRecords + kUnits * sizeof(Record);
   static_assert(kBytes + 1024 <= 227 * 1024, "shared memory per CTA");
+  static_assert(kFewWarps * kFewRing <= kBytes, "rings of the few rows");
 };
 
 // Valid keys of tile j of a unit's list, and whether it is the sequence's own.
@@ -101,6 +109,28 @@ __device__ __forceinline__ int tile_keys(int j, int np, int plen, int len,
 // ------------------------------------------------------------- the list
 __device__ __forceinline__ int places(int steps) {
   return steps == 0 ? 0 : steps + kOver;
+}
+
+__device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
+  kv8::Cut c;
+  c.n = max(1, min(ctas, total));
+  c.q = total / c.n;
+  c.rest = total - c.q * c.n;
+  return c;
+}
+
+// kFew: CTAs that take the prefix, of those of the launch; the others take the
+// sequences' own keys.  In proportion to the time that either takes an SM: a
+// step (256 rows, 128 keys) as long as kStepTiles of the few rows' tiles.
+constexpr int kStepTiles = 10;
+__device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
+                                           int few) {
+  if (few == 0) return p.grid;
+  const long long many =
+      static_cast<long long>(p.pack_blocks) * p.Hkv * places(np) * kStepTiles;
+  if (many == 0) return 0;
+  const long long n = (p.grid * many + (many + few) / 2) / (many + few);
+  return max(1, min(static_cast<int>(n), p.grid - 1));
 }
 
 // A unit, or the part of one, that a CTA works on: key tiles [j0, j1) of its
@@ -122,12 +152,13 @@ __device__ __forceinline__ int pair_steps(const PrefixParams& p, int np, int i,
     *len = *n_new = 0;
     return np;
   }
-  const int b = (i - p.pack_blocks) / p.row_blocks;
+  const int b = fast_div(i - p.pack_blocks, p.fd_blocks);
   const int u = i - p.pack_blocks - b * p.row_blocks;
   *len = kv8::seq_len(p, b);
   *n_new = kv8::seq_new(p, b);
-  if (u * kUnitRows >= *n_new * p.group) return 0;
-  return tiles_seen(p, *len, *n_new, u * kUnitRows, (u + 1) * kUnitRows) +
+  const int r0 = u * 2 * p.tile_rows;
+  if (r0 >= *n_new * p.group) return 0;
+  return tiles_seen(p, *len, *n_new, r0, r0 + 2 * p.tile_rows) +
          (p.mode == kJoint ? np : 0);
 }
 
@@ -146,16 +177,40 @@ struct Walk {
       w.b = -1;
       w.u = i;
     } else {
-      w.b = (i - p.pack_blocks) / p.row_blocks;
+      w.b = fast_div(i - p.pack_blocks, p.fd_blocks);
       w.u = i - p.pack_blocks - w.b * p.row_blocks;
     }
   }
 
+  // A share of `count` places that begins at place `off` of unit w.
+  __device__ __forceinline__ bool start_at(int off, int count) {
+    const int at = off - kOver;  // steps before it (negative: empty places)
+    w.j0 = max(0, at);
+    w.j1 = min(w.steps, at + count);
+    left = count - (w.j1 - at);
+    return w.j1 > w.j0;
+  }
+
+  // The share of CTA cta_ of `ctas`.
   __device__ __forceinline__ bool take(const PrefixParams& p, int cta_,
-                                       int lane) {
+                                       int ctas, int np_, int lane) {
     cta = cta_;
-    np = prefix_tiles(p);
+    np = np_;
     const int pairs = all_pairs(p);
+    if (p.mode == kFew) {  // units alike
+      const int each = places(np);
+      const int total = pairs * p.Hkv * each;
+      if (total == 0) return false;
+      cut = make_cut(ctas, total);
+      if (cta >= cut.n) return false;
+      const int x = cut.first(cta), count = cut.first(cta + 1) - x;
+      const int unit = x / each, i = unit / p.Hkv;
+      set_pair(p, i);
+      w.h = unit - i * p.Hkv;
+      w.len = w.n_new = 0;
+      w.steps = np;
+      return start_at(x - unit * each, count);
+    }
     int total = 0;
     for (int i = lane; i < pairs; i += 32) {
       int len, n_new;
@@ -166,7 +221,7 @@ struct Walk {
       total += __shfl_xor_sync(0xffffffffu, total, s);
     total *= p.Hkv;
     if (total == 0) return false;
-    cut = kv8::make_cut<1>(p, total);
+    cut = make_cut(ctas, total);
     if (cta >= cut.n) return false;
     const int x = cut.first(cta);
     const int count = cut.first(cta + 1) - x;
@@ -191,12 +246,7 @@ struct Walk {
         w.n_new = __shfl_sync(0xffffffffu, n_new, l);
         w.steps = __shfl_sync(0xffffffffu, steps, l);
         w.h = off / places(w.steps);
-        // Steps of the unit before the share (negative: empty places).
-        const int at = off - w.h * places(w.steps) - kOver;
-        w.j0 = max(0, at);
-        w.j1 = min(w.steps, at + count);
-        left = count - (w.j1 - at);
-        return w.j1 > w.j0;
+        return start_at(off - w.h * places(w.steps), count);
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -239,21 +289,21 @@ __device__ __forceinline__ void fill_record(const PrefixParams& p,
   rec->h = w.h;
   rec->len = w.len;
   rec->n_new = w.n_new;
-  rec->row0 = w.u * kUnitRows;
+  rec->tile0 = 2 * w.u;
   const bool whole = w.j0 == 0 && w.j1 == w.steps;
   if (p.mode == kJoint)
-    rec->dest = whole ? kFinal : walk.cta + (w.j0 == 0 ? p.many_grid : 0);
+    rec->dest = whole ? kFinal : walk.cta + (w.j0 == 0 ? p.grid : 0);
   else
     rec->dest = w.j0 == 0 ? kBase : walk.cta;
   for (int t = 0; t < 2; ++t) {
-    const int r0 = w.u * kUnitRows + t * kTM;
+    const int tile = 2 * w.u + t, r0 = tile * p.tile_rows;
     int hi = 0;
     rec->full[t] = 0;
     if (w.b < 0) {
-      if (r0 < static_cast<long long>(p.B) * p.rows) hi = np;
+      if (tile * p.tile_seqs < p.B) hi = np;
     } else if (r0 < w.n_new * p.group) {
-      hi = np + tiles_seen(p, w.len, w.n_new, r0, r0 + kTM);
-      rec->full[t] = kv8::row_end(p, w.len, w.n_new, r0) / kTN;
+      hi = np + tiles_seen(p, w.len, w.n_new, r0, r0 + p.tile_rows);
+      rec->full[t] = row_end(p, w.len, w.n_new, r0) / kTN;
     }
     rec->n[t] = max(0, min(hi, w.j1) - w.j0);
   }
@@ -265,11 +315,12 @@ template <int D>
 __device__ __forceinline__ void write_unseen(const PrefixParams& p, int lane) {
   if (p.mode != kJoint) return;
   const int np = prefix_tiles(p);
-  for (int i = blockIdx.x; i < p.B * p.row_blocks; i += gridDim.x) {
+  for (int i = blockIdx.x; i < p.B * p.row_blocks; i += p.grid) {
     int len, n_new;
     if (pair_steps(p, np, i, &len, &n_new) > 0) continue;
-    const int b = i / p.row_blocks, r0 = (i - b * p.row_blocks) * kUnitRows;
-    const int n = min(kUnitRows, n_new * p.group - r0);
+    const int b = fast_div(i, p.fd_blocks);
+    const int r0 = (i - b * p.row_blocks) * 2 * p.tile_rows;
+    const int n = min(2 * p.tile_rows, n_new * p.group - r0);
     for (int j = lane; j < n * p.Hkv; j += 32) {
       const int h = j / n, r = r0 + j - h * n;
       const long long row = q_row_index(p, b, h, r);
@@ -278,6 +329,34 @@ __device__ __forceinline__ void write_unseen(const PrefixParams& p, int lane) {
       if (p.lse != nullptr) p.lse[row] = -INFINITY;
     }
   }
+}
+
+// Row i of tile t of a unit: its sequence (-1: none) and row of the K/V head
+// there.
+__device__ __forceinline__ int row_of(const PrefixParams& p,
+                                      volatile Record* rec, int t, int i,
+                                      int* row) {
+  const int tile = rec->tile0 + t;
+  if (rec->b >= 0) {
+    *row = tile * p.tile_rows + i;
+    return i < p.tile_rows && *row < rec->n_new * p.group ? rec->b : -1;
+  }
+  const int s = fast_div(i, p.fd_rows);  // sequence within the tile
+  const int b = tile * p.tile_seqs + s;
+  *row = i - s * p.rows;
+  if (s >= p.tile_seqs || b >= p.B) return -1;
+  return *row < kv8::seq_new(p, b) * p.group ? b : -1;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m,
+                                            uint32_t bar, int c0, int c1,
+                                            int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::"
+      "complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2),
+      "r"(c3)
+      : "memory");
 }
 
 // One 32-byte sector: a thread's row stores then fill sectors whole.
@@ -299,7 +378,8 @@ __device__ __forceinline__ void store_row(uint4* dst, const uint32_t* x,
 }
 
 // ------------------------------------------------------------ the kernel
-template <int D, bool kBF16>
+// NT: 8-row groups of the few-row work (0: not kFew).
+template <int D, bool kBF16, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_many_kernel(const __grid_constant__ Maps maps,
                        const __grid_constant__ PrefixParams p) {
@@ -315,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_unit = bar_empty + 8 * L::kSlots;   // [kUnits]
   const uint32_t bar_ufree = bar_unit + 8 * kUnits;      // [kUnits]
   const uint32_t bar_q = bar_ufree + 8 * kUnits;         // [2]
-  const uint32_t bar_s = bar_q + 16;                     // [2]
+  const uint32_t bar_qfree = bar_q + 16;                 // [2]
+  const uint32_t bar_s = bar_qfree + 16;                 // [2]
   const uint32_t bar_p = bar_s + 16;                     // [2]
   const uint32_t bar_o = bar_p + 16;                     // [2]
   const uint32_t bar_end = bar_o + 16;                   // [1]
@@ -328,21 +409,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x < L::kNumBars) {
     const uint32_t bar = s_base + L::kBars + 8 * threadIdx.x;
-    // Q tiles: one arrival per warp of the four; units read: one per warp of
-    // the other roles (11); P: one per softmax thread of the tile.
+    // Units read: one arrival per warp of the other roles (11); P: one per
+    // softmax thread of the tile.
     uint32_t count = 1;
     if (bar >= bar_ufree && bar < bar_q) count = 11;
-    if (bar >= bar_q && bar < bar_s) count = 4;
     if (bar >= bar_p && bar < bar_o) count = kTM;
     ptx::mbar_init(bar, count);
     if (threadIdx.x == 0) *abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (threadIdx.x >= 32 && threadIdx.x < 40)
-    ptx::prefetch_tensormap(&maps.m[threadIdx.x - 32]);
+  if (threadIdx.x >= 32 && threadIdx.x < 41)
+    ptx::prefetch_tensormap(threadIdx.x == 40 ? &maps.q
+                                              : &maps.m[threadIdx.x - 32]);
   // Tensor memory is taken behind the wait for the kernel ahead (which may
   // still have to take its own) and before the one behind may start.
   ptx::griddep_wait();
+  const int np = prefix_tiles(p);
+  int ctas = p.grid;
+  if constexpr (NT > 0) {
+    const int few = few_total<D>(p, lane);
+    ctas = prefix_ctas(p, np, few);
+    const int cta = static_cast<int>(blockIdx.x) - ctas;
+    if (cta >= 0) {
+      ptx::griddep_launch_dependents();
+      if (warp < 4) {
+        ptx::setmaxnreg_dec<kRegsControl>();
+      } else {
+        ptx::setmaxnreg_inc<kRegsSoftmax>();
+        few_share<D, NT, kBF16>(p, cta * kFewWarps + warp - 4,
+                                (p.grid - ctas) * kFewWarps, few, lane,
+                                s_base + (warp - 4) * kFewRing);
+      }
+      return;
+    }
+  }
   if (warp == 0) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
@@ -376,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) {
       // ------------------------------------------------ units of the share
       Walk walk;
-      bool more = walk.take(p, static_cast<int>(blockIdx.x), lane);
+      bool more =
+          walk.take(p, static_cast<int>(blockIdx.x), ctas, np, lane);
       const int plen = prefix_len(p);
       int4 split = make_int4(0, 0, 0, 0);
       for (int k = 0; ok; ++k) {
@@ -408,24 +509,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0 && p.mode == kJoint) p.split[blockIdx.x] = split;
     } else if (warp == 3) {
-      // --------------------------------------- ends of V's last tiles
-      // In step with the MMA issuer, which asks for each when it has arrived
-      // (a warp that looked at some phases only of the ring's barriers could
-      // take one for another).
+      // ------------------------------- query rows, ends of V's last tiles
+      // The ends in step with the MMA issuer, which asks for each when it has
+      // arrived (a warp that looked at some phases only of the ring's barriers
+      // could take one for another).
       int it = 1;  // V tiles of the stream are odd
-      int uses = 0;
+      int ends = 0, q_uses[2] = {0, 0};
+      const int q_tokens = fast_div(p.tile_rows, p.fd_group);
+      const uint32_t q_bytes =
+          (p.mode == kJoint ? p.tile_rows : p.tile_seqs * p.rows) * D * 2;
       for (int k = 0; ok; ++k) {
         volatile Record* rec = get_unit(k);
         if (rec == nullptr) break;
         const int n = rec->n_kv, j0 = rec->j0, np = rec->np;
         const int plen = rec->plen, len = rec->len;
+        const int n0 = rec->n[0], n1 = rec->n[1];
+        const int b = rec->b, h = rec->h, tile0 = rec->tile0;
         release_unit(k);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (t ? n1 : n0) == 0) continue;
+          if (q_uses[t] > 0) ok = wait(bar_qfree + 8 * t, q_uses[t] - 1, 5);
+          if (!ok) break;
+          ++q_uses[t];
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar_q + 8 * t, q_bytes);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(s_base + L::kQ + t * L::kTile + c * L::kBox, &maps.q,
+                          bar_q + 8 * t, c * 64, h * p.group,
+                          b < 0 ? 0 : (tile0 + t) * q_tokens,
+                          b < 0 ? (tile0 + t) * p.tile_seqs : b);
+          }
+        }
+        if (!ok) break;
         for (int j = 0; j < n; ++j, it += 2) {
           bool own;
           const int valid = tile_keys(j0 + j, np, plen, len, &own);
           if (valid % 16 == 0) continue;
           const int slot = it % L::kSlots;
-          ok = wait(bar_end, uses++, 5);
+          ok = wait(bar_end, ends++, 5);
           if (!ok) break;
           const uint32_t at = s_base + L::kRing + slot * L::kTile;
           const int rows = 16 - valid % 16;
@@ -440,6 +563,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) ptx::mbar_arrive(bar_cleared);
         }
       }
+      if (!ok) {  // let the copies in flight land
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (q_uses[t] > 0)
+            drain_wait(bar_q + 8 * t, (q_uses[t] - 1) & 1, p);
+      }
+      __syncwarp();
       write_unseen<D>(p, lane);
     } else if (warp == 1) {
       // -------------------------------------------------------- tile copies
@@ -487,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 0) {
       // -------------------------------------------------------- MMA issue
-      const uint32_t idesc_qk = ptx::idesc_f16(kBF16, kTM, kTN, false, false);
+      const uint32_t idesc_qk =
+          ptx::idesc_f16(kBF16, kTM, kTN, false, p.negate != 0);
       const uint32_t idesc_pv = ptx::idesc_f16(kBF16, kTM, D, true, false);
       constexpr uint32_t kHi = ptx::sdesc_hi_sw128(1024);
       const uint32_t q_lo = ptx::sdesc_lo(s_base + L::kQ, 16);
@@ -507,12 +638,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // `steps` of 16 keys.
       auto issue_pv = [&](int t, int slot, bool acc, int steps) {
         const uint32_t b0 = v_lo + slot * kTile16;
+        if (steps == kTN / 16) {
 #pragma unroll
-        for (int kk = 0; kk < kTN / 16; ++kk)
-          if (kk < steps)
+          for (int kk = 0; kk < kTN / 16; ++kk)
             ptx::mma_ts_elect(tmem + kOCol + t * D, tmem + t * kTN + kk * 8,
                               b0 + ((kk * 16 * 128) >> 4), kHi, idesc_pv,
                               (acc || kk > 0) ? 1u : 0u);
+        } else {
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk)
+            ptx::mma_ts_elect(tmem + kOCol + t * D, tmem + t * kTN + kk * 8,
+                              b0 + ((kk * 16 * 128) >> 4), kHi, idesc_pv,
+                              (acc || kk > 0) ? 1u : 0u);
+        }
       };
       int it = 0;  // tiles consumed
       int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
@@ -544,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++q_uses[t];
           ptx::tc_fence_after();
           issue_qk(t, it % L::kSlots);
+          if (n == 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
           issued = true;
         }
         if (!ok) break;
@@ -585,6 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tc_fence_after();
             }
             issue_qk(t, slot_k);
+            // Behind the tile's last S its query rows make room.
+            if (j + 1 == n - 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
           }
           if (!ok) break;
           ptx::tc_commit_elect(bar_empty + 8 * slot_v);
@@ -615,54 +756,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 1e-37 vanish next to any maximum).
     const float c = fmaxf(p.scale_log2, 1e-37f);
     int s_uses = 0, o_uses = 0;
-    // This thread's row of unit `rec`: the sequence (-1: none) and its row of
-    // the K/V head there.
-    auto row_of = [&](volatile Record* rec, int* row) -> int {
-      int x = rec->row0 + t * kTM + r;
-      int b = rec->b;
-      if (b >= 0) {
-        *row = x;
-        return x < rec->n_new * p.group ? b : -1;
-      }
-      b = x / p.rows;
-      x -= b * p.rows;
-      *row = x;
-      if (b >= p.B) return -1;
-      return x < kv8::seq_new(p, b) * p.group ? b : -1;
-    };
-    // This thread's Q row of unit `rec` to shared memory, with the sign of the
-    // scale.  The buffer is free: every S of the tile has been read.
-    auto stage_q = [&](volatile Record* rec) {
-      int row;
-      const int b = row_of(rec, &row);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (b >= 0 ? q_row_index(p, b, rec->h, row) * D : 0));
-      const uint32_t sign = p.negate ? 0x80008000u : 0u;
-      const uint32_t dst = s_base + L::kQ + t * L::kTile + r * 128;
-      const uint32_t sw = r % 8;
-      uint4 y[D / 8];
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k)
-        y[k] = b >= 0 ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k)
-        ptx::st_shared_v4(dst + (k / 8) * L::kBox + (((k % 8) ^ sw) << 4),
-                          y[k].x ^ sign, y[k].y ^ sign, y[k].z ^ sign,
-                          y[k].w ^ sign);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar_q + 8 * t);
-    };
-    volatile Record* rec = get_unit(0);
-    if (rec != nullptr && rec->n[t] > 0) stage_q(rec);
-    for (int k = 0; rec != nullptr; ++k) {
+    for (int k = 0; ok; ++k) {
+      volatile Record* rec = get_unit(k);
+      if (rec == nullptr) break;
       const int n = rec->n[t], j0 = rec->j0, np = rec->np;
       const int plen = rec->plen, len = rec->len;
       const int full = rec->full[t];
       int vis = len;  // own keys that this row sees
-      if (rec->b >= 0) {
-        const int row = rec->row0 + t * kTM + r, n_new = rec->n_new;
-        if (row < n_new * p.group) vis = kv8::row_end(p, len, n_new, row);
+      // A warp without rows keeps in step but computes nothing: its P are
+      // whatever S left there, which reaches its own rows of O only.
+      bool live;
+      {
+        int row;
+        const bool row_ok = row_of(p, rec, t, r, &row) >= 0;
+        live = __any_sync(0xffffffffu, row_ok);
+        if (rec->b >= 0 && row_ok) vis = row_end(p, len, rec->n_new, row);
       }
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
@@ -675,6 +783,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++s_uses;
         ptx::tc_fence_after();
+        if (!live) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar_p + 8 * t);
+          continue;
+        }
         uint32_t sr[kTN];
 #pragma unroll
         for (int q = 0; q < kTN / 32; ++q)
@@ -749,10 +862,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive(bar_p + 8 * t);
       }
       if (!ok) break;
-      // The next unit's Q while this one's last products run.
-      volatile Record* next = get_unit(k + 1);
-      if (!ok) break;
-      if (next != nullptr && next->n[t] > 0) stage_q(next);
       if (n > 0) {
         ok = wait(bar_o + 8 * t, o_uses, 4);
         if (!ok) break;
@@ -761,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int dest = rec->dest, h = rec->h;
       int row;
-      const int b = row_of(rec, &row);
+      const int b = row_of(p, rec, t, r, &row);
       const bool row_ok = b >= 0;
       // O leaves as the average that it is.  A row that sees nothing: 0,
       // whatever its accumulator holds.
@@ -806,10 +915,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           dst_o = p.base_o;
           dst_lse2 = p.base_lse2;
           const long long all = static_cast<long long>(p.B) * p.rows;
-          at = rec->b < 0 ? h * all + rec->row0 + t * kTM + r
+          at = rec->b < 0 ? h * all + static_cast<long long>(b) * p.rows
                           : p.Hkv * all +
                                 (static_cast<long long>(b) * p.Hkv + h) *
-                                    p.rows + row;
+                                    p.rows;
+          at += row;
         } else {
           at = static_cast<long long>(dest) * kUnitRows + t * kTM + r;
         }
@@ -836,7 +946,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::tc_fence_before();
       release_unit(k);
-      rec = next;
     }
   }
 
@@ -848,19 +957,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kBF16>
-cudaError_t launch(PrefixParams p, const CUtensorMap* maps,
+template <int D, bool kBF16, int NT>
+cudaError_t launch(const PrefixParams& p, const CUtensorMap* maps,
                    cudaStream_t stream) {
-  p.grid = p.many_grid;
   constexpr int kBytes = Smem<D>::kBytes + 1024;
   const cudaError_t err = cudaFuncSetAttribute(
-      prefix_many_kernel<D, kBF16>,
+      prefix_many_kernel<D, kBF16, NT>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (err != cudaSuccess) return err;
   Maps m;
   for (int i = 0; i < 8; ++i) m.m[i] = maps[i];
-  return kv8::launch_pdl(prefix_many_kernel<D, kBF16>, p.many_grid, kThreads,
+  m.q = maps[8];
+  return kv8::launch_pdl(prefix_many_kernel<D, kBF16, NT>, p.grid, kThreads,
                          kBytes, stream, m, p);
+}
+
+template <int D, bool kBF16>
+cudaError_t launch_dt(const PrefixParams& p, const CUtensorMap* maps,
+                      cudaStream_t stream) {
+  if (p.mode != kFew) return launch<D, kBF16, 0>(p, maps, stream);
+  return few_rows(p.rows) == 8 ? launch<D, kBF16, 1>(p, maps, stream)
+                               : launch<D, kBF16, 2>(p, maps, stream);
 }
 
 }  // namespace
@@ -868,10 +985,10 @@ cudaError_t launch(PrefixParams p, const CUtensorMap* maps,
 cudaError_t launch_many(int D, bool bf16, const PrefixParams& p,
                         const CUtensorMap* maps, cudaStream_t stream) {
   if (D == 64)
-    return bf16 ? launch<64, true>(p, maps, stream)
-                : launch<64, false>(p, maps, stream);
-  return bf16 ? launch<128, true>(p, maps, stream)
-              : launch<128, false>(p, maps, stream);
+    return bf16 ? launch_dt<64, true>(p, maps, stream)
+                : launch_dt<64, false>(p, maps, stream);
+  return bf16 ? launch_dt<128, true>(p, maps, stream)
+              : launch_dt<128, false>(p, maps, stream);
 }
 
 }  // namespace prefix

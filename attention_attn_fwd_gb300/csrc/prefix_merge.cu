@@ -1,5 +1,4 @@
-// Joins the parts of a query row's attention behind a shared prefix: a warp per
-// row.  With part s the average O_s and the log-sum-exp L_s of its keys,
+// Joins the parts of a query row's attention behind a shared prefix.  With part s the average O_s and the log-sum-exp L_s of its keys,
 //   O = sum_s 2^(L_s - m) O_s / sum_s 2^(L_s - m),  LSE = m + log2(the sum).
 #include "prefix_common.cuh"
 
@@ -11,135 +10,183 @@ using kv8::kNone;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 8;  // parts whose O a warp has in flight
 
-// The sum over parts 0 .. n - 1, where at(s) gives the row of part s in an
-// array of O rows and one of LSEs.  (A part that sees nothing has the factor 0
-// and no O.)
-template <int D, bool kBF16, class At>
-__device__ __forceinline__ void join(const PrefixParams& p, int n,
-                                     long long row, int lane, At at) {
+// What a warp has of a row: the sum over its parts, relative to 2^mx.
+struct Sum {
+  float mx, sum;
+  float4 acc;
+};
+
+// Parts [s0, s1) by one warp, where at(s, &o) gives the LSE of part s and the
+// place of its O.  (O is read before its factor is known; a part that sees
+// nothing has the factor 0 and no O.)
+template <int D, class At>
+__device__ __forceinline__ Sum add_parts(int s0, int s1, int lane, At at) {
   constexpr int kCols = D / 4;          // float4 columns
   constexpr int kGroups = 32 / kCols;   // parts a warp reads at a time
   const int col = lane % kCols, sub = lane / kCols;
-  float mx = kNone, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 32) {
+  Sum t{kNone, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (; s0 < s1; s0 += 32) {
+    const int count = min(32, s1 - s0);
+    const float4* o = nullptr;
     float x = -INFINITY;
-    if (s0 + lane < n) {
-      const float *o, *lse2;
-      const long long i = at(s0 + lane, &o, &lse2);
-      x = lse2[i];
-    }
-    float m = mx;
-    m = fmaxf(m, x);
+    if (lane < count) x = at(s0 + lane, &o);
+    const unsigned long long o_bits = reinterpret_cast<unsigned long long>(o);
+    float m = fmaxf(t.mx, x);
 #pragma unroll
     for (int k = 16; k > 0; k /= 2)
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    const float before = ptx::ex2(mx - m);
+    const float before = ptx::ex2(t.mx - m);
     const float f_all = ptx::ex2(x - m);
-    mx = m;
-    acc.x *= before;
-    acc.y *= before;
-    acc.z *= before;
-    acc.w *= before;
-    sum = sum * before + f_all;  // (a lane's share)
-    const int count = min(32, n - s0);
-#pragma unroll 4
-    for (int k = 0; k < count; k += kGroups) {
-      const int s = k + sub;
-      const float f = __shfl_sync(0xffffffffu, f_all, s % 32);
-      if (s < count && f != 0.f) {
-        const float *o, *lse2;
-        const long long i = at(s0 + s, &o, &lse2);
-        const float4 y = reinterpret_cast<const float4*>(o)[i * kCols + col];
-        acc.x += y.x * f;
-        acc.y += y.y * f;
-        acc.z += y.z * f;
-        acc.w += y.w * f;
+    t.mx = m;
+    t.acc.x *= before;
+    t.acc.y *= before;
+    t.acc.z *= before;
+    t.acc.w *= before;
+    t.sum = t.sum * before + f_all;  // (a lane's share)
+    for (int k0 = 0; k0 < count; k0 += kAhead * kGroups) {
+      float4 y[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = k0 + i * kGroups + sub;
+        const float4* from = reinterpret_cast<const float4*>(
+            __shfl_sync(0xffffffffu, o_bits, k % 32));
+        y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < count) y[i] = from[col];
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = k0 + i * kGroups + sub;
+        const float f = __shfl_sync(0xffffffffu, f_all, k % 32);
+        if (k < count && f != 0.f) {
+          t.acc.x += y[i].x * f;
+          t.acc.y += y[i].y * f;
+          t.acc.z += y[i].z * f;
+          t.acc.w += y[i].w * f;
+        }
       }
     }
   }
   // (The lanes' shares were scaled alike.)
 #pragma unroll
-  for (int k = 16; k > 0; k /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  for (int k = 16; k > 0; k /= 2)
+    t.sum += __shfl_xor_sync(0xffffffffu, t.sum, k);
   if constexpr (kGroups == 2) {
-    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
-    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
-    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+    t.acc.x += __shfl_xor_sync(0xffffffffu, t.acc.x, 16);
+    t.acc.y += __shfl_xor_sync(0xffffffffu, t.acc.y, 16);
+    t.acc.z += __shfl_xor_sync(0xffffffffu, t.acc.z, 16);
+    t.acc.w += __shfl_xor_sync(0xffffffffu, t.acc.w, 16);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if (lane < kCols) {
-    uint2 out;
-    out.x = ptx::pack2<kBF16>(acc.x * inv, acc.y * inv);
-    out.y = ptx::pack2<kBF16>(acc.z * inv, acc.w * inv);
-    reinterpret_cast<uint2*>(p.o + row * D)[col] = out;
-  }
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[row] = sum == 0.f ? -INFINITY
-                            : (mx + log2f(sum)) * 0.69314718055994531f;
+  return t;
 }
 
-// kFew and kPacked: every row, with the parts over the prefix first.
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads)
-    prefix_merge_kernel(const __grid_constant__ PrefixParams p) {
+__device__ __forceinline__ void write_row(const PrefixParams& p, long long row,
+                                          const Sum& t, int lane) {
+  const float inv = t.sum == 0.f ? 0.f : 1.f / t.sum;
+  if (lane < D / 4) {
+    uint2 out;
+    out.x = ptx::pack2<kBF16>(t.acc.x * inv, t.acc.y * inv);
+    out.y = ptx::pack2<kBF16>(t.acc.z * inv, t.acc.w * inv);
+    reinterpret_cast<uint2*>(p.o + row * D)[lane] = out;
+  }
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[row] = t.sum == 0.f ? -INFINITY
+                              : (t.mx + log2f(t.sum)) * 0.69314718055994531f;
+}
+
+// kFew and kPacked: every row, with the parts over the prefix first, by
+// row_warps warps.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kThreads, 3)
+    prefix_merge_kernel(const __grid_constant__ PrefixParams p,
+                        int row_warps) {
+  __shared__ float2 sm_sum[kWarps];
+  __shared__ float4 sm_acc[kWarps][D / 4];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long id = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long id =
+      (static_cast<long long>(blockIdx.x) * kWarps + warp) / row_warps;
   const int R = p.rows;
   const long long all = static_cast<long long>(p.B) * R;  // rows of a head
   const bool in = id < all * p.Hkv;
   // (b, h, r), r fastest.
-  const int bh = in ? static_cast<int>(id / R) : 0;
+  const int bh =
+      !in ? 0
+      : id < 0x7fffffff ? fast_div(static_cast<int>(id), p.fd_rows)
+                        : static_cast<int>(id / R);
   const int r = in ? static_cast<int>(id - static_cast<long long>(bh) * R) : 0;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int len = kv8::seq_len(p, b), n_new = kv8::seq_new(p, b);
   const int np = prefix_tiles(p);
-  const int x = b * R + r;
-  const int u = r / kUnitRows;
+  // Its Q tiles over the prefix and over the own keys, and places in their
+  // units.
+  const int tile = fast_div(b, p.fd_tile_seqs);
+  const int in_unit = tile % 2 * kTM + (b - tile * p.tile_seqs) * R + r;
+  const int own_tile = fast_div(r, p.fd_tile_rows);
+  const int own_in_unit =
+      own_tile % 2 * kTM + r - own_tile * p.tile_rows;
+  const int u = own_tile / 2, r0 = u * 2 * p.tile_rows;
   // (Lengths are read ahead of the wait: the kernels ahead do not write them.)
-  int few_first = 0, few_n = 0;
-  if (p.mode == kFew && len > 0 && in) {
-    constexpr int kKeys = few_keys<D>();
-    const int tiles = (len + kKeys - 1) / kKeys;
-    int first;
-    const int total = kv8::list_tiles<kKeys, kFewOver>(p, b, lane, &first);
-    const kv8::Cut cut = kv8::make_cut<kFewWarps>(p, total);
-    first += h * (tiles + kFewOver) + kFewOver;
-    few_first = cut.owner(first);
-    few_n = cut.owner(first + tiles - 1) - few_first + 1;
-  }
   kv8::start_after_previous();
-  if (!in || r >= n_new * p.group) return;
+  const bool live = in && r < n_new * p.group;
   int2 pre = make_int2(0, 0), own = make_int2(0, 0);
-  if (np > 0)
-    pre = p.info[static_cast<long long>(x / kUnitRows) * p.Hkv + h];
-  if (p.mode == kFew)
-    own = make_int2(few_first, few_n);
-  else if (tiles_seen(p, len, n_new, u * kUnitRows, (u + 1) * kUnitRows) > 0)
-    own = p.info[(static_cast<long long>(p.pack_blocks) +
-                  static_cast<long long>(b) * p.row_blocks + u) * p.Hkv + h];
-  auto at = [&](int s, const float** o, const float** lse2) -> long long {
-    *o = p.base_o;
-    *lse2 = p.base_lse2;
-    if (s == 0 && pre.y > 0) return h * all + x;
-    if (s < pre.y) {
-      *o = p.slot_o;
-      *lse2 = p.slot_lse2;
-      return static_cast<long long>(pre.x + s) * kUnitRows + x % kUnitRows;
-    }
-    s -= pre.y;
+  if (live) {
+    if (np > 0)
+      pre = p.info[static_cast<long long>(tile / 2) * p.Hkv + h];
     if (p.mode == kFew) {
-      *o = p.few_o;
-      *lse2 = p.few_lse2;
-      return (static_cast<long long>(own.x + s) + bh) * few_rows(R) + r;
+      if (len > 0) own = p.own_info[bh];
+    } else if (tiles_seen(p, len, n_new, r0, r0 + 2 * p.tile_rows) > 0) {
+      own = p.info[(static_cast<long long>(p.pack_blocks) +
+                    static_cast<long long>(b) * p.row_blocks + u) * p.Hkv + h];
     }
-    if (s == 0) return p.Hkv * all + static_cast<long long>(bh) * R + r;
-    *o = p.slot_o;
-    *lse2 = p.slot_lse2;
-    return static_cast<long long>(own.x + s) * kUnitRows + r % kUnitRows;
+  }
+  auto at = [&](int s, const float4** o) -> float {
+    const float *from = p.base_o, *lse2 = p.base_lse2;
+    long long i;
+    if (s == 0 && pre.y > 0) {
+      i = h * all + static_cast<long long>(b) * R + r;
+    } else if (s < pre.y) {
+      from = p.slot_o;
+      lse2 = p.slot_lse2;
+      i = static_cast<long long>(pre.x + s) * kUnitRows + in_unit;
+    } else if (p.mode == kFew) {
+      from = p.few_o;
+      lse2 = p.few_lse2;
+      i = (static_cast<long long>(own.x + s - pre.y) + bh) * few_rows(R) + r;
+    } else if (s == pre.y) {
+      i = p.Hkv * all + static_cast<long long>(bh) * R + r;
+    } else {
+      from = p.slot_o;
+      lse2 = p.slot_lse2;
+      i = static_cast<long long>(own.x + s - pre.y) * kUnitRows +
+          own_in_unit;
+    }
+    *o = reinterpret_cast<const float4*>(from) + i * (D / 4);
+    return lse2[i];
   };
-  join<D, kBF16>(p, pre.y + own.y, q_row_index(p, b, h, r), lane, at);
+  const int n = pre.y + own.y, w = warp % row_warps;
+  Sum t = add_parts<D>(n * w / row_warps, n * (w + 1) / row_warps, lane, at);
+  if (row_warps > 1) {
+    if (lane == 0) sm_sum[warp] = make_float2(t.mx, t.sum);
+    if (lane < D / 4) sm_acc[warp][lane] = t.acc;
+    __syncthreads();
+    if (w != 0) return;
+    float mx = t.mx;
+    for (int i = 1; i < row_warps; ++i) mx = fmaxf(mx, sm_sum[warp + i].x);
+    Sum all_of{mx, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int i = 0; i < row_warps; ++i) {
+      const float f = ptx::ex2(sm_sum[warp + i].x - mx);
+      const float4 y = sm_acc[warp + i][lane % (D / 4)];
+      all_of.sum += sm_sum[warp + i].y * f;
+      all_of.acc.x += y.x * f;
+      all_of.acc.y += y.y * f;
+      all_of.acc.z += y.z * f;
+      all_of.acc.w += y.w * f;
+    }
+    t = all_of;
+  }
+  if (live) write_row<D, kBF16>(p, q_row_index(p, b, h, r), t, lane);
 }
 
 // kJoint: the rows of each CTA's unit that went on behind it.
@@ -155,27 +202,35 @@ __global__ void __launch_bounds__(kThreads)
   const int4 split = p.split[cta];
   const int b = split.x, h = split.y, parts = split.w;
   if (parts == 0) return;
-  const int r = split.z * kUnitRows + i;
-  if (r >= kv8::seq_new(p, b) * p.group) return;
-  auto at = [&](int s, const float** o, const float** lse2) -> long long {
-    *o = p.slot_o;
-    *lse2 = p.slot_lse2;
-    return static_cast<long long>(s == 0 ? p.many_grid + cta : cta + s) *
-               kUnitRows + i;
+  const int tile = i / kTM, in_tile = i % kTM;
+  const int r = (2 * split.z + tile) * p.tile_rows + in_tile;
+  if (in_tile >= p.tile_rows || r >= kv8::seq_new(p, b) * p.group) return;
+  auto at = [&](int s, const float4** o) -> float {
+    const long long j =
+        static_cast<long long>(s == 0 ? p.grid + cta : cta + s) *
+            kUnitRows + i;
+    *o = reinterpret_cast<const float4*>(p.slot_o) + j * (D / 4);
+    return p.slot_lse2[j];
   };
-  join<D, kBF16>(p, parts, q_row_index(p, b, h, r), lane, at);
+  const Sum t = add_parts<D>(0, parts, lane, at);
+  write_row<D, kBF16>(p, q_row_index(p, b, h, r), t, lane);
 }
 
 template <int D, bool kBF16>
 cudaError_t launch(PrefixParams p, cudaStream_t stream) {
   if (p.mode == kJoint)
     return kv8::launch_pdl(prefix_join_kernel<D, kBF16>,
-                           static_cast<long long>(p.many_grid) * kParts,
+                           static_cast<long long>(p.grid) * kParts,
                            kThreads, 0, stream, p);
-  p.grid = p.few_grid;
   const long long rows = static_cast<long long>(p.B) * p.rows * p.Hkv;
+  // Warps a row: as many as make the machine's warps busy, rows having some 20
+  // parts where they are few.
+  int row_warps = kWarps;
+  while (row_warps > 1 && rows * row_warps > 32LL * p.grid)
+    row_warps /= 2;
   return kv8::launch_pdl(prefix_merge_kernel<D, kBF16>,
-                         (rows + kWarps - 1) / kWarps, kThreads, 0, stream, p);
+                         (rows * row_warps + kWarps - 1) / kWarps, kThreads, 0,
+                         stream, p, row_warps);
 }
 
 }  // namespace

@@ -602,7 +602,8 @@ typedef struct {
  *           and sees the prefix and its own tokens up to it (the new tokens
  *           are its last n_b); 0: every row sees all lens[b] of them.
  *           A row that sees no token gets O = 0 and LSE = -inf.
- * Hq        a multiple of the cache's Hkv; scale finite, any sign;
+ * Hq        a multiple of the cache's Hkv, 128 times it at most (else
+ *           ATTN_ERR_UNSUPPORTED); scale finite, any sign;
  * dtype     ATTN_F16 or ATTN_BF16, of Q, O and the cache;
  *           NaN: a row of Q with NaN gets NaN and leaves the others alone; a
  *           NaN of K reaches the rows that see its token; a NaN or infinity of
@@ -612,7 +613,7 @@ typedef struct {
  *           attn_prefix_workspace_bytes(...) bytes; contents need no
  *           initialisation.  It must not be used by another call until this
  *           one has run.
- * Two or three kernels on `stream`.  O, LSE and workspace must not overlap each
+ * Two kernels on `stream`.  O, LSE and workspace must not overlap each
  * other or any input.  B == 0 or Sq == 0 is a successful no-op.  Deterministic
  * for a given device, shape and lengths.
  */

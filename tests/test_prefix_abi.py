@@ -68,6 +68,7 @@ def test_bad_caches_are_refused(lib, change, code):
     (dict(O=16 * MB), INVALID), (dict(O=8 * MB), INVALID),
     (dict(LSE=65 * MB), INVALID), (dict(LSE=50 * MB), INVALID),
     (dict(ws=64 * MB), INVALID), (dict(Sq=1 << 30), INVALID),
+    (dict(Hq=258), UNSUPPORTED),
 ])
 def test_refusals(lib, kw, code):
     assert fwd(lib, cache(), **kw) == code

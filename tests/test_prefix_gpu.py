@@ -162,6 +162,12 @@ CASES = [
     (2, 8, 4, 64, 500, 1, 64, [500, 777], 777, None, True),
     (2, 2, 1, 128, 250, 0, 1, [0, 300], 300, [0, 250], True),
     (2, 2, 1, 64, 125, 77, 77, [0, 300], 300, None, False),
+    # Groups that do not divide a tile's rows, and the largest.
+    (2, 5, 1, 64, 100, 140, 140, [100, 333], 333, None, True),
+    (3, 21, 3, 128, 15, 300, 300, [15, 40, 129], 130, [15, 1, 14], True),
+    (2, 127, 1, 64, 3, 200, 200, [3, 20], 20, None, True),
+    (3, 128, 1, 128, 1, 200, 200, [1, 20, 0], 20, [1, 1, 0], True),
+    (2, 256, 2, 64, 2, 130, 130, [2, 200], 200, None, True),
 ]
 
 
