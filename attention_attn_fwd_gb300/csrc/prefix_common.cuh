@@ -61,7 +61,7 @@ struct PrefixParams {
   float* few_lse2;
   int2* own_info;         // [B, Hkv]: first warp and number of parts
   int grid;               // CTAs of the launch
-  FastDiv fd_group, fd_rows, fd_blocks, fd_tile_seqs, fd_tile_rows;
+  FastDiv fd_group, fd_rows, fd_blocks, fd_tile_seqs, fd_tile_rows, fd_hkv;
   unsigned long long timeout_ns;
   unsigned int* status;
 };

@@ -94,17 +94,40 @@ __device__ __forceinline__ int few_places(int tiles) {
 }
 // Tiles of a sequence (of each of its heads): none where no row wants them.
 template <int D>
-__device__ __forceinline__ int few_tiles(const PrefixParams& p, int b) {
-  const int len = kv8::seq_len(p, b);
-  return kv8::seq_new(p, b) > 0 ? (len + few_keys<D>() - 1) / few_keys<D>()
-                                : 0;
+__device__ __forceinline__ int few_tiles_of(const PrefixParams& p, int len,
+                                            int n_new) {
+  len = kv8::clamp_len(len, p.capacity, p.status);
+  n_new = kv8::clamp_len(n_new, p.Sq, p.status);
+  return n_new > 0 ? (len + few_keys<D>() - 1) / few_keys<D>() : 0;
 }
+template <int D>
+__device__ __forceinline__ int few_tiles(const PrefixParams& p, int b) {
+  return few_tiles_of<D>(p, p.lens[b],
+                         p.new_lens == nullptr ? p.Sq : p.new_lens[b]);
+}
+
+// The lengths of the lane's first sequence, fetched ahead of their use.
+struct FewLens {
+  int len, n_new;
+  __device__ __forceinline__ void load(const PrefixParams& p, int lane) {
+    len = 0;
+    n_new = p.Sq;
+    if (lane < p.B) {
+      len = p.lens[lane];
+      if (p.new_lens != nullptr) n_new = p.new_lens[lane];
+    }
+  }
+};
 
 // Places of all segments, for every lane of the calling warp.
 template <int D>
-__device__ __forceinline__ int few_total(const PrefixParams& p, int lane) {
-  int t = 0;
-  for (int b = lane; b < p.B; b += 32) t += few_places<D>(few_tiles<D>(p, b));
+__device__ __forceinline__ int few_total(const PrefixParams& p,
+                                         const FewLens& ahead, int lane) {
+  int t = lane < p.B ? few_places<D>(few_tiles_of<D>(p, ahead.len,
+                                                     ahead.n_new))
+                     : 0;
+  for (int b = lane + 32; b < p.B; b += 32)
+    t += few_places<D>(few_tiles<D>(p, b));
 #pragma unroll
   for (int s = 16; s > 0; s /= 2) t += __shfl_xor_sync(0xffffffffu, t, s);
   return t * p.Hkv;

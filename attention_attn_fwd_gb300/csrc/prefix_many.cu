@@ -49,8 +49,8 @@ constexpr int kThreads = 384;
 constexpr float kTau = 8.f;  // lazy rescale threshold (log2 units)
 // Registers: the launch gives every thread 168; the shares of the three
 // warpgroups add up to 3 * 168.
-constexpr int kRegsControl = 88;
-constexpr int kRegsSoftmax = 208;
+constexpr int kRegsControl = 72;
+constexpr int kRegsSoftmax = 216;
 static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * 168,
               "register split exceeds the launch allocation");
 
@@ -78,7 +78,6 @@ struct Record {
   int tile0;      // first Q tile
   int dest;
   int n[2];       // key tiles each Q tile sees
-  int full[2];    // own tiles below this one are seen whole by each valid row
 };
 
 template <int D>
@@ -122,15 +121,15 @@ __device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
 // kFew: CTAs that take the prefix, of those of the launch; the others take the
 // sequences' own keys.  In proportion to the time that either takes an SM: a
 // step (256 rows, 128 keys) as long as kStepTiles of the few rows' tiles.
-constexpr int kStepTiles = 10;
+constexpr int kStepTiles = 32;
 __device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
                                            int few) {
   if (few == 0) return p.grid;
-  const long long many =
-      static_cast<long long>(p.pack_blocks) * p.Hkv * places(np) * kStepTiles;
-  if (many == 0) return 0;
-  const long long n = (p.grid * many + (many + few) / 2) / (many + few);
-  return max(1, min(static_cast<int>(n), p.grid - 1));
+  if (np == 0) return 0;
+  const float many = static_cast<float>(p.pack_blocks * p.Hkv) *
+                     static_cast<float>(places(np) * kStepTiles);
+  const int n = static_cast<int>(p.grid * (many / (many + few)) + 0.5f);
+  return max(1, min(n, p.grid - 1));
 }
 
 // A unit, or the part of one, that a CTA works on: key tiles [j0, j1) of its
@@ -204,7 +203,7 @@ struct Walk {
       cut = make_cut(ctas, total);
       if (cta >= cut.n) return false;
       const int x = cut.first(cta), count = cut.first(cta + 1) - x;
-      const int unit = x / each, i = unit / p.Hkv;
+      const int unit = x / each, i = fast_div(unit, p.fd_hkv);
       set_pair(p, i);
       w.h = unit - i * p.Hkv;
       w.len = w.n_new = 0;
@@ -298,12 +297,10 @@ __device__ __forceinline__ void fill_record(const PrefixParams& p,
   for (int t = 0; t < 2; ++t) {
     const int tile = 2 * w.u + t, r0 = tile * p.tile_rows;
     int hi = 0;
-    rec->full[t] = 0;
     if (w.b < 0) {
       if (tile * p.tile_seqs < p.B) hi = np;
     } else if (r0 < w.n_new * p.group) {
       hi = np + tiles_seen(p, w.len, w.n_new, r0, r0 + p.tile_rows);
-      rec->full[t] = row_end(p, w.len, w.n_new, r0) / kTN;
     }
     rec->n[t] = max(0, min(hi, w.j1) - w.j0);
   }
@@ -378,6 +375,69 @@ __device__ __forceinline__ void store_row(uint4* dst, const uint32_t* x,
 }
 
 // ------------------------------------------------------------ the kernel
+// S = Q K^T of D / 16 steps and its commit to `bar`, by one elected lane: one
+// election for all of them (an election an instruction, and descriptors made
+// between them, kept the issuing warp behind the tensor cores).  Descriptors as
+// (lo, hi) words; a step's operands lie 32 bytes on, every fourth box by box.
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b,
+                                             uint32_t hi, uint32_t idesc,
+                                             uint32_t bar) {
+#define ATTN_STEP(off, p)                                                   \
+  "add.u32 la, %1, " off ";\n\tadd.u32 lb, %2, " off ";\n\t"              \
+  "mov.b64 da, {la, %3};\n\tmov.b64 db, {lb, %3};\n\t"                    \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " p ";\n\t"
+#define ATTN_BEGIN                                                          \
+  "{\n\t.reg .pred e, no, yes;\n\t.reg .b64 da, db;\n\t"                 \
+  ".reg .b32 la, lb;\n\t"                                                  \
+  "setp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"                   \
+  "elect.sync _|e, 0xffffffff;\n\t"
+#define ATTN_END                                                            \
+  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."   \
+  "b64 [%5];\n\t}"
+  if constexpr (D == 128) {
+    asm volatile(ATTN_BEGIN ATTN_STEP("0", "no") ATTN_STEP("2", "yes")
+                     ATTN_STEP("4", "yes") ATTN_STEP("6", "yes")
+                         ATTN_STEP("1024", "yes") ATTN_STEP("1026", "yes")
+                             ATTN_STEP("1028", "yes")
+                                 ATTN_STEP("1030", "yes") ATTN_END ::"r"(d),
+                 "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(bar)
+                 : "memory");
+  } else {
+    asm volatile(ATTN_BEGIN ATTN_STEP("0", "no") ATTN_STEP("2", "yes")
+                     ATTN_STEP("4", "yes") ATTN_STEP("6", "yes")
+                         ATTN_END ::"r"(d),
+                 "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(bar)
+                 : "memory");
+  }
+#undef ATTN_STEP
+#undef ATTN_BEGIN
+#undef ATTN_END
+}
+
+// O (+)= P V of a whole tile, eight steps of 16 keys: P in tensor memory from
+// `a` on, 8 columns a step, V 2 KB on.
+__device__ __forceinline__ void issue_output(uint32_t d, uint32_t a,
+                                             uint32_t b, uint32_t hi,
+                                             uint32_t idesc, uint32_t acc) {
+#define ATTN_STEP(at, off, p)                                               \
+  "add.u32 ta, %1, " at ";\n\tadd.u32 lb, %2, " off ";\n\t"               \
+  "mov.b64 db, {lb, %3};\n\t"                                              \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, " p ";\n\t"
+  asm volatile(
+      "{\n\t.reg .pred e, acc, yes;\n\t.reg .b64 db;\n\t"
+      ".reg .b32 ta, lb;\n\t"
+      "setp.ne.b32 acc, %5, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t" ATTN_STEP("0", "0", "acc")
+          ATTN_STEP("8", "128", "yes") ATTN_STEP("16", "256", "yes")
+              ATTN_STEP("24", "384", "yes") ATTN_STEP("32", "512", "yes")
+                  ATTN_STEP("40", "640", "yes") ATTN_STEP("48", "768", "yes")
+                      ATTN_STEP("56", "896", "yes") "}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+#undef ATTN_STEP
+}
+
 // NT: 8-row groups of the few-row work (0: not kFew).
 template <int D, bool kBF16, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -421,17 +481,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x >= 32 && threadIdx.x < 41)
     ptx::prefetch_tensormap(threadIdx.x == 40 ? &maps.q
                                               : &maps.m[threadIdx.x - 32]);
-  // Tensor memory is taken behind the wait for the kernel ahead (which may
-  // still have to take its own) and before the one behind may start.
+  __syncthreads();
   ptx::griddep_wait();
-  const int np = prefix_tiles(p);
+  // (The merge kernel behind takes no tensor memory, and lets no other kernel
+  // start before it has waited for this one.)
+  ptx::griddep_launch_dependents();
+  FewLens few_lens;
+  if constexpr (NT > 0) few_lens.load(p, lane);
+  const int plen = prefix_len(p), np = (plen + kTN - 1) / kTN;
   int ctas = p.grid;
   if constexpr (NT > 0) {
-    const int few = few_total<D>(p, lane);
+    const int few = few_total<D>(p, few_lens, lane);
     ctas = prefix_ctas(p, np, few);
     const int cta = static_cast<int>(blockIdx.x) - ctas;
     if (cta >= 0) {
-      ptx::griddep_launch_dependents();
       if (warp < 4) {
         ptx::setmaxnreg_dec<kRegsControl>();
       } else {
@@ -443,15 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
   }
-  if (warp == 0) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
-    ptx::tmem_relinquish();
+  // Tensor memory is taken behind the wait for the kernel ahead (which may
+  // still have to take its own); the warps that use it meet here, the others
+  // go ahead.
+  uint32_t tmem = 0;
+  if (warp == 0 || warp >= 4) {
+    if (warp == 0) {
+      ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+      ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    ptx::named_barrier_sync(1, kThreads - 96);
+    ptx::tc_fence_after();
+    tmem = *tmem_slot;
   }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  ptx::griddep_launch_dependents();
 
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase, int role) {
@@ -478,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk walk;
       bool more =
           walk.take(p, static_cast<int>(blockIdx.x), ctas, np, lane);
-      const int plen = prefix_len(p);
       int4 split = make_int4(0, 0, 0, 0);
       for (int k = 0; ok; ++k) {
         if (k >= kUnits)
@@ -625,35 +692,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_lo = ptx::sdesc_lo(s_base + L::kRing, 16);
       const uint32_t v_lo = ptx::sdesc_lo(s_base + L::kRing, L::kBox);
       constexpr uint32_t kTile16 = L::kTile >> 4;
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);  // uniform
       auto issue_qk = [&](int t, int slot) {
-        const uint32_t a0 = q_lo + t * kTile16, b0 = k_lo + slot * kTile16;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * L::kBox + (kk % 4) * 32) >> 4;
-          ptx::mma_ss_elect(tmem + t * kTN, a0 + off, b0 + off, kHi, idesc_qk,
-                            kk > 0 ? 1u : 0u);
-        }
-        ptx::tc_commit_elect(bar_s + 8 * t);
+        issue_scores<D>(tm + t * kTN, q_lo + t * kTile16,
+                        k_lo + slot * kTile16, kHi, idesc_qk, bar_s + 8 * t);
       };
       // `steps` of 16 keys.
       auto issue_pv = [&](int t, int slot, bool acc, int steps) {
         const uint32_t b0 = v_lo + slot * kTile16;
         if (steps == kTN / 16) {
-#pragma unroll
-          for (int kk = 0; kk < kTN / 16; ++kk)
-            ptx::mma_ts_elect(tmem + kOCol + t * D, tmem + t * kTN + kk * 8,
-                              b0 + ((kk * 16 * 128) >> 4), kHi, idesc_pv,
-                              (acc || kk > 0) ? 1u : 0u);
+          issue_output(tm + kOCol + t * D, tm + t * kTN, b0, kHi, idesc_pv,
+                       acc ? 1u : 0u);
         } else {
 #pragma unroll 1
           for (int kk = 0; kk < steps; ++kk)
-            ptx::mma_ts_elect(tmem + kOCol + t * D, tmem + t * kTN + kk * 8,
+            ptx::mma_ts_elect(tm + kOCol + t * D, tm + t * kTN + kk * 8,
                               b0 + ((kk * 16 * 128) >> 4), kHi, idesc_pv,
                               (acc || kk > 0) ? 1u : 0u);
         }
       };
-      int it = 0;  // tiles consumed
-      int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+      // One copy of the code for both Q tiles and for a unit's first S: cold
+      // instructions cost a short launch's first steps 2 us a copy.
+      int slot = 0, phase = 0;  // of the ring's next tile
+      uint32_t q_parity = 0, p_parity = 0;  // bit t: of tile t's barriers
       int ends = 0;  // tiles cleared behind their last key
       bool issued = false;
       for (int k = 0; ok; ++k) {
@@ -672,71 +733,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int len = __reduce_max_sync(0xffffffffu, rec->len);
         if (n_kv == 0) break;
         release_unit(k);
-        ok = wait(bar_full + 8 * (it % L::kSlots), it / L::kSlots, 2);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int n = t ? n1 : n0;
-          if (!ok || n == 0) continue;
-          ok = wait(bar_q + 8 * t, q_uses[t], 2);
-          if (!ok) break;
-          ++q_uses[t];
-          ptx::tc_fence_after();
-          issue_qk(t, it % L::kSlots);
-          if (n == 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
-          issued = true;
-        }
-        if (!ok) break;
-        ptx::tc_commit_elect(bar_empty + 8 * (it % L::kSlots));
-        const int it0 = it;
-        for (int j = 0; j < n_kv && ok; ++j) {
-          const int it_v = it0 + 2 * j + 1, it_k = it0 + 2 * j + 2;
-          const int slot_v = it_v % L::kSlots, slot_k = it_k % L::kSlots;
-          bool own;
-          const int valid = tile_keys(j0 + j, np, plen, len, &own);
+        // Tiles that lengths end in: the prefix's last and the own last one.
+        const int end_p = np - 1 - j0, keys_p = plen - (np - 1) * kTN;
+        const int end_own = np + (len - 1) / kTN - j0;
+        const int keys_own = (len - 1) % kTN + 1;
+#pragma unroll 1
+        for (int j = -1; j < n_kv; ++j) {
+          // V_j lies in the slot ahead of K_j+1's.
+          const int slot_v = slot, phase_v = phase;
+          if (j >= 0 && ++slot == L::kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+          int valid = kTN;
+          bool clear = false, k_ready = false;
+          if (j >= 0) {
+            if (j == end_p) valid = keys_p;
+            if (j == end_own) valid = keys_own;
+            ok = wait(bar_full + 8 * slot_v, phase_v, 2);
+            if (!ok) break;
+            clear = valid % 16 != 0;
+            if (clear && lane == 0) ptx::mbar_arrive(bar_end);
+          }
           const int steps = (valid + 15) / 16;
-          ok = wait(bar_full + 8 * slot_v, it_v / L::kSlots, 2);
-          if (!ok) break;
-          bool clear = valid % 16 != 0;
-          if (clear && lane == 0) ptx::mbar_arrive(bar_end);
-          bool k_ready = false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int n = t ? n1 : n0;
-            if (!ok || j >= n) continue;
-            ok = wait(bar_p + 8 * t, p_uses[t], 2);
-            if (!ok) break;
-            ++p_uses[t];
-            if (clear) {
-              ok = wait(bar_cleared, ends++, 2);
+            if (j >= n || n == 0) continue;
+            if (j >= 0) {
+              ok = wait(bar_p + 8 * t, p_parity >> t, 2);
               if (!ok) break;
-              clear = false;
-            }
-            ptx::tc_fence_after();
-            issue_pv(t, slot_v, j > 0, steps);
-            if (j == n - 1) {
-              ptx::tc_commit_elect(bar_o + 8 * t);
-              continue;
+              p_parity ^= 1u << t;
+              if (clear) {
+                ok = wait(bar_cleared, ends++, 2);
+                if (!ok) break;
+                clear = false;
+              }
+              ptx::tc_fence_after();
+              issue_pv(t, slot_v, j > 0, steps);
+              if (j == n - 1) {
+                ptx::tc_commit_elect(bar_o + 8 * t);
+                continue;
+              }
+            } else {
+              ok = wait(bar_q + 8 * t, q_parity >> t, 2);
+              if (!ok) break;
+              q_parity ^= 1u << t;
             }
             if (!k_ready) {
-              ok = wait(bar_full + 8 * slot_k, it_k / L::kSlots, 2);
+              ok = wait(bar_full + 8 * slot, phase, 2);
               if (!ok) break;
               k_ready = true;
-              ptx::tc_fence_after();
             }
-            issue_qk(t, slot_k);
+            ptx::tc_fence_after();
+            issue_qk(t, slot);
+            issued = true;
             // Behind the tile's last S its query rows make room.
             if (j + 1 == n - 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
           }
           if (!ok) break;
-          ptx::tc_commit_elect(bar_empty + 8 * slot_v);
+          if (j >= 0) ptx::tc_commit_elect(bar_empty + 8 * slot_v);
           if (j + 1 < n_kv) {
             // (Where no Q tile sees the next keys, nobody waited for them.)
-            if (!k_ready) ok = wait(bar_full + 8 * slot_k, it_k / L::kSlots, 2);
+            if (!k_ready) ok = wait(bar_full + 8 * slot, phase, 2);
             if (!ok) break;
-            ptx::tc_commit_elect(bar_empty + 8 * slot_k);
+            ptx::tc_commit_elect(bar_empty + 8 * slot);
+            if (++slot == L::kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
           }
         }
-        it = it0 + 2 * n_kv;
       }
       if (!ok && issued) {  // the MMAs issued end before TMEM is released
         ptx::tc_commit_elect(bar_drain);
@@ -750,40 +817,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp / 4 - 1;
     const int r = threadIdx.x % kTM;  // row within the tile
     const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + t * kTN;
+    const uint32_t t_scores = tmem + lane_off + t * kTN;
     const uint32_t t_o = tmem + lane_off + kOCol + t * D;
     // Factor of the scores, held off 0 so that -inf stays -inf (scores times
     // 1e-37 vanish next to any maximum).
     const float c = fmaxf(p.scale_log2, 1e-37f);
     int s_uses = 0, o_uses = 0;
+    // Before the first scores a step is made of whatever O's columns hold, to
+    // no effect but that its instructions have been fetched (2.5 us of the
+    // first real step otherwise; the first products overwrite O).
+    int first = -1;
     for (int k = 0; ok; ++k) {
       volatile Record* rec = get_unit(k);
       if (rec == nullptr) break;
-      const int n = rec->n[t], j0 = rec->j0, np = rec->np;
-      const int plen = rec->plen, len = rec->len;
-      const int full = rec->full[t];
-      int vis = len;  // own keys that this row sees
+      const int n = rec->n[t];
+      // Keys left from the tile at hand on: of the prefix (none behind its
+      // tiles), and own ones that this row sees.
+      int left = 0, left_own;
       // A warp without rows keeps in step but computes nothing: its P are
       // whatever S left there, which reaches its own rows of O only.
       bool live;
       {
-        int row;
+        const int j0 = rec->j0, np = rec->np, len = rec->len;
+        int row, vis = len;
         const bool row_ok = row_of(p, rec, t, r, &row) >= 0;
         live = __any_sync(0xffffffffu, row_ok);
         if (rec->b >= 0 && row_ok) vis = row_end(p, len, rec->n_new, row);
+        if (np > 0) left = rec->plen - j0 * kTN;
+        left_own = vis - (j0 - np) * kTN;
       }
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < n; ++j) {
-        bool own;
-        int lim = tile_keys(j0 + j, np, plen, len, &own);
-        if (own && j0 + j - np >= full)
-          lim = min(lim, vis - (j0 + j - np) * kTN);
+      for (int j = first; j < n; ++j) {
+        const bool dry = j < 0;
+        const int lim = left > 0 ? left : left_own;
         const bool masked = __any_sync(0xffffffffu, lim < kTN);
-        ok = wait(bar_s + 8 * t, s_uses, 4);
-        if (!ok) break;
-        ++s_uses;
-        ptx::tc_fence_after();
+        if (!dry) {
+          left -= kTN;
+          left_own -= kTN;
+          ok = wait(bar_s + 8 * t, s_uses, 4);
+          if (!ok) break;
+          ++s_uses;
+          ptx::tc_fence_after();
+        }
+        const uint32_t t_s = dry ? t_o : t_scores;
         if (!live) {
+          if (dry) continue;
           ptx::tc_fence_before();
           ptx::mbar_arrive(bar_p + 8 * t);
           continue;
@@ -858,9 +936,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_st();
         l_run += (sm[0] + sm[1]) + (sm[2] + sm[3]);
         m_run = m_new;
+        if (dry) {
+          m_run = -INFINITY;
+          l_run = 0.f;
+          continue;
+        }
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar_p + 8 * t);
       }
+      first = 0;
       if (!ok) break;
       if (n > 0) {
         ok = wait(bar_o + 8 * t, o_uses, 4);

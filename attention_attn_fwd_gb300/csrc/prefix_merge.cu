@@ -8,7 +8,7 @@ namespace {
 
 using kv8::kNone;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 8;  // parts whose O a warp has in flight
 
@@ -18,53 +18,64 @@ struct Sum {
   float4 acc;
 };
 
-// Parts [s0, s1) by one warp, where at(s, &o) gives the LSE of part s and the
-// place of its O.  (O is read before its factor is known; a part that sees
-// nothing has the factor 0 and no O.)
+__device__ __forceinline__ void add(float4& acc, const float4& y, float f) {
+  if (f == 0.f) return;  // a part that sees nothing has no O
+  acc.x += y.x * f;
+  acc.y += y.y * f;
+  acc.z += y.z * f;
+  acc.w += y.w * f;
+}
+
+// Parts [s0, s1) by one warp, where at(s, &o, &lse2) gives the places of part
+// s's O and LSE.  (O is on its way before its factor is known.)
 template <int D, class At>
 __device__ __forceinline__ Sum add_parts(int s0, int s1, int lane, At at) {
   constexpr int kCols = D / 4;          // float4 columns
   constexpr int kGroups = 32 / kCols;   // parts a warp reads at a time
+  constexpr int kBatch = kAhead * kGroups;
   const int col = lane % kCols, sub = lane / kCols;
   Sum t{kNone, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   for (; s0 < s1; s0 += 32) {
     const int count = min(32, s1 - s0);
     const float4* o = nullptr;
     float x = -INFINITY;
-    if (lane < count) x = at(s0 + lane, &o);
-    const unsigned long long o_bits = reinterpret_cast<unsigned long long>(o);
-    float m = fmaxf(t.mx, x);
-#pragma unroll
-    for (int k = 16; k > 0; k /= 2)
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    const float before = ptx::ex2(t.mx - m);
-    const float f_all = ptx::ex2(x - m);
-    t.mx = m;
-    t.acc.x *= before;
-    t.acc.y *= before;
-    t.acc.z *= before;
-    t.acc.w *= before;
-    t.sum = t.sum * before + f_all;  // (a lane's share)
-    for (int k0 = 0; k0 < count; k0 += kAhead * kGroups) {
+    if (lane < count) {
+      const float* lse2;
+      at(s0 + lane, &o, &lse2);
+      x = *lse2;
+    }
+    const unsigned long long place = reinterpret_cast<unsigned long long>(o);
+    float f_all = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
       float4 y[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int k = k0 + i * kGroups + sub;
         const float4* from = reinterpret_cast<const float4*>(
-            __shfl_sync(0xffffffffu, o_bits, k % 32));
+            __shfl_sync(0xffffffffu, place, k % 32));
         y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k < count) y[i] = from[col];
+      }
+      if (k0 == 0) {
+        float m = fmaxf(t.mx, x);
+#pragma unroll
+        for (int k = 16; k > 0; k /= 2)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const float before = ptx::ex2(t.mx - m);
+        f_all = ptx::ex2(x - m);
+        t.mx = m;
+        t.acc.x *= before;
+        t.acc.y *= before;
+        t.acc.z *= before;
+        t.acc.w *= before;
+        t.sum = t.sum * before + f_all;  // (a lane's share)
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int k = k0 + i * kGroups + sub;
         const float f = __shfl_sync(0xffffffffu, f_all, k % 32);
-        if (k < count && f != 0.f) {
-          t.acc.x += y[i].x * f;
-          t.acc.y += y[i].y * f;
-          t.acc.z += y[i].z * f;
-          t.acc.w += y[i].w * f;
-        }
+        if (k < count) add(t.acc, y[i], f);
       }
     }
   }
@@ -99,7 +110,7 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, long long row,
 // kFew and kPacked: every row, with the parts over the prefix first, by
 // row_warps warps.
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 8)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p,
                         int row_warps) {
   __shared__ float2 sm_sum[kWarps];
@@ -116,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       : id < 0x7fffffff ? fast_div(static_cast<int>(id), p.fd_rows)
                         : static_cast<int>(id / R);
   const int r = in ? static_cast<int>(id - static_cast<long long>(bh) * R) : 0;
-  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int b = fast_div(bh, p.fd_hkv), h = bh - b * p.Hkv;
   const int len = kv8::seq_len(p, b), n_new = kv8::seq_new(p, b);
   const int np = prefix_tiles(p);
   // Its Q tiles over the prefix and over the own keys, and places in their
@@ -141,29 +152,29 @@ __global__ void __launch_bounds__(kThreads, 3)
                     static_cast<long long>(b) * p.row_blocks + u) * p.Hkv + h];
     }
   }
-  auto at = [&](int s, const float4** o) -> float {
-    const float *from = p.base_o, *lse2 = p.base_lse2;
+  auto at = [&](int s, const float4** o, const float** lse2) {
+    const float *from = p.base_o, *from2 = p.base_lse2;
     long long i;
     if (s == 0 && pre.y > 0) {
       i = h * all + static_cast<long long>(b) * R + r;
     } else if (s < pre.y) {
       from = p.slot_o;
-      lse2 = p.slot_lse2;
+      from2 = p.slot_lse2;
       i = static_cast<long long>(pre.x + s) * kUnitRows + in_unit;
     } else if (p.mode == kFew) {
       from = p.few_o;
-      lse2 = p.few_lse2;
+      from2 = p.few_lse2;
       i = (static_cast<long long>(own.x + s - pre.y) + bh) * few_rows(R) + r;
     } else if (s == pre.y) {
       i = p.Hkv * all + static_cast<long long>(bh) * R + r;
     } else {
       from = p.slot_o;
-      lse2 = p.slot_lse2;
+      from2 = p.slot_lse2;
       i = static_cast<long long>(own.x + s - pre.y) * kUnitRows +
           own_in_unit;
     }
     *o = reinterpret_cast<const float4*>(from) + i * (D / 4);
-    return lse2[i];
+    *lse2 = from2 + i;
   };
   const int n = pre.y + own.y, w = warp % row_warps;
   Sum t = add_parts<D>(n * w / row_warps, n * (w + 1) / row_warps, lane, at);
@@ -189,31 +200,69 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (live) write_row<D, kBF16>(p, q_row_index(p, b, h, r), t, lane);
 }
 
-// kJoint: the rows of each CTA's unit that went on behind it.
-constexpr int kParts = kUnitRows / kWarps;  // CTAs per unit
+// kJoint: the rows of each CTA's unit that went on behind it, four by a warp.
+constexpr int kJoinRows = 4;
+constexpr int kParts = kUnitRows / kWarps / kJoinRows;  // CTAs per unit
 
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     prefix_join_kernel(const __grid_constant__ PrefixParams p) {
+  constexpr int kCols = D / 4;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x / kParts;
-  const int i = (blockIdx.x - cta * kParts) * kWarps + warp;
+  const int i0 = ((blockIdx.x - cta * kParts) * kWarps + warp) * kJoinRows;
   kv8::start_after_previous();
   const int4 split = p.split[cta];
   const int b = split.x, h = split.y, parts = split.w;
   if (parts == 0) return;
-  const int tile = i / kTM, in_tile = i % kTM;
-  const int r = (2 * split.z + tile) * p.tile_rows + in_tile;
-  if (in_tile >= p.tile_rows || r >= kv8::seq_new(p, b) * p.group) return;
-  auto at = [&](int s, const float4** o) -> float {
-    const long long j =
-        static_cast<long long>(s == 0 ? p.grid + cta : cta + s) *
-            kUnitRows + i;
-    *o = reinterpret_cast<const float4*>(p.slot_o) + j * (D / 4);
-    return p.slot_lse2[j];
+  const int rows = kv8::seq_new(p, b) * p.group;
+  const int tile = i0 / kTM, in_tile = i0 % kTM;
+  const int r0 = (2 * split.z + tile) * p.tile_rows + in_tile;
+  const int n = min(kJoinRows, min(p.tile_rows - in_tile, rows - r0));
+  auto place = [&](int s, int i) {
+    return static_cast<long long>(s == 0 ? p.grid + cta : cta + s) *
+               kUnitRows + i;
   };
-  const Sum t = add_parts<D>(0, parts, lane, at);
-  write_row<D, kBF16>(p, q_row_index(p, b, h, r), t, lane);
+  if (parts == 2 && D == 128) {
+    // The usual case, all rows at once: lane 2 i + s has row i's part s.
+    float x = -INFINITY;
+    if (lane < 2 * n) x = p.slot_lse2[place(lane % 2, i0 + lane / 2)];
+    float4 y[kJoinRows][2];
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        y[i][s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n)
+          y[i][s] = reinterpret_cast<const float4*>(
+              p.slot_o)[place(s, i0 + i) * kCols + lane % kCols];
+      }
+    const float m = fmaxf(kNone, fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1)));
+    const float f = ptx::ex2(x - m);
+    const float sum = f + __shfl_xor_sync(0xffffffffu, f, 1);
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      Sum t;
+      t.mx = __shfl_sync(0xffffffffu, m, 2 * i);
+      t.sum = __shfl_sync(0xffffffffu, sum, 2 * i);
+      t.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        add(t.acc, y[i][s], __shfl_sync(0xffffffffu, f, 2 * i + s));
+      if (i < n)
+        write_row<D, kBF16>(p, q_row_index(p, b, h, r0 + i), t, lane);
+    }
+    return;
+  }
+  for (int i = 0; i < n; ++i) {
+    const Sum t = add_parts<D>(
+        0, parts, lane, [&](int s, const float4** o, const float** lse2) {
+          const long long j = place(s, i0 + i);
+          *o = reinterpret_cast<const float4*>(p.slot_o) + j * kCols;
+          *lse2 = p.slot_lse2 + j;
+        });
+    write_row<D, kBF16>(p, q_row_index(p, b, h, r0 + i), t, lane);
+  }
 }
 
 template <int D, bool kBF16>
