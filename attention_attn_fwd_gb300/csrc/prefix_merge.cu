@@ -8,8 +8,10 @@ namespace {
 
 using kv8::kNone;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kAhead = 8;  // parts whose O a warp has in flight
 
 // What a warp has of a row: the sum over its parts, relative to 2^mx.
@@ -110,7 +112,7 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, long long row,
 // kFew and kPacked: every row, with the parts over the prefix first, by
 // row_warps warps.
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads, 8)
+__global__ void __launch_bounds__(kThreads, 4)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p,
                         int row_warps) {
   __shared__ float2 sm_sum[kWarps];
@@ -202,15 +204,16 @@ __global__ void __launch_bounds__(kThreads, 8)
 
 // kJoint: the rows of each CTA's unit that went on behind it, four by a warp.
 constexpr int kJoinRows = 4;
-constexpr int kParts = kUnitRows / kWarps / kJoinRows;  // CTAs per unit
+constexpr int kParts = kUnitRows / kJoinWarps / kJoinRows;  // CTAs per unit
 
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads, 8)
+__global__ void __launch_bounds__(kJoinThreads, 8)
     prefix_join_kernel(const __grid_constant__ PrefixParams p) {
   constexpr int kCols = D / 4;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x / kParts;
-  const int i0 = ((blockIdx.x - cta * kParts) * kWarps + warp) * kJoinRows;
+  const int i0 =
+      ((blockIdx.x - cta * kParts) * kJoinWarps + warp) * kJoinRows;
   kv8::start_after_previous();
   const int4 split = p.split[cta];
   const int b = split.x, h = split.y, parts = split.w;
@@ -270,7 +273,7 @@ cudaError_t launch(PrefixParams p, cudaStream_t stream) {
   if (p.mode == kJoint)
     return kv8::launch_pdl(prefix_join_kernel<D, kBF16>,
                            static_cast<long long>(p.grid) * kParts,
-                           kThreads, 0, stream, p);
+                           kJoinThreads, 0, stream, p);
   const long long rows = static_cast<long long>(p.B) * p.rows * p.Hkv;
   // Warps a row: as many as make the machine's warps busy, rows having some 20
   // parts where they are few.

@@ -32,6 +32,11 @@ using kv8::start_after_previous;
 using kv8::unpack2;
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kRows = 8;       // rows of a group, all in flight at once
+constexpr int kRowsBwd = 4;    // of the backward's (two inputs each)
+constexpr int kHeadsBwd = 8;   // heads of a group
+constexpr int kFwdBlocks = 6;  // CTAs an SM holds
+constexpr int kBwdBlocks = 5;
 
 // What a lane holds of each row.
 template <int D, bool kInterleaved>
@@ -54,16 +59,6 @@ struct Lane {
     }
   }
 };
-
-// Numbers i and j of the lane's eight that pair e rotates.
-template <bool kInterleaved>
-__host__ __device__ constexpr int first_of(int e) {
-  return kInterleaved ? 2 * e : e;
-}
-template <bool kInterleaved>
-__host__ __device__ constexpr int second_of(int e) {
-  return kInterleaved ? 2 * e + 1 : e + 4;
-}
 
 // A token and what its rows need.
 struct Token {
@@ -119,37 +114,78 @@ __device__ __forceinline__ void turns(const RopeParams& p, const Token& k,
   }
 }
 
-template <bool kBF16>
-__device__ __forceinline__ void load8(const uint16_t* row, const int* at,
-                                      uint2* w) {
-  w[0] = __ldg(reinterpret_cast<const uint2*>(row + at[0]));
-  w[1] = __ldg(reinterpret_cast<const uint2*>(row + at[1]));
+// Two fp32 numbers and packed arithmetic on them.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 parts(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r.v)
+      : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 swapped(F2 a) {
+  const float2 p = parts(a);
+  return f2(p.y, p.x);
+}
+__device__ __forceinline__ F2 chosen(bool first, F2 a, F2 b) {
+  F2 r;
+  r.v = first ? a.v : b.v;
+  return r;
+}
+
+// A lane's eight numbers of a row as they lie in memory, and as fp32.
+struct Row {
+  uint2 w[2];
+};
+__device__ __forceinline__ Row load_row(const uint16_t* row, const int* at) {
+  Row r;
+  r.w[0] = __ldg(reinterpret_cast<const uint2*>(row + at[0]));
+  r.w[1] = __ldg(reinterpret_cast<const uint2*>(row + at[1]));
+  return r;
 }
 template <bool kBF16>
-__device__ __forceinline__ void widen(const uint2* w, float* x) {
+__device__ __forceinline__ void widen(const Row& r, F2* x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float2 a = unpack2<kBF16>(w[i].x), b = unpack2<kBF16>(w[i].y);
-    x[4 * i] = a.x;
-    x[4 * i + 1] = a.y;
-    x[4 * i + 2] = b.x;
-    x[4 * i + 3] = b.y;
+    const float2 a = unpack2<kBF16>(r.w[i].x), b = unpack2<kBF16>(r.w[i].y);
+    x[2 * i] = f2(a.x, a.y);
+    x[2 * i + 1] = f2(b.x, b.y);
   }
 }
 template <bool kBF16>
-__device__ __forceinline__ void store8(uint16_t* row, const int* at,
-                                       const float* x) {
+__device__ __forceinline__ void store_row(uint16_t* row, const int* at,
+                                          const F2* x) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    *reinterpret_cast<uint2*>(row + at[i]) =
-        make_uint2(ptx::pack2<kBF16>(x[4 * i], x[4 * i + 1]),
-                   ptx::pack2<kBF16>(x[4 * i + 2], x[4 * i + 3]));
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = parts(x[2 * i]), b = parts(x[2 * i + 1]);
+    *reinterpret_cast<uint2*>(row + at[i]) = make_uint2(
+        ptx::pack2<kBF16>(a.x, a.y), ptx::pack2<kBF16>(b.x, b.y));
+  }
 }
 
-// The lane's norm weights.
+// The lane's norm weights (1 without).
 template <bool kBF16>
 __device__ __forceinline__ void load_weights(const RopeParams& p, int kind,
                                              const int* at, float* w) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 1.f;
   if (p.w[kind] == nullptr) return;
   if (p.w_f32) {
     const float* f = static_cast<const float*>(p.w[kind]);
@@ -165,6 +201,48 @@ __device__ __forceinline__ void load_weights(const RopeParams& p, int kind,
   }
 }
 
+// The rotation of a lane's numbers n = x w by angles t as products with
+// factors made once: of pair (a, b) the turned ones are
+//   a w_a cos t - b w_b sin t,  b w_b cos t + a w_a sin t.
+// Packed, own[i] multiplies x[i] and other[i] the numbers that x[i]'s partners
+// are: x[i ^ 2], or neighbours with each other.
+struct Turn {
+  F2 own[4], other[4];
+};
+// sign: -1 turns back.
+template <bool kInterleaved>
+__device__ __forceinline__ Turn make_turn(const float* w, const float* c,
+                                          const float* s, float sign) {
+  Turn t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kInterleaved) {
+      const float u = sign * s[i];
+      t.own[i] = f2(w[2 * i] * c[i], w[2 * i + 1] * c[i]);
+      t.other[i] = f2(-w[2 * i + 1] * u, w[2 * i] * u);
+    } else {
+      const int e = 2 * (i % 2);  // first of its two pairs
+      const float u = i < 2 ? -sign : sign;
+      const float* v = i < 2 ? w + 4 : w;
+      t.own[i] = f2(w[2 * i] * c[e], w[2 * i + 1] * c[e + 1]);
+      t.other[i] = f2(u * v[e] * s[e], u * v[e + 1] * s[e + 1]);
+    }
+  }
+  return t;
+}
+// whole: every lane's numbers are rotated; turns: this lane's are.
+template <bool kInterleaved>
+__device__ __forceinline__ void rotate(const Turn& t, const F2* x, F2* y,
+                                       bool whole, bool turns) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const F2 o = mul(x[i], t.own[i]);
+    y[i] = fma(kInterleaved ? swapped(x[i]) : x[i ^ 2], t.other[i], o);
+    // (Not x + 0 * partner: an infinity would make that NaN.)
+    if (!whole) y[i] = chosen(turns, y[i], o);
+  }
+}
+
 template <int kLanes>
 __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
@@ -175,22 +253,22 @@ __device__ __forceinline__ float group_sum(float x) {
 // x becomes x f, and the row's norm factor is r f: f is 1 but for rows whose
 // squares pass fp32's largest number.  Returns r.
 template <int D>
-__device__ __forceinline__ float norm_factor(float* x, float eps, float* f) {
-  *f = 1.f;
-  float ss = 0.f;
+__device__ __forceinline__ float norm_factor(F2* x, float eps, float* f) {
+  auto squares = [&] {
+    F2 ss = mul(x[0], x[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = group_sum<D / 8>(ss);
+    for (int i = 1; i < 4; ++i) ss = fma(x[i], x[i], ss);
+    const float2 p = parts(ss);
+    return group_sum<D / 8>(p.x + p.y);
+  };
+  *f = 1.f;
+  float ss = squares();
   if (__any_sync(kFull, ss == INFINITY)) {
     const bool big = ss == INFINITY;
     if (big) *f = 0x1p-96f;
-    float again = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] *= *f;
-      again = fmaf(x[i], x[i], again);
-    }
-    again = group_sum<D / 8>(again);
+    for (int i = 0; i < 4; ++i) x[i] = mul(x[i], f2(*f, *f));
+    const float again = squares();
     if (big) {
       ss = again;
       eps = 0.f;
@@ -199,203 +277,193 @@ __device__ __forceinline__ float norm_factor(float* x, float eps, float* f) {
   return rsqrtf(fmaf(ss, 1.f / D, eps));
 }
 
-// The kind of a head (0 Q, 1 K, 2 V) in the list of all, and its number there.
-__device__ __forceinline__ int head_kind(const RopeParams& p, int h, int* at) {
-  const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
-  *at = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
-  return kind;
+// A block's heads: `count` of kind `kind` (0 Q, 1 K, 2 V) from `first` on.
+struct Heads {
+  int kind, first, count;
+};
+__device__ __forceinline__ Heads find_heads(const RopeParams& p, int y) {
+  Heads h;
+  h.kind = y < p.q_blocks ? 0 : y < p.q_blocks + p.kv_blocks ? 1 : 2;
+  if (h.kind > 0) y -= p.q_blocks + (h.kind - 1) * p.kv_blocks;
+  h.first = y * p.head_block;
+  h.count = min(p.head_block, (h.kind == 0 ? p.Hq : p.Hkv) - h.first);
+  return h;
 }
 
 // ---------------------------------------------------------------- forward
-constexpr int kAhead = 4;  // rows of a group in flight
-
 template <int D, bool kBF16, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads)
-    rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kFwdBlocks)
+    rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 8;
+  constexpr int kGroups = kThreads / kLanes;
   const Lane<D, kInterleaved> lane(threadIdx.x % kLanes, p.rot);
+  const int block = fast_div(blockIdx.x, p.fd_blocks);
+  const Heads h = find_heads(p, blockIdx.x - block * p.blocks);
   start_after_previous();
-  const Token k =
-      find_token(p, blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes);
-  const int h0 = blockIdx.y * p.head_block;
-  const int h1 = min(h0 + p.head_block, p.heads);
-
-  auto load = [&](int h, uint2* w) {
-    int at;
-    const int kind = head_kind(p, h, &at);
-    load8<kBF16>(p.x[kind] + k.b * p.x_b[kind] + k.s * p.x_s[kind] +
-                     at * p.x_h[kind],
-                 lane.at, w);
-  };
-  uint2 in[kAhead][2];
+  const Token k = find_token(p, block * kGroups + threadIdx.x / kLanes);
+  const uint16_t* x = p.x[h.kind] + k.b * p.x_b[h.kind] +
+                      k.s * p.x_s[h.kind] + h.first * p.x_h[h.kind];
+  // Every row of the group at once.
+  Row in[kRows];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    in[i][0] = in[i][1] = make_uint2(0u, 0u);
-    if (k.in && h0 + i < h1) load(h0 + i, in[i]);
+  for (int i = 0; i < kRows; ++i) {
+    in[i].w[0] = in[i].w[1] = make_uint2(0u, 0u);
+    if (k.in && i < h.count) in[i] = load_row(x + i * p.x_h[h.kind], lane.at);
   }
-  float wq[8], wk[8], c[4], s[4];
-  load_weights<kBF16>(p, 0, lane.at, wq);
-  load_weights<kBF16>(p, 1, lane.at, wk);
-  turns(p, k, lane.pair, c, s);
-
-  for (int h = h0; h < h1; h += kAhead) {
+  const int rows = h.kind == 0 ? p.S : p.capacity;
+  uint16_t* out =
+      p.y[h.kind] +
+      ((static_cast<long long>(k.b) * (h.kind == 0 ? p.Hq : p.Hkv) + h.first) *
+           rows + (h.kind == 0 ? k.s : k.row)) * D;
+  const long long step = static_cast<long long>(rows) * D;
+  if (h.kind == 2) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (h + i >= h1) break;
-      int at;
-      const int kind = head_kind(p, h + i, &at);
-      const int H = kind == 0 ? p.Hq : p.Hkv;
-      const int rows = kind == 0 ? p.S : p.capacity;
-      uint16_t* out =
-          p.y[kind] + ((static_cast<long long>(k.b) * H + at) * rows +
-                       (kind == 0 ? k.s : k.row)) * D;
-      if (kind == 2) {
-        if (k.in) {
-          *reinterpret_cast<uint2*>(out + lane.at[0]) = in[i][0];
-          *reinterpret_cast<uint2*>(out + lane.at[1]) = in[i][1];
-        }
-      } else {
-        float x[8], y[8];
-        widen<kBF16>(in[i], x);
-        if (p.w[kind] != nullptr) {
-          float f;
-          const float r = norm_factor<D>(x, p.eps, &f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= r * (kind == 0 ? wq[e] : wk[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int a = first_of<kInterleaved>(e);
-          const int b = second_of<kInterleaved>(e);
-          y[a] = x[a];
-          y[b] = x[b];
-          if (lane.pair >= 0) {
-            y[a] = x[a] * c[e] - x[b] * s[e];
-            y[b] = x[a] * s[e] + x[b] * c[e];
-          }
-        }
-        if (k.in) store8<kBF16>(out, lane.at, y);
-      }
-      if (k.in && h + i + kAhead < h1) load(h + i + kAhead, in[i]);
+    for (int i = 0; i < kRows; ++i) {
+      if (!k.in || i >= h.count) break;
+      *reinterpret_cast<uint2*>(out + i * step + lane.at[0]) = in[i].w[0];
+      *reinterpret_cast<uint2*>(out + i * step + lane.at[1]) = in[i].w[1];
     }
+    return;
+  }
+  Turn turn;
+  {
+    float w[8], c[4], s[4];
+    load_weights<kBF16>(p, h.kind, lane.at, w);
+    turns(p, k, lane.pair, c, s);
+    turn = make_turn<kInterleaved>(w, c, s, 1.f);
+  }
+  const bool norm = p.w[h.kind] != nullptr, whole = p.rot == D;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (i >= h.count) break;
+    F2 n[4], y[4];
+    widen<kBF16>(in[i], n);
+    if (norm) {
+      float f;
+      const float r = norm_factor<D>(n, p.eps, &f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) n[e] = mul(n[e], f2(r, r));
+    }
+    rotate<kInterleaved>(turn, n, y, whole, lane.pair >= 0);
+    if (k.in) store_row<kBF16>(out + i * step, lane.at, y);
   }
 }
 
 // --------------------------------------------------------------- backward
-constexpr int kAheadBwd = 2;
-
 template <int D, bool kBF16, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads)
-    rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks)
+    rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kThreads / kLanes;
   const int group = threadIdx.x / kLanes;
   const Lane<D, kInterleaved> lane(threadIdx.x % kLanes, p.rot);
+  const int stripe = fast_div(blockIdx.x, p.fd_blocks);
+  const int stripes = gridDim.x / p.blocks;
+  const int y_block = blockIdx.x - stripe * p.blocks;
+  const Heads h = find_heads(p, y_block);
   start_after_previous();
-  const int h0 = blockIdx.y * p.head_block;
-  const int h1 = min(h0 + p.head_block, p.heads);
-  float wq[8], wk[8], dwq[8], dwk[8];
+  const bool norm = h.kind < 2 && p.w[h.kind] != nullptr;
+  const bool whole = p.rot == D;
+  float w[8];
+  F2 dw[4];
+  if (h.kind < 2) load_weights<kBF16>(p, h.kind, lane.at, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-  load_weights<kBF16>(p, 0, lane.at, wq);
-  load_weights<kBF16>(p, 1, lane.at, wk);
+  for (int e = 0; e < 4; ++e) dw[e] = f2(0.f, 0.f);
 
-  const int blocks = (p.tokens + kGroups - 1) / kGroups;
-  for (int blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
+  const int token_blocks = (p.tokens + kGroups - 1) / kGroups;
+  const long long step = static_cast<long long>(p.S) * D;
+  for (int blk = stripe; blk < token_blocks; blk += stripes) {
     const Token k = find_token(p, blk * kGroups + group);
-    auto load = [&](int h, uint2* dy, uint2* x) {
-      int at;
-      const int kind = head_kind(p, h, &at);
-      const int H = kind == 0 ? p.Hq : p.Hkv;
-      load8<kBF16>(
-          p.y[kind] +
-              ((static_cast<long long>(k.b) * H + at) * p.S + k.s) * D,
-          lane.at, dy);
-      if (kind < 2 && p.w[kind] != nullptr)
-        load8<kBF16>(p.x[kind] + k.b * p.x_b[kind] + k.s * p.x_s[kind] +
-                         at * p.x_h[kind],
-                     lane.at, x);
+    const uint16_t* dy =
+        p.y[h.kind] +
+        ((static_cast<long long>(k.b) * (h.kind == 0 ? p.Hq : p.Hkv) +
+          h.first) * p.S + k.s) * D;
+    uint16_t* dx = p.dx[h.kind] + k.b * p.dx_b[h.kind] +
+                   k.s * p.dx_s[h.kind] + h.first * p.dx_h[h.kind];
+    const uint16_t* x = nullptr;
+    if (norm)
+      x = p.x[h.kind] + k.b * p.x_b[h.kind] + k.s * p.x_s[h.kind] +
+          h.first * p.x_h[h.kind];
+    Row gy[kRowsBwd], gx[kRowsBwd];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < kRowsBwd; ++i) {
+        gy[i].w[0] = gy[i].w[1] = gx[i].w[0] = gx[i].w[1] =
+            make_uint2(0u, 0u);
+        if (!k.in || i0 + i >= h.count) continue;
+        gy[i] = load_row(dy + (i0 + i) * step, lane.at);
+        if (norm) gx[i] = load_row(x + (i0 + i) * p.x_h[h.kind], lane.at);
+      }
     };
-    uint2 gy[kAheadBwd][2], gx[kAheadBwd][2];
+    load(0);
+    if (h.kind == 2) {
+      for (int i0 = 0; i0 < h.count; i0 += kRowsBwd) {
+        if (i0 > 0) load(i0);
 #pragma unroll
-    for (int i = 0; i < kAheadBwd; ++i) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) gy[i][j] = gx[i][j] = make_uint2(0u, 0u);
-      if (k.in && h0 + i < h1) load(h0 + i, gy[i], gx[i]);
+        for (int i = 0; i < kRowsBwd; ++i) {
+          if (!k.in || i0 + i >= h.count) break;
+          uint16_t* to = dx + (i0 + i) * p.dx_h[2];
+          *reinterpret_cast<uint2*>(to + lane.at[0]) = gy[i].w[0];
+          *reinterpret_cast<uint2*>(to + lane.at[1]) = gy[i].w[1];
+        }
+      }
+      continue;
     }
-    float c[4], s[4];
-    turns(p, k, lane.pair, c, s);
-    for (int h = h0; h < h1; h += kAheadBwd) {
+    Turn back;
+    {
+      float one[8], c[4], s[4];
 #pragma unroll
-      for (int i = 0; i < kAheadBwd; ++i) {
-        if (h + i >= h1) break;
-        int at;
-        const int kind = head_kind(p, h + i, &at);
-        uint16_t* out = p.dx[kind] + k.b * p.dx_b[kind] +
-                        k.s * p.dx_s[kind] + at * p.dx_h[kind];
-        if (kind == 2) {
-          if (k.in) {
-            *reinterpret_cast<uint2*>(out + lane.at[0]) = gy[i][0];
-            *reinterpret_cast<uint2*>(out + lane.at[1]) = gy[i][1];
-          }
-        } else {
-          float dy[8], dn[8];
-          widen<kBF16>(gy[i], dy);
+      for (int e = 0; e < 8; ++e) one[e] = 1.f;
+      turns(p, k, lane.pair, c, s);
+      back = make_turn<kInterleaved>(one, c, s, -1.f);
+    }
+    for (int i0 = 0; i0 < h.count; i0 += kRowsBwd) {
+      if (i0 > 0) load(i0);
+#pragma unroll
+      for (int i = 0; i < kRowsBwd; ++i) {
+        if (i0 + i >= h.count) break;
+        F2 d[4], g[4];
+        widen<kBF16>(gy[i], d);
+        rotate<kInterleaved>(back, d, g, whole, lane.pair >= 0);
+        if (norm) {
+          F2 n[4];
+          widen<kBF16>(gx[i], n);
+          float f;
+          const float r = norm_factor<D>(n, p.eps, &f);
+          F2 sum = f2(0.f, 0.f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int a = first_of<kInterleaved>(e);
-            const int b = second_of<kInterleaved>(e);
-            dn[a] = dy[a];
-            dn[b] = dy[b];
-            if (lane.pair >= 0) {
-              dn[a] = dy[a] * c[e] + dy[b] * s[e];
-              dn[b] = dy[b] * c[e] - dy[a] * s[e];
-            }
+            n[e] = mul(n[e], f2(r, r));  // x^
+            dw[e] = fma(g[e], n[e], dw[e]);
+            g[e] = mul(g[e], f2(w[2 * e], w[2 * e + 1]));
+            sum = fma(g[e], n[e], sum);
           }
-          if (p.w[kind] != nullptr) {
-            float x[8];
-            widen<kBF16>(gx[i], x);
-            float f, dot = 0.f;
-            const float r = norm_factor<D>(x, p.eps, &f);
+          const float2 both = parts(sum);
+          const float mean = group_sum<kLanes>(both.x + both.y) * (-1.f / D);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] *= r;  // x^
-              const float add = dn[e] * x[e];
-              if (kind == 0)
-                dwq[e] += add;
-              else
-                dwk[e] += add;
-              dn[e] *= kind == 0 ? wq[e] : wk[e];
-              dot = fmaf(dn[e], x[e], dot);
-            }
-            dot = group_sum<kLanes>(dot) * (1.f / D);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dn[e] = r * f * (dn[e] - x[e] * dot);
-          }
-          if (k.in) store8<kBF16>(out, lane.at, dn);
+          for (int e = 0; e < 4; ++e)
+            g[e] = mul(fma(n[e], f2(mean, mean), g[e]), f2(r * f, r * f));
         }
-        if (k.in && h + i + kAheadBwd < h1)
-          load(h + i + kAheadBwd, gy[i], gx[i]);
+        if (k.in) store_row<kBF16>(dx + (i0 + i) * p.dx_h[h.kind], lane.at, g);
       }
     }
   }
-  if (p.w[0] == nullptr && p.w[1] == nullptr) return;
+  if (!norm) return;
   // The CTA's sums over its groups, in their order.
   __shared__ float sums[kGroups][D];
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = parts(dw[e]);
+    float* at = &sums[group][lane.at[e / 2] + 2 * (e % 2)];
+    at[0] = v.x;
+    at[1] = v.y;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += kThreads) {
+    float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      sums[group][lane.at[e / 4] + e % 4] = kind == 0 ? dwq[e] : dwk[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float sum = 0.f;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) sum += sums[g][threadIdx.x];
-      const int cta = blockIdx.y * gridDim.x + blockIdx.x;
-      p.part[(2LL * cta + kind) * D + threadIdx.x] = sum;
-    }
-    __syncthreads();
+    for (int g = 0; g < kGroups; ++g) sum += sums[g][i];
+    p.part[(static_cast<long long>(y_block) * stripes + stripe) * D + i] = sum;
   }
 }
 
@@ -404,73 +472,75 @@ constexpr int kSumThreads = 1024;
 
 __global__ void __launch_bounds__(kSumThreads)
     rope_dw_kernel(const float* part, float* dwq, float* dwk, int D,
-                   int ctas) {
+                   int q_ctas, int kv_ctas) {
   __shared__ float sums[32][33];
   start_after_previous();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int col = blockIdx.x * 32 + lane;
+  const int kind = blockIdx.x / (D / 32);
+  const int col = blockIdx.x % (D / 32) * 32 + lane;
+  float* out = kind == 0 ? dwq : dwk;
+  if (out == nullptr) return;
+  const int first = kind == 0 ? 0 : q_ctas;
+  const int count = kind == 0 ? q_ctas : kv_ctas;
   float sum = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < ctas; i += 32) sum += part[2LL * i * D + col];
+#pragma unroll 8
+  for (int i = warp; i < count; i += 32)
+    sum += part[static_cast<long long>(first + i) * D + col];
   sums[warp][lane] = sum;
   __syncthreads();
   if (warp != 0) return;
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) sum += sums[i][lane];
-  float* out = col < D ? dwq : dwk;
-  if (out != nullptr) out[col % D] = sum;
+  out[col] = sum;
 }
 
-template <class Kernel, class... Args>
-cudaError_t launch_grid(Kernel kernel, dim3 grid, cudaStream_t stream,
-                        Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// Heads that a group of lanes takes.
-int pick_head_block(const RopeParams& p, int groups, int sms) {
-  const long long blocks = (p.tokens + groups - 1) / groups;
-  int block = p.heads;
-  while (block > kAhead &&
-         blocks * ((p.heads + block - 1) / block) < 8LL * sms)
-    block = (block + 1) / 2;
-  return std::max(block, (p.heads + kMaxHeadBlocks - 1) / kMaxHeadBlocks);
+// Cuts the heads into blocks of head_block.
+void cut_heads(RopeParams* p, int head_block) {
+  const bool values = p->heads > p->Hq + p->Hkv;
+  p->head_block = head_block;
+  p->q_blocks = (p->Hq + head_block - 1) / head_block;
+  p->kv_blocks = (p->Hkv + head_block - 1) / head_block;
+  p->blocks = p->q_blocks + p->kv_blocks * (values ? 2 : 1);
+  p->fd_blocks = make_fast_div(p->blocks);
 }
 
 template <int D, bool kBF16, bool kInterleaved>
 cudaError_t launch_fwd(RopeParams p, int sms, cudaStream_t stream) {
   constexpr int kGroups = kThreads / (D / 8);
-  p.head_block = pick_head_block(p, kGroups, sms);
-  const dim3 grid((p.tokens + kGroups - 1) / kGroups,
-                  (p.heads + p.head_block - 1) / p.head_block);
-  return launch_grid(rope_kernel<D, kBF16, kInterleaved>, grid, stream, p);
+  const long long token_blocks = (p.tokens + kGroups - 1LL) / kGroups;
+  // Fewer heads a group where these would not fill the machine.
+  int head_block = kRows;
+  cut_heads(&p, head_block);
+  while (head_block > 1 && token_blocks * p.blocks < 2LL * sms)
+    cut_heads(&p, head_block /= 2);
+  const long long grid = token_blocks * p.blocks;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_pdl(rope_kernel<D, kBF16, kInterleaved>, grid, kThreads, 0,
+                    stream, p);
 }
 
 template <int D, bool kBF16, bool kInterleaved>
 cudaError_t launch_bwd(RopeParams p, int sms, cudaStream_t stream) {
   constexpr int kGroups = kThreads / (D / 8);
-  p.head_block = pick_head_block(p, kGroups, sms);
-  const int ny = (p.heads + p.head_block - 1) / p.head_block;
-  const int nx = std::min((p.tokens + kGroups - 1) / kGroups,
-                     bwd_ctas(sms) / ny);
+  const int token_blocks = (p.tokens + kGroups - 1) / kGroups;
+  int head_block = kHeadsBwd;
+  cut_heads(&p, head_block);
+  while (head_block > 1 &&
+         static_cast<long long>(token_blocks) * p.blocks < 2LL * sms)
+    cut_heads(&p, head_block /= 2);
+  // (Each CTA of Q and K leaves a row of sums.)
+  while (p.blocks > bwd_ctas(sms)) cut_heads(&p, head_block *= 2);
+  const int stripes = std::min(token_blocks, bwd_ctas(sms) / p.blocks);
   cudaError_t err =
-      launch_grid(rope_bwd_kernel<D, kBF16, kInterleaved>, dim3(nx, ny),
-                  stream, p);
+      launch_pdl(rope_bwd_kernel<D, kBF16, kInterleaved>,
+                 static_cast<long long>(stripes) * p.blocks, kThreads, 0,
+                 stream, p);
   if (err != cudaSuccess || (p.w[0] == nullptr && p.w[1] == nullptr))
     return err;
   return launch_pdl(rope_dw_kernel, 2 * D / 32, kSumThreads, 0, stream,
                     static_cast<const float*>(p.part), p.dw[0], p.dw[1], D,
-                    nx * ny);
+                    p.q_blocks * stripes, p.kv_blocks * stripes);
 }
 
 template <int D>

@@ -244,7 +244,7 @@ int current_sms() {
 }
 
 size_t bwd_workspace(int sms, int D) {
-  return static_cast<size_t>(attn::rope::bwd_ctas(sms)) * 2 * D * 4;
+  return static_cast<size_t>(attn::rope::bwd_ctas(sms)) * D * 4;
 }
 
 attn_status_t bwd_impl(const attn_rope_t* rope, const void* dq, const void* dk,

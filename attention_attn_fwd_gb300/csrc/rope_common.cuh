@@ -6,10 +6,12 @@
 
 #include <cuda_runtime.h>
 
+#include "fast_div.h"
+
 namespace attn {
 namespace rope {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct RopeParams {
   // Rotation: angle of pair i = position on axis axis[i] times phase[i], in
@@ -30,11 +32,13 @@ struct RopeParams {
   long long dx_b[3], dx_s[3], dx_h[3];
   const void* w[2];                 // norm weights, or nullptr: no norm
   float* dw[2];
-  float* part;                      // backward: [CTAs, 2, D]
+  float* part;                      // backward: [CTAs, D]
   unsigned int* status;
   int B, S, tokens;                 // tokens: B * S
   int Hq, Hkv, heads;               // heads: of Q, K and (if given) V
-  int head_block;                   // heads of a group of lanes
+  int head_block;                   // heads of a group of lanes, all of a kind
+  int q_blocks, kv_blocks, blocks;  // blocks of heads: Q's, K's, all
+  FastDiv fd_blocks;
   int capacity;                     // rows of a head of y[1] and y[2]
   int rot, w_f32;
   float eps;
@@ -45,12 +49,8 @@ cudaError_t launch_rope(int D, bool bf16, bool interleaved,
                         const RopeParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_rope_bwd(int D, bool bf16, bool interleaved,
                             const RopeParams& p, int sms, cudaStream_t stream);
-// Blocks of heads at most, and CTAs of a backward launch (each leaves a row of
-// partial sums).
-constexpr int kMaxHeadBlocks = 1024;
-constexpr int bwd_ctas(int sms) {
-  return 8 * sms > kMaxHeadBlocks ? 8 * sms : kMaxHeadBlocks;
-}
+// CTAs of a backward launch at most (each leaves a row of partial sums).
+constexpr int bwd_ctas(int sms) { return 10 * sms; }
 
 }  // namespace rope
 }  // namespace attn
