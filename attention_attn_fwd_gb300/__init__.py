@@ -13,6 +13,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 
 __all__ = [
@@ -82,10 +83,8 @@ class _RopeStruct(ctypes.Structure):
         (n, ctypes.c_int) for n in ("D", "rot", "axes", "interleaved")]
 
 
-class _Heads(ctypes.Structure):
-    """attn_heads_t of include/attn.h."""
-    _fields_ = [("p", ctypes.c_void_p)] + [
-        (n, ctypes.c_longlong) for n in ("stride_b", "stride_s", "stride_h")]
+# attn_heads_t of include/attn.h: pointer, stride_b, stride_s, stride_h.
+_heads = struct.Struct("@Pqqq").pack
 
 
 class _Prefix(ctypes.Structure):
@@ -178,7 +177,8 @@ def load_library():
         lib.attn_kv8_workspace_bytes.restype = sz
         lib.attn_kv8_evict.argtypes = [cp, cp, vp, vp, i, i, vp, vp]
         lib.attn_kv8_evict.restype = i
-        rp, hp = ctypes.POINTER(_RopeStruct), ctypes.POINTER(_Heads)
+        # (attn_heads_t's are handed over as their packed bytes.)
+        rp, hp = ctypes.POINTER(_RopeStruct), ctypes.c_char_p
         lib.attn_rope_phase.argtypes = [ctypes.POINTER(ctypes.c_double), i,
                                         ctypes.POINTER(ctypes.c_ulonglong)]
         lib.attn_rope_phase.restype = i
@@ -431,7 +431,7 @@ def attn_qk_rope(rope, q, k, v, q_weight, k_weight, weight_f32, eps,
     """Raw C-ABI call; ``rope`` is a ``Rope``, q, k, v are (pointer, stride_b,
     stride_s, stride_h) or None, other pointers integers."""
     return int(load_library().attn_qk_rope(
-        rope.struct, *[_Heads(*x) if x else None for x in (q, k, v)],
+        rope.struct, *[_heads(*x) if x else None for x in (q, k, v)],
         q_weight or None, k_weight or None, int(weight_f32), float(eps),
         positions or None, lens or None, new_lens or None, offset or None,
         q_out or None, k_out or None, v_out or None, B, S, Hq, Hkv, capacity,
@@ -443,7 +443,7 @@ def attn_qk_rope_bwd(rope, dq_out, dk_out, dv_out, q, k, q_weight, k_weight,
                      dq_weight, dk_weight, B, S, Hq, Hkv, dtype, workspace,
                      workspace_bytes, stream) -> int:
     """Raw C-ABI call; arguments like those of ``attn_qk_rope``."""
-    view = [_Heads(*x) if x else None for x in (q, k, dq, dk, dv)]
+    view = [_heads(*x) if x else None for x in (q, k, dq, dk, dv)]
     return int(load_library().attn_qk_rope_bwd(
         rope.struct, dq_out or None, dk_out or None, dv_out or None,
         view[0], view[1], q_weight or None, k_weight or None, int(weight_f32),
@@ -979,7 +979,7 @@ class Rope:
         signed = [x - (1 << 64) if x >> 63 else x for x in phase]
         self.phase = torch.tensor(signed, dtype=torch.int64, device=dev)
         self.axis = torch.tensor(axes, dtype=torch.uint8, device=dev)
-        self.D, self.rot = D, 2 * len(freq)
+        self.D, self.rot, self.weight_shape = D, 2 * len(freq), (D,)
         self.axes = max(axes, default=0) + 1
         self.interleaved = bool(interleaved)
         self.device = self.phase.device
@@ -1006,35 +1006,36 @@ class Rope:
                    axes, interleaved, device)
 
 
-def _heads_view(name, t, B, S, H, D, dtype):
+def _heads_view(name, t, shape, dtype):
     """attn_heads_t of a [B, S, H, D] tensor of any strides but the last."""
-    if t.shape != (B, S, H, D) or t.dtype is not dtype:
+    if t.dtype is not dtype or t.shape != shape:
         raise AttnError("%s must be %s of %s, got %s of %s" % (
-            name, [B, S, H, D], dtype, list(t.shape), t.dtype),
+            name, list(shape), dtype, list(t.shape), t.dtype),
             ATTN_ERR_INVALID_ARG)
     b, s, h, d = t.stride()
     if d != 1:
         raise AttnError("%s's last dimension must be contiguous" % name,
                         ATTN_ERR_INVALID_ARG)
-    return _Heads(t.data_ptr(), b, s, h)
+    return _heads(t.data_ptr(), b, s, h)
 
 
 def _rope_weights(rope, q_weight, k_weight, dtype):
     """(pointer, pointer, whether float32) of the norms' weights."""
-    out, f32 = [None, None], None
-    for i, w in enumerate((q_weight, k_weight)):
+    wt = None
+    for w in (q_weight, k_weight):
         if w is None:
             continue
-        if w.shape != (rope.D,) or not w.is_contiguous() or \
-                w.dtype not in (dtype, rope.float32):
+        if w.shape != rope.weight_shape or not w.is_contiguous() or \
+                (w.dtype is not dtype and w.dtype is not rope.float32):
             raise AttnError("weights must be contiguous [%d] of %s or float32"
                             % (rope.D, dtype), ATTN_ERR_INVALID_ARG)
-        if f32 not in (None, w.dtype is rope.float32):
+        if wt is not None and w.dtype is not wt:
             raise AttnError("both weights must be of one type",
                             ATTN_ERR_INVALID_ARG)
-        f32 = w.dtype is rope.float32
-        out[i] = w.data_ptr()
-    return out[0], out[1], bool(f32)
+        wt = w.dtype
+    return (None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(),
+            wt is rope.float32)
 
 
 def _rope_positions(rope, positions, B, S):
@@ -1045,6 +1046,15 @@ def _rope_positions(rope, positions, B, S):
     else:
         _check_tensor("positions", positions, (B, S), rope.int32)
     return positions.data_ptr()
+
+
+def _counts(rope, name, t, n):
+    """Pointer of an int32 [n] tensor, or None."""
+    if t is None:
+        return None
+    if t.dtype is not rope.int32 or t.shape != (n,) or not t.is_contiguous():
+        _check_tensor(name, t, (n,), rope.int32)
+    return t.data_ptr()
 
 
 def _rope_dtype(rope, name, t):
@@ -1079,15 +1089,11 @@ def qk_rope(rope, q, k, v=None, q_weight=None, k_weight=None, eps=1e-6,
     dtype, D = q.dtype, rope.D
     B, S, Hq, _ = q.shape
     Hkv = k.shape[2] if k.dim() == 4 else 0
-    heads = [_heads_view("q", q, B, S, Hq, D, dtype),
-             _heads_view("k", k, B, S, Hkv, D, dtype),
-             None if v is None else _heads_view("v", v, B, S, Hkv, D, dtype)]
+    shape = (B, S, Hkv, D)
+    hq = _heads_view("q", q, (B, S, Hq, D), dtype)
+    hk = _heads_view("k", k, shape, dtype)
+    hv = None if v is None else _heads_view("v", v, shape, dtype)
     wq, wk, f32 = _rope_weights(rope, q_weight, k_weight, dtype)
-    pos = _rope_positions(rope, positions, B, S)
-    for name, t, n in (("lens", lens, B), ("new_lens", new_lens, B),
-                       ("offset", offset, 1)):
-        if t is not None:
-            _check_tensor(name, t, (n,), rope.int32)
     if q_out is None or k_out is None or (v_out is None and v is not None):
         if lens is not None and (k_out is None or
                                  (v_out is None and v is not None)):
@@ -1104,17 +1110,20 @@ def qk_rope(rope, q, k, v=None, q_weight=None, k_weight=None, eps=1e-6,
             if v_out is None and v is not None:
                 v_out = torch.empty_like(k_out)
     cap = k_out.shape[2] if k_out.dim() == 4 else 0
+    shape = (B, Hkv, cap, D)
     _check_tensor("q_out", q_out, (B, Hq, S, D), dtype)
-    _check_tensor("k_out", k_out, (B, Hkv, cap, D), dtype)
-    if v is not None:
-        _check_tensor("v_out", v_out, (B, Hkv, cap, D), dtype)
-    _kv8_call("attn_qk_rope", rope.lib.attn_qk_rope, rope, stream, *heads, wq,
-              wk, f32, eps, pos,
-              None if lens is None else lens.data_ptr(),
-              None if new_lens is None else new_lens.data_ptr(),
-              None if offset is None else offset.data_ptr(),
-              q_out.data_ptr(), k_out.data_ptr(),
-              None if v is None else v_out.data_ptr(), B, S, Hq, Hkv, cap, dt)
+    _check_tensor("k_out", k_out, shape, dtype)
+    if v is None:
+        to_v = None
+    else:
+        _check_tensor("v_out", v_out, shape, dtype)
+        to_v = v_out.data_ptr()
+    _kv8_call("attn_qk_rope", rope.lib.attn_qk_rope, rope, stream, hq, hk, hv,
+              wq, wk, f32, eps, _rope_positions(rope, positions, B, S),
+              _counts(rope, "lens", lens, B),
+              _counts(rope, "new_lens", new_lens, B),
+              _counts(rope, "offset", offset, 1), q_out.data_ptr(),
+              k_out.data_ptr(), to_v, B, S, Hq, Hkv, cap, dt)
     return q_out, k_out, v_out
 
 
@@ -1140,60 +1149,55 @@ def qk_rope_bwd(rope, dq, dk, q=None, k=None, dv=None, q_weight=None,
     None.  ``workspace``: from ``qk_rope_bwd_workspace``, allocated when not
     given.
     """
-    import torch
     dt = _rope_dtype(rope, "dq", dq)
     dtype, D = dq.dtype, rope.D
     B, Hq, S, _ = dq.shape
     Hkv = dk.shape[1] if dk.dim() == 4 else 0
     _check_tensor("dq", dq, (B, Hq, S, D), dtype)
-    _check_tensor("dk", dk, (B, Hkv, S, D), dtype)
+    shape = (B, Hkv, S, D)
+    _check_tensor("dk", dk, shape, dtype)
     if dv is not None:
-        _check_tensor("dv", dv, (B, Hkv, S, D), dtype)
+        _check_tensor("dv", dv, shape, dtype)
     wq, wk, f32 = _rope_weights(rope, q_weight, k_weight, dtype)
-    pos = _rope_positions(rope, positions, B, S)
-    if offset is not None:
-        _check_tensor("offset", offset, (1,), rope.int32)
-    x = [None, None]
-    for i, (name, t, w, H) in enumerate((("q", q, wq, Hq), ("k", k, wk, Hkv))):
-        if w is None:
-            continue
-        if t is None:
-            raise AttnError("%s was normed and must be given" % name,
-                            ATTN_ERR_INVALID_ARG)
-        x[i] = _heads_view(name, t, B, S, H, D, dtype)
-    with _kv8_memory(rope, stream):
-        if dq_out is None:
-            dq_out = torch.empty((B, S, Hq, D), dtype=dtype,
-                                 device=rope.device)
-        if dk_out is None:
-            dk_out = torch.empty((B, S, Hkv, D), dtype=dtype,
-                                 device=rope.device)
-        if dv is None:
-            dv_out = None
-        elif dv_out is None:
-            dv_out = torch.empty((B, S, Hkv, D), dtype=dtype,
-                                 device=rope.device)
-        dw = [dq_weight, dk_weight]
-        for i, w in enumerate((wq, wk)):
-            if w is None:
-                dw[i] = None
-            elif dw[i] is None:
-                dw[i] = torch.empty(D, dtype=torch.float32,
-                                    device=rope.device)
-            else:
-                _check_tensor("weights' gradients", dw[i], (D,), rope.float32)
-        if workspace is None and (wq or wk):
-            workspace = qk_rope_bwd_workspace(rope)
+    if (q is None and wq is not None) or (k is None and wk is not None):
+        raise AttnError("what was normed must be given", ATTN_ERR_INVALID_ARG)
+    q_shape, k_shape = (B, S, Hq, D), (B, S, Hkv, D)
+    hq = None if wq is None else _heads_view("q", q, q_shape, dtype)
+    hk = None if wk is None else _heads_view("k", k, k_shape, dtype)
+    dw = [None if wq is None else dq_weight, None if wk is None else dk_weight]
+    if dq_out is None or dk_out is None or (dv is not None and dv_out is None) \
+            or (dw[0] is None and wq) or (dw[1] is None and wk) or \
+            (workspace is None and (wq or wk)):
+        import torch
+        with _kv8_memory(rope, stream):
+            if dq_out is None:
+                dq_out = torch.empty(q_shape, dtype=dtype, device=rope.device)
+            if dk_out is None:
+                dk_out = torch.empty(k_shape, dtype=dtype, device=rope.device)
+            if dv is not None and dv_out is None:
+                dv_out = torch.empty(k_shape, dtype=dtype, device=rope.device)
+            for i, w in enumerate((wq, wk)):
+                if w and dw[i] is None:
+                    dw[i] = torch.empty(D, dtype=torch.float32,
+                                        device=rope.device)
+            if workspace is None and (wq or wk):
+                workspace = qk_rope_bwd_workspace(rope)
+    for w in dw:
+        if w is not None:
+            _check_tensor("weights' gradients", w, (D,), rope.float32)
     if workspace is not None and not workspace.is_contiguous():
         raise AttnError("workspace must be contiguous", ATTN_ERR_INVALID_ARG)
-    out = [_heads_view("dq_out", dq_out, B, S, Hq, D, dtype),
-           _heads_view("dk_out", dk_out, B, S, Hkv, D, dtype),
-           None if dv is None else
-           _heads_view("dv_out", dv_out, B, S, Hkv, D, dtype)]
+    if dv is None:
+        dv_out = from_v = to_v = None
+    else:
+        from_v = dv.data_ptr()
+        to_v = _heads_view("dv_out", dv_out, k_shape, dtype)
     _kv8_call("attn_qk_rope_bwd", rope.lib.attn_qk_rope_bwd, rope, stream,
-              dq.data_ptr(), dk.data_ptr(),
-              None if dv is None else dv.data_ptr(), *x, wq, wk, f32, eps, pos,
-              None if offset is None else offset.data_ptr(), *out,
+              dq.data_ptr(), dk.data_ptr(), from_v, hq, hk, wq, wk, f32, eps,
+              _rope_positions(rope, positions, B, S),
+              _counts(rope, "offset", offset, 1),
+              _heads_view("dq_out", dq_out, q_shape, dtype),
+              _heads_view("dk_out", dk_out, k_shape, dtype), to_v,
               None if dw[0] is None else dw[0].data_ptr(),
               None if dw[1] is None else dw[1].data_ptr(), B, S, Hq, Hkv, dt,
               None if workspace is None else workspace.data_ptr(),

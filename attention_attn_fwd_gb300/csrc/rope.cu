@@ -35,7 +35,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 8;       // rows of a group, all in flight at once
 constexpr int kRowsBwd = 4;    // of the backward's (two inputs each)
 constexpr int kHeadsBwd = 8;   // heads of a group
-constexpr int kFwdBlocks = 6;  // CTAs an SM holds
+// CTAs an SM holds.
+constexpr int fwd_blocks(int D) { return D == 128 ? 8 : 7; }
 constexpr int kBwdBlocks = 5;
 
 // What a lane holds of each row.
@@ -292,7 +293,7 @@ __device__ __forceinline__ Heads find_heads(const RopeParams& p, int y) {
 
 // ---------------------------------------------------------------- forward
 template <int D, bool kBF16, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, kFwdBlocks)
+__global__ void __launch_bounds__(kThreads, fwd_blocks(D))
     rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kThreads / kLanes;

@@ -55,14 +55,15 @@ def rope(**kw):
 def view(p, S, H, D=64, **kw):
     a = dict(p=p, stride_b=S * H * D, stride_s=H * D, stride_h=D)
     a.update(kw)
-    return attn._Heads(*[a[n] for n, _ in attn._Heads._fields_])
+    return attn._heads(a["p"] or 0, a["stride_b"], a["stride_s"],
+                       a["stride_h"])
 
 
 def fwd(lib, r=None, q={}, k={}, v={}, wq=None, wk=None, f32=0, eps=1e-6,
         pos=None, lens=None, new=None, off=None, qo=64 * MB, ko=65 * MB,
         vo=66 * MB, B=2, S=4, Hq=4, Hkv=2, cap=4, dtype=BF16):
     r = rope() if r is None else r
-    views = [x if x is None or isinstance(x, attn._Heads) else
+    views = [x if x is None or isinstance(x, bytes) else
              view(**{**dict(p=p, S=S, H=H), **x}) for x, p, H in (
                  (q, 16 * MB, 4), (k, 17 * MB, 2), (v, 18 * MB, 2))]
     return lib.attn_qk_rope(ctypes.byref(r), *views, wq, wk, f32, eps, pos,
@@ -75,7 +76,7 @@ def bwd(lib, r=None, dq=16 * MB, dk=17 * MB, dv=18 * MB, q={}, k={}, wq=20 * MB,
         dxv={}, dwq=22 * MB, dwk=23 * MB, B=2, S=4, Hq=4, Hkv=2, dtype=BF16,
         ws=32 * MB, ws_bytes=16 * MB):
     r = rope() if r is None else r
-    views = [x if x is None or isinstance(x, attn._Heads) else
+    views = [x if x is None or isinstance(x, bytes) else
              view(**{**dict(p=p, S=S, H=H), **x}) for x, p, H in (
                  (q, 24 * MB, 4), (k, 25 * MB, 2), (dxq, 64 * MB, 4),
                  (dxk, 65 * MB, 2), (dxv, 66 * MB, 2))]
