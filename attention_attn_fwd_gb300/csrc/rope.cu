@@ -33,11 +33,11 @@ using kv8::unpack2;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 8;       // rows of a group, all in flight at once
-constexpr int kRowsBwd = 4;    // of the backward's (two inputs each)
+constexpr int kStagesBwd = 4;  // the backward's ring: rows of a group
 constexpr int kHeadsBwd = 8;   // heads of a group
 // CTAs an SM holds.
 constexpr int fwd_blocks(int D) { return D == 128 ? 8 : 7; }
-constexpr int kBwdBlocks = 5;
+constexpr int kBwdBlocks = 6;
 
 // What a lane holds of each row.
 template <int D, bool kInterleaved>
@@ -351,6 +351,24 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks(D))
 }
 
 // --------------------------------------------------------------- backward
+// 16-byte asynchronous copy; zeros, and nothing read, unless `in`.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src,
+                                       bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ Row shared_row(uint32_t row, const int* at) {
+  Row r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(r.w[i].x), "=r"(r.w[i].y)
+                 : "r"(row + 2 * at[i])
+                 : "memory");
+  return r;
+}
+
 template <int D, bool kBF16, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks)
     rope_bwd_kernel(const __grid_constant__ RopeParams p) {
@@ -371,82 +389,103 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks)
 #pragma unroll
   for (int e = 0; e < 4; ++e) dw[e] = f2(0.f, 0.f);
 
+  // A warp's rows, one of each group at a time: token blocks of the stripe, and
+  // the heads of each.  They run ahead through a ring in shared memory.
+  __shared__ __align__(16) uint8_t ring[kThreads / 32][kStagesBwd][1024];
   const int token_blocks = (p.tokens + kGroups - 1) / kGroups;
   const long long step = static_cast<long long>(p.S) * D;
+  const int in_warp = threadIdx.x % 32 / kLanes, l = threadIdx.x % kLanes;
+  const uint32_t slots = ptx::smem_u32(ring[threadIdx.x / 32]);
+  constexpr uint32_t kRowBytes = 2 * D;  // of an input; a slot: [group][dy, x]
+  const uint32_t mine = slots + in_warp * 2 * kRowBytes;
+  struct {
+    int blk, i;
+    bool in;
+    const uint16_t *dy, *x;
+  } ahead{};
+  auto enter = [&] {
+    const Token k = find_token(p, ahead.blk * kGroups + group);
+    ahead.in = k.in;
+    ahead.dy = p.y[h.kind] +
+               ((static_cast<long long>(k.b) * (h.kind == 0 ? p.Hq : p.Hkv) +
+                 h.first) * p.S + k.s) * D + 8 * l;
+    if (norm)
+      ahead.x = p.x[h.kind] + k.b * p.x_b[h.kind] + k.s * p.x_s[h.kind] +
+                h.first * p.x_h[h.kind] + 8 * l;
+  };
+  auto load = [&](int stage) {
+    if (ahead.blk < token_blocks) {
+      const uint32_t to = mine + stage * 1024 + 16 * l;
+      copy16(to, ahead.dy, ahead.in);
+      if (norm) copy16(to + kRowBytes, ahead.x, ahead.in);
+      ahead.dy += step;
+      if (norm) ahead.x += p.x_h[h.kind];
+      if (++ahead.i == h.count) {
+        ahead.i = 0;
+        ahead.blk += stripes;
+        if (ahead.blk < token_blocks) enter();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  ahead.blk = stripe;
+  ahead.i = 0;
+  enter();
+#pragma unroll
+  for (int i = 0; i < kStagesBwd; ++i) load(i);
+  int stage = 0;
   for (int blk = stripe; blk < token_blocks; blk += stripes) {
     const Token k = find_token(p, blk * kGroups + group);
-    const uint16_t* dy =
-        p.y[h.kind] +
-        ((static_cast<long long>(k.b) * (h.kind == 0 ? p.Hq : p.Hkv) +
-          h.first) * p.S + k.s) * D;
     uint16_t* dx = p.dx[h.kind] + k.b * p.dx_b[h.kind] +
                    k.s * p.dx_s[h.kind] + h.first * p.dx_h[h.kind];
-    const uint16_t* x = nullptr;
-    if (norm)
-      x = p.x[h.kind] + k.b * p.x_b[h.kind] + k.s * p.x_s[h.kind] +
-          h.first * p.x_h[h.kind];
-    Row gy[kRowsBwd], gx[kRowsBwd];
-    auto load = [&](int i0) {
-#pragma unroll
-      for (int i = 0; i < kRowsBwd; ++i) {
-        gy[i].w[0] = gy[i].w[1] = gx[i].w[0] = gx[i].w[1] =
-            make_uint2(0u, 0u);
-        if (!k.in || i0 + i >= h.count) continue;
-        gy[i] = load_row(dy + (i0 + i) * step, lane.at);
-        if (norm) gx[i] = load_row(x + (i0 + i) * p.x_h[h.kind], lane.at);
-      }
-    };
-    load(0);
-    if (h.kind == 2) {
-      for (int i0 = 0; i0 < h.count; i0 += kRowsBwd) {
-        if (i0 > 0) load(i0);
-#pragma unroll
-        for (int i = 0; i < kRowsBwd; ++i) {
-          if (!k.in || i0 + i >= h.count) break;
-          uint16_t* to = dx + (i0 + i) * p.dx_h[2];
-          *reinterpret_cast<uint2*>(to + lane.at[0]) = gy[i].w[0];
-          *reinterpret_cast<uint2*>(to + lane.at[1]) = gy[i].w[1];
-        }
-      }
-      continue;
-    }
     Turn back;
-    {
+    if (h.kind < 2) {
       float one[8], c[4], s[4];
 #pragma unroll
       for (int e = 0; e < 8; ++e) one[e] = 1.f;
       turns(p, k, lane.pair, c, s);
       back = make_turn<kInterleaved>(one, c, s, -1.f);
     }
-    for (int i0 = 0; i0 < h.count; i0 += kRowsBwd) {
-      if (i0 > 0) load(i0);
-#pragma unroll
-      for (int i = 0; i < kRowsBwd; ++i) {
-        if (i0 + i >= h.count) break;
-        F2 d[4], g[4];
-        widen<kBF16>(gy[i], d);
-        rotate<kInterleaved>(back, d, g, whole, lane.pair >= 0);
-        if (norm) {
-          F2 n[4];
-          widen<kBF16>(gx[i], n);
-          float f;
-          const float r = norm_factor<D>(n, p.eps, &f);
-          F2 sum = f2(0.f, 0.f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            n[e] = mul(n[e], f2(r, r));  // x^
-            dw[e] = fma(g[e], n[e], dw[e]);
-            g[e] = mul(g[e], f2(w[2 * e], w[2 * e + 1]));
-            sum = fma(g[e], n[e], sum);
-          }
-          const float2 both = parts(sum);
-          const float mean = group_sum<kLanes>(both.x + both.y) * (-1.f / D);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            g[e] = mul(fma(n[e], f2(mean, mean), g[e]), f2(r * f, r * f));
+    for (int i = 0; i < h.count; ++i, dx += p.dx_h[h.kind]) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStagesBwd - 1) : "memory");
+      __syncwarp();
+      Row gy, gx;
+      const uint32_t from = mine + stage * 1024;
+      gy = shared_row(from, lane.at);
+      if (norm) gx = shared_row(from + kRowBytes, lane.at);
+      __syncwarp();  // the slot has been read
+      load(stage);
+      stage = stage + 1 == kStagesBwd ? 0 : stage + 1;
+      if (h.kind == 2) {
+        if (k.in) {
+          *reinterpret_cast<uint2*>(dx + lane.at[0]) = gy.w[0];
+          *reinterpret_cast<uint2*>(dx + lane.at[1]) = gy.w[1];
         }
-        if (k.in) store_row<kBF16>(dx + (i0 + i) * p.dx_h[h.kind], lane.at, g);
+        continue;
       }
+      F2 d[4], g[4];
+      widen<kBF16>(gy, d);
+      rotate<kInterleaved>(back, d, g, whole, lane.pair >= 0);
+      if (norm) {
+        F2 n[4];
+        widen<kBF16>(gx, n);
+        float f;
+        const float r = norm_factor<D>(n, p.eps, &f);
+        F2 sum = f2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          n[e] = mul(n[e], f2(r, r));  // x^
+          dw[e] = fma(g[e], n[e], dw[e]);
+          g[e] = mul(g[e], f2(w[2 * e], w[2 * e + 1]));
+          sum = fma(g[e], n[e], sum);
+        }
+        const float2 both = parts(sum);
+        const float mean = group_sum<kLanes>(both.x + both.y) * (-1.f / D);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          g[e] = mul(fma(n[e], f2(mean, mean), g[e]), f2(r * f, r * f));
+      }
+      if (k.in) store_row<kBF16>(dx, lane.at, g);
     }
   }
   if (!norm) return;

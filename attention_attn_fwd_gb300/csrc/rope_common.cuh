@@ -50,7 +50,7 @@ cudaError_t launch_rope(int D, bool bf16, bool interleaved,
 cudaError_t launch_rope_bwd(int D, bool bf16, bool interleaved,
                             const RopeParams& p, int sms, cudaStream_t stream);
 // CTAs of a backward launch at most (each leaves a row of partial sums).
-constexpr int bwd_ctas(int sms) { return 10 * sms; }
+constexpr int bwd_ctas(int sms) { return 6 * sms; }
 
 }  // namespace rope
 }  // namespace attn
