@@ -26,10 +26,10 @@
 // device memory and the cut follows them.  A unit's parts are joined by the
 // merge kernels (prefix_merge.cu).
 //
-// Roles (384 threads): warp 0 MMA issue, warp 1 tile copies, warp 2 walks the
-// share and publishes its units in shared memory, warp 3 copies the units'
-// query rows and clears the ends of V, warps 4-7 / 8-11 softmax and output of Q
-// tile 0 / 1.  Every wait is bounded as in the forward kernel.
+// Roles (384 threads): warps 0 and 2 MMA issue of Q tile 0 / 1, warp 1 tile
+// copies, warp 3 walks the share, publishes its units in shared memory, copies
+// their query rows and clears the ends of V, warps 4-7 / 8-11 softmax and
+// output of Q tile 0 / 1.  Every wait is bounded as in the forward kernel.
 //
 // A Q tile is one copy by a tensor map whose box is (heads of the group, tokens,
 // sequences), asked for as soon as the last S of the unit before is done.
@@ -46,6 +46,7 @@ namespace {
 using kv8::kNone;
 
 constexpr int kThreads = 384;
+constexpr int kHalf = kTN / 2;  // keys of a step
 constexpr float kTau = 8.f;  // lazy rescale threshold (log2 units)
 // Registers: the launch gives every thread 168; the shares of the three
 // warpgroups add up to 3 * 168.
@@ -88,9 +89,9 @@ struct Smem {
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTile;
   static constexpr int kBars = kRing + kSlots * kTile;
-  // kv_full, kv_empty [slots], unit_full, unit_empty, q[2], q_free[2], s[2],
-  // p[2], o[2], end, cleared, drain
-  static constexpr int kNumBars = 2 * kSlots + 2 * kUnits + 13;
+  // kv_full, kv_empty [slots], unit_full, unit_empty, q[2], q_free[2],
+  // s[2][2], p[2][2], pv[2], o[2], end, cleared, drain[2]
+  static constexpr int kNumBars = 2 * kSlots + 2 * kUnits + 20;
   static constexpr int kMisc = kBars + 8 * kNumBars;  // TMEM base, abort
   static constexpr int kRecords = kMisc + 8;
   static constexpr int kBytes = kRecords + kUnits * sizeof(Record);
@@ -415,13 +416,14 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b,
 #undef ATTN_END
 }
 
-// O (+)= P V of a whole tile, eight steps of 16 keys: P in tensor memory from
-// `a` on, 8 columns a step, V 2 KB on.
+// O (+)= P V of half a tile, four steps of 16 keys, and a commit to `bar`: P in
+// tensor memory from `a` on, 8 columns a step, V 2 KB on.
 __device__ __forceinline__ void issue_output(uint32_t d, uint32_t a,
                                              uint32_t b, uint32_t hi,
-                                             uint32_t idesc, uint32_t acc) {
+                                             uint32_t idesc, uint32_t acc,
+                                             uint32_t bar) {
 #define ATTN_STEP(at, off, p)                                               \
-  "add.u32 ta, %1, " at ";\n\tadd.u32 lb, %2, " off ";\n\t"               \
+  "add.u32 ta, %1, " at ";\n\tadd.u32 lb, %2, " off ";\n\t"              \
   "mov.b64 db, {lb, %3};\n\t"                                              \
   "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, " p ";\n\t"
   asm volatile(
@@ -430,10 +432,10 @@ __device__ __forceinline__ void issue_output(uint32_t d, uint32_t a,
       "setp.ne.b32 acc, %5, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t" ATTN_STEP("0", "0", "acc")
           ATTN_STEP("8", "128", "yes") ATTN_STEP("16", "256", "yes")
-              ATTN_STEP("24", "384", "yes") ATTN_STEP("32", "512", "yes")
-                  ATTN_STEP("40", "640", "yes") ATTN_STEP("48", "768", "yes")
-                      ATTN_STEP("56", "896", "yes") "}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+              ATTN_STEP("24", "384", "yes")
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
+      "b64 [%6];\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(bar)
       : "memory");
 #undef ATTN_STEP
 }
@@ -456,12 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_ufree = bar_unit + 8 * kUnits;      // [kUnits]
   const uint32_t bar_q = bar_ufree + 8 * kUnits;         // [2]
   const uint32_t bar_qfree = bar_q + 16;                 // [2]
-  const uint32_t bar_s = bar_qfree + 16;                 // [2]
-  const uint32_t bar_p = bar_s + 16;                     // [2]
-  const uint32_t bar_o = bar_p + 16;                     // [2]
+  const uint32_t bar_s = bar_qfree + 16;                 // [tile][buffer]
+  const uint32_t bar_p = bar_s + 32;                     // [tile][buffer]
+  const uint32_t bar_pv = bar_p + 32;                    // [2]
+  const uint32_t bar_o = bar_pv + 16;                    // [2]
   const uint32_t bar_end = bar_o + 16;                   // [1]
   const uint32_t bar_cleared = bar_end + 8;              // [1]
-  const uint32_t bar_drain = bar_end + 16;               // [1]
+  const uint32_t bar_drain = bar_end + 16;               // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
   volatile Record* records = reinterpret_cast<Record*>(smem + L::kRecords);
@@ -469,11 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x < L::kNumBars) {
     const uint32_t bar = s_base + L::kBars + 8 * threadIdx.x;
-    // Units read: one arrival per warp of the other roles (11); P: one per
-    // softmax thread of the tile.
+    // Tiles used, and ends of V asked for: one arrival per issuing warp (2);
+    // units read: one per warp of the other roles (11); P: one per softmax
+    // thread of the tile.
     uint32_t count = 1;
+    if ((bar >= bar_empty && bar < bar_unit) || bar == bar_end) count = 2;
     if (bar >= bar_ufree && bar < bar_q) count = 11;
-    if (bar >= bar_p && bar < bar_o) count = kTM;
+    if (bar >= bar_p && bar < bar_pv) count = kTM;
     ptx::mbar_init(bar, count);
     if (threadIdx.x == 0) *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -510,13 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // still have to take its own); the warps that use it meet here, the others
   // go ahead.
   uint32_t tmem = 0;
-  if (warp == 0 || warp >= 4) {
+  if (warp == 0 || warp == 2 || warp >= 4) {
     if (warp == 0) {
       ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
       ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    ptx::named_barrier_sync(1, kThreads - 96);
+    ptx::named_barrier_sync(1, kThreads - 64);
     ptx::tc_fence_after();
     tmem = *tmem_slot;
   }
@@ -541,18 +546,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     ptx::setmaxnreg_dec<kRegsControl>();
-    if (warp == 2) {
-      // ------------------------------------------------ units of the share
+    if (warp == 3) {
+      // --------- units of the share, their query rows, ends of V's last tiles
       Walk walk;
       bool more =
           walk.take(p, static_cast<int>(blockIdx.x), ctas, np, lane);
       int4 split = make_int4(0, 0, 0, 0);
-      for (int k = 0; ok; ++k) {
+      int published = 0;
+      // Units are published one ahead of the one at hand (all roles can end
+      // every unit before that without this warp, so that the wait ends).
+      auto publish = [&] {
+        const int k = published++;
         if (k >= kUnits)
           ok = wait(bar_ufree + 8 * (k % kUnits), k / kUnits - 1, 1);
-        if (!ok) break;
-        volatile Record* rec = records + k % kUnits;
+        if (!ok) return;
         if (lane == 0) {
+          volatile Record* rec = records + k % kUnits;
           if (more)
             fill_record(p, walk, plen, rec);
           else
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(bar_unit + 8 * (k % kUnits));
         }
         __syncwarp();
-        if (!more) break;
+        if (!more) return;
         const Unit& w = walk.w;
         if (w.j0 == 0) {
           const int parts =
@@ -573,26 +582,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         more = walk.next(p);
-      }
-      if (lane == 0 && p.mode == kJoint) p.split[blockIdx.x] = split;
-    } else if (warp == 3) {
-      // ------------------------------- query rows, ends of V's last tiles
-      // The ends in step with the MMA issuer, which asks for each when it has
+      };
+      publish();
+      // The ends in step with the MMA issuers, which ask for each when it has
       // arrived (a warp that looked at some phases only of the ring's barriers
       // could take one for another).
-      int it = 1;  // V tiles of the stream are odd
+      int slot_v = 1;  // V tiles of the stream are odd
       int ends = 0, q_uses[2] = {0, 0};
       const int q_tokens = fast_div(p.tile_rows, p.fd_group);
       const uint32_t q_bytes =
           (p.mode == kJoint ? p.tile_rows : p.tile_seqs * p.rows) * D * 2;
       for (int k = 0; ok; ++k) {
-        volatile Record* rec = get_unit(k);
-        if (rec == nullptr) break;
-        const int n = rec->n_kv, j0 = rec->j0, np = rec->np;
-        const int plen = rec->plen, len = rec->len;
+        volatile Record* rec = records + k % kUnits;
+        const int n = rec->n_kv;
+        if (n == 0) break;
+        const int j0 = rec->j0, unit_np = rec->np, len = rec->len;
         const int n0 = rec->n[0], n1 = rec->n[1];
         const int b = rec->b, h = rec->h, tile0 = rec->tile0;
-        release_unit(k);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || (t ? n1 : n0) == 0) continue;
@@ -610,11 +616,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        for (int j = 0; j < n; ++j, it += 2) {
+        publish();
+        if (!ok) break;
+        for (int j = 0; j < n; ++j) {
           bool own;
-          const int valid = tile_keys(j0 + j, np, plen, len, &own);
+          const int valid = tile_keys(j0 + j, unit_np, plen, len, &own);
+          const int slot = slot_v;
+          slot_v += 2;
+          if (slot_v >= L::kSlots) slot_v -= L::kSlots;
           if (valid % 16 == 0) continue;
-          const int slot = it % L::kSlots;
           ok = wait(bar_end, ends++, 5);
           if (!ok) break;
           const uint32_t at = s_base + L::kRing + slot * L::kTile;
@@ -637,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_wait(bar_q + 8 * t, (q_uses[t] - 1) & 1, p);
       }
       __syncwarp();
+      if (lane == 0 && p.mode == kJoint) p.split[blockIdx.x] = split;
       write_unseen<D>(p, lane);
     } else if (warp == 1) {
       // -------------------------------------------------------- tile copies
@@ -682,41 +693,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_wait(bar_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1, p);
       }
       __syncwarp();
-    } else if (warp == 0) {
-      // -------------------------------------------------------- MMA issue
+    } else {
+      // ----------------------------------------- MMA issue, a warp a Q tile
+      const int t = warp / 2;
       const uint32_t idesc_qk =
-          ptx::idesc_f16(kBF16, kTM, kTN, false, p.negate != 0);
+          ptx::idesc_f16(kBF16, kTM, kHalf, false, p.negate != 0);
       const uint32_t idesc_pv = ptx::idesc_f16(kBF16, kTM, D, true, false);
       constexpr uint32_t kHi = ptx::sdesc_hi_sw128(1024);
       const uint32_t q_lo = ptx::sdesc_lo(s_base + L::kQ, 16);
       const uint32_t k_lo = ptx::sdesc_lo(s_base + L::kRing, 16);
       const uint32_t v_lo = ptx::sdesc_lo(s_base + L::kRing, L::kBox);
       constexpr uint32_t kTile16 = L::kTile >> 4;
+      constexpr uint32_t kHalf16 = (kHalf * 128) >> 4;  // half a tile's rows on
       const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);  // uniform
-      auto issue_qk = [&](int t, int slot) {
-        issue_scores<D>(tm + t * kTN, q_lo + t * kTile16,
-                        k_lo + slot * kTile16, kHi, idesc_qk, bar_s + 8 * t);
-      };
-      // `steps` of 16 keys.
-      auto issue_pv = [&](int t, int slot, bool acc, int steps) {
-        const uint32_t b0 = v_lo + slot * kTile16;
-        if (steps == kTN / 16) {
-          issue_output(tm + kOCol + t * D, tm + t * kTN, b0, kHi, idesc_pv,
-                       acc ? 1u : 0u);
-        } else {
-#pragma unroll 1
-          for (int kk = 0; kk < steps; ++kk)
-            ptx::mma_ts_elect(tm + kOCol + t * D, tm + t * kTN + kk * 8,
-                              b0 + ((kk * 16 * 128) >> 4), kHi, idesc_pv,
-                              (acc || kk > 0) ? 1u : 0u);
-        }
-      };
-      // One copy of the code for both Q tiles and for a unit's first S: cold
-      // instructions cost a short launch's first steps 2 us a copy.
-      int slot = 0, phase = 0;  // of the ring's next tile
-      uint32_t q_parity = 0, p_parity = 0;  // bit t: of tile t's barriers
+      // The ring's tile that S, and that O, takes next (K_0, V_0, K_1, ...).
+      int slot_k = 0, phase_k = 0, slot_v = 1, phase_v = 0;
+      int s_count = 0, o_count = 0;  // steps issued
+      int q_uses = 0;
       int ends = 0;  // tiles cleared behind their last key
       bool issued = false;
+      auto two_on = [&](int& slot, int& phase) {
+        slot += 2;
+        if (slot >= L::kSlots) {
+          slot -= L::kSlots;
+          phase ^= 1;
+        }
+      };
       for (int k = 0; ok; ++k) {
         ok = wait(bar_unit + 8 * (k % kUnits), k / kUnits, 1);
         if (!ok) break;
@@ -724,8 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // compiler, and with them the ring position: descriptors then stay in
         // uniform registers (else every MMA moves them there first).
         volatile Record* rec = records + k % kUnits;
-        const int n0 = __reduce_max_sync(0xffffffffu, rec->n[0]);
-        const int n1 = __reduce_max_sync(0xffffffffu, rec->n[1]);
+        const int n = __reduce_max_sync(0xffffffffu, rec->n[t]);
         const int n_kv = __reduce_max_sync(0xffffffffu, rec->n_kv);
         const int j0 = __reduce_max_sync(0xffffffffu, rec->j0);
         const int np = __reduce_max_sync(0xffffffffu, rec->np);
@@ -737,77 +738,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end_p = np - 1 - j0, keys_p = plen - (np - 1) * kTN;
         const int end_own = np + (len - 1) / kTN - j0;
         const int keys_own = (len - 1) % kTN + 1;
-#pragma unroll 1
-        for (int j = -1; j < n_kv; ++j) {
-          // V_j lies in the slot ahead of K_j+1's.
-          const int slot_v = slot, phase_v = phase;
-          if (j >= 0 && ++slot == L::kSlots) {
-            slot = 0;
-            phase ^= 1;
+        auto valid_of = [&](int j) {
+          return j == end_p ? keys_p : j == end_own ? keys_own : kTN;
+        };
+        // Next steps of S and of O: tile and half.
+        int jk = 0, hk = 0, jv = 0, hv = 0;
+        auto scores = [&] {
+          const bool last_half = valid_of(jk) <= kHalf * (hk + 1);
+          if (hk == 0) {
+            ok = wait(bar_full + 8 * slot_k, phase_k, 2);
+            if (!ok) return;
           }
-          int valid = kTN;
-          bool clear = false, k_ready = false;
-          if (j >= 0) {
-            if (j == end_p) valid = keys_p;
-            if (j == end_own) valid = keys_own;
+          if (jk < n) {
+            if (jk == 0 && hk == 0) {
+              ok = wait(bar_q + 8 * t, q_uses++, 2);
+              if (!ok) return;
+            }
+            ptx::tc_fence_after();
+            const int buf = s_count++ & 1;
+            issue_scores<D>(tm + t * kTN + buf * kHalf, q_lo + t * kTile16,
+                            k_lo + slot_k * kTile16 + hk * kHalf16, kHi,
+                            idesc_qk, bar_s + 16 * t + 8 * buf);
+            issued = true;
+            // Behind the tile's last S its query rows make room.
+            if (last_half && jk == n - 1)
+              ptx::tc_commit_elect(bar_qfree + 8 * t);
+          }
+          hk = last_half ? 0 : 1;
+          if (last_half) {
+            ptx::tc_commit_elect(bar_empty + 8 * slot_k);
+            two_on(slot_k, phase_k);
+            ++jk;
+          }
+        };
+        scores();
+        while (ok && jv < n_kv) {
+          // The next step's S is made while the softmax works on this one's.
+          if (jk < n_kv) scores();
+          if (!ok) break;
+          const int valid = valid_of(jv);
+          const bool last_half = valid <= kHalf * (hv + 1);
+          bool clear = false;
+          if (hv == 0) {
             ok = wait(bar_full + 8 * slot_v, phase_v, 2);
             if (!ok) break;
             clear = valid % 16 != 0;
             if (clear && lane == 0) ptx::mbar_arrive(bar_end);
           }
-          const int steps = (valid + 15) / 16;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int n = t ? n1 : n0;
-            if (j >= n || n == 0) continue;
-            if (j >= 0) {
-              ok = wait(bar_p + 8 * t, p_parity >> t, 2);
-              if (!ok) break;
-              p_parity ^= 1u << t;
-              if (clear) {
-                ok = wait(bar_cleared, ends++, 2);
-                if (!ok) break;
-                clear = false;
-              }
-              ptx::tc_fence_after();
-              issue_pv(t, slot_v, j > 0, steps);
-              if (j == n - 1) {
-                ptx::tc_commit_elect(bar_o + 8 * t);
-                continue;
-              }
-            } else {
-              ok = wait(bar_q + 8 * t, q_parity >> t, 2);
-              if (!ok) break;
-              q_parity ^= 1u << t;
-            }
-            if (!k_ready) {
-              ok = wait(bar_full + 8 * slot, phase, 2);
-              if (!ok) break;
-              k_ready = true;
-            }
-            ptx::tc_fence_after();
-            issue_qk(t, slot);
-            issued = true;
-            // Behind the tile's last S its query rows make room.
-            if (j + 1 == n - 1) ptx::tc_commit_elect(bar_qfree + 8 * t);
-          }
-          if (!ok) break;
-          if (j >= 0) ptx::tc_commit_elect(bar_empty + 8 * slot_v);
-          if (j + 1 < n_kv) {
-            // (Where no Q tile sees the next keys, nobody waited for them.)
-            if (!k_ready) ok = wait(bar_full + 8 * slot, phase, 2);
+          if (clear) {
+            ok = wait(bar_cleared, ends++, 2);
             if (!ok) break;
-            ptx::tc_commit_elect(bar_empty + 8 * slot);
-            if (++slot == L::kSlots) {
-              slot = 0;
-              phase ^= 1;
+          }
+          if (jv < n) {
+            const int steps = (min(kHalf, valid - hv * kHalf) + 15) / 16;
+            const int buf = o_count & 1;
+            ok = wait(bar_p + 16 * t + 8 * buf, o_count >> 1, 2);
+            if (!ok) break;
+            ++o_count;
+            ptx::tc_fence_after();
+            const uint32_t d = tm + kOCol + t * D;
+            const uint32_t a = tm + t * kTN + buf * kHalf;
+            const uint32_t b = v_lo + slot_v * kTile16 + hv * kHalf16;
+            const bool acc = jv > 0 || hv > 0;
+            if (steps == kHalf / 16) {
+              issue_output(d, a, b, kHi, idesc_pv, acc ? 1u : 0u,
+                           bar_pv + 8 * t);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < steps; ++kk)
+                ptx::mma_ts_elect(d, a + kk * 8, b + ((kk * 16 * 128) >> 4),
+                                  kHi, idesc_pv, (acc || kk > 0) ? 1u : 0u);
+              ptx::tc_commit_elect(bar_pv + 8 * t);
             }
+            if (last_half && jv == n - 1) ptx::tc_commit_elect(bar_o + 8 * t);
+          }
+          hv = last_half ? 0 : 1;
+          if (last_half) {
+            ptx::tc_commit_elect(bar_empty + 8 * slot_v);
+            two_on(slot_v, phase_v);
+            ++jv;
           }
         }
       }
       if (!ok && issued) {  // the MMAs issued end before TMEM is released
-        ptx::tc_commit_elect(bar_drain);
-        drain_wait(bar_drain, 0, p);
+        ptx::tc_commit_elect(bar_drain + 8 * t);
+        drain_wait(bar_drain + 8 * t, 0, p);
       }
       __syncwarp();
     }
@@ -822,129 +837,136 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Factor of the scores, held off 0 so that -inf stays -inf (scores times
     // 1e-37 vanish next to any maximum).
     const float c = fmaxf(p.scale_log2, 1e-37f);
-    int s_uses = 0, o_uses = 0;
+    int count = 0, o_uses = 0;  // steps and units done
     // Before the first scores a step is made of whatever O's columns hold, to
     // no effect but that its instructions have been fetched (2.5 us of the
     // first real step otherwise; the first products overwrite O).
-    int first = -1;
+    bool dry = true;
     for (int k = 0; ok; ++k) {
       volatile Record* rec = get_unit(k);
       if (rec == nullptr) break;
       const int n = rec->n[t];
       // Keys left from the tile at hand on: of the prefix (none behind its
-      // tiles), and own ones that this row sees.
-      int left = 0, left_own;
+      // tiles) and own ones, of which this row does not see the last `hidden`.
+      int left = 0, left_own, hidden = 0;
       // A warp without rows keeps in step but computes nothing: its P are
-      // whatever S left there, which reaches its own rows of O only.
-      bool live;
+      // whatever S left there, which reaches its own rows of O only.  Beside
+      // rows, those of no row (made of what shared memory held) have no say in
+      // when the warp rescales.
+      bool live, row_here;
       {
         const int j0 = rec->j0, np = rec->np, len = rec->len;
-        int row, vis = len;
-        const bool row_ok = row_of(p, rec, t, r, &row) >= 0;
-        live = __any_sync(0xffffffffu, row_ok);
-        if (rec->b >= 0 && row_ok) vis = row_end(p, len, rec->n_new, row);
+        int row;
+        row_here = row_of(p, rec, t, r, &row) >= 0;
+        live = __any_sync(0xffffffffu, row_here);
+        if (rec->b >= 0 && row_here)
+          hidden = len - row_end(p, len, rec->n_new, row);
         if (np > 0) left = rec->plen - j0 * kTN;
-        left_own = vis - (j0 - np) * kTN;
+        left_own = len - (j0 - np) * kTN;
       }
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = first; j < n; ++j) {
-        const bool dry = j < 0;
-        const int lim = left > 0 ? left : left_own;
-        const bool masked = __any_sync(0xffffffffu, lim < kTN);
+      bool first = true;
+      int half = 0;
+      for (int j = 0; j < n;) {
+        const int keys = left > 0 ? left : left_own;
+        const int lim = (left > 0 ? left : left_own - hidden) - half * kHalf;
+        const int buf = count & 1;
         if (!dry) {
-          left -= kTN;
-          left_own -= kTN;
-          ok = wait(bar_s + 8 * t, s_uses, 4);
+          ok = wait(bar_s + 16 * t + 8 * buf, count >> 1, 4);
           if (!ok) break;
-          ++s_uses;
           ptx::tc_fence_after();
         }
-        const uint32_t t_s = dry ? t_o : t_scores;
-        if (!live) {
-          if (dry) continue;
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar_p + 8 * t);
-          continue;
-        }
-        uint32_t sr[kTN];
+        if (live) {
+          const bool masked = __any_sync(0xffffffffu, lim < kHalf);
+          const uint32_t t_s = dry ? t_o : t_scores + buf * kHalf;
+          uint32_t sr[kHalf];
 #pragma unroll
-        for (int q = 0; q < kTN / 32; ++q)
-          ptx::tmem_ld32(t_s + 32 * q, sr + 32 * q);
-        ptx::tmem_wait_ld();
-        if (masked) {
+          for (int q = 0; q < kHalf / 32; ++q)
+            ptx::tmem_ld32(t_s + 32 * q, sr + 32 * q);
+          ptx::tmem_wait_ld();
+          if (masked) {
 #pragma unroll
-          for (int q = 0; q < kTN; ++q)
-            if (q >= lim) sr[q] = __float_as_uint(-INFINITY);
-        }
-        float mx4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          mx4[q] = ptx::fmax3(__uint_as_float(sr[q]),
-                              __uint_as_float(sr[q + 4]),
-                              __uint_as_float(sr[q + 8]));
-#pragma unroll
-        for (int q = 12; q < kTN; q += 8) {
+            for (int q = 0; q < kHalf; ++q)
+              if (q >= lim) sr[q] = __float_as_uint(-INFINITY);
+          }
+          float mx4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mx4[e] = q + 4 + e < kTN
-                         ? ptx::fmax3(mx4[e], __uint_as_float(sr[q + e]),
-                                      __uint_as_float(sr[q + 4 + e]))
-                         : fmaxf(mx4[e], __uint_as_float(sr[q + e]));
-        }
-        const float mx =
-            fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
-        float m_new = m_run;
-        if (__any_sync(0xffffffffu, mx > m_run + kTau))
-          m_new = fmaxf(m_run, mx);
-        const float alpha =
-            (m_new == -INFINITY) ? 1.f : ptx::ex2(m_run - m_new);
-        const float neg_m = (m_new == -INFINITY) ? 0.f : kShift - m_new;
-        float sm[4] = {0.f, 0.f, 0.f, 0.f};
+            mx4[e] = fmaxf(__uint_as_float(sr[e]), __uint_as_float(sr[e + 4]));
 #pragma unroll
-        for (int q = 0; q < kTN / 32; ++q) {
-          uint32_t pk[16];
+          for (int q = 8; q < kHalf; q += 8)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int i = 32 * q + 2 * e;
-            float x0, x1;
-            ptx::ffma2(x0, x1, __uint_as_float(sr[i]),
-                       __uint_as_float(sr[i + 1]), c, neg_m);
-            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-            if (e & 1)
-              ptx::fadd2(sm[2], sm[3], p0, p1);
-            else
-              ptx::fadd2(sm[0], sm[1], p0, p1);
-            pk[e] = ptx::pack2<kBF16>(p0, p1);
+            for (int e = 0; e < 4; ++e)
+              mx4[e] = ptx::fmax3(mx4[e], __uint_as_float(sr[q + e]),
+                                  __uint_as_float(sr[q + 4 + e]));
+          const float mx =
+              fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+          float m_new = m_run;
+          if (__any_sync(0xffffffffu, row_here && mx > m_run + kTau))
+            m_new = fmaxf(m_run, mx);
+          const float alpha =
+              (m_new == -INFINITY) ? 1.f : ptx::ex2(m_run - m_new);
+          const float neg_m = (m_new == -INFINITY) ? 0.f : kShift - m_new;
+          float sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < kHalf / 32; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int i = 32 * q + 2 * e;
+              float x0, x1;
+              ptx::ffma2(x0, x1, __uint_as_float(sr[i]),
+                         __uint_as_float(sr[i + 1]), c, neg_m);
+              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              if (e & 1)
+                ptx::fadd2(sm[2], sm[3], p0, p1);
+              else
+                ptx::fadd2(sm[0], sm[1], p0, p1);
+              pk[e] = ptx::pack2<kBF16>(p0, p1);
+            }
+            ptx::tmem_st16(t_s + 16 * q, pk);
           }
-          ptx::tmem_st16(t_s + 16 * q, pk);
-        }
-        if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
-          // O *= alpha (the PV before was issued before this S, whose commit
-          // has been awaited).
+          if (!first && !dry && __any_sync(0xffffffffu, m_new != m_run)) {
+            // O *= alpha, behind the products of the step before.  (Those of
+            // the one before that are done, as this step's S came after them:
+            // the barrier's phase is that step's or the next.)
+            ok = wait(bar_pv + 8 * t, count - 1, 4);
+            if (!ok) break;
+            ptx::tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            ptx::tmem_ld32(t_o + 32 * q, o);
-            ptx::tmem_wait_ld();
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              ptx::tmem_ld32(t_o + 32 * q, o);
+              ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            ptx::tmem_st32(t_o + 32 * q, o);
+              for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              ptx::tmem_st32(t_o + 32 * q, o);
+            }
           }
+          l_run = l_run * alpha + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
+          ptx::tmem_wait_st();
+          m_run = m_new;
         }
-        l_run *= alpha;
-        ptx::tmem_wait_st();
-        l_run += (sm[0] + sm[1]) + (sm[2] + sm[3]);
-        m_run = m_new;
         if (dry) {
+          dry = false;
           m_run = -INFINITY;
           l_run = 0.f;
           continue;
         }
+        first = false;
+        ++count;
         ptx::tc_fence_before();
-        ptx::mbar_arrive(bar_p + 8 * t);
+        ptx::mbar_arrive(bar_p + 16 * t + 8 * buf);
+        if (half == 0 && keys > kHalf) {
+          half = 1;
+        } else {
+          half = 0;
+          left -= kTN;
+          left_own -= kTN;
+          ++j;
+        }
       }
-      first = 0;
       if (!ok) break;
       if (n > 0) {
         ok = wait(bar_o + 8 * t, o_uses, 4);
