@@ -84,7 +84,7 @@ template <int D>
 __host__ __device__ constexpr int few_keys() {
   return 2048 / D;
 }
-constexpr int kFewOver = 2;
+constexpr int kFewOver = 3;
 
 // Own tokens that row r of a sequence sees.
 __device__ __forceinline__ int row_end(const PrefixParams& p, int len,
