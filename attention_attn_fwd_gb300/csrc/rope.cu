@@ -554,10 +554,8 @@ cudaError_t launch_fwd(RopeParams p, int sms, cudaStream_t stream) {
   cut_heads(&p, head_block);
   while (head_block > 1 && token_blocks * p.blocks < 2LL * sms)
     cut_heads(&p, head_block /= 2);
-  const long long grid = token_blocks * p.blocks;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(rope_kernel<D, kBF16, kInterleaved>, grid, kThreads, 0,
-                    stream, p);
+  return launch_pdl(rope_kernel<D, kBF16, kInterleaved>,
+                    token_blocks * p.blocks, kThreads, 0, stream, p);
 }
 
 template <int D, bool kBF16, bool kInterleaved>

@@ -121,6 +121,10 @@ attn_status_t check_sizes(int B, int S, int Hq, int Hkv, float eps,
       Hkv > kMaxHeads || (dtype != ATTN_F16 && dtype != ATTN_BF16) ||
       static_cast<long long>(B) * S > kMaxTokens)
     return ATTN_ERR_INVALID_ARG;
+  // Thread blocks of a launch: 8 tokens of 8 heads of a kind at least.
+  const long long blocks = (Hq + 7) / 8 + 2LL * ((Hkv + 7) / 8);
+  if ((static_cast<long long>(B) * S / 8 + 1) * blocks > 0x7fffffffLL)
+    return ATTN_ERR_INVALID_ARG;
   if (wq != nullptr || wk != nullptr) {
     if (!(eps > 0.f) || !std::isfinite(eps)) return ATTN_ERR_INVALID_ARG;
     const uintptr_t a = weight_f32 ? 4 : 2;

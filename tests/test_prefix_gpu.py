@@ -385,6 +385,46 @@ def test_streams_and_graphs(Sq):
             assert all(same_bits(a, b) for a, b in zip(want, o))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,D,Sq,plen", [
+    (4, 8, 2, 128, 20, 450), (3, 4, 2, 64, 40, 333), (4, 8, 2, 128, 1, 450),
+    (5, 6, 2, 128, 3, 200), (4, 8, 2, 128, 200, 450)])
+def test_the_same_bits_side_by_side(B, Hq, Hkv, D, Sq, plen, dtype):
+    """Calls on three streams at once, whatever shared memory held before."""
+    c = make(B, Hkv, D, plen, plen, [250 - 7 * i for i in range(B)], 300,
+             dtype)
+    q = randn(B, Hq, Sq, D, dtype=dtype, seed=3)
+    want = [x.clone() for x in attn.prefix_fwd(c, q)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    spaces = [attn.prefix_workspace(c, Hq, Sq) for _ in streams]
+    outs = [[torch.zeros_like(x) for x in want] for _ in streams]
+    for _ in range(10):
+        for _ in range(4):
+            for s, w, o in zip(streams, spaces, outs):
+                attn.prefix_fwd(c, q, out=o[0], lse=o[1], workspace=w,
+                                stream=s)
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(want, o))
+            for x in o:
+                x.zero_()
+        # Another shape's numbers in shared memory.
+        noise = make(B, Hkv, D, 100, 100, [90] * B, 90, dtype, seed=77)
+        attn.prefix_fwd(noise, q * 50, causal=False)
+
+
+def test_many_sequences():
+    """More sequences than a warp's lanes, several times over."""
+    B = 1500
+    lens = [(37 * i) % 23 for i in range(B)]
+    new = [min(1, n) for n in lens]
+    c = make(B, 1, 64, 300, 300, lens, 23, "bf16")
+    check(c, 2, 1, "bf16", new)
+    check(make(B, 1, 64, 300, 300, [n + 9 for n in lens], 40, "f16"), 2, 9,
+          "f16")
+
+
 def test_calls_in_a_row_share_a_workspace():
     """Different shapes one behind the other on one stream and workspace."""
     c = make(4, 2, 64, 500, 500, [200, 210, 300, 290], 300, "f16")

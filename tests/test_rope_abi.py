@@ -95,6 +95,7 @@ BOTH = [
     (dict(B=-1), INVALID), (dict(S=-1), INVALID), (dict(Hq=0), INVALID),
     (dict(Hkv=0), INVALID), (dict(dtype=E4M3), INVALID), (dict(dtype=9), INVALID),
     (dict(B=1 << 16, S=1 << 15), INVALID), (dict(Hq=1 << 21), INVALID),
+    (dict(B=1 << 15, S=1 << 15, Hq=1 << 8), INVALID),
     (dict(wq=20 * MB, eps=0.0), INVALID),
     (dict(wq=20 * MB, eps=-1.0), INVALID),
     (dict(wq=20 * MB, eps=math.nan), INVALID),

@@ -356,6 +356,109 @@ def test_empty_calls():
         assert not d[3].any() and not d[4].any()
 
 
+LAYOUTS = ["heads first", "part of a longer row", "one batch entry for all"]
+
+
+def laid_out(x, layout):
+    """The values of x [B, S, H, D] in memory of another layout."""
+    B, S, H, D = x.shape
+    if layout == "heads first":
+        return x.transpose(1, 2).contiguous().transpose(1, 2)
+    if layout == "part of a longer row":
+        room = torch.full((B, S, H + 3, D + 8), math.nan, dtype=x.dtype,
+                          device=x.device)
+        room[:, :, 1:H + 1, 8:] = x
+        return room[:, :, 1:H + 1, 8:]
+    return x[:1].expand(B, S, H, D)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_strided_inputs(layout):
+    B, S, D = 3, 21, 64
+    rope = attn.Rope(freqs(D), D)
+    w = weight(D, torch.float32, 1).cuda()
+    x = [laid_out(heads(B, S, H, D, "f16", H).cuda(), layout)
+         for H in (6, 2, 2)]
+    got = attn.qk_rope(rope, *x, w, w, EPS)
+    want = attn.qk_rope(rope, *[y.contiguous() for y in x], w, w, EPS)
+    dy = [heads(B, S, H, D, "f16", 9).transpose(1, 2).contiguous().cuda()
+          for H in (6, 2, 2)]
+    back = attn.qk_rope_bwd(rope, *dy[:2], x[0], x[1], dv=dy[2], q_weight=w,
+                            k_weight=w, eps=EPS)
+    plain = attn.qk_rope_bwd(rope, *dy[:2], x[0].contiguous(),
+                             x[1].contiguous(), dv=dy[2], q_weight=w,
+                             k_weight=w, eps=EPS)
+    for a, b in zip((*got, *back), (*want, *plain)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS[:2])
+def test_strided_gradients(layout):
+    B, S, D = 2, 19, 128
+    rope = attn.Rope(freqs(D), D)
+    dy = [heads(B, S, H, D, "bf16", 9).transpose(1, 2).contiguous().cuda()
+          for H in (3, 1, 1)]
+    want = attn.qk_rope_bwd(rope, *dy[:2], dv=dy[2])
+    out = [laid_out(torch.zeros_like(x), layout) for x in want[:3]]
+    got = attn.qk_rope_bwd(rope, *dy[:2], dv=dy[2], dq_out=out[0],
+                           dk_out=out[1], dv_out=out[2])
+    for a, b, c in zip(got, want, out):
+        assert a is c and torch.equal(a, b)
+
+
+def test_one_of_two_is_normed():
+    B, S, D = 2, 9, 64
+    rope = attn.Rope(freqs(D), D)
+    w = weight(D, torch.float16, 1).cuda()
+    q, k = (heads(B, S, H, D, "f16", H).cuda() for H in (4, 2))
+    both, none = attn.qk_rope(rope, q, k, None, w, w, EPS), \
+        attn.qk_rope(rope, q, k)
+    got = attn.qk_rope(rope, q, k, None, w, None, EPS)
+    assert torch.equal(got[0], both[0]) and torch.equal(got[1], none[1])
+    got = attn.qk_rope(rope, q, k, None, None, w, EPS)
+    assert torch.equal(got[0], none[0]) and torch.equal(got[1], both[1])
+    dy = [heads(B, S, H, D, "f16", 9).transpose(1, 2).contiguous().cuda()
+          for H in (4, 2)]
+    both = attn.qk_rope_bwd(rope, *dy, q, k, q_weight=w, k_weight=w, eps=EPS)
+    none = attn.qk_rope_bwd(rope, *dy)
+    got = attn.qk_rope_bwd(rope, *dy, q, None, q_weight=w, eps=EPS)
+    assert torch.equal(got[0], both[0]) and torch.equal(got[1], none[1])
+    assert torch.equal(got[3], both[3]) and got[4] is None
+    got = attn.qk_rope_bwd(rope, *dy, None, k, k_weight=w, eps=EPS)
+    assert torch.equal(got[0], none[0]) and torch.equal(got[1], both[1])
+    assert got[3] is None and torch.equal(got[4], both[4])
+
+
+def test_many_heads_and_tokens():
+    """Heads and tokens that fill and pass the launch's blocks; a backward whose
+    blocks of heads are more than its thread blocks."""
+    D = 64
+    rope = attn.Rope(freqs(D), D)
+    w = weight(D, torch.float32, 1).cuda()
+    for B, S, Hq, Hkv in ((1, 1, 513, 27), (3, 683, 9, 7), (1, 3, 9000, 1)):
+        q, k = (heads(B, S, H, D, "bf16", 2).cuda() for H in (Hq, Hkv))
+        got = attn.qk_rope(rope, q, k, None, w, w, EPS)
+        t = ref.angles(freqs(D), [0] * 32, torch.arange(S).expand(1, B, S))
+        for x, y in ((q, got[0]), (k, got[1])):
+            z, pair = forward(x.cpu(), w.cpu(), t, False, "bf16")
+            near(y, z.transpose(1, 2), bound(z, pair, "bf16").transpose(1, 2))
+        dy = [torch.randn_like(x) for x in got[:2]]
+        back = attn.qk_rope_bwd(rope, *dy, q, k, q_weight=w, k_weight=w,
+                                eps=EPS)
+        again = attn.qk_rope_bwd(rope, *dy, q, k, q_weight=w, k_weight=w,
+                                 eps=EPS)
+        for a, b in zip(back, again):
+            assert a is None or torch.equal(a, b)
+        d = dy[0].double().cpu().transpose(1, 2)
+        dx, dw = ref.qk_rope_bwd(d, q.cpu().double(), w.cpu().double(), t,
+                                 False, EPS)
+        terms = (forward(d, None, -t, False, "bf16")[1] *
+                 ref.norm(q.cpu().double(), torch.ones(D), EPS).abs())
+        near(back[3], dw, 2.0 ** -16 * terms.sum(dim=(0, 1, 2)))
+        assert (back[0].double().cpu() - dx).abs().max() <= \
+            2.0 ** -7 * dx.abs().max()
+
+
 # ------------------------------------------------------ streams and graphs
 
 def test_on_another_stream_and_in_a_graph():
@@ -451,3 +554,35 @@ def test_a_training_step_through_attention():
                     (got[4], ws[1].grad)):
         err = (g.double().cpu() - want).abs().max()
         assert err <= 2.0 ** -5 * want.abs().max(), float(err)
+
+
+def test_a_decoding_step_into_an_8_bit_cache():
+    """qk_rope, kv8_append and kv8_fwd in turn: the keys that the cache holds
+    are qk_rope's, to E4M3's half step."""
+    B, Hq, Hkv, D, cap, n = 2, 4, 2, 64, 100, 37
+    rope = attn.Rope.make(D)
+    w = weight(D, torch.float32, 1).cuda()
+    cache = attn.KV8Cache.empty(B, Hkv, cap, D, block=32)
+    x = heads(B, n + 1, Hq + 2 * Hkv, D, "bf16", 3).cuda()
+    whole = attn.qk_rope(rope, *x.split((Hq, Hkv, Hkv), 2), w, w, EPS)
+    first = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for part in (x[:, :n], x[:, n:]):
+        q, k, v = part.split((Hq, Hkv, Hkv), 2)
+        qr, kr, vr = attn.qk_rope(rope, q, k, v, w, w, EPS, offset=first)
+        cache.lens += part.shape[1]
+        attn.kv8_append(cache, kr, vr)
+        o, lse = attn.kv8_fwd(cache, qr)
+        first += part.shape[1]
+    scale = cache.k_scale.repeat_interleave(32, 2)[:, :, :n + 1, None]
+    held = cache.k[:, :, :n + 1].float() * scale
+    off = (held - whole[1].float()).abs()
+    assert (off <= 2.0 ** -4 * whole[1].float().abs() +
+            2.0 ** -10 * scale).all()
+    k, v = (y.repeat_interleave(Hq // Hkv, 1).double() for y in (
+        held, cache.v[:, :, :n + 1].float() *
+        cache.v_scale.repeat_interleave(32, 2)[:, :, :n + 1, None]))
+    s = whole[0][:, :, n:].double() @ k.transpose(2, 3) / math.sqrt(D)
+    want = torch.softmax(s, -1) @ v
+    # (P is rounded to fp16, O to bf16.)
+    assert ((o.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9 *
+            (torch.softmax(s, -1) @ v.abs())).all()
