@@ -247,6 +247,22 @@ def test_large_values(Sq):
             (half + 2.0 ** -11) * a).all()
 
 
+@pytest.mark.parametrize("Sq", [1, 20, 200])
+def test_small_values(Sq):
+    """V near 2^-100.  P is held times 2^-24, so sums of P V have steps of
+    2^-149 at the least: each of the 700 is off by 2^-150 at most, which is
+    2^-126 of O, together below 2^-116."""
+    c = make(2, 1, 64, 400, 400, [300, 300], 300, "bf16")
+    c.prefix_v.mul_(2.0 ** -100)
+    c.v.mul_(2.0 ** -100)
+    q = randn(2, 2, Sq, 64, dtype="bf16", seed=5)
+    o, lse = attn.prefix_fwd(c, q)
+    want, z, a = exact(c, q, [Sq] * 2, True, 0.125)
+    half = 2.0 ** -8
+    assert ((o.double() - want).abs() <= half * want.abs() +
+            (half + 2.0 ** -11) * a + 2.0 ** -116).all()
+
+
 @pytest.mark.parametrize("Sq", [1, 2, 20, 200])
 def test_nan_stays_in_its_row(Sq):
     c = make(3, 2, 64, 140, 140, [200, 201, 256], 300, "f16")
