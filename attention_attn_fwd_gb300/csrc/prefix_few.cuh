@@ -17,7 +17,12 @@
 // Tiles reach shared memory by 16-byte asynchronous copies, a ring per warp
 // that runs ahead across segments; rows past a length are filled with zeros
 // and read nothing.  Chunk j of row r lies at chunk j ^ r % 8, so that
-// ldmatrix reads share no banks.
+// ldmatrix reads share no banks.  Three tiles ahead: 192 KB of the CTA's eight
+// warps are in flight or worked on, all that an SM holds.
+//
+// What bounds it: the bytes of K and V.  256 sequences of 300 own tokens, 16
+// heads of 64 (157 MB with a prefix of 2048, which takes some CTAs): 36 us and 7
+// of the merge, of which loads can go for about 28; the rest is the start.
 #pragma once
 
 #include "prefix_common.cuh"

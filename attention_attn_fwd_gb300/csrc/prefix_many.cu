@@ -15,21 +15,36 @@
 // that lengths end in is copied in boxes of 16 rows, its P V has as many
 // 16-key steps, and a warp clears V's rows between the length and the last
 // step's end (what lies there was never written and may be NaN; P is 0 there).
-// P is rounded to the inputs' type (2^-12 relative in fp16, 2^-9 in bf16: half
-// a step, that of O itself) and held times 2^kShift: in fp16, whose numbers end at
-// 65504, so that weights stay normal down to 2^-21 of the row's largest; in
-// bf16, whose V may come near fp32's largest number, so that sums of P V do not
-// pass it.  The row sums take P unrounded.
+// P is rounded to the inputs' type, the tensor cores' operand (off by 2^-11
+// relative at most in fp16, 2^-8 in bf16, as O itself) and held times 2^kShift:
+// in fp16, whose numbers end at 65504, so that weights stay normal down to 2^-21
+// of the row's largest; in bf16, whose V may come near fp32's largest number, so
+// that sums of P V do not pass it.  The row sums take P unrounded.
 //
-// Steps (unit, key tile) form one list, with some empty places before each
+// The key tiles of all units form one list, with some empty places before each
 // unit's, cut into equal consecutive shares, one per CTA: lengths come from
 // device memory and the cut follows them.  A unit's parts are joined by the
 // merge kernels (prefix_merge.cu).
 //
+// A tile is worked on in steps of 64 keys, two score buffers a Q tile, so that
+// the tensor cores make one step's scores while the softmax works on the other:
+// 1.5 us a tile of keys by 256 rows, D = 128, of which the products' shared
+// memory reads take 1.33 (a 64-key product of scores reads 6 KB in the time of
+// 4).  Steps of 128 keys, whose products would need 1.11, took 1.6 to 1.75: one
+// score buffer is all that tensor memory holds of them beside O.
+//
+// What bounds it: those products, where rows are many (8 prompts' chunks of 512
+// tokens behind 3584, 32 heads: 205 us, 1.26 PFLOP/s); the keys' bytes, the
+// start (about 8 us: launch, lengths, cold instructions) and the parts' way
+// through memory (128 KB a CTA) in a decoding step (64 sequences behind 8192
+// tokens: 46 us for 171 MB with the merge).
+//
 // Roles (384 threads): warps 0 and 2 MMA issue of Q tile 0 / 1, warp 1 tile
 // copies, warp 3 walks the share, publishes its units in shared memory, copies
 // their query rows and clears the ends of V, warps 4-7 / 8-11 softmax and
-// output of Q tile 0 / 1.  Every wait is bounded as in the forward kernel.
+// output of Q tile 0 / 1.  (One warp for both tiles' products fell behind the
+// tensor cores: 300 us for those 205.)  Every wait is bounded as in the
+// forward kernel.
 //
 // A Q tile is one copy by a tensor map whose box is (heads of the group, tokens,
 // sequences), asked for as soon as the last S of the unit before is done.
@@ -56,8 +71,12 @@ static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * 168,
               "register split exceeds the launch allocation");
 
 constexpr int kUnits = 4;  // published units held at a time
-// Empty places of the list before each unit's steps, for what a part of a unit
-// takes besides them.
+// Empty places of the list before a unit's key tiles, for what a part of a unit
+// takes besides them.  64 sequences behind 8192 tokens, one new token each: 47.1
+// us, without 49.5; 32 behind 65531: 52.9 and 57.0.  None where a sequence's
+// rows meet its own keys alone (kPacked), whose Q tile may be the other one
+// than the unit's before, and whose key tiles take less time (32 sequences, 24
+// rows, 700 own keys behind 8192: 67 us; 75 with 4).
 constexpr int kOver = 4;
 
 // Tile maps: keys and values of the prefix and the sequences, whole tiles and
@@ -76,7 +95,7 @@ struct Record {
   int j0;         // first of them
   int np, plen;   // tiles and keys of the prefix in the unit's list
   int b, h, len, n_new;  // b < 0: rows of all sequences
-  int tile0;      // first Q tile
+  int tile0;      // first Q tile (-1: there is but tile 0, and it comes second)
   int dest;
   int n[2];       // key tiles each Q tile sees
 };
@@ -107,8 +126,12 @@ __device__ __forceinline__ int tile_keys(int j, int np, int plen, int len,
 }
 
 // ------------------------------------------------------------- the list
-__device__ __forceinline__ int places(int steps) {
-  return steps == 0 ? 0 : steps + kOver;
+__device__ __forceinline__ int over(const PrefixParams& p, int i) {
+  return p.mode == kPacked && i >= p.pack_blocks ? 0 : kOver;
+}
+__device__ __forceinline__ int places(const PrefixParams& p, int i,
+                                      int steps) {
+  return steps == 0 ? 0 : steps + over(p, i);
 }
 
 __device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
@@ -121,20 +144,22 @@ __device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
 
 // kFew: CTAs that take the prefix, of those of the launch; the others take the
 // sequences' own keys.  In proportion to the time that either takes an SM: a
-// step (256 rows, 128 keys) as long as kStepTiles of the few rows' tiles.
+// unit's key tile (256 rows) as long as kStepTiles of the few rows' tiles.
+// (64 sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 47, 44 and
+// 53 us; at 16 54, 51 and 52, at 64 46, 45 and 83.)
 constexpr int kStepTiles = 32;
 __device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
                                            int few) {
   if (few == 0) return p.grid;
   if (np == 0) return 0;
   const float many = static_cast<float>(p.pack_blocks * p.Hkv) *
-                     static_cast<float>(places(np) * kStepTiles);
+                     static_cast<float>(places(p, 0, np) * kStepTiles);
   const int n = static_cast<int>(p.grid * (many / (many + few)) + 0.5f);
   return max(1, min(n, p.grid - 1));
 }
 
-// A unit, or the part of one, that a CTA works on: key tiles [j0, j1) of its
-// `steps`.  Units are numbered (i, h), h fastest: i < pack_blocks rows of all
+// A unit, or the part of one, that a CTA works on: [j0, j1) of its `steps` key
+// tiles.  Units are numbered (i, h), h fastest: i < pack_blocks rows of all
 // sequences, then (b, block).
 struct Unit {
   int i, b, u, h;
@@ -183,8 +208,9 @@ struct Walk {
   }
 
   // A share of `count` places that begins at place `off` of unit w.
-  __device__ __forceinline__ bool start_at(int off, int count) {
-    const int at = off - kOver;  // steps before it (negative: empty places)
+  __device__ __forceinline__ bool start_at(const PrefixParams& p, int off,
+                                           int count) {
+    const int at = off - over(p, w.i);  // tiles before it (negative: places)
     w.j0 = max(0, at);
     w.j1 = min(w.steps, at + count);
     left = count - (w.j1 - at);
@@ -198,7 +224,7 @@ struct Walk {
     np = np_;
     const int pairs = all_pairs(p);
     if (p.mode == kFew) {  // units alike
-      const int each = places(np);
+      const int each = places(p, 0, np);
       const int total = pairs * p.Hkv * each;
       if (total == 0) return false;
       cut = make_cut(ctas, total);
@@ -209,12 +235,12 @@ struct Walk {
       w.h = unit - i * p.Hkv;
       w.len = w.n_new = 0;
       w.steps = np;
-      return start_at(x - unit * each, count);
+      return start_at(p, x - unit * each, count);
     }
     int total = 0;
     for (int i = lane; i < pairs; i += 32) {
       int len, n_new;
-      total += places(pair_steps(p, np, i, &len, &n_new));
+      total += places(p, i, pair_steps(p, np, i, &len, &n_new));
     }
 #pragma unroll
     for (int s = 16; s > 0; s /= 2)
@@ -230,7 +256,7 @@ struct Walk {
       const int i = i0 + lane;
       int len = 0, n_new = 0, steps = 0;
       if (i < pairs) steps = pair_steps(p, np, i, &len, &n_new);
-      const int t = places(steps) * p.Hkv;
+      const int t = places(p, i, steps) * p.Hkv;
       int incl = t;
 #pragma unroll
       for (int s = 1; s < 32; s *= 2) {
@@ -245,8 +271,9 @@ struct Walk {
         w.len = __shfl_sync(0xffffffffu, len, l);
         w.n_new = __shfl_sync(0xffffffffu, n_new, l);
         w.steps = __shfl_sync(0xffffffffu, steps, l);
-        w.h = off / places(w.steps);
-        return start_at(off - w.h * places(w.steps), count);
+        const int each = places(p, w.i, w.steps);
+        w.h = off / each;
+        return start_at(p, off - w.h * each, count);
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -254,7 +281,7 @@ struct Walk {
   }
 
   __device__ __forceinline__ bool next(const PrefixParams& p) {
-    if (left <= kOver) return false;
+    if (left <= 0) return false;
     if (++w.h == p.Hkv) {
       w.h = 0;
       int i = w.i;
@@ -264,9 +291,10 @@ struct Walk {
       } while (w.steps == 0);
       set_pair(p, i);
     }
+    if (left <= over(p, w.i)) return false;
     w.j0 = 0;
-    w.j1 = min(w.steps, left - kOver);
-    left -= places(w.j1);
+    w.j1 = min(w.steps, left - over(p, w.i));
+    left -= places(p, w.i, w.j1);
     return true;
   }
 
@@ -278,7 +306,7 @@ struct Walk {
 
 __device__ __forceinline__ void fill_record(const PrefixParams& p,
                                             const Walk& walk, int plen,
-                                            volatile Record* rec) {
+                                            int swap, volatile Record* rec) {
   const Unit& w = walk.w;
   rec->n_kv = w.j1 - w.j0;
   rec->j0 = w.j0;
@@ -289,18 +317,18 @@ __device__ __forceinline__ void fill_record(const PrefixParams& p,
   rec->h = w.h;
   rec->len = w.len;
   rec->n_new = w.n_new;
-  rec->tile0 = 2 * w.u;
+  rec->tile0 = 2 * w.u - swap;
   const bool whole = w.j0 == 0 && w.j1 == w.steps;
   if (p.mode == kJoint)
     rec->dest = whole ? kFinal : walk.cta + (w.j0 == 0 ? p.grid : 0);
   else
     rec->dest = w.j0 == 0 ? kBase : walk.cta;
   for (int t = 0; t < 2; ++t) {
-    const int tile = 2 * w.u + t, r0 = tile * p.tile_rows;
+    const int tile = 2 * w.u - swap + t, r0 = tile * p.tile_rows;
     int hi = 0;
     if (w.b < 0) {
       if (tile * p.tile_seqs < p.B) hi = np;
-    } else if (r0 < w.n_new * p.group) {
+    } else if (tile >= 0 && r0 < w.n_new * p.group) {
       hi = np + tiles_seen(p, w.len, w.n_new, r0, r0 + p.tile_rows);
     }
     rec->n[t] = max(0, min(hi, w.j1) - w.j0);
@@ -337,7 +365,9 @@ __device__ __forceinline__ int row_of(const PrefixParams& p,
   const int tile = rec->tile0 + t;
   if (rec->b >= 0) {
     *row = tile * p.tile_rows + i;
-    return i < p.tile_rows && *row < rec->n_new * p.group ? rec->b : -1;
+    return tile >= 0 && i < p.tile_rows && *row < rec->n_new * p.group
+               ? rec->b
+               : -1;
   }
   const int s = fast_div(i, p.fd_rows);  // sequence within the tile
   const int b = tile * p.tile_seqs + s;
@@ -553,6 +583,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           walk.take(p, static_cast<int>(blockIdx.x), ctas, np, lane);
       int4 split = make_int4(0, 0, 0, 0);
       int published = 0;
+      // A sequence's rows that fill one Q tile at most take either in turn, so
+      // that a unit's first steps go along with the last of the unit before.
+      const bool turns = p.rows <= p.tile_rows;
+      int swap = 1;
       // Units are published one ahead of the one at hand (all roles can end
       // every unit before that without this warp, so that the wait ends).
       auto publish = [&] {
@@ -560,10 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k >= kUnits)
           ok = wait(bar_ufree + 8 * (k % kUnits), k / kUnits - 1, 1);
         if (!ok) return;
+        swap = turns && more && walk.w.b >= 0 ? swap ^ 1 : 0;
         if (lane == 0) {
           volatile Record* rec = records + k % kUnits;
           if (more)
-            fill_record(p, walk, plen, rec);
+            fill_record(p, walk, plen, swap, rec);
           else
             rec->n_kv = 0;
           ptx::mbar_arrive(bar_unit + 8 * (k % kUnits));
@@ -592,11 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q_tokens = fast_div(p.tile_rows, p.fd_group);
       const uint32_t q_bytes =
           (p.mode == kJoint ? p.tile_rows : p.tile_seqs * p.rows) * D * 2;
-      for (int k = 0; ok; ++k) {
+      auto load_q = [&](int k) {
         volatile Record* rec = records + k % kUnits;
-        const int n = rec->n_kv;
-        if (n == 0) break;
-        const int j0 = rec->j0, unit_np = rec->np, len = rec->len;
         const int n0 = rec->n[0], n1 = rec->n[1];
         const int b = rec->b, h = rec->h, tile0 = rec->tile0;
 #pragma unroll
@@ -615,9 +647,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                           b < 0 ? (tile0 + t) * p.tile_seqs : b);
           }
         }
+      };
+      int loaded = 0;  // units whose query rows are asked for
+      for (int k = 0; ok; ++k) {
+        volatile Record* rec = records + k % kUnits;
+        const int n = rec->n_kv;
+        if (n == 0) break;
+        const int j0 = rec->j0, unit_np = rec->np, len = rec->len;
+        if (loaded == k) {
+          load_q(k);
+          ++loaded;
+        }
         if (!ok) break;
         publish();
         if (!ok) break;
+        // The next unit's, where they take the other tile (which the unit
+        // before this one had: all its ends are cleared).
+        volatile Record* next = records + (k + 1) % kUnits;
+        if (turns && rec->b >= 0 && next->n_kv > 0) {
+          load_q(k + 1);
+          ++loaded;
+          if (!ok) break;
+        }
         for (int j = 0; j < n; ++j) {
           bool own;
           const int valid = tile_keys(j0 + j, unit_np, plen, len, &own);
@@ -1027,7 +1078,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     p.rows;
           at += row;
         } else {
-          at = static_cast<long long>(dest) * kUnitRows + t * kTM + r;
+          at = static_cast<long long>(dest) * kUnitRows +
+               ((rec->tile0 + t) & 1) * kTM + r;
         }
         if (n > 0) {
 #pragma unroll

@@ -1,5 +1,13 @@
-// Joins the parts of a query row's attention behind a shared prefix.  With part s the average O_s and the log-sum-exp L_s of its keys,
+// Joins the parts of a query row's attention behind a shared prefix.  With part
+// s the average O_s and the log-sum-exp L_s of its keys (in log2 units),
 //   O = sum_s 2^(L_s - m) O_s / sum_s 2^(L_s - m),  LSE = m + log2(the sum).
+// All in fp32; one rounding, to the output.
+//
+// What bounds it: a chain of loads (lengths, where the parts are, their L, their
+// O), some 4 us, each as far as a cold cache; so the O are asked for before
+// their factors are known, and rows are spread over warps where they are few.
+// Where they are many, warps take four at once: 32768 rows of 128, two parts
+// each, in 18 us (a row a warp 31).
 #include "prefix_common.cuh"
 
 namespace attn {
@@ -13,6 +21,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kAhead = 8;  // parts whose O a warp has in flight
+// Rows an SM from which on warps take four (2520 rows in all, 35 a head: 24 us
+// of the whole call, 27 by four).
+constexpr long long kManyRows = 32;
 
 // What a warp has of a row: the sum over its parts, relative to 2^mx.
 struct Sum {
@@ -109,8 +120,58 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, long long row,
                               : (t.mx + log2f(t.sum)) * 0.69314718055994531f;
 }
 
-// kFew and kPacked: every row, with the parts over the prefix first, by
-// row_warps warps.
+// What the rows of a K/V head of a sequence have in common (kFew, kPacked):
+// the CTAs (or warps) and numbers of their parts over the prefix and over the
+// own keys.
+struct Parts {
+  int2 pre, own;
+  long long base, bh;
+  int in_unit;
+
+  __device__ __forceinline__ Parts(const PrefixParams& p, int bh_, int b,
+                                   int h, int np, int len, int n_new) {
+    bh = bh_;
+    const int tile = fast_div(b, p.fd_tile_seqs);
+    in_unit = tile % 2 * kTM + (b - tile * p.tile_seqs) * p.rows;
+    base = (static_cast<long long>(h) * p.B + b) * p.rows;
+    pre = own = make_int2(0, 0);
+    if (np > 0) pre = p.info[static_cast<long long>(tile / 2) * p.Hkv + h];
+    if (p.mode == kFew) {
+      if (len > 0) own = p.own_info[bh];
+    } else if (tiles_seen(p, len, n_new, 0, p.rows) > 0) {
+      own = p.info[(static_cast<long long>(p.pack_blocks) + b) * p.Hkv + h];
+    }
+  }
+  // Row r's part s: those over the prefix first.
+  __device__ __forceinline__ void at(const PrefixParams& p, int s, int r,
+                                     int cols, const float4** o,
+                                     const float** lse2) const {
+    const float *from = p.base_o, *from2 = p.base_lse2;
+    long long i;
+    if (s == 0 && pre.y > 0) {
+      i = base + r;
+    } else if (s < pre.y) {
+      from = p.slot_o;
+      from2 = p.slot_lse2;
+      i = static_cast<long long>(pre.x + s) * kUnitRows + in_unit + r;
+    } else if (p.mode == kFew) {
+      from = p.few_o;
+      from2 = p.few_lse2;
+      i = (static_cast<long long>(own.x + s - pre.y) + bh) *
+              few_rows(p.rows) + r;
+    } else if (s == pre.y) {
+      i = (static_cast<long long>(p.Hkv) * p.B + bh) * p.rows + r;
+    } else {
+      from = p.slot_o;
+      from2 = p.slot_lse2;
+      i = static_cast<long long>(own.x + s - pre.y) * kUnitRows + r;
+    }
+    *o = reinterpret_cast<const float4*>(from) + i * cols;
+    *lse2 = from2 + i;
+  }
+};
+
+// kFew and kPacked, where rows are few: each by row_warps warps.
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kThreads, 4)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p,
@@ -120,66 +181,30 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const long long id =
       (static_cast<long long>(blockIdx.x) * kWarps + warp) / row_warps;
-  const int R = p.rows;
-  const long long all = static_cast<long long>(p.B) * R;  // rows of a head
-  const bool in = id < all * p.Hkv;
   // (b, h, r), r fastest.
+  const bool in = id < static_cast<long long>(p.B) * p.rows * p.Hkv;
   const int bh =
       !in ? 0
       : id < 0x7fffffff ? fast_div(static_cast<int>(id), p.fd_rows)
-                        : static_cast<int>(id / R);
-  const int r = in ? static_cast<int>(id - static_cast<long long>(bh) * R) : 0;
+                        : static_cast<int>(id / p.rows);
+  const int r =
+      in ? static_cast<int>(id - static_cast<long long>(bh) * p.rows) : 0;
   const int b = fast_div(bh, p.fd_hkv), h = bh - b * p.Hkv;
   const int len = kv8::seq_len(p, b), n_new = kv8::seq_new(p, b);
   const int np = prefix_tiles(p);
-  // Its Q tiles over the prefix and over the own keys, and places in their
-  // units.
-  const int tile = fast_div(b, p.fd_tile_seqs);
-  const int in_unit = tile % 2 * kTM + (b - tile * p.tile_seqs) * R + r;
-  const int own_tile = fast_div(r, p.fd_tile_rows);
-  const int own_in_unit =
-      own_tile % 2 * kTM + r - own_tile * p.tile_rows;
-  const int u = own_tile / 2, r0 = u * 2 * p.tile_rows;
   // (Lengths are read ahead of the wait: the kernels ahead do not write them.)
   kv8::start_after_previous();
   const bool live = in && r < n_new * p.group;
-  int2 pre = make_int2(0, 0), own = make_int2(0, 0);
+  Sum t{kNone, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int w = warp % row_warps;
   if (live) {
-    if (np > 0)
-      pre = p.info[static_cast<long long>(tile / 2) * p.Hkv + h];
-    if (p.mode == kFew) {
-      if (len > 0) own = p.own_info[bh];
-    } else if (tiles_seen(p, len, n_new, r0, r0 + 2 * p.tile_rows) > 0) {
-      own = p.info[(static_cast<long long>(p.pack_blocks) +
-                    static_cast<long long>(b) * p.row_blocks + u) * p.Hkv + h];
-    }
+    const Parts parts(p, bh, b, h, np, len, n_new);
+    const int n = parts.pre.y + parts.own.y;
+    t = add_parts<D>(n * w / row_warps, n * (w + 1) / row_warps, lane,
+                     [&](int s, const float4** o, const float** lse2) {
+                       parts.at(p, s, r, D / 4, o, lse2);
+                     });
   }
-  auto at = [&](int s, const float4** o, const float** lse2) {
-    const float *from = p.base_o, *from2 = p.base_lse2;
-    long long i;
-    if (s == 0 && pre.y > 0) {
-      i = h * all + static_cast<long long>(b) * R + r;
-    } else if (s < pre.y) {
-      from = p.slot_o;
-      from2 = p.slot_lse2;
-      i = static_cast<long long>(pre.x + s) * kUnitRows + in_unit;
-    } else if (p.mode == kFew) {
-      from = p.few_o;
-      from2 = p.few_lse2;
-      i = (static_cast<long long>(own.x + s - pre.y) + bh) * few_rows(R) + r;
-    } else if (s == pre.y) {
-      i = p.Hkv * all + static_cast<long long>(bh) * R + r;
-    } else {
-      from = p.slot_o;
-      from2 = p.slot_lse2;
-      i = static_cast<long long>(own.x + s - pre.y) * kUnitRows +
-          own_in_unit;
-    }
-    *o = reinterpret_cast<const float4*>(from) + i * (D / 4);
-    *lse2 = from2 + i;
-  };
-  const int n = pre.y + own.y, w = warp % row_warps;
-  Sum t = add_parts<D>(n * w / row_warps, n * (w + 1) / row_warps, lane, at);
   if (row_warps > 1) {
     if (lane == 0) sm_sum[warp] = make_float2(t.mx, t.sum);
     if (lane < D / 4) sm_acc[warp][lane] = t.acc;
@@ -202,14 +227,132 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (live) write_row<D, kBF16>(p, q_row_index(p, b, h, r), t, lane);
 }
 
-// kJoint: the rows of each CTA's unit that went on behind it, four by a warp.
+// `n` rows, kJoinRows at most, of `parts` parts each by one warp, all rows at
+// once: at(s, i, &o, &lse2) as above for row i, row_at(i) its row of O.
 constexpr int kJoinRows = 4;
+constexpr int kJoinParts = 32 / kJoinRows;  // whose LSEs a warp reads at once
+
+template <int D, bool kBF16, class At, class RowAt>
+__device__ __forceinline__ void join_rows(const PrefixParams& p, int n,
+                                          int parts, int lane, At at,
+                                          RowAt row_at) {
+  constexpr int kCols = D / 4;
+  constexpr int kGroups = 32 / kCols;  // rows a warp reads at a time
+  constexpr int kLoads = kJoinRows / kGroups;
+  constexpr int kBatch = kAhead / kLoads;  // parts in flight
+  const int col = lane % kCols, sub = lane / kCols;
+  const int i_lane = lane / kJoinParts, s_lane = lane % kJoinParts;
+  float mx = kNone, sum = 0.f;  // of the lane's row, its share of the sum
+  float4 acc[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int s0 = 0; s0 < parts; s0 += kJoinParts) {
+    const int count = min(kJoinParts, parts - s0);
+    const float4* o = nullptr;
+    float x = -INFINITY, f_all = 0.f;
+    if (s_lane < count && i_lane < n) {
+      const float* lse2;
+      at(s0 + s_lane, i_lane, &o, &lse2);
+      x = *lse2;
+    }
+    const unsigned long long place = reinterpret_cast<unsigned long long>(o);
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+      float4 y[kBatch][kLoads];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const float4* from = reinterpret_cast<const float4*>(__shfl_sync(
+              0xffffffffu, place,
+              (j * kGroups + sub) * kJoinParts + (k0 + k) % kJoinParts));
+          y[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 + k < count && from != nullptr) y[k][j] = from[col];
+        }
+      if (k0 == 0) {
+        float m = fmaxf(mx, x);
+#pragma unroll
+        for (int k = kJoinParts / 2; k > 0; k /= 2)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const float before = ptx::ex2(mx - m);
+        f_all = ptx::ex2(x - m);
+        mx = m;
+        sum = sum * before + f_all;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const float f = __shfl_sync(0xffffffffu, before,
+                                      (j * kGroups + sub) * kJoinParts);
+          acc[j].x *= f;
+          acc[j].y *= f;
+          acc[j].z *= f;
+          acc[j].w *= f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const float f = __shfl_sync(
+              0xffffffffu, f_all,
+              (j * kGroups + sub) * kJoinParts + (k0 + k) % kJoinParts);
+          if (k0 + k < count) add(acc[j], y[k][j], f);
+        }
+    }
+  }
+#pragma unroll
+  for (int k = kJoinParts / 2; k > 0; k /= 2)
+    sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int i = j * kGroups + sub;
+    const float f = __shfl_sync(0xffffffffu, inv, i * kJoinParts);
+    if (i >= n) continue;
+    uint2 out;
+    out.x = ptx::pack2<kBF16>(acc[j].x * f, acc[j].y * f);
+    out.y = ptx::pack2<kBF16>(acc[j].z * f, acc[j].w * f);
+    reinterpret_cast<uint2*>(p.o + row_at(i) * D)[col] = out;
+  }
+  if (s_lane == 0 && i_lane < n && p.lse != nullptr)
+    p.lse[row_at(i_lane)] =
+        sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+}
+
+// kFew and kPacked, where rows are many: four of a (sequence, K/V head) by a
+// warp.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kJoinThreads, 8)
+    prefix_rows_kernel(const __grid_constant__ PrefixParams p, int chunks,
+                       FastDiv fd_chunks) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int id = blockIdx.x * kJoinWarps + warp;
+  const bool in = id < chunks;
+  const int bh = in ? fast_div(id, fd_chunks) : 0;
+  const int b = fast_div(bh, p.fd_hkv), h = bh - b * p.Hkv;
+  const int len = kv8::seq_len(p, b), n_new = kv8::seq_new(p, b);
+  const int np = prefix_tiles(p);
+  kv8::start_after_previous();
+  if (!in) return;
+  const int r0 =
+      (id - bh * ((p.rows + kJoinRows - 1) / kJoinRows)) * kJoinRows;
+  const int n = min(kJoinRows, n_new * p.group - r0);
+  if (n <= 0) return;
+  const Parts parts(p, bh, b, h, np, len, n_new);
+  join_rows<D, kBF16>(
+      p, n, parts.pre.y + parts.own.y, lane,
+      [&](int s, int i, const float4** o, const float** lse2) {
+        parts.at(p, s, r0 + i, D / 4, o, lse2);
+      },
+      [&](int i) { return q_row_index(p, b, h, r0 + i); });
+}
+
+// kJoint: the rows of each CTA's unit that went on behind it.
 constexpr int kParts = kUnitRows / kJoinWarps / kJoinRows;  // CTAs per unit
 
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kJoinThreads, 8)
     prefix_join_kernel(const __grid_constant__ PrefixParams p) {
-  constexpr int kCols = D / 4;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x / kParts;
   const int i0 =
@@ -222,50 +365,17 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
   const int tile = i0 / kTM, in_tile = i0 % kTM;
   const int r0 = (2 * split.z + tile) * p.tile_rows + in_tile;
   const int n = min(kJoinRows, min(p.tile_rows - in_tile, rows - r0));
-  auto place = [&](int s, int i) {
-    return static_cast<long long>(s == 0 ? p.grid + cta : cta + s) *
-               kUnitRows + i;
-  };
-  if (parts == 2 && D == 128) {
-    // The usual case, all rows at once: lane 2 i + s has row i's part s.
-    float x = -INFINITY;
-    if (lane < 2 * n) x = p.slot_lse2[place(lane % 2, i0 + lane / 2)];
-    float4 y[kJoinRows][2];
-#pragma unroll
-    for (int i = 0; i < kJoinRows; ++i)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        y[i][s] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n)
-          y[i][s] = reinterpret_cast<const float4*>(
-              p.slot_o)[place(s, i0 + i) * kCols + lane % kCols];
-      }
-    const float m = fmaxf(kNone, fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1)));
-    const float f = ptx::ex2(x - m);
-    const float sum = f + __shfl_xor_sync(0xffffffffu, f, 1);
-#pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) {
-      Sum t;
-      t.mx = __shfl_sync(0xffffffffu, m, 2 * i);
-      t.sum = __shfl_sync(0xffffffffu, sum, 2 * i);
-      t.acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        add(t.acc, y[i][s], __shfl_sync(0xffffffffu, f, 2 * i + s));
-      if (i < n)
-        write_row<D, kBF16>(p, q_row_index(p, b, h, r0 + i), t, lane);
-    }
-    return;
-  }
-  for (int i = 0; i < n; ++i) {
-    const Sum t = add_parts<D>(
-        0, parts, lane, [&](int s, const float4** o, const float** lse2) {
-          const long long j = place(s, i0 + i);
-          *o = reinterpret_cast<const float4*>(p.slot_o) + j * kCols;
-          *lse2 = p.slot_lse2 + j;
-        });
-    write_row<D, kBF16>(p, q_row_index(p, b, h, r0 + i), t, lane);
-  }
+  if (n <= 0) return;
+  join_rows<D, kBF16>(
+      p, n, parts, lane,
+      [&](int s, int i, const float4** o, const float** lse2) {
+        const long long j =
+            static_cast<long long>(s == 0 ? p.grid + cta : cta + s) *
+                kUnitRows + i0 + i;
+        *o = reinterpret_cast<const float4*>(p.slot_o) + j * (D / 4);
+        *lse2 = p.slot_lse2 + j;
+      },
+      [&](int i) { return q_row_index(p, b, h, r0 + i); });
 }
 
 template <int D, bool kBF16>
@@ -274,9 +384,18 @@ cudaError_t launch(PrefixParams p, cudaStream_t stream) {
     return kv8::launch_pdl(prefix_join_kernel<D, kBF16>,
                            static_cast<long long>(p.grid) * kParts,
                            kJoinThreads, 0, stream, p);
-  const long long rows = static_cast<long long>(p.B) * p.rows * p.Hkv;
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  const long long rows = heads * p.rows;
+  const int per_head = (p.rows + kJoinRows - 1) / kJoinRows;
+  if (p.rows >= kJoinRows && rows > kManyRows * p.grid)
+    return kv8::launch_pdl(prefix_rows_kernel<D, kBF16>,
+                           (heads * per_head + kJoinWarps - 1) / kJoinWarps,
+                           kJoinThreads, 0, stream, p,
+                           static_cast<int>(heads * per_head),
+                           make_fast_div(per_head));
   // Warps a row: as many as make the machine's warps busy, rows having some 20
-  // parts where they are few.
+  // parts where they are few (8 sequences behind 4096 tokens: 18.2 us of the
+  // whole call, 20.6 by a warp a row; 32 behind 65531: 52 and 57).
   int row_warps = kWarps;
   while (row_warps > 1 && rows * row_warps > 32LL * p.grid)
     row_warps /= 2;
