@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks(D))
 // Reads two rows and writes one, with twice the forward's arithmetic between: a
 // training step's 570 MB take 106 us, 5.4 TB/s (a copy's rate would be 85).  Rows
 // run ahead through shared memory, as registers have no room for them beside the
-// weights' sums (119 us with loads just ahead of their use, 127 with the next
+// weights' sums (121 us with loads just ahead of their use, 127 with the next
 // row's in registers).  Each CTA keeps to a block of heads and walks over tokens,
 // so that the weights' sums stay in registers; they meet as fp32 in a fixed
 // order: results do not change from run to run.
