@@ -223,8 +223,7 @@ __device__ __forceinline__ int seq_new(const Params& p, int b) {
 }
 // Visible tokens of row r (token-major: row r = token r / group, head
 // r % group) of a sequence.
-template <class Params>
-__device__ __forceinline__ int row_end(const Params& p, int len, int n_new,
+__device__ __forceinline__ int row_end(const FwdParams& p, int len, int n_new,
                                        int r) {
   if (!p.causal) return len;
   return min(len, max(0, len - n_new + r / p.group + 1));
@@ -240,8 +239,8 @@ __device__ __forceinline__ int places(int len) {
 
 // Places before sequence `seq` and of all sequences, for every lane of the
 // calling warp.
-template <int kKeys, int kOver, class Params>
-__device__ __forceinline__ int list_tiles(const Params& p, int seq,
+template <int kKeys, int kOver>
+__device__ __forceinline__ int list_tiles(const FwdParams& p, int seq,
                                           int lane, int* before) {
   int t = 0, pre = 0;
   for (int b = lane; b < p.B; b += 32) {
@@ -270,8 +269,8 @@ struct Cut {
   }
 };
 // kLeast places a CTA are the finest cut.
-template <int kLeast, class Params>
-__device__ __forceinline__ Cut make_cut(const Params& p, int total) {
+template <int kLeast>
+__device__ __forceinline__ Cut make_cut(const FwdParams& p, int total) {
   Cut c;
   c.n = max(1, min(p.grid, (total + kLeast - 1) / kLeast));
   c.q = total / c.n;
@@ -288,8 +287,8 @@ struct Segment {
 };
 
 // CTA's share: its number of places (0: none) and first segment.
-template <int kKeys, int kOver, int kLeast, class Params>
-__device__ __forceinline__ int take_share(const Params& p, int cta,
+template <int kKeys, int kOver, int kLeast>
+__device__ __forceinline__ int take_share(const FwdParams& p, int cta,
                                           int lane, Segment* s) {
   int first = 0, count = 0, base = 0;
   if (p.B > 32) {
@@ -333,8 +332,8 @@ __device__ __forceinline__ int take_share(const Params& p, int cta,
   return 0;
 }
 
-template <int kKeys, int kOver, class Params>
-__device__ __forceinline__ void next_segment(const Params& p, Segment& c) {
+template <int kKeys, int kOver>
+__device__ __forceinline__ void next_segment(const FwdParams& p, Segment& c) {
   c.pos = c.end + kOver;
   if (++c.h == p.Hkv) {
     c.h = 0;

@@ -120,6 +120,14 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, long long row,
                               : (t.mx + log2f(t.sum)) * 0.69314718055994531f;
 }
 
+// First part and number of parts within `n` slots: a kernel ahead whose wait ran
+// out may not have written them.
+__device__ __forceinline__ int2 within(int2 x, int n) {
+  x.y = min(max(x.y, 0), n);
+  x.x = min(max(x.x, 0), n - x.y);
+  return x;
+}
+
 // What the rows of a K/V head of a sequence have in common (kFew, kPacked):
 // the CTAs (or warps) and numbers of their parts over the prefix and over the
 // own keys.
@@ -135,11 +143,15 @@ struct Parts {
     in_unit = tile % 2 * kTM + (b - tile * p.tile_seqs) * p.rows;
     base = (static_cast<long long>(h) * p.B + b) * p.rows;
     pre = own = make_int2(0, 0);
-    if (np > 0) pre = p.info[static_cast<long long>(tile / 2) * p.Hkv + h];
+    if (np > 0)
+      pre = within(p.info[static_cast<long long>(tile / 2) * p.Hkv + h],
+                   p.grid);
     if (p.mode == kFew) {
       if (len > 0) own = p.own_info[bh];
     } else if (tiles_seen(p, len, n_new, 0, p.rows) > 0) {
-      own = p.info[(static_cast<long long>(p.pack_blocks) + b) * p.Hkv + h];
+      own = within(
+          p.info[(static_cast<long long>(p.pack_blocks) + b) * p.Hkv + h],
+          p.grid);
     }
   }
   // Row r's part s: those over the prefix first.

@@ -441,6 +441,20 @@ def test_many_sequences():
           "f16")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("B,Hkv,group,Sq,D", [
+    (60, 9, 4, 5, 128), (50, 10, 3, 40, 64), (1, 600, 2, 10, 128),
+    (1, 500, 2, 60, 64), (3, 300, 1, 18, 128)])
+def test_several_units_a_block(B, Hkv, group, Sq, D, dtype):
+    """More (sequence, head) units of one Q tile than thread blocks, of one
+    key tile to four, of lengths that end anywhere in a tile; causal and not."""
+    lens = [Sq + 83 * i % 431 for i in range(B)]
+    c = make(B, Hkv, D, 200, 201, lens, 480, dtype)
+    check(c, Hkv * group, Sq, dtype)
+    new = [(Sq - 5 * i) % (Sq + 1) for i in range(B)]
+    check(c, Hkv * group, Sq, dtype, new, causal=False)
+
+
 def test_calls_in_a_row_share_a_workspace():
     """Different shapes one behind the other on one stream and workspace."""
     c = make(4, 2, 64, 500, 500, [200, 210, 300, 290], 300, "f16")
