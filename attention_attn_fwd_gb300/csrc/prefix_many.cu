@@ -37,7 +37,7 @@
 // tokens behind 3584, 32 heads: 205 us, 1.26 PFLOP/s); the keys' bytes, the
 // start (about 8 us: launch, lengths, cold instructions) and the parts' way
 // through memory (128 KB a CTA) in a decoding step (64 sequences behind 8192
-// tokens: 46 us for 171 MB with the merge).
+// tokens: 43 us for 171 MB with the merge).
 //
 // Roles (384 threads): warps 0 and 2 MMA issue of Q tile 0 / 1, warp 1 tile
 // copies, warp 3 walks the share, publishes its units in shared memory, copies
@@ -73,7 +73,7 @@ static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * 168,
 constexpr int kUnits = 4;  // published units held at a time
 // Empty places of the list before a unit's key tiles, for what a part of a unit
 // takes besides them.  64 sequences behind 8192 tokens, one new token each: 47.1
-// us, without 49.5; 32 behind 65531: 52.9 and 57.0.  None where a sequence's
+// us, without 49.5; 32 behind 65531: 52.9 and 57.0 (before other steps).  None where a sequence's
 // rows meet its own keys alone (kPacked), whose Q tile may be the other one
 // than the unit's before, and whose key tiles take less time (32 sequences, 24
 // rows, 700 own keys behind 8192: 67 us; 75 with 4).
@@ -145,8 +145,10 @@ __device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
 // kFew: CTAs that take the prefix, of those of the launch; the others take the
 // sequences' own keys.  In proportion to the time that either takes an SM: a
 // unit's key tile (256 rows) as long as kStepTiles of the few rows' tiles.
-// (64 sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 47, 44 and
-// 53 us; at 16 54, 51 and 52, at 64 46, 45 and 83.)
+// (64 sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 43.2, 43.6
+// and 51.5 us; at 24 47, 45 and 52, at 64 46, 45 and 83.)  What is left over goes
+// to the own keys: rounded to the nearest, 32 sequences of one own token behind
+// 65536 took 61 us of 49, all own keys meeting one CTA.
 constexpr int kStepTiles = 32;
 __device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
                                            int few) {
@@ -154,7 +156,7 @@ __device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
   if (np == 0) return 0;
   const float many = static_cast<float>(p.pack_blocks * p.Hkv) *
                      static_cast<float>(places(p, 0, np) * kStepTiles);
-  const int n = static_cast<int>(p.grid * (many / (many + few)) + 0.5f);
+  const int n = static_cast<int>(p.grid * (many / (many + few)));
   return max(1, min(n, p.grid - 1));
 }
 
