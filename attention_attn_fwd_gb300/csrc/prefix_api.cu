@@ -102,7 +102,8 @@ bool counts_fit(const Sizes& z, const Plan& p) {
 }
 
 struct Workspace {
-  size_t base_o, base_lse2, slot_o, slot_lse2, info, split, few_o, few_lse2, own_info;
+  size_t base_o, base_lse2, slot_o, slot_lse2, info, split;
+  size_t few_o, few_lse2, own_info;
   size_t total;
 };
 
@@ -114,7 +115,8 @@ Workspace workspace_layout(const Sizes& z, const Plan& p) {
   const size_t slots = static_cast<size_t>(p.grid) * (joint ? 2 : 1) *
                        attn::prefix::kUnitRows;
   const size_t units =
-      joint ? 0 : static_cast<size_t>(p.pack_blocks + z.B * p.row_blocks) * z.Hkv;
+      joint ? 0
+            : static_cast<size_t>(p.pack_blocks + z.B * p.row_blocks) * z.Hkv;
   const size_t few =
       p.mode == attn::prefix::kFew
           ? (static_cast<size_t>(p.grid) * attn::prefix::kFewWarps +

@@ -20,17 +20,17 @@ constexpr int kFewWarps = 8;         // of a block that works on few rows
 
 // How the query rows meet the keys (R rows of a K/V head per sequence, row r =
 // token r / group, head r % group):
-//   kFew    R <= 16: units of two Q tiles, each the rows of as many sequences as
-//           it holds, over the prefix; the sequences' own keys by thread blocks
-//           set aside for them (prefix_few.cuh);
+//   kFew    R <= 16: units of two Q tiles, each the rows of as many sequences
+//           as it holds, over the prefix; the sequences' own keys by thread
+//           blocks set aside for them (prefix_few.cuh);
 //   kPacked R <= 128, several sequences: such units over the prefix, and units
 //           of each sequence over its own keys;
 //   kJoint  units of each sequence over the prefix and its own keys in turn.
-// 8 K/V heads of 128, 700 own keys behind 8192: 32 sequences of 4, 8 and 16 rows
-// take 34, 40 and 46 us by kFew, 48, 53 and 61 by kPacked (4 sequences: 22, 22
-// and 27, by kPacked 22, 22 and 23); 24, 64 and 128 rows take 67, 95 and 144 by
-// kPacked, 194, 195 and 197 by kJoint (4 sequences: 23, 28 and 35; 40, 41 and 44).
-// More rows fill a Q tile without others'.
+// 8 K/V heads of 128, 700 own keys behind 8192: 32 sequences of 4, 8 and 16
+// rows take 34, 40 and 46 us by kFew, 48, 53 and 61 by kPacked (4 sequences: 22,
+// 22 and 27, by kPacked 22, 22 and 23); 24, 64 and 128 rows take 67, 95 and 144
+// by kPacked, 194, 195 and 197 by kJoint (4 sequences: 23, 28 and 35; 40, 41 and
+// 44).  More rows fill a Q tile without others'.
 enum Mode { kFew = 0, kPacked = 1, kJoint = 2 };
 
 struct PrefixParams {
@@ -84,10 +84,10 @@ __device__ __forceinline__ long long q_row_index(const PrefixParams& p, int b,
   return (static_cast<long long>(b) * p.Hq + h * p.group + hd) * p.Sq + tok;
 }
 
-// The few-row work's tiles: 4 KB of keys; and empty places before a segment
-// (64 sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 43, 44 and
-// 51 us; with 2 44, 44 and 52, and 32 sequences of one own token behind 65536
-// 60 for 49; with 5 45, 44 and 52).
+// The few-row work's tiles: 4 KB of keys; and empty places before a segment (64
+// sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 43, 44 and 51
+// us; with 2 44, 44 and 52, and 32 sequences of one own token behind 65536 60
+// for 49; with 5 45, 44 and 52).
 template <int D>
 __host__ __device__ constexpr int few_keys() {
   return 2048 / D;

@@ -21,8 +21,8 @@
 // warps are in flight or worked on, all that an SM holds.
 //
 // What bounds it: the bytes of K and V.  256 sequences of 300 own tokens, 16
-// heads of 64 (157 MB with a prefix of 2048, which takes some CTAs): 36 us and 7
-// of the merge, of which loads can go for about 28; the rest is the start.
+// heads of 64 (157 MB with a prefix of 2048, which takes some CTAs): 36 us and
+// 7 of the merge, of which loads can go for about 28; the rest is the start.
 #pragma once
 
 #include "prefix_common.cuh"

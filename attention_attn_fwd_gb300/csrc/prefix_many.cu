@@ -12,14 +12,14 @@
 //
 // S = Q K^T and O += P V run as tcgen05 MMAs with fp32 accumulators in TMEM, K
 // and V by tensor-map copies into a ring of 128-byte-swizzled tiles.  A tile
-// that lengths end in is copied in boxes of 16 rows, its P V has as many
-// 16-key steps, and a warp clears V's rows between the length and the last
-// step's end (what lies there was never written and may be NaN; P is 0 there).
-// P is rounded to the inputs' type, the tensor cores' operand (off by 2^-11
-// relative at most in fp16, 2^-8 in bf16, as O itself) and held times 2^kShift:
-// in fp16, whose numbers end at 65504, so that weights stay normal down to 2^-21
-// of the row's largest; in bf16, whose V may come near fp32's largest number, so
-// that sums of P V do not pass it.  The row sums take P unrounded.
+// that lengths end in is copied in boxes of 16 rows, its P V has as many 16-key
+// steps, and a warp clears V's rows between the length and the last step's end
+// (what lies there was never written and may be NaN; P is 0 there). P is
+// rounded to the inputs' type, the tensor cores' operand (off by 2^-11 relative
+// at most in fp16, 2^-8 in bf16, as O itself) and held times 2^kShift: in fp16,
+// whose numbers end at 65504, so that weights stay normal down to 2^-21 of the
+// row's largest; in bf16, whose V may come near fp32's largest number, so that
+// sums of P V do not pass it.  The row sums take P unrounded.
 //
 // The key tiles of all units form one list, with some empty places before each
 // unit's, cut into equal consecutive shares, one per CTA: lengths come from
@@ -46,10 +46,10 @@
 // tensor cores: 300 us for those 205.)  Every wait is bounded as in the
 // forward kernel.
 //
-// A Q tile is one copy by a tensor map whose box is (heads of the group, tokens,
-// sequences), asked for as soon as the last S of the unit before is done.
-// (Gathered by the softmax threads, a row each, it took them 3 to 5 us between
-// two units; by one warp's 16-byte copies 2.5 to 4.)
+// A Q tile is one copy by a tensor map whose box is (heads of the group,
+// tokens, sequences), asked for as soon as the last S of the unit before is
+// done. (Gathered by the softmax threads, a row each, it took them 3 to 5 us
+// between two units; by one warp's 16-byte copies 2.5 to 4.)
 #include "attn_sync.cuh"
 #include "prefix_common.cuh"
 #include "prefix_few.cuh"
@@ -72,11 +72,11 @@ static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * 168,
 
 constexpr int kUnits = 4;  // published units held at a time
 // Empty places of the list before a unit's key tiles, for what a part of a unit
-// takes besides them.  64 sequences behind 8192 tokens, one new token each: 47.1
-// us, without 49.5; 32 behind 65531: 52.9 and 57.0 (before other steps).  None where a sequence's
-// rows meet its own keys alone (kPacked), whose Q tile may be the other one
-// than the unit's before, and whose key tiles take less time (32 sequences, 24
-// rows, 700 own keys behind 8192: 67 us; 75 with 4).
+// takes besides them.  64 sequences behind 8192 tokens, one new token each:
+// 47.1 us, without 49.5; 32 behind 65531: 52.9 and 57.0 (before other steps).
+// None where a sequence's rows meet its own keys alone (kPacked), whose Q tile
+// may be the other one than the unit's before, and whose key tiles take less
+// time (32 sequences, 24 rows, 700 own keys behind 8192: 67 us; 75 with 4).
 constexpr int kOver = 4;
 
 // Tile maps: keys and values of the prefix and the sequences, whole tiles and
@@ -144,11 +144,11 @@ __device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
 
 // kFew: CTAs that take the prefix, of those of the launch; the others take the
 // sequences' own keys.  In proportion to the time that either takes an SM: a
-// unit's key tile (256 rows) as long as kStepTiles of the few rows' tiles.
-// (64 sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 43.2, 43.6
-// and 51.5 us; at 24 47, 45 and 52, at 64 46, 45 and 83.)  What is left over goes
-// to the own keys: rounded to the nearest, 32 sequences of one own token behind
-// 65536 took 61 us of 49, all own keys meeting one CTA.
+// unit's key tile (256 rows) as long as kStepTiles of the few rows' tiles. (64
+// sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 43.2, 43.6
+// and 51.5 us; at 24 47, 45 and 52, at 64 46, 45 and 83.)  What is left over
+// goes to the own keys: rounded to the nearest, 32 sequences of one own token
+// behind 65536 took 61 us of 49, all own keys meeting one CTA.
 constexpr int kStepTiles = 32;
 __device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
                                            int few) {

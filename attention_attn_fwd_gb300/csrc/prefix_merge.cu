@@ -3,11 +3,11 @@
 //   O = sum_s 2^(L_s - m) O_s / sum_s 2^(L_s - m),  LSE = m + log2(the sum).
 // All in fp32; one rounding, to the output.
 //
-// What bounds it: a chain of loads (lengths, where the parts are, their L, their
-// O), some 4 us, each as far as a cold cache; so the O are asked for before
-// their factors are known, and rows are spread over warps where they are few.
-// Where they are many, warps take four at once: 32768 rows of 128, two parts
-// each, in 18 us (a row a warp 31).
+// What bounds it: a chain of loads (lengths, where the parts are, their L,
+// their O), some 4 us, each as far as a cold cache; so the O are asked for
+// before their factors are known, and rows are spread over warps where they are
+// few. Where they are many, warps take four at once: 32768 rows of 128, two
+// parts each, in 18 us (a row a warp 31).
 #include "prefix_common.cuh"
 
 namespace attn {
@@ -120,8 +120,8 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, long long row,
                               : (t.mx + log2f(t.sum)) * 0.69314718055994531f;
 }
 
-// First part and number of parts within `n` slots: a kernel ahead whose wait ran
-// out may not have written them.
+// First part and number of parts within `n` slots: a kernel ahead whose wait
+// ran out may not have written them.
 __device__ __forceinline__ int2 within(int2 x, int n) {
   x.y = min(max(x.y, 0), n);
   x.x = min(max(x.x, 0), n - x.y);
