@@ -71,7 +71,9 @@ Plan make_plan(const Sizes& z, int sms) {
   Plan p;
   const int group = z.Hq / z.Hkv;
   p.rows = static_cast<long long>(group) * z.Sq;
-  p.mode = p.rows <= 16                ? attn::prefix::kFew
+  const long long few =
+      4LL * z.B * z.Hkv > sms || z.B == 1 ? 16 : 8;  // see Mode
+  p.mode = p.rows <= few              ? attn::prefix::kFew
            : p.rows > kTM || z.B == 1 ? attn::prefix::kJoint
                                       : attn::prefix::kPacked;
   p.tile_seqs =

@@ -20,17 +20,19 @@ constexpr int kFewWarps = 8;         // of a block that works on few rows
 
 // How the query rows meet the keys (R rows of a K/V head per sequence, row r =
 // token r / group, head r % group):
-//   kFew    R <= 16: units of two Q tiles, each the rows of as many sequences
-//           as it holds, over the prefix; the sequences' own keys by thread
-//           blocks set aside for them (prefix_few.cuh);
+//   kFew    R <= 16 (8 for few sequences and heads): units of two Q tiles, each
+//           the rows of as many sequences as it holds, over the prefix; the
+//           sequences' own keys by thread blocks set aside for them
+//           (prefix_few.cuh);
 //   kPacked R <= 128, several sequences: such units over the prefix, and units
 //           of each sequence over its own keys;
 //   kJoint  units of each sequence over the prefix and its own keys in turn.
 // 8 K/V heads of 128, 700 own keys behind 8192: 32 sequences of 4, 8 and 16
-// rows take 34, 40 and 46 us by kFew, 48, 53 and 61 by kPacked (4 sequences: 22,
-// 22 and 27, by kPacked 22, 22 and 23); 24, 64 and 128 rows take 67, 95 and 144
-// by kPacked, 194, 195 and 197 by kJoint (4 sequences: 23, 28 and 35; 40, 41 and
-// 44).  More rows fill a Q tile without others'.
+// rows take 34, 40 and 46 us by kFew, 48, 53 and 61 by kPacked; 4 sequences 21,
+// 22 and 26, by kPacked 22, 22 and 22 (2 sequences of 12 rows: 24.6 and 19.8).
+// 24, 64 and 128 rows take 67, 95 and 144 by kPacked, 194, 195 and 197 by kJoint
+// (4 sequences: 23, 28 and 35; 40, 41 and 44).  More rows fill a Q tile without
+// others'.
 enum Mode { kFew = 0, kPacked = 1, kJoint = 2 };
 
 struct PrefixParams {

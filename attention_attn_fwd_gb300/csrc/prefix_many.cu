@@ -144,18 +144,24 @@ __device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
 
 // kFew: CTAs that take the prefix, of those of the launch; the others take the
 // sequences' own keys.  In proportion to the time that either takes an SM: a
-// unit's key tile (256 rows) as long as kStepTiles of the few rows' tiles. (64
-// sequences behind 8192 tokens, 256 behind 2048, 32 behind 65531: 43.2, 43.6
-// and 51.5 us; at 24 47, 45 and 52, at 64 46, 45 and 83.)  What is left over
-// goes to the own keys: rounded to the nearest, 32 sequences of one own token
-// behind 65536 took 61 us of 49, all own keys meeting one CTA.
-constexpr int kStepTiles = 32;
+// unit's key tile (256 rows) as long as 32 of the few rows' tiles, or as 20
+// where the prefix is more than 8 tiles a CTA, whose stream then keeps the
+// memory busy and the own tiles waiting.  (64 sequences behind 8192 tokens, 256
+// behind 2048: 43.3 and 43.6 us; at 20 49 and 50, at 64 46 and 45.  2 and 24
+// sequences of 12 rows, 8 K/V heads, 700 own keys behind 60000: 56 and 111 us;
+// at 32 83 and 144, at 14 56 and 109.)  What is left over goes to the own keys:
+// rounded to the nearest, 32 sequences of one own token behind 65536 took 61 us
+// of 49, all own keys meeting one CTA.
+constexpr int kStepTiles = 32, kStepTilesFar = 20, kFar = 8;
 __device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
                                            int few) {
   if (few == 0) return p.grid;
   if (np == 0) return 0;
-  const float many = static_cast<float>(p.pack_blocks * p.Hkv) *
-                     static_cast<float>(places(p, 0, np) * kStepTiles);
+  const float tiles = static_cast<float>(p.pack_blocks * p.Hkv) *
+                      static_cast<float>(places(p, 0, np));
+  const float many =
+      tiles * (tiles > static_cast<float>(kFar * p.grid) ? kStepTilesFar
+                                                         : kStepTiles);
   const int n = static_cast<int>(p.grid * (many / (many + few)));
   return max(1, min(n, p.grid - 1));
 }

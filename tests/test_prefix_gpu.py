@@ -179,6 +179,30 @@ def test_against_float64(case, dtype):
           causal)
 
 
+# Nine to sixteen rows of more sequences and heads.
+WIDE = [
+    (20, 12, 3, 64, 3, 77, 80, [3, 50, 700, 0, 2] * 4, 701,
+     [3, 1, 2, 0, 2] * 4, True),
+    (45, 16, 1, 128, 1, 513, 600, [31 * i % 90 for i in range(45)], 100,
+     [int(31 * i % 90 > 0) for i in range(45)], True),
+    (21, 6, 2, 64, 5, 333, 333, [5 + 7 * i for i in range(21)], 150, None,
+     False),
+    (40, 8, 1, 128, 2, 0, 5, [2 + 113 * i % 700 for i in range(40)], 702,
+     [1 + i % 2 for i in range(40)], True),
+    (10, 80, 5, 128, 1, 128, 128, [128, 1, 129, 17] * 2 + [300, 16], 300, None,
+     True),
+    (3, 144, 16, 64, 1, 1000, 1001, [5, 900, 77], 900, None, True),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", WIDE)
+def test_nine_to_sixteen_rows(case, dtype):
+    B, Hq, Hkv, D, Sq, plen, pcap, lens, cap, new, causal = case
+    check(make(B, Hkv, D, plen, pcap, lens, cap, dtype), Hq, Sq, dtype, new,
+          causal)
+
+
 @pytest.mark.parametrize("Sq,group", [(1, 4), (5, 7), (40, 2), (70, 3),
                                       (300, 1)])
 def test_matches_the_loops_of_the_definition(Sq, group):
