@@ -33,6 +33,7 @@ __all__ = [
     "attn_qk_rope_bwd_workspace_bytes",
     "Rope", "qk_rope", "qk_rope_bwd", "qk_rope_bwd_workspace",
     "attn_prefix_fwd", "attn_prefix_workspace_bytes",
+    "attn_selftest_prefix_timeout",
     "PrefixCache", "prefix_fwd", "prefix_workspace",
     "library_path", "load_library",
 ]
@@ -194,6 +195,9 @@ def load_library():
         lib.attn_prefix_fwd.argtypes = [ctypes.POINTER(_Prefix), vp, vp, vp, i,
                                         i, vp, f, i, i, vp, sz, vp]
         lib.attn_prefix_fwd.restype = i
+        lib.attn_selftest_prefix_timeout.argtypes = [
+            *lib.attn_prefix_fwd.argtypes[:-1], i, ctypes.c_ulonglong, vp]
+        lib.attn_selftest_prefix_timeout.restype = i
         lib.attn_prefix_workspace_bytes.argtypes = [i] * 7
         lib.attn_prefix_workspace_bytes.restype = sz
         _lib = lib
@@ -464,6 +468,19 @@ def attn_prefix_fwd(cache, Q, O, LSE, Hq, Sq, new_lens, scale, causal, dtype,
         cache.struct, Q or None, O or None, LSE or None, Hq, Sq,
         new_lens or None, float(scale), int(causal), int(dtype),
         workspace or None, int(workspace_bytes), stream or None))
+
+
+def attn_selftest_prefix_timeout(cache, Q, O, LSE, Hq, Sq, new_lens, scale,
+                                 causal, dtype, workspace, workspace_bytes,
+                                 query_rows, timeout_ns, stream) -> int:
+    """Raw C-ABI call of the bounded-wait self-test of ``attn_prefix_fwd`` (one
+    CTA leaves out a key tile, or with ``query_rows`` query rows; waits give up
+    after ``timeout_ns``)."""
+    return int(load_library().attn_selftest_prefix_timeout(
+        cache.struct, Q or None, O or None, LSE or None, Hq, Sq,
+        new_lens or None, float(scale), int(causal), int(dtype),
+        workspace or None, int(workspace_bytes), int(query_rows),
+        int(timeout_ns), stream or None))
 
 
 def attn_prefix_workspace_bytes(B, Hq, Hkv, Sq, prefix_capacity, capacity,
