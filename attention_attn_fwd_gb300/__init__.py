@@ -196,7 +196,7 @@ def load_library():
                                         i, vp, f, i, i, vp, sz, vp]
         lib.attn_prefix_fwd.restype = i
         lib.attn_selftest_prefix_timeout.argtypes = [
-            *lib.attn_prefix_fwd.argtypes[:-1], i, ctypes.c_ulonglong, vp]
+            *lib.attn_prefix_fwd.argtypes[:-1], i, i, ctypes.c_ulonglong, vp]
         lib.attn_selftest_prefix_timeout.restype = i
         lib.attn_prefix_workspace_bytes.argtypes = [i] * 7
         lib.attn_prefix_workspace_bytes.restype = sz
@@ -472,14 +472,15 @@ def attn_prefix_fwd(cache, Q, O, LSE, Hq, Sq, new_lens, scale, causal, dtype,
 
 def attn_selftest_prefix_timeout(cache, Q, O, LSE, Hq, Sq, new_lens, scale,
                                  causal, dtype, workspace, workspace_bytes,
-                                 query_rows, timeout_ns, stream) -> int:
-    """Raw C-ABI call of the bounded-wait self-test of ``attn_prefix_fwd`` (one
-    CTA leaves out a key tile, or with ``query_rows`` query rows; waits give up
-    after ``timeout_ns``)."""
+                                 block, query_rows, timeout_ns,
+                                 stream) -> int:
+    """Raw C-ABI call of the bounded-wait self-test of ``attn_prefix_fwd``
+    (thread block ``block`` waits in vain for a key tile, or with ``query_rows``
+    for query rows; waits give up after ``timeout_ns``)."""
     return int(load_library().attn_selftest_prefix_timeout(
         cache.struct, Q or None, O or None, LSE or None, Hq, Sq,
         new_lens or None, float(scale), int(causal), int(dtype),
-        workspace or None, int(workspace_bytes), int(query_rows),
+        workspace or None, int(workspace_bytes), int(block), int(query_rows),
         int(timeout_ns), stream or None))
 
 

@@ -152,7 +152,7 @@ attn_status_t fwd_impl(const attn_prefix_cache_t* c, const void* Q, void* O,
                        float scale, int causal, attn_dtype_t dtype,
                        void* workspace, size_t workspace_bytes,
                        cudaStream_t stream, unsigned long long timeout_ns = 0,
-                       int withhold = attn::prefix::kWithholdNone) {
+                       int hold_keys = -1, int hold_rows = -1) {
   if (c == nullptr) return ATTN_ERR_INVALID_ARG;
   const Sizes z{c->B, Hq, c->Hkv, Sq, c->prefix_capacity, c->capacity, c->D};
   attn_status_t st = check_sizes(z);
@@ -240,7 +240,8 @@ attn_status_t fwd_impl(const attn_prefix_cache_t* c, const void* Q, void* O,
   p.fd_hkv = attn::make_fast_div(p.Hkv);
   p.fd_tile_seqs = attn::make_fast_div(p.tile_seqs);
   p.fd_tile_rows = attn::make_fast_div(p.tile_rows);
-  p.withhold = withhold;
+  p.hold_keys = hold_keys;
+  p.hold_rows = hold_rows;
   p.timeout_ns = timeout_ns != 0 ? timeout_ns : attn::wait_timeout_ns();
   p.status = attn::device_status_word(dev);
   if (p.status == nullptr) return ATTN_ERR_CUDA;
@@ -291,13 +292,13 @@ attn_status_t attn_selftest_prefix_timeout(
     const attn_prefix_cache_t* cache, const void* Q, void* O, float* LSE,
     int Hq, int Sq, const int* new_lens, float scale, int causal,
     attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
-    int query_rows, unsigned long long timeout_ns, attn_stream_t stream) {
-  if (timeout_ns == 0) return ATTN_ERR_INVALID_ARG;
+    int block, int query_rows, unsigned long long timeout_ns,
+    attn_stream_t stream) {
+  if (timeout_ns == 0 || block < 0) return ATTN_ERR_INVALID_ARG;
   return fwd_impl(cache, Q, O, LSE, Hq, Sq, new_lens, scale, causal, dtype,
                   workspace, workspace_bytes,
                   reinterpret_cast<cudaStream_t>(stream), timeout_ns,
-                  query_rows != 0 ? attn::prefix::kWithholdRows
-                                  : attn::prefix::kWithholdKeys);
+                  query_rows != 0 ? -1 : block, query_rows != 0 ? block : -1);
 }
 
 size_t attn_prefix_workspace_bytes(int B, int Hq, int Hkv, int Sq,

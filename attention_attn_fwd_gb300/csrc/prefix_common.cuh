@@ -35,11 +35,6 @@ constexpr int kFewWarps = 8;         // of a block that works on few rows
 // others'.
 enum Mode { kFew = 0, kPacked = 1, kJoint = 2 };
 
-// What the self-test of the bounded waits leaves out in the CTA that has the
-// first key tile of the first unit: the copy of that tile, or of the unit's
-// query rows.
-enum Withhold { kWithholdNone = 0, kWithholdKeys = 1, kWithholdRows = 2 };
-
 struct PrefixParams {
   const uint16_t* k;      // own keys and values [B, Hkv, capacity, D]
   const uint16_t* v;
@@ -73,7 +68,9 @@ struct PrefixParams {
   float* few_lse2;
   int2* own_info;         // [B, Hkv]: first warp and number of parts
   int grid;               // CTAs of the launch
-  int withhold;           // see Withhold
+  // Self-test of the bounded waits: a CTA whose first key tile, or first query
+  // rows, never count as there (-1: none).
+  int hold_keys, hold_rows;
   FastDiv fd_group, fd_rows, fd_blocks, fd_tile_seqs, fd_tile_rows, fd_hkv;
   unsigned long long timeout_ns;
   unsigned int* status;

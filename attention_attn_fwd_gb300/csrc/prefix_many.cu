@@ -367,14 +367,6 @@ __device__ __forceinline__ void write_unseen(const PrefixParams& p, int lane) {
   }
 }
 
-// Whether the self-test of the waits leaves out what `withhold` names for this
-// part of a unit: the one that has the first key tile of the first unit.
-__device__ __forceinline__ bool withheld(const PrefixParams& p,
-                                         volatile Record* rec, int withhold) {
-  return p.withhold == withhold && rec->h == 0 && rec->j0 == 0 &&
-         rec->tile0 == 0 && rec->b == (p.mode == kJoint ? 0 : -1);
-}
-
 // Row i of tile t of a unit: its sequence (-1: none) and row of the K/V head
 // there.
 __device__ __forceinline__ int row_of(const PrefixParams& p,
@@ -527,6 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if ((bar >= bar_empty && bar < bar_unit) || bar == bar_end) count = 2;
     if (bar >= bar_ufree && bar < bar_q) count = 11;
     if (bar >= bar_p && bar < bar_pv) count = kTM;
+    // (Self-test: an arrival more than comes.)
+    const int cta = static_cast<int>(blockIdx.x);
+    if ((cta == p.hold_keys && bar == bar_full) ||
+        (cta == p.hold_rows && bar >= bar_q && bar < bar_qfree))
+      count = 2;
     ptx::mbar_init(bar, count);
     if (threadIdx.x == 0) *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -642,7 +639,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // could take one for another).
       int slot_v = 1;  // V tiles of the stream are odd
       int ends = 0, q_uses[2] = {0, 0};
-      bool q_held[2] = {false, false};  // (self-test) asked for, but not copied
       const int q_tokens = fast_div(p.tile_rows, p.fd_group);
       const uint32_t q_bytes =
           (p.mode == kJoint ? p.tile_rows : p.tile_seqs * p.rows) * D * 2;
@@ -650,15 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile Record* rec = records + k % kUnits;
         const int n0 = rec->n[0], n1 = rec->n[1];
         const int b = rec->b, h = rec->h, tile0 = rec->tile0;
-        const bool hold = withheld(p, rec, kWithholdRows);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || (t ? n1 : n0) == 0) continue;
           if (q_uses[t] > 0) ok = wait(bar_qfree + 8 * t, q_uses[t] - 1, 5);
           if (!ok) break;
           ++q_uses[t];
-          q_held[t] = hold;
-          if (lane == 0 && !hold) {
+          if (lane == 0) {
             ptx::mbar_arrive_expect_tx(bar_q + 8 * t, q_bytes);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
@@ -715,21 +709,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The copies in flight land before the CTA ends, whoever gave up.
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        if (q_uses[t] > 0 && !q_held[t])
+        if (q_uses[t] > 0)
           drain_wait(bar_q + 8 * t, (q_uses[t] - 1) & 1, p);
       __syncwarp();
       if (lane == 0 && p.mode == kJoint) p.split[blockIdx.x] = split;
       write_unseen<D>(p, lane);
     } else if (warp == 1) {
       // -------------------------------------------------------- tile copies
-      int it = 0, held = -1;  // held: (self-test) the tile left out
+      int it = 0;
       for (int k = 0; ok; ++k) {
         volatile Record* rec = get_unit(k);
         if (rec == nullptr) break;
         const int n = rec->n_kv, j0 = rec->j0, np = rec->np;
         const int plen = rec->plen, len = rec->len, h = rec->h;
         const int own_plane = rec->b * p.Hkv + h;
-        if (withheld(p, rec, kWithholdKeys)) held = it;
         release_unit(k);
         for (int j = 0; j < n && ok; ++j) {
           bool own;
@@ -744,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = it % L::kSlots, use = it / L::kSlots;
             if (use > 0) ok = wait(bar_empty + 8 * slot, use - 1, 1);
             if (!ok) break;
-            if (lane == 0 && it != held) {
+            if (lane == 0) {
               const uint32_t bar = bar_full + 8 * slot;
               const uint32_t dst = s_base + L::kRing + slot * L::kTile;
               const CUtensorMap* m =
@@ -762,8 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The copies in flight land before the CTA ends, whoever gave up.
       for (int i = max(0, it - L::kSlots); i < it; ++i)
-        if (i != held)
-          drain_wait(bar_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1, p);
+        drain_wait(bar_full + 8 * (i % L::kSlots), (i / L::kSlots) & 1, p);
       __syncwarp();
     } else {
       // ----------------------------------------- MMA issue, a warp a Q tile

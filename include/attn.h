@@ -683,19 +683,17 @@ attn_status_t attn_selftest_wait_timeout(const void* Q, const void* K,
 
 /*
  * attn_selftest_prefix_timeout — the same of attn_prefix_fwd: its arguments and
- * checks, every wait gives up after timeout_ns (> 0), and the CTA that has the
- * first key tile of the first unit (over the prefix, or where that is empty or
- * a sequence's rows fill units themselves, of the first sequence) never loads
- * that tile, or with query_rows non-zero the unit's query rows.  That CTA's
- * other copies and products end before it does.  The rows it works on are left
- * undefined, those of the other CTAs are right.  Where no CTA has such a tile (an
- * empty prefix behind rows that are packed with other sequences') nothing is
- * left out.  For tests of the failure path only.
+ * checks, every wait gives up after timeout_ns (> 0), and thread block `block`
+ * (>= 0) waits in vain for its first key tile, or with query_rows non-zero for
+ * its first query rows.  That block's copies and products end before it does.
+ * The rows it works on are left undefined, those of the other blocks are right.
+ * A block that has no key tiles gives up nothing.  For tests of the failure path
+ * only.
  */
 attn_status_t attn_selftest_prefix_timeout(
     const attn_prefix_cache_t* cache, const void* Q, void* O, float* LSE,
     int Hq, int Sq, const int* new_lens, float scale, int causal,
-    attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+    attn_dtype_t dtype, void* workspace, size_t workspace_bytes, int block,
     int query_rows, unsigned long long timeout_ns, attn_stream_t stream);
 
 /*

@@ -1,13 +1,12 @@
 """Waits that run out behind a shared prefix, through the C ABI.
 
-``attn_selftest_prefix_timeout`` leaves out the first key tile, or the first
-unit's query rows, in one CTA, with a 10 ms limit.  Shares of a key tile or two,
-all of whose copies are under way before any wait, are the ones whose copying
-warps have done everything long before another role gives up.  The call has to
-return, the status word to report it, the rows of other K/V heads to be right
-(what an aborted CTA left of the list in the workspace is not trusted: it
-begins as ones, or large numbers), and the next calls to give the same bits as
-before.
+In ``attn_selftest_prefix_timeout`` one CTA waits in vain for its first key tile,
+or its first query rows, with a 10 ms limit.  In shares of a key tile or two all
+copies are under way before any wait, so that the copying warps have done
+everything long before another role gives up.  The call has to return, the
+status word to report it, the rows of other K/V heads to be right (what a CTA
+that gave up left of the list in the workspace is not trusted: it begins as
+ones, or large numbers), and the next calls to give the same bits as before.
 """
 import time
 
@@ -30,14 +29,15 @@ def built():
     __graft_entry__.build()
 
 
-# B, Hq, Hkv, D, Sq, prefix, own: the three ways of few, packed and many rows,
-# with shares of one or two key tiles and of several units.
+# B, Hq, Hkv, D, Sq, prefix, own, and a CTA that has key tiles: the three ways of
+# few, packed and many rows, with shares of one or two key tiles (the first four
+# places of the list are empty) and of several units.
 CASES = [
-    (4, 8, 2, 128, 1, 450, 250), (5, 6, 2, 64, 3, 200, 250),
-    (4, 8, 2, 128, 20, 450, 250), (3, 4, 2, 64, 40, 333, 250),
-    (4, 8, 2, 128, 200, 450, 250), (2, 4, 2, 64, 70, 0, 250),
-    (2, 4, 2, 128, 1, 60000, 250), (40, 16, 16, 64, 70, 900, 300),
-    (1, 600, 300, 128, 60, 200, 300),
+    (4, 8, 2, 128, 1, 450, 250, 4), (5, 6, 2, 64, 3, 200, 250, 5),
+    (4, 8, 2, 128, 20, 450, 250, 4), (3, 4, 2, 64, 40, 333, 250, 4),
+    (4, 8, 2, 128, 200, 450, 250, 2), (2, 4, 2, 64, 70, 0, 250, 4),
+    (2, 4, 2, 128, 1, 60000, 250, 1), (40, 16, 16, 64, 70, 900, 300, 0),
+    (1, 600, 300, 128, 60, 200, 300, 0),
 ]
 
 
@@ -45,7 +45,7 @@ CASES = [
 @pytest.mark.parametrize("rows", [0, 1])
 @pytest.mark.parametrize("case", CASES)
 def test_a_wait_runs_out(case, rows, fill):
-    B, Hq, Hkv, D, Sq, P, own = case
+    B, Hq, Hkv, D, Sq, P, own, block = case
     dtype = "bf16" if rows else "f16"
     joint = Hq // Hkv * Sq > 128 or B == 1
     c = make(B, Hkv, D, P, max(P, 1), [own - 7 * (i % 9) for i in range(B)],
@@ -61,7 +61,7 @@ def test_a_wait_runs_out(case, rows, fill):
     st = attn.attn_selftest_prefix_timeout(
         c, q.data_ptr(), o.data_ptr(), lse.data_ptr(), Hq, Sq, 0, D ** -0.5,
         True, attn.ATTN_BF16 if dtype == "bf16" else attn.ATTN_F16,
-        ws.data_ptr(), ws.numel(), rows, LIMIT_NS,
+        ws.data_ptr(), ws.numel(), block, rows, LIMIT_NS,
         torch.cuda.current_stream().cuda_stream)
     assert st == attn.ATTN_OK
     st, code = attn.attn_device_status()
@@ -89,5 +89,5 @@ def test_no_time_is_refused():
     ws = attn.prefix_workspace(c, 2, 1)
     assert attn.attn_selftest_prefix_timeout(
         c, q.data_ptr(), torch.empty_like(q).data_ptr(), 0, 2, 1, 0, 0.1, True,
-        attn.ATTN_F16, ws.data_ptr(), ws.numel(), 0, 0, 0) == \
+        attn.ATTN_F16, ws.data_ptr(), ws.numel(), 0, 0, 0, 0) == \
         attn.ATTN_ERR_INVALID_ARG
