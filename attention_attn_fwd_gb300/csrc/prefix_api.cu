@@ -1,5 +1,6 @@
 // C ABI of the attention behind a shared prefix: argument checks, the choice
 // of kernels and launches.  No device memory is allocated here.
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -86,7 +87,8 @@ Plan make_plan(const Sizes& z, int sms) {
   p.row_blocks = p.mode == attn::prefix::kFew
                      ? 0
                      : units_of((p.rows + p.tile_rows - 1) / p.tile_rows);
-  p.grid = sms > 2 ? sms : 2;  // (one for the prefix, one for own keys)
+  // (One for the prefix, one for own keys; the merge counts on 224 at most.)
+  p.grid = std::min(std::max(sms, 2), 224);
   return p;
 }
 

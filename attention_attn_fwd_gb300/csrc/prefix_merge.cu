@@ -8,6 +8,11 @@
 // before their factors are known, and rows are spread over warps where they are
 // few. Where they are many, warps take four at once: 32768 rows of 128, two
 // parts each, in 18 us (a row a warp 31).
+//
+// A part's weight 2^(L_s - m) is held times kSlack: the weights of all parts of
+// a row then sum to 1 at most, and their products with O_s stay within fp32 where
+// V (and so each O_s) comes near its largest number.  A power of two, so that
+// nothing is rounded by it and the results' bits are those without it.
 #include "prefix_common.cuh"
 
 namespace attn {
@@ -21,6 +26,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kAhead = 8;  // parts whose O a warp has in flight
+// 1 / (more parts than a row has: one per CTA over the prefix, and over the own
+// keys one per CTA or, of few rows, per warp of the CTAs set aside for them;
+// 1369 of 152 CTAs).
+constexpr float kSlack = 0x1p-11f;
+static_assert((1 + kFewWarps) * 224 < 2048, "parts of a row (SMs: 224)");
 // Rows an SM from which on warps take four (2520 rows in all, 35 a head: 24 us
 // of the whole call, 27 by four).
 constexpr long long kManyRows = 32;
@@ -76,7 +86,7 @@ __device__ __forceinline__ Sum add_parts(int s0, int s1, int lane, At at) {
         for (int k = 16; k > 0; k /= 2)
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         const float before = ptx::ex2(t.mx - m);
-        f_all = ptx::ex2(x - m);
+        f_all = ptx::ex2(x - m) * kSlack;
         t.mx = m;
         t.acc.x *= before;
         t.acc.y *= before;
@@ -117,7 +127,8 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, long long row,
   }
   if (lane == 0 && p.lse != nullptr)
     p.lse[row] = t.sum == 0.f ? -INFINITY
-                              : (t.mx + log2f(t.sum)) * 0.69314718055994531f;
+                              : (t.mx + log2f(t.sum * (1.f / kSlack))) *
+                                    0.69314718055994531f;
 }
 
 // First part and number of parts within `n` slots: a kernel ahead whose wait
@@ -288,7 +299,7 @@ __device__ __forceinline__ void join_rows(const PrefixParams& p, int n,
         for (int k = kJoinParts / 2; k > 0; k /= 2)
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         const float before = ptx::ex2(mx - m);
-        f_all = ptx::ex2(x - m);
+        f_all = ptx::ex2(x - m) * kSlack;
         mx = m;
         sum = sum * before + f_all;
 #pragma unroll
@@ -328,7 +339,9 @@ __device__ __forceinline__ void join_rows(const PrefixParams& p, int n,
   }
   if (s_lane == 0 && i_lane < n && p.lse != nullptr)
     p.lse[row_at(i_lane)] =
-        sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+        sum == 0.f ? -INFINITY
+                   : (mx + log2f(sum * (1.f / kSlack))) *
+                         0.69314718055994531f;
 }
 
 // kFew and kPacked, where rows are many: four of a (sequence, K/V head) by a

@@ -590,7 +590,11 @@ typedef struct {
  * attn_prefix_fwd — attention of Sq query rows per sequence over the prefix
  * and the sequence's own tokens behind it, one softmax over both, in the
  * scores, softmax and sums of attn_fwd (fp32; the weights are rounded to the
- * inputs' type for their product with V).
+ * inputs' type for their product with V).  For that product they are held
+ * times a power of two.  In bf16 it is 2^-24: sums over 2^16 keys (2^24 of like
+ * weights) stay within fp32 for every finite V, and a key's share of O is off by
+ * 2^-126 at most, by which values of V below 2^-100 lose bits.  In fp16 it is
+ * 2^7: weights down to 2^-21 of the row's largest keep their bits.
  *
  * Q         device, [B, Hq, Sq, D] contiguous, dtype (read);
  * O         device, [B, Hq, Sq, D] contiguous, dtype (written);
