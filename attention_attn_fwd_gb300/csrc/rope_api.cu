@@ -62,37 +62,64 @@ attn_status_t make_view(const attn_heads_t* v, const Sizes& z, int H,
   return ATTN_OK;
 }
 
-// Whether no two places of a view share an element.
-bool writable(const View& v, const Sizes& z) {
-  struct Dim {
-    long long stride;
-    int n;
-  } d[3] = {{v.b, z.B}, {v.s, z.S}, {v.h, v.H}};
-  std::sort(d, d + 3,
+// A dimension of places: its stride and how many there are.
+struct Dim {
+  long long stride;
+  int n;
+};
+
+// Whether runs of `extent` elements at the places of `count` dimensions share no
+// element: each dimension, from the smallest stride up, steps over all that
+// lies within.
+bool nested(long long extent, Dim* d, int count) {
+  std::sort(d, d + count,
             [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
-  long long extent = z.D;
-  for (const Dim& x : d) {
-    if (x.n == 1) continue;
-    if (x.stride < extent) return false;
-    extent += x.stride * (x.n - 1);
+  for (int i = 0; i < count; ++i) {
+    if (d[i].n == 1) continue;
+    if (d[i].stride < extent) return false;
+    extent += d[i].stride * (d[i].n - 1);
   }
   return true;
 }
 
-// Whether two writable views share no element: apart altogether, or the heads
-// of both side by side within every token of one buffer.
+// Whether no two places of a view share an element.
+bool writable(const View& v, const Sizes& z) {
+  Dim d[3] = {{v.b, z.B}, {v.s, z.S}, {v.h, v.H}};
+  return nested(z.D, d, 3);
+}
+
+// Whether two writable views share no element: for some of the dimensions, all
+// of x's places along these lie before y's, and so they do at every step of the
+// others, which both views take alike and which step over what lies within.
+// (All dimensions: apart altogether.  Heads alone: side by side in a token, as
+// parts of a packed projection.  Heads and tokens: parts of a packed tensor
+// with the heads ahead of the tokens.  None: in turn.)
 bool apart(const View& x, const View& y, const Sizes& z) {
-  const Range a = x.range(), b = y.range();
-  if (!attn::ranges_overlap(a.p, a.n, b.p, b.n)) return true;
-  if (x.b != y.b || x.s != y.s) return false;
-  const long long ex = x.h * (x.H - 1) + z.D, ey = y.h * (y.H - 1) + z.D;
   const long long off =
       (reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p)) / 2;
-  if (off >= 0 ? off < ex : -off < ey) return false;
-  const long long both = off >= 0 ? off + ey : -off + ex;
-  long long token = z.S > 1 ? x.s : x.b;
-  if (z.S > 1 && z.B > 1) token = std::min(x.s, x.b);
-  return both <= token;
+  if (off < 0) return apart(y, x, z);
+  const Dim dx[3] = {{x.b, z.B}, {x.s, z.S}, {x.h, x.H}};
+  const Dim dy[3] = {{y.b, z.B}, {y.s, z.S}, {y.h, y.H}};
+  for (int within = 0; within < 8; ++within) {
+    long long ex = z.D, ey = z.D;
+    Dim rest[3];
+    int count = 0;
+    bool alike = true;
+    for (int i = 0; i < 3; ++i) {
+      if (within >> i & 1) {
+        ex += dx[i].stride * (dx[i].n - 1);
+        ey += dy[i].stride * (dy[i].n - 1);
+        continue;
+      }
+      // (The stride of a dimension of one element says nothing.)
+      const Dim& longer = dx[i].n >= dy[i].n ? dx[i] : dy[i];
+      alike &= std::min(dx[i].n, dy[i].n) == 1 ||
+               dx[i].stride == dy[i].stride;
+      rest[count++] = longer;
+    }
+    if (alike && off >= ex && nested(off + ey, rest, count)) return true;
+  }
+  return false;
 }
 
 bool any_overlap(const Range& a, const Range* others, int count) {

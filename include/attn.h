@@ -530,8 +530,10 @@ attn_status_t attn_qk_rope(const attn_rope_t* rope, const attn_heads_t* q,
  * q, k       the forward's views (read where they were normed; else NULL
  *            will do);
  * dq, dk, dv views (written): the gradients of q, k and v.  No two of their
- *            places may share an element; they may lie side by side within
- *            each token of one buffer, as the forward's inputs may;
+ *            places may share an element; they may be parts of one packed
+ *            buffer: side by side within each token, as the forward's inputs
+ *            may, or behind one another in each sequence or altogether
+ *            (refused where no order of the strides shows them apart);
  * dq_weight, dk_weight  device float32 [D] (written), given exactly where the
  *            weight is; summed in fp32 in a fixed order;
  * workspace  device, 256-byte aligned, at least
