@@ -448,8 +448,9 @@ attn_status_t attn_kv8_evict(const attn_kv8_t* src, const attn_kv8_t* dst,
  *
  * phase  device, [rot / 2]: freq[i] in units of 2^-64 of a turn, from
  *        attn_rope_phase.  Positions are multiplied with it modulo 2^64, so
- *        that the fraction of a turn is exact at any distance; the angle is
- *        then off by 2^-22 or less;
+ *        that the fraction of a turn is exact at any distance; the angle, in
+ *        (-pi, pi], is then off by 2^-23 of itself and a unit of the phase per
+ *        position;
  * axis   device, [rot / 2] values below `axes`; not read when axes is 1.
  * D in {64, 128}, rot a multiple of 8 from 0 (norm only) to D, 1 <= axes <=
  * 255.
