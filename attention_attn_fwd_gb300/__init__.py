@@ -998,7 +998,7 @@ class Rope:
         self.phase = torch.tensor(signed, dtype=torch.int64, device=dev)
         self.axis = torch.tensor(axes, dtype=torch.uint8, device=dev)
         self.D, self.rot, self.weight_shape = D, 2 * len(freq), (D,)
-        self.axes = max(axes, default=0) + 1
+        self.axes = self.most_axes = max(axes, default=0) + 1
         self.interleaved = bool(interleaved)
         self.device = self.phase.device
         # What every call needs, looked up once.
@@ -1015,13 +1015,20 @@ class Rope:
     def make(cls, D, base=10000.0, rot=None, sections=None, interleaved=False,
              device="cuda"):
         """Frequencies base^(-2i / rot) of rot (D unless given) elements;
-        ``sections``: pairs of each axis in turn, rot / 2 in all."""
+        ``sections``: pairs of each axis in turn, rot / 2 in all (positions
+        may be given for all of them, also where the last have no pairs)."""
         rot = D if rot is None else rot
+        if rot < 0 or rot % 8:
+            raise AttnError("the rotated elements must be a multiple of 8, "
+                            "got %r" % (rot,), ATTN_ERR_UNSUPPORTED)
         axes = None
         if sections is not None:
             axes = [a for a, n in enumerate(sections) for _ in range(n)]
-        return cls([base ** (-2.0 * i / rot) for i in range(rot // 2)], D,
+        rope = cls([base ** (-2.0 * i / rot) for i in range(rot // 2)], D,
                    axes, interleaved, device)
+        if sections is not None:
+            rope.most_axes = max(rope.axes, len(sections))
+        return rope
 
 
 def _heads_view(name, t, shape, dtype):
@@ -1060,7 +1067,10 @@ def _rope_positions(rope, positions, B, S):
     if positions is None:
         return None
     if rope.axes > 1 or positions.dim() == 3:
-        _check_tensor("positions", positions, (rope.axes, B, S), rope.int32)
+        n = rope.axes  # (axes behind the last with pairs are not read)
+        if positions.dim() == 3 and positions.shape[0] == rope.most_axes:
+            n = rope.most_axes
+        _check_tensor("positions", positions, (n, B, S), rope.int32)
     else:
         _check_tensor("positions", positions, (B, S), rope.int32)
     return positions.data_ptr()
