@@ -476,14 +476,12 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       ++nd;
       ++s;
     }
-    if (!ok) {
-      // Let every copy still in flight land before the CTA goes away.
-      drain_wait(bar_kv, 0, p);
-      for (int i = max(0, nq - L::kQSlots); i < nq; ++i)
-        drain_wait(bar_qf + 8 * (i % L::kQSlots), (i / L::kQSlots) & 1, p);
-      for (int i = max(0, nd - L::kDoSlots); i < nd; ++i)
-        drain_wait(bar_df + 8 * (i % L::kDoSlots), (i / L::kDoSlots) & 1, p);
-    }
+    // Every copy lands before the CTA goes away, whichever role gave up.
+    drain_wait(bar_kv, 0, p);
+    for (int i = max(0, nq - L::kQSlots); i < nq; ++i)
+      drain_wait(bar_qf + 8 * (i % L::kQSlots), (i / L::kQSlots) & 1, p);
+    for (int i = max(0, nd - L::kDoSlots); i < nd; ++i)
+      drain_wait(bar_df + 8 * (i % L::kDoSlots), (i / L::kDoSlots) & 1, p);
     __syncwarp();
   } else if (warp == kVecWarp) {
     // ------------------------------------------- per-step vector staging
@@ -613,7 +611,7 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       hm = hm_next;
     }
     if (ok && s > 0) ptx::tc_commit_elect(bar_acc);
-    if (!ok && issued) {
+    if (issued) {
       ptx::tc_commit_elect(bar_drain);
       drain_wait(bar_drain, 0, p);
     }
@@ -924,14 +922,12 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
                                kvplane);
       ++nv;
     }
-    if (!ok) {
-      // Let every copy still in flight land before the CTA goes away.
-      drain_wait(bar_q, 0, p);
-      for (int i = max(0, nk - L::kKSlots); i < nk; ++i)
-        drain_wait(bar_kf + 8 * (i % L::kKSlots), (i / L::kKSlots) & 1, p);
-      for (int i = max(0, nv - L::kVSlots); i < nv; ++i)
-        drain_wait(bar_vf + 8 * (i % L::kVSlots), (i / L::kVSlots) & 1, p);
-    }
+    // Every copy lands before the CTA goes away, whichever role gave up.
+    drain_wait(bar_q, 0, p);
+    for (int i = max(0, nk - L::kKSlots); i < nk; ++i)
+      drain_wait(bar_kf + 8 * (i % L::kKSlots), (i / L::kKSlots) & 1, p);
+    for (int i = max(0, nv - L::kVSlots); i < nv; ++i)
+      drain_wait(bar_vf + 8 * (i % L::kVSlots), (i / L::kVSlots) & 1, p);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------ MMA issuer
@@ -1036,7 +1032,7 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       n_next = n_after;
     }
     if (ok && s > 0) ptx::tc_commit_elect(bar_acc);
-    if (!ok && issued) {
+    if (issued) {
       ptx::tc_commit_elect(bar_drain);
       drain_wait(bar_drain, 0, p);
     }

@@ -550,14 +550,12 @@ __global__ void __launch_bounds__(cfg::kThreads, 1)
         }
       }
     }
-    if (!ok) {
-      // Let every copy still in flight land before the CTA goes away.
-      for (int t = 0; t < 2; ++t)
-        if (q_loads[t] > 0) drain_wait(bar_q + 8 * t, (q_loads[t] - 1) & 1, p);
-      for (int i = max(0, it - nslots); i < it; ++i)
-        if (!(withhold && i == 0))
-          drain_wait(bar_full + 8 * (i % nslots), (i / nslots) & 1, p);
-    }
+    // Every copy lands before the CTA goes away, whichever role gave up.
+    for (int t = 0; t < 2; ++t)
+      if (q_loads[t] > 0) drain_wait(bar_q + 8 * t, (q_loads[t] - 1) & 1, p);
+    for (int i = max(0, it - nslots); i < it; ++i)
+      if (!(withhold && i == 0))
+        drain_wait(bar_full + 8 * (i % nslots), (i / nslots) & 1, p);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------ MMA issuer
@@ -831,8 +829,8 @@ __global__ void __launch_bounds__(cfg::kThreads, 1)
       }
       it = it0 + 2 * w.n_kv;
     }
-    if (!ok && issued_any) {
-      // Wait for the MMAs already issued before TMEM is released.
+    if (issued_any) {
+      // The MMAs issued end before TMEM is released, whichever role gave up.
       ptx::tc_commit_elect(bar_drain);
       drain_wait(bar_drain, 0, p);
     }
@@ -1331,6 +1329,8 @@ __global__ void __launch_bounds__(cfg::kThreads, 1)
       }
       ptx::tc_fence_before();
     }
+    // P and O of a step that was given up, too, are in TMEM before it is freed.
+    ptx::tmem_wait_st();
     // Output boxes still being stored must be read out of shared memory
     // (and written) before the CTA exits.
     if constexpr (kStageO) {

@@ -267,11 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok) {  // let the copies in flight land
-      for (int i = max(0, it - L::kRawSlots); i < it; ++i)
-        drain_wait(bar_rfull + 8 * (i % L::kRawSlots),
-                   (i / L::kRawSlots) & 1, p);
-    }
+    // The copies in flight land before the CTA ends, whoever gave up.
+    for (int i = max(0, it - L::kRawSlots); i < it; ++i)
+      drain_wait(bar_rfull + 8 * (i % L::kRawSlots), (i / L::kRawSlots) & 1,
+                 p);
     __syncwarp();
   } else if (warp == 0) {
     // ---------------------------------------------------------- MMA issue
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         issued = true;
       }
     }
-    if (!ok && issued) {  // the MMAs issued end before TMEM is released
+    if (issued) {  // the MMAs issued end before TMEM is released
       ptx::tc_commit_elect(bar_drain);
       drain_wait(bar_drain, 0, p);
     }
