@@ -71,14 +71,6 @@ __host__ __device__ constexpr int tile_keys() {
   return 2048 / D;
 }
 
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;"
-               : "=r"(y)
-               : "r"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
@@ -86,27 +78,6 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-
-// 16-byte asynchronous copy past L1; the second form writes zeros and reads
-// nothing unless `in`.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-               "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst,
-                                                   const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-               "l"(src), "r"(in ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // One tile of a warp's ring: 2 KB of K codes, then 2 KB of V codes.  Chunk j
@@ -174,9 +145,9 @@ struct Loader {
       if ((t + 1) * kKeys <= seg.len) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          cp_async16(dst_k + to + 512 * i, k + off + 512 * i);
-          cp_async16(((i & 1) ? dst_v1 : dst_v0) + to + 512 * i,
-                     v + off + 512 * i);
+          ptx::cp_async16(dst_k + to + 512 * i, k + off + 512 * i);
+          ptx::cp_async16(((i & 1) ? dst_v1 : dst_v0) + to + 512 * i,
+                          v + off + 512 * i);
         }
       } else {  // rows past the length become zeros
         const int left = seg.len - t * kKeys - lane / kPerRow;
@@ -184,14 +155,14 @@ struct Loader {
         for (int i = 0; i < 4; ++i) {
           const bool in = i * kRowStep < left;
           const long long at = in ? off + 512 * i : 0;
-          cp_async16_or_zero(dst_k + to + 512 * i, k + at, in);
-          cp_async16_or_zero(((i & 1) ? dst_v1 : dst_v0) + to + 512 * i,
-                             v + at, in);
+          ptx::cp_async16_or_zero(dst_k + to + 512 * i, k + at, in);
+          ptx::cp_async16_or_zero(
+              ((i & 1) ? dst_v1 : dst_v0) + to + 512 * i, v + at, in);
         }
       }
       pos += kStep;
     }
-    cp_async_commit();
+    ptx::cp_async_commit();
   }
 };
 
@@ -410,7 +381,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
         vs_all = in ? __ldg(vsb + (key >> p.block_shift)) : 0.f;
         held = 0;
       }
-      cp_async_wait<kStages - 1>();
+      ptx::cp_async_wait<kStages - 1>();
       __syncwarp();
       const uint32_t tile = ring + stage * 4096;
 #pragma unroll
@@ -539,9 +510,9 @@ __global__ void __launch_bounds__(Config<D, NT>::kThreads, Config<D, NT>::kCtas)
             w[e] = ptx::ex2(s[nt][e] - m[nt][e & 1]);
             l[nt][e & 1] += w[e];
           }
-          pb[nt][0] = movmatrix_trans(
+          pb[nt][0] = ptx::movmatrix_trans(
               ptx::pack2<false>(w[0] * p_factor, w[1] * p_factor));
-          pb[nt][1] = movmatrix_trans(
+          pb[nt][1] = ptx::movmatrix_trans(
               ptx::pack2<false>(w[2] * p_factor, w[3] * p_factor));
         }
         // O^T += V^T P^T: V rows 2c, 2c + 1, 2c + 8, 2c + 9 of the step.

@@ -241,7 +241,6 @@ attn_status_t fwd_impl(const attn_prefix_cache_t* c, const void* Q, void* O,
   p.fd_blocks = attn::make_fast_div(p.row_blocks > 0 ? p.row_blocks : 1);
   p.fd_hkv = attn::make_fast_div(p.Hkv);
   p.fd_tile_seqs = attn::make_fast_div(p.tile_seqs);
-  p.fd_tile_rows = attn::make_fast_div(p.tile_rows);
   p.hold_keys = hold_keys;
   p.hold_rows = hold_rows;
   p.timeout_ns = timeout_ns != 0 ? timeout_ns : attn::wait_timeout_ns();

@@ -71,7 +71,7 @@ struct PrefixParams {
   // Self-test of the bounded waits: a CTA whose first key tile, or first query
   // rows, never count as there (-1: none).
   int hold_keys, hold_rows;
-  FastDiv fd_group, fd_rows, fd_blocks, fd_tile_seqs, fd_tile_rows, fd_hkv;
+  FastDiv fd_group, fd_rows, fd_blocks, fd_tile_seqs, fd_hkv;
   unsigned long long timeout_ns;
   unsigned int* status;
 };

@@ -30,34 +30,6 @@
 namespace attn {
 namespace prefix {
 
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;"
-               : "=r"(y)
-               : "r"(x));
-  return y;
-}
-
-// 16-byte asynchronous copy past L1; zeros, and nothing read, unless `in`.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-               "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst,
-                                                   const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-               "l"(src), "r"(in ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void ldmatrix4(uint32_t* a, uint32_t addr) {
   asm volatile(
       "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -254,8 +226,8 @@ struct FewLoader {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
           const uint32_t dst = to + chunk_at<D>(r0 + i * kRowStep, j);
-          cp_async16(dst, k + off + i * kRowStep * D);
-          cp_async16(dst + kFewTile, v + off + i * kRowStep * D);
+          ptx::cp_async16(dst, k + off + i * kRowStep * D);
+          ptx::cp_async16(dst + kFewTile, v + off + i * kRowStep * D);
         }
       } else {
 #pragma unroll 2
@@ -263,13 +235,13 @@ struct FewLoader {
           const uint32_t dst = to + chunk_at<D>(r0 + i * kRowStep, j);
           const bool in = r0 + i * kRowStep < left;
           const long long at = in ? off + i * kRowStep * D : 0;
-          cp_async16_or_zero(dst, k + at, in);
-          cp_async16_or_zero(dst + kFewTile, v + at, in);
+          ptx::cp_async16_or_zero(dst, k + at, in);
+          ptx::cp_async16_or_zero(dst + kFewTile, v + at, in);
         }
       }
       ++pos;
     }
-    cp_async_commit();
+    ptx::cp_async_commit();
   }
 };
 
@@ -355,7 +327,7 @@ __device__ __forceinline__ void few_share(const PrefixParams& p, int gw,
 
     const int last = min(seg.end, count);  // end of the warp's part
     for (int pos = max(seg.pos, 0); pos < last; ++pos) {
-      cp_async_wait<kFewStages - 1>();
+      ptx::cp_async_wait<kFewStages - 1>();
       __syncwarp();
       const uint32_t tile = ring + stage * 2 * kFewTile;
 #pragma unroll
@@ -425,8 +397,8 @@ __device__ __forceinline__ void few_share(const PrefixParams& p, int gw,
             w[e] = ptx::ex2((s[nt][e] - m[nt][e & 1]) + kShift);
             l[nt][e & 1] += w[e];
           }
-          pb[nt][0] = movmatrix_trans(ptx::pack2<kBF16>(w[0], w[1]));
-          pb[nt][1] = movmatrix_trans(ptx::pack2<kBF16>(w[2], w[3]));
+          pb[nt][0] = ptx::movmatrix_trans(ptx::pack2<kBF16>(w[0], w[1]));
+          pb[nt][1] = ptx::movmatrix_trans(ptx::pack2<kBF16>(w[2], w[3]));
         }
         // O^T += V^T P^T: row i of a thread's O is element 16 i + g8 (+ 8).
 #pragma unroll

@@ -379,13 +379,7 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks(D))
 // row's in registers).  Each CTA keeps to a block of heads and walks over tokens,
 // so that the weights' sums stay in registers; they meet as fp32 in a fixed
 // order: results do not change from run to run.
-// 16-byte asynchronous copy; zeros, and nothing read, unless `in`.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src,
-                                       bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-               "l"(src), "r"(in ? 16 : 0)
-               : "memory");
-}
+
 __device__ __forceinline__ Row shared_row(uint32_t row, const int* at) {
   Row r;
 #pragma unroll
@@ -444,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks)
   auto load = [&](int stage) {
     if (ahead.blk < token_blocks) {
       const uint32_t to = mine + stage * 1024 + 16 * l;
-      copy16(to, ahead.dy, ahead.in);
-      if (norm) copy16(to + kRowBytes, ahead.x, ahead.in);
+      ptx::cp_async16_or_zero(to, ahead.dy, ahead.in);
+      if (norm) ptx::cp_async16_or_zero(to + kRowBytes, ahead.x, ahead.in);
       ahead.dy += step;
       if (norm) ahead.x += p.x_h[h.kind];
       if (++ahead.i == h.count) {
@@ -454,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks)
         if (ahead.blk < token_blocks) enter();
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    ptx::cp_async_commit();
   };
   ahead.blk = stripe;
   ahead.i = 0;
@@ -475,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks)
       back = make_turn<kInterleaved>(one, c, s, -1.f);
     }
     for (int i = 0; i < h.count; ++i, dx += p.dx_h[h.kind]) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStagesBwd - 1) : "memory");
+      ptx::cp_async_wait<kStagesBwd - 1>();
       __syncwarp();
       Row gy, gx;
       const uint32_t from = mine + stage * 1024;
