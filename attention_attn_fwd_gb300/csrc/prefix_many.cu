@@ -146,25 +146,26 @@ __device__ __forceinline__ kv8::Cut make_cut(int ctas, int total) {
 
 // kFew: CTAs that take the prefix, of those of the launch; the others take the
 // sequences' own keys.  In proportion to the time that either takes an SM: a
-// unit's key tile (256 rows) as long as 32 of the few rows' tiles, or as 20
-// where the prefix is more than 8 tiles a CTA, whose stream then keeps the
-// memory busy and the own tiles waiting.  (64 sequences behind 8192 tokens, 256
-// behind 2048: 43.3 and 43.6 us; at 20 49 and 50, at 64 46 and 45.  2 and 24
-// sequences of 12 rows, 8 K/V heads, 700 own keys behind 60000: 56 and 111 us;
-// at 32 83 and 144, at 14 56 and 109.)  What is left over goes to the own keys:
-// rounded to the nearest, 32 sequences of one own token behind 65536 took 61 us
-// of 49, all own keys meeting one CTA.
-constexpr int kStepTiles = 32, kStepTilesFar = 20, kFar = 8;
+// unit's key tile (256 rows) as long as 32 of the few rows' tiles where the
+// prefix is 6 tiles a CTA (of all) or less, as 20 from 18 on, whose stream then
+// keeps the memory busy and the own tiles waiting, and in even steps between.
+// At 32 and at 20, us: 64 sequences, 8 K/V heads, 700 own keys behind 9472 tokens
+// (4 a CTA) 52.7 and 58.6, behind 18944 (8) 58.5 and 64.0 (as it is 57.2), behind
+// 28416 65.5 and 68.8 (64.0), behind 37888 (16) 73.4 and 73.5 (72.1), behind
+// 85248 111 and 106; 24 sequences of 12 rows behind 9216 (8) 41.6 and 42.1, behind
+// 41472 (34) 109 and 84.  (All at 26: 54.2, 59.3, 64.7, 70.5, 104, 39.9, 91.)  What
+// is left over goes to the own keys: rounded to the nearest, 32 sequences of one
+// own token behind 65536 took 61 us of 49, all own keys meeting one CTA.
 __device__ __forceinline__ int prefix_ctas(const PrefixParams& p, int np,
                                            int few) {
   if (few == 0) return p.grid;
   if (np == 0) return 0;
   const float tiles = static_cast<float>(p.pack_blocks * p.Hkv) *
                       static_cast<float>(places(p, 0, np));
-  const float many =
-      tiles * (tiles > static_cast<float>(kFar * p.grid) ? kStepTilesFar
-                                                         : kStepTiles);
-  const int n = static_cast<int>(p.grid * (many / (many + few)));
+  const float far = 38.f * p.grid - tiles;  // 32 at 6 tiles a CTA, 20 at 18
+  const float many = tiles * fmaxf(20.f * p.grid, fminf(32.f * p.grid, far));
+  const int n = static_cast<int>(
+      p.grid * (many / (many + static_cast<float>(few) * p.grid)));
   return max(1, min(n, p.grid - 1));
 }
 
