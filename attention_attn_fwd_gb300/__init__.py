@@ -967,7 +967,20 @@ def kv8_evict(cache, weights, keep, recent=0, out=None, out_weights=None,
     return out, out_weights, indices
 
 
-class Rope:
+class _Handle:
+    """Handle whose tensors' addresses are handed over in ``struct``: they are
+    changed in place (``cache.lens += 1``); another tensor in the place of one
+    would not be the one that calls read, and is refused."""
+    held = ()
+
+    def __setattr__(self, name, value):
+        if name in self.held and getattr(self, name, value) is not value:
+            raise AttnError("%s is changed in place, or a handle made of "
+                            "another tensor" % name, ATTN_ERR_INVALID_ARG)
+        object.__setattr__(self, name, value)
+
+
+class Rope(_Handle):
     """Handle of a rotation of heads by position (``attn_rope_t``).
 
     ``freq``: the rot / 2 pairs' frequencies in radians per position (any
@@ -976,6 +989,7 @@ class Rope:
     ``interleaved``.  ``axes``: the axis of each pair, 0 up (all 0 unless
     given), for positions on several axes (time, height, width).
     """
+    held = ("phase", "axis")
 
     def __init__(self, freq, D, axes=None, interleaved=False, device="cuda"):
         import torch
@@ -1233,7 +1247,7 @@ def qk_rope_bwd(rope, dq, dk, q=None, k=None, dv=None, q_weight=None,
     return dq_out, dk_out, dv_out, dw[0], dw[1]
 
 
-class PrefixCache:
+class PrefixCache(_Handle):
     """Handle of the keys and values of a batch whose sequences share a prefix
     (``attn_prefix_cache_t``).
 
@@ -1242,10 +1256,11 @@ class PrefixCache:
     sequence's own behind it, of which lens (int32 [B]) are used, the current
     step's new ones included.  All contiguous, float16 or bfloat16, on one CUDA
     device; the tensors stay the caller's and are kept alive by the handle.
-    Advance ``lens`` first, then write the new tokens (``qk_rope`` with
-    lens=cache.lens, offset=cache.prefix_len, k_out=cache.k, v_out=cache.v),
-    then ``prefix_fwd``.
+    Advance ``lens`` first (in place), then write the new tokens (``qk_rope``
+    with lens=cache.lens, offset=cache.prefix_len, k_out=cache.k,
+    v_out=cache.v), then ``prefix_fwd``.
     """
+    held = ("prefix_k", "prefix_v", "prefix_len", "k", "v", "lens")
 
     def __init__(self, prefix_k, prefix_v, prefix_len, k, v, lens):
         import torch
