@@ -551,11 +551,13 @@ __global__ void __launch_bounds__(cfg::kThreads, 1)
       }
     }
     // Every copy lands before the CTA goes away, whichever role gave up.
-    for (int t = 0; t < 2; ++t)
-      if (q_loads[t] > 0) drain_wait(bar_q + 8 * t, (q_loads[t] - 1) & 1, p);
+#pragma unroll 1
     for (int i = max(0, it - nslots); i < it; ++i)
       if (!(withhold && i == 0))
         drain_wait(bar_full + 8 * (i % nslots), (i / nslots) & 1, p);
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t)
+      if (q_loads[t] > 0) drain_wait(bar_q + 8 * t, (q_loads[t] - 1) & 1, p);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------ MMA issuer
