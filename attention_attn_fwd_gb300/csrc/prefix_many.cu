@@ -1,5 +1,6 @@
 // Attention of many query rows over a shared prefix, and over the sequences'
-// own keys where a K/V head has more than 16 query rows.
+// own keys where a K/V head has too many query rows for the few-row work (more
+// than 16, or 8 of few sequences and heads: see Mode).
 //
 // The prefix's keys are the same for every sequence, so its query rows are
 // packed across the batch: a 128-row Q tile holds the rows of as many
@@ -19,7 +20,9 @@
 // at most in fp16, 2^-8 in bf16, as O itself) and held times 2^kShift: in fp16,
 // whose numbers end at 65504, so that weights stay normal down to 2^-21 of the
 // row's largest; in bf16, whose V may come near fp32's largest number, so that
-// sums of P V do not pass it.  The row sums take P unrounded.
+// sums of P V do not pass it (over 2^16 keys a part, 2^24 of like weights); a
+// product is then off by 2^-150 at most, 2^-126 of O, which values of V below
+// 2^-100 feel.  The row sums take P unrounded.
 //
 // The key tiles of all units form one list, with some empty places before each
 // unit's, cut into equal consecutive shares, one per CTA: lengths come from
@@ -28,22 +31,25 @@
 //
 // A tile is worked on in steps of 64 keys, two score buffers a Q tile, so that
 // the tensor cores make one step's scores while the softmax works on the other:
-// 1.5 us a tile of keys by 256 rows, D = 128, of which the products' shared
-// memory reads take 1.33 (a 64-key product of scores reads 6 KB in the time of
-// 4).  Steps of 128 keys, whose products would need 1.11, took 1.6 to 1.75: one
-// score buffer is all that tensor memory holds of them beside O.
+// about 3000 clocks a tile of keys by 256 rows, D = 128 (1.5 us; 1.66 where a
+// call is long enough for the power limit to lower the clock), of which the
+// products' shared memory reads take 2560 (a 64-key product of scores reads 6 KB
+// in the time of 4).  Steps of 128 keys took 1.6 to 1.75 us here: one score
+// buffer is all that tensor memory holds of them beside O.
 //
-// What bounds it: those products, where rows are many (8 prompts' chunks of 512
-// tokens behind 3584, 32 heads: 205 us, 1.26 PFLOP/s); the keys' bytes, the
-// start (about 8 us: launch, lengths, cold instructions) and the parts' way
-// through memory (128 KB a CTA) in a decoding step (64 sequences behind 8192
-// tokens: 43 us for 171 MB with the merge).
+// What bounds it: those products, where rows are many and keys too; 8 prompts'
+// chunks of 512 tokens, 32 heads, take 36 us and 1.66 for each of a CTA's key
+// tiles: 205 to 215 us behind 3584 (103 tiles, 1.20 to 1.25 PFLOP/s), 391 behind
+// 7680.  (Of the 36, about 8 are the start, 9 changes of units, 6 the join.)  The
+// keys' bytes, the start (about 8 us: launch, lengths, cold instructions) and the
+// parts' way through memory (128 KB a CTA) in a decoding step (64 sequences
+// behind 8192 tokens: 44 to 46 us for 171 MB with the merge).
 //
 // Roles (384 threads): warps 0 and 2 MMA issue of Q tile 0 / 1, warp 1 tile
 // copies, warp 3 walks the share, publishes its units in shared memory, copies
 // their query rows and clears the ends of V, warps 4-7 / 8-11 softmax and
 // output of Q tile 0 / 1.  (One warp for both tiles' products fell behind the
-// tensor cores: 300 us for those 205.)  Every wait is bounded as in the
+// tensor cores: 300 us where two took 205.)  Every wait is bounded as in the
 // forward kernel.  Before a CTA ends, also after a wait that ran out in any of
 // its roles, each role has seen what it started land: the copies in shared
 // memory, the products in tensor memory, which is freed behind them.
@@ -75,7 +81,8 @@ static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * 168,
 constexpr int kUnits = 4;  // published units held at a time
 // Empty places of the list before a unit's key tiles, for what a part of a unit
 // takes besides them.  64 sequences behind 8192 tokens, one new token each:
-// 47.1 us, without 49.5; 32 behind 65531: 52.9 and 57.0 (before other steps).
+// 44.0 us, with 2 47.2, without 48.9; 32 behind 65531: 51.3, 52.9 and 57.5; but 8
+// behind 4096, whose parts are short, 18.2, 18.3 and 17.6.
 // None where a sequence's rows meet its own keys alone (kPacked), whose Q tile
 // may be the other one than the unit's before, and whose key tiles take less
 // time (32 sequences, 24 rows, 700 own keys behind 8192: 67 us; 75 with 4).

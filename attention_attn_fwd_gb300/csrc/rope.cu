@@ -21,7 +21,7 @@
 //
 // What bounds it: the bytes, each read and written once.  The prompt's 168 MB
 // take 28.9 us, 5.8 TB/s (a copy's rate would be 25.0); the video tokens' 100 MB
-// 18.6, 5.3 TB/s (of the rest, three axes' positions and angles for no more than
+// 18.7, 5.3 TB/s (of the rest, three axes' positions and angles for no more than
 // 8 heads of a token); one token of 8 sequences 3.1 us on the device, a launch.
 // Registers limit what is in flight, hence a CTA's one kind of head, whose
 // factors of norm and rotation are made once, and packed arithmetic.
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks(D))
 
 // --------------------------------------------------------------- backward
 // Reads two rows and writes one, with twice the forward's arithmetic between: a
-// training step's 570 MB take 106 us, 5.4 TB/s (a copy's rate would be 85).  Rows
+// training step's 570 MB take 107 us, 5.3 TB/s (a copy's rate would be 85).  Rows
 // run ahead through shared memory, as registers have no room for them beside the
 // weights' sums (121 us with loads just ahead of their use, 127 with the next
 // row's in registers).  Each CTA keeps to a block of heads and walks over tokens,

@@ -643,8 +643,9 @@ const char* attn_status_string(attn_status_t status);
  * clears the library's device status word.  *code receives 0 when no kernel
  * wait has run out since the last call; otherwise a non-zero code
  * (bit 0: a wait timed out, bits 8-15 then name the pipeline role that gave
- * up; bit 1: an attn_kv8_* call met a length outside its range and clamped
- * it) and the function returns ATTN_ERR_TIMEOUT, or ATTN_ERR_INVALID_ARG
+ * up; bit 1: a call that reads lengths on the device, attn_kv8_*, attn_qk_rope
+ * or attn_prefix_fwd, met one outside its range and clamped it) and the function
+ * returns ATTN_ERR_TIMEOUT, or ATTN_ERR_INVALID_ARG
  * when bit 1 alone is set.  code may be NULL.
  * Every wait of every kernel in flight ORs into the one word, so the
  * device-wide form sees them all; attn_stream_status below waits for one
